@@ -31,7 +31,9 @@ EXPORTS = ("moe_status_str", "moe_version", "moe_route", "moe_route_scored", "mo
            "moe_fp8_packed_size", "moe_pack_fp8",
            "moe_workspace_size", "moe_forward",
            "moe_forward_profiled", "moe_forward_scored", "moe_ffn_dense", "moe_forward_noalloc",
-           "moe_workspace_views", "moe_forward_expire_wait", "moe_check", "moe_check_noalloc")
+           "moe_workspace_views", "moe_forward_expire_wait", "moe_check", "moe_check_noalloc",
+           "moe_quant_fp8b", "moe_norm_fp8b", "moe_gemm_fp8b", "moe_grouped_gemm_fp8b",
+           "moe_gate_up_fp8b")
 
 _lib = None
 _debug_lib = None
@@ -128,6 +130,20 @@ def _declare(L):
     L.moe_forward_expire_wait.restype = i
     L.moe_workspace_views.argtypes = [i, i, i, i, i, i, i, vp]
     L.moe_workspace_views.restype = i
+    f = ctypes.c_float
+    L.moe_quant_fp8b.argtypes = [vp, i, i, i, i, ll, i, vp, vp, vp]
+    L.moe_quant_fp8b.restype = i
+    L.moe_norm_fp8b.argtypes = [vp, i, i, i, ll, vp, i, i, ll, vp, vp, i, vp, i, f, vp, vp, vp, vp,
+                                vp]
+    L.moe_norm_fp8b.restype = i
+    L.moe_gemm_fp8b.argtypes = [vp, vp, i, i, ll, vp, vp, i, vp, i, ll, vp, vp]
+    L.moe_gemm_fp8b.restype = i
+    L.moe_grouped_gemm_fp8b.argtypes = [vp, vp, i, i, ll, vp, vp, i, i, vp, vp, i, vp, i, ll, vp,
+                                        vp]
+    L.moe_grouped_gemm_fp8b.restype = i
+    L.moe_gate_up_fp8b.argtypes = [vp, vp, i, i, ll, vp, vp, vp, vp, i, i, vp, vp, i, vp, vp, vp,
+                                   vp]
+    L.moe_gate_up_fp8b.restype = i
     L.moe_check.argtypes = [vp, vp, vp]
     L.moe_check.restype = i
     L.moe_check_noalloc.argtypes = [vp, vp]
@@ -442,3 +458,243 @@ def moe_check(workspace: torch.Tensor) -> int:
     word = ctypes.c_uint32(0)
     _check(L.moe_check(_ptr(workspace), ctypes.byref(word), _stream(workspace)), "moe_check")
     return word.value
+
+
+# ---- block-scaled fp8 operators (E4M3 codes; one fp32 scale per row and 128
+# columns, or per 128 x 128 block).  Unlike the calls above these check shapes,
+# types, devices and strides here: their operands come in pairs that a wrong
+# pairing would read out of bounds.
+
+def _need(t: torch.Tensor, name: str, shape, dtypes, device, rows_strided: bool = False):
+    """The operand's pointer, after checks of device, type, shape and strides
+    (rows_strided: rows may be further apart than their length)."""
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous() and not (rows_strided and t.stride(-1) == 1):
+        raise ValueError(f"{name}: strides {t.stride()} are not supported, make it contiguous")
+    return t.data_ptr()
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    return t.stride(-2) if t.shape[-2] > 1 else t.shape[-1]
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _call_fp8b(name: str, device: torch.device, *args):
+    """The library call on `device`'s current stream, with that device current."""
+    if device.type != "cuda":
+        raise ValueError(f"{name}: tensors are on {device}, expected a CUDA device")
+    f = getattr(_lib or load_library(), name)
+    if device.index == torch.cuda.current_device():
+        status = f(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = f(*args, torch.cuda.current_stream(device).cuda_stream)
+    if status != 0:
+        raise MoeError(status, name)
+
+
+_FP8 = (torch.float8_e4m3fn, torch.uint8)
+_REAL = (torch.float32, torch.bfloat16)
+_F32 = (torch.float32,)
+_BF16 = (torch.bfloat16,)
+_I32 = (torch.int32,)
+
+
+def moe_quant_fp8b(x: torch.Tensor, block_rows: int = 1, codes: Optional[torch.Tensor] = None,
+                   scales: Optional[torch.Tensor] = None):
+    """Block-scaled fp8 of x [rows, cols] or [batch, rows, cols] (fp32 / bf16) ->
+    (codes float8_e4m3fn like x, scales fp32 [..., ceil(rows/block_rows), ceil(cols/128)]).
+
+    block_rows: 1 for activations (a scale per row and 128 columns), 128 for
+    weights (a scale per 128 x 128 block).
+    """
+    if x.dim() not in (2, 3):
+        raise ValueError(f"x: {x.dim()} dimensions, expected 2 or 3")
+    if block_rows not in (1, 128):
+        raise ValueError(f"block_rows: {block_rows}, expected 1 or 128")
+    dev = x.device
+    rows, cols = x.shape[-2:]
+    batch = x.shape[0] if x.dim() == 3 else 1
+    px = _need(x, "x", x.shape, _REAL, dev, rows_strided=True)
+    ldx = _row_stride(x)
+    if x.dim() == 3 and batch > 1 and rows > 0 and x.stride(0) != rows * ldx:
+        raise ValueError(f"x: strides {x.stride()} are not supported, make it contiguous")
+    s_shape = (*x.shape[:-2], -(-rows // block_rows), _blocks(cols))
+    if codes is None:
+        codes = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev)
+    if scales is None:
+        scales = torch.empty(s_shape, dtype=torch.float32, device=dev)
+    _call_fp8b("moe_quant_fp8b", dev, px, _act_dtype(x), batch, rows, cols, ldx, block_rows,
+               _need(codes, "codes", x.shape, _FP8, dev), _need(scales, "scales", s_shape, _F32, dev))
+    return codes, scales
+
+
+def moe_norm_fp8b(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                  delta: Optional[torch.Tensor] = None, topk_w: Optional[torch.Tensor] = None,
+                  inv: Optional[torch.Tensor] = None, want_normed: bool = True,
+                  resid: Optional[torch.Tensor] = None, normed: Optional[torch.Tensor] = None,
+                  codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None):
+    """Residual addition, RMS norm and quantisation -> (resid, normed, codes, scales).
+
+    x [T, d] fp32 / bf16.  delta None: r = x (resid is x itself).  delta [T, d]:
+    r = x + delta.  With topk_w [T, k] and inv [T*k] (moe_route, moe_permute):
+    delta holds grouped rows, r[t] = x[t] + sum_j topk_w[t, j] delta[inv[t*k + j]].
+    resid: r in x's type; normed: bf16 RMS norm of r times weight (None with
+    want_normed=False); codes, scales: the same in block-scaled fp8.  resid may
+    be x.
+    """
+    T, d = x.shape
+    dev = x.device
+    k = 0
+    if (topk_w is None) != (inv is None):
+        raise ValueError("topk_w and inv go together")
+    pd = pw = pi = pr = pn = None
+    dd = ldd = n_delta = 0
+    px = _need(x, "x", x.shape, _REAL, dev, rows_strided=True)
+    if delta is not None:
+        n_delta = delta.shape[0]
+        if inv is not None:
+            k = topk_w.shape[-1]
+            pw = _need(topk_w, "topk_w", (T, k), _F32, dev)
+            pi = _need(inv, "inv", inv.shape, _I32, dev)
+            if inv.numel() != T * k:
+                raise ValueError(f"inv: {inv.numel()} values, expected {T * k}")
+            if k == 0:
+                raise ValueError("topk_w: no experts per token")
+        pd = _need(delta, "delta", (n_delta if k else T, d), _REAL, dev, rows_strided=True)
+        dd, ldd = _act_dtype(delta), _row_stride(delta)
+        if resid is None:
+            resid = torch.empty((T, d), dtype=x.dtype, device=dev)
+        pr = _need(resid, "resid", (T, d), (x.dtype,), dev)
+    elif inv is not None:
+        raise ValueError("topk_w and inv need delta")
+    else:
+        resid = x
+    if want_normed:
+        if normed is None:
+            normed = torch.empty((T, d), dtype=torch.bfloat16, device=dev)
+        pn = _need(normed, "normed", (T, d), _BF16, dev)
+    else:
+        normed = None
+    if codes is None:
+        codes = torch.empty((T, d), dtype=torch.float8_e4m3fn, device=dev)
+    if scales is None:
+        scales = torch.empty((T, _blocks(d)), dtype=torch.float32, device=dev)
+    _call_fp8b("moe_norm_fp8b", dev, px, _act_dtype(x), T, d, _row_stride(x), pd, dd, n_delta, ldd,
+               pw, pi, k, _need(weight, "weight", (d,), _REAL, dev), _act_dtype(weight), eps, pr, pn,
+               _need(codes, "codes", (T, d), _FP8, dev),
+               _need(scales, "scales", (T, _blocks(d)), _F32, dev))
+    return resid, normed, codes, scales
+
+
+def _product_out(out, rows, N, out_dtype, dev):
+    if out is None:
+        if out_dtype not in _REAL:
+            raise TypeError(f"out_dtype: {out_dtype}, expected torch.float32 or torch.bfloat16")
+        return torch.empty((rows, N), dtype=out_dtype, device=dev)
+    return out
+
+
+def _status_ptr(status, dev):
+    if status is None:
+        return None
+    if status.numel() < 1:
+        raise ValueError("status: empty")
+    return _need(status, "status", status.shape, _I32, dev)
+
+
+def moe_gemm_fp8b(x_q: torch.Tensor, x_s: torch.Tensor, w_q: torch.Tensor, w_s: torch.Tensor,
+                  out: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+                  status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """x [T, K] times W^T, W [N, K], in block-scaled fp8 -> out [T, N] bf16 / fp32.
+
+    status: optional int32 device word that collects device-side errors (zero it
+    once; moe_check(status) reads it).
+    """
+    T, K = x_q.shape
+    N = w_q.shape[0]
+    dev = x_q.device
+    out = _product_out(out, T, N, out_dtype, dev)
+    po = _need(out, "out", (T, N), _REAL, dev, rows_strided=True)
+    _call_fp8b("moe_gemm_fp8b", dev, _need(x_q, "x_q", (T, K), _FP8, dev, rows_strided=True),
+               _need(x_s, "x_s", (T, _blocks(K)), _F32, dev), T, K, _row_stride(x_q),
+               _need(w_q, "w_q", (N, K), _FP8, dev),
+               _need(w_s, "w_s", (_blocks(N), _blocks(K)), _F32, dev), N, po, _act_dtype(out),
+               _row_stride(out), _status_ptr(status, dev))
+    return out
+
+
+def _groups(offsets, perm_tok, E, x_rows, dev):
+    """(offsets pointer, perm_tok pointer, grouped rows)."""
+    rows = x_rows if perm_tok is None else perm_tok.numel()
+    pp = None if perm_tok is None else _need(perm_tok, "perm_tok", (rows,), _I32, dev)
+    if offsets is None:
+        if E != 1:
+            raise ValueError(f"offsets are required for {E} experts")
+        return None, pp, rows
+    return _need(offsets, "offsets", (E + 1,), _I32, dev), pp, rows
+
+
+def moe_grouped_gemm_fp8b(x_q: torch.Tensor, x_s: torch.Tensor, w_q: torch.Tensor,
+                          w_s: torch.Tensor, offsets: torch.Tensor,
+                          perm_tok: Optional[torch.Tensor] = None,
+                          out: Optional[torch.Tensor] = None,
+                          out_dtype: torch.dtype = torch.bfloat16,
+                          status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Every expert's product with its rows, in block-scaled fp8 -> out [rows, N].
+
+    w_q [E, N, K], w_s [E, ceil(N/128), ceil(K/128)]; rows of expert e are
+    [offsets[e], offsets[e+1]) (moe_permute), row r is x's row perm_tok[r], or r
+    itself without perm_tok.  Rows from offsets[E] on are left as they were.
+    """
+    x_rows, K = x_q.shape
+    E, N = w_q.shape[:2]
+    dev = x_q.device
+    po, pp, rows = _groups(offsets, perm_tok, E, x_rows, dev)
+    out = _product_out(out, rows, N, out_dtype, dev)
+    pout = _need(out, "out", (rows, N), _REAL, dev, rows_strided=True)
+    _call_fp8b("moe_grouped_gemm_fp8b", dev, _need(x_q, "x_q", (x_rows, K), _FP8, dev, rows_strided=True),
+               _need(x_s, "x_s", (x_rows, _blocks(K)), _F32, dev), x_rows, K, _row_stride(x_q),
+               _need(w_q, "w_q", (E, N, K), _FP8, dev),
+               _need(w_s, "w_s", (E, _blocks(N), _blocks(K)), _F32, dev), E, N, po, pp, rows, pout,
+               _act_dtype(out), _row_stride(out), _status_ptr(status, dev))
+    return out
+
+
+def moe_gate_up_fp8b(x_q: torch.Tensor, x_s: torch.Tensor, wg_q: torch.Tensor, wg_s: torch.Tensor,
+                     wu_q: torch.Tensor, wu_s: torch.Tensor,
+                     offsets: Optional[torch.Tensor] = None,
+                     perm_tok: Optional[torch.Tensor] = None, h_q: Optional[torch.Tensor] = None,
+                     h_s: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None):
+    """h = SiLU(W_g x) * (W_u x) per grouped row, quantised -> (h_q [rows, F], h_s).
+
+    wg_q, wu_q [E, F, d] (or [F, d] without offsets: a dense layer) with scales
+    [E, ceil(F/128), ceil(d/128)]; offsets and perm_tok as moe_grouped_gemm_fp8b.
+    """
+    x_rows, d = x_q.shape
+    dev = x_q.device
+    lead = wg_q.shape[:-2]
+    E, F = (lead[0] if lead else 1), wg_q.shape[-2]
+    if len(lead) > 1:
+        raise ValueError(f"wg_q: {wg_q.dim()} dimensions, expected 2 or 3")
+    po, pp, rows = _groups(offsets, perm_tok, E, x_rows, dev)
+    w_shape, s_shape = (*lead, F, d), (*lead, _blocks(F), _blocks(d))
+    if h_q is None:
+        h_q = torch.empty((rows, F), dtype=torch.float8_e4m3fn, device=dev)
+    if h_s is None:
+        h_s = torch.empty((rows, _blocks(F)), dtype=torch.float32, device=dev)
+    _call_fp8b("moe_gate_up_fp8b", dev, _need(x_q, "x_q", (x_rows, d), _FP8, dev, rows_strided=True),
+               _need(x_s, "x_s", (x_rows, _blocks(d)), _F32, dev), x_rows, d, _row_stride(x_q),
+               _need(wg_q, "wg_q", w_shape, _FP8, dev), _need(wg_s, "wg_s", s_shape, _F32, dev),
+               _need(wu_q, "wu_q", w_shape, _FP8, dev), _need(wu_s, "wu_s", s_shape, _F32, dev), E, F,
+               po, pp, rows, _need(h_q, "h_q", (rows, F), _FP8, dev),
+               _need(h_s, "h_s", (rows, _blocks(F)), _F32, dev), _status_ptr(status, dev))
+    return h_q, h_s

@@ -1,0 +1,678 @@
+// fp8b_gemm.cu -- products of block-scaled fp8 matrices on the tensor cores
+// (tcgen05 kind::f8f6f4, TMA, TMEM): dense, grouped by expert with ragged
+// sizes, and the grouped gate/up pair with SwiGLU and quantisation behind it.
+//
+//   y[r,n] = sum_b sx[r,b] sw[n/128,b] P_b[r,n],   P_b[r,n] = sum_{i in block b} cx[r,i] cw[n,i]
+//
+// with E4M3 codes c, an activation scale per row and 128 columns and a weight
+// scale per 128 x 128 block.  The scales change every 128 columns of the
+// reduction, so the tensor cores sum one block (four MMAs of K = 32, fp32)
+// into one of two TMEM buffers, and the epilogue warps add that partial sum,
+// times the two scales, to the row's running fp32 sums in registers while the
+// tensor cores fill the other buffer.
+//
+// A tile is 128 rows x 256 columns (PRODUCT), or 128 rows x 128 columns of
+// both W_gate and W_up (GATEUP: the epilogue has whole 128-column groups of h,
+// so it quantises them without a second pass).  Warp 0 loads (TMA boxes of 32
+// rows, or gathers of four rows each through perm_tok -- only as many as the
+// tile has rows), warp 1 multiplies, warps 2-9 hold the sums: warp w the TMEM
+// lanes of quarter w % 4 and one half of the columns.
+//
+// Rows of a tile past the end of its group are left out of the loads and the
+// stores (their lanes of the MMA compute on whatever the buffer holds; rows
+// do not mix).  Columns past N and the last block's columns past K are zeros
+// by TMA's fill.
+//
+// Few tiles (decode): the reduction is split over a cluster of 2, 4 or 8 CTAs
+// (SPLIT), whose partial sums meet in distributed shared memory, one row per
+// warp, added in the order of the blocks.
+//
+// Every wait is bounded (2 s).  Where one gives up, the rows of the CTA's
+// remaining tiles are written as NaN, and the status word says so if the
+// caller passed one.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "fp8b.h"
+#include "kernels.h"
+#include "sm100.cuh"
+
+namespace moe {
+namespace tc {
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();   // tc_gemm.cu
+}
+namespace fp8b {
+
+using namespace sm100;
+
+constexpr int BM = 128, BN = 256, BK = kBlock;   // one MMA k-block = one scale block
+constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE = A_BYTES + B_BYTES;
+constexpr int STAGES = 4;
+constexpr int ABOX = 32;                         // rows per A load
+constexpr int TMEM_COLS = 512;                   // two partial sums of 256 columns
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kPartRow = BN + 4;                 // floats per row of a split partial sum (16-byte
+                                                 // stores of 8 rows fall in distinct banks)
+
+enum Mode { PRODUCT = 0, GATEUP = 1 };
+
+struct Params {
+    const float *x_s;         // [x_rows, KB]
+    const float *w_s[2];      // [E, NB, KB] of W (PRODUCT) or W_gate, W_up
+    const int32_t *offsets;   // [E+1], or NULL: one group of all rows
+    const int32_t *perm_tok;  // [rows] (gathering)
+    int E, rows, x_rows, K, N, KB, NB, n_tiles;
+    void *out;                // PRODUCT: [rows, ldo] bf16 or fp32
+    long long ldo;
+    int out_f32, out_vec;     // out_vec: 16-byte stores are aligned
+    uint8_t *h_q;             // GATEUP: [rows, N] codes, [rows, NB] scales
+    float *h_s;
+    uint32_t *status;
+    int split;                // CTAs per cluster (SPLIT)
+};
+
+struct alignas(16) Ctl {
+    uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], drain;
+    uint32_t tmem_base;
+    int abort_flag;
+    int total;
+    int off[kMaxExperts + 1], tile_start[kMaxExperts + 1], mtiles[kMaxExperts];
+    uint32_t amax[2][BM];     // GATEUP: each row's largest |h| per column half
+};
+constexpr size_t kSmem = 1024 + (size_t)STAGES * STAGE + sizeof(Ctl);
+static_assert(kSmem <= 232448, "shared memory per CTA");
+static_assert((size_t)BM * kPartRow * 4 <= (size_t)STAGES * STAGE, "split partial sums reuse the ring");
+
+// Instruction descriptor of tcgen05.mma kind::f8f6f4: fp32 accumulate, A and B
+// E4M3 (format 0), both K-major, shape M x N.
+constexpr uint32_t idesc_e4m3(int M, int N)
+{
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+// Four rows y0..y3 of a 2-D tensor (box one row high), one below the other.
+__device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int4 y)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w), "r"(smem_u32(bar))
+        : "memory");
+}
+// Wait for the warp's TMEM loads; the registers pass through it, so that
+// nothing that reads them moves above it.
+__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&v)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ float lo2(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi2(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+// two fp32 fused multiply-adds in one instruction, each rounded as fmaf is
+__device__ __forceinline__ void fma2(uint64_t &acc, uint64_t a, uint64_t b)
+{
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+// SwiGLU with the fast exponential and an approximate divide (relative error
+// ~1e-6, far below the codes' 2^-4; for g < -87, 1 + e^-g overflows and h is 0)
+__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+
+// sixteen codes of v * inv (see quant_mul)
+template <typename F>
+__device__ __forceinline__ uint4 encode16(F v, float inv)
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = e4m3x2(v(4 * i) * inv, v(4 * i + 1) * inv) | (e4m3x2(v(4 * i + 2) * inv, v(4 * i + 3) * inv) << 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Factor that takes h to codes: 1 / s.  h already carries the sums' rounding
+// errors, so a code on the border of two may go either way and the product
+// with the reciprocal (half an ulp off) replaces the divide.  Where 1 / s is
+// not finite (s = 0 or below 2^-126: h all zero or below 2^-117) the codes are
+// zero; NaN stays NaN.
+__device__ __forceinline__ float quant_mul(float s) { return s >= 1.17549435e-38f || s != s ? 1.0f / s : 0.0f; }
+
+// One output value's stores: columns [n0, n0 + 4) of row r.
+__device__ __forceinline__ void store4(const Params &p, long long r, int n0, float a, float b, float c, float d)
+{
+    const float v[4] = {a, b, c, d};
+    if (p.out_f32) {
+        float *o = static_cast<float *>(p.out) + r * p.ldo + n0;
+        if (p.out_vec && n0 + 4 <= p.N) *reinterpret_cast<float4 *>(o) = make_float4(a, b, c, d);
+        else
+            for (int i = 0; i < 4; ++i)
+                if (n0 + i < p.N) o[i] = v[i];
+    } else {
+        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + r * p.ldo + n0;
+        if (p.out_vec && n0 + 4 <= p.N) {
+            const __nv_bfloat162 q0 = __floats2bfloat162_rn(a, b), q1 = __floats2bfloat162_rn(c, d);
+            *reinterpret_cast<uint2 *>(o) = make_uint2(*reinterpret_cast<const uint32_t *>(&q0),
+                                                       *reinterpret_cast<const uint32_t *>(&q1));
+        } else
+            for (int i = 0; i < 4; ++i)
+                if (n0 + i < p.N) o[i] = __float2bfloat16_rn(v[i]);
+    }
+}
+
+struct Tile { int e, nt, row0, cnt; };   // expert, column tile, first grouped row, rows
+
+// tile -> its expert, column tile and rows; within an expert the row tiles run
+// fastest, so CTAs running at the same time share weight tiles through L2.
+__device__ __forceinline__ Tile tile_at(const Ctl &c, int E, int t)
+{
+    int lo = 0, hi = E - 1;   // largest e with tile_start[e] <= t
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (c.tile_start[mid] <= t) lo = mid;
+        else hi = mid - 1;
+    }
+    const int local = t - c.tile_start[lo], m = c.mtiles[lo];
+    Tile r;
+    r.e = lo;
+    r.nt = local / m;
+    const int mt = local - r.nt * m;
+    r.row0 = c.off[lo] + mt * BM;
+    r.cnt = min(BM, c.off[lo + 1] - r.row0);
+    return r;
+}
+
+template <int MODE, bool GATHER, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1)
+product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w0,
+               const __grid_constant__ CUtensorMap tm_w1, const Params p)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    Ctl &c = *reinterpret_cast<Ctl *>(smem + STAGES * STAGE);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int E = p.E;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) { mbar_init(&c.full[s], 1); mbar_init(&c.empty[s], 1); }
+        for (int b = 0; b < 2; ++b) { mbar_init(&c.tfull[b], 1); mbar_init(&c.tempty[b], kEpiWarps); }
+        mbar_init(&c.drain, 1);
+        c.abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_x)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_w0)) : "memory");
+        if (MODE == GATEUP)
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_w1)) : "memory");
+    }
+    if (warp == 1) tmem_alloc(&c.tmem_base, TMEM_COLS);
+    tc_fence_before();
+    pdl_enter();
+    // group bounds, kept inside [0, rows] whatever the array holds
+    for (int e = threadIdx.x; e <= E; e += kThreads)
+        c.off[e] = p.offsets ? min(max(p.offsets[e], 0), p.rows) : e * p.rows;
+    __syncthreads();
+    if (warp == 0) {
+        // exclusive scan of row tiles * column tiles over experts (8 per lane)
+        int local[8], sum = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int e = lane * 8 + j;
+            int m = 0;
+            if (e < E) {
+                m = (max(c.off[e + 1] - c.off[e], 0) + BM - 1) / BM;
+                c.mtiles[e] = m;
+            }
+            local[j] = m * p.n_tiles;
+            sum += local[j];
+        }
+        int incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        int run = incl - sum;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int e = lane * 8 + j;
+            if (e < E) c.tile_start[e] = run;
+            run += local[j];
+        }
+        if (lane == 31) c.total = incl;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+
+    const uint32_t tmem = c.tmem_base;
+    const int total = c.total;
+    const int S = SPLIT ? p.split : 1;
+    const int rank = SPLIT ? (int)cluster_rank() : 0;
+    const int first = SPLIT ? blockIdx.x / S : blockIdx.x;
+    const int stride = SPLIT ? gridDim.x / S : gridDim.x;
+    // this CTA's blocks of the reduction
+    const int kb0 = (int)((long long)p.KB * rank / S), kb1 = (int)((long long)p.KB * (rank + 1) / S);
+    volatile int *abort_flag = &c.abort_flag;
+
+    if (warp == 0) {
+        // ------------------------------------------------ loads
+        uint32_t it = 0;
+        bool ok = true;
+        for (int t = first; t < total && ok; t += stride) {
+            const Tile tile = tile_at(c, E, t);
+            int4 tok = make_int4(0, 0, 0, 0);
+            const int loads = GATHER ? (tile.cnt + 3) / 4 : (tile.cnt + ABOX - 1) / ABOX;
+            if (GATHER && lane < loads) {
+                // (an index out of range is read as row 0: its row is dropped by its scale)
+                int v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = min(4 * lane + i, tile.cnt - 1);
+                    v[i] = __ldg(p.perm_tok + tile.row0 + r);
+                    if (v[i] < 0 || v[i] >= p.x_rows) v[i] = 0;
+                }
+                tok = make_int4(v[0], v[1], v[2], v[3]);
+            }
+            const uint32_t bytes = (uint32_t)loads * (GATHER ? 4 * BK : ABOX * BK) + B_BYTES;
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const int s = it % STAGES;
+                ok = __all_sync(0xffffffffu, mbar_wait(&c.empty[s], ((it / STAGES) & 1u) ^ 1u, abort_flag));
+                if (!ok) break;
+                uint8_t *sa = smem + s * STAGE, *sb = sa + A_BYTES;
+                if (lane == 0) {
+                    mbar_expect_tx(&c.full[s], bytes);
+                    if (MODE == GATEUP) {
+                        tma_load_3d(sb, &tm_w0, &c.full[s], kb * BK, tile.nt * (BN / 2), tile.e);
+                        tma_load_3d(sb + B_BYTES / 2, &tm_w1, &c.full[s], kb * BK, tile.nt * (BN / 2), tile.e);
+                    } else {
+                        tma_load_3d(sb, &tm_w0, &c.full[s], kb * BK, tile.nt * BN, tile.e);
+                    }
+                }
+                __syncwarp();
+                if (lane < loads) {
+                    if (GATHER) tma_gather4(sa + lane * 4 * BK, &tm_x, &c.full[s], kb * BK, tok);
+                    else tma_load_2d(sa + lane * ABOX * BK, &tm_x, &c.full[s], kb * BK, tile.row0 + lane * ABOX);
+                }
+            }
+        }
+        if (!ok) {
+            if (lane == 0) flag_status(p.status, kDevTimeout);
+            c.abort_flag = 1;
+            // let loads already issued land before the CTA exits
+            for (uint32_t j = (it >= STAGES ? it - STAGES : 0); j < it; ++j) {
+                volatile int no_abort = 0;
+                mbar_wait(&c.full[j % STAGES], (j / STAGES) & 1u, &no_abort, 1000000ull);
+            }
+        }
+    } else if (warp == 1 && lane == 0) {
+        // ------------------------------------------------ multiply
+        constexpr uint32_t idesc = idesc_e4m3(BM, BN);
+        uint32_t it = 0;
+        bool ok = true;
+        for (int t = first; t < total && ok; t += stride) {
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const int s = it % STAGES;
+                const uint32_t b = it & 1u;
+                if (!mbar_wait(&c.tempty[b], ((it >> 1) & 1u) ^ 1u, abort_flag) ||
+                    !mbar_wait(&c.full[s], (it / STAGES) & 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t a0 = smem_u32(smem + s * STAGE);
+                const uint64_t da = sw128_desc(a0), db = sw128_desc(a0 + A_BYTES);
+#pragma unroll
+                for (int kk = 0; kk < BK / 32; ++kk)
+                    umma_f8(tmem + b * BN, desc_step(da, kk * 32), desc_step(db, kk * 32), idesc, kk != 0);
+                umma_commit(&c.empty[s]);
+                umma_commit(&c.tfull[b]);
+            }
+        }
+        if (!ok) {
+            flag_status(p.status, kDevTimeout);
+            c.abort_flag = 1;
+            umma_commit(&c.drain);   // MMAs in flight end before TMEM is freed
+            volatile int no_abort = 0;
+            mbar_wait(&c.drain, 0, &no_abort);
+        }
+    } else if (warp >= 2) {
+        // ------------------------------------------------ sums and output
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const int row = quarter * 32 + lane;
+        uint32_t it = 0;
+        bool ok = true;   // once false, no more waits: the remaining rows become NaN
+        for (int t = first; t < total; t += stride) {
+            const Tile tile = tile_at(c, E, t);
+            const bool valid = row < tile.cnt;
+            const long long r = tile.row0 + row;
+            const float *xs = nullptr;
+            if (valid) {
+                const int src = GATHER ? __ldg(p.perm_tok + r) : (int)r;
+                if (src >= 0 && src < p.x_rows) xs = p.x_s + (size_t)src * p.KB;
+            }
+            // the weight scales of the columns this warp sums: gate and up, or
+            // one 128-column block (none past the last: its sums are zero)
+            const int nb = MODE == GATEUP ? tile.nt : min(tile.nt * 2 + half, p.NB - 1);
+            const float *ws0 = p.w_s[0] + ((size_t)tile.e * p.NB + nb) * p.KB;
+            const float *ws1 = MODE == GATEUP ? p.w_s[1] + ((size_t)tile.e * p.NB + nb) * p.KB : ws0;
+            uint64_t acc[64];   // 128 sums: PRODUCT columns half*128 ..; GATEUP 64 of gate, 64 of up
+#pragma unroll
+            for (int i = 0; i < 64; ++i) acc[i] = 0ull;
+            float nx = xs ? __ldg(xs + kb0) : 0.f, n0 = __ldg(ws0 + kb0), n1 = MODE == GATEUP ? __ldg(ws1 + kb0) : 0.f;
+#pragma unroll 1
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const uint32_t b = it & 1u;
+                const float f0 = nx * n0, f1 = MODE == GATEUP ? nx * n1 : f0;
+                const uint64_t m0 = pack2(__float_as_uint(f0), __float_as_uint(f0));
+                const uint64_t m1 = pack2(__float_as_uint(f1), __float_as_uint(f1));
+                if (kb + 1 < kb1) {
+                    nx = xs ? __ldg(xs + kb + 1) : 0.f;
+                    n0 = __ldg(ws0 + kb + 1);
+                    if (MODE == GATEUP) n1 = __ldg(ws1 + kb + 1);
+                }
+                ok = ok && __all_sync(0xffffffffu, mbar_wait(&c.tfull[b], (it >> 1) & 1u, abort_flag));
+                tc_fence_after();
+                const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + b * BN;
+                // the eight 16-column chunks, one load ahead of the sums
+                uint32_t v[2][16];
+                auto col = [&](int j) { return MODE == GATEUP ? (j >> 2) * (BN / 2) + half * 64 + (j & 3) * 16
+                                                              : half * (BN / 2) + j * 16; };
+                tmem_ld16(base + col(0), v[0]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    tmem_ld_wait16(v[j & 1]);
+                    if (j < 7) tmem_ld16(base + col(j + 1), v[(j + 1) & 1]);
+                    const uint64_t m = j < 4 ? m0 : m1;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) fma2(acc[j * 8 + i], pack2(v[j & 1][2 * i], v[j & 1][2 * i + 1]), m);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c.tempty[b]);
+            }
+            if (!ok) {
+                c.abort_flag = 1;
+                const uint64_t nan2 = 0x7fffffff7fffffffull;
+#pragma unroll
+                for (int i = 0; i < 64; ++i) acc[i] = nan2;
+            }
+            auto val = [&](int i) { return (i & 1) ? hi2(acc[i >> 1]) : lo2(acc[i >> 1]); };
+            if constexpr (SPLIT) {
+                // every MMA of this CTA has completed: the ring holds the partial
+                // sums from here on, in tile column order
+                float *part = reinterpret_cast<float *>(smem) + row * kPartRow;
+                if (valid) {
+#pragma unroll
+                    for (int i = 0; i < 128; i += 4) {
+                        const int cc = MODE == GATEUP ? (i >> 6) * (BN / 2) + half * 64 + (i & 63) : half * (BN / 2) + i;
+                        *reinterpret_cast<float4 *>(part + cc) = make_float4(val(i), val(i + 1), val(i + 2), val(i + 3));
+                    }
+                }
+                break;   // one tile per cluster
+            } else if constexpr (MODE == GATEUP) {
+                uint32_t m = 0u;
+                float h[64];
+#pragma unroll
+                for (int i = 0; i < 64; ++i) {
+                    h[i] = swiglu(val(i), val(64 + i));
+                    m = max(m, mag_bits(h[i]));
+                }
+                // the other half of the row's 128 columns is in the warp of the
+                // same quarter: the two meet at a barrier of their own (both
+                // take every turn of the tile loop, whatever happened before)
+                c.amax[half][row] = m;
+                asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+                m = max(m, c.amax[half ^ 1][row]);
+                asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+                const float s = block_scale(m), inv = quant_mul(s);
+                if (valid) {
+                    const int n0 = tile.nt * (BN / 2) + half * 64;
+#pragma unroll
+                    for (int i = 0; i < 64; i += 16)
+                        if (n0 + i < p.N)
+                            *reinterpret_cast<uint4 *>(p.h_q + r * p.N + n0 + i) = encode16([&](int q) { return h[i + q]; }, inv);
+                    if (half == 0) p.h_s[r * p.NB + tile.nt] = s;
+                }
+            } else {
+                if (valid) {
+                    const int n0 = tile.nt * BN + half * (BN / 2);
+#pragma unroll
+                    for (int i = 0; i < 128; i += 4) store4(p, r, n0 + i, val(i), val(i + 1), val(i + 2), val(i + 3));
+                }
+            }
+        }
+    }
+
+    if constexpr (SPLIT) {
+        cluster_sync_all();   // every CTA's partial sums are written
+        if (first < total && warp >= 2) {
+            // row by row, the clusters' CTAs in turn, a warp to a row: lane l adds
+            // columns 4l.. and 128 + 4l.. over the CTAs in the order of the blocks
+            const Tile tile = tile_at(c, E, first);
+            // (a CTA that gave up may still have had loads landing on its sums)
+            bool failed = false;
+            for (int q = 0; q < S; ++q) failed |= ld_cluster_u32(peer_addr(&c.abort_flag, q)) != 0u;
+            for (int row = rank + S * (warp - 2); row < tile.cnt; row += S * kEpiWarps) {
+                float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+#pragma unroll 4
+                for (int q = 0; q < S; ++q) {
+                    const uint32_t at = peer_addr(smem, q) + (uint32_t)(row * kPartRow + 4 * lane) * 4;
+                    const float4 x = ld_cluster_f4(at), y = ld_cluster_f4(at + 4 * (BN / 2));
+                    a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+                    b.x += y.x; b.y += y.y; b.z += y.z; b.w += y.w;
+                }
+                if (failed) a.x = a.y = a.z = a.w = b.x = b.y = b.z = b.w = __uint_as_float(0x7fffffffu);
+                const long long r = tile.row0 + row;
+                if constexpr (MODE == GATEUP) {
+                    const float h[4] = {swiglu(a.x, b.x), swiglu(a.y, b.y), swiglu(a.z, b.z), swiglu(a.w, b.w)};
+                    const uint32_t m = __reduce_max_sync(0xffffffffu, max(max(mag_bits(h[0]), mag_bits(h[1])),
+                                                                         max(mag_bits(h[2]), mag_bits(h[3]))));
+                    const float s = block_scale(m), inv = quant_mul(s);
+                    const int n0 = tile.nt * (BN / 2) + 4 * lane;
+                    if (n0 < p.N)
+                        *reinterpret_cast<uint32_t *>(p.h_q + r * p.N + n0) =
+                            e4m3x2(h[0] * inv, h[1] * inv) | (e4m3x2(h[2] * inv, h[3] * inv) << 16);
+                    if (lane == 0) p.h_s[r * p.NB + tile.nt] = s;
+                } else {
+                    store4(p, r, tile.nt * BN + 4 * lane, a.x, a.y, a.z, a.w);
+                    store4(p, r, tile.nt * BN + BN / 2 + 4 * lane, b.x, b.y, b.z, b.w);
+                }
+            }
+        }
+        cluster_sync_all();   // no CTA leaves while a peer reads its shared memory
+    } else {
+        __syncthreads();
+    }
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+// ------------------------------------------------------------------- host
+// [n, rows, cols] codes with rows `ld` bytes apart, box {128 columns, box_rows},
+// 128-byte swizzle.
+bool code_map(CUtensorMap *m, const void *base, int n, int rows, int cols, long long ld, uint32_t box_rows)
+{
+    auto enc = tc::encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)n};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld, (cuuint64_t)ld * (cuuint64_t)rows};
+    const cuuint32_t box[3] = {(cuuint32_t)BK, box_rows, 1};
+    const cuuint32_t one[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, n ? 3 : 2, const_cast<void *>(base), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MODE, bool GATHER, bool SPLIT>
+cudaError_t launch_variant(const CUtensorMap &x, const CUtensorMap &w0, const CUtensorMap &w1, const Params &p,
+                           long long tiles, int num_sms, cudaStream_t stream)
+{
+    static PerDeviceFlag done;
+    const int dev = current_device();
+    auto *kern = product_kernel<MODE, GATHER, SPLIT>;
+    if (!done.done(dev)) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+        if (e != cudaSuccess) return e;
+        done.mark(dev);
+    }
+    if (SPLIT)
+        return launch_pdl_cluster(kern, dim3((unsigned)(tiles * p.split)), dim3(kThreads), kSmem, stream, p.split, x,
+                                  w0, w1, p);
+    return launch_pdl(kern, dim3((unsigned)(tiles < num_sms ? tiles : num_sms)), dim3(kThreads), kSmem, stream, x, w0,
+                      w1, p);
+}
+
+template <int MODE>
+cudaError_t launch_product(const void *x_q, long long ldx, const void *w0, const void *w1, Params p, cudaStream_t stream)
+{
+    CUtensorMap mx, mw0, mw1;
+    const bool gather = p.perm_tok != nullptr;
+    const uint32_t wbox = MODE == GATEUP ? BN / 2 : BN;
+    if (!code_map(&mx, x_q, 0, p.x_rows, p.K, ldx, gather ? 1 : ABOX) || !code_map(&mw0, w0, p.E, p.N, p.K, p.K, wbox))
+        return cudaErrorInvalidValue;
+    if (MODE == GATEUP) {
+        if (!code_map(&mw1, w1, p.E, p.N, p.K, p.K, wbox)) return cudaErrorInvalidValue;
+    } else {
+        mw1 = mw0;
+    }
+    p.n_tiles = ceil_div(p.N, MODE == GATEUP ? BN / 2 : BN);
+    const int num_sms = device_sm_count();
+    // most tiles there can be: every expert with rows may own a ragged row tile
+    const long long groups = (long long)p.rows / BM + (p.E < p.rows ? p.E : p.rows);
+    const long long tiles = groups * p.n_tiles;
+    if (tiles > 0x3fffffffLL) return cudaErrorInvalidValue;
+    // fewer tiles than half the SMs: split the reduction while there are SMs
+    // and blocks for it
+    p.split = 1;
+    while (p.split < 8 && tiles * p.split * 2 <= num_sms && p.split * 2 <= p.KB) p.split *= 2;
+    if (p.split > 1)
+        return gather ? launch_variant<MODE, true, true>(mx, mw0, mw1, p, tiles, num_sms, stream)
+                      : launch_variant<MODE, false, true>(mx, mw0, mw1, p, tiles, num_sms, stream);
+    return gather ? launch_variant<MODE, true, false>(mx, mw0, mw1, p, tiles, num_sms, stream)
+                  : launch_variant<MODE, false, false>(mx, mw0, mw1, p, tiles, num_sms, stream);
+}
+
+bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// The checks the products share; MOE_OK with *go = false for an empty call.
+moe_status product_args(const void *x_q, const float *x_s, int x_rows, int K, long long ldx, const void *w_q,
+                        const float *w_s, int E, int N, const int32_t *offsets, const int32_t *perm_tok, int rows,
+                        const void *status, bool *go)
+{
+    *go = false;
+    if (x_rows < 0 || rows < 0 || K <= 0 || K % 16 || N <= 0 || E <= 0) return MOE_ERR_INVALID_ARG;
+    if (ldx < K || ldx % 16) return MOE_ERR_INVALID_ARG;
+    if (E > kMaxExperts) return MOE_ERR_UNSUPPORTED;
+    if (E > 1 && !offsets && rows > 0) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (!perm_tok && rows > x_rows) return MOE_ERR_INVALID_ARG;
+    if (x_rows == 0) return MOE_ERR_INVALID_ARG;
+    if (rows > INT32_MAX / 2 || x_rows > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
+    if (!x_q || !x_s || !w_q || !w_s) return MOE_ERR_INVALID_ARG;
+    if (!aligned_to(x_q, 16) || !aligned_to(w_q, 16) || !aligned_to(x_s, 4) || !aligned_to(w_s, 4) ||
+        !aligned_to(offsets, 4) || !aligned_to(perm_tok, 4) || !aligned_to(status, 4))
+        return MOE_ERR_INVALID_ARG;
+    *go = true;
+    return MOE_OK;
+}
+
+Params params_of(const float *x_s, int x_rows, int K, const float *s0, const float *s1, int E, int N,
+                 const int32_t *offsets, const int32_t *perm_tok, int rows, uint32_t *status)
+{
+    Params p{};
+    p.x_s = x_s; p.w_s[0] = s0; p.w_s[1] = s1; p.offsets = offsets; p.perm_tok = perm_tok;
+    p.E = E; p.rows = rows; p.x_rows = x_rows; p.K = K; p.N = N;
+    p.KB = ceil_div(K, kBlock); p.NB = ceil_div(N, kBlock);
+    p.status = status;
+    return p;
+}
+
+}  // namespace fp8b
+}  // namespace moe
+
+using namespace moe;
+using namespace moe::fp8b;
+
+extern "C" {
+
+moe_status moe_grouped_gemm_fp8b(const void *x_q, const float *x_s, int x_rows, int K, long long ldx,
+                                 const void *w_q, const float *w_s, int E, int N, const int32_t *offsets,
+                                 const int32_t *perm_tok, int rows, void *out, moe_dtype out_dt, long long ldo,
+                                 uint32_t *status, moe_stream stream)
+{
+    bool go;
+    const moe_status st = product_args(x_q, x_s, x_rows, K, ldx, w_q, w_s, E, N, offsets, perm_tok, rows, status, &go);
+    if (st != MOE_OK) return st;
+    if ((out_dt != MOE_F32 && out_dt != MOE_BF16) || ldo < N) return MOE_ERR_INVALID_ARG;
+    if (!go) return MOE_OK;
+    if (!out || !aligned_to(out, out_dt == MOE_F32 ? 4 : 2)) return MOE_ERR_INVALID_ARG;
+    Params p = params_of(x_s, x_rows, K, w_s, nullptr, E, N, offsets, perm_tok, rows, status);
+    p.out = out; p.ldo = ldo; p.out_f32 = out_dt == MOE_F32;
+    // four columns a store: 16 bytes of fp32, 8 of bf16
+    p.out_vec = ldo % 4 == 0 && aligned_to(out, out_dt == MOE_F32 ? 16 : 8);
+    const cudaError_t e = launch_product<PRODUCT>(x_q, ldx, w_q, nullptr, p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+moe_status moe_gemm_fp8b(const void *x_q, const float *x_s, int T, int K, long long ldx, const void *w_q,
+                         const float *w_s, int N, void *out, moe_dtype out_dt, long long ldo, uint32_t *status,
+                         moe_stream stream)
+{
+    return moe_grouped_gemm_fp8b(x_q, x_s, T, K, ldx, w_q, w_s, 1, N, nullptr, nullptr, T, out, out_dt, ldo, status,
+                                 stream);
+}
+
+moe_status moe_gate_up_fp8b(const void *x_q, const float *x_s, int x_rows, int d, long long ldx, const void *wg_q,
+                            const float *wg_s, const void *wu_q, const float *wu_s, int E, int F,
+                            const int32_t *offsets, const int32_t *perm_tok, int rows, void *h_q, float *h_s,
+                            uint32_t *status, moe_stream stream)
+{
+    bool go;
+    moe_status st = product_args(x_q, x_s, x_rows, d, ldx, wg_q, wg_s, E, F, offsets, perm_tok, rows, status, &go);
+    if (st != MOE_OK) return st;
+    if (F % 16) return MOE_ERR_INVALID_ARG;
+    if (!go) return MOE_OK;
+    if (!wu_q || !wu_s || !h_q || !h_s) return MOE_ERR_INVALID_ARG;
+    if (!aligned_to(wu_q, 16) || !aligned_to(wu_s, 4) || !aligned_to(h_q, 16) || !aligned_to(h_s, 4))
+        return MOE_ERR_INVALID_ARG;
+    Params p = params_of(x_s, x_rows, d, wg_s, wu_s, E, F, offsets, perm_tok, rows, status);
+    p.h_q = static_cast<uint8_t *>(h_q); p.h_s = h_s;
+    const cudaError_t e = launch_product<GATEUP>(x_q, ldx, wg_q, wu_q, p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // extern "C"

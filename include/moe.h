@@ -427,6 +427,121 @@ MOE_API moe_status moe_forward_noalloc(const void *x, moe_dtype act_dt, int T, i
                                        moe_stream stream);
 
 /*
+ * Block-scaled fp8 operators ("fp8b"): the expert FFN with 8-bit codes on both
+ * sides of its products, as separate calls around moe_route and moe_permute.
+ * (No counterpart on the source pages: an addition of this library, beside the
+ * weight-only MOE_FP8 experts of moe_forward.)
+ *
+ * A matrix is E4M3 codes (as for MOE_FP8), row-major, with fp32 scales;
+ * value = code * scale.
+ *   activations [rows, K]: one scale per row and 128 columns, scales
+ *     [rows, ceil(K/128)];
+ *   weights [E, N, K]: one scale per block of 128 rows x 128 columns, scales
+ *     [E, ceil(N/128), ceil(K/128)] (blocks do not cross experts).
+ * K (d, F) is a multiple of 16; the last block of a row may be shorter.  Code
+ * buffers are 16-byte aligned, scales 4-byte.
+ * Quantisation of a block: s = max|x| / 448 in fp32, code = E4M3 nearest to
+ * x / s, ties to even.  All zeros (or so small that s underflows): s = 0,
+ * codes 0.  A block that holds an infinity or NaN: s = NaN, NaN codes.
+ *
+ * A layer as a chain of these calls, every one asynchronous on one stream:
+ *   moe_norm_fp8b     residual + the previous layer's combine, RMS norm, codes
+ *   moe_route, moe_permute                   (on the norm's bf16 output)
+ *   moe_gate_up_fp8b  x rows through perm_tok -> h codes in grouped order
+ *   moe_grouped_gemm_fp8b                    -> y [T*k, d] in grouped order
+ *   the next layer's moe_norm_fp8b with (y, inv, topk_w)
+ *
+ * Failure handling: the products' kernels bound every wait (2 s).  Where one
+ * gives up, the output rows concerned are NaN (codes 0x7F with NaN scales),
+ * and `status`, a device word that may be NULL, gets the bit that moe_check
+ * reports as MOE_ERR_TIMEOUT.  The word is OR-ed into and never cleared: the
+ * caller zeroes it once and may share it between calls; moe_check reads it
+ * (as a workspace of its own).
+ * Reproducibility: every call gives bitwise identical results from run to run.
+ */
+
+/*
+ * moe_quant_fp8b -- codes and scales of x [batch, rows, cols] (fp32 or bf16;
+ *   rows `ldx` elements apart, ldx >= cols and a multiple of 8, batches
+ *   rows*ldx apart; 16-byte aligned).
+ *   block_rows: 1 (activations) or 128 (weights; the last block of each batch
+ *   entry may have fewer rows).
+ *   codes [batch, rows, cols] and scales [batch, ceil(rows/block_rows),
+ *   ceil(cols/128)] out.
+ */
+MOE_API moe_status moe_quant_fp8b(const void *x, moe_dtype x_dt, int batch, int rows, int cols,
+                                  long long ldx, int block_rows, void *codes, float *scales,
+                                  moe_stream stream);
+
+/*
+ * moe_norm_fp8b -- residual addition, RMS norm and quantisation of T rows:
+ *     r[t]   = x[t]                                          (delta NULL)
+ *              x[t] + delta[t]                               (k == 0)
+ *              x[t] + sum_j topk_w[t,j] delta[inv[t*k + j]]  (k in 1..8)
+ *     y[t,i] = r[t,i] * weight[i] / sqrt(mean_i r[t,i]^2 + eps)
+ *   The sums are fp32 in slot order and y is taken from the unrounded r.
+ *   x [T, d] (fp32 or bf16, rows ldx apart); delta [delta_rows, d] (fp32 or
+ *   bf16, rows ldd apart; delta_rows >= T when k == 0): with k > 0 the
+ *   grouped outputs of a layer, inv and topk_w [T, k] as moe_permute and
+ *   moe_route write them.  A slot whose inv is outside [0, delta_rows) adds
+ *   nothing.  weight [d] fp32 or bf16.
+ *   resid [T, d] out in x's type (contiguous; required with delta, untouched
+ *   without; may be x itself when ldx == d); normed [T, d] bf16 out, or NULL;
+ *   codes [T, d] and scales [T, ceil(d/128)] out: y per row and 128 columns.
+ *   Apart from resid == x no output may overlap an input.
+ *   d a multiple of 16, at most 16384; ldx, ldd multiples of 8; x, delta,
+ *   weight, resid, normed and codes 16-byte aligned.
+ */
+MOE_API moe_status moe_norm_fp8b(const void *x, moe_dtype x_dt, int T, int d, long long ldx,
+                                 const void *delta, moe_dtype delta_dt, int delta_rows,
+                                 long long ldd, const float *topk_w, const int32_t *inv, int k,
+                                 const void *weight, moe_dtype weight_dt, float eps, void *resid,
+                                 void *normed, void *codes, float *scales, moe_stream stream);
+
+/*
+ * moe_gemm_fp8b -- out[T, N] = x W^T, fp32 sums.  x_q [T, K] codes (rows ldx
+ *   bytes apart, ldx a multiple of 16), x_s [T, ceil(K/128)]; w_q [N, K],
+ *   w_s [ceil(N/128), ceil(K/128)]; out fp32 or bf16 (out_dt), rows ldo
+ *   elements apart.  Any N >= 1.
+ */
+MOE_API moe_status moe_gemm_fp8b(const void *x_q, const float *x_s, int T, int K, long long ldx,
+                                 const void *w_q, const float *w_s, int N, void *out,
+                                 moe_dtype out_dt, long long ldo, uint32_t *status,
+                                 moe_stream stream);
+
+/*
+ * moe_grouped_gemm_fp8b -- the product of every expert with its rows:
+ *     out[r] = x[perm_tok[r]] W[e]^T   for r in [offsets[e], offsets[e+1])
+ *   offsets [E+1] and perm_tok [rows] (NULL: row r is x's row r; then
+ *   rows <= x_rows) are device arrays as moe_permute writes them; offsets may
+ *   be NULL when E == 1 (all rows).  Experts may be without rows.  Output rows
+ *   that no group holds (offsets[E] < rows: a padded batch) are left as they
+ *   were.  Offsets are clamped to [0, rows]; a row whose perm_tok is outside
+ *   [0, x_rows) is undefined, and no other memory is touched.
+ *   w_q [E, N, K], w_s [E, ceil(N/128), ceil(K/128)], E <= 256; the other
+ *   arguments as moe_gemm_fp8b.
+ */
+MOE_API moe_status moe_grouped_gemm_fp8b(const void *x_q, const float *x_s, int x_rows, int K,
+                                         long long ldx, const void *w_q, const float *w_s, int E,
+                                         int N, const int32_t *offsets, const int32_t *perm_tok,
+                                         int rows, void *out, moe_dtype out_dt, long long ldo,
+                                         uint32_t *status, moe_stream stream);
+
+/*
+ * moe_gate_up_fp8b -- both products of a SwiGLU expert and its h, quantised:
+ *     h[r] = SiLU(W_g[e] x[perm_tok[r]]) * (W_u[e] x[perm_tok[r]])
+ *   h_q [rows, F] codes and h_s [rows, ceil(F/128)] out, from the unrounded
+ *   fp32 h.  wg_q, wu_q [E, F, d] with scales [E, ceil(F/128), ceil(d/128)];
+ *   F a multiple of 16.  Groups, perm_tok and rows as moe_grouped_gemm_fp8b
+ *   (E == 1 with offsets NULL is the dense layer's).
+ */
+MOE_API moe_status moe_gate_up_fp8b(const void *x_q, const float *x_s, int x_rows, int d,
+                                    long long ldx, const void *wg_q, const float *wg_s,
+                                    const void *wu_q, const float *wu_s, int E, int F,
+                                    const int32_t *offsets, const int32_t *perm_tok, int rows,
+                                    void *h_q, float *h_s, uint32_t *status, moe_stream stream);
+
+/*
  * Test hook of the failure handling.  Every wait of the library's
  * tensor-core kernels is bounded (2 s); a wait that gives up records
  * MOE_ERR_TIMEOUT in the status word, the kernel's other roles stop, its
