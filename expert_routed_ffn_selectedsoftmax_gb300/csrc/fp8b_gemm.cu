@@ -13,10 +13,12 @@
 //
 // A tile is 128 rows x 256 columns (PRODUCT), or 128 rows x 128 columns of
 // both W_gate and W_up (GATEUP: the epilogue has whole 128-column groups of h,
-// so it quantises them without a second pass).  Warp 0 loads (TMA boxes of 32
-// rows, or gathers of four rows each through perm_tok -- only as many as the
-// tile has rows), warp 1 multiplies, warps 2-9 hold the sums: warp w the TMEM
-// lanes of quarter w % 4 and one half of the columns.
+// so it quantises them without a second pass).  Warp 0 loads by TMA (rows in
+// boxes of 32, only as many as the tile has), warps 2-3 copy rows gathered
+// through perm_tok (cp.async; TMA's four-row gathers took 75 clocks each, 32 of
+// them twice as long as a block's products), warp 1 multiplies, warps 4-11 hold the sums: warp w the TMEM
+// lanes of quarter w % 4 and one half of the columns (128 of them, or 64 of
+// gate and the same 64 of up).
 //
 // Rows of a tile past the end of its group are left out of the loads and the
 // stores (their lanes of the MMA compute on whatever the buffer holds; rows
@@ -49,15 +51,23 @@ constexpr int BM = 128, BN = 256, BK = kBlock;   // one MMA k-block = one scale 
 constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE = A_BYTES + B_BYTES;
 constexpr int STAGES = 4;
 constexpr int ABOX = 32;                         // rows per A load
+constexpr uint32_t kGatherLag = 2;               // gathered stages in flight before the oldest is handed over
+static_assert(kGatherLag < STAGES, "a stage is handed over before it is needed again");
 constexpr int TMEM_COLS = 512;                   // two partial sums of 256 columns
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kThreads = 128 + 32 * kEpiWarps;   // warps 0-3: load, multiply, TMEM, idle
+// registers a thread after the split at start (setmaxnreg): the block launches
+// with 168 x 12 warps = 2016; 4 warps keep 88 and 8 take 208: 352 + 1664 = 2016
+constexpr int kRegsLaunch = 168, kRegsAux = 88, kRegsEpi = 208;
+static_assert(4 * kRegsAux + kEpiWarps * kRegsEpi <= 12 * kRegsLaunch, "more registers than the block has");
 constexpr int kPartRow = BN + 4;                 // floats per row of a split partial sum (16-byte
                                                  // stores of 8 rows fall in distinct banks)
 
 enum Mode { PRODUCT = 0, GATEUP = 1 };
 
 struct Params {
+    const uint8_t *x_q;       // gathering: [x_rows, K] codes, rows ldx bytes apart
+    long long ldx;
     const float *x_s;         // [x_rows, KB]
     const float *w_s[2];      // [E, NB, KB] of W (PRODUCT) or W_gate, W_up
     const int32_t *offsets;   // [E+1], or NULL: one group of all rows
@@ -65,7 +75,7 @@ struct Params {
     int E, rows, x_rows, K, N, KB, NB, n_tiles;
     void *out;                // PRODUCT: [rows, ldo] bf16 or fp32
     long long ldo;
-    int out_f32, out_vec;     // out_vec: 16-byte stores are aligned
+    int out_f32, out_vec;     // out_vec: rows are multiples of 16 bytes apart, from a 16-byte boundary
     uint8_t *h_q;             // GATEUP: [rows, N] codes, [rows, NB] scales
     float *h_s;
     uint32_t *status;
@@ -73,14 +83,15 @@ struct Params {
 };
 
 struct alignas(16) Ctl {
-    uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], drain;
+    uint64_t full[STAGES], empty[STAGES], tfull[2][2], tempty[2][2], drain;   // [buffer][column half]
     uint32_t tmem_base;
     int abort_flag;
     int total;
     int off[kMaxExperts + 1], tile_start[kMaxExperts + 1], mtiles[kMaxExperts];
     uint32_t amax[2][BM];     // GATEUP: each row's largest |h| per column half
 };
-constexpr size_t kSmem = 1024 + (size_t)STAGES * STAGE + sizeof(Ctl);
+constexpr int kStaging = 32 * 64;                // bytes per epilogue warp: 64 of each of its rows
+constexpr size_t kSmem = 1024 + (size_t)STAGES * STAGE + sizeof(Ctl) + kEpiWarps * kStaging;
 static_assert(kSmem <= 232448, "shared memory per CTA");
 static_assert((size_t)BM * kPartRow * 4 <= (size_t)STAGES * STAGE, "split partial sums reuse the ring");
 
@@ -108,15 +119,29 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, u
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
 }
-// Four rows y0..y3 of a 2-D tensor (box one row high), one below the other.
-__device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int4 y)
+// 16 bytes, or 16 zeros where `in` is false
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool in)
 {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w), "r"(smem_u32(bar))
-        : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
+template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// mbar_wait, inline as a whole: across a call the compiler cannot keep the
+// sums of the epilogue warps in the registers that setmaxnreg gives them.
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+                                         unsigned long long timeout_ns = kTimeoutNs)
+{
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 255u) == 0) {
+            if (*abort_flag) return false;
+            if (globaltimer() - t0 > timeout_ns) return false;
+        }
+    }
+}
+
 // Wait for the warp's TMEM loads; the registers pass through it, so that
 // nothing that reads them moves above it.
 __device__ __forceinline__ void tmem_ld_wait16(uint32_t (&v)[16])
@@ -169,26 +194,71 @@ __device__ __forceinline__ uint4 encode16(F v, float inv)
 // zero; NaN stays NaN.
 __device__ __forceinline__ float quant_mul(float s) { return s >= 1.17549435e-38f || s != s ? 1.0f / s : 0.0f; }
 
-// One output value's stores: columns [n0, n0 + 4) of row r.
-__device__ __forceinline__ void store4(const Params &p, long long r, int n0, float a, float b, float c, float d)
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
 {
-    const float v[4] = {a, b, c, d};
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// Four output values: columns [n0, n0 + 4) of row r (split sums: a warp writes
+// 128 neighbouring columns of one row at a time).
+__device__ __forceinline__ void store4(const Params &p, long long r, int n0, float4 v)
+{
+    const float w[4] = {v.x, v.y, v.z, v.w};
     if (p.out_f32) {
         float *o = static_cast<float *>(p.out) + r * p.ldo + n0;
-        if (p.out_vec && n0 + 4 <= p.N) *reinterpret_cast<float4 *>(o) = make_float4(a, b, c, d);
+        if (p.out_vec && n0 + 4 <= p.N) *reinterpret_cast<float4 *>(o) = v;
         else
             for (int i = 0; i < 4; ++i)
-                if (n0 + i < p.N) o[i] = v[i];
+                if (n0 + i < p.N) o[i] = w[i];
     } else {
         __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + r * p.ldo + n0;
         if (p.out_vec && n0 + 4 <= p.N) {
-            const __nv_bfloat162 q0 = __floats2bfloat162_rn(a, b), q1 = __floats2bfloat162_rn(c, d);
-            *reinterpret_cast<uint2 *>(o) = make_uint2(*reinterpret_cast<const uint32_t *>(&q0),
-                                                       *reinterpret_cast<const uint32_t *>(&q1));
+            *reinterpret_cast<uint2 *>(o) = make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
         } else
             for (int i = 0; i < 4; ++i)
-                if (n0 + i < p.N) o[i] = __float2bfloat16_rn(v[i]);
+                if (n0 + i < p.N) o[i] = __float2bfloat16_rn(w[i]);
     }
+}
+
+// 64 bytes of each of the warp's 32 rows (lane l holds row l's) to global
+// memory: turned through shared memory so that a store instruction covers 8
+// rows x 64 bytes, whole 32-byte sectors, instead of 32 rows x 16 bytes, which
+// took longer than the products of a tile (8192 x 2048 x 5632: 178 us against
+// 100 us without the stores).  16-byte piece q of row r lies at q ^ (r / 2 % 4),
+// so neither side has bank conflicts.  `g`: row 0's bytes; `rows` of the 32 and
+// the first `bytes` of the 64 exist; `vec`: 16-byte stores are aligned, else
+// elements of `size` bytes are stored one by one.
+__device__ __forceinline__ void store_rows(uint8_t *stg, int lane, const uint4 (&d)[4], uint8_t *g, long long pitch,
+                                           int rows, int bytes, bool vec, int size)
+{
+#pragma unroll
+    for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4 *>(stg + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) = d[q];
+    __syncwarp();
+    const int q = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 2);
+        const uint4 v = *reinterpret_cast<const uint4 *>(stg + r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
+        if (r >= rows || q * 16 >= bytes) continue;
+        uint8_t *o = g + r * pitch + q * 16;
+        if (vec && q * 16 + 16 <= bytes) {
+            *reinterpret_cast<uint4 *>(o) = v;
+        } else {
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (q * 16 + k * 4 >= bytes) break;
+                if (size == 4) {
+                    *reinterpret_cast<uint32_t *>(o + k * 4) = w[k];
+                } else {
+                    *reinterpret_cast<uint16_t *>(o + k * 4) = (uint16_t)w[k];
+                    if (q * 16 + k * 4 + 2 < bytes) *reinterpret_cast<uint16_t *>(o + k * 4 + 2) = (uint16_t)(w[k] >> 16);
+                }
+            }
+        }
+    }
+    __syncwarp();
 }
 
 struct Tile { int e, nt, row0, cnt; };   // expert, column tile, first grouped row, rows
@@ -225,8 +295,8 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     const int E = p.E;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) { mbar_init(&c.full[s], 1); mbar_init(&c.empty[s], 1); }
-        for (int b = 0; b < 2; ++b) { mbar_init(&c.tfull[b], 1); mbar_init(&c.tempty[b], kEpiWarps); }
+        for (int s = 0; s < STAGES; ++s) { mbar_init(&c.full[s], GATHER ? 3 : 1); mbar_init(&c.empty[s], 1); }
+        for (int b = 0; b < 4; ++b) { mbar_init(&c.tfull[b >> 1][b & 1], 1); mbar_init(&c.tempty[b >> 1][b & 1], kEpiWarps / 2); }
         mbar_init(&c.drain, 1);
         c.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -235,7 +305,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         if (MODE == GATEUP)
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_w1)) : "memory");
     }
-    if (warp == 1) tmem_alloc(&c.tmem_base, TMEM_COLS);
+    if (warp == 2) tmem_alloc(&c.tmem_base, TMEM_COLS);
     tc_fence_before();
     pdl_enter();
     // group bounds, kept inside [0, rows] whatever the array holds
@@ -284,46 +354,40 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     // this CTA's blocks of the reduction
     const int kb0 = (int)((long long)p.KB * rank / S), kb1 = (int)((long long)p.KB * (rank + 1) / S);
     volatile int *abort_flag = &c.abort_flag;
-
+    if (warp < 4) {
+        // (inside the branch: the compiler gives each side its own limit)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsAux));
     if (warp == 0) {
         // ------------------------------------------------ loads
         uint32_t it = 0;
         bool ok = true;
         for (int t = first; t < total && ok; t += stride) {
             const Tile tile = tile_at(c, E, t);
-            int4 tok = make_int4(0, 0, 0, 0);
-            const int loads = GATHER ? (tile.cnt + 3) / 4 : (tile.cnt + ABOX - 1) / ABOX;
-            if (GATHER && lane < loads) {
-                // (an index out of range is read as row 0: its row is dropped by its scale)
-                int v[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = min(4 * lane + i, tile.cnt - 1);
-                    v[i] = __ldg(p.perm_tok + tile.row0 + r);
-                    if (v[i] < 0 || v[i] >= p.x_rows) v[i] = 0;
-                }
-                tok = make_int4(v[0], v[1], v[2], v[3]);
-            }
-            const uint32_t bytes = (uint32_t)loads * (GATHER ? 4 * BK : ABOX * BK) + B_BYTES;
+            const int loads = GATHER ? 0 : (tile.cnt + ABOX - 1) / ABOX;
+            const uint32_t bytes = (uint32_t)(loads * ABOX * BK) + B_BYTES;
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int s = it % STAGES;
-                ok = __all_sync(0xffffffffu, mbar_wait(&c.empty[s], ((it / STAGES) & 1u) ^ 1u, abort_flag));
+                ok = __all_sync(0xffffffffu, bar_wait(&c.empty[s], ((it / STAGES) & 1u) ^ 1u, abort_flag));
                 if (!ok) break;
                 uint8_t *sa = smem + s * STAGE, *sb = sa + A_BYTES;
                 if (lane == 0) {
                     mbar_expect_tx(&c.full[s], bytes);
                     if (MODE == GATEUP) {
-                        tma_load_3d(sb, &tm_w0, &c.full[s], kb * BK, tile.nt * (BN / 2), tile.e);
-                        tma_load_3d(sb + B_BYTES / 2, &tm_w1, &c.full[s], kb * BK, tile.nt * (BN / 2), tile.e);
+                        // per column half: 64 rows of W_gate, 64 of W_up
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint8_t *at = sb + h * (B_BYTES / 2);
+                            const int n = tile.nt * (BN / 2) + h * 64;
+                            tma_load_3d(at, &tm_w0, &c.full[s], kb * BK, n, tile.e);
+                            tma_load_3d(at + B_BYTES / 4, &tm_w1, &c.full[s], kb * BK, n, tile.e);
+                        }
                     } else {
                         tma_load_3d(sb, &tm_w0, &c.full[s], kb * BK, tile.nt * BN, tile.e);
                     }
                 }
                 __syncwarp();
-                if (lane < loads) {
-                    if (GATHER) tma_gather4(sa + lane * 4 * BK, &tm_x, &c.full[s], kb * BK, tok);
-                    else tma_load_2d(sa + lane * ABOX * BK, &tm_x, &c.full[s], kb * BK, tile.row0 + lane * ABOX);
-                }
+                if (!GATHER && lane < loads)
+                    tma_load_2d(sa + lane * ABOX * BK, &tm_x, &c.full[s], kb * BK, tile.row0 + lane * ABOX);
             }
         }
         if (!ok) {
@@ -332,31 +396,37 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             // let loads already issued land before the CTA exits
             for (uint32_t j = (it >= STAGES ? it - STAGES : 0); j < it; ++j) {
                 volatile int no_abort = 0;
-                mbar_wait(&c.full[j % STAGES], (j / STAGES) & 1u, &no_abort, 1000000ull);
+                bar_wait(&c.full[j % STAGES], (j / STAGES) & 1u, &no_abort, 1000000ull);
             }
         }
     } else if (warp == 1 && lane == 0) {
         // ------------------------------------------------ multiply
-        constexpr uint32_t idesc = idesc_e4m3(BM, BN);
+        constexpr uint32_t idesc = idesc_e4m3(BM, BN / 2);
         uint32_t it = 0;
         bool ok = true;
         for (int t = first; t < total && ok; t += stride) {
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int s = it % STAGES;
                 const uint32_t b = it & 1u;
-                if (!mbar_wait(&c.tempty[b], ((it >> 1) & 1u) ^ 1u, abort_flag) ||
-                    !mbar_wait(&c.full[s], (it / STAGES) & 1u, abort_flag)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
+                ok = bar_wait(&c.full[s], (it / STAGES) & 1u, abort_flag);
                 const uint32_t a0 = smem_u32(smem + s * STAGE);
-                const uint64_t da = sw128_desc(a0), db = sw128_desc(a0 + A_BYTES);
+                const uint64_t da = sw128_desc(a0);
+                // the two column halves have buffers of their own, so that the
+                // sums of one are taken while the other is multiplied
 #pragma unroll
-                for (int kk = 0; kk < BK / 32; ++kk)
-                    umma_f8(tmem + b * BN, desc_step(da, kk * 32), desc_step(db, kk * 32), idesc, kk != 0);
+                for (int h = 0; h < 2; ++h) {
+                    ok = ok && bar_wait(&c.tempty[b][h], ((it >> 1) & 1u) ^ 1u, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t db = sw128_desc(a0 + A_BYTES + h * (B_BYTES / 2));
+#pragma unroll
+                    for (int kk = 0; kk < BK / 32; ++kk)
+                        umma_f8(tmem + b * BN + h * (BN / 2), desc_step(da, kk * 32), desc_step(db, kk * 32), idesc,
+                                kk != 0);
+                    umma_commit(&c.tfull[b][h]);
+                }
+                if (!ok) break;
                 umma_commit(&c.empty[s]);
-                umma_commit(&c.tfull[b]);
             }
         }
         if (!ok) {
@@ -364,12 +434,65 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             c.abort_flag = 1;
             umma_commit(&c.drain);   // MMAs in flight end before TMEM is freed
             volatile int no_abort = 0;
-            mbar_wait(&c.drain, 0, &no_abort);
+            bar_wait(&c.drain, 0, &no_abort);
         }
-    } else if (warp >= 2) {
+    } else if (GATHER && warp >= 2) {
+        // ------------------------------------------------ gathered rows
+        // warp 2: rows 0-63 of the tile, warp 3: rows 64-127; 8 lanes copy one
+        // row's 128 bytes, 4 rows an instruction, into the swizzled layout that
+        // TMA gives the other operand
+        const int rsub = lane >> 3, chunk = lane & 7, first_row = (warp - 2) * 64;
+        const uint8_t *src0 = p.x_q + chunk * 16;
+        uint32_t it = 0, arrived = 0;
+        bool ok = true;
+        // the copies of stages up to `arrived` have landed: hand them to the MMA
+        auto hand_over = [&]() {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c.full[arrived % STAGES]);
+            ++arrived;
+        };
+        for (int t = first; t < total && ok; t += stride) {
+            const Tile tile = tile_at(c, E, t);
+            int tok[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int r = first_row + 4 * i + rsub;
+                tok[i] = r < tile.cnt ? __ldg(p.perm_tok + tile.row0 + r) : -1;
+                if (tok[i] >= p.x_rows) tok[i] = -1;   // (out of range: not read, its row is undefined)
+            }
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const int s = it % STAGES;
+                ok = __all_sync(0xffffffffu, bar_wait(&c.empty[s], ((it / STAGES) & 1u) ^ 1u, abort_flag));
+                if (!ok) break;
+                const bool in = kb * BK + chunk * 16 < p.K;
+                const uint32_t sa = smem_u32(smem + s * STAGE) + (first_row + rsub) * BK;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (tok[i] >= 0)
+                        cp_async16(sa + i * 4 * BK + ((chunk ^ ((4 * i + rsub) & 7)) << 4),
+                                   src0 + (in ? tok[i] * p.ldx + kb * BK : 0), in);
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                if (it - arrived >= kGatherLag) {
+                    cp_async_wait<kGatherLag>();
+                    hand_over();
+                }
+            }
+        }
+        cp_async_wait<0>();
+        if (ok) {
+            while (arrived < it) hand_over();
+        } else {
+            if (lane == 0) flag_status(p.status, kDevTimeout);
+            c.abort_flag = 1;
+        }
+    }
+    } else {
         // ------------------------------------------------ sums and output
-        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
         const int row = quarter * 32 + lane;
+        uint8_t *stg = reinterpret_cast<uint8_t *>(&c + 1) + (warp - 4) * kStaging;
         uint32_t it = 0;
         bool ok = true;   // once false, no more waits: the remaining rows become NaN
         for (int t = first; t < total; t += stride) {
@@ -401,25 +524,26 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                     n0 = __ldg(ws0 + kb + 1);
                     if (MODE == GATEUP) n1 = __ldg(ws1 + kb + 1);
                 }
-                ok = ok && __all_sync(0xffffffffu, mbar_wait(&c.tfull[b], (it >> 1) & 1u, abort_flag));
+                ok = ok && __all_sync(0xffffffffu, bar_wait(&c.tfull[b][half], (it >> 1) & 1u, abort_flag));
                 tc_fence_after();
-                const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + b * BN;
-                // the eight 16-column chunks, one load ahead of the sums
+                const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + b * BN + half * (BN / 2);
+                // eight chunks of 16 columns, one load ahead of the sums
                 uint32_t v[2][16];
-                auto col = [&](int j) { return MODE == GATEUP ? (j >> 2) * (BN / 2) + half * 64 + (j & 3) * 16
-                                                              : half * (BN / 2) + j * 16; };
-                tmem_ld16(base + col(0), v[0]);
+                tmem_ld16(base, v[0]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     tmem_ld_wait16(v[j & 1]);
-                    if (j < 7) tmem_ld16(base + col(j + 1), v[(j + 1) & 1]);
+                    if (j < 7) {
+                        tmem_ld16(base + (j + 1) * 16, v[(j + 1) & 1]);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&c.tempty[b][half]);
+                    }
                     const uint64_t m = j < 4 ? m0 : m1;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) fma2(acc[j * 8 + i], pack2(v[j & 1][2 * i], v[j & 1][2 * i + 1]), m);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&c.tempty[b]);
             }
             if (!ok) {
                 c.abort_flag = 1;
@@ -456,19 +580,44 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                 m = max(m, c.amax[half ^ 1][row]);
                 asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
                 const float s = block_scale(m), inv = quant_mul(s);
-                if (valid) {
-                    const int n0 = tile.nt * (BN / 2) + half * 64;
+                const int n0 = tile.nt * (BN / 2) + half * 64;
+                uint4 d[4];
 #pragma unroll
-                    for (int i = 0; i < 64; i += 16)
-                        if (n0 + i < p.N)
-                            *reinterpret_cast<uint4 *>(p.h_q + r * p.N + n0 + i) = encode16([&](int q) { return h[i + q]; }, inv);
+                for (int i = 0; i < 4; ++i) d[i] = encode16([&](int q) { return h[16 * i + q]; }, inv);
+                store_rows(stg, lane, d, p.h_q + (r - lane) * p.N + n0, p.N, tile.cnt - quarter * 32, p.N - n0, true, 1);
+                if (valid) {
                     if (half == 0) p.h_s[r * p.NB + tile.nt] = s;
                 }
             } else {
-                if (valid) {
-                    const int n0 = tile.nt * BN + half * (BN / 2);
+                const int n0 = tile.nt * BN + half * (BN / 2), rows = tile.cnt - quarter * 32;
+                const bool f32 = p.out_f32;
+                const int size = f32 ? 4 : 2;
+                uint8_t *g = static_cast<uint8_t *>(p.out) + ((r - lane) * p.ldo + n0) * size;
+                const int bytes = min(p.N - n0, BN / 2) * size;
+                if (f32) {
 #pragma unroll
-                    for (int i = 0; i < 128; i += 4) store4(p, r, n0 + i, val(i), val(i + 1), val(i + 2), val(i + 3));
+                    for (int j = 0; j < 8; ++j) {
+                        uint4 d[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int i = j * 16 + q * 4;
+                            d[q] = make_uint4(__float_as_uint(val(i)), __float_as_uint(val(i + 1)),
+                                              __float_as_uint(val(i + 2)), __float_as_uint(val(i + 3)));
+                        }
+                        store_rows(stg, lane, d, g + j * 64, p.ldo * 4, rows, bytes - j * 64, p.out_vec, 4);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint4 d[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int i = j * 32 + q * 8;
+                            d[q] = make_uint4(bf16x2(val(i), val(i + 1)), bf16x2(val(i + 2), val(i + 3)),
+                                              bf16x2(val(i + 4), val(i + 5)), bf16x2(val(i + 6), val(i + 7)));
+                        }
+                        store_rows(stg, lane, d, g + j * 64, p.ldo * 2, rows, bytes - j * 64, p.out_vec, 2);
+                    }
                 }
             }
         }
@@ -476,14 +625,14 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
 
     if constexpr (SPLIT) {
         cluster_sync_all();   // every CTA's partial sums are written
-        if (first < total && warp >= 2) {
+        if (first < total && warp >= 4) {
             // row by row, the clusters' CTAs in turn, a warp to a row: lane l adds
             // columns 4l.. and 128 + 4l.. over the CTAs in the order of the blocks
             const Tile tile = tile_at(c, E, first);
             // (a CTA that gave up may still have had loads landing on its sums)
             bool failed = false;
             for (int q = 0; q < S; ++q) failed |= ld_cluster_u32(peer_addr(&c.abort_flag, q)) != 0u;
-            for (int row = rank + S * (warp - 2); row < tile.cnt; row += S * kEpiWarps) {
+            for (int row = rank + S * (warp - 4); row < tile.cnt; row += S * kEpiWarps) {
                 float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
 #pragma unroll 4
                 for (int q = 0; q < S; ++q) {
@@ -505,8 +654,8 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                             e4m3x2(h[0] * inv, h[1] * inv) | (e4m3x2(h[2] * inv, h[3] * inv) << 16);
                     if (lane == 0) p.h_s[r * p.NB + tile.nt] = s;
                 } else {
-                    store4(p, r, tile.nt * BN + 4 * lane, a.x, a.y, a.z, a.w);
-                    store4(p, r, tile.nt * BN + BN / 2 + 4 * lane, b.x, b.y, b.z, b.w);
+                    store4(p, r, tile.nt * BN + 4 * lane, a);
+                    store4(p, r, tile.nt * BN + BN / 2 + 4 * lane, b);
                 }
             }
         }
@@ -514,7 +663,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     } else {
         __syncthreads();
     }
-    if (warp == 1) {
+    if (warp == 2) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, TMEM_COLS);
@@ -561,9 +710,13 @@ cudaError_t launch_product(const void *x_q, long long ldx, const void *w0, const
 {
     CUtensorMap mx, mw0, mw1;
     const bool gather = p.perm_tok != nullptr;
-    const uint32_t wbox = MODE == GATEUP ? BN / 2 : BN;
-    if (!code_map(&mx, x_q, 0, p.x_rows, p.K, ldx, gather ? 1 : ABOX) || !code_map(&mw0, w0, p.E, p.N, p.K, p.K, wbox))
+    const uint32_t wbox = MODE == GATEUP ? BN / 4 : BN;
+    p.x_q = static_cast<const uint8_t *>(x_q);
+    p.ldx = ldx;
+    if (!code_map(&mw0, w0, p.E, p.N, p.K, p.K, wbox))
         return cudaErrorInvalidValue;
+    if (gather) mx = mw0;   // (unused: gathered rows are copied 16 bytes at a time)
+    else if (!code_map(&mx, x_q, 0, p.x_rows, p.K, ldx, ABOX)) return cudaErrorInvalidValue;
     if (MODE == GATEUP) {
         if (!code_map(&mw1, w1, p.E, p.N, p.K, p.K, wbox)) return cudaErrorInvalidValue;
     } else {
@@ -642,8 +795,7 @@ moe_status moe_grouped_gemm_fp8b(const void *x_q, const float *x_s, int x_rows, 
     if (!out || !aligned_to(out, out_dt == MOE_F32 ? 4 : 2)) return MOE_ERR_INVALID_ARG;
     Params p = params_of(x_s, x_rows, K, w_s, nullptr, E, N, offsets, perm_tok, rows, status);
     p.out = out; p.ldo = ldo; p.out_f32 = out_dt == MOE_F32;
-    // four columns a store: 16 bytes of fp32, 8 of bf16
-    p.out_vec = ldo % 4 == 0 && aligned_to(out, out_dt == MOE_F32 ? 16 : 8);
+    p.out_vec = ldo % (out_dt == MOE_F32 ? 4 : 8) == 0 && aligned_to(out, 16);
     const cudaError_t e = launch_product<PRODUCT>(x_q, ldx, w_q, nullptr, p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
