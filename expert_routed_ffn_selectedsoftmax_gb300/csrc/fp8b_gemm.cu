@@ -14,9 +14,10 @@
 // A tile is 128 rows x 256 columns (PRODUCT), or 128 rows x 128 columns of
 // both W_gate and W_up (GATEUP: the epilogue has whole 128-column groups of h,
 // so it quantises them without a second pass).  Warp 0 loads by TMA (rows in
-// boxes of 32, only as many as the tile has), warps 2-3 copy rows gathered
-// through perm_tok (cp.async; TMA's four-row gathers took 75 clocks each, 32 of
-// them twice as long as a block's products), warp 1 multiplies, warps 4-11 hold the sums: warp w the TMEM
+// boxes of 32, only as many as the tile has); rows gathered through perm_tok are
+// copied by warps 0 and 3 (cp.async; TMA's four-row gathers took 75 clocks each,
+// 32 of them twice as long as a block's products).  Warps 1 and 2 multiply a
+// column half each.  Warps 4-11 hold the sums: warp w the TMEM
 // lanes of quarter w % 4 and one half of the columns (128 of them, or 64 of
 // gate and the same 64 of up).
 //
@@ -55,7 +56,7 @@ constexpr uint32_t kGatherLag = 2;               // gathered stages in flight be
 static_assert(kGatherLag < STAGES, "a stage is handed over before it is needed again");
 constexpr int TMEM_COLS = 512;                   // two partial sums of 256 columns
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 128 + 32 * kEpiWarps;   // warps 0-3: load, multiply, TMEM, idle
+constexpr int kThreads = 128 + 32 * kEpiWarps;   // warps 0-3: load, multiply, multiply, gather
 // registers a thread after the split at start (setmaxnreg): the block launches
 // with 168 x 12 warps = 2016; 4 warps keep 88 and 8 take 208: 352 + 1664 = 2016
 constexpr int kRegsLaunch = 168, kRegsAux = 88, kRegsEpi = 208;
@@ -83,7 +84,7 @@ struct Params {
 };
 
 struct alignas(16) Ctl {
-    uint64_t full[STAGES], empty[STAGES], tfull[2][2], tempty[2][2], drain;   // [buffer][column half]
+    uint64_t full[STAGES], empty[STAGES], tfull[2][2], tempty[2][2], drain[2];   // [buffer][column half]
     uint32_t tmem_base;
     int abort_flag;
     int total;
@@ -101,15 +102,22 @@ constexpr uint32_t idesc_e4m3(int M, int N)
 {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                        uint32_t accumulate)
+template <bool ACCUMULATE>
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc)
 {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "n"(ACCUMULATE ? 1 : 0)
         : "memory");
+}
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t is;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(is));
+    return is != 0;
 }
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z)
 {
@@ -295,9 +303,9 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     const int E = p.E;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) { mbar_init(&c.full[s], GATHER ? 3 : 1); mbar_init(&c.empty[s], 1); }
+        for (int s = 0; s < STAGES; ++s) { mbar_init(&c.full[s], GATHER ? 3 : 1); mbar_init(&c.empty[s], 2); }
         for (int b = 0; b < 4; ++b) { mbar_init(&c.tfull[b >> 1][b & 1], 1); mbar_init(&c.tempty[b >> 1][b & 1], kEpiWarps / 2); }
-        mbar_init(&c.drain, 1);
+        for (int h = 0; h < 2; ++h) mbar_init(&c.drain[h], 1);
         c.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_x)) : "memory");
@@ -305,7 +313,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         if (MODE == GATEUP)
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_w1)) : "memory");
     }
-    if (warp == 2) tmem_alloc(&c.tmem_base, TMEM_COLS);
+    if (warp == 3) tmem_alloc(&c.tmem_base, TMEM_COLS);
     tc_fence_before();
     pdl_enter();
     // group bounds, kept inside [0, rows] whatever the array holds
@@ -357,136 +365,129 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     if (warp < 4) {
         // (inside the branch: the compiler gives each side its own limit)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsAux));
-    if (warp == 0) {
-        // ------------------------------------------------ loads
-        uint32_t it = 0;
-        bool ok = true;
-        for (int t = first; t < total && ok; t += stride) {
-            const Tile tile = tile_at(c, E, t);
-            const int loads = GATHER ? 0 : (tile.cnt + ABOX - 1) / ABOX;
-            const uint32_t bytes = (uint32_t)(loads * ABOX * BK) + B_BYTES;
-            for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                const int s = it % STAGES;
-                ok = __all_sync(0xffffffffu, bar_wait(&c.empty[s], ((it / STAGES) & 1u) ^ 1u, abort_flag));
-                if (!ok) break;
-                uint8_t *sa = smem + s * STAGE, *sb = sa + A_BYTES;
-                if (lane == 0) {
-                    mbar_expect_tx(&c.full[s], bytes);
-                    if (MODE == GATEUP) {
-                        // per column half: 64 rows of W_gate, 64 of W_up
+        if (warp == 0 || (GATHER && warp == 3)) {
+            // -------------------------------------------- loads
+            // Warp 0: the weights (and rows in order) by TMA.  Gathered rows:
+            // warp 0 copies rows 0-63 of the tile, warp 3 rows 64-127, 8 lanes to
+            // a row's 128 bytes, 4 rows an instruction, into the swizzled layout
+            // that TMA gives the other operand.
+            const int rsub = lane >> 3, chunk = lane & 7, first_row = warp ? 64 : 0;
+            uint32_t it = 0, arrived = 0;
+            bool ok = true;
+            // the copies of the stages before `upto` have landed: hand them to the MMA
+            auto hand_over = [&](uint32_t upto) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                for (; arrived < upto; ++arrived)
+                    if (lane == 0) mbar_arrive(&c.full[arrived % STAGES]);
+            };
+            for (int t = first; t < total && ok; t += stride) {
+                const Tile tile = tile_at(c, E, t);
+                const int boxes = GATHER ? 0 : (tile.cnt + ABOX - 1) / ABOX;
+                int tok[GATHER ? 16 : 1];
+                if (GATHER) {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint8_t *at = sb + h * (B_BYTES / 2);
-                            const int n = tile.nt * (BN / 2) + h * 64;
-                            tma_load_3d(at, &tm_w0, &c.full[s], kb * BK, n, tile.e);
-                            tma_load_3d(at + B_BYTES / 4, &tm_w1, &c.full[s], kb * BK, n, tile.e);
-                        }
-                    } else {
-                        tma_load_3d(sb, &tm_w0, &c.full[s], kb * BK, tile.nt * BN, tile.e);
+                    for (int i = 0; i < 16; ++i) {
+                        const int r = first_row + 4 * i + rsub;
+                        tok[i] = r < tile.cnt ? __ldg(p.perm_tok + tile.row0 + r) : -1;
+                        if (tok[i] >= p.x_rows) tok[i] = -1;   // (out of range: not read, its row is undefined)
                     }
                 }
-                __syncwarp();
-                if (!GATHER && lane < loads)
-                    tma_load_2d(sa + lane * ABOX * BK, &tm_x, &c.full[s], kb * BK, tile.row0 + lane * ABOX);
-            }
-        }
-        if (!ok) {
-            if (lane == 0) flag_status(p.status, kDevTimeout);
-            c.abort_flag = 1;
-            // let loads already issued land before the CTA exits
-            for (uint32_t j = (it >= STAGES ? it - STAGES : 0); j < it; ++j) {
-                volatile int no_abort = 0;
-                bar_wait(&c.full[j % STAGES], (j / STAGES) & 1u, &no_abort, 1000000ull);
-            }
-        }
-    } else if (warp == 1 && lane == 0) {
-        // ------------------------------------------------ multiply
-        constexpr uint32_t idesc = idesc_e4m3(BM, BN / 2);
-        uint32_t it = 0;
-        bool ok = true;
-        for (int t = first; t < total && ok; t += stride) {
-            for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                const int s = it % STAGES;
-                const uint32_t b = it & 1u;
-                ok = bar_wait(&c.full[s], (it / STAGES) & 1u, abort_flag);
-                const uint32_t a0 = smem_u32(smem + s * STAGE);
-                const uint64_t da = sw128_desc(a0);
-                // the two column halves have buffers of their own, so that the
-                // sums of one are taken while the other is multiplied
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    const int s = it % STAGES;
+                    ok = __all_sync(0xffffffffu, bar_wait(&c.empty[s], ((it / STAGES) & 1u) ^ 1u, abort_flag));
+                    if (!ok) break;
+                    uint8_t *sa = smem + s * STAGE, *sb = sa + A_BYTES;
+                    if (warp == 0 && lane == 0) {
+                        mbar_expect_tx(&c.full[s], (uint32_t)(boxes * ABOX * BK) + B_BYTES);
+                        if (MODE == GATEUP) {
+                            // per column half: 64 rows of W_gate, 64 of W_up
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    ok = ok && bar_wait(&c.tempty[b][h], ((it >> 1) & 1u) ^ 1u, abort_flag);
+                            for (int h = 0; h < 2; ++h) {
+                                uint8_t *at = sb + h * (B_BYTES / 2);
+                                const int n = tile.nt * (BN / 2) + h * 64;
+                                tma_load_3d(at, &tm_w0, &c.full[s], kb * BK, n, tile.e);
+                                tma_load_3d(at + B_BYTES / 4, &tm_w1, &c.full[s], kb * BK, n, tile.e);
+                            }
+                        } else {
+                            tma_load_3d(sb, &tm_w0, &c.full[s], kb * BK, tile.nt * BN, tile.e);
+                        }
+                    }
+                    __syncwarp();
+                    if constexpr (GATHER) {
+                        const bool in = kb * BK + chunk * 16 < p.K;
+                        const uint32_t at = smem_u32(sa) + (first_row + rsub) * BK;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (tok[i] >= 0)
+                                cp_async16(at + i * 4 * BK + ((chunk ^ ((4 * i + rsub) & 7)) << 4),
+                                           p.x_q + (in ? tok[i] * p.ldx + kb * BK + chunk * 16 : 0), in);
+                        asm volatile("cp.async.commit_group;" ::: "memory");
+                        if (it - arrived >= kGatherLag) {
+                            cp_async_wait<kGatherLag>();
+                            hand_over(arrived + 1);
+                        }
+                    } else if (lane < boxes) {
+                        tma_load_2d(sa + lane * ABOX * BK, &tm_x, &c.full[s], kb * BK, tile.row0 + lane * ABOX);
+                    }
+                }
+            }
+            if (GATHER) {
+                cp_async_wait<0>();
+                if (ok) hand_over(it);
+            }
+            if (!ok) {
+                if (lane == 0) flag_status(p.status, kDevTimeout);
+                c.abort_flag = 1;
+                // let loads already issued land before the CTA exits (gathered
+                // stages may miss an arrival: then the wait's limit ends it)
+                for (uint32_t j = (it >= STAGES ? it - STAGES : 0); j < it; ++j) {
+                    volatile int no_abort = 0;
+                    bar_wait(&c.full[j % STAGES], (j / STAGES) & 1u, &no_abort, 1000000ull);
+                }
+            }
+        } else if (warp == 1 || warp == 2) {
+            // -------------------------------------------- multiply
+            // Warp 1 multiplies the first column half, warp 2 the second, into
+            // TMEM buffers of their own: between the MMAs of two blocks an
+            // issuer spends about as long on its waits and commits as the MMAs
+            // take, which the other warp's MMAs fill.  The whole warp runs the
+            // loop and one elected lane issues, so that the descriptors stay in
+            // uniform registers (a loop of lane 0 alone: 80 clocks to issue an MMA).
+            constexpr uint32_t idesc = idesc_e4m3(BM, BN / 2);
+            const bool leader = elect_one();
+            const int h = warp - 1;
+            const uint32_t ring = smem_u32(smem), d0 = tmem + h * (BN / 2);
+            uint32_t it = 0;
+            bool ok = true;
+            for (int t = first; t < total && ok; t += stride) {
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    const int s = it % STAGES;
+                    const uint32_t b = it & 1u;
+                    ok = bar_wait(&c.tempty[b][h], ((it >> 1) & 1u) ^ 1u, abort_flag) &&
+                         bar_wait(&c.full[s], (it / STAGES) & 1u, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint64_t db = sw128_desc(a0 + A_BYTES + h * (B_BYTES / 2));
+                    const uint64_t da = sw128_desc(ring + s * STAGE);
+                    const uint64_t db = sw128_desc(ring + s * STAGE + A_BYTES + h * (B_BYTES / 2));
+                    if (leader) {
+                        umma_f8<false>(d0 + b * BN, da, db, idesc);
 #pragma unroll
-                    for (int kk = 0; kk < BK / 32; ++kk)
-                        umma_f8(tmem + b * BN + h * (BN / 2), desc_step(da, kk * 32), desc_step(db, kk * 32), idesc,
-                                kk != 0);
-                    umma_commit(&c.tfull[b][h]);
-                }
-                if (!ok) break;
-                umma_commit(&c.empty[s]);
-            }
-        }
-        if (!ok) {
-            flag_status(p.status, kDevTimeout);
-            c.abort_flag = 1;
-            umma_commit(&c.drain);   // MMAs in flight end before TMEM is freed
-            volatile int no_abort = 0;
-            bar_wait(&c.drain, 0, &no_abort);
-        }
-    } else if (GATHER && warp >= 2) {
-        // ------------------------------------------------ gathered rows
-        // warp 2: rows 0-63 of the tile, warp 3: rows 64-127; 8 lanes copy one
-        // row's 128 bytes, 4 rows an instruction, into the swizzled layout that
-        // TMA gives the other operand
-        const int rsub = lane >> 3, chunk = lane & 7, first_row = (warp - 2) * 64;
-        const uint8_t *src0 = p.x_q + chunk * 16;
-        uint32_t it = 0, arrived = 0;
-        bool ok = true;
-        // the copies of stages up to `arrived` have landed: hand them to the MMA
-        auto hand_over = [&]() {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&c.full[arrived % STAGES]);
-            ++arrived;
-        };
-        for (int t = first; t < total && ok; t += stride) {
-            const Tile tile = tile_at(c, E, t);
-            int tok[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int r = first_row + 4 * i + rsub;
-                tok[i] = r < tile.cnt ? __ldg(p.perm_tok + tile.row0 + r) : -1;
-                if (tok[i] >= p.x_rows) tok[i] = -1;   // (out of range: not read, its row is undefined)
-            }
-            for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                const int s = it % STAGES;
-                ok = __all_sync(0xffffffffu, bar_wait(&c.empty[s], ((it / STAGES) & 1u) ^ 1u, abort_flag));
-                if (!ok) break;
-                const bool in = kb * BK + chunk * 16 < p.K;
-                const uint32_t sa = smem_u32(smem + s * STAGE) + (first_row + rsub) * BK;
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (tok[i] >= 0)
-                        cp_async16(sa + i * 4 * BK + ((chunk ^ ((4 * i + rsub) & 7)) << 4),
-                                   src0 + (in ? tok[i] * p.ldx + kb * BK : 0), in);
-                asm volatile("cp.async.commit_group;" ::: "memory");
-                if (it - arrived >= kGatherLag) {
-                    cp_async_wait<kGatherLag>();
-                    hand_over();
+                        for (int kk = 1; kk < BK / 32; ++kk)
+                            umma_f8<true>(d0 + b * BN, desc_step(da, kk * 32), desc_step(db, kk * 32), idesc);
+                        umma_commit(&c.tfull[b][h]);
+                        umma_commit(&c.empty[s]);
+                    }
                 }
             }
+            if (!ok) {
+                if (leader) flag_status(p.status, kDevTimeout);
+                c.abort_flag = 1;
+                if (leader) umma_commit(&c.drain[h]);   // MMAs in flight end before TMEM is freed
+                volatile int no_abort = 0;
+                bar_wait(&c.drain[h], 0, &no_abort);
+            }
         }
-        cp_async_wait<0>();
-        if (ok) {
-            while (arrived < it) hand_over();
-        } else {
-            if (lane == 0) flag_status(p.status, kDevTimeout);
-            c.abort_flag = 1;
-        }
-    }
     } else {
         // ------------------------------------------------ sums and output
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
@@ -663,7 +664,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     } else {
         __syncthreads();
     }
-    if (warp == 2) {
+    if (warp == 3) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, TMEM_COLS);
