@@ -15,4 +15,4 @@ from .binding import (EXPORTS, MOE_BF16, MOE_F32, MOE_PATH_AUTO, MOE_PATH_DECODE
                       moe_forward_noalloc, moe_pack_q8_0, moe_permute, moe_q8_0_packed_size,
                       moe_route, moe_workspace_size, moe_workspace_views, read_routing,
                       moe_quant_fp8b, moe_norm_fp8b, moe_gemm_fp8b, moe_grouped_gemm_fp8b,
-                      moe_gate_up_fp8b, VIEW_NAMES)
+                      moe_gate_up_fp8b, moe_fp8b_workspace_size, VIEW_NAMES)

@@ -8,6 +8,7 @@ been built the first call raises -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import Optional
 
@@ -33,7 +34,7 @@ EXPORTS = ("moe_status_str", "moe_version", "moe_route", "moe_route_scored", "mo
            "moe_forward_profiled", "moe_forward_scored", "moe_ffn_dense", "moe_forward_noalloc",
            "moe_workspace_views", "moe_forward_expire_wait", "moe_check", "moe_check_noalloc",
            "moe_quant_fp8b", "moe_norm_fp8b", "moe_gemm_fp8b", "moe_grouped_gemm_fp8b",
-           "moe_gate_up_fp8b")
+           "moe_gate_up_fp8b", "moe_fp8b_workspace_size")
 
 _lib = None
 _debug_lib = None
@@ -139,10 +140,12 @@ def _declare(L):
     L.moe_gemm_fp8b.argtypes = [vp, vp, i, i, ll, vp, vp, i, vp, i, ll, vp, vp]
     L.moe_gemm_fp8b.restype = i
     L.moe_grouped_gemm_fp8b.argtypes = [vp, vp, i, i, ll, vp, vp, i, i, vp, vp, i, vp, i, ll, vp,
-                                        vp]
+                                        sz, vp, vp]
+    L.moe_fp8b_workspace_size.argtypes = [i, i]
+    L.moe_fp8b_workspace_size.restype = sz
     L.moe_grouped_gemm_fp8b.restype = i
     L.moe_gate_up_fp8b.argtypes = [vp, vp, i, i, ll, vp, vp, vp, vp, i, i, vp, vp, i, vp, vp, vp,
-                                   vp]
+                                   sz, vp, vp]
     L.moe_gate_up_fp8b.restype = i
     L.moe_check.argtypes = [vp, vp, vp]
     L.moe_check.restype = i
@@ -461,51 +464,37 @@ def moe_check(workspace: torch.Tensor) -> int:
 
 
 # ---- block-scaled fp8 operators (E4M3 codes; one fp32 scale per row and 128
-# columns, or per 128 x 128 block).  Unlike the calls above these check shapes,
-# types, devices and strides here: their operands come in pairs that a wrong
-# pairing would read out of bounds.
+# columns, or per 128 x 128 block).  Their tensors are checked, and their outputs
+# allocated, in the compiled module _fp8b (csrc/fp8b_binding.cpp): ValueError /
+# TypeError for tensors that do not fit one another, MoeError for what the
+# library refuses.
 
-def _need(t: torch.Tensor, name: str, shape, dtypes, device, rows_strided: bool = False):
-    """The operand's pointer, after checks of device, type, shape and strides
-    (rows_strided: rows may be further apart than their length)."""
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous() and not (rows_strided and t.stride(-1) == 1):
-        raise ValueError(f"{name}: strides {t.stride()} are not supported, make it contiguous")
-    return t.data_ptr()
+_fp8b_module = None
 
 
-def _row_stride(t: torch.Tensor) -> int:
-    return t.stride(-2) if t.shape[-2] > 1 else t.shape[-1]
+def _fp8b():
+    global _fp8b_module
+    if _fp8b_module is None:
+        load_library()
+        path = _build.BINDING_PATH
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build the CUDA library first "
+                               "(python -m expert_routed_ffn_selectedsoftmax_gb300.build)")
+        spec = importlib.util.spec_from_file_location("_fp8b", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _fp8b_module = module
+    return _fp8b_module
 
 
-def _blocks(n: int) -> int:
-    return (n + 127) // 128
+def _checked(out, where: str):
+    if type(out) is int:   # the status of a refused call
+        raise MoeError(out, where)
+    return out
 
 
-def _call_fp8b(name: str, device: torch.device, *args):
-    """The library call on `device`'s current stream, with that device current."""
-    if device.type != "cuda":
-        raise ValueError(f"{name}: tensors are on {device}, expected a CUDA device")
-    f = getattr(_lib or load_library(), name)
-    if device.index == torch.cuda.current_device():
-        status = f(*args, torch.cuda.current_stream(device).cuda_stream)
-    else:
-        with torch.cuda.device(device):
-            status = f(*args, torch.cuda.current_stream(device).cuda_stream)
-    if status != 0:
-        raise MoeError(status, name)
-
-
-_FP8 = (torch.float8_e4m3fn, torch.uint8)
-_REAL = (torch.float32, torch.bfloat16)
-_F32 = (torch.float32,)
-_BF16 = (torch.bfloat16,)
-_I32 = (torch.int32,)
+def moe_fp8b_workspace_size(rows: int, K: int) -> int:
+    return int(load_library().moe_fp8b_workspace_size(rows, K))
 
 
 def moe_quant_fp8b(x: torch.Tensor, block_rows: int = 1, codes: Optional[torch.Tensor] = None,
@@ -516,25 +505,7 @@ def moe_quant_fp8b(x: torch.Tensor, block_rows: int = 1, codes: Optional[torch.T
     block_rows: 1 for activations (a scale per row and 128 columns), 128 for
     weights (a scale per 128 x 128 block).
     """
-    if x.dim() not in (2, 3):
-        raise ValueError(f"x: {x.dim()} dimensions, expected 2 or 3")
-    if block_rows not in (1, 128):
-        raise ValueError(f"block_rows: {block_rows}, expected 1 or 128")
-    dev = x.device
-    rows, cols = x.shape[-2:]
-    batch = x.shape[0] if x.dim() == 3 else 1
-    px = _need(x, "x", x.shape, _REAL, dev, rows_strided=True)
-    ldx = _row_stride(x)
-    if x.dim() == 3 and batch > 1 and rows > 0 and x.stride(0) != rows * ldx:
-        raise ValueError(f"x: strides {x.stride()} are not supported, make it contiguous")
-    s_shape = (*x.shape[:-2], -(-rows // block_rows), _blocks(cols))
-    if codes is None:
-        codes = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev)
-    if scales is None:
-        scales = torch.empty(s_shape, dtype=torch.float32, device=dev)
-    _call_fp8b("moe_quant_fp8b", dev, px, _act_dtype(x), batch, rows, cols, ldx, block_rows,
-               _need(codes, "codes", x.shape, _FP8, dev), _need(scales, "scales", s_shape, _F32, dev))
-    return codes, scales
+    return _checked((_fp8b_module or _fp8b()).quant(x, block_rows, codes, scales), "moe_quant_fp8b")
 
 
 def moe_norm_fp8b(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
@@ -551,64 +522,8 @@ def moe_norm_fp8b(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     want_normed=False); codes, scales: the same in block-scaled fp8.  resid may
     be x.
     """
-    T, d = x.shape
-    dev = x.device
-    k = 0
-    if (topk_w is None) != (inv is None):
-        raise ValueError("topk_w and inv go together")
-    pd = pw = pi = pr = pn = None
-    dd = ldd = n_delta = 0
-    px = _need(x, "x", x.shape, _REAL, dev, rows_strided=True)
-    if delta is not None:
-        n_delta = delta.shape[0]
-        if inv is not None:
-            k = topk_w.shape[-1]
-            pw = _need(topk_w, "topk_w", (T, k), _F32, dev)
-            pi = _need(inv, "inv", inv.shape, _I32, dev)
-            if inv.numel() != T * k:
-                raise ValueError(f"inv: {inv.numel()} values, expected {T * k}")
-            if k == 0:
-                raise ValueError("topk_w: no experts per token")
-        pd = _need(delta, "delta", (n_delta if k else T, d), _REAL, dev, rows_strided=True)
-        dd, ldd = _act_dtype(delta), _row_stride(delta)
-        if resid is None:
-            resid = torch.empty((T, d), dtype=x.dtype, device=dev)
-        pr = _need(resid, "resid", (T, d), (x.dtype,), dev)
-    elif inv is not None:
-        raise ValueError("topk_w and inv need delta")
-    else:
-        resid = x
-    if want_normed:
-        if normed is None:
-            normed = torch.empty((T, d), dtype=torch.bfloat16, device=dev)
-        pn = _need(normed, "normed", (T, d), _BF16, dev)
-    else:
-        normed = None
-    if codes is None:
-        codes = torch.empty((T, d), dtype=torch.float8_e4m3fn, device=dev)
-    if scales is None:
-        scales = torch.empty((T, _blocks(d)), dtype=torch.float32, device=dev)
-    _call_fp8b("moe_norm_fp8b", dev, px, _act_dtype(x), T, d, _row_stride(x), pd, dd, n_delta, ldd,
-               pw, pi, k, _need(weight, "weight", (d,), _REAL, dev), _act_dtype(weight), eps, pr, pn,
-               _need(codes, "codes", (T, d), _FP8, dev),
-               _need(scales, "scales", (T, _blocks(d)), _F32, dev))
-    return resid, normed, codes, scales
-
-
-def _product_out(out, rows, N, out_dtype, dev):
-    if out is None:
-        if out_dtype not in _REAL:
-            raise TypeError(f"out_dtype: {out_dtype}, expected torch.float32 or torch.bfloat16")
-        return torch.empty((rows, N), dtype=out_dtype, device=dev)
-    return out
-
-
-def _status_ptr(status, dev):
-    if status is None:
-        return None
-    if status.numel() < 1:
-        raise ValueError("status: empty")
-    return _need(status, "status", status.shape, _I32, dev)
+    return _checked((_fp8b_module or _fp8b()).norm(x, weight, eps, delta, topk_w, inv, want_normed, resid,
+                                                   normed, codes, scales), "moe_norm_fp8b")
 
 
 def moe_gemm_fp8b(x_q: torch.Tensor, x_s: torch.Tensor, w_q: torch.Tensor, w_s: torch.Tensor,
@@ -616,31 +531,14 @@ def moe_gemm_fp8b(x_q: torch.Tensor, x_s: torch.Tensor, w_q: torch.Tensor, w_s: 
                   status: Optional[torch.Tensor] = None) -> torch.Tensor:
     """x [T, K] times W^T, W [N, K], in block-scaled fp8 -> out [T, N] bf16 / fp32.
 
-    status: optional int32 device word that collects device-side errors (zero it
-    once; moe_check(status) reads it).
+    x_s [T, ceil(K/128)], w_s [ceil(N/128), ceil(K/128)]; x_q's and out's rows
+    may be further apart than their length.  status: optional int32 device word
+    that collects device-side errors (zero it once; moe_check(status) reads it).
     """
-    T, K = x_q.shape
-    N = w_q.shape[0]
-    dev = x_q.device
-    out = _product_out(out, T, N, out_dtype, dev)
-    po = _need(out, "out", (T, N), _REAL, dev, rows_strided=True)
-    _call_fp8b("moe_gemm_fp8b", dev, _need(x_q, "x_q", (T, K), _FP8, dev, rows_strided=True),
-               _need(x_s, "x_s", (T, _blocks(K)), _F32, dev), T, K, _row_stride(x_q),
-               _need(w_q, "w_q", (N, K), _FP8, dev),
-               _need(w_s, "w_s", (_blocks(N), _blocks(K)), _F32, dev), N, po, _act_dtype(out),
-               _row_stride(out), _status_ptr(status, dev))
-    return out
-
-
-def _groups(offsets, perm_tok, E, x_rows, dev):
-    """(offsets pointer, perm_tok pointer, grouped rows)."""
-    rows = x_rows if perm_tok is None else perm_tok.numel()
-    pp = None if perm_tok is None else _need(perm_tok, "perm_tok", (rows,), _I32, dev)
-    if offsets is None:
-        if E != 1:
-            raise ValueError(f"offsets are required for {E} experts")
-        return None, pp, rows
-    return _need(offsets, "offsets", (E + 1,), _I32, dev), pp, rows
+    if w_q.dim() != 2:
+        raise ValueError(f"w_q: {w_q.dim()} dimensions, expected 2")
+    return _checked((_fp8b_module or _fp8b()).product(x_q, x_s, w_q, w_s, None, None, out, out_dtype, None, status),
+                    "moe_gemm_fp8b")
 
 
 def moe_grouped_gemm_fp8b(x_q: torch.Tensor, x_s: torch.Tensor, w_q: torch.Tensor,
@@ -648,53 +546,33 @@ def moe_grouped_gemm_fp8b(x_q: torch.Tensor, x_s: torch.Tensor, w_q: torch.Tenso
                           perm_tok: Optional[torch.Tensor] = None,
                           out: Optional[torch.Tensor] = None,
                           out_dtype: torch.dtype = torch.bfloat16,
+                          workspace: Optional[torch.Tensor] = None,
                           status: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Every expert's product with its rows, in block-scaled fp8 -> out [rows, N].
 
     w_q [E, N, K], w_s [E, ceil(N/128), ceil(K/128)]; rows of expert e are
     [offsets[e], offsets[e+1]) (moe_permute), row r is x's row perm_tok[r], or r
     itself without perm_tok.  Rows from offsets[E] on are left as they were.
+    workspace: with perm_tok, scratch of moe_fp8b_workspace_size(rows, K) bytes
+    (allocated when not given).
     """
-    x_rows, K = x_q.shape
-    E, N = w_q.shape[:2]
-    dev = x_q.device
-    po, pp, rows = _groups(offsets, perm_tok, E, x_rows, dev)
-    out = _product_out(out, rows, N, out_dtype, dev)
-    pout = _need(out, "out", (rows, N), _REAL, dev, rows_strided=True)
-    _call_fp8b("moe_grouped_gemm_fp8b", dev, _need(x_q, "x_q", (x_rows, K), _FP8, dev, rows_strided=True),
-               _need(x_s, "x_s", (x_rows, _blocks(K)), _F32, dev), x_rows, K, _row_stride(x_q),
-               _need(w_q, "w_q", (E, N, K), _FP8, dev),
-               _need(w_s, "w_s", (E, _blocks(N), _blocks(K)), _F32, dev), E, N, po, pp, rows, pout,
-               _act_dtype(out), _row_stride(out), _status_ptr(status, dev))
-    return out
+    if w_q.dim() != 3:
+        raise ValueError(f"w_q: {w_q.dim()} dimensions, expected 3")
+    return _checked((_fp8b_module or _fp8b()).product(x_q, x_s, w_q, w_s, offsets, perm_tok, out, out_dtype,
+                                                      workspace, status), "moe_grouped_gemm_fp8b")
 
 
 def moe_gate_up_fp8b(x_q: torch.Tensor, x_s: torch.Tensor, wg_q: torch.Tensor, wg_s: torch.Tensor,
                      wu_q: torch.Tensor, wu_s: torch.Tensor,
                      offsets: Optional[torch.Tensor] = None,
                      perm_tok: Optional[torch.Tensor] = None, h_q: Optional[torch.Tensor] = None,
-                     h_s: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None):
+                     h_s: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                     status: Optional[torch.Tensor] = None):
     """h = SiLU(W_g x) * (W_u x) per grouped row, quantised -> (h_q [rows, F], h_s).
 
     wg_q, wu_q [E, F, d] (or [F, d] without offsets: a dense layer) with scales
-    [E, ceil(F/128), ceil(d/128)]; offsets and perm_tok as moe_grouped_gemm_fp8b.
+    [E, ceil(F/128), ceil(d/128)]; offsets, perm_tok and workspace as
+    moe_grouped_gemm_fp8b.
     """
-    x_rows, d = x_q.shape
-    dev = x_q.device
-    lead = wg_q.shape[:-2]
-    E, F = (lead[0] if lead else 1), wg_q.shape[-2]
-    if len(lead) > 1:
-        raise ValueError(f"wg_q: {wg_q.dim()} dimensions, expected 2 or 3")
-    po, pp, rows = _groups(offsets, perm_tok, E, x_rows, dev)
-    w_shape, s_shape = (*lead, F, d), (*lead, _blocks(F), _blocks(d))
-    if h_q is None:
-        h_q = torch.empty((rows, F), dtype=torch.float8_e4m3fn, device=dev)
-    if h_s is None:
-        h_s = torch.empty((rows, _blocks(F)), dtype=torch.float32, device=dev)
-    _call_fp8b("moe_gate_up_fp8b", dev, _need(x_q, "x_q", (x_rows, d), _FP8, dev, rows_strided=True),
-               _need(x_s, "x_s", (x_rows, _blocks(d)), _F32, dev), x_rows, d, _row_stride(x_q),
-               _need(wg_q, "wg_q", w_shape, _FP8, dev), _need(wg_s, "wg_s", s_shape, _F32, dev),
-               _need(wu_q, "wu_q", w_shape, _FP8, dev), _need(wu_s, "wu_s", s_shape, _F32, dev), E, F,
-               po, pp, rows, _need(h_q, "h_q", (rows, F), _FP8, dev),
-               _need(h_s, "h_s", (rows, _blocks(F)), _F32, dev), _status_ptr(status, dev))
-    return h_q, h_s
+    return _checked((_fp8b_module or _fp8b()).gate_up(x_q, x_s, wg_q, wg_s, wu_q, wu_s, offsets, perm_tok, h_q, h_s,
+                                                      workspace, status), "moe_gate_up_fp8b")

@@ -1,7 +1,10 @@
-"""Compile the CUDA library (csrc/*.cu) into libmoe_gb300.so, in-tree.
+"""Compile the CUDA library (csrc/*.cu) into libmoe_gb300.so, in-tree, and the
+Python module of the block-scaled fp8 operators (csrc/fp8b_binding.cpp) into
+_fp8b.so beside it.
 
-nvcc, one -gencode for sm_103a, translation units compiled in parallel, no
-cmake.  Rebuilds only when a source or header is newer than the library.
+nvcc, one -gencode for sm_103a, translation units compiled in parallel (the
+module by the host compiler against PyTorch's headers), no cmake.  Rebuilds only
+when a source or header is newer than what was built.
 """
 from __future__ import annotations
 
@@ -10,6 +13,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +25,10 @@ LIB_PATH = os.path.join(PKG, "libmoe_gb300.so")
 # kernels are given, include/moe_debug.h)
 DEBUG_BUILD_DIR = os.path.join(ROOT, "_build_debug")
 DEBUG_LIB_PATH = os.path.join(PKG, "libmoe_gb300_debug.so")
+
+# the Python module of the block-scaled fp8 operators
+BINDING_SRC = os.path.join(CSRC, "fp8b_binding.cpp")
+BINDING_PATH = os.path.join(PKG, "_fp8b.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr",
@@ -39,7 +47,7 @@ def sources():
 
 
 def _deps():
-    return sources() + glob.glob(os.path.join(CSRC, "*.h")) + \
+    return sources() + [BINDING_SRC] + glob.glob(os.path.join(CSRC, "*.h")) + \
         glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h")) + \
         [os.path.abspath(__file__)]
 
@@ -51,14 +59,45 @@ def up_to_date(lib: str = LIB_PATH) -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def _compile_binding(build_dir: str) -> str:
+    """fp8b_binding.cpp -> object file (host compiler, PyTorch's headers)."""
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda_inc = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    obj = os.path.join(build_dir, "fp8b_binding.o")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda_inc,
+           "-I", INCLUDE, "-c", BINDING_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on {os.path.basename(BINDING_SRC)}:\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L", PKG, "-l:" + os.path.basename(LIB_PATH),
+           "-L", lib, "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-lc10", "-lc10_cuda",
+           "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"linking {os.path.basename(BINDING_PATH)} failed:\n{r.stderr}")
+    os.replace(tmp, BINDING_PATH)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: bool = False) -> str:
-    """Compile libmoe_gb300.so (or, with debug=True, libmoe_gb300_debug.so
-    with MOE_DEBUG=1) from csrc/*.cu; returns the library's path."""
+    """Compile libmoe_gb300.so and _fp8b.so (or, with debug=True,
+    libmoe_gb300_debug.so with MOE_DEBUG=1) from csrc/; returns the library's
+    path."""
     lib = DEBUG_LIB_PATH if debug else LIB_PATH
     build_dir = DEBUG_BUILD_DIR if debug else BUILD_DIR
     if debug:
         extra_flags = (*extra_flags, "-DMOE_DEBUG=1")
-    if not force and up_to_date(lib):
+    if not force and up_to_date(lib) and (debug or up_to_date(BINDING_PATH)):
         return lib
     nvcc = _nvcc()
     os.makedirs(build_dir, exist_ok=True)
@@ -74,7 +113,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
         return obj
 
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        binding = None if debug else ex.submit(_compile_binding, build_dir)
         objs = list(ex.map(compile_one, srcs))
     tmp = lib + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
@@ -82,6 +122,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, lib)
+    if binding is not None:
+        _link_binding(binding.result())
     return lib
 
 

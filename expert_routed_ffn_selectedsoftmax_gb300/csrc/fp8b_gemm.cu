@@ -14,9 +14,9 @@
 // A tile is 128 rows x 256 columns (PRODUCT), or 128 rows x 128 columns of
 // both W_gate and W_up (GATEUP: the epilogue has whole 128-column groups of h,
 // so it quantises them without a second pass).  Warp 0 loads by TMA (rows in
-// boxes of 32, only as many as the tile has); rows gathered through perm_tok are
-// copied by warps 0 and 3 (cp.async; TMA's four-row gathers took 75 clocks each,
-// 32 of them twice as long as a block's products).  Warps 1 and 2 multiply a
+// boxes of 32, only as many as the tile has); rows that a split product gathers
+// through perm_tok are copied by warps 0 and 3 (cp.async; TMA's four-row gathers
+// took 75 clocks each).  Warps 1 and 2 multiply a
 // column half each.  Warps 4-11 hold the sums: warp w the TMEM
 // lanes of quarter w % 4 and one half of the columns (128 of them, or 64 of
 // gate and the same 64 of up).
@@ -184,23 +184,6 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr)
 // SwiGLU with the fast exponential and an approximate divide (relative error
 // ~1e-6, far below the codes' 2^-4; for g < -87, 1 + e^-g overflows and h is 0)
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
-
-// sixteen codes of v * inv (see quant_mul)
-template <typename F>
-__device__ __forceinline__ uint4 encode16(F v, float inv)
-{
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = e4m3x2(v(4 * i) * inv, v(4 * i + 1) * inv) | (e4m3x2(v(4 * i + 2) * inv, v(4 * i + 3) * inv) << 16);
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-// Factor that takes h to codes: 1 / s.  h already carries the sums' rounding
-// errors, so a code on the border of two may go either way and the product
-// with the reciprocal (half an ulp off) replaces the divide.  Where 1 / s is
-// not finite (s = 0 or below 2^-126: h all zero or below 2^-117) the codes are
-// zero; NaN stays NaN.
-__device__ __forceinline__ float quant_mul(float s) { return s >= 1.17549435e-38f || s != s ? 1.0f / s : 0.0f; }
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
 {
@@ -580,11 +563,15 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                 asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
                 m = max(m, c.amax[half ^ 1][row]);
                 asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
-                const float s = block_scale(m), inv = quant_mul(s);
+                const float s = block_scale(m), f = code_factor(s);
                 const int n0 = tile.nt * (BN / 2) + half * 64;
                 uint4 d[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) d[i] = encode16([&](int q) { return h[16 * i + q]; }, inv);
+                for (int i = 0; i < 4; ++i) {
+                    const float *v = h + 16 * i;
+                    d[i] = make_uint4(encode4(v[0], v[1], v[2], v[3], f), encode4(v[4], v[5], v[6], v[7], f),
+                                      encode4(v[8], v[9], v[10], v[11], f), encode4(v[12], v[13], v[14], v[15], f));
+                }
                 store_rows(stg, lane, d, p.h_q + (r - lane) * p.N + n0, p.N, tile.cnt - quarter * 32, p.N - n0, true, 1);
                 if (valid) {
                     if (half == 0) p.h_s[r * p.NB + tile.nt] = s;
@@ -648,11 +635,10 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                     const float h[4] = {swiglu(a.x, b.x), swiglu(a.y, b.y), swiglu(a.z, b.z), swiglu(a.w, b.w)};
                     const uint32_t m = __reduce_max_sync(0xffffffffu, max(max(mag_bits(h[0]), mag_bits(h[1])),
                                                                          max(mag_bits(h[2]), mag_bits(h[3]))));
-                    const float s = block_scale(m), inv = quant_mul(s);
+                    const float s = block_scale(m), f = code_factor(s);
                     const int n0 = tile.nt * (BN / 2) + 4 * lane;
                     if (n0 < p.N)
-                        *reinterpret_cast<uint32_t *>(p.h_q + r * p.N + n0) =
-                            e4m3x2(h[0] * inv, h[1] * inv) | (e4m3x2(h[2] * inv, h[3] * inv) << 16);
+                        *reinterpret_cast<uint32_t *>(p.h_q + r * p.N + n0) = encode4(h[0], h[1], h[2], h[3], f);
                     if (lane == 0) p.h_s[r * p.NB + tile.nt] = s;
                 } else {
                     store4(p, r, tile.nt * BN + 4 * lane, a);
@@ -671,7 +657,37 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     }
 }
 
+// Rows gathered through perm_tok into group order, codes and scales, a warp to
+// a row; an index outside [0, x_rows) gives a row of zeros.
+constexpr int kGatherWarps = 8;
+__global__ void __launch_bounds__(32 * kGatherWarps)
+gather_kernel(const uint8_t *__restrict__ x_q, const float *__restrict__ x_s, long long ldx, int x_rows, int K, int KB,
+              const int32_t *__restrict__ perm_tok, int rows, uint8_t *__restrict__ g_q, float *__restrict__ g_s)
+{
+    pdl_enter();
+    const int lane = threadIdx.x & 31;
+    const long long r = (long long)blockIdx.x * kGatherWarps + (threadIdx.x >> 5);
+    if (r >= rows) return;
+    const int tok = __ldg(perm_tok + r);
+    const bool in = tok >= 0 && tok < x_rows;
+    const uint4 *src = reinterpret_cast<const uint4 *>(x_q + (in ? tok : 0) * ldx);
+    uint4 *dst = reinterpret_cast<uint4 *>(g_q + r * K);
+    constexpr int U = 4;   // loads in flight per lane
+    for (int i0 = lane; i0 < K / 16; i0 += 32 * U) {
+        uint4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            v[u] = in && i0 + 32 * u < K / 16 ? __ldg(src + i0 + 32 * u) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i0 + 32 * u < K / 16) dst[i0 + 32 * u] = v[u];
+    }
+    for (int i = lane; i < KB; i += 32) g_s[r * KB + i] = in ? __ldg(x_s + (long long)tok * KB + i) : 0.f;
+}
+
 // ------------------------------------------------------------------- host
+size_t gathered_codes_bytes(int rows, int K) { return align_up((size_t)rows * K, 256); }
+
 // [n, rows, cols] codes with rows `ld` bytes apart, box {128 columns, box_rows},
 // 128-byte swizzle.
 bool code_map(CUtensorMap *m, const void *base, int n, int rows, int cols, long long ld, uint32_t box_rows)
@@ -707,22 +723,9 @@ cudaError_t launch_variant(const CUtensorMap &x, const CUtensorMap &w0, const CU
 }
 
 template <int MODE>
-cudaError_t launch_product(const void *x_q, long long ldx, const void *w0, const void *w1, Params p, cudaStream_t stream)
+cudaError_t launch_product(const void *x_q, long long ldx, const void *w0, const void *w1, Params p, void *workspace,
+                           cudaStream_t stream)
 {
-    CUtensorMap mx, mw0, mw1;
-    const bool gather = p.perm_tok != nullptr;
-    const uint32_t wbox = MODE == GATEUP ? BN / 4 : BN;
-    p.x_q = static_cast<const uint8_t *>(x_q);
-    p.ldx = ldx;
-    if (!code_map(&mw0, w0, p.E, p.N, p.K, p.K, wbox))
-        return cudaErrorInvalidValue;
-    if (gather) mx = mw0;   // (unused: gathered rows are copied 16 bytes at a time)
-    else if (!code_map(&mx, x_q, 0, p.x_rows, p.K, ldx, ABOX)) return cudaErrorInvalidValue;
-    if (MODE == GATEUP) {
-        if (!code_map(&mw1, w1, p.E, p.N, p.K, p.K, wbox)) return cudaErrorInvalidValue;
-    } else {
-        mw1 = mw0;
-    }
     p.n_tiles = ceil_div(p.N, MODE == GATEUP ? BN / 2 : BN);
     const int num_sms = device_sm_count();
     // most tiles there can be: every expert with rows may own a ragged row tile
@@ -733,11 +736,37 @@ cudaError_t launch_product(const void *x_q, long long ldx, const void *w0, const
     // and blocks for it
     p.split = 1;
     while (p.split < 8 && tiles * p.split * 2 <= num_sms && p.split * 2 <= p.KB) p.split *= 2;
-    if (p.split > 1)
-        return gather ? launch_variant<MODE, true, true>(mx, mw0, mw1, p, tiles, num_sms, stream)
+    if (p.perm_tok && p.split == 1) {
+        // Rows go into group order once, ahead of the product: every column
+        // tile would gather them again, and a loop that copies rows feeds the
+        // tensor cores more slowly than TMA does (4096 rows x 2048 against 2 x
+        // 2816 columns of 16 experts: 100 us gathering in the kernel, 62 us on
+        // rows in order, plus 4 us for this copy).  A split product reads each
+        // row about once and saves itself the launch.
+        uint8_t *g_q = static_cast<uint8_t *>(workspace);
+        float *g_s = reinterpret_cast<float *>(g_q + gathered_codes_bytes(p.rows, p.K));
+        const cudaError_t e = launch_pdl(gather_kernel, dim3((unsigned)ceil_div(p.rows, kGatherWarps)),
+                                         dim3(32 * kGatherWarps), 0, stream, static_cast<const uint8_t *>(x_q), p.x_s,
+                                         ldx, p.x_rows, p.K, p.KB, p.perm_tok, p.rows, g_q, g_s);
+        if (e != cudaSuccess) return e;
+        x_q = g_q;
+        ldx = p.K;
+        p.x_s = g_s;
+        p.x_rows = p.rows;
+        p.perm_tok = nullptr;
+    }
+    p.x_q = static_cast<const uint8_t *>(x_q);
+    p.ldx = ldx;
+    CUtensorMap mx, mw0, mw1;
+    const uint32_t wbox = MODE == GATEUP ? BN / 4 : BN;
+    if (!code_map(&mw0, w0, p.E, p.N, p.K, p.K, wbox)) return cudaErrorInvalidValue;
+    if (MODE != GATEUP) mw1 = mw0;
+    else if (!code_map(&mw1, w1, p.E, p.N, p.K, p.K, wbox)) return cudaErrorInvalidValue;
+    if (p.perm_tok) mx = mw0;   // (unused: gathered rows are copied 16 bytes at a time)
+    else if (!code_map(&mx, x_q, 0, p.x_rows, p.K, ldx, ABOX)) return cudaErrorInvalidValue;
+    if (p.split == 1) return launch_variant<MODE, false, false>(mx, mw0, mw1, p, tiles, num_sms, stream);
+    return p.perm_tok ? launch_variant<MODE, true, true>(mx, mw0, mw1, p, tiles, num_sms, stream)
                       : launch_variant<MODE, false, true>(mx, mw0, mw1, p, tiles, num_sms, stream);
-    return gather ? launch_variant<MODE, true, false>(mx, mw0, mw1, p, tiles, num_sms, stream)
-                  : launch_variant<MODE, false, false>(mx, mw0, mw1, p, tiles, num_sms, stream);
 }
 
 bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -745,7 +774,7 @@ bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t
 // The checks the products share; MOE_OK with *go = false for an empty call.
 moe_status product_args(const void *x_q, const float *x_s, int x_rows, int K, long long ldx, const void *w_q,
                         const float *w_s, int E, int N, const int32_t *offsets, const int32_t *perm_tok, int rows,
-                        const void *status, bool *go)
+                        const void *status, const void *workspace, size_t ws_bytes, bool *go)
 {
     *go = false;
     if (x_rows < 0 || rows < 0 || K <= 0 || K % 16 || N <= 0 || E <= 0) return MOE_ERR_INVALID_ARG;
@@ -760,6 +789,10 @@ moe_status product_args(const void *x_q, const float *x_s, int x_rows, int K, lo
     if (!aligned_to(x_q, 16) || !aligned_to(w_q, 16) || !aligned_to(x_s, 4) || !aligned_to(w_s, 4) ||
         !aligned_to(offsets, 4) || !aligned_to(perm_tok, 4) || !aligned_to(status, 4))
         return MOE_ERR_INVALID_ARG;
+    if (perm_tok) {
+        if (!workspace || !aligned_to(workspace, 256)) return MOE_ERR_INVALID_ARG;
+        if (ws_bytes < moe_fp8b_workspace_size(rows, K)) return MOE_ERR_WORKSPACE;
+    }
     *go = true;
     return MOE_OK;
 }
@@ -783,13 +816,20 @@ using namespace moe::fp8b;
 
 extern "C" {
 
+size_t moe_fp8b_workspace_size(int rows, int K)
+{
+    if (rows < 0 || K <= 0 || K % 16) return 0;
+    return gathered_codes_bytes(rows, K) + align_up((size_t)rows * ceil_div(K, kBlock) * 4, 256);
+}
+
 moe_status moe_grouped_gemm_fp8b(const void *x_q, const float *x_s, int x_rows, int K, long long ldx,
                                  const void *w_q, const float *w_s, int E, int N, const int32_t *offsets,
                                  const int32_t *perm_tok, int rows, void *out, moe_dtype out_dt, long long ldo,
-                                 uint32_t *status, moe_stream stream)
+                                 void *workspace, size_t ws_bytes, uint32_t *status, moe_stream stream)
 {
     bool go;
-    const moe_status st = product_args(x_q, x_s, x_rows, K, ldx, w_q, w_s, E, N, offsets, perm_tok, rows, status, &go);
+    const moe_status st = product_args(x_q, x_s, x_rows, K, ldx, w_q, w_s, E, N, offsets, perm_tok, rows, status,
+                                        workspace, ws_bytes, &go);
     if (st != MOE_OK) return st;
     if ((out_dt != MOE_F32 && out_dt != MOE_BF16) || ldo < N) return MOE_ERR_INVALID_ARG;
     if (!go) return MOE_OK;
@@ -797,7 +837,7 @@ moe_status moe_grouped_gemm_fp8b(const void *x_q, const float *x_s, int x_rows, 
     Params p = params_of(x_s, x_rows, K, w_s, nullptr, E, N, offsets, perm_tok, rows, status);
     p.out = out; p.ldo = ldo; p.out_f32 = out_dt == MOE_F32;
     p.out_vec = ldo % (out_dt == MOE_F32 ? 4 : 8) == 0 && aligned_to(out, 16);
-    const cudaError_t e = launch_product<PRODUCT>(x_q, ldx, w_q, nullptr, p, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_product<PRODUCT>(x_q, ldx, w_q, nullptr, p, workspace, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -805,17 +845,18 @@ moe_status moe_gemm_fp8b(const void *x_q, const float *x_s, int T, int K, long l
                          const float *w_s, int N, void *out, moe_dtype out_dt, long long ldo, uint32_t *status,
                          moe_stream stream)
 {
-    return moe_grouped_gemm_fp8b(x_q, x_s, T, K, ldx, w_q, w_s, 1, N, nullptr, nullptr, T, out, out_dt, ldo, status,
-                                 stream);
+    return moe_grouped_gemm_fp8b(x_q, x_s, T, K, ldx, w_q, w_s, 1, N, nullptr, nullptr, T, out, out_dt, ldo, nullptr, 0,
+                                 status, stream);
 }
 
 moe_status moe_gate_up_fp8b(const void *x_q, const float *x_s, int x_rows, int d, long long ldx, const void *wg_q,
                             const float *wg_s, const void *wu_q, const float *wu_s, int E, int F,
                             const int32_t *offsets, const int32_t *perm_tok, int rows, void *h_q, float *h_s,
-                            uint32_t *status, moe_stream stream)
+                            void *workspace, size_t ws_bytes, uint32_t *status, moe_stream stream)
 {
     bool go;
-    moe_status st = product_args(x_q, x_s, x_rows, d, ldx, wg_q, wg_s, E, F, offsets, perm_tok, rows, status, &go);
+    moe_status st = product_args(x_q, x_s, x_rows, d, ldx, wg_q, wg_s, E, F, offsets, perm_tok, rows, status, workspace,
+                                 ws_bytes, &go);
     if (st != MOE_OK) return st;
     if (F % 16) return MOE_ERR_INVALID_ARG;
     if (!go) return MOE_OK;
@@ -824,7 +865,7 @@ moe_status moe_gate_up_fp8b(const void *x_q, const float *x_s, int x_rows, int d
         return MOE_ERR_INVALID_ARG;
     Params p = params_of(x_s, x_rows, d, wg_s, wu_s, E, F, offsets, perm_tok, rows, status);
     p.h_q = static_cast<uint8_t *>(h_q); p.h_s = h_s;
-    const cudaError_t e = launch_product<GATEUP>(x_q, ldx, wg_q, wu_q, p, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_product<GATEUP>(x_q, ldx, wg_q, wu_q, p, workspace, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

@@ -2,7 +2,7 @@
 // residual addition and RMS norm of a transformer layer.
 //
 // Quantisation of a block X (one row x 128 columns, or 128 x 128):
-//   s = max|X| / 448 (fp32),  c = e4m3(x / s);  a value is then c * s.
+//   s = max|X| / 448,  c = e4m3(x * (1 / s)), both in fp32;  a value is then c * s.
 // Norm: r[t] = x[t] + sum_j w[t,j] delta[inv[t,j]] (a layer's combine, in slot
 //   order) or x[t] + delta[t];  y[t,i] = r[t,i] g[i] / sqrt(mean_i r[t,i]^2 + eps);
 //   r goes to the residual stream, y to bf16 (the router's input) and to codes.
@@ -46,6 +46,52 @@ __device__ __forceinline__ uint32_t max8(const float (&v)[8])
     for (int i = 0; i < 8; ++i) m = max(m, mag_bits(v[i]));
     return m;
 }
+__device__ __forceinline__ uint2 encode8(const float (&v)[8], float f)
+{
+    return make_uint2(encode4(v[0], v[1], v[2], v[3], f), encode4(v[4], v[5], v[6], v[7], f));
+}
+
+// Eight values as loaded (bf16 stays packed: half the registers, and the
+// maximum two values an instruction).
+template <typename XT> struct Raw8;
+template <> struct Raw8<float> {
+    uint4 a, b;
+    __device__ __forceinline__ void load(const float *p)
+    {
+        a = __ldg(reinterpret_cast<const uint4 *>(p));
+        b = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+    }
+    __device__ __forceinline__ void zero() { a = b = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ void get(float (&v)[8]) const
+    {
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+    }
+    __device__ __forceinline__ uint32_t max_bits() const
+    {
+        float v[8];
+        get(v);
+        return max8(v);
+    }
+};
+template <> struct Raw8<__nv_bfloat16> {
+    uint4 a;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = __ldg(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ void get(float (&v)[8]) const
+    {
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { v[2 * i] = bf16lo(w[i]); v[2 * i + 1] = bf16hi(w[i]); }
+    }
+    __device__ __forceinline__ uint32_t max_bits() const
+    {
+        const uint32_t k = 0x7fff7fffu;
+        const uint32_t m = __vmaxu2(__vmaxu2(a.x & k, a.y & k), __vmaxu2(a.z & k, a.w & k));
+        return max(m << 16, m & 0xffff0000u);
+    }
+};
 
 // ------------------------------------------------------------- quantisation
 constexpr int kRowThreads = 256, kRowUnroll = 4;
@@ -64,7 +110,7 @@ quant_rows_kernel(const XT *__restrict__ x, long long rows, int cols, long long 
     // (every lane of a warp takes the same number of turns: the shuffles are warp-wide)
     const long long turns = (total + step * kRowUnroll - 1) / (step * kRowUnroll);
     for (long long turn = 0; turn < turns; ++turn) {
-        Chunk8 c[kRowUnroll];
+        Raw8<XT> c[kRowUnroll];
         long long row[kRowUnroll];
         int col[kRowUnroll], blk[kRowUnroll];
         bool in[kRowUnroll];
@@ -75,16 +121,16 @@ quant_rows_kernel(const XT *__restrict__ x, long long rows, int cols, long long 
             blk[u] = (int)(b - row[u] * nblk);
             col[u] = blk[u] * kBlock + l16 * 8;
             in[u] = b < total && col[u] < cols;
-            if (in[u]) load8(x + row[u] * ldx + col[u], c[u]);
-            else
-#pragma unroll
-                for (int i = 0; i < 8; ++i) c[u].v[i] = 0.f;
+            if (in[u]) c[u].load(x + row[u] * ldx + col[u]);
+            else c[u].zero();
         }
 #pragma unroll
         for (int u = 0; u < kRowUnroll; ++u) {
-            const float s = block_scale(max16(max8(c[u].v)));
+            const float s = block_scale(max16(c[u].max_bits()));
             if (!in[u]) continue;
-            *reinterpret_cast<uint2 *>(codes + row[u] * cols + col[u]) = encode8(c[u].v, s);
+            float v[8];
+            c[u].get(v);
+            *reinterpret_cast<uint2 *>(codes + row[u] * cols + col[u]) = encode8(v, code_factor(s));
             if (l16 == 0) scales[row[u] * nblk + blk[u]] = s;
         }
     }
@@ -92,7 +138,8 @@ quant_rows_kernel(const XT *__restrict__ x, long long rows, int cols, long long 
 
 constexpr int kTileThreads = 256, kTileChunks = kBlock * kBlock / 8 / kTileThreads;
 
-// One 128 x 128 block per CTA, held in registers (8 chunks of 8 values a thread).
+// One 128 x 128 block per CTA, held in registers as loaded (8 chunks of 8
+// values a thread).
 template <typename XT>
 __global__ void __launch_bounds__(kTileThreads)
 quant_tiles_kernel(const XT *__restrict__ x, int rows, int cols, long long ldx, int nr, int nc,
@@ -106,30 +153,30 @@ quant_tiles_kernel(const XT *__restrict__ x, int rows, int cols, long long ldx, 
     const long long b = band / nr;
     const int r0 = (int)(band - b * nr) * kBlock;
     const int col = bc * kBlock + (threadIdx.x & 15) * 8;
-    Chunk8 c[kTileChunks];
+    Raw8<XT> c[kTileChunks];
     uint32_t m = 0u;
 #pragma unroll
     for (int i = 0; i < kTileChunks; ++i) {
         const int r = r0 + (threadIdx.x >> 4) + i * (kTileThreads / 16);
-        if (r < rows && col < cols) load8(x + (b * rows + r) * ldx + col, c[i]);
-        else
-#pragma unroll
-            for (int j = 0; j < 8; ++j) c[i].v[j] = 0.f;
+        if (r < rows && col < cols) c[i].load(x + (b * rows + r) * ldx + col);
+        else c[i].zero();
     }
 #pragma unroll
-    for (int i = 0; i < kTileChunks; ++i) m = max(m, max8(c[i].v));
+    for (int i = 0; i < kTileChunks; ++i) m = max(m, c[i].max_bits());
     m = __reduce_max_sync(0xffffffffu, m);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kTileThreads / 32; ++w) m = max(m, part[w]);
-    const float s = block_scale(m);
+    const float s = block_scale(m), f = code_factor(s);
     if (threadIdx.x == 0) scales[tile] = s;
 #pragma unroll
     for (int i = 0; i < kTileChunks; ++i) {
         const int r = r0 + (threadIdx.x >> 4) + i * (kTileThreads / 16);
+        float v[8];
+        c[i].get(v);
         if (r < rows && col < cols)
-            *reinterpret_cast<uint2 *>(codes + (b * rows + r) * cols + col) = encode8(c[i].v, s);
+            *reinterpret_cast<uint2 *>(codes + (b * rows + r) * cols + col) = encode8(v, f);
     }
 }
 
@@ -219,7 +266,7 @@ norm_kernel(const NormArgs a)
         }
         const float s = block_scale(max16(max8(r[j].v)));
         if (in) {
-            *reinterpret_cast<uint2 *>(a.codes + t * a.d + col) = encode8(r[j].v, s);
+            *reinterpret_cast<uint2 *>(a.codes + t * a.d + col) = encode8(r[j].v, code_factor(s));
             if ((threadIdx.x & 15) == 0) a.scales[t * a.nblk + col / kBlock] = s;
         }
     }

@@ -440,9 +440,10 @@ MOE_API moe_status moe_forward_noalloc(const void *x, moe_dtype act_dt, int T, i
  *     [E, ceil(N/128), ceil(K/128)] (blocks do not cross experts).
  * K (d, F) is a multiple of 16; the last block of a row may be shorter.  Code
  * buffers are 16-byte aligned, scales 4-byte.
- * Quantisation of a block: s = max|x| / 448 in fp32, code = E4M3 nearest to
- * x / s, ties to even.  All zeros (or so small that s underflows): s = 0,
- * codes 0.  A block that holds an infinity or NaN: s = NaN, NaN codes.
+ * Quantisation of a block: s = max|x| / 448, code = E4M3 nearest to x * (1/s),
+ * ties to even, each operation rounded to fp32.  All zeros, or so small that s
+ * would be below 2^-126: s = 0, codes 0.  A block that holds an infinity or
+ * NaN: s = NaN, NaN codes.
  *
  * A layer as a chain of these calls, every one asynchronous on one stream:
  *   moe_norm_fp8b     residual + the previous layer's combine, RMS norm, codes
@@ -510,6 +511,12 @@ MOE_API moe_status moe_gemm_fp8b(const void *x_q, const float *x_s, int T, int K
                                  moe_stream stream);
 
 /*
+ * Bytes of device workspace the two calls below need when they gather rows
+ * through perm_tok (`rows` of them, K columns); 0 on invalid sizes.
+ */
+MOE_API size_t moe_fp8b_workspace_size(int rows, int K);
+
+/*
  * moe_grouped_gemm_fp8b -- the product of every expert with its rows:
  *     out[r] = x[perm_tok[r]] W[e]^T   for r in [offsets[e], offsets[e+1])
  *   offsets [E+1] and perm_tok [rows] (NULL: row r is x's row r; then
@@ -518,6 +525,9 @@ MOE_API moe_status moe_gemm_fp8b(const void *x_q, const float *x_s, int T, int K
  *   that no group holds (offsets[E] < rows: a padded batch) are left as they
  *   were.  Offsets are clamped to [0, rows]; a row whose perm_tok is outside
  *   [0, x_rows) is undefined, and no other memory is touched.
+ *   workspace: with perm_tok, scratch of at least moe_fp8b_workspace_size(rows,
+ *   K) bytes, 256-byte aligned, not shared by calls that can overlap; without
+ *   perm_tok it is not used and may be NULL.
  *   w_q [E, N, K], w_s [E, ceil(N/128), ceil(K/128)], E <= 256; the other
  *   arguments as moe_gemm_fp8b.
  */
@@ -525,21 +535,23 @@ MOE_API moe_status moe_grouped_gemm_fp8b(const void *x_q, const float *x_s, int 
                                          long long ldx, const void *w_q, const float *w_s, int E,
                                          int N, const int32_t *offsets, const int32_t *perm_tok,
                                          int rows, void *out, moe_dtype out_dt, long long ldo,
-                                         uint32_t *status, moe_stream stream);
+                                         void *workspace, size_t ws_bytes, uint32_t *status,
+                                         moe_stream stream);
 
 /*
  * moe_gate_up_fp8b -- both products of a SwiGLU expert and its h, quantised:
  *     h[r] = SiLU(W_g[e] x[perm_tok[r]]) * (W_u[e] x[perm_tok[r]])
  *   h_q [rows, F] codes and h_s [rows, ceil(F/128)] out, from the unrounded
  *   fp32 h.  wg_q, wu_q [E, F, d] with scales [E, ceil(F/128), ceil(d/128)];
- *   F a multiple of 16.  Groups, perm_tok and rows as moe_grouped_gemm_fp8b
+ *   F a multiple of 16.  Groups, perm_tok, rows and workspace as moe_grouped_gemm_fp8b
  *   (E == 1 with offsets NULL is the dense layer's).
  */
 MOE_API moe_status moe_gate_up_fp8b(const void *x_q, const float *x_s, int x_rows, int d,
                                     long long ldx, const void *wg_q, const float *wg_s,
                                     const void *wu_q, const float *wu_s, int E, int F,
                                     const int32_t *offsets, const int32_t *perm_tok, int rows,
-                                    void *h_q, float *h_s, uint32_t *status, moe_stream stream);
+                                    void *h_q, float *h_s, void *workspace, size_t ws_bytes,
+                                    uint32_t *status, moe_stream stream);
 
 /*
  * Test hook of the failure handling.  Every wait of the library's

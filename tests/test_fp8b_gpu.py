@@ -1,8 +1,8 @@
 """The block-scaled fp8 operators against their definitions in 64 bits.
 
 Tolerances, derived before the first run:
-  codes of given inputs   bit for bit: scale and quotient are single IEEE fp32
-                          operations, the code the nearest to the quotient.
+  codes of given inputs   bit for bit: scale, reciprocal and product are single
+                          IEEE fp32 operations, the code the nearest.
   products                a block's 128 exact products are summed on the tensor
                           cores (each addition off by at most 2^-23 of the sum
                           of magnitudes), then each block's sum takes three
@@ -59,9 +59,9 @@ def quant(x, block_rows):
     amax = t.abs().amax(dim=(-3, -1))        # (propagates NaN)
     # (a tensor divisor: torch divides by a Python number through its reciprocal)
     s = torch.where(torch.isfinite(amax), amax / torch.full_like(amax, FMAX), torch.nan)
-    each = s[..., :, None, :, None]
-    c = torch.where(each == 0, torch.zeros_like(t), t / each)
-    c = torch.where(each.isnan(), torch.nan, c.clamp(-FMAX, FMAX)).reshape(pad.shape)
+    s = torch.where(s < 2.0 ** -126, torch.zeros_like(s), s)
+    f = torch.where(s == 0, s, torch.ones_like(s) / s)[..., :, None, :, None]
+    c = torch.where(f.isnan(), torch.nan, (t * f).clamp(-FMAX, FMAX)).reshape(pad.shape)
     return c[..., :rows, :cols].to(F8).contiguous(), s
 
 
@@ -111,7 +111,7 @@ def test_quant_special_values(moe, block_rows):
     x = rand(9 * 128, 128)
     x[0:128] = 0
     x[128:256] = 1e-44                      # amax / 448 underflows to zero
-    x[256:384] *= 1e-40                     # the scale is subnormal
+    x[256:384] *= 1e-36                     # the scale is about the smallest normal number: some rows' are 0
     x[384:512] *= 3e37
     x[512:640, 5] = float("inf")
     x[640:768, 77] = float("nan")

@@ -57,23 +57,23 @@ def test_norm_arguments(lib):
 
 def test_product_arguments(lib):
     base = dict(xq=FAKE, xs=FAKE, xr=8, K=256, ldx=256, wq=FAKE, ws=FAKE, E=4, N=64, off=FAKE, perm=None, rows=8,
-                out=FAKE, odt=BF16, ldo=64, st=None)
+                out=FAKE, odt=BF16, ldo=64, ws_=FAKE, wsb=1 << 20, st=None)
 
     def grouped(**kw):
         a = dict(base, **kw)
         return lib.moe_grouped_gemm_fp8b(a["xq"], a["xs"], a["xr"], a["K"], a["ldx"], a["wq"], a["ws"], a["E"],
                                          a["N"], a["off"], a["perm"], a["rows"], a["out"], a["odt"], a["ldo"],
-                                         a["st"], None)
+                                         a["ws_"], a["wsb"], a["st"], None)
 
     def gate_up(**kw):
         a = dict(dict(base, uq=FAKE, us=FAKE, hq=FAKE, hs=FAKE), **kw)
         return lib.moe_gate_up_fp8b(a["xq"], a["xs"], a["xr"], a["K"], a["ldx"], a["wq"], a["ws"], a["uq"],
                                     a["us"], a["E"], a["N"], a["off"], a["perm"], a["rows"], a["hq"], a["hs"],
-                                    a["st"], None)
+                                    a["ws_"], a["wsb"], a["st"], None)
     both = (dict(xr=-1), dict(K=0), dict(K=24, ldx=32), dict(ldx=240), dict(ldx=264), dict(E=0), dict(N=0),
             dict(rows=-1), dict(off=None), dict(rows=9), dict(xr=0, perm=FAKE), dict(xq=None), dict(xs=None),
             dict(wq=None), dict(ws=None), dict(xq=ODD), dict(wq=ODD), dict(xs=ODD2), dict(ws=ODD2),
-            dict(off=ODD2), dict(perm=ODD2), dict(st=ODD2))
+            dict(off=ODD2), dict(perm=ODD2), dict(st=ODD2), dict(perm=FAKE, ws_=None), dict(perm=FAKE, ws_=vp(0x10080)))
     for bad in both:
         assert grouped(**bad) == I, bad
         assert gate_up(**bad) == I, bad
@@ -82,6 +82,10 @@ def test_product_arguments(lib):
     for bad in (dict(N=72), dict(uq=None), dict(us=None), dict(hq=None), dict(hs=None), dict(uq=ODD), dict(hq=ODD),
                 dict(us=ODD2), dict(hs=ODD2)):
         assert gate_up(**bad) == I, bad
+    # scratch of gathered rows: 8 x 256 codes and 8 x 2 scales, each to 256 bytes
+    assert lib.moe_fp8b_workspace_size(8, 256) == 2048 + 256
+    assert lib.moe_fp8b_workspace_size(8, 250) == 0 and lib.moe_fp8b_workspace_size(-1, 256) == 0
+    assert grouped(perm=FAKE, wsb=2303) == 3 and gate_up(perm=FAKE, wsb=2303) == 3      # MOE_ERR_WORKSPACE
     assert grouped(E=257) == U and gate_up(E=257) == U
     assert grouped(rows=0, xr=0, xq=None, out=None) == OK and gate_up(rows=0, xr=0, xq=None, hq=None) == OK
     g = lambda **kw: lib.moe_gemm_fp8b(*dict(dict(a=FAKE, b=FAKE, T=4, K=256, l=256, c=FAKE, d=FAKE, N=64, o=FAKE,
@@ -129,6 +133,6 @@ def test_binding_refuses_wrong_pairs():
             moe.moe_norm_fp8b(**dict(nm, **bad))
     for bad, err in ((dict(x=torch.zeros(256)), ValueError), (dict(block_rows=64), ValueError),
                      (dict(x=torch.zeros(4, 4, dtype=torch.int32)), TypeError), (dict(x=x.t()), ValueError),
-                     (dict(x=torch.zeros(2, 4, 512)[:, :3]), ValueError), (dict(scales=torch.zeros(4, 3)), ValueError)):
+                     (dict(x=torch.zeros(2, 4, 512)[:, :3]), ValueError), (dict(x=[1.0]), TypeError), (dict(scales=torch.zeros(4, 3)), ValueError)):
         with pytest.raises(err):
             moe.moe_quant_fp8b(**dict(dict(x=x), **bad))
