@@ -1,0 +1,434 @@
+// fp8b_decode.cu -- the products of fp8b_gemm.cu for few rows per expert
+// (decode): the weights are streamed once, and everything else has to fit into
+// the time that takes.
+//
+// The roles of the operands are exchanged: the weights are the MMA's 128 rows
+// (TMEM lanes) and up to 32 token rows its columns, so that a block's partial
+// sum is 32 columns of TMEM instead of 256, and every lane of the epilogue holds
+// an output column with its tokens -- stores of a token are contiguous over the
+// warp as they are.  (Tokens as the rows: a decode batch of 4 rows per expert
+// kept 4 of 128 lanes busy, and the tile's epilogue and two waves of tiles cost
+// more than the weights' time.)
+//
+// A tile is 128 output columns (PRODUCT: of W; GATEUP: of W_gate and W_up) of
+// one expert times up to 32 of its rows.  Warp 0 loads (TMA; token rows in a box
+// of 32, or gathered four at a time through perm_tok), warp 1 multiplies, warps
+// 2-5 hold the sums.  A token's scale belongs to a column here, so each warp
+// lays out the block's 32 factors sx[t] * sw in shared memory and reads them
+// back as broadcasts.  Two CTAs share an SM (ring of 3 or 5 stages each), so one
+// tile's start and end overlap the other's loads.
+//
+// Few tiles: the reduction is split over a cluster (SPLIT) as in fp8b_gemm.cu;
+// token t is finished by CTA t % split of the cluster.
+#include "fp8b_tc.cuh"
+
+namespace moe {
+namespace fp8b {
+
+namespace {
+
+constexpr int NT = 32;                       // token rows of a tile
+constexpr int M = 128, BK = kBlock;
+constexpr int W_BYTES = M * BK, X_BYTES = NT * BK;
+constexpr int kBuffers = 4;                  // partial sums in TMEM
+constexpr int kEpiWarps = 4;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+
+template <int MODE> struct Cfg {
+    static constexpr int NW = MODE == GATEUP ? 2 : 1;           // weight matrices
+    static constexpr int STAGE = NW * W_BYTES + X_BYTES;
+    static constexpr int STAGES = MODE == GATEUP ? 3 : 5;
+    static constexpr int TMEM_COLS = kBuffers * NW * NT;        // 128 or 256
+    static constexpr size_t RING = (size_t)STAGES * STAGE;
+};
+constexpr int kMaxStages = 5;
+
+struct alignas(16) Ctl {
+    uint64_t full[kMaxStages], empty[kMaxStages], tfull[kBuffers], tempty[kBuffers], drain;
+    uint32_t tmem_base;
+    int abort_flag;
+    uint32_t amax[kEpiWarps][NT];            // GATEUP: each warp's largest |h| per token
+    float factor[kEpiWarps][2][NT];          // [warp][matrix][token]
+    Groups g;
+};
+template <int MODE> constexpr size_t smem_bytes() { return 1024 + Cfg<MODE>::RING + sizeof(Ctl); }
+static_assert(smem_bytes<PRODUCT>() <= 115712 && smem_bytes<GATEUP>() <= 115712, "two CTAs per SM");
+static_assert((size_t)NT * 2 * M * 4 <= Cfg<GATEUP>::RING && (size_t)NT * M * 4 <= Cfg<PRODUCT>::RING,
+              "split partial sums reuse the ring");
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr));
+}
+// Wait for the warp's TMEM loads; the registers pass through it, so that
+// nothing that reads them moves above it.
+__device__ __forceinline__ void tmem_ld_wait32(uint32_t (&v)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
+                   "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                   "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+__device__ __forceinline__ void store_out(const Params &p, long long r, int n, float v)
+{
+    if (p.out_f32) static_cast<float *>(p.out)[r * p.ldo + n] = v;
+    else static_cast<__nv_bfloat16 *>(p.out)[r * p.ldo + n] = __float2bfloat16_rn(v);
+}
+
+template <int MODE, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 2)
+decode_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w0,
+              const __grid_constant__ CUtensorMap tm_w1, const Params p)
+{
+    using C = Cfg<MODE>;
+    constexpr int NW = C::NW, STAGES = C::STAGES;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    Ctl &c = *reinterpret_cast<Ctl *>(smem + C::RING);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int E = p.E;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) { mbar_init(&c.full[s], 1); mbar_init(&c.empty[s], 1); }
+        for (int b = 0; b < kBuffers; ++b) { mbar_init(&c.tfull[b], 1); mbar_init(&c.tempty[b], kEpiWarps); }
+        mbar_init(&c.drain, 1);
+        c.abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_x)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_w0)) : "memory");
+        if (MODE == GATEUP)
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_w1)) : "memory");
+    }
+    if (warp == 1) tmem_alloc(&c.tmem_base, C::TMEM_COLS);
+    tc_fence_before();
+    pdl_enter();
+    load_groups(c.g, p);
+    __syncthreads();
+    if (warp == 0) scan_groups(c.g, p, NT, lane);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+
+    const uint32_t tmem = c.tmem_base;
+    const int total = c.g.total;
+    const int S = SPLIT ? p.split : 1;
+    const int rank = SPLIT ? (int)cluster_rank() : 0;
+    const int first = SPLIT ? blockIdx.x / S : blockIdx.x;
+    const int stride = SPLIT ? gridDim.x / S : gridDim.x;
+    // this CTA's blocks of the reduction
+    const int kb0 = (int)((long long)p.KB * rank / S), kb1 = (int)((long long)p.KB * (rank + 1) / S);
+    volatile int *abort_flag = &c.abort_flag;
+
+    if (warp == 0) {
+        // ------------------------------------------------ loads
+        uint32_t it = 0;
+        bool ok = true;
+        for (int t = first; t < total && ok; t += stride) {
+            const Tile tile = tile_at(c.g, E, t, NT);
+            int4 tok = make_int4(0, 0, 0, 0);
+            const int gathers = p.perm_tok ? (tile.cnt + 3) / 4 : 0;
+            if (lane < gathers) {
+                int v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // (an index out of range reads row 0: its row is undefined)
+                    v[i] = __ldg(p.perm_tok + tile.row0 + min(4 * lane + i, tile.cnt - 1));
+                    if (v[i] < 0 || v[i] >= p.x_rows) v[i] = 0;
+                }
+                tok = make_int4(v[0], v[1], v[2], v[3]);
+            }
+            const uint32_t bytes = NW * W_BYTES + (p.perm_tok ? gathers * 4 * BK : X_BYTES);
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const int s = it % STAGES;
+                ok = __all_sync(0xffffffffu, bar_wait(&c.empty[s], ((it / STAGES) & 1u) ^ 1u, abort_flag));
+                if (!ok) break;
+                uint8_t *sw = smem + s * C::STAGE, *sx = sw + NW * W_BYTES;
+                if (lane == 0) {
+                    mbar_expect_tx(&c.full[s], bytes);
+                    tma_load_3d(sw, &tm_w0, &c.full[s], kb * BK, tile.nt * M, tile.e);
+                    if (MODE == GATEUP) tma_load_3d(sw + W_BYTES, &tm_w1, &c.full[s], kb * BK, tile.nt * M, tile.e);
+                    if (!p.perm_tok) tma_load_2d(sx, &tm_x, &c.full[s], kb * BK, tile.row0);
+                }
+                __syncwarp();
+                if (lane < gathers) tma_gather4(sx + lane * 4 * BK, &tm_x, &c.full[s], kb * BK, tok);
+            }
+        }
+        if (!ok) {
+            if (lane == 0) flag_status(p.status, kDevTimeout);
+            c.abort_flag = 1;
+            // let loads already issued land before the CTA exits
+            for (uint32_t j = (it >= STAGES ? it - STAGES : 0); j < it; ++j) {
+                volatile int no_abort = 0;
+                bar_wait(&c.full[j % STAGES], (j / STAGES) & 1u, &no_abort, 1000000ull);
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ multiply
+        constexpr uint32_t idesc = idesc_e4m3(M, NT);
+        const bool leader = elect_one();
+        const uint32_t ring = smem_u32(smem);
+        uint32_t it = 0;
+        bool ok = true;
+        for (int t = first; t < total && ok; t += stride) {
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const int s = it % STAGES;
+                const uint32_t b = it % kBuffers;
+                ok = bar_wait(&c.tempty[b], ((it / kBuffers) & 1u) ^ 1u, abort_flag) &&
+                     bar_wait(&c.full[s], (it / STAGES) & 1u, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t dw = sw128_desc(ring + s * C::STAGE), dx = sw128_desc(ring + s * C::STAGE + NW * W_BYTES);
+                const uint32_t d = tmem + b * NW * NT;
+                if (leader) {
+#pragma unroll
+                    for (int w = 0; w < NW; ++w) {
+                        const uint64_t da = desc_step(dw, w * W_BYTES);
+                        umma_f8<false>(d + w * NT, da, dx, idesc);
+#pragma unroll
+                        for (int kk = 1; kk < BK / 32; ++kk)
+                            umma_f8<true>(d + w * NT, desc_step(da, kk * 32), desc_step(dx, kk * 32), idesc);
+                    }
+                    umma_commit(&c.tfull[b]);
+                    umma_commit(&c.empty[s]);
+                }
+            }
+        }
+        if (!ok) {
+            if (leader) flag_status(p.status, kDevTimeout);
+            c.abort_flag = 1;
+            if (leader) umma_commit(&c.drain);   // MMAs in flight end before TMEM is freed
+            volatile int no_abort = 0;
+            bar_wait(&c.drain, 0, &no_abort);
+        }
+    } else {
+        // ------------------------------------------------ sums and output
+        const int ew = warp - 2, quarter = warp & 3, chan = quarter * 32 + lane;
+        uint32_t it = 0;
+        bool ok = true;   // once false, no more waits: the remaining rows become NaN
+        for (int t = first; t < total; t += stride) {
+            const Tile tile = tile_at(c.g, E, t, NT);
+            // lane l of every warp holds token l's scales
+            const float *xs = nullptr;
+            if (lane < tile.cnt) {
+                const int r = tile.row0 + lane;
+                const int src = p.perm_tok ? __ldg(p.perm_tok + r) : r;
+                if (src >= 0 && src < p.x_rows) xs = p.x_s + (size_t)src * p.KB;
+            }
+            const float *ws[2];
+#pragma unroll
+            for (int w = 0; w < NW; ++w) ws[w] = p.w_s[w] + ((size_t)tile.e * p.NB + tile.nt) * p.KB;
+            uint64_t acc[NW][NT / 2];
+#pragma unroll
+            for (int w = 0; w < NW; ++w)
+#pragma unroll
+                for (int i = 0; i < NT / 2; ++i) acc[w][i] = 0ull;
+            float nx = xs ? __ldg(xs + kb0) : 0.f, nw[2] = {__ldg(ws[0] + kb0), NW == 2 ? __ldg(ws[NW - 1] + kb0) : 0.f};
+#pragma unroll 1
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const uint32_t b = it % kBuffers;
+                float(&f)[2][NT] = c.factor[ew];
+                __syncwarp();   // (the block before has been read)
+#pragma unroll
+                for (int w = 0; w < NW; ++w) f[w][lane] = nx * nw[w];
+                if (kb + 1 < kb1) {
+                    nx = xs ? __ldg(xs + kb + 1) : 0.f;
+#pragma unroll
+                    for (int w = 0; w < NW; ++w) nw[w] = __ldg(ws[w] + kb + 1);
+                }
+                __syncwarp();
+                ok = ok && __all_sync(0xffffffffu, bar_wait(&c.tfull[b], (it / kBuffers) & 1u, abort_flag));
+                tc_fence_after();
+                const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + b * NW * NT;
+#pragma unroll
+                for (int w = 0; w < NW; ++w) {
+                    uint32_t v[NT];
+                    tmem_ld32(base + w * NT, v);
+                    tmem_ld_wait32(v);
+                    if (w == NW - 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&c.tempty[b]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < NT / 4; ++i) {
+                        const float4 q = *reinterpret_cast<const float4 *>(&f[w][4 * i]);
+                        fma2(acc[w][2 * i], pack2(v[4 * i], v[4 * i + 1]), pack2(__float_as_uint(q.x), __float_as_uint(q.y)));
+                        fma2(acc[w][2 * i + 1], pack2(v[4 * i + 2], v[4 * i + 3]), pack2(__float_as_uint(q.z), __float_as_uint(q.w)));
+                    }
+                }
+            }
+            if (!ok) {
+                c.abort_flag = 1;
+#pragma unroll
+                for (int w = 0; w < NW; ++w)
+#pragma unroll
+                    for (int i = 0; i < NT / 2; ++i) acc[w][i] = 0x7fffffff7fffffffull;
+            }
+            auto val = [&](int w, int i) { return (i & 1) ? hi2(acc[w][i >> 1]) : lo2(acc[w][i >> 1]); };
+            const int n = tile.nt * M + chan;
+            if constexpr (SPLIT) {
+                // every MMA of this CTA has completed: the ring holds the partial
+                // sums from here on, [token][matrix][channel]
+                float *part = reinterpret_cast<float *>(smem) + chan;
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    if (i >= tile.cnt) break;
+#pragma unroll
+                    for (int w = 0; w < NW; ++w) part[(i * NW + w) * M] = val(w, i);
+                }
+                break;   // one tile per cluster
+            } else if constexpr (MODE == GATEUP) {
+                uint32_t mine = 0u;   // lane l: largest |h| of token l over the warp's channels
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    if (i >= tile.cnt) break;
+                    const float h = swiglu(val(0, i), val(NW - 1, i));
+                    const uint32_t m = __reduce_max_sync(0xffffffffu, mag_bits(h));
+                    if (lane == i) mine = m;
+                    // (h takes the place of its gate sum)
+                    acc[0][i >> 1] = (i & 1) ? pack2((uint32_t)acc[0][i >> 1], __float_as_uint(h))
+                                             : pack2(__float_as_uint(h), (uint32_t)(acc[0][i >> 1] >> 32));
+                }
+                c.amax[ew][lane] = mine;
+                epilogue_barrier();   // (all four warps take every turn of the tile loop, whatever happened before)
+#pragma unroll
+                for (int w = 0; w < kEpiWarps; ++w) mine = max(mine, c.amax[w][lane]);
+                epilogue_barrier();
+                const float s = block_scale(mine), f = code_factor(s);
+                if (ew == 0 && lane < tile.cnt) p.h_s[(size_t)(tile.row0 + lane) * p.NB + tile.nt] = s;
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    if (i >= tile.cnt) break;
+                    const float q = val(0, i) * __shfl_sync(0xffffffffu, f, i);
+                    if (n < p.N) p.h_q[(size_t)(tile.row0 + i) * p.N + n] = (uint8_t)e4m3x2(q, 0.f);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    if (i >= tile.cnt) break;
+                    if (n < p.N) store_out(p, tile.row0 + i, n, val(0, i));
+                }
+            }
+        }
+    }
+
+    if constexpr (SPLIT) {
+        cluster_sync_all();   // every CTA's partial sums are written
+        if (first < total && warp >= 2) {
+            // tokens rank, rank + S, ...: a thread to a channel adds the CTAs'
+            // sums in the order of the blocks
+            const Tile tile = tile_at(c.g, E, first, NT);
+            const int ew = warp - 2, chan = (warp & 3) * 32 + lane, n = tile.nt * M + chan;
+            // (a CTA that gave up may still have had loads landing on its sums)
+            bool failed = false;
+            for (int q = 0; q < S; ++q) failed |= ld_cluster_u32(peer_addr(&c.abort_flag, q)) != 0u;
+            for (int i = rank; i < tile.cnt; i += S) {
+                float v[2] = {0.f, 0.f};
+#pragma unroll 8
+                for (int q = 0; q < S; ++q) {
+                    const uint32_t at = peer_addr(smem, q) + (uint32_t)(i * NW * M + chan) * 4;
+#pragma unroll
+                    for (int w = 0; w < NW; ++w) v[w] += ld_cluster_f32(at + w * M * 4);
+                }
+                if (failed) v[0] = v[1] = __uint_as_float(0x7fffffffu);
+                const long long r = tile.row0 + i;
+                if constexpr (MODE == GATEUP) {
+                    const float h = swiglu(v[0], v[1]);
+                    uint32_t m = __reduce_max_sync(0xffffffffu, mag_bits(h));
+                    if (lane == 0) c.amax[ew][0] = m;
+                    epilogue_barrier();
+#pragma unroll
+                    for (int w = 0; w < kEpiWarps; ++w) m = max(m, c.amax[w][0]);
+                    epilogue_barrier();
+                    const float s = block_scale(m);
+                    if (n < p.N) p.h_q[r * p.N + n] = (uint8_t)e4m3x2(h * code_factor(s), 0.f);
+                    if (threadIdx.x == 64) p.h_s[r * p.NB + tile.nt] = s;
+                } else if (n < p.N) {
+                    store_out(p, r, n, v[0]);
+                }
+            }
+        }
+        cluster_sync_all();   // no CTA leaves while a peer reads its shared memory
+    } else {
+        __syncthreads();
+    }
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TMEM_COLS);
+    }
+}
+
+template <int MODE, bool SPLIT>
+cudaError_t launch_variant(const CUtensorMap &x, const CUtensorMap &w0, const CUtensorMap &w1, const Params &p,
+                           long long tiles, int num_sms, cudaStream_t stream)
+{
+    static PerDeviceFlag done;
+    const int dev = current_device();
+    auto *kern = decode_kernel<MODE, SPLIT>;
+    constexpr size_t smem = smem_bytes<MODE>();
+    if (!done.done(dev)) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        done.mark(dev);
+    }
+    if (SPLIT)
+        return launch_pdl_cluster(kern, dim3((unsigned)(tiles * p.split)), dim3(kThreads), smem, stream, p.split, x, w0,
+                                  w1, p);
+    return launch_pdl(kern, dim3((unsigned)(tiles < 2 * num_sms ? tiles : 2 * num_sms)), dim3(kThreads), smem, stream,
+                      x, w0, w1, p);
+}
+
+}  // namespace
+
+// Few rows per expert: at most 24 on average over the experts that can have any
+// (a tile holds 32; an expert with more takes several tiles, which read its
+// weights again through L2).
+bool decode_fits(const Params &p)
+{
+    const long long experts = p.E < p.rows ? p.E : p.rows;
+    return p.rows <= 24 * experts;
+}
+
+template <int MODE>
+cudaError_t launch_decode(const void *x_q, long long ldx, const void *w0, const void *w1, Params p, int num_sms,
+                          cudaStream_t stream)
+{
+    p.n_tiles = ceil_div(p.N, M);
+    // most tiles there can be: every expert with rows may own a ragged row tile
+    const long long groups = (long long)p.rows / NT + (p.E < p.rows ? p.E : p.rows);
+    const long long tiles = groups * p.n_tiles;
+    if (tiles > 0x3fffffffLL) return cudaErrorInvalidValue;
+    // tiles for fewer than half the places (two CTAs an SM): split the reduction
+    p.split = 1;
+    if (tiles <= num_sms) {
+        const long long each = 2LL * num_sms / tiles;
+        p.split = (int)(each < 8 ? each : 8);
+        if (p.split > p.KB) p.split = p.KB;
+    }
+    CUtensorMap mx, mw0, mw1;
+    if (!code_map(&mx, x_q, 0, p.x_rows, p.K, ldx, p.perm_tok ? 1 : NT) || !code_map(&mw0, w0, p.E, p.N, p.K, p.K, M))
+        return cudaErrorInvalidValue;
+    if (MODE != GATEUP) mw1 = mw0;
+    else if (!code_map(&mw1, w1, p.E, p.N, p.K, p.K, M)) return cudaErrorInvalidValue;
+    return p.split > 1 ? launch_variant<MODE, true>(mx, mw0, mw1, p, tiles, num_sms, stream)
+                       : launch_variant<MODE, false>(mx, mw0, mw1, p, tiles, num_sms, stream);
+}
+
+template cudaError_t launch_decode<PRODUCT>(const void *, long long, const void *, const void *, Params, int, cudaStream_t);
+template cudaError_t launch_decode<GATEUP>(const void *, long long, const void *, const void *, Params, int, cudaStream_t);
+
+}  // namespace fp8b
+}  // namespace moe

@@ -14,46 +14,32 @@
 // A tile is 128 rows x 256 columns (PRODUCT), or 128 rows x 128 columns of
 // both W_gate and W_up (GATEUP: the epilogue has whole 128-column groups of h,
 // so it quantises them without a second pass).  Warp 0 loads by TMA (rows in
-// boxes of 32, only as many as the tile has); rows that a split product gathers
-// through perm_tok are copied by warps 0 and 3 (cp.async; TMA's four-row gathers
-// took 75 clocks each).  Warps 1 and 2 multiply a
-// column half each.  Warps 4-11 hold the sums: warp w the TMEM
-// lanes of quarter w % 4 and one half of the columns (128 of them, or 64 of
-// gate and the same 64 of up).
+// boxes of 32, only as many as the tile has), warps 1 and 2 multiply a column
+// half each, warps 4-11 hold the sums: warp w the TMEM lanes of quarter w % 4
+// and one half of the columns (128 of them, or 64 of gate and the same 64 of up).
+// Batches of few rows per expert take the kernel of fp8b_decode.cu instead.
 //
 // Rows of a tile past the end of its group are left out of the loads and the
 // stores (their lanes of the MMA compute on whatever the buffer holds; rows
 // do not mix).  Columns past N and the last block's columns past K are zeros
 // by TMA's fill.
 //
-// Few tiles (decode): the reduction is split over a cluster of 2, 4 or 8 CTAs
-// (SPLIT), whose partial sums meet in distributed shared memory, one row per
-// warp, added in the order of the blocks.
+// Few tiles: the reduction is split over a cluster of up to 8 CTAs (SPLIT),
+// whose partial sums meet in distributed shared memory, one row per warp, added
+// in the order of the blocks.
 //
 // Every wait is bounded (2 s).  Where one gives up, the rows of the CTA's
 // remaining tiles are written as NaN, and the status word says so if the
 // caller passed one.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include "fp8b.h"
-#include "kernels.h"
-#include "sm100.cuh"
+#include "fp8b_tc.cuh"
 
 namespace moe {
-namespace tc {
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn();   // tc_gemm.cu
-}
 namespace fp8b {
-
-using namespace sm100;
 
 constexpr int BM = 128, BN = 256, BK = kBlock;   // one MMA k-block = one scale block
 constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE = A_BYTES + B_BYTES;
 constexpr int STAGES = 4;
 constexpr int ABOX = 32;                         // rows per A load
-constexpr uint32_t kGatherLag = 2;               // gathered stages in flight before the oldest is handed over
-static_assert(kGatherLag < STAGES, "a stage is handed over before it is needed again");
 constexpr int TMEM_COLS = 512;                   // two partial sums of 256 columns
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;   // warps 0-3: load, multiply, multiply, gather
@@ -64,91 +50,17 @@ static_assert(4 * kRegsAux + kEpiWarps * kRegsEpi <= 12 * kRegsLaunch, "more reg
 constexpr int kPartRow = BN + 4;                 // floats per row of a split partial sum (16-byte
                                                  // stores of 8 rows fall in distinct banks)
 
-enum Mode { PRODUCT = 0, GATEUP = 1 };
-
-struct Params {
-    const uint8_t *x_q;       // gathering: [x_rows, K] codes, rows ldx bytes apart
-    long long ldx;
-    const float *x_s;         // [x_rows, KB]
-    const float *w_s[2];      // [E, NB, KB] of W (PRODUCT) or W_gate, W_up
-    const int32_t *offsets;   // [E+1], or NULL: one group of all rows
-    const int32_t *perm_tok;  // [rows] (gathering)
-    int E, rows, x_rows, K, N, KB, NB, n_tiles;
-    void *out;                // PRODUCT: [rows, ldo] bf16 or fp32
-    long long ldo;
-    int out_f32, out_vec;     // out_vec: rows are multiples of 16 bytes apart, from a 16-byte boundary
-    uint8_t *h_q;             // GATEUP: [rows, N] codes, [rows, NB] scales
-    float *h_s;
-    uint32_t *status;
-    int split;                // CTAs per cluster (SPLIT)
-};
-
 struct alignas(16) Ctl {
     uint64_t full[STAGES], empty[STAGES], tfull[2][2], tempty[2][2], drain[2];   // [buffer][column half]
     uint32_t tmem_base;
     int abort_flag;
-    int total;
-    int off[kMaxExperts + 1], tile_start[kMaxExperts + 1], mtiles[kMaxExperts];
+    Groups g;
     uint32_t amax[2][BM];     // GATEUP: each row's largest |h| per column half
 };
 constexpr int kStaging = 32 * 64;                // bytes per epilogue warp: 64 of each of its rows
 constexpr size_t kSmem = 1024 + (size_t)STAGES * STAGE + sizeof(Ctl) + kEpiWarps * kStaging;
 static_assert(kSmem <= 232448, "shared memory per CTA");
 static_assert((size_t)BM * kPartRow * 4 <= (size_t)STAGES * STAGE, "split partial sums reuse the ring");
-
-// Instruction descriptor of tcgen05.mma kind::f8f6f4: fp32 accumulate, A and B
-// E4M3 (format 0), both K-major, shape M x N.
-constexpr uint32_t idesc_e4m3(int M, int N)
-{
-    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-template <bool ACCUMULATE>
-__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "n"(ACCUMULATE ? 1 : 0)
-        : "memory");
-}
-// One lane of the (converged) warp.
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t is;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(is));
-    return is != 0;
-}
-__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-        : "memory");
-}
-// 16 bytes, or 16 zeros where `in` is false
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool in)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
-}
-template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-// mbar_wait, inline as a whole: across a call the compiler cannot keep the
-// sums of the epilogue warps in the registers that setmaxnreg gives them.
-__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
-                                         unsigned long long timeout_ns = kTimeoutNs)
-{
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer();
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((it & 255u) == 0) {
-            if (*abort_flag) return false;
-            if (globaltimer() - t0 > timeout_ns) return false;
-        }
-    }
-}
 
 // Wait for the warp's TMEM loads; the registers pass through it, so that
 // nothing that reads them moves above it.
@@ -160,35 +72,12 @@ __device__ __forceinline__ void tmem_ld_wait16(uint32_t (&v)[16])
                  :
                  : "memory");
 }
-__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-    return r;
-}
-__device__ __forceinline__ float lo2(uint64_t v) { return __uint_as_float((uint32_t)v); }
-__device__ __forceinline__ float hi2(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
-// two fp32 fused multiply-adds in one instruction, each rounded as fmaf is
-__device__ __forceinline__ void fma2(uint64_t &acc, uint64_t a, uint64_t b)
-{
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
-}
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr)
 {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                  : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
     return v;
-}
-
-// SwiGLU with the fast exponential and an approximate divide (relative error
-// ~1e-6, far below the codes' 2^-4; for g < -87, 1 + e^-g overflows and h is 0)
-__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
-
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
-{
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&v);
 }
 
 // Four output values: columns [n0, n0 + 4) of row r (split sums: a warp writes
@@ -252,29 +141,7 @@ __device__ __forceinline__ void store_rows(uint8_t *stg, int lane, const uint4 (
     __syncwarp();
 }
 
-struct Tile { int e, nt, row0, cnt; };   // expert, column tile, first grouped row, rows
-
-// tile -> its expert, column tile and rows; within an expert the row tiles run
-// fastest, so CTAs running at the same time share weight tiles through L2.
-__device__ __forceinline__ Tile tile_at(const Ctl &c, int E, int t)
-{
-    int lo = 0, hi = E - 1;   // largest e with tile_start[e] <= t
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (c.tile_start[mid] <= t) lo = mid;
-        else hi = mid - 1;
-    }
-    const int local = t - c.tile_start[lo], m = c.mtiles[lo];
-    Tile r;
-    r.e = lo;
-    r.nt = local / m;
-    const int mt = local - r.nt * m;
-    r.row0 = c.off[lo] + mt * BM;
-    r.cnt = min(BM, c.off[lo + 1] - r.row0);
-    return r;
-}
-
-template <int MODE, bool GATHER, bool SPLIT>
+template <int MODE, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w0,
                const __grid_constant__ CUtensorMap tm_w1, const Params p)
@@ -286,7 +153,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     const int E = p.E;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) { mbar_init(&c.full[s], GATHER ? 3 : 1); mbar_init(&c.empty[s], 2); }
+        for (int s = 0; s < STAGES; ++s) { mbar_init(&c.full[s], 1); mbar_init(&c.empty[s], 2); }
         for (int b = 0; b < 4; ++b) { mbar_init(&c.tfull[b >> 1][b & 1], 1); mbar_init(&c.tempty[b >> 1][b & 1], kEpiWarps / 2); }
         for (int h = 0; h < 2; ++h) mbar_init(&c.drain[h], 1);
         c.abort_flag = 0;
@@ -299,45 +166,15 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     if (warp == 3) tmem_alloc(&c.tmem_base, TMEM_COLS);
     tc_fence_before();
     pdl_enter();
-    // group bounds, kept inside [0, rows] whatever the array holds
-    for (int e = threadIdx.x; e <= E; e += kThreads)
-        c.off[e] = p.offsets ? min(max(p.offsets[e], 0), p.rows) : e * p.rows;
+    load_groups(c.g, p);
     __syncthreads();
-    if (warp == 0) {
-        // exclusive scan of row tiles * column tiles over experts (8 per lane)
-        int local[8], sum = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int e = lane * 8 + j;
-            int m = 0;
-            if (e < E) {
-                m = (max(c.off[e + 1] - c.off[e], 0) + BM - 1) / BM;
-                c.mtiles[e] = m;
-            }
-            local[j] = m * p.n_tiles;
-            sum += local[j];
-        }
-        int incl = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-        }
-        int run = incl - sum;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int e = lane * 8 + j;
-            if (e < E) c.tile_start[e] = run;
-            run += local[j];
-        }
-        if (lane == 31) c.total = incl;
-    }
+    if (warp == 0) scan_groups(c.g, p, BM, lane);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
 
     const uint32_t tmem = c.tmem_base;
-    const int total = c.total;
+    const int total = c.g.total;
     const int S = SPLIT ? p.split : 1;
     const int rank = SPLIT ? (int)cluster_rank() : 0;
     const int first = SPLIT ? blockIdx.x / S : blockIdx.x;
@@ -348,40 +185,19 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     if (warp < 4) {
         // (inside the branch: the compiler gives each side its own limit)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsAux));
-        if (warp == 0 || (GATHER && warp == 3)) {
+        if (warp == 0) {
             // -------------------------------------------- loads
-            // Warp 0: the weights (and rows in order) by TMA.  Gathered rows:
-            // warp 0 copies rows 0-63 of the tile, warp 3 rows 64-127, 8 lanes to
-            // a row's 128 bytes, 4 rows an instruction, into the swizzled layout
-            // that TMA gives the other operand.
-            const int rsub = lane >> 3, chunk = lane & 7, first_row = warp ? 64 : 0;
-            uint32_t it = 0, arrived = 0;
+            uint32_t it = 0;
             bool ok = true;
-            // the copies of the stages before `upto` have landed: hand them to the MMA
-            auto hand_over = [&](uint32_t upto) {
-                fence_proxy_async_smem();
-                __syncwarp();
-                for (; arrived < upto; ++arrived)
-                    if (lane == 0) mbar_arrive(&c.full[arrived % STAGES]);
-            };
             for (int t = first; t < total && ok; t += stride) {
-                const Tile tile = tile_at(c, E, t);
-                const int boxes = GATHER ? 0 : (tile.cnt + ABOX - 1) / ABOX;
-                int tok[GATHER ? 16 : 1];
-                if (GATHER) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int r = first_row + 4 * i + rsub;
-                        tok[i] = r < tile.cnt ? __ldg(p.perm_tok + tile.row0 + r) : -1;
-                        if (tok[i] >= p.x_rows) tok[i] = -1;   // (out of range: not read, its row is undefined)
-                    }
-                }
+                const Tile tile = tile_at(c.g, E, t, BM);
+                const int boxes = (tile.cnt + ABOX - 1) / ABOX;
                 for (int kb = kb0; kb < kb1; ++kb, ++it) {
                     const int s = it % STAGES;
                     ok = __all_sync(0xffffffffu, bar_wait(&c.empty[s], ((it / STAGES) & 1u) ^ 1u, abort_flag));
                     if (!ok) break;
                     uint8_t *sa = smem + s * STAGE, *sb = sa + A_BYTES;
-                    if (warp == 0 && lane == 0) {
+                    if (lane == 0) {
                         mbar_expect_tx(&c.full[s], (uint32_t)(boxes * ABOX * BK) + B_BYTES);
                         if (MODE == GATEUP) {
                             // per column half: 64 rows of W_gate, 64 of W_up
@@ -397,33 +213,14 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                         }
                     }
                     __syncwarp();
-                    if constexpr (GATHER) {
-                        const bool in = kb * BK + chunk * 16 < p.K;
-                        const uint32_t at = smem_u32(sa) + (first_row + rsub) * BK;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (tok[i] >= 0)
-                                cp_async16(at + i * 4 * BK + ((chunk ^ ((4 * i + rsub) & 7)) << 4),
-                                           p.x_q + (in ? tok[i] * p.ldx + kb * BK + chunk * 16 : 0), in);
-                        asm volatile("cp.async.commit_group;" ::: "memory");
-                        if (it - arrived >= kGatherLag) {
-                            cp_async_wait<kGatherLag>();
-                            hand_over(arrived + 1);
-                        }
-                    } else if (lane < boxes) {
+                    if (lane < boxes)
                         tma_load_2d(sa + lane * ABOX * BK, &tm_x, &c.full[s], kb * BK, tile.row0 + lane * ABOX);
-                    }
                 }
-            }
-            if (GATHER) {
-                cp_async_wait<0>();
-                if (ok) hand_over(it);
             }
             if (!ok) {
                 if (lane == 0) flag_status(p.status, kDevTimeout);
                 c.abort_flag = 1;
-                // let loads already issued land before the CTA exits (gathered
-                // stages may miss an arrival: then the wait's limit ends it)
+                // let loads already issued land before the CTA exits
                 for (uint32_t j = (it >= STAGES ? it - STAGES : 0); j < it; ++j) {
                     volatile int no_abort = 0;
                     bar_wait(&c.full[j % STAGES], (j / STAGES) & 1u, &no_abort, 1000000ull);
@@ -480,14 +277,10 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         uint32_t it = 0;
         bool ok = true;   // once false, no more waits: the remaining rows become NaN
         for (int t = first; t < total; t += stride) {
-            const Tile tile = tile_at(c, E, t);
+            const Tile tile = tile_at(c.g, E, t, BM);
             const bool valid = row < tile.cnt;
             const long long r = tile.row0 + row;
-            const float *xs = nullptr;
-            if (valid) {
-                const int src = GATHER ? __ldg(p.perm_tok + r) : (int)r;
-                if (src >= 0 && src < p.x_rows) xs = p.x_s + (size_t)src * p.KB;
-            }
+            const float *xs = valid ? p.x_s + r * p.KB : nullptr;
             // the weight scales of the columns this warp sums: gate and up, or
             // one 128-column block (none past the last: its sums are zero)
             const int nb = MODE == GATEUP ? tile.nt : min(tile.nt * 2 + half, p.NB - 1);
@@ -537,8 +330,10 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             }
             auto val = [&](int i) { return (i & 1) ? hi2(acc[i >> 1]) : lo2(acc[i >> 1]); };
             if constexpr (SPLIT) {
-                // every MMA of this CTA has completed: the ring holds the partial
-                // sums from here on, in tile column order
+                // once the other half's MMAs have completed too, the ring holds
+                // the partial sums, in tile column order
+                const uint32_t last = it - 1;
+                if (!bar_wait(&c.tfull[last & 1u][half ^ 1], (last >> 1) & 1u, abort_flag)) c.abort_flag = 1;
                 float *part = reinterpret_cast<float *>(smem) + row * kPartRow;
                 if (valid) {
 #pragma unroll
@@ -616,7 +411,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         if (first < total && warp >= 4) {
             // row by row, the clusters' CTAs in turn, a warp to a row: lane l adds
             // columns 4l.. and 128 + 4l.. over the CTAs in the order of the blocks
-            const Tile tile = tile_at(c, E, first);
+            const Tile tile = tile_at(c.g, E, first, BM);
             // (a CTA that gave up may still have had loads landing on its sums)
             bool failed = false;
             for (int q = 0; q < S; ++q) failed |= ld_cluster_u32(peer_addr(&c.abort_flag, q)) != 0u;
@@ -688,28 +483,13 @@ gather_kernel(const uint8_t *__restrict__ x_q, const float *__restrict__ x_s, lo
 // ------------------------------------------------------------------- host
 size_t gathered_codes_bytes(int rows, int K) { return align_up((size_t)rows * K, 256); }
 
-// [n, rows, cols] codes with rows `ld` bytes apart, box {128 columns, box_rows},
-// 128-byte swizzle.
-bool code_map(CUtensorMap *m, const void *base, int n, int rows, int cols, long long ld, uint32_t box_rows)
-{
-    auto enc = tc::encode_fn();
-    if (!enc) return false;
-    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)n};
-    const cuuint64_t strides[2] = {(cuuint64_t)ld, (cuuint64_t)ld * (cuuint64_t)rows};
-    const cuuint32_t box[3] = {(cuuint32_t)BK, box_rows, 1};
-    const cuuint32_t one[3] = {1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, n ? 3 : 2, const_cast<void *>(base), dims, strides, box, one,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-template <int MODE, bool GATHER, bool SPLIT>
+template <int MODE, bool SPLIT>
 cudaError_t launch_variant(const CUtensorMap &x, const CUtensorMap &w0, const CUtensorMap &w1, const Params &p,
                            long long tiles, int num_sms, cudaStream_t stream)
 {
     static PerDeviceFlag done;
     const int dev = current_device();
-    auto *kern = product_kernel<MODE, GATHER, SPLIT>;
+    auto *kern = product_kernel<MODE, SPLIT>;
     if (!done.done(dev)) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
         if (e != cudaSuccess) return e;
@@ -726,23 +506,14 @@ template <int MODE>
 cudaError_t launch_product(const void *x_q, long long ldx, const void *w0, const void *w1, Params p, void *workspace,
                            cudaStream_t stream)
 {
-    p.n_tiles = ceil_div(p.N, MODE == GATEUP ? BN / 2 : BN);
     const int num_sms = device_sm_count();
-    // most tiles there can be: every expert with rows may own a ragged row tile
-    const long long groups = (long long)p.rows / BM + (p.E < p.rows ? p.E : p.rows);
-    const long long tiles = groups * p.n_tiles;
-    if (tiles > 0x3fffffffLL) return cudaErrorInvalidValue;
-    // fewer tiles than half the SMs: split the reduction while there are SMs
-    // and blocks for it
-    p.split = 1;
-    while (p.split < 8 && tiles * p.split * 2 <= num_sms && p.split * 2 <= p.KB) p.split *= 2;
-    if (p.perm_tok && p.split == 1) {
+    if (decode_fits(p)) return launch_decode<MODE>(x_q, ldx, w0, w1, p, num_sms, stream);
+    if (p.perm_tok) {
         // Rows go into group order once, ahead of the product: every column
         // tile would gather them again, and a loop that copies rows feeds the
         // tensor cores more slowly than TMA does (4096 rows x 2048 against 2 x
         // 2816 columns of 16 experts: 100 us gathering in the kernel, 62 us on
-        // rows in order, plus 4 us for this copy).  A split product reads each
-        // row about once and saves itself the launch.
+        // rows in order, plus 4 us for this copy).
         uint8_t *g_q = static_cast<uint8_t *>(workspace);
         float *g_s = reinterpret_cast<float *>(g_q + gathered_codes_bytes(p.rows, p.K));
         const cudaError_t e = launch_pdl(gather_kernel, dim3((unsigned)ceil_div(p.rows, kGatherWarps)),
@@ -755,18 +526,27 @@ cudaError_t launch_product(const void *x_q, long long ldx, const void *w0, const
         p.x_rows = p.rows;
         p.perm_tok = nullptr;
     }
-    p.x_q = static_cast<const uint8_t *>(x_q);
-    p.ldx = ldx;
+    p.n_tiles = ceil_div(p.N, MODE == GATEUP ? BN / 2 : BN);
+    // most tiles there can be: every expert with rows may own a ragged row tile
+    const long long groups = (long long)p.rows / BM + (p.E < p.rows ? p.E : p.rows);
+    const long long tiles = groups * p.n_tiles;
+    if (tiles > 0x3fffffffLL) return cudaErrorInvalidValue;
+    // tiles for fewer than half the SMs: the reduction is split over as many
+    // CTAs as there are SMs and blocks for (at most 8, the portable cluster)
+    p.split = 1;
+    if (2 * tiles <= num_sms) {
+        const long long each = num_sms / tiles;
+        p.split = (int)(each < 8 ? each : 8);
+        if (p.split > p.KB) p.split = p.KB;
+    }
     CUtensorMap mx, mw0, mw1;
     const uint32_t wbox = MODE == GATEUP ? BN / 4 : BN;
-    if (!code_map(&mw0, w0, p.E, p.N, p.K, p.K, wbox)) return cudaErrorInvalidValue;
+    if (!code_map(&mx, x_q, 0, p.x_rows, p.K, ldx, ABOX) || !code_map(&mw0, w0, p.E, p.N, p.K, p.K, wbox))
+        return cudaErrorInvalidValue;
     if (MODE != GATEUP) mw1 = mw0;
     else if (!code_map(&mw1, w1, p.E, p.N, p.K, p.K, wbox)) return cudaErrorInvalidValue;
-    if (p.perm_tok) mx = mw0;   // (unused: gathered rows are copied 16 bytes at a time)
-    else if (!code_map(&mx, x_q, 0, p.x_rows, p.K, ldx, ABOX)) return cudaErrorInvalidValue;
-    if (p.split == 1) return launch_variant<MODE, false, false>(mx, mw0, mw1, p, tiles, num_sms, stream);
-    return p.perm_tok ? launch_variant<MODE, true, true>(mx, mw0, mw1, p, tiles, num_sms, stream)
-                      : launch_variant<MODE, false, true>(mx, mw0, mw1, p, tiles, num_sms, stream);
+    return p.split > 1 ? launch_variant<MODE, true>(mx, mw0, mw1, p, tiles, num_sms, stream)
+                       : launch_variant<MODE, false>(mx, mw0, mw1, p, tiles, num_sms, stream);
 }
 
 bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
