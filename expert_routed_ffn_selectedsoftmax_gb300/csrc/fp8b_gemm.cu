@@ -38,17 +38,18 @@ namespace fp8b {
 
 constexpr int BM = 128, BN = 256, BK = kBlock;   // one MMA k-block = one scale block
 constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE = A_BYTES + B_BYTES;
-constexpr int STAGES = 4;
+constexpr int STAGES = 3;
 constexpr int ABOX = 32;                         // rows per A load
 constexpr int TMEM_COLS = 512;                   // two partial sums of 256 columns
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 128 + 32 * kEpiWarps;   // warps 0-3: load, multiply, multiply, gather
+constexpr int kThreads = 128 + 32 * kEpiWarps;   // warps 0-3: load, multiply, multiply, TMEM
 // registers a thread after the split at start (setmaxnreg): the block launches
-// with 168 x 12 warps = 2016; 4 warps keep 88 and 8 take 208: 352 + 1664 = 2016
-constexpr int kRegsLaunch = 168, kRegsAux = 88, kRegsEpi = 208;
-static_assert(4 * kRegsAux + kEpiWarps * kRegsEpi <= 12 * kRegsLaunch, "more registers than the block has");
+// with 168 x 12 warps = 2016; 4 warps keep 56 and 8 take 224: 224 + 1792 = 2016
+constexpr int kRegsLaunch = 168, kRegsAux = 56, kRegsEpi = 224;
+static_assert(4 * kRegsAux + kEpiWarps * kRegsEpi <= (kThreads / 32) * kRegsLaunch, "more registers than the block has");
 constexpr int kPartRow = BN + 4;                 // floats per row of a split partial sum (16-byte
                                                  // stores of 8 rows fall in distinct banks)
+constexpr int kStaging = 32 * 256;               // bytes per epilogue warp: 256 of each of its rows
 
 struct alignas(16) Ctl {
     uint64_t full[STAGES], empty[STAGES], tfull[2][2], tempty[2][2], drain[2];   // [buffer][column half]
@@ -57,21 +58,40 @@ struct alignas(16) Ctl {
     Groups g;
     uint32_t amax[2][BM];     // GATEUP: each row's largest |h| per column half
 };
-constexpr int kStaging = 32 * 64;                // bytes per epilogue warp: 64 of each of its rows
-constexpr size_t kSmem = 1024 + (size_t)STAGES * STAGE + sizeof(Ctl) + kEpiWarps * kStaging;
+constexpr size_t kRing = (size_t)STAGES * STAGE;          // then the staging (from a multiple of 1024
+constexpr size_t kCtl = kRing + kEpiWarps * kStaging;     // bytes: the stores' swizzle), then Ctl
+constexpr size_t kSmem = 1024 + kCtl + sizeof(Ctl);
 static_assert(kSmem <= 232448, "shared memory per CTA");
-static_assert((size_t)BM * kPartRow * 4 <= (size_t)STAGES * STAGE, "split partial sums reuse the ring");
+static_assert((size_t)BM * kPartRow * 4 <= kRing, "split partial sums reuse the ring");
 
-// Wait for the warp's TMEM loads; the registers pass through it, so that
-// nothing that reads them moves above it.
-__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&v)[16])
+#define MOE_OUTS16(v, i)                                                                                        \
+    "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), "=r"(v[i + 6]), \
+        "=r"(v[i + 7]), "=r"(v[i + 8]), "=r"(v[i + 9]), "=r"(v[i + 10]), "=r"(v[i + 11]), "=r"(v[i + 12]),      \
+        "=r"(v[i + 13]), "=r"(v[i + 14]), "=r"(v[i + 15])
+// 64 consecutive columns of the warp's 32 TMEM lanes, and the wait for them (one
+// statement: nothing that reads the registers can move above the wait)
+__device__ __forceinline__ void tmem_ld64_wait(uint32_t taddr, uint32_t (&v)[64])
 {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
-                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
-                 :
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,"
+        "%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : MOE_OUTS16(v, 0), MOE_OUTS16(v, 16), MOE_OUTS16(v, 32), MOE_OUTS16(v, 48)
+        : "r"(taddr)
+        : "memory");
+}
+// A tile from shared to global memory; at most the tensor's bounds are written.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int x, int y)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(src))
                  : "memory");
 }
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// this thread's stores: their shared memory has been read / they are complete
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr)
 {
     float4 v;
@@ -107,8 +127,8 @@ __device__ __forceinline__ void store4(const Params &p, long long r, int n0, flo
 // took longer than the products of a tile (8192 x 2048 x 5632: 178 us against
 // 100 us without the stores).  16-byte piece q of row r lies at q ^ (r / 2 % 4),
 // so neither side has bank conflicts.  `g`: row 0's bytes; `rows` of the 32 and
-// the first `bytes` of the 64 exist; `vec`: 16-byte stores are aligned, else
-// elements of `size` bytes are stored one by one.
+// the first `bytes` exist; `vec`: 16-byte stores are aligned, else elements of
+// `size` bytes are stored one by one.
 __device__ __forceinline__ void store_rows(uint8_t *stg, int lane, const uint4 (&d)[4], uint8_t *g, long long pitch,
                                            int rows, int bytes, bool vec, int size)
 {
@@ -120,20 +140,21 @@ __device__ __forceinline__ void store_rows(uint8_t *stg, int lane, const uint4 (
     for (int i = 0; i < 4; ++i) {
         const int r = i * 8 + (lane >> 2);
         const uint4 v = *reinterpret_cast<const uint4 *>(stg + r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
-        if (r >= rows || q * 16 >= bytes) continue;
-        uint8_t *o = g + r * pitch + q * 16;
-        if (vec && q * 16 + 16 <= bytes) {
+        const int at = q * 16;
+        if (r >= rows || at >= bytes) continue;
+        uint8_t *o = g + r * pitch + at;
+        if (vec && at + 16 <= bytes) {
             *reinterpret_cast<uint4 *>(o) = v;
         } else {
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                if (q * 16 + k * 4 >= bytes) break;
+                if (at + k * 4 >= bytes) break;
                 if (size == 4) {
                     *reinterpret_cast<uint32_t *>(o + k * 4) = w[k];
                 } else {
                     *reinterpret_cast<uint16_t *>(o + k * 4) = (uint16_t)w[k];
-                    if (q * 16 + k * 4 + 2 < bytes) *reinterpret_cast<uint16_t *>(o + k * 4 + 2) = (uint16_t)(w[k] >> 16);
+                    if (at + k * 4 + 2 < bytes) *reinterpret_cast<uint16_t *>(o + k * 4 + 2) = (uint16_t)(w[k] >> 16);
                 }
             }
         }
@@ -144,11 +165,11 @@ __device__ __forceinline__ void store_rows(uint8_t *stg, int lane, const uint4 (
 template <int MODE, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w0,
-               const __grid_constant__ CUtensorMap tm_w1, const Params p)
+               const __grid_constant__ CUtensorMap tm_w1, const __grid_constant__ CUtensorMap tm_out, const Params p)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    Ctl &c = *reinterpret_cast<Ctl *>(smem + STAGES * STAGE);
+    Ctl &c = *reinterpret_cast<Ctl *>(smem + kCtl);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int E = p.E;
 
@@ -180,7 +201,8 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     const int first = SPLIT ? blockIdx.x / S : blockIdx.x;
     const int stride = SPLIT ? gridDim.x / S : gridDim.x;
     // this CTA's blocks of the reduction
-    const int kb0 = (int)((long long)p.KB * rank / S), kb1 = (int)((long long)p.KB * (rank + 1) / S);
+    const int kb0 = SPLIT ? (int)((long long)p.KB * rank / S) : 0;
+    const int kb1 = SPLIT ? (int)((long long)p.KB * (rank + 1) / S) : p.KB;
     volatile int *abort_flag = &c.abort_flag;
     if (warp < 4) {
         // (inside the branch: the compiler gives each side its own limit)
@@ -191,7 +213,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             bool ok = true;
             for (int t = first; t < total && ok; t += stride) {
                 const Tile tile = tile_at(c.g, E, t, BM);
-                const int boxes = (tile.cnt + ABOX - 1) / ABOX;
+                const int boxes = (tile.cnt + ABOX - 1) / ABOX;   // only as many as the tile has rows
                 for (int kb = kb0; kb < kb1; ++kb, ++it) {
                     const int s = it % STAGES;
                     ok = __all_sync(0xffffffffu, bar_wait(&c.empty[s], ((it / STAGES) & 1u) ^ 1u, abort_flag));
@@ -200,7 +222,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                     if (lane == 0) {
                         mbar_expect_tx(&c.full[s], (uint32_t)(boxes * ABOX * BK) + B_BYTES);
                         if (MODE == GATEUP) {
-                            // per column half: 64 rows of W_gate, 64 of W_up
+                            // per column half: 64 rows of W_gate, the same 64 of W_up
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 uint8_t *at = sb + h * (B_BYTES / 2);
@@ -229,11 +251,12 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         } else if (warp == 1 || warp == 2) {
             // -------------------------------------------- multiply
             // Warp 1 multiplies the first column half, warp 2 the second, into
-            // TMEM buffers of their own: between the MMAs of two blocks an
-            // issuer spends about as long on its waits and commits as the MMAs
-            // take, which the other warp's MMAs fill.  The whole warp runs the
-            // loop and one elected lane issues, so that the descriptors stay in
-            // uniform registers (a loop of lane 0 alone: 80 clocks to issue an MMA).
+            // TMEM buffers of their own: a buffer's turn -- MMAs, their commit,
+            // the epilogue's reads, its arrival -- takes several times as long as
+            // the MMAs, and four buffers in turn hide more of it than two.  The
+            // whole warp runs the loop and one elected lane issues, so that the
+            // descriptors stay in uniform registers (a loop of lane 0 alone: 80
+            // clocks to issue an MMA).
             constexpr uint32_t idesc = idesc_e4m3(BM, BN / 2);
             const bool leader = elect_one();
             const int h = warp - 1;
@@ -273,23 +296,34 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
         const int quarter = warp & 3, half = (warp - 4) >> 2;
         const int row = quarter * 32 + lane;
-        uint8_t *stg = reinterpret_cast<uint8_t *>(&c + 1) + (warp - 4) * kStaging;
+        uint8_t *stg = smem + kRing + (warp - 4) * kStaging;
         uint32_t it = 0;
         bool ok = true;   // once false, no more waits: the remaining rows become NaN
-        for (int t = first; t < total; t += stride) {
-            const Tile tile = tile_at(c.g, E, t, BM);
-            const bool valid = row < tile.cnt;
-            const long long r = tile.row0 + row;
-            const float *xs = valid ? p.x_s + r * p.KB : nullptr;
+        Tile next;
+        const float *xs = nullptr;
+        uint32_t ws = 0;   // place of the weight scales (one for each 16 KB of codes: 32 bits do)
+        float nx = 0.f, n0 = 0.f, n1 = 0.f;   // the next block's scales
+        // tile t's place and its first scales, asked for ahead of the tile before's output
+        auto enter = [&](int t) {
+            if (t >= total) return;
+            next = tile_at(c.g, E, t, BM);
+            xs = row < next.cnt ? p.x_s + (long long)(next.row0 + row) * p.KB : nullptr;
             // the weight scales of the columns this warp sums: gate and up, or
             // one 128-column block (none past the last: its sums are zero)
-            const int nb = MODE == GATEUP ? tile.nt : min(tile.nt * 2 + half, p.NB - 1);
-            const float *ws0 = p.w_s[0] + ((size_t)tile.e * p.NB + nb) * p.KB;
-            const float *ws1 = MODE == GATEUP ? p.w_s[1] + ((size_t)tile.e * p.NB + nb) * p.KB : ws0;
+            const int nb = MODE == GATEUP ? next.nt : min(next.nt * 2 + half, p.NB - 1);
+            ws = (uint32_t)((next.e * p.NB + nb) * p.KB + kb0);
+            nx = xs ? __ldg(xs + kb0) : 0.f;
+            n0 = __ldg(p.w_s[0] + ws);
+            if (MODE == GATEUP) n1 = __ldg(p.w_s[1] + ws);
+        };
+        enter(first);
+        for (int t = first; t < total; t += stride) {
+            const Tile tile = next;
+            const bool valid = row < tile.cnt;
+            const long long r = tile.row0 + row;
             uint64_t acc[64];   // 128 sums: PRODUCT columns half*128 ..; GATEUP 64 of gate, 64 of up
 #pragma unroll
             for (int i = 0; i < 64; ++i) acc[i] = 0ull;
-            float nx = xs ? __ldg(xs + kb0) : 0.f, n0 = __ldg(ws0 + kb0), n1 = MODE == GATEUP ? __ldg(ws1 + kb0) : 0.f;
 #pragma unroll 1
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const uint32_t b = it & 1u;
@@ -298,30 +332,30 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                 const uint64_t m1 = pack2(__float_as_uint(f1), __float_as_uint(f1));
                 if (kb + 1 < kb1) {
                     nx = xs ? __ldg(xs + kb + 1) : 0.f;
-                    n0 = __ldg(ws0 + kb + 1);
-                    if (MODE == GATEUP) n1 = __ldg(ws1 + kb + 1);
+                    n0 = __ldg(p.w_s[0] + ++ws);
+                    if (MODE == GATEUP) n1 = __ldg(p.w_s[1] + ws);
                 }
                 ok = ok && __all_sync(0xffffffffu, bar_wait(&c.tfull[b][half], (it >> 1) & 1u, abort_flag));
                 tc_fence_after();
                 const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + b * BN + half * (BN / 2);
-                // eight chunks of 16 columns, one load ahead of the sums
-                uint32_t v[2][16];
-                tmem_ld16(base, v[0]);
+                // Two loads of 64 columns: the buffer's reads are in the chain that
+                // decides how soon it can be filled again (eight loads of 16, one
+                // ahead of the sums, took 540 clocks of a block's 900).
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    tmem_ld_wait16(v[j & 1]);
-                    if (j < 7) {
-                        tmem_ld16(base + (j + 1) * 16, v[(j + 1) & 1]);
-                    } else {
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t v[64];
+                    tmem_ld64_wait(base + j * 64, v);
+                    if (j == 1) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&c.tempty[b][half]);
                     }
-                    const uint64_t m = j < 4 ? m0 : m1;
+                    const uint64_t m = j ? m1 : m0;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) fma2(acc[j * 8 + i], pack2(v[j & 1][2 * i], v[j & 1][2 * i + 1]), m);
+                    for (int i = 0; i < 32; ++i) fma2(acc[j * 32 + i], pack2(v[2 * i], v[2 * i + 1]), m);
                 }
             }
+            enter(t + stride);
             if (!ok) {
                 c.abort_flag = 1;
                 const uint64_t nan2 = 0x7fffffff7fffffffull;
@@ -334,12 +368,12 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                 // the partial sums, in tile column order
                 const uint32_t last = it - 1;
                 if (!bar_wait(&c.tfull[last & 1u][half ^ 1], (last >> 1) & 1u, abort_flag)) c.abort_flag = 1;
-                float *part = reinterpret_cast<float *>(smem) + row * kPartRow;
+                float *sums = reinterpret_cast<float *>(smem) + row * kPartRow;
                 if (valid) {
 #pragma unroll
                     for (int i = 0; i < 128; i += 4) {
                         const int cc = MODE == GATEUP ? (i >> 6) * (BN / 2) + half * 64 + (i & 63) : half * (BN / 2) + i;
-                        *reinterpret_cast<float4 *>(part + cc) = make_float4(val(i), val(i + 1), val(i + 2), val(i + 3));
+                        *reinterpret_cast<float4 *>(sums + cc) = make_float4(val(i), val(i + 1), val(i + 2), val(i + 3));
                     }
                 }
                 break;   // one tile per cluster
@@ -351,7 +385,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                     h[i] = swiglu(val(i), val(64 + i));
                     m = max(m, mag_bits(h[i]));
                 }
-                // the other half of the row's 128 columns is in the warp of the
+                // the other half of the row's 128 channels is in the warp of the
                 // same quarter: the two meet at a barrier of their own (both
                 // take every turn of the tile loop, whatever happened before)
                 c.amax[half][row] = m;
@@ -359,7 +393,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                 m = max(m, c.amax[half ^ 1][row]);
                 asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
                 const float s = block_scale(m), f = code_factor(s);
-                const int n0 = tile.nt * (BN / 2) + half * 64;
+                const int c0 = tile.nt * (BN / 2) + half * 64;
                 uint4 d[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -367,43 +401,73 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                     d[i] = make_uint4(encode4(v[0], v[1], v[2], v[3], f), encode4(v[4], v[5], v[6], v[7], f),
                                       encode4(v[8], v[9], v[10], v[11], f), encode4(v[12], v[13], v[14], v[15], f));
                 }
-                store_rows(stg, lane, d, p.h_q + (r - lane) * p.N + n0, p.N, tile.cnt - quarter * 32, p.N - n0, true, 1);
-                if (valid) {
-                    if (half == 0) p.h_s[r * p.NB + tile.nt] = s;
-                }
+                store_rows(stg, lane, d, p.h_q + (r - lane) * p.N + c0, p.N, tile.cnt - quarter * 32, p.N - c0, true, 1);
+                if (valid && half == 0) p.h_s[r * p.NB + tile.nt] = s;
             } else {
-                const int n0 = tile.nt * BN + half * (BN / 2), rows = tile.cnt - quarter * 32;
+                const int c0 = tile.nt * BN + half * (BN / 2), rows = tile.cnt - quarter * 32;
                 const bool f32 = p.out_f32;
                 const int size = f32 ? 4 : 2;
-                uint8_t *g = static_cast<uint8_t *>(p.out) + ((r - lane) * p.ldo + n0) * size;
-                const int bytes = min(p.N - n0, BN / 2) * size;
-                if (f32) {
+                // Slices with all of their 32 rows go out by TMA: the warp goes on
+                // to the next tile while they drain.  (All CTAs end their tiles
+                // together, and waiting for the burst of their stores to be taken
+                // cost 2 us a tile.)
+                const bool tma = p.out_tma && rows >= 32;
+                if (lane == 0) bulk_wait_read();   // the staging of the tile before has been read
+                __syncwarp();
+                // the k-th 128 bytes of each row: 64 columns of bf16, 32 of fp32
+                auto piece = [&](int k, uint4 (&d)[8]) {
+                    if (f32) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        uint4 d[4];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const int i = j * 16 + q * 4;
+                        for (int q = 0; q < 8; ++q) {
+                            const int i = k * 32 + q * 4;
                             d[q] = make_uint4(__float_as_uint(val(i)), __float_as_uint(val(i + 1)),
                                               __float_as_uint(val(i + 2)), __float_as_uint(val(i + 3)));
                         }
-                        store_rows(stg, lane, d, g + j * 64, p.ldo * 4, rows, bytes - j * 64, p.out_vec, 4);
-                    }
-                } else {
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint4 d[4];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const int i = j * 32 + q * 8;
+                        for (int q = 0; q < 8; ++q) {
+                            const int i = (k & 1) * 64 + q * 8;
                             d[q] = make_uint4(bf16x2(val(i), val(i + 1)), bf16x2(val(i + 2), val(i + 3)),
                                               bf16x2(val(i + 4), val(i + 5)), bf16x2(val(i + 6), val(i + 7)));
                         }
-                        store_rows(stg, lane, d, g + j * 64, p.ldo * 2, rows, bytes - j * 64, p.out_vec, 2);
+                    }
+                };
+                const int cols = 128 / size;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (!f32 && k >= 2) break;
+                    const int n = c0 + k * cols;
+                    uint8_t *at = stg + (k & 1) * 4096;
+                    uint4 d[8];
+                    piece(k, d);
+                    if (tma) {
+                        if (k == 2) {   // the first pieces' staging again
+                            if (lane == 0) bulk_wait_read();
+                            __syncwarp();
+                        }
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            *reinterpret_cast<uint4 *>(at + lane * 128 + ((q ^ (lane & 7)) << 4)) = d[q];
+                        if (k & 1) {
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                if (n - cols < p.N) tma_store_2d(&tm_out, stg, n - cols, (int)r);
+                                if (n < p.N) tma_store_2d(&tm_out, at, n, (int)r);
+                                bulk_commit();
+                            }
+                        }
+                    } else {
+                        uint8_t *g = static_cast<uint8_t *>(p.out) + ((r - lane) * p.ldo + n) * size;
+                        const int bytes = (p.N - n) * size;
+                        const uint4 lo[4] = {d[0], d[1], d[2], d[3]}, hi[4] = {d[4], d[5], d[6], d[7]};
+                        store_rows(at, lane, lo, g, p.ldo * size, rows, bytes, p.out_vec, size);
+                        store_rows(at, lane, hi, g + 64, p.ldo * size, rows, bytes - 64, p.out_vec, size);
                     }
                 }
             }
         }
+        if (MODE == PRODUCT && lane == 0) bulk_wait_all();
     }
 
     if constexpr (SPLIT) {
@@ -441,10 +505,10 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                 }
             }
         }
-        cluster_sync_all();   // no CTA leaves while a peer reads its shared memory
-    } else {
-        __syncthreads();
     }
+    // no CTA leaves while another reads its shared memory
+    if (SPLIT) cluster_sync_all();
+    else __syncthreads();
     if (warp == 3) {
         __syncwarp();
         tc_fence_after();
@@ -483,9 +547,24 @@ gather_kernel(const uint8_t *__restrict__ x_q, const float *__restrict__ x_s, lo
 // ------------------------------------------------------------------- host
 size_t gathered_codes_bytes(int rows, int K) { return align_up((size_t)rows * K, 256); }
 
+// out [rows, N], rows ldo apart, box {128 bytes of columns, 32 rows}, 128-byte swizzle
+bool out_map(CUtensorMap *m, const Params &p)
+{
+    auto enc = tc::encode_fn();
+    if (!enc) return false;
+    const int size = p.out_f32 ? 4 : 2;
+    const cuuint64_t dims[2] = {(cuuint64_t)p.N, (cuuint64_t)p.rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)p.ldo * size};
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / size), 32};
+    const cuuint32_t one[2] = {1, 1};
+    return enc(m, p.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.out, dims, strides,
+               box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int MODE, bool SPLIT>
-cudaError_t launch_variant(const CUtensorMap &x, const CUtensorMap &w0, const CUtensorMap &w1, const Params &p,
-                           long long tiles, int num_sms, cudaStream_t stream)
+cudaError_t launch_variant(const CUtensorMap &x, const CUtensorMap &w0, const CUtensorMap &w1,
+                           const CUtensorMap &out, const Params &p, long long tiles, int num_sms, cudaStream_t stream)
 {
     static PerDeviceFlag done;
     const int dev = current_device();
@@ -497,9 +576,9 @@ cudaError_t launch_variant(const CUtensorMap &x, const CUtensorMap &w0, const CU
     }
     if (SPLIT)
         return launch_pdl_cluster(kern, dim3((unsigned)(tiles * p.split)), dim3(kThreads), kSmem, stream, p.split, x,
-                                  w0, w1, p);
+                                  w0, w1, out, p);
     return launch_pdl(kern, dim3((unsigned)(tiles < num_sms ? tiles : num_sms)), dim3(kThreads), kSmem, stream, x, w0,
-                      w1, p);
+                      w1, out, p);
 }
 
 template <int MODE>
@@ -528,8 +607,7 @@ cudaError_t launch_product(const void *x_q, long long ldx, const void *w0, const
     }
     p.n_tiles = ceil_div(p.N, MODE == GATEUP ? BN / 2 : BN);
     // most tiles there can be: every expert with rows may own a ragged row tile
-    const long long groups = (long long)p.rows / BM + (p.E < p.rows ? p.E : p.rows);
-    const long long tiles = groups * p.n_tiles;
+    const long long tiles = ((long long)p.rows / BM + (p.E < p.rows ? p.E : p.rows)) * p.n_tiles;
     if (tiles > 0x3fffffffLL) return cudaErrorInvalidValue;
     // tiles for fewer than half the SMs: the reduction is split over as many
     // CTAs as there are SMs and blocks for (at most 8, the portable cluster)
@@ -539,14 +617,19 @@ cudaError_t launch_product(const void *x_q, long long ldx, const void *w0, const
         p.split = (int)(each < 8 ? each : 8);
         if (p.split > p.KB) p.split = p.KB;
     }
-    CUtensorMap mx, mw0, mw1;
-    const uint32_t wbox = MODE == GATEUP ? BN / 4 : BN;
+    CUtensorMap mx, mw0, mw1, mout;
+    constexpr uint32_t wbox = MODE == GATEUP ? BN / 4 : BN;
     if (!code_map(&mx, x_q, 0, p.x_rows, p.K, ldx, ABOX) || !code_map(&mw0, w0, p.E, p.N, p.K, p.K, wbox))
         return cudaErrorInvalidValue;
     if (MODE != GATEUP) mw1 = mw0;
     else if (!code_map(&mw1, w1, p.E, p.N, p.K, p.K, wbox)) return cudaErrorInvalidValue;
-    return p.split > 1 ? launch_variant<MODE, true>(mx, mw0, mw1, p, tiles, num_sms, stream)
-                       : launch_variant<MODE, false>(mx, mw0, mw1, p, tiles, num_sms, stream);
+    // the output as a tensor, where its rows suit TMA (a split product stores a
+    // row at a time)
+    p.out_tma = MODE == PRODUCT && p.split == 1 && p.out_vec;
+    if (!p.out_tma) mout = mx;
+    else if (!out_map(&mout, p)) return cudaErrorInvalidValue;
+    return p.split > 1 ? launch_variant<MODE, true>(mx, mw0, mw1, mout, p, tiles, num_sms, stream)
+                       : launch_variant<MODE, false>(mx, mw0, mw1, mout, p, tiles, num_sms, stream);
 }
 
 bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

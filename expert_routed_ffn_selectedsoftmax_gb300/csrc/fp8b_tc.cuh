@@ -28,6 +28,7 @@ struct Params {
     void *out;                // PRODUCT: [rows, ldo] bf16 or fp32
     long long ldo;
     int out_f32, out_vec;     // out_vec: rows are multiples of 16 bytes apart, from a 16-byte boundary
+    int out_tma;              // whole 32-row slices go out by TMA
     uint8_t *h_q;             // GATEUP: [rows, N] codes, [rows, NB] scales
     float *h_s;
     uint32_t *status;
