@@ -292,16 +292,22 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
                 }
                 break;   // one tile per cluster
             } else if constexpr (MODE == GATEUP) {
+                // (eight tokens at a time, with or without rows: a branch for each
+                // would put their exponentials one after the other)
                 uint32_t mine = 0u;   // lane l: largest |h| of token l over the warp's channels
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    if (i >= tile.cnt) break;
-                    const float h = swiglu(val(0, i), val(NW - 1, i));
-                    const uint32_t m = __reduce_max_sync(0xffffffffu, mag_bits(h));
-                    if (lane == i) mine = m;
-                    // (h takes the place of its gate sum)
-                    acc[0][i >> 1] = (i & 1) ? pack2((uint32_t)acc[0][i >> 1], __float_as_uint(h))
-                                             : pack2(__float_as_uint(h), (uint32_t)(acc[0][i >> 1] >> 32));
+                for (int i0 = 0; i0 < NT; i0 += 8) {
+                    if (i0 >= tile.cnt) break;
+                    float h[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        h[i] = swiglu(val(0, i0 + i), val(NW - 1, i0 + i));
+                        const uint32_t m = __reduce_max_sync(0xffffffffu, mag_bits(h[i]));
+                        if (lane == i0 + i) mine = m;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)   // (h takes the place of its gate sum)
+                        acc[0][i0 / 2 + i] = pack2(__float_as_uint(h[2 * i]), __float_as_uint(h[2 * i + 1]));
                 }
                 c.amax[ew][lane] = mine;
                 epilogue_barrier();   // (all four warps take every turn of the tile loop, whatever happened before)
@@ -310,17 +316,23 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
                 epilogue_barrier();
                 const float s = block_scale(mine), f = code_factor(s);
                 if (ew == 0 && lane < tile.cnt) p.h_s[(size_t)(tile.row0 + lane) * p.NB + tile.nt] = s;
+                uint8_t *o = p.h_q + (size_t)tile.row0 * p.N + n;
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    if (i >= tile.cnt) break;
-                    const float q = val(0, i) * __shfl_sync(0xffffffffu, f, i);
-                    if (n < p.N) p.h_q[(size_t)(tile.row0 + i) * p.N + n] = (uint8_t)e4m3x2(q, 0.f);
+                for (int i0 = 0; i0 < NT; i0 += 8) {
+                    if (i0 >= tile.cnt) break;
+#pragma unroll
+                    for (int i = i0; i < i0 + 8; ++i) {
+                        const float q = val(0, i) * __shfl_sync(0xffffffffu, f, i);
+                        if (i < tile.cnt && n < p.N) o[(size_t)i * p.N] = (uint8_t)e4m3x2(q, 0.f);
+                    }
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    if (i >= tile.cnt) break;
-                    if (n < p.N) store_out(p, tile.row0 + i, n, val(0, i));
+                for (int i0 = 0; i0 < NT; i0 += 8) {
+                    if (i0 >= tile.cnt) break;
+#pragma unroll
+                    for (int i = i0; i < i0 + 8; ++i)
+                        if (i < tile.cnt && n < p.N) store_out(p, tile.row0 + i, n, val(0, i));
                 }
             }
         }
