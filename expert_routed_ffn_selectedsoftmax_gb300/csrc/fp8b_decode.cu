@@ -124,11 +124,12 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
     if (!p.offsets) pdl_enter();
 
     const uint32_t tmem = c.tmem_base;
-    const int total = c.g.total;
     const int S = SPLIT ? p.split : 1;
     const int rank = SPLIT ? (int)cluster_rank() : 0;
     const int first = SPLIT ? blockIdx.x / S : blockIdx.x;
     const int stride = SPLIT ? gridDim.x / S : gridDim.x;
+    // (a cluster takes one tile, whatever total the offsets add up to)
+    const int total = SPLIT ? min(c.g.total, first + 1) : c.g.total;
     // this CTA's blocks of the reduction
     const int kb0 = (int)((long long)p.KB * rank / S), kb1 = (int)((long long)p.KB * (rank + 1) / S);
     volatile int *abort_flag = &c.abort_flag;

@@ -195,11 +195,12 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     tc_fence_after();
 
     const uint32_t tmem = c.tmem_base;
-    const int total = c.g.total;
     const int S = SPLIT ? p.split : 1;
     const int rank = SPLIT ? (int)cluster_rank() : 0;
     const int first = SPLIT ? blockIdx.x / S : blockIdx.x;
     const int stride = SPLIT ? gridDim.x / S : gridDim.x;
+    // (a cluster takes one tile, whatever total the offsets add up to)
+    const int total = SPLIT ? min(c.g.total, first + 1) : c.g.total;
     // this CTA's blocks of the reduction
     const int kb0 = SPLIT ? (int)((long long)p.KB * rank / S) : 0;
     const int kb1 = SPLIT ? (int)((long long)p.KB * (rank + 1) / S) : p.KB;
