@@ -18,9 +18,12 @@
 // back as broadcasts.  Two CTAs share an SM (ring of 3 or 5 stages each), so one
 // tile's start and end overlap the other's loads.
 //
-// Few tiles: the reduction is split over a cluster (SPLIT) as in fp8b_gemm.cu;
-// token t is finished by CTA t % split of the cluster.
+// Few tiles: the reduction is split over a cluster of up to 8 CTAs (SPLIT), whose
+// partial sums meet in distributed shared memory; token t is finished by CTA
+// t % split of the cluster, which adds the CTAs' sums in the order of the blocks.
 #include "fp8b_tc.cuh"
+
+#include <type_traits>
 
 namespace moe {
 namespace fp8b {
@@ -349,31 +352,63 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
             // (a CTA that gave up may still have had loads landing on its sums)
             bool failed = false;
             for (int q = 0; q < S; ++q) failed |= ld_cluster_u32(peer_addr(&c.abort_flag, q)) != 0u;
-            for (int i = rank; i < tile.cnt; i += S) {
-                float v[2] = {0.f, 0.f};
-#pragma unroll 8
-                for (int q = 0; q < S; ++q) {
-                    const uint32_t at = peer_addr(smem, q) + (uint32_t)(i * NW * M + chan) * 4;
+            // (four tokens in flight where this CTA has more than one: one after the
+            // other, their reads of the other CTAs' memory took longer than the
+            // products)
+            auto finish = [&](auto tokens) {
+                constexpr int U = decltype(tokens)::value, kPeers = U == 1 ? 8 : 2;   // (eight reads in flight)
+                for (int i0 = rank, turn = 0; i0 < tile.cnt; i0 += U * S, turn ^= 1) {
+                    float v[U][NW];
 #pragma unroll
-                    for (int w = 0; w < NW; ++w) v[w] += ld_cluster_f32(at + w * M * 4);
-                }
-                if (failed) v[0] = v[1] = __uint_as_float(0x7fffffffu);
-                const long long r = tile.row0 + i;
-                if constexpr (MODE == GATEUP) {
-                    const float h = swiglu(v[0], v[1]);
-                    uint32_t m = __reduce_max_sync(0xffffffffu, mag_bits(h));
-                    if (lane == 0) c.amax[ew][0] = m;
-                    epilogue_barrier();
+                    for (int u = 0; u < U; ++u)
 #pragma unroll
-                    for (int w = 0; w < kEpiWarps; ++w) m = max(m, c.amax[w][0]);
-                    epilogue_barrier();
-                    const float s = block_scale(m);
-                    if (n < p.N) p.h_q[r * p.N + n] = (uint8_t)e4m3x2(h * code_factor(s), 0.f);
-                    if (threadIdx.x == 64) p.h_s[r * p.NB + tile.nt] = s;
-                } else if (n < p.N) {
-                    store_out(p, r, n, v[0]);
+                        for (int w = 0; w < NW; ++w) v[u][w] = 0.f;
+#pragma unroll kPeers
+                    for (int q = 0; q < S; ++q) {
+                        const uint32_t at = peer_addr(smem, q) + (uint32_t)chan * 4;
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            const int i = min(i0 + u * S, tile.cnt - 1);
+#pragma unroll
+                            for (int w = 0; w < NW; ++w) v[u][w] += ld_cluster_f32(at + (uint32_t)((i * NW + w) * M) * 4);
+                        }
+                    }
+                    if (failed) {
+#pragma unroll
+                        for (int u = 0; u < U; ++u)
+#pragma unroll
+                            for (int w = 0; w < NW; ++w) v[u][w] = __uint_as_float(0x7fffffffu);
+                    }
+                    if constexpr (MODE == GATEUP) {
+                        float h[U];
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            h[u] = swiglu(v[u][0], v[u][NW - 1]);
+                            const uint32_t m = __reduce_max_sync(0xffffffffu, mag_bits(h[u]));
+                            if (lane == 0) c.amax[ew][turn * U + u] = m;
+                        }
+                        epilogue_barrier();   // (the other turn's places are written next)
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            uint32_t m = 0u;
+#pragma unroll
+                            for (int w = 0; w < kEpiWarps; ++w) m = max(m, c.amax[w][turn * U + u]);
+                            const float s = block_scale(m);
+                            const long long r = tile.row0 + i0 + u * S;
+                            if (i0 + u * S < tile.cnt) {
+                                if (n < p.N) p.h_q[r * p.N + n] = (uint8_t)e4m3x2(h[u] * code_factor(s), 0.f);
+                                if (threadIdx.x == 64) p.h_s[r * p.NB + tile.nt] = s;
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < U; ++u)
+                            if (i0 + u * S < tile.cnt && n < p.N) store_out(p, tile.row0 + i0 + u * S, n, v[u][0]);
+                    }
                 }
-            }
+            };
+            if (tile.cnt <= S) finish(std::integral_constant<int, 1>());
+            else finish(std::integral_constant<int, 4>());
         }
         cluster_sync_all();   // no CTA leaves while a peer reads its shared memory
     } else {
@@ -408,13 +443,25 @@ cudaError_t launch_variant(const CUtensorMap &x, const CUtensorMap &w0, const CU
 
 }  // namespace
 
-// Few rows per expert: at most 24 on average over the experts that can have any
-// (a tile holds 32; an expert with more takes several tiles, which read its
-// weights again through L2).
-bool decode_fits(const Params &p)
+// Most tiles there can be: an expert with r rows has (r - 1) / NT + 1, so as
+// many experts as possible with rows, and the rest of the rows in whole tiles.
+static long long most_tiles(const Params &p)
 {
     const long long experts = p.E < p.rows ? p.E : p.rows;
-    return p.rows <= 24 * experts;
+    return ((p.rows - experts) / NT + experts) * ceil_div(p.N, M);
+}
+
+// Few rows per expert (at most 16 on average over the experts that can have
+// any), or so few tiles that each has an SM: beyond, the rows' tiles read the
+// weights again too often.  Against the other kernel, us a call (here / there):
+// 64 experts of 1024 x 2 x 512, rows per expert 2: 12.1 / 17.8, 16: 15.7 / 21.2,
+// 24: 21.2 / 21.3, 64: 27.5 / 22.8; one of 2048 x 5632 (44 column tiles), rows 16:
+// 6.1 / 10.3, 96: 7.8 / 10.3, 128: 9.6 / 10.4, 256: 15.9 / 10.5; 4096 x 4096 (32),
+// 16: 6.2 / 16.1, 128: 12.1 / 16.4, 192: 17.4 / 16.5.
+bool decode_fits(const Params &p, int num_sms)
+{
+    const long long experts = p.E < p.rows ? p.E : p.rows;
+    return p.rows <= 16 * experts || most_tiles(p) <= num_sms;
 }
 
 template <int MODE>
@@ -422,9 +469,7 @@ cudaError_t launch_decode(const void *x_q, long long ldx, const void *w0, const 
                           cudaStream_t stream)
 {
     p.n_tiles = ceil_div(p.N, M);
-    // most tiles there can be: every expert with rows may own a ragged row tile
-    const long long groups = (long long)p.rows / NT + (p.E < p.rows ? p.E : p.rows);
-    const long long tiles = groups * p.n_tiles;
+    const long long tiles = most_tiles(p);
     if (tiles > 0x3fffffffLL) return cudaErrorInvalidValue;
     // tiles for fewer than half the SMs: split the reduction over a CTA for each
     // SM, at most 8 a tile (one token, 2048 x 5632 in 44 tiles: 2 CTAs a tile

@@ -17,16 +17,12 @@
 // boxes of 32, only as many as the tile has), warps 1 and 2 multiply a column
 // half each, warps 4-11 hold the sums: warp w the TMEM lanes of quarter w % 4
 // and one half of the columns (128 of them, or 64 of gate and the same 64 of up).
-// Batches of few rows per expert take the kernel of fp8b_decode.cu instead.
+// Calls of few rows take the kernel of fp8b_decode.cu instead.
 //
 // Rows of a tile past the end of its group are left out of the loads and the
 // stores (their lanes of the MMA compute on whatever the buffer holds; rows
 // do not mix).  Columns past N and the last block's columns past K are zeros
 // by TMA's fill.
-//
-// Few tiles: the reduction is split over a cluster of up to 8 CTAs (SPLIT),
-// whose partial sums meet in distributed shared memory, one row per warp, added
-// in the order of the blocks.
 //
 // Every wait is bounded (2 s).  Where one gives up, the rows of the CTA's
 // remaining tiles are written as NaN, and the status word says so if the
@@ -47,8 +43,6 @@ constexpr int kThreads = 128 + 32 * kEpiWarps;   // warps 0-3: load, multiply, m
 // with 168 x 12 warps = 2016; 4 warps keep 56 and 8 take 224: 224 + 1792 = 2016
 constexpr int kRegsLaunch = 168, kRegsAux = 56, kRegsEpi = 224;
 static_assert(4 * kRegsAux + kEpiWarps * kRegsEpi <= (kThreads / 32) * kRegsLaunch, "more registers than the block has");
-constexpr int kPartRow = BN + 4;                 // floats per row of a split partial sum (16-byte
-                                                 // stores of 8 rows fall in distinct banks)
 constexpr int kStaging = 32 * 256;               // bytes per epilogue warp: 256 of each of its rows
 
 struct alignas(16) Ctl {
@@ -62,8 +56,6 @@ constexpr size_t kRing = (size_t)STAGES * STAGE;          // then the staging (f
 constexpr size_t kCtl = kRing + kEpiWarps * kStaging;     // bytes: the stores' swizzle), then Ctl
 constexpr size_t kSmem = 1024 + kCtl + sizeof(Ctl);
 static_assert(kSmem <= 232448, "shared memory per CTA");
-static_assert((size_t)BM * kPartRow * 4 <= kRing, "split partial sums reuse the ring");
-
 #define MOE_OUTS16(v, i)                                                                                        \
     "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), "=r"(v[i + 6]), \
         "=r"(v[i + 7]), "=r"(v[i + 8]), "=r"(v[i + 9]), "=r"(v[i + 10]), "=r"(v[i + 11]), "=r"(v[i + 12]),      \
@@ -92,35 +84,6 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 // this thread's stores: their shared memory has been read / they are complete
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr)
-{
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-    return v;
-}
-
-// Four output values: columns [n0, n0 + 4) of row r (split sums: a warp writes
-// 128 neighbouring columns of one row at a time).
-__device__ __forceinline__ void store4(const Params &p, long long r, int n0, float4 v)
-{
-    const float w[4] = {v.x, v.y, v.z, v.w};
-    if (p.out_f32) {
-        float *o = static_cast<float *>(p.out) + r * p.ldo + n0;
-        if (p.out_vec && n0 + 4 <= p.N) *reinterpret_cast<float4 *>(o) = v;
-        else
-            for (int i = 0; i < 4; ++i)
-                if (n0 + i < p.N) o[i] = w[i];
-    } else {
-        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + r * p.ldo + n0;
-        if (p.out_vec && n0 + 4 <= p.N) {
-            *reinterpret_cast<uint2 *>(o) = make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
-        } else
-            for (int i = 0; i < 4; ++i)
-                if (n0 + i < p.N) o[i] = __float2bfloat16_rn(w[i]);
-    }
-}
-
 // 64 bytes of each of the warp's 32 rows (lane l holds row l's) to global
 // memory: turned through shared memory so that a store instruction covers 8
 // rows x 64 bytes, whole 32-byte sectors, instead of 32 rows x 16 bytes, which
@@ -162,7 +125,7 @@ __device__ __forceinline__ void store_rows(uint8_t *stg, int lane, const uint4 (
     __syncwarp();
 }
 
-template <int MODE, bool SPLIT>
+template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
 product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w0,
                const __grid_constant__ CUtensorMap tm_w1, const __grid_constant__ CUtensorMap tm_out, const Params p)
@@ -195,15 +158,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     tc_fence_after();
 
     const uint32_t tmem = c.tmem_base;
-    const int S = SPLIT ? p.split : 1;
-    const int rank = SPLIT ? (int)cluster_rank() : 0;
-    const int first = SPLIT ? blockIdx.x / S : blockIdx.x;
-    const int stride = SPLIT ? gridDim.x / S : gridDim.x;
-    // (a cluster takes one tile, whatever total the offsets add up to)
-    const int total = SPLIT ? min(c.g.total, first + 1) : c.g.total;
-    // this CTA's blocks of the reduction
-    const int kb0 = SPLIT ? (int)((long long)p.KB * rank / S) : 0;
-    const int kb1 = SPLIT ? (int)((long long)p.KB * (rank + 1) / S) : p.KB;
+    const int total = c.g.total, first = blockIdx.x, stride = gridDim.x;
     volatile int *abort_flag = &c.abort_flag;
     if (warp < 4) {
         // (inside the branch: the compiler gives each side its own limit)
@@ -215,7 +170,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             for (int t = first; t < total && ok; t += stride) {
                 const Tile tile = tile_at(c.g, E, t, BM);
                 const int boxes = (tile.cnt + ABOX - 1) / ABOX;   // only as many as the tile has rows
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                for (int kb = 0; kb < p.KB; ++kb, ++it) {
                     const int s = it % STAGES;
                     ok = __all_sync(0xffffffffu, bar_wait(&c.empty[s], ((it / STAGES) & 1u) ^ 1u, abort_flag));
                     if (!ok) break;
@@ -265,7 +220,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             uint32_t it = 0;
             bool ok = true;
             for (int t = first; t < total && ok; t += stride) {
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                for (int kb = 0; kb < p.KB; ++kb, ++it) {
                     const int s = it % STAGES;
                     const uint32_t b = it & 1u;
                     ok = bar_wait(&c.tempty[b][h], ((it >> 1) & 1u) ^ 1u, abort_flag) &&
@@ -312,8 +267,8 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             // the weight scales of the columns this warp sums: gate and up, or
             // one 128-column block (none past the last: its sums are zero)
             const int nb = MODE == GATEUP ? next.nt : min(next.nt * 2 + half, p.NB - 1);
-            ws = (uint32_t)((next.e * p.NB + nb) * p.KB + kb0);
-            nx = xs ? __ldg(xs + kb0) : 0.f;
+            ws = (uint32_t)((next.e * p.NB + nb) * p.KB);
+            nx = xs ? __ldg(xs) : 0.f;
             n0 = __ldg(p.w_s[0] + ws);
             if (MODE == GATEUP) n1 = __ldg(p.w_s[1] + ws);
         };
@@ -326,12 +281,12 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
 #pragma unroll
             for (int i = 0; i < 64; ++i) acc[i] = 0ull;
 #pragma unroll 1
-            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+            for (int kb = 0; kb < p.KB; ++kb, ++it) {
                 const uint32_t b = it & 1u;
                 const float f0 = nx * n0, f1 = MODE == GATEUP ? nx * n1 : f0;
                 const uint64_t m0 = pack2(__float_as_uint(f0), __float_as_uint(f0));
                 const uint64_t m1 = pack2(__float_as_uint(f1), __float_as_uint(f1));
-                if (kb + 1 < kb1) {
+                if (kb + 1 < p.KB) {
                     nx = xs ? __ldg(xs + kb + 1) : 0.f;
                     n0 = __ldg(p.w_s[0] + ++ws);
                     if (MODE == GATEUP) n1 = __ldg(p.w_s[1] + ws);
@@ -364,21 +319,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                 for (int i = 0; i < 64; ++i) acc[i] = nan2;
             }
             auto val = [&](int i) { return (i & 1) ? hi2(acc[i >> 1]) : lo2(acc[i >> 1]); };
-            if constexpr (SPLIT) {
-                // once the other half's MMAs have completed too, the ring holds
-                // the partial sums, in tile column order
-                const uint32_t last = it - 1;
-                if (!bar_wait(&c.tfull[last & 1u][half ^ 1], (last >> 1) & 1u, abort_flag)) c.abort_flag = 1;
-                float *sums = reinterpret_cast<float *>(smem) + row * kPartRow;
-                if (valid) {
-#pragma unroll
-                    for (int i = 0; i < 128; i += 4) {
-                        const int cc = MODE == GATEUP ? (i >> 6) * (BN / 2) + half * 64 + (i & 63) : half * (BN / 2) + i;
-                        *reinterpret_cast<float4 *>(sums + cc) = make_float4(val(i), val(i + 1), val(i + 2), val(i + 3));
-                    }
-                }
-                break;   // one tile per cluster
-            } else if constexpr (MODE == GATEUP) {
+            if constexpr (MODE == GATEUP) {
                 uint32_t m = 0u;
                 float h[64];
 #pragma unroll
@@ -471,45 +412,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         if (MODE == PRODUCT && lane == 0) bulk_wait_all();
     }
 
-    if constexpr (SPLIT) {
-        cluster_sync_all();   // every CTA's partial sums are written
-        if (first < total && warp >= 4) {
-            // row by row, the clusters' CTAs in turn, a warp to a row: lane l adds
-            // columns 4l.. and 128 + 4l.. over the CTAs in the order of the blocks
-            const Tile tile = tile_at(c.g, E, first, BM);
-            // (a CTA that gave up may still have had loads landing on its sums)
-            bool failed = false;
-            for (int q = 0; q < S; ++q) failed |= ld_cluster_u32(peer_addr(&c.abort_flag, q)) != 0u;
-            for (int row = rank + S * (warp - 4); row < tile.cnt; row += S * kEpiWarps) {
-                float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-#pragma unroll 4
-                for (int q = 0; q < S; ++q) {
-                    const uint32_t at = peer_addr(smem, q) + (uint32_t)(row * kPartRow + 4 * lane) * 4;
-                    const float4 x = ld_cluster_f4(at), y = ld_cluster_f4(at + 4 * (BN / 2));
-                    a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
-                    b.x += y.x; b.y += y.y; b.z += y.z; b.w += y.w;
-                }
-                if (failed) a.x = a.y = a.z = a.w = b.x = b.y = b.z = b.w = __uint_as_float(0x7fffffffu);
-                const long long r = tile.row0 + row;
-                if constexpr (MODE == GATEUP) {
-                    const float h[4] = {swiglu(a.x, b.x), swiglu(a.y, b.y), swiglu(a.z, b.z), swiglu(a.w, b.w)};
-                    const uint32_t m = __reduce_max_sync(0xffffffffu, max(max(mag_bits(h[0]), mag_bits(h[1])),
-                                                                         max(mag_bits(h[2]), mag_bits(h[3]))));
-                    const float s = block_scale(m), f = code_factor(s);
-                    const int n0 = tile.nt * (BN / 2) + 4 * lane;
-                    if (n0 < p.N)
-                        *reinterpret_cast<uint32_t *>(p.h_q + r * p.N + n0) = encode4(h[0], h[1], h[2], h[3], f);
-                    if (lane == 0) p.h_s[r * p.NB + tile.nt] = s;
-                } else {
-                    store4(p, r, tile.nt * BN + 4 * lane, a);
-                    store4(p, r, tile.nt * BN + BN / 2 + 4 * lane, b);
-                }
-            }
-        }
-    }
-    // no CTA leaves while another reads its shared memory
-    if (SPLIT) cluster_sync_all();
-    else __syncthreads();
+    __syncthreads();
     if (warp == 3) {
         __syncwarp();
         tc_fence_after();
@@ -563,21 +466,18 @@ bool out_map(CUtensorMap *m, const Params &p)
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE, bool SPLIT>
-cudaError_t launch_variant(const CUtensorMap &x, const CUtensorMap &w0, const CUtensorMap &w1,
+template <int MODE>
+cudaError_t launch_kernel(const CUtensorMap &x, const CUtensorMap &w0, const CUtensorMap &w1,
                            const CUtensorMap &out, const Params &p, long long tiles, int num_sms, cudaStream_t stream)
 {
     static PerDeviceFlag done;
     const int dev = current_device();
-    auto *kern = product_kernel<MODE, SPLIT>;
+    auto *kern = product_kernel<MODE>;
     if (!done.done(dev)) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
         if (e != cudaSuccess) return e;
         done.mark(dev);
     }
-    if (SPLIT)
-        return launch_pdl_cluster(kern, dim3((unsigned)(tiles * p.split)), dim3(kThreads), kSmem, stream, p.split, x,
-                                  w0, w1, out, p);
     return launch_pdl(kern, dim3((unsigned)(tiles < num_sms ? tiles : num_sms)), dim3(kThreads), kSmem, stream, x, w0,
                       w1, out, p);
 }
@@ -587,7 +487,7 @@ cudaError_t launch_product(const void *x_q, long long ldx, const void *w0, const
                            cudaStream_t stream)
 {
     const int num_sms = device_sm_count();
-    if (decode_fits(p)) return launch_decode<MODE>(x_q, ldx, w0, w1, p, num_sms, stream);
+    if (decode_fits(p, num_sms)) return launch_decode<MODE>(x_q, ldx, w0, w1, p, num_sms, stream);
     if (p.perm_tok) {
         // Rows go into group order once, ahead of the product: every column
         // tile would gather them again, and a loop that copies rows feeds the
@@ -607,30 +507,22 @@ cudaError_t launch_product(const void *x_q, long long ldx, const void *w0, const
         p.perm_tok = nullptr;
     }
     p.n_tiles = ceil_div(p.N, MODE == GATEUP ? BN / 2 : BN);
-    // most tiles there can be: every expert with rows may own a ragged row tile
-    const long long tiles = ((long long)p.rows / BM + (p.E < p.rows ? p.E : p.rows)) * p.n_tiles;
+    // most tiles there can be: an expert with r rows has (r - 1) / BM + 1, so as
+    // many experts as possible with rows, and the rest of the rows in whole tiles
+    const long long experts = p.E < p.rows ? p.E : p.rows;
+    const long long tiles = ((p.rows - experts) / BM + experts) * p.n_tiles;
     if (tiles > 0x3fffffffLL) return cudaErrorInvalidValue;
-    // tiles for fewer than half the SMs: the reduction is split over as many
-    // CTAs as there are SMs and blocks for (at most 8, the portable cluster)
-    p.split = 1;
-    if (2 * tiles <= num_sms) {
-        const long long each = num_sms / tiles;
-        p.split = (int)(each < 8 ? each : 8);
-        if (p.split > p.KB) p.split = p.KB;
-    }
     CUtensorMap mx, mw0, mw1, mout;
     constexpr uint32_t wbox = MODE == GATEUP ? BN / 4 : BN;
     if (!code_map(&mx, x_q, 0, p.x_rows, p.K, ldx, ABOX) || !code_map(&mw0, w0, p.E, p.N, p.K, p.K, wbox))
         return cudaErrorInvalidValue;
     if (MODE != GATEUP) mw1 = mw0;
     else if (!code_map(&mw1, w1, p.E, p.N, p.K, p.K, wbox)) return cudaErrorInvalidValue;
-    // the output as a tensor, where its rows suit TMA (a split product stores a
-    // row at a time)
-    p.out_tma = MODE == PRODUCT && p.split == 1 && p.out_vec;
+    // the output as a tensor, where its rows suit TMA
+    p.out_tma = MODE == PRODUCT && p.out_vec;
     if (!p.out_tma) mout = mx;
     else if (!out_map(&mout, p)) return cudaErrorInvalidValue;
-    return p.split > 1 ? launch_variant<MODE, true>(mx, mw0, mw1, mout, p, tiles, num_sms, stream)
-                       : launch_variant<MODE, false>(mx, mw0, mw1, mout, p, tiles, num_sms, stream);
+    return launch_kernel<MODE>(mx, mw0, mw1, mout, p, tiles, num_sms, stream);
 }
 
 bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

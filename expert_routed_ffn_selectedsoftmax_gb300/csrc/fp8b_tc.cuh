@@ -32,7 +32,7 @@ struct Params {
     uint8_t *h_q;             // GATEUP: [rows, N] codes, [rows, NB] scales
     float *h_s;
     uint32_t *status;
-    int split;                // CTAs per cluster (SPLIT)
+    int split;                // CTAs per cluster (fp8b_decode.cu)
 };
 
 // Instruction descriptor of tcgen05.mma kind::f8f6f4: fp32 accumulate, A and B
@@ -193,7 +193,7 @@ inline bool code_map(CUtensorMap *m, const void *base, int n, int rows, int cols
 }
 
 // fp8b_decode.cu: the products of few rows, weights as the MMA's rows
-bool decode_fits(const Params &p);
+bool decode_fits(const Params &p, int num_sms);
 template <int MODE>
 cudaError_t launch_decode(const void *x_q, long long ldx, const void *w0, const void *w1, Params p, int num_sms,
                           cudaStream_t stream);
