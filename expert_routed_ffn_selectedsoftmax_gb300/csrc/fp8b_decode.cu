@@ -214,9 +214,11 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
         if (!ok) {
             if (leader) flag_status(p.status, kDevTimeout);
             c.abort_flag = 1;
-            if (leader) umma_commit(&c.drain);   // MMAs in flight end before TMEM is freed
-            volatile int no_abort = 0;
-            bar_wait(&c.drain, 0, &no_abort);
+            if (it > 0) {   // MMAs in flight end before TMEM is freed
+                if (leader) umma_commit(&c.drain);
+                volatile int no_abort = 0;
+                bar_wait(&c.drain, 0, &no_abort);
+            }
         }
     } else {
         // ------------------------------------------------ sums and output
@@ -255,6 +257,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
                 }
                 __syncwarp();
                 ok = ok && __all_sync(0xffffffffu, bar_wait(&c.tfull[b], (it / kBuffers) & 1u, abort_flag));
+                if (!ok) continue;   // (TMEM that no MMA has written is not read)
                 tc_fence_after();
                 const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + b * NW * NT;
 #pragma unroll

@@ -242,9 +242,11 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             if (!ok) {
                 if (leader) flag_status(p.status, kDevTimeout);
                 c.abort_flag = 1;
-                if (leader) umma_commit(&c.drain[h]);   // MMAs in flight end before TMEM is freed
-                volatile int no_abort = 0;
-                bar_wait(&c.drain[h], 0, &no_abort);
+                if (it > 0) {   // MMAs in flight end before TMEM is freed
+                    if (leader) umma_commit(&c.drain[h]);
+                    volatile int no_abort = 0;
+                    bar_wait(&c.drain[h], 0, &no_abort);
+                }
             }
         }
     } else {
@@ -292,6 +294,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                     if (MODE == GATEUP) n1 = __ldg(p.w_s[1] + ws);
                 }
                 ok = ok && __all_sync(0xffffffffu, bar_wait(&c.tfull[b][half], (it >> 1) & 1u, abort_flag));
+                if (!ok) continue;   // (TMEM that no MMA has written is not read)
                 tc_fence_after();
                 const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + b * BN + half * (BN / 2);
                 // Two loads of 64 columns: the buffer's reads are in the chain that

@@ -478,6 +478,19 @@ def test_status_word(moe):
     assert moe.moe_check(status) == 0
 
 
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [4, 8, 16, 40])
+def test_narrow_outputs_of_many_rows(moe, N, out):
+    """Outputs narrower than the stores' boxes, rows 16 bytes apart and more."""
+    T, K = 6000, 144
+    xq, xs = pair(T, K)
+    wq, ws = pair(N, K, seed=3, block_rows=128)
+    wide = torch.full((T + 2, N), 3.0, dtype=DT[out], device=DEV)
+    y = moe.moe_gemm_fp8b(xq, xs, wq, ws, out=wide[1:-1])
+    check_product(y, value(xq, xs, 1), value(wq, ws, 128), K)
+    assert bool((wide[0] == 3).all()) and bool((wide[-1] == 3).all())
+
+
 # --------------------------------------------------- streams, graphs, chains
 
 def layer(E, d, F, seed):
