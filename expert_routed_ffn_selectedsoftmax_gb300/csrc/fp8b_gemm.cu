@@ -11,6 +11,16 @@
 // times the two scales, to the row's running fp32 sums in registers while the
 // tensor cores fill the other buffer.
 //
+// What bounds it: 8192 x 2048 x 5632 takes 82 us, 2.3 PFLOP/s (a library product
+// with one scale for each matrix, which needs no such turns: 51 us).  A block of
+// a 128 x 256 tile takes 870 clocks of which the MMAs are 470: the rest is the
+// turn of a TMEM buffer -- commit, wake, read, sums, arrival, wake -- that the
+// other buffers' MMAs do not cover, and a tile's end, where its sums are written
+// while the MMAs run at most two blocks ahead (the ncu capture shows the tensor
+// pipe 54 % busy, shared memory and L2 a third, issue slots 45 %).  Tried and no
+// faster: CTA pairs (M = 256; 85 us, and ragged groups pad more), one issuing warp
+// with N = 256 (89), sixteen epilogue warps (98), scalar sums (89).
+//
 // A tile is 128 rows x 256 columns (PRODUCT), or 128 rows x 128 columns of
 // both W_gate and W_up (GATEUP: the epilogue has whole 128-column groups of h,
 // so it quantises them without a second pass).  Warp 0 loads by TMA (rows in
@@ -56,6 +66,7 @@ constexpr size_t kRing = (size_t)STAGES * STAGE;          // then the staging (f
 constexpr size_t kCtl = kRing + kEpiWarps * kStaging;     // bytes: the stores' swizzle), then Ctl
 constexpr size_t kSmem = 1024 + kCtl + sizeof(Ctl);
 static_assert(kSmem <= 232448, "shared memory per CTA");
+
 #define MOE_OUTS16(v, i)                                                                                        \
     "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), "=r"(v[i + 6]), \
         "=r"(v[i + 7]), "=r"(v[i + 8]), "=r"(v[i + 9]), "=r"(v[i + 10]), "=r"(v[i + 11]), "=r"(v[i + 12]),      \
@@ -470,8 +481,8 @@ bool out_map(CUtensorMap *m, const Params &p)
 }
 
 template <int MODE>
-cudaError_t launch_kernel(const CUtensorMap &x, const CUtensorMap &w0, const CUtensorMap &w1,
-                           const CUtensorMap &out, const Params &p, long long tiles, int num_sms, cudaStream_t stream)
+cudaError_t launch_kernel(const CUtensorMap &x, const CUtensorMap &w0, const CUtensorMap &w1, const CUtensorMap &out,
+                          const Params &p, long long tiles, int num_sms, cudaStream_t stream)
 {
     static PerDeviceFlag done;
     const int dev = current_device();

@@ -459,6 +459,7 @@ MOE_API moe_status moe_forward_noalloc(const void *x, moe_dtype act_dt, int T, i
  * caller zeroes it once and may share it between calls; moe_check reads it
  * (as a workspace of its own).
  * Reproducibility: every call gives bitwise identical results from run to run.
+ * No output may overlap an input or another output (moe_norm_fp8b's resid aside).
  */
 
 /*

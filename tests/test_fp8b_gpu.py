@@ -326,15 +326,17 @@ def test_gemm_scales_act_on_their_own_block(moe):
     assert torch.equal(bad, want)
 
 
-def test_gemm_strided(moe):
-    T, K, N = 45, 384, 200
+@pytest.mark.parametrize("T", [45, 3007])
+def test_gemm_strided(moe, T):
+    """Rows further apart than their length, in and out, aligned and not."""
+    K, N = 384, 1000
     wide = torch.zeros(T, 1024, device=DEV).to(F8)
     xq, xs = pair(T, K)
     wide[:, 512:512 + K] = xq
     wq, ws = pair(N, K, seed=2, block_rows=128)
     for dt in DT.values():
         for pad in (0, 8, 5):       # 5: rows whose 16-byte pieces are not aligned
-            buf = torch.full((T, N + pad + 3), 7.0, dtype=dt, device=DEV)
+            buf = torch.full((T, N + pad + (8 if pad == 8 else 3)), 7.0, dtype=dt, device=DEV)
             y = moe.moe_gemm_fp8b(wide[:, 512:512 + K], xs, wq, ws, out=buf[:, pad:pad + N])
             check_product(y, value(xq, xs, 1), value(wq, ws, 128), K)
             assert bool((buf[:, :pad] == 7).all()) and bool((buf[:, pad + N:] == 7).all())
@@ -443,9 +445,10 @@ def test_padded_batch_leaves_the_rest(moe, T, E):
         assert bool((pad[0] == 3).all()) and bool((pad[-1] == 3).all())
 
 
-def test_rows_out_of_range_stay_their_own(moe):
+@pytest.mark.parametrize("T", [50, 5000])
+def test_rows_out_of_range_stay_their_own(moe, T):
     """A perm_tok outside [0, x_rows) spoils its own row alone."""
-    T, E, K, N = 50, 3, 256, 128
+    E, K, N = 3, 256, 128
     off, perm, _ = grouping(T, E, 1, seed=1)
     xq, xs = pair(T, K)
     wq, ws = pair(N, K, seed=4, block_rows=128, lead=(E,))
@@ -468,6 +471,36 @@ def test_empty(moe):
     out = torch.full((6, 8), 2.0, device=DEV)
     moe.moe_grouped_gemm_fp8b(q(6, 128), f(6, 1), q(4, 8, 128), f(4, 1, 1), off, out=out)
     assert bool((out == 2).all())
+
+
+def test_given_workspace(moe):
+    """A workspace of the caller's, used again by the next call; one too small."""
+    T, E, K, N = 2000, 4, 256, 512
+    off, perm, _ = grouping(T, E, 2, seed=1)
+    xq, xs = pair(T, K)
+    wq, ws = pair(N, K, seed=4, block_rows=128, lead=(E,))
+    work = torch.empty(moe.moe_fp8b_workspace_size(2 * T, K), dtype=torch.uint8, device=DEV)
+    want = moe.moe_grouped_gemm_fp8b(xq, xs, wq, ws, off, perm_tok=perm)
+    h_want = moe.moe_gate_up_fp8b(xq, xs, wq, ws, wq, ws, offsets=off, perm_tok=perm)
+    for _ in range(2):
+        got = moe.moe_grouped_gemm_fp8b(xq, xs, wq, ws, off, perm_tok=perm, workspace=work)
+        h = moe.moe_gate_up_fp8b(xq, xs, wq, ws, wq, ws, offsets=off, perm_tok=perm, workspace=work)
+    assert torch.equal(got, want) and torch.equal(bits(h[0]), bits(h_want[0])) and torch.equal(h[1], h_want[1])
+    with pytest.raises(moe.MoeError) as e:
+        moe.moe_grouped_gemm_fp8b(xq, xs, wq, ws, off, perm_tok=perm, workspace=work[:-1])
+    assert e.value.status == 3      # MOE_ERR_WORKSPACE
+
+
+def test_few_and_many_rows_agree(moe):
+    """The same rows through the few-rows kernel (alone) and the tiled one (among
+    many): the sums differ by their order at most."""
+    K, N = 1024, 640
+    xq, xs = pair(6000, K)
+    wq, ws = pair(N, K, seed=4, block_rows=128)
+    many = moe.moe_gemm_fp8b(xq, xs, wq, ws, out_dtype=torch.float32)
+    few = moe.moe_gemm_fp8b(xq[:20], xs[:20], wq, ws, out_dtype=torch.float32)
+    tol = product_bound(value(xq[:20], xs[:20], 1), value(wq, ws, 128), K)
+    assert bool(((many[:20].double() - few.double()).abs() <= 2 * tol).all())
 
 
 def test_status_word(moe):
@@ -544,11 +577,12 @@ def test_layers_in_a_row(moe, T, E, k, d, F):
     check_norm(prev["resid"], layers[0]["norm"], 1e-6, (resid, normed, q, s), prev["y"], prev["topk_w"], prev["inv"])
 
 
-def test_streams_and_captured_graphs(moe):
+@pytest.mark.parametrize("T", [48, 1500])     # (the second gathers into a workspace)
+def test_streams_and_captured_graphs(moe, T):
     """The stack of layers on a side stream, and captured and replayed with new
     inputs, gives what it gives eagerly, bit for bit; two captured graphs
     replayed side by side do not disturb each other."""
-    T, E, k, d, F = 48, 16, 2, 512, 256
+    E, k, d, F = 16, 2, 512, 256
     layers = [layer(E, d, F, seed=40 + i) for i in range(2)]
     xs = [rand(T, d, seed=i, sd=2.0) for i in range(4)]
     want = [run_layers(moe, x, layers, k) for x in xs]
