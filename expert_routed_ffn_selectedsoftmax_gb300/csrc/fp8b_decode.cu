@@ -53,10 +53,11 @@ constexpr int kMaxStages = 5;
 
 struct alignas(16) Ctl {
     uint64_t full[kMaxStages], empty[kMaxStages], tfull[kBuffers], tempty[kBuffers], drain;
+    uint64_t never;                          // nothing arrives here (test hook)
     uint32_t tmem_base;
     int abort_flag;
     uint32_t amax[kEpiWarps][NT];            // GATEUP: each warp's largest |h| per token
-    float factor[kEpiWarps][2][NT];          // [warp][matrix][token]
+    alignas(16) float factor[kEpiWarps][2][NT];   // [warp][matrix][token], read four at a time
     Groups g;
 };
 template <int MODE> constexpr size_t smem_bytes() { return 1024 + Cfg<MODE>::RING + sizeof(Ctl); }
@@ -112,6 +113,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
         for (int s = 0; s < STAGES; ++s) { mbar_init(&c.full[s], 1); mbar_init(&c.empty[s], 1); }
         for (int b = 0; b < kBuffers; ++b) { mbar_init(&c.tfull[b], 1); mbar_init(&c.tempty[b], kEpiWarps); }
         mbar_init(&c.drain, 1);
+        mbar_init(&c.never, 1);
         c.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_x)) : "memory");
@@ -145,7 +147,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
     if (warp == 0) {
         // ------------------------------------------------ loads
         uint32_t it = 0;
-        bool ok = true;
+        bool ok = p.expire_ns == 0 || __all_sync(0xffffffffu, bar_wait(&c.never, 0, abort_flag, p.expire_ns));
         for (int t = first; t < total && ok; t += stride) {
             const Tile tile = tile_at(c.g, E, t, NT);
             int4 tok = make_int4(0, 0, 0, 0);

@@ -57,6 +57,7 @@ constexpr int kStaging = 32 * 256;               // bytes per epilogue warp: 256
 
 struct alignas(16) Ctl {
     uint64_t full[STAGES], empty[STAGES], tfull[2][2], tempty[2][2], drain[2];   // [buffer][column half]
+    uint64_t never;           // nothing arrives here (test hook)
     uint32_t tmem_base;
     int abort_flag;
     Groups g;
@@ -151,6 +152,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         for (int s = 0; s < STAGES; ++s) { mbar_init(&c.full[s], 1); mbar_init(&c.empty[s], 2); }
         for (int b = 0; b < 4; ++b) { mbar_init(&c.tfull[b >> 1][b & 1], 1); mbar_init(&c.tempty[b >> 1][b & 1], kEpiWarps / 2); }
         for (int h = 0; h < 2; ++h) mbar_init(&c.drain[h], 1);
+        mbar_init(&c.never, 1);
         c.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_x)) : "memory");
@@ -177,7 +179,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         if (warp == 0) {
             // -------------------------------------------- loads
             uint32_t it = 0;
-            bool ok = true;
+            bool ok = p.expire_ns == 0 || __all_sync(0xffffffffu, bar_wait(&c.never, 0, abort_flag, p.expire_ns));
             for (int t = first; t < total && ok; t += stride) {
                 const Tile tile = tile_at(c.g, E, t, BM);
                 const int boxes = (tile.cnt + ABOX - 1) / ABOX;   // only as many as the tile has rows
@@ -584,6 +586,30 @@ Params params_of(const float *x_s, int x_rows, int K, const float *s0, const flo
 using namespace moe;
 using namespace moe::fp8b;
 
+namespace {
+
+moe_status grouped_gemm(const void *x_q, const float *x_s, int x_rows, int K, long long ldx, const void *w_q,
+                        const float *w_s, int E, int N, const int32_t *offsets, const int32_t *perm_tok, int rows,
+                        void *out, moe_dtype out_dt, long long ldo, void *workspace, size_t ws_bytes, uint32_t *status,
+                        uint32_t expire_ns, moe_stream stream)
+{
+    bool go;
+    const moe_status st = product_args(x_q, x_s, x_rows, K, ldx, w_q, w_s, E, N, offsets, perm_tok, rows, status,
+                                        workspace, ws_bytes, &go);
+    if (st != MOE_OK) return st;
+    if ((out_dt != MOE_F32 && out_dt != MOE_BF16) || ldo < N) return MOE_ERR_INVALID_ARG;
+    if (!go) return MOE_OK;
+    if (!out || !aligned_to(out, out_dt == MOE_F32 ? 4 : 2)) return MOE_ERR_INVALID_ARG;
+    Params p = params_of(x_s, x_rows, K, w_s, nullptr, E, N, offsets, perm_tok, rows, status);
+    p.expire_ns = expire_ns;
+    p.out = out; p.ldo = ldo; p.out_f32 = out_dt == MOE_F32;
+    p.out_vec = ldo % (out_dt == MOE_F32 ? 4 : 8) == 0 && aligned_to(out, 16);
+    const cudaError_t e = launch_product<PRODUCT>(x_q, ldx, w_q, nullptr, p, workspace, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // namespace
+
 extern "C" {
 
 size_t moe_fp8b_workspace_size(int rows, int K)
@@ -597,18 +623,19 @@ moe_status moe_grouped_gemm_fp8b(const void *x_q, const float *x_s, int x_rows, 
                                  const int32_t *perm_tok, int rows, void *out, moe_dtype out_dt, long long ldo,
                                  void *workspace, size_t ws_bytes, uint32_t *status, moe_stream stream)
 {
-    bool go;
-    const moe_status st = product_args(x_q, x_s, x_rows, K, ldx, w_q, w_s, E, N, offsets, perm_tok, rows, status,
-                                        workspace, ws_bytes, &go);
-    if (st != MOE_OK) return st;
-    if ((out_dt != MOE_F32 && out_dt != MOE_BF16) || ldo < N) return MOE_ERR_INVALID_ARG;
-    if (!go) return MOE_OK;
-    if (!out || !aligned_to(out, out_dt == MOE_F32 ? 4 : 2)) return MOE_ERR_INVALID_ARG;
-    Params p = params_of(x_s, x_rows, K, w_s, nullptr, E, N, offsets, perm_tok, rows, status);
-    p.out = out; p.ldo = ldo; p.out_f32 = out_dt == MOE_F32;
-    p.out_vec = ldo % (out_dt == MOE_F32 ? 4 : 8) == 0 && aligned_to(out, 16);
-    const cudaError_t e = launch_product<PRODUCT>(x_q, ldx, w_q, nullptr, p, workspace, static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return grouped_gemm(x_q, x_s, x_rows, K, ldx, w_q, w_s, E, N, offsets, perm_tok, rows, out, out_dt, ldo, workspace,
+                        ws_bytes, status, 0, stream);
+}
+
+moe_status moe_grouped_gemm_fp8b_expire_wait(const void *x_q, const float *x_s, int x_rows, int K, long long ldx,
+                                             const void *w_q, const float *w_s, int E, int N, const int32_t *offsets,
+                                             const int32_t *perm_tok, int rows, void *out, moe_dtype out_dt,
+                                             long long ldo, void *workspace, size_t ws_bytes, uint32_t *status,
+                                             uint32_t wait_ns, moe_stream stream)
+{
+    if (wait_ns == 0 || wait_ns > 100000000u) return MOE_ERR_INVALID_ARG;
+    return grouped_gemm(x_q, x_s, x_rows, K, ldx, w_q, w_s, E, N, offsets, perm_tok, rows, out, out_dt, ldo, workspace,
+                        ws_bytes, status, wait_ns, stream);
 }
 
 moe_status moe_gemm_fp8b(const void *x_q, const float *x_s, int T, int K, long long ldx, const void *w_q,

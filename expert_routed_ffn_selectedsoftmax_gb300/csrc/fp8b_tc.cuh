@@ -32,6 +32,7 @@ struct Params {
     uint8_t *h_q;             // GATEUP: [rows, N] codes, [rows, NB] scales
     float *h_s;
     uint32_t *status;
+    uint32_t expire_ns;       // > 0: the loading warp's first wait gives up after this long (test hook)
     int split;                // CTAs per cluster (fp8b_decode.cu)
 };
 

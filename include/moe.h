@@ -589,6 +589,19 @@ MOE_API moe_status moe_forward_expire_wait(const void *x, moe_dtype act_dt, int 
                                            int kernel_family, uint32_t wait_ns, moe_stream stream);
 
 /*
+ * moe_grouped_gemm_fp8b_expire_wait -- the same hook for the block-scaled fp8
+ * products: moe_grouped_gemm_fp8b (whichever of its kernels the sizes choose)
+ * with its loading warps' first wait limited to `wait_ns` (1 ns .. 100 ms).
+ * Every row of every group becomes NaN and `status` reports MOE_ERR_TIMEOUT.
+ * Not for production use.
+ */
+MOE_API moe_status moe_grouped_gemm_fp8b_expire_wait(
+    const void *x_q, const float *x_s, int x_rows, int K, long long ldx, const void *w_q,
+    const float *w_s, int E, int N, const int32_t *offsets, const int32_t *perm_tok, int rows,
+    void *out, moe_dtype out_dt, long long ldo, void *workspace, size_t ws_bytes, uint32_t *status,
+    uint32_t wait_ns, moe_stream stream);
+
+/*
  * moe_check_noalloc -- moe_check for moe_forward_noalloc: wait for `stream`,
  * then read the status word the most recent moe_forward_noalloc on the
  * current device left in the library's static scratch (MOE_OK,

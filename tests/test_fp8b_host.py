@@ -88,6 +88,9 @@ def test_product_arguments(lib):
     assert grouped(perm=FAKE, wsb=2303) == 3 and gate_up(perm=FAKE, wsb=2303) == 3      # MOE_ERR_WORKSPACE
     assert grouped(E=257) == U and gate_up(E=257) == U
     assert grouped(rows=0, xr=0, xq=None, out=None) == OK and gate_up(rows=0, xr=0, xq=None, hq=None) == OK
+    for ns in (0, 100_000_001):
+        assert lib.moe_grouped_gemm_fp8b_expire_wait(FAKE, FAKE, 8, 256, 256, FAKE, FAKE, 4, 64, FAKE, None, 8, FAKE, F32,
+                                                     64, None, 0, None, ns, None) == I
     g = lambda **kw: lib.moe_gemm_fp8b(*dict(dict(a=FAKE, b=FAKE, T=4, K=256, l=256, c=FAKE, d=FAKE, N=64, o=FAKE,
                                                   t=BF16, m=64, s=None, z=None), **kw).values())
     for bad in (dict(T=-1), dict(K=250), dict(l=128), dict(N=0), dict(t=5), dict(m=32), dict(a=None), dict(o=None)):
