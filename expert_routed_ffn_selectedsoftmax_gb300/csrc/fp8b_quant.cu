@@ -200,7 +200,7 @@ struct NormArgs {
 // One row per CTA, NV chunks of 8 values a thread, all in registers.  DT: the
 // added rows' type (int: nothing is added).
 template <typename XT, typename DT, int NV>
-__global__ void __launch_bounds__(kNormMaxThreads)
+__global__ void __launch_bounds__(kNormMaxThreads, NV == 1 ? 4 : 1)   // (NV 1: 32 registers, 2048 threads an SM)
 norm_kernel(const NormArgs a)
 {
     pdl_enter();
@@ -251,22 +251,39 @@ norm_kernel(const NormArgs a)
     if (lane == 0) part[warp] = sum;
     __syncthreads();
     sum = warp_sum(lane < nwarps ? part[lane] : 0.f);
-    const float scale = 1.0f / sqrtf(sum / (float)a.d + a.eps);
+    const float rs = 1.0f / sqrtf(sum / (float)a.d + a.eps);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int col = (threadIdx.x + j * blockDim.x) * 8;
         const bool in = col < a.d;
+        // y = z * rs with z = r * g
         if (in) {
             Chunk8 g;
             if (a.weight_bf16) load8(static_cast<const __nv_bfloat16 *>(a.weight) + col, g);
             else load8(static_cast<const float *>(a.weight) + col, g);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) r[j].v[i] *= scale * g.v[i];
-            if (a.normed) store8(a.normed + t * a.d + col, r[j].v);
+            for (int i = 0; i < 8; ++i) r[j].v[i] *= g.v[i];
+            if (a.normed) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) g.v[i] = r[j].v[i] * rs;
+                store8(a.normed + t * a.d + col, g.v);
+            }
         }
-        const float s = block_scale(max16(max8(r[j].v)));
+        const uint32_t zbits = max16(max8(r[j].v));
         if (in) {
-            *reinterpret_cast<uint2 *>(a.codes + t * a.d + col) = encode8(r[j].v, code_factor(s));
+            // The codes are those of y / s = 448 z / max|z|: the root and its
+            // rounding cancel, which leaves the roundings of z, of 448 / max|z| and
+            // of their product.  Where max|z| is so small that its factor could
+            // overflow, z is scaled by rs first.
+            const float zmax = __uint_as_float(zbits), ymax = zmax * rs;
+            const float s = block_scale(zbits >= kInfBits ? zbits : mag_bits(ymax));
+            const bool tiny = zmax < 0x1p-100f;
+            const float f = s > 0.f ? kFp8Max / (tiny ? ymax : zmax) : s;   // (s = 0: zero codes, NaN: NaN)
+            if (tiny) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) r[j].v[i] *= rs;
+            }
+            *reinterpret_cast<uint2 *>(a.codes + t * a.d + col) = encode8(r[j].v, f);
             if ((threadIdx.x & 15) == 0) a.scales[t * a.nblk + col / kBlock] = s;
         }
     }

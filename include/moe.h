@@ -489,7 +489,8 @@ MOE_API moe_status moe_quant_fp8b(const void *x, moe_dtype x_dt, int batch, int 
  *   nothing.  weight [d] fp32 or bf16.
  *   resid [T, d] out in x's type (contiguous; required with delta, untouched
  *   without; may be x itself when ldx == d); normed [T, d] bf16 out, or NULL;
- *   codes [T, d] and scales [T, ceil(d/128)] out: y per row and 128 columns.
+ *   codes [T, d] and scales [T, ceil(d/128)] out: y per row and 128 columns
+ *   (the codes' quotient y / s to two ulps of fp32).
  *   Apart from resid == x no output may overlap an input.
  *   d a multiple of 16, at most 16384; ldx, ldd multiples of 8; x, delta,
  *   weight, resid, normed and codes 16-byte aligned.

@@ -246,6 +246,25 @@ def test_norm_zero_and_non_finite_rows(moe):
     assert torch.equal(bits(one[2]), bits(q[3:])) and torch.equal(one[3], s[3:])
 
 
+@pytest.mark.parametrize("size", [1e-42, 1e-38, 1e-37, 1e-30, 1e-20, 1e15])
+def test_norm_of_small_and_large_rows(moe, size):
+    """Values whose squares vanish beside eps, scales at the smallest normal
+    number and below (those blocks are zeros), and large ones."""
+    x, w = (rand(5, 384) * size), 1 + rand(384, sd=0.1)
+    _, y, q, s = moe.moe_norm_fp8b(x, w, 1e-6)
+    _, want, err = norm_ref(x, w, 1e-6)
+    rms = torch.sqrt((x.double() ** 2).mean(1, keepdim=True) + 1e-6)
+    yerr = err / rms * w.double().abs() + want.abs() * 2.0 ** -18 + 2.0 ** -149 * 1e3
+    amax = want.abs().view(5, 3, B).amax(2)
+    zero = (s == 0) & (amax / FMAX < 2.0 ** -126 * 1.001)      # counted as zeros
+    assert bool(((s > 0) | zero).all())
+    keep = (s > 0).repeat_interleave(B, 1)
+    assert not q.float()[~keep].any()
+    got = value(q, s, 1)
+    tol = yerr + (want.abs() + yerr) * (2.0 ** -4 + 2.0 ** -22) + s.double().repeat_interleave(B, 1) * 2.0 ** -10
+    assert bool((((got - want).abs() <= tol) | ~keep).all())
+
+
 def test_norm_in_place_and_strided(moe):
     T, d = 21, 512
     wide, dwide = rand(T, 1024), rand(T, 768).bfloat16()
