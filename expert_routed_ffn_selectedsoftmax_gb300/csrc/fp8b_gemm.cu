@@ -55,6 +55,8 @@ constexpr int kRegsLaunch = 168, kRegsAux = 56, kRegsEpi = 224;
 static_assert(4 * kRegsAux + kEpiWarps * kRegsEpi <= (kThreads / 32) * kRegsLaunch, "more registers than the block has");
 constexpr int kStaging = 32 * 256;               // bytes per epilogue warp: 256 of each of its rows
 
+constexpr int kTable = 32;
+
 struct alignas(16) Ctl {
     uint64_t full[STAGES], empty[STAGES], tfull[2][2], tempty[2][2], drain[2];   // [buffer][column half]
     uint64_t never;           // nothing arrives here (test hook)
@@ -62,6 +64,7 @@ struct alignas(16) Ctl {
     int abort_flag;
     Groups g;
     uint32_t amax[2][BM];     // GATEUP: each row's largest |h| per column half
+    Tile tiles[kTable];       // this CTA's first tiles (each role asks for them in turn)
 };
 constexpr size_t kRing = (size_t)STAGES * STAGE;          // then the staging (from a multiple of 1024
 constexpr size_t kCtl = kRing + kEpiWarps * kStaging;     // bytes: the stores' swizzle), then Ctl
@@ -174,6 +177,11 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
 
     const uint32_t tmem = c.tmem_base;
     const int total = c.g.total, first = blockIdx.x, stride = gridDim.x;
+    // (a search and two divides a tile, 500 to 1200 clocks at each tile's end)
+    if (threadIdx.x < kTable && first + (int)threadIdx.x * stride < total)
+        c.tiles[threadIdx.x] = tile_at(c.g, E, first + threadIdx.x * stride, BM);
+    __syncthreads();
+    auto nth_tile = [&](int i, int t) { return i < kTable ? c.tiles[i] : tile_at(c.g, E, t, BM); };
     volatile int *abort_flag = &c.abort_flag;
     if (warp < 4) {
         // (inside the branch: the compiler gives each side its own limit)
@@ -182,8 +190,8 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             // -------------------------------------------- loads
             uint32_t it = 0;
             bool ok = !EXPIRE || __all_sync(0xffffffffu, bar_wait(&c.never, 0, abort_flag, p.expire_ns));
-            for (int t = first; t < total && ok; t += stride) {
-                const Tile tile = tile_at(c.g, E, t, BM);
+            for (int t = first, i = 0; t < total && ok; t += stride, ++i) {
+                const Tile tile = nth_tile(i, t);
                 const int boxes = (tile.cnt + ABOX - 1) / ABOX;   // only as many as the tile has rows
                 for (int kb = 0; kb < p.KB; ++kb, ++it) {
                     const int s = it % STAGES;
@@ -277,9 +285,9 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         uint32_t ws = 0;   // place of the weight scales (one for each 16 KB of codes: 32 bits do)
         float nx = 0.f, n0 = 0.f, n1 = 0.f;   // the next block's scales
         // tile t's place and its first scales, asked for ahead of the tile before's output
-        auto enter = [&](int t) {
+        auto enter = [&](int i, int t) {
             if (t >= total) return;
-            next = tile_at(c.g, E, t, BM);
+            next = nth_tile(i, t);
             xs = row < next.cnt ? p.x_s + (long long)(next.row0 + row) * p.KB : nullptr;
             // the weight scales of the columns this warp sums: gate and up, or
             // one 128-column block (none past the last: its sums are zero)
@@ -289,8 +297,8 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             n0 = __ldg(p.w_s[0] + ws);
             if (MODE == GATEUP) n1 = __ldg(p.w_s[1] + ws);
         };
-        enter(first);
-        for (int t = first; t < total; t += stride) {
+        enter(0, first);
+        for (int t = first, n = 1; t < total; t += stride, ++n) {
             const Tile tile = next;
             const bool valid = row < tile.cnt;
             const long long r = tile.row0 + row;
@@ -329,7 +337,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                     for (int i = 0; i < 32; ++i) fma2(acc[j * 32 + i], pack2(v[2 * i], v[2 * i + 1]), m);
                 }
             }
-            enter(t + stride);
+            enter(n, t + stride);
             if (!ok) {
                 c.abort_flag = 1;
                 const uint64_t nan2 = 0x7fffffff7fffffffull;
