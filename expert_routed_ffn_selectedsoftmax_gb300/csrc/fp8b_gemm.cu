@@ -105,10 +105,10 @@ __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wa
 // took longer than the products of a tile (8192 x 2048 x 5632: 178 us against
 // 100 us without the stores).  16-byte piece q of row r lies at q ^ (r / 2 % 4),
 // so neither side has bank conflicts.  `g`: row 0's bytes; `rows` of the 32 and
-// the first `bytes` exist; `vec`: 16-byte stores are aligned, else elements of
-// `size` bytes are stored one by one.
+// the first `bytes` exist; rows lie at multiples of 16 bytes, and a last piece
+// that is not whole is stored by elements of `size` bytes.
 __device__ __forceinline__ void store_rows(uint8_t *stg, int lane, const uint4 (&d)[4], uint8_t *g, long long pitch,
-                                           int rows, int bytes, bool vec, int size)
+                                           int rows, int bytes, int size)
 {
 #pragma unroll
     for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4 *>(stg + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) = d[q];
@@ -121,7 +121,7 @@ __device__ __forceinline__ void store_rows(uint8_t *stg, int lane, const uint4 (
         const int at = q * 16;
         if (r >= rows || at >= bytes) continue;
         uint8_t *o = g + r * pitch + at;
-        if (vec && at + 16 <= bytes) {
+        if (at + 16 <= bytes) {
             *reinterpret_cast<uint4 *>(o) = v;
         } else {
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -138,6 +138,21 @@ __device__ __forceinline__ void store_rows(uint8_t *stg, int lane, const uint4 (
         }
     }
     __syncwarp();
+}
+
+// One staged 128-byte piece of each of `rows` rows (16-byte part q of row r at
+// q ^ (r % 8)) to rows of any alignment, element by element.
+template <typename T>
+__device__ __forceinline__ void store_elements(const Params &p, const uint8_t *at, int lane, long long row0, int n, int rows)
+{
+    constexpr int V = 16 / (int)sizeof(T);   // elements of a 16-byte part
+    T *o = static_cast<T *>(p.out) + row0 * p.ldo + n;
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r)
+#pragma unroll
+        for (int c = lane; c < 8 * V; c += 32)
+            if (n + c < p.N)
+                o[r * p.ldo + c] = *reinterpret_cast<const T *>(at + r * 128 + (((c / V) ^ (r & 7)) << 4) + (c % V) * sizeof(T));
 }
 
 // EXPIRE: the test hook (p.expire_ns), a variant of its own so that the other
@@ -369,7 +384,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                     d[i] = make_uint4(encode4(v[0], v[1], v[2], v[3], f), encode4(v[4], v[5], v[6], v[7], f),
                                       encode4(v[8], v[9], v[10], v[11], f), encode4(v[12], v[13], v[14], v[15], f));
                 }
-                store_rows(stg, lane, d, p.h_q + (r - lane) * p.N + c0, p.N, tile.cnt - quarter * 32, p.N - c0, true, 1);
+                store_rows(stg, lane, d, p.h_q + (r - lane) * p.N + c0, p.N, tile.cnt - quarter * 32, p.N - c0, 1);
                 if (valid && half == 0) p.h_s[r * p.NB + tile.nt] = s;
             } else {
                 const int c0 = tile.nt * BN + half * (BN / 2), rows = tile.cnt - quarter * 32;
@@ -425,12 +440,22 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                                 bulk_commit();
                             }
                         }
-                    } else {
+                    } else if (p.out_vec) {
                         uint8_t *g = static_cast<uint8_t *>(p.out) + ((r - lane) * p.ldo + n) * size;
                         const int bytes = (p.N - n) * size;
                         const uint4 lo[4] = {d[0], d[1], d[2], d[3]}, hi[4] = {d[4], d[5], d[6], d[7]};
-                        store_rows(at, lane, lo, g, p.ldo * size, rows, bytes, p.out_vec, size);
-                        store_rows(at, lane, hi, g + 64, p.ldo * size, rows, bytes - 64, p.out_vec, size);
+                        store_rows(at, lane, lo, g, p.ldo * size, rows, bytes, size);
+                        store_rows(at, lane, hi, g + 64, p.ldo * size, rows, bytes - 64, size);
+                    } else {
+                        // rows that are not 16-byte aligned: staged as for TMA, then a
+                        // row at a time, 32 neighbouring elements an instruction
+                        __syncwarp();
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            *reinterpret_cast<uint4 *>(at + lane * 128 + ((q ^ (lane & 7)) << 4)) = d[q];
+                        __syncwarp();
+                        if (f32) store_elements<uint32_t>(p, at, lane, r - lane, n, min(rows, 32));
+                        else store_elements<uint16_t>(p, at, lane, r - lane, n, min(rows, 32));
                     }
                 }
             }
