@@ -569,8 +569,10 @@ cudaError_t launch_product(const void *x_q, long long ldx, const void *w0, const
         return cudaErrorInvalidValue;
     if (MODE != GATEUP) mw1 = mw0;
     else if (!code_map(&mw1, w1, p.E, p.N, p.K, p.K, wbox)) return cudaErrorInvalidValue;
-    // the output as a tensor, where its rows suit TMA
-    p.out_tma = MODE == PRODUCT && p.out_vec;
+    // the output as a tensor, where its rows suit TMA: it stores whole 16-byte
+    // parts, the last one of a row too, so rows that end inside one would lose
+    // what lies behind them (another column slice of the caller's tensor)
+    p.out_tma = MODE == PRODUCT && p.out_vec && p.N % (p.out_f32 ? 4 : 8) == 0;
     if (!p.out_tma) mout = mx;
     else if (!out_map(&mout, p)) return cudaErrorInvalidValue;
     if (MODE == PRODUCT && p.expire_ns)

@@ -312,6 +312,46 @@ def test_gemm(moe, out, T, K, N):
     assert torch.equal(y, moe.moe_gemm_fp8b(xq, xs, wq, ws, out_dtype=DT[out]))
 
 
+@pytest.mark.parametrize("T", [1, 16])
+@pytest.mark.parametrize("K", [896, 912, 1008, 1040, 1296])
+def test_gemm_of_few_rows_whole_and_split(moe, T, K):
+    """Reductions of 7 to 11 blocks, the last one ragged: on both sides of the
+    length from which few tiles split it, also where the parts are unequal."""
+    N = 1024
+    xq, xs = pair(T, K)
+    wq, ws = pair(N, K, seed=6, block_rows=128)
+    y = moe.moe_gemm_fp8b(xq, xs, wq, ws, out_dtype=torch.float32)
+    check_product(y, value(xq, xs, 1), value(wq, ws, 128), K)
+    assert torch.equal(y, moe.moe_gemm_fp8b(xq, xs, wq, ws, out_dtype=torch.float32))
+
+
+@pytest.mark.parametrize("T", [1, 16])
+@pytest.mark.parametrize("d", [384, 400, 512, 656])
+def test_gate_up_of_few_rows_whole_and_split(moe, T, d):
+    """The same for gate/up, which splits from 4 blocks."""
+    F = 400
+    xq, xs = pair(T, d)
+    (gq, gs), (uq, us) = (quant(rand(F, d, seed=s, sd=d ** -0.5), 128) for s in (1, 2))
+    hq, hs = moe.moe_gate_up_fp8b(xq, xs, gq, gs, uq, us)
+    h, err = swiglu_ref(value(xq, xs, 1), value(gq, gs, 128), value(uq, us, 128), d)
+    check_codes(hq, hs, h, err)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [129, 255, 1001, 1050])
+@pytest.mark.parametrize("pad", [0, 3, 6, 7])
+@pytest.mark.parametrize("T", [20, 4000])     # (few rows, and the tiled kernel)
+def test_unaligned_output_rows(moe, out, N, pad, T):
+    """Rows that begin or end inside 16 bytes: nothing beside them is written."""
+    K = 272
+    xq, xs = pair(T, K)
+    wq, ws = pair(N, K, seed=3, block_rows=128)
+    wide = torch.full((T + 2, N + pad), 3.0, dtype=DT[out], device=DEV)
+    y = moe.moe_gemm_fp8b(xq, xs, wq, ws, out=wide[1:-1, :N])
+    check_product(y, value(xq, xs, 1), value(wq, ws, 128), K)
+    assert bool((wide[0] == 3).all()) and bool((wide[-1] == 3).all()) and bool((wide[:, N:] == 3).all())
+
+
 def test_gemm_every_code(moe):
     """Every finite code of both signs on both sides, exact sums: one nonzero
     weight per output column."""
