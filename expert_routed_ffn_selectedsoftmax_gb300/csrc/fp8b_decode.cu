@@ -484,9 +484,13 @@ cudaError_t launch_decode(const void *x_q, long long ldx, const void *w0, const 
     // tiles for fewer than half the SMs: split the reduction over a CTA for each
     // SM, at most 8 a tile (one token, 2048 x 5632 in 44 tiles: 2 CTAs a tile
     // 5.8 us, 4: 6.2, 6: 6.5; 1024 x 2 x 512 of two experts in 8 tiles: 2 CTAs a
-    // tile 6.4 us, 4: 5.9, 8: 5.4)
+    // tile 6.4 us, 4: 5.9, 8: 5.4).  Short reductions stay whole, as the CTAs'
+    // meeting costs more than the blocks it saves: a product of 16 tokens and 1024
+    // columns takes 4.1 us split and 3.7 whole at K = 512, 5.1 and 4.5 at 896, 5.2
+    // and 6.8 at 2048 (one token 3.6 and 4.3 at 1024); gate/up, with two products a
+    // block, of one token and F = 512 5.0 and 4.75 at d = 256, 5.3 and 5.6 at 512.
     p.split = 1;
-    if (2 * tiles <= num_sms) {
+    if (2 * tiles <= num_sms && p.KB >= (MODE == GATEUP ? 4 : 8)) {
         const long long each = num_sms / tiles;
         p.split = (int)(each < 8 ? each : 8);
         if (p.split > p.KB) p.split = p.KB;
