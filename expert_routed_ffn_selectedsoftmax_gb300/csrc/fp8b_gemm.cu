@@ -11,7 +11,7 @@
 // times the two scales, to the row's running fp32 sums in registers while the
 // tensor cores fill the other buffer.
 //
-// What bounds it: 8192 x 2048 x 5632 takes 82 us, 2.3 PFLOP/s (a library product
+// What bounds it: 8192 x 2048 x 5632 takes 81 us, 2.3 PFLOP/s (a library product
 // with one scale for each matrix, which needs no such turns: 51 us).  A block of
 // a 128 x 256 tile takes 870 clocks of which the MMAs are 470: the rest is the
 // turn of a TMEM buffer -- commit, wake, read, sums, arrival, wake -- that the
