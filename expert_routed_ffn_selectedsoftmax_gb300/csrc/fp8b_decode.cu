@@ -489,6 +489,9 @@ cudaError_t launch_decode(const void *x_q, long long ldx, const void *w0, const 
     // columns takes 4.1 us split and 3.7 whole at K = 512, 5.1 and 4.5 at 896, 5.2
     // and 6.8 at 2048 (one token 3.6 and 4.3 at 1024); gate/up, with two products a
     // block, of one token and F = 512 5.0 and 4.75 at d = 256, 5.3 and 5.6 at 512.
+    // More tiles than half the SMs stay whole too: two CTAs a tile take 8.4 us for 7.7
+    // at 32 rows x 2048 x 77 tiles, 12.2 for 10.1 at 150 (at K = 6352 and 77 tiles
+    // they would win, 17.7 for 20.3).
     p.split = 1;
     if (2 * tiles <= num_sms && p.KB >= (MODE == GATEUP ? 4 : 8)) {
         const long long each = num_sms / tiles;
