@@ -191,7 +191,7 @@ const char *moe_status_str(int status)
     }
 }
 
-int moe_version(void) { return 102; }
+int moe_version(void) { return 103; }
 
 moe_status moe_route(const void *x, moe_dtype act_dt, int T, int d, const void *w_router,
                      const float *sel_bias, int E, int k, int32_t *topk_idx, float *topk_w,

@@ -143,11 +143,12 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
     // this CTA's blocks of the reduction
     const int kb0 = (int)((long long)p.KB * rank / S), kb1 = (int)((long long)p.KB * (rank + 1) / S);
     volatile int *abort_flag = &c.abort_flag;
+    uint32_t issued = 0;   // blocks this warp has loaded or multiplied
 
     if (warp == 0) {
         // ------------------------------------------------ loads
         uint32_t it = 0;
-        bool ok = p.expire_ns == 0 || __all_sync(0xffffffffu, bar_wait(&c.never, 0, abort_flag, p.expire_ns));
+        bool ok = !expires(p, LOADS) || __all_sync(0xffffffffu, mbar_wait_slow(&c.never, 0, abort_flag, p.expire_ns));
         for (int t = first; t < total && ok; t += stride) {
             const Tile tile = tile_at(c.g, E, t, NT);
             int4 tok = make_int4(0, 0, 0, 0);
@@ -181,12 +182,8 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
         if (!ok) {
             if (lane == 0) flag_status(p.status, kDevTimeout);
             c.abort_flag = 1;
-            // let loads already issued land before the CTA exits
-            for (uint32_t j = (it >= STAGES ? it - STAGES : 0); j < it; ++j) {
-                volatile int no_abort = 0;
-                bar_wait(&c.full[j % STAGES], (j / STAGES) & 1u, &no_abort, 1000000ull);
-            }
         }
+        issued = it;
     } else if (warp == 1) {
         // ------------------------------------------------ multiply
         constexpr uint32_t idesc = idesc_e4m3(M, NT);
@@ -221,17 +218,14 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
         if (!ok) {
             if (leader) flag_status(p.status, kDevTimeout);
             c.abort_flag = 1;
-            if (it > 0) {   // MMAs in flight end before TMEM is freed
-                if (leader) umma_commit(&c.drain);
-                volatile int no_abort = 0;
-                bar_wait(&c.drain, 0, &no_abort);
-            }
         }
+        issued = it;
     } else {
         // ------------------------------------------------ sums and output
         const int ew = warp - 2, quarter = warp & 3, chan = quarter * 32 + lane;
         uint32_t it = 0;
-        bool ok = true;   // once false, no more waits: the remaining rows become NaN
+        // (once false, no more waits: the remaining rows become NaN)
+        bool ok = !expires(p, SUMS) || __all_sync(0xffffffffu, mbar_wait_slow(&c.never, 0, abort_flag, p.expire_ns));
         for (int t = first; t < total; t += stride) {
             const Tile tile = tile_at(c.g, E, t, NT);
             // lane l of every warp holds token l's scales
@@ -286,6 +280,8 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
                 }
             }
             if (!ok) {
+                // (the other roles may have left their loops: this warp reports too)
+                if (lane == 0) flag_status(p.status, kDevTimeout);
                 c.abort_flag = 1;
 #pragma unroll
                 for (int w = 0; w < NW; ++w)
@@ -422,6 +418,20 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
         }
         cluster_sync_all();   // no CTA leaves while a peer reads its shared memory
     } else {
+        __syncthreads();
+    }
+    if (*abort_flag) {
+        // A role gave up, and nothing says that the sums' warps have waited for
+        // what the others issued (which may have left their loops before): loads
+        // land before the CTA exits, MMAs end before TMEM is freed.
+        volatile int no_abort = 0;
+        if (warp == 0) {
+            for (uint32_t j = issued >= STAGES ? issued - STAGES : 0; j < issued; ++j)
+                mbar_wait_slow(&c.full[j % STAGES], (j / STAGES) & 1u, &no_abort, 1000000ull);
+        } else if (warp == 1 && issued > 0) {
+            if (elect_one()) umma_commit(&c.drain);
+            mbar_wait_slow(&c.drain, 0, &no_abort, kTimeoutNs);
+        }
         __syncthreads();
     }
     if (warp == 1) {

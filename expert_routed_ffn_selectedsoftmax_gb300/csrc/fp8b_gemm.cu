@@ -198,13 +198,14 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     __syncthreads();
     auto nth_tile = [&](int i, int t) { return i < kTable ? c.tiles[i] : tile_at(c.g, E, t, BM); };
     volatile int *abort_flag = &c.abort_flag;
+    uint32_t issued = 0;   // blocks this warp has loaded or multiplied
     if (warp < 4) {
         // (inside the branch: the compiler gives each side its own limit)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsAux));
         if (warp == 0) {
             // -------------------------------------------- loads
             uint32_t it = 0;
-            bool ok = !EXPIRE || __all_sync(0xffffffffu, bar_wait(&c.never, 0, abort_flag, p.expire_ns));
+            bool ok = !(EXPIRE && expires(p, LOADS)) || __all_sync(0xffffffffu, bar_wait(&c.never, 0, abort_flag, p.expire_ns));
             for (int t = first, i = 0; t < total && ok; t += stride, ++i) {
                 const Tile tile = nth_tile(i, t);
                 const int boxes = (tile.cnt + ABOX - 1) / ABOX;   // only as many as the tile has rows
@@ -236,12 +237,8 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             if (!ok) {
                 if (lane == 0) flag_status(p.status, kDevTimeout);
                 c.abort_flag = 1;
-                // let loads already issued land before the CTA exits
-                for (uint32_t j = (it >= STAGES ? it - STAGES : 0); j < it; ++j) {
-                    volatile int no_abort = 0;
-                    bar_wait(&c.full[j % STAGES], (j / STAGES) & 1u, &no_abort, 1000000ull);
-                }
             }
+            issued = it;
         } else if (warp == 1 || warp == 2) {
             // -------------------------------------------- multiply
             // Warp 1 multiplies the first column half, warp 2 the second, into
@@ -280,12 +277,8 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             if (!ok) {
                 if (leader) flag_status(p.status, kDevTimeout);
                 c.abort_flag = 1;
-                if (it > 0) {   // MMAs in flight end before TMEM is freed
-                    if (leader) umma_commit(&c.drain[h]);
-                    volatile int no_abort = 0;
-                    bar_wait(&c.drain[h], 0, &no_abort);
-                }
             }
+            issued = it;
         }
     } else {
         // ------------------------------------------------ sums and output
@@ -294,7 +287,8 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         const int row = quarter * 32 + lane;
         uint8_t *stg = smem + kRing + (warp - 4) * kStaging;
         uint32_t it = 0;
-        bool ok = true;   // once false, no more waits: the remaining rows become NaN
+        // (once false, no more waits: the remaining rows become NaN)
+        bool ok = !(EXPIRE && expires(p, SUMS)) || __all_sync(0xffffffffu, bar_wait(&c.never, 0, abort_flag, p.expire_ns));
         Tile next;
         const float *xs = nullptr;
         uint32_t ws = 0;   // place of the weight scales (one for each 16 KB of codes: 32 bits do)
@@ -354,6 +348,8 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             }
             enter(n, t + stride);
             if (!ok) {
+                // (the other roles may have left their loops: this warp reports too)
+                if (lane == 0) flag_status(p.status, kDevTimeout);
                 c.abort_flag = 1;
                 const uint64_t nan2 = 0x7fffffff7fffffffull;
 #pragma unroll
@@ -464,6 +460,20 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     }
 
     __syncthreads();
+    if (*abort_flag) {
+        // A role gave up, and nothing says that the sums' warps have waited for
+        // what the others issued (which may have left their loops before): loads
+        // land before the CTA exits, MMAs end before TMEM is freed.
+        volatile int no_abort = 0;
+        if (warp == 0) {
+            for (uint32_t j = issued >= STAGES ? issued - STAGES : 0; j < issued; ++j)
+                bar_wait(&c.full[j % STAGES], (j / STAGES) & 1u, &no_abort, 1000000ull);
+        } else if ((warp == 1 || warp == 2) && issued > 0) {
+            if (elect_one()) umma_commit(&c.drain[warp - 1]);
+            bar_wait(&c.drain[warp - 1], 0, &no_abort);
+        }
+        __syncthreads();
+    }
     if (warp == 3) {
         __syncwarp();
         tc_fence_after();
@@ -627,10 +637,12 @@ using namespace moe::fp8b;
 
 namespace {
 
+bool hook_limit_ok(uint32_t wait_ns) { return wait_ns > 0 && wait_ns <= 100000000u; }
+
 moe_status grouped_gemm(const void *x_q, const float *x_s, int x_rows, int K, long long ldx, const void *w_q,
                         const float *w_s, int E, int N, const int32_t *offsets, const int32_t *perm_tok, int rows,
                         void *out, moe_dtype out_dt, long long ldo, void *workspace, size_t ws_bytes, uint32_t *status,
-                        uint32_t expire_ns, moe_stream stream)
+                        uint32_t expire_ns, Role expire_role, moe_stream stream)
 {
     bool go;
     const moe_status st = product_args(x_q, x_s, x_rows, K, ldx, w_q, w_s, E, N, offsets, perm_tok, rows, status,
@@ -641,6 +653,7 @@ moe_status grouped_gemm(const void *x_q, const float *x_s, int x_rows, int K, lo
     if (!out || !aligned_to(out, out_dt == MOE_F32 ? 4 : 2)) return MOE_ERR_INVALID_ARG;
     Params p = params_of(x_s, x_rows, K, w_s, nullptr, E, N, offsets, perm_tok, rows, status);
     p.expire_ns = expire_ns;
+    p.expire_role = expire_role;
     p.out = out; p.ldo = ldo; p.out_f32 = out_dt == MOE_F32;
     p.out_vec = ldo % (out_dt == MOE_F32 ? 4 : 8) == 0 && aligned_to(out, 16);
     const cudaError_t e = launch_product<PRODUCT>(x_q, ldx, w_q, nullptr, p, workspace, static_cast<cudaStream_t>(stream));
@@ -663,7 +676,7 @@ moe_status moe_grouped_gemm_fp8b(const void *x_q, const float *x_s, int x_rows, 
                                  void *workspace, size_t ws_bytes, uint32_t *status, moe_stream stream)
 {
     return grouped_gemm(x_q, x_s, x_rows, K, ldx, w_q, w_s, E, N, offsets, perm_tok, rows, out, out_dt, ldo, workspace,
-                        ws_bytes, status, 0, stream);
+                        ws_bytes, status, 0, LOADS, stream);
 }
 
 moe_status moe_grouped_gemm_fp8b_expire_wait(const void *x_q, const float *x_s, int x_rows, int K, long long ldx,
@@ -672,9 +685,20 @@ moe_status moe_grouped_gemm_fp8b_expire_wait(const void *x_q, const float *x_s, 
                                              long long ldo, void *workspace, size_t ws_bytes, uint32_t *status,
                                              uint32_t wait_ns, moe_stream stream)
 {
-    if (wait_ns == 0 || wait_ns > 100000000u) return MOE_ERR_INVALID_ARG;
+    if (!hook_limit_ok(wait_ns)) return MOE_ERR_INVALID_ARG;
     return grouped_gemm(x_q, x_s, x_rows, K, ldx, w_q, w_s, E, N, offsets, perm_tok, rows, out, out_dt, ldo, workspace,
-                        ws_bytes, status, wait_ns, stream);
+                        ws_bytes, status, wait_ns, LOADS, stream);
+}
+
+moe_status moe_grouped_gemm_fp8b_expire_sums(const void *x_q, const float *x_s, int x_rows, int K, long long ldx,
+                                             const void *w_q, const float *w_s, int E, int N, const int32_t *offsets,
+                                             const int32_t *perm_tok, int rows, void *out, moe_dtype out_dt,
+                                             long long ldo, void *workspace, size_t ws_bytes, uint32_t *status,
+                                             uint32_t wait_ns, moe_stream stream)
+{
+    if (!hook_limit_ok(wait_ns)) return MOE_ERR_INVALID_ARG;
+    return grouped_gemm(x_q, x_s, x_rows, K, ldx, w_q, w_s, E, N, offsets, perm_tok, rows, out, out_dt, ldo, workspace,
+                        ws_bytes, status, wait_ns, SUMS, stream);
 }
 
 moe_status moe_gemm_fp8b(const void *x_q, const float *x_s, int T, int K, long long ldx, const void *w_q,

@@ -18,6 +18,7 @@ namespace fp8b {
 using namespace sm100;
 
 enum Mode { PRODUCT = 0, GATEUP = 1 };
+enum Role { LOADS = 0, SUMS = 1 };   // whose first wait a test hook lets expire
 
 struct Params {
     const float *x_s;         // [x_rows, KB]
@@ -32,7 +33,8 @@ struct Params {
     uint8_t *h_q;             // GATEUP: [rows, N] codes, [rows, NB] scales
     float *h_s;
     uint32_t *status;
-    uint32_t expire_ns;       // > 0: the loading warp's first wait gives up after this long (test hook)
+    uint32_t expire_ns;       // > 0: the first wait of `expire_role` gives up after this long (test hook)
+    int expire_role;
     int split;                // CTAs per cluster (fp8b_decode.cu)
 };
 
@@ -91,6 +93,9 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatil
         }
     }
 }
+
+// The test hook: whether this role's first wait is to give up.
+__device__ __forceinline__ bool expires(const Params &p, Role role) { return p.expire_ns && p.expire_role == role; }
 
 __device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi)
 {

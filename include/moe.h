@@ -603,6 +603,16 @@ MOE_API moe_status moe_grouped_gemm_fp8b_expire_wait(
     uint32_t wait_ns, moe_stream stream);
 
 /*
+ * moe_grouped_gemm_fp8b_expire_sums -- the same with the first wait of the warps
+ * that sum and write the output: their loads and products run meanwhile.
+ */
+MOE_API moe_status moe_grouped_gemm_fp8b_expire_sums(
+    const void *x_q, const float *x_s, int x_rows, int K, long long ldx, const void *w_q,
+    const float *w_s, int E, int N, const int32_t *offsets, const int32_t *perm_tok, int rows,
+    void *out, moe_dtype out_dt, long long ldo, void *workspace, size_t ws_bytes, uint32_t *status,
+    uint32_t wait_ns, moe_stream stream);
+
+/*
  * moe_check_noalloc -- moe_check for moe_forward_noalloc: wait for `stream`,
  * then read the status word the most recent moe_forward_noalloc on the
  * current device left in the library's static scratch (MOE_OK,

@@ -603,6 +603,43 @@ def test_expired_wait_is_reported_and_not_silent(moe, T, E, K, N):
         check_product(y[a:b], xv[a:b], wv[e], K)
 
 
+# split over a cluster, few rows, tiled; one or two blocks of K for a CTA, so that
+# its loads and products are all issued before the sums give up, and more
+SUMS = [(1, 1, 1024, 256), (40, 24, 256, 512), (3000, 3, 256, 1040), (1, 1, 2816, 256), (40, 24, 1024, 512), (3000, 3, 1040, 1040)]
+
+
+@pytest.mark.parametrize("T,E,K,N", SUMS)
+def test_expired_sums_are_reported(moe, T, E, K, N):
+    """The wait of the summing warps gives up while every load and product goes
+    on: the status word reports it too, also where the other warps have left
+    their loops by then; rows are NaN, the rest is left, the next call is right."""
+    import ctypes
+    L = moe.load_library()
+    xq, xs = pair(T, K)
+    wq, ws = pair(N, K, seed=4, block_rows=128, lead=(E,))
+    off = torch.linspace(0, T, E + 1, device=DEV).int()
+    off[-1] = max(T - 1, 1)
+    status = torch.zeros(64, dtype=torch.int32, device=DEV)
+    out = torch.full((T, N), 3.0, device=DEV)
+    p = lambda t: ctypes.c_void_p(t.data_ptr())
+    st = L.moe_grouped_gemm_fp8b_expire_sums(p(xq), p(xs), T, K, K, p(wq), p(ws), E, N, p(off), None, T, p(out), 0, N,
+                                             None, 0, p(status), 1_000_000,
+                                             ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert st == 0
+    with pytest.raises(moe.MoeError) as e:
+        moe.moe_check(status)
+    assert e.value.status == 5      # MOE_ERR_TIMEOUT
+    n = int(off[-1])
+    assert bool(out[:n].isnan().all()) and bool((out[n:] == 3).all())
+    status.zero_()
+    y = moe.moe_grouped_gemm_fp8b(xq, xs, wq, ws, off, out_dtype=torch.float32, status=status)
+    assert moe.moe_check(status) == 0
+    xv, wv = value(xq, xs, 1), value(wq, ws, 128)
+    for e in range(E):
+        a, b = int(off[e]), int(off[e + 1])
+        check_product(y[a:b], xv[a:b], wv[e], K)
+
+
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 @pytest.mark.parametrize("N", [4, 8, 16, 40])
 def test_narrow_outputs_of_many_rows(moe, N, out):
