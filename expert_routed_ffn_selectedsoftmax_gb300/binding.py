@@ -35,7 +35,8 @@ EXPORTS = ("moe_status_str", "moe_version", "moe_route", "moe_route_scored", "mo
            "moe_workspace_views", "moe_forward_expire_wait", "moe_check", "moe_check_noalloc",
            "moe_quant_fp8b", "moe_norm_fp8b", "moe_gemm_fp8b", "moe_grouped_gemm_fp8b",
            "moe_gate_up_fp8b", "moe_fp8b_workspace_size", "moe_grouped_gemm_fp8b_expire_wait",
-           "moe_grouped_gemm_fp8b_expire_sums")
+           "moe_grouped_gemm_fp8b_expire_sums", "moe_gate_up_fp8b_expire_wait",
+           "moe_gate_up_fp8b_expire_sums")
 
 _lib = None
 _debug_lib = None
@@ -144,6 +145,10 @@ def _declare(L):
                                         sz, vp, vp]
     for hook in (L.moe_grouped_gemm_fp8b_expire_wait, L.moe_grouped_gemm_fp8b_expire_sums):
         hook.argtypes = [vp, vp, i, i, ll, vp, vp, i, i, vp, vp, i, vp, i, ll, vp, sz, vp, ctypes.c_uint32, vp]
+        hook.restype = i
+    for hook in (L.moe_gate_up_fp8b_expire_wait, L.moe_gate_up_fp8b_expire_sums):
+        hook.argtypes = [vp, vp, i, i, ll, vp, vp, vp, vp, i, i, vp, vp, i, vp, vp, vp, sz, vp,
+                         ctypes.c_uint32, vp]
         hook.restype = i
     L.moe_fp8b_workspace_size.argtypes = [i, i]
     L.moe_fp8b_workspace_size.restype = sz

@@ -585,8 +585,7 @@ cudaError_t launch_product(const void *x_q, long long ldx, const void *w0, const
     p.out_tma = MODE == PRODUCT && p.out_vec && p.N % (p.out_f32 ? 4 : 8) == 0;
     if (!p.out_tma) mout = mx;
     else if (!out_map(&mout, p)) return cudaErrorInvalidValue;
-    if (MODE == PRODUCT && p.expire_ns)
-        return launch_kernel<PRODUCT, true>(mx, mw0, mw1, mout, p, tiles, num_sms, stream);
+    if (p.expire_ns) return launch_kernel<MODE, true>(mx, mw0, mw1, mout, p, tiles, num_sms, stream);
     return launch_kernel<MODE, false>(mx, mw0, mw1, mout, p, tiles, num_sms, stream);
 }
 
@@ -660,6 +659,28 @@ moe_status grouped_gemm(const void *x_q, const float *x_s, int x_rows, int K, lo
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+moe_status gate_up(const void *x_q, const float *x_s, int x_rows, int d, long long ldx, const void *wg_q,
+                   const float *wg_s, const void *wu_q, const float *wu_s, int E, int F, const int32_t *offsets,
+                   const int32_t *perm_tok, int rows, void *h_q, float *h_s, void *workspace, size_t ws_bytes,
+                   uint32_t *status, uint32_t expire_ns, Role expire_role, moe_stream stream)
+{
+    bool go;
+    const moe_status st = product_args(x_q, x_s, x_rows, d, ldx, wg_q, wg_s, E, F, offsets, perm_tok, rows, status,
+                                        workspace, ws_bytes, &go);
+    if (st != MOE_OK) return st;
+    if (F % 16) return MOE_ERR_INVALID_ARG;
+    if (!go) return MOE_OK;
+    if (!wu_q || !wu_s || !h_q || !h_s) return MOE_ERR_INVALID_ARG;
+    if (!aligned_to(wu_q, 16) || !aligned_to(wu_s, 4) || !aligned_to(h_q, 16) || !aligned_to(h_s, 4))
+        return MOE_ERR_INVALID_ARG;
+    Params p = params_of(x_s, x_rows, d, wg_s, wu_s, E, F, offsets, perm_tok, rows, status);
+    p.expire_ns = expire_ns;
+    p.expire_role = expire_role;
+    p.h_q = static_cast<uint8_t *>(h_q); p.h_s = h_s;
+    const cudaError_t e = launch_product<GATEUP>(x_q, ldx, wg_q, wu_q, p, workspace, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -714,19 +735,30 @@ moe_status moe_gate_up_fp8b(const void *x_q, const float *x_s, int x_rows, int d
                             const int32_t *offsets, const int32_t *perm_tok, int rows, void *h_q, float *h_s,
                             void *workspace, size_t ws_bytes, uint32_t *status, moe_stream stream)
 {
-    bool go;
-    moe_status st = product_args(x_q, x_s, x_rows, d, ldx, wg_q, wg_s, E, F, offsets, perm_tok, rows, status, workspace,
-                                 ws_bytes, &go);
-    if (st != MOE_OK) return st;
-    if (F % 16) return MOE_ERR_INVALID_ARG;
-    if (!go) return MOE_OK;
-    if (!wu_q || !wu_s || !h_q || !h_s) return MOE_ERR_INVALID_ARG;
-    if (!aligned_to(wu_q, 16) || !aligned_to(wu_s, 4) || !aligned_to(h_q, 16) || !aligned_to(h_s, 4))
-        return MOE_ERR_INVALID_ARG;
-    Params p = params_of(x_s, x_rows, d, wg_s, wu_s, E, F, offsets, perm_tok, rows, status);
-    p.h_q = static_cast<uint8_t *>(h_q); p.h_s = h_s;
-    const cudaError_t e = launch_product<GATEUP>(x_q, ldx, wg_q, wu_q, p, workspace, static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return gate_up(x_q, x_s, x_rows, d, ldx, wg_q, wg_s, wu_q, wu_s, E, F, offsets, perm_tok, rows, h_q, h_s, workspace,
+                   ws_bytes, status, 0, LOADS, stream);
+}
+
+moe_status moe_gate_up_fp8b_expire_wait(const void *x_q, const float *x_s, int x_rows, int d, long long ldx,
+                                        const void *wg_q, const float *wg_s, const void *wu_q, const float *wu_s, int E,
+                                        int F, const int32_t *offsets, const int32_t *perm_tok, int rows, void *h_q,
+                                        float *h_s, void *workspace, size_t ws_bytes, uint32_t *status,
+                                        uint32_t wait_ns, moe_stream stream)
+{
+    if (!hook_limit_ok(wait_ns)) return MOE_ERR_INVALID_ARG;
+    return gate_up(x_q, x_s, x_rows, d, ldx, wg_q, wg_s, wu_q, wu_s, E, F, offsets, perm_tok, rows, h_q, h_s, workspace,
+                   ws_bytes, status, wait_ns, LOADS, stream);
+}
+
+moe_status moe_gate_up_fp8b_expire_sums(const void *x_q, const float *x_s, int x_rows, int d, long long ldx,
+                                        const void *wg_q, const float *wg_s, const void *wu_q, const float *wu_s, int E,
+                                        int F, const int32_t *offsets, const int32_t *perm_tok, int rows, void *h_q,
+                                        float *h_s, void *workspace, size_t ws_bytes, uint32_t *status,
+                                        uint32_t wait_ns, moe_stream stream)
+{
+    if (!hook_limit_ok(wait_ns)) return MOE_ERR_INVALID_ARG;
+    return gate_up(x_q, x_s, x_rows, d, ldx, wg_q, wg_s, wu_q, wu_s, E, F, offsets, perm_tok, rows, h_q, h_s, workspace,
+                   ws_bytes, status, wait_ns, SUMS, stream);
 }
 
 }  // extern "C"

@@ -613,6 +613,22 @@ MOE_API moe_status moe_grouped_gemm_fp8b_expire_sums(
     uint32_t wait_ns, moe_stream stream);
 
 /*
+ * moe_gate_up_fp8b_expire_wait, moe_gate_up_fp8b_expire_sums -- the two hooks for
+ * moe_gate_up_fp8b: every row of every group becomes NaN codes (0x7F) with NaN
+ * scales.
+ */
+MOE_API moe_status moe_gate_up_fp8b_expire_wait(
+    const void *x_q, const float *x_s, int x_rows, int d, long long ldx, const void *wg_q,
+    const float *wg_s, const void *wu_q, const float *wu_s, int E, int F, const int32_t *offsets,
+    const int32_t *perm_tok, int rows, void *h_q, float *h_s, void *workspace, size_t ws_bytes,
+    uint32_t *status, uint32_t wait_ns, moe_stream stream);
+MOE_API moe_status moe_gate_up_fp8b_expire_sums(
+    const void *x_q, const float *x_s, int x_rows, int d, long long ldx, const void *wg_q,
+    const float *wg_s, const void *wu_q, const float *wu_s, int E, int F, const int32_t *offsets,
+    const int32_t *perm_tok, int rows, void *h_q, float *h_s, void *workspace, size_t ws_bytes,
+    uint32_t *status, uint32_t wait_ns, moe_stream stream);
+
+/*
  * moe_check_noalloc -- moe_check for moe_forward_noalloc: wait for `stream`,
  * then read the status word the most recent moe_forward_noalloc on the
  * current device left in the library's static scratch (MOE_OK,

@@ -640,6 +640,42 @@ def test_expired_sums_are_reported(moe, T, E, K, N):
         check_product(y[a:b], xv[a:b], wv[e], K)
 
 
+@pytest.mark.parametrize("who", ["wait", "sums"])
+@pytest.mark.parametrize("T,E,d,F", [(1, 1, 512, 256), (40, 24, 256, 272), (3000, 3, 256, 400), (1, 1, 2816, 256),
+                                     (40, 24, 1024, 400), (3000, 3, 1040, 400)])
+def test_expired_gate_up(moe, T, E, d, F, who):
+    """The same for gate/up (split over a cluster, few rows, tiled), for the loads'
+    wait and the sums': NaN codes with NaN scales, reported, the rest as it was."""
+    import ctypes
+    L = moe.load_library()
+    xq, xs = pair(T, d)
+    (gq, gs), (uq, us) = (quant(rand(E, F, d, seed=s, sd=d ** -0.5), 128) for s in (1, 2))
+    off = torch.linspace(0, T, E + 1, device=DEV).int()
+    off[-1] = max(T - 1, 1)
+    status = torch.zeros(64, dtype=torch.int32, device=DEV)
+    hq = torch.full((T, F), 5, dtype=torch.uint8, device=DEV)
+    hs = torch.full((T, blocks(F)), 9.0, device=DEV)
+    p = lambda t: ctypes.c_void_p(t.data_ptr())
+    hook = getattr(L, f"moe_gate_up_fp8b_expire_{who}")
+    assert hook(p(xq), p(xs), T, d, d, p(gq), p(gs), p(uq), p(us), E, F, p(off), None, T, p(hq), p(hs), None, 0,
+                p(status), 1_000_000, ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)) == 0
+    with pytest.raises(moe.MoeError) as e:
+        moe.moe_check(status)
+    assert e.value.status == 5      # MOE_ERR_TIMEOUT
+    n = int(off[-1])
+    assert bool((hq[:n] == 0x7F).all()) and bool(hs[:n].isnan().all())
+    assert bool((hq[n:] == 5).all()) and bool((hs[n:] == 9).all())
+    status.zero_()
+    hq, hs = moe.moe_gate_up_fp8b(xq, xs, gq, gs, uq, us, offsets=off, status=status)
+    assert moe.moe_check(status) == 0
+    xv, gv, uv = value(xq, xs, 1), value(gq, gs, 128), value(uq, us, 128)
+    for e in range(E):
+        a, b = int(off[e]), int(off[e + 1])
+        if a < b:
+            h, err = swiglu_ref(xv[a:b], gv[e], uv[e], d)
+            check_codes(hq[a:b], hs[a:b], h, err)
+
+
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 @pytest.mark.parametrize("N", [4, 8, 16, 40])
 def test_narrow_outputs_of_many_rows(moe, N, out):

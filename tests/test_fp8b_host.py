@@ -99,10 +99,13 @@ def test_product_arguments(lib):
 
 
 def test_hook_arguments(lib):
-    """The wait's limit of the hook on the sums: 1 ns to 100 ms."""
+    """The wait's limit of the hooks: 1 ns to 100 ms."""
     for ns in (0, 100_000_001):
         assert lib.moe_grouped_gemm_fp8b_expire_sums(FAKE, FAKE, 8, 256, 256, FAKE, FAKE, 4, 64, FAKE, None, 8, FAKE, F32,
                                                      64, None, 0, None, ns, None) == I
+        for hook in (lib.moe_gate_up_fp8b_expire_wait, lib.moe_gate_up_fp8b_expire_sums):
+            assert hook(FAKE, FAKE, 8, 256, 256, FAKE, FAKE, FAKE, FAKE, 4, 64, FAKE, None, 8, FAKE, FAKE, None, 0, None,
+                        ns, None) == I
 
 
 def test_binding_refuses_wrong_pairs():
