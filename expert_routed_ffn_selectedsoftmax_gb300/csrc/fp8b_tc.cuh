@@ -110,8 +110,13 @@ __device__ __forceinline__ void fma2(uint64_t &acc, uint64_t a, uint64_t b)
 {
     asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
 }
-// SwiGLU with the fast exponential and an approximate divide (relative error
-// ~1e-6, far below the codes' 2^-4; for g < -87, 1 + e^-g overflows and h is 0)
+// SwiGLU with the fast exponential and an approximate divide.  __expf(-g) is off
+// by at most 2 + 1.173 |g| units in the last place, the sum, the divide (2 units)
+// and the product by 3 more, so h is off by (5 + 1.18 |g|) 2^-23 of itself: 7e-7
+// at g = 1, 1.3e-5 at g = -87, against the codes' 2^-4 (the scale, in fp32, is off
+// by as much).  From g = -87.4 down the divisor is above 2^126, where __fdividef
+// gives 0 (and infinity below -88.8, which gives 0 too): |silu(g)| < |g| 2^-126
+// counts as 0.  g = -inf gives NaN, as -inf * 0 in the definition does.
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)

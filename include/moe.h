@@ -544,7 +544,8 @@ MOE_API moe_status moe_grouped_gemm_fp8b(const void *x_q, const float *x_s, int 
  * moe_gate_up_fp8b -- both products of a SwiGLU expert and its h, quantised:
  *     h[r] = SiLU(W_g[e] x[perm_tok[r]]) * (W_u[e] x[perm_tok[r]])
  *   h_q [rows, F] codes and h_s [rows, ceil(F/128)] out, from the unrounded
- *   fp32 h.  wg_q, wu_q [E, F, d] with scales [E, ceil(F/128), ceil(d/128)];
+ *   fp32 h.  SiLU(g) is within (5 + 1.18 |g|) 2^-23 of itself, and 0 for g
+ *   below about -87.  wg_q, wu_q [E, F, d] with scales [E, ceil(F/128), ceil(d/128)];
  *   F a multiple of 16.  Groups, perm_tok, rows and workspace as moe_grouped_gemm_fp8b
  *   (E == 1 with offsets NULL is the dense layer's).
  */

@@ -476,6 +476,62 @@ def test_gate_up_dense(moe, T):
     check_codes(hq, hs, h, err)
 
 
+# rows, d of the few-rows kernel, whole and split over a cluster, and of the tiled one
+GATE_RANGE = [(201, 256), (201, 640), (5025, 256)]
+
+
+def one_column(sx, d, F, su):
+    """Operands whose sums are exact: x has +-1 in column 200 and |sx| as that
+    block's scale, the gate's weights are 1 there, the up weights small codes times
+    su: g = sx in every column, u = sx * code * su."""
+    rows = sx.shape[0]
+    xq = torch.zeros(rows, d, device=DEV)
+    xq[:, 200] = torch.where(sx < 0, -1.0, 1.0)
+    xs = torch.ones(rows, blocks(d), device=DEV)
+    xs[:, 1] = sx.abs()
+    gq, uq = torch.zeros(F, d, device=DEV), torch.zeros(F, d, device=DEV)
+    gq[:, 200] = 1.0
+    uq[:, 200] = 1 + (torch.arange(F, device=DEV) % 29).div(4, rounding_mode="floor") / 4
+    one = torch.ones(blocks(F), blocks(d), device=DEV)
+    return (xq.to(F8), xs, gq.to(F8), one, uq.to(F8), one * su), uq[:, 200].double() * su
+
+
+@pytest.mark.parametrize("rows,d", GATE_RANGE)
+def test_gate_up_over_the_gate_sums_range(moe, rows, d):
+    """g from -100 to 100 on exact sums.  Off by __expf's 2 + 1.173 |g| units in
+    the last place (2^-23), 2 of the divide and half a unit each of the sum and
+    the product: (5 + 1.18 |g|) 2^-23 |h|; |silu| below |g| 2^-125 may count as 0.
+    The up sums are large, so that h at g = -87 is far from the smallest numbers."""
+    F, g = 272, torch.linspace(-100, 100, 201, device=DEV).repeat(rows // 201)
+    args, up = one_column(g, d, F, 2.0 ** 40)
+    hq, hs = moe.moe_gate_up_fp8b(*args)
+    g = g.double()[:, None]
+    u = g * up
+    h = g * torch.sigmoid(g) * u
+    check_codes(hq, hs, h, h.abs() * (5 + 1.18 * g.abs()) * 2.0 ** -23 + g.abs() * u.abs() * 2.0 ** -125)
+    below = (g[:, 0] < -89) | (g[:, 0] == 0)
+    assert not hs[below].any() and not hq[below].float().any() and bool((hs[(g[:, 0] > -87) & ~below] > 0).all())
+
+
+@pytest.mark.parametrize("rows,d", GATE_RANGE)
+def test_gate_up_of_non_finite_gate_sums(moe, rows, d):
+    """Gate sums that are NaN, infinite or overflow: NaN codes with NaN scales in
+    their rows, as the definition has it; the other rows keep theirs."""
+    F = 272
+    g = torch.linspace(-20, 20, 201, device=DEV).repeat(rows // 201)
+    args, _ = one_column(g, d, F, 1.0)
+    hq, hs = moe.moe_gate_up_fp8b(*args)
+    bad = [0, 3, 40, 77, rows - 1]
+    for r, v in zip(bad, (float("nan"), float("inf"), float("-inf"), 3e38, -3e38)):
+        args[0][r, 200] = -2.0 if v < 0 else 2.0
+        args[1][r, 1] = abs(v)
+    bq, bs = moe.moe_gate_up_fp8b(*args)
+    keep = torch.ones(rows, dtype=torch.bool, device=DEV)
+    keep[bad] = False
+    assert torch.equal(bits(bq)[keep], bits(hq)[keep]) and torch.equal(bs[keep], hs[keep])
+    assert bool(bs[~keep].isnan().all()) and bool(bq[~keep].float().isnan().all())
+
+
 @pytest.mark.parametrize("T,E", [(6, 4), (400, 4), (3000, 7)])
 def test_padded_batch_leaves_the_rest(moe, T, E):
     """Groups that do not start at 0 and end before the last row: rows outside
