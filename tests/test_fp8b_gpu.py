@@ -19,6 +19,8 @@ Tolerances, derived before the first run:
                           y: the mean of squares, root, divide and two products
                           together under 2^-18 relative.
 """
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -745,6 +747,160 @@ def test_narrow_outputs_of_many_rows(moe, N, out):
     assert bool((wide[0] == 3).all()) and bool((wide[-1] == 3).all())
 
 
+# ------------------------------------- which kernel, and the tiled one's values
+
+class KernelNode(ctypes.Structure):          # CUDA_KERNEL_NODE_PARAMS_v2
+    _fields_ = [("func", ctypes.c_void_p), ("dims", ctypes.c_uint * 7), ("params", ctypes.c_void_p),
+                ("extra", ctypes.c_void_p), ("kern", ctypes.c_void_p), ("ctx", ctypes.c_void_p)]
+
+
+def kernel_of(call):
+    """"tiled", "few rows" or "split": the product kernel that `call` launches, by
+    the names of the kernels in its captured graph."""
+    call()                                   # (set-up of a kernel's first launch is not captured)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(graph):
+        call()
+    cu, raw, n = ctypes.CDLL("libcuda.so.1"), ctypes.c_void_p(graph.raw_cuda_graph()), ctypes.c_size_t(0)
+    assert cu.cuGraphGetNodes(raw, None, ctypes.byref(n)) == 0
+    nodes = (ctypes.c_void_p * n.value)()
+    assert cu.cuGraphGetNodes(raw, nodes, ctypes.byref(n)) == 0
+    names = []
+    for node in nodes:
+        kind, p, name = ctypes.c_int(-1), KernelNode(), ctypes.c_char_p()
+        assert cu.cuGraphNodeGetType(ctypes.c_void_p(node), ctypes.byref(kind)) == 0
+        if kind.value != 0:                  # CU_GRAPH_NODE_TYPE_KERNEL
+            continue
+        assert cu.cuGraphKernelNodeGetParams_v2(ctypes.c_void_p(node), ctypes.byref(p)) == 0
+        get = (cu.cuFuncGetName, p.func) if p.func else (cu.cuKernelGetName, p.kern)
+        assert get[0](ctypes.byref(name), ctypes.c_void_p(get[1])) == 0
+        names.append(name.value.decode())
+    if any("product_kernel" in m for m in names):
+        return "tiled"
+    few = [m for m in names if "decode_kernel" in m]
+    assert len(few) == 1, names
+    return "split" if "decode_kernelILi0ELb1E" in few[0] or "decode_kernelILi1ELb1E" in few[0] else "few rows"
+
+
+def by_rule(rows, E, N, K, gate_up):
+    """The rule for the product's kernel (fp8b_decode.cu) on this device."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    experts = min(E, rows)
+    tiles = ((rows - experts) // 32 + experts) * blocks(N)
+    if rows > 16 * experts and tiles > sms:
+        return "tiled"
+    return "split" if 2 * tiles <= sms and blocks(K) >= (4 if gate_up else 8) else "few rows"
+
+
+TILED_GEMM = [(2500, 2816, 384), (4000, 1040, 1000), (3000, 272, 130), (5000, 144, 7), (2600, 640, 2050)]
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("T,K,N", TILED_GEMM)
+def test_gemm_tiled(moe, out, T, K, N):
+    """Sizes above the few-rows rule: long reductions, ragged last blocks."""
+    xq, xs = pair(T, K)
+    wq, ws = pair(N, K, seed=5, block_rows=128)
+    call = lambda: moe.moe_gemm_fp8b(xq, xs, wq, ws, out_dtype=DT[out])
+    assert kernel_of(call) == "tiled" == by_rule(T, 1, N, K, False)
+    y = call()
+    check_product(y, value(xq, xs, 1), value(wq, ws, 128), K)
+    assert torch.equal(y, call())
+
+
+@pytest.mark.parametrize("T", [254 * 20, 254 * 33 + 5])
+def test_gemm_tiled_every_code(moe, T):
+    """Every finite code of both signs on both sides through the tiled kernel."""
+    codes = torch.tensor([c for c in range(256) if c & 0x7F != 0x7F], dtype=torch.uint8, device=DEV)   # 254
+    K = 256
+    left = codes.repeat(-(-T // 254))[:T]
+    xq, wq = torch.zeros(T, K, dtype=torch.uint8, device=DEV), torch.zeros(254, K, dtype=torch.uint8, device=DEV)
+    xq[:, 200], wq[:, 200] = left, codes
+    xs, ws = torch.ones(T, 2, device=DEV), torch.ones(2, 2, device=DEV)
+    call = lambda: moe.moe_gemm_fp8b(xq, xs, wq, ws, out_dtype=torch.float32)
+    assert kernel_of(call) == "tiled" == by_rule(T, 1, 254, K, False)
+    assert torch.equal(call().double(), left.view(F8).double()[:, None] * codes.view(F8).double()[None, :])
+
+
+@pytest.mark.parametrize("T", [5000, 8191])
+def test_gemm_tiled_scales_act_on_their_own_block(moe, T):
+    """Scales of very different size per block of K, of N and per row; a zero and a
+    NaN scale stay in their rows and columns, in the tiled kernel."""
+    K, N = 5 * 128, 3 * 128 + 16
+    xq, xs = pair(T, K)
+    wq, ws = pair(N, K, seed=3, block_rows=128)
+    xs = xs * 4.0 ** torch.randint(-8, 8, xs.shape, device=DEV)
+    ws = ws * 4.0 ** torch.randint(-8, 8, ws.shape, device=DEV)
+    xs[7] = 0
+    call = lambda: moe.moe_gemm_fp8b(xq, xs, wq, ws, out_dtype=torch.float32)
+    assert kernel_of(call) == "tiled" == by_rule(T, 1, N, K, False)
+    check_product(call(), value(xq, xs, 1), value(wq, ws, 128), K)
+    xs[9, 2], xs[T - 1, 4], ws[1, 3] = float("nan"), float("nan"), float("nan")
+    bad = call().isnan()
+    want = torch.zeros_like(bad)
+    want[9] = want[T - 1] = True
+    want[:, 128:256] = True
+    assert torch.equal(bad, want)
+
+
+@pytest.mark.parametrize("T,d,F", [(3000, 272, 400), (3000, 1040, 384), (2700, 2816, 272), (6000, 144, 16)])
+def test_gate_up_dense_tiled(moe, T, d, F):
+    """The dense layer's call (no offsets) above the few-rows rule, with ragged last
+    blocks of d and of F."""
+    xq, xs = pair(T, d)
+    (gq, gs), (uq, us) = (quant(rand(F, d, seed=s, sd=d ** -0.5), 128) for s in (1, 2))
+    call = lambda: moe.moe_gate_up_fp8b(xq, xs, gq, gs, uq, us)
+    assert kernel_of(call) == "tiled" == by_rule(T, 1, F, d, True)
+    hq, hs = call()
+    h, err = swiglu_ref(value(xq, xs, 1), value(gq, gs, 128), value(uq, us, 128), d)
+    check_codes(hq, hs, h, err)
+
+
+TILED_GROUPS = [(3000, 3, 1, 272, 400, 2.0), (2600, 8, 2, 400, 272, 1.0), (5000, 16, 1, 640, 384, 0.5), (4000, 64, 4, 144, 80, 1.0)]
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("T,E,k,K,N,skew", TILED_GROUPS)
+def test_grouped_tiled(moe, T, E, k, K, N, skew, gather):
+    """The grouped products and gate/up above the few-rows rule, ragged last blocks."""
+    off, perm, _ = grouping(T, E, k, seed=T + E, skew=skew)
+    rows = T * k
+    xq, xs = pair(T if gather else rows, K)
+    (gq, gs), (uq, us) = (quant(rand(E, N, K, seed=s, sd=K ** -0.5), 128) for s in (11, 12))
+    p = perm if gather else None
+    product = lambda: moe.moe_grouped_gemm_fp8b(xq, xs, gq, gs, off, perm_tok=p, out_dtype=torch.float32)
+    gate_up = lambda: moe.moe_gate_up_fp8b(xq, xs, gq, gs, uq, us, offsets=off, perm_tok=p)
+    assert kernel_of(product) == kernel_of(gate_up) == "tiled" == by_rule(rows, E, N, K, False)
+    y, (hq, hs) = product(), gate_up()
+    xv = value(xq, xs, 1)
+    xv = xv[perm.long()] if gather else xv
+    gv, uv = value(gq, gs, 128), value(uq, us, 128)
+    for e in range(E):
+        a, b = int(off[e]), int(off[e + 1])
+        if a < b:
+            check_product(y[a:b], xv[a:b], gv[e], K)
+            h, err = swiglu_ref(xv[a:b], gv[e], uv[e], K)
+            check_codes(hq[a:b], hs[a:b], h, err)
+
+
+@pytest.mark.parametrize("T,E,K,N,gate_up,kind", [
+    (1, 1, 1024, 256, False, "split"), (16, 1, 912, 1024, False, "split"), (16, 1, 896, 1024, False, "few rows"),
+    (40, 24, 640, 512, False, "few rows"), (300, 1, 2816, 384, False, "split"), (2500, 1, 2816, 384, False, "tiled"),
+    (1, 1, 512, 256, True, "split"), (16, 1, 384, 400, True, "few rows"), (300, 1, 256, 400, True, "few rows"),
+    (3000, 1, 256, 400, True, "tiled")])
+def test_which_kernel(moe, T, E, K, N, gate_up, kind):
+    """The kernel that cases of these tests are meant for, by the rule and as launched."""
+    off = torch.linspace(0, T, E + 1, device=DEV).int()
+    xq, xs = pair(T, K)
+    wq, ws = pair(N, K, seed=4, block_rows=128, lead=(E,))
+    if gate_up:
+        call = lambda: moe.moe_gate_up_fp8b(xq, xs, wq, ws, wq, ws, offsets=off)
+    else:
+        call = lambda: moe.moe_grouped_gemm_fp8b(xq, xs, wq, ws, off)
+    assert kernel_of(call) == kind == by_rule(T, E, N, K, gate_up)
+
+
 # --------------------------------------------------- streams, graphs, chains
 
 def layer(E, d, F, seed):
@@ -796,6 +952,11 @@ def test_layers_in_a_row(moe, T, E, k, d, F):
                 check_product(m["y"][a:b], hv[a:b], value(*(t[e] for t in w["d"]), 128), F)
         prev = m
     check_norm(prev["resid"], layers[0]["norm"], 1e-6, (resid, normed, q, s), prev["y"], prev["topk_w"], prev["inv"])
+
+
+def test_layers_of_many_rows(moe):
+    """Two layers whose products all take the tiled kernel, rows gathered."""
+    test_layers_in_a_row(moe, 3000, 8, 2, 272, 400)
 
 
 @pytest.mark.parametrize("T", [48, 1500])     # (the second gathers into a workspace)
