@@ -5,6 +5,10 @@ _fp8b.so beside it.
 nvcc, one -gencode for sm_103a, translation units compiled in parallel (the
 module by the host compiler against PyTorch's headers), no cmake.  Rebuilds only
 when a source or header is newer than what was built.
+
+The library is all that the C ABI needs.  Where the module cannot be built (no
+PyTorch or Python headers), build() says so in a warning and the library stands;
+only the calls that go through the module need it, and they raise without it.
 """
 from __future__ import annotations
 
@@ -14,6 +18,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -47,16 +52,20 @@ def sources():
 
 
 def _deps():
-    return sources() + [BINDING_SRC] + glob.glob(os.path.join(CSRC, "*.h")) + \
+    return sources() + glob.glob(os.path.join(CSRC, "*.h")) + \
         glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h")) + \
         [os.path.abspath(__file__)]
+
+
+def _binding_deps():
+    return [BINDING_SRC, os.path.join(INCLUDE, "moe.h"), os.path.abspath(__file__)]
 
 
 def up_to_date(lib: str = LIB_PATH) -> bool:
     if not os.path.exists(lib):
         return False
     t = os.path.getmtime(lib)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return all(os.path.getmtime(p) <= t for p in (_binding_deps() if lib == BINDING_PATH else _deps()))
 
 
 def _compile_binding(build_dir: str) -> str:
@@ -64,6 +73,7 @@ def _compile_binding(build_dir: str) -> str:
     import torch
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     cuda_inc = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    os.makedirs(build_dir, exist_ok=True)
     obj = os.path.join(build_dir, "fp8b_binding.o")
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
@@ -90,14 +100,40 @@ def _link_binding(obj: str) -> None:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: bool = False) -> str:
-    """Compile libmoe_gb300.so and _fp8b.so (or, with debug=True,
-    libmoe_gb300_debug.so with MOE_DEBUG=1) from csrc/; returns the library's
-    path."""
+    """Compile libmoe_gb300.so (or, with debug=True, libmoe_gb300_debug.so with
+    MOE_DEBUG=1) from csrc/, and _fp8b.so beside the former; returns the
+    library's path.  Raises where the library cannot be built; warns where the
+    module cannot (build_binding() raises)."""
+    if debug:
+        return _build_library(force, verbose, extra_flags, debug)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        stale = force or not up_to_date(BINDING_PATH)
+        obj = ex.submit(_compile_binding, BUILD_DIR) if stale else None
+        lib = _build_library(force, verbose, extra_flags, debug)
+        if obj is not None:
+            try:
+                _link_binding(obj.result())
+            except Exception as e:   # (no PyTorch, no headers, no host compiler)
+                if os.path.exists(BINDING_PATH):   # of older sources: not to be loaded beside this library
+                    os.remove(BINDING_PATH)
+                warnings.warn(f"{os.path.basename(BINDING_PATH)} was not built, the block-scaled fp8 calls of the "
+                              f"Python binding will raise: {e}", RuntimeWarning, stacklevel=2)
+    return lib
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile _fp8b.so if it is stale (the library has to be there); returns its path."""
+    if force or not up_to_date(BINDING_PATH):
+        _link_binding(_compile_binding(BUILD_DIR))
+    return BINDING_PATH
+
+
+def _build_library(force, verbose, extra_flags, debug) -> str:
     lib = DEBUG_LIB_PATH if debug else LIB_PATH
     build_dir = DEBUG_BUILD_DIR if debug else BUILD_DIR
     if debug:
         extra_flags = (*extra_flags, "-DMOE_DEBUG=1")
-    if not force and up_to_date(lib) and (debug or up_to_date(BINDING_PATH)):
+    if not force and up_to_date(lib):
         return lib
     nvcc = _nvcc()
     os.makedirs(build_dir, exist_ok=True)
@@ -113,8 +149,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
         return obj
 
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
-        binding = None if debug else ex.submit(_compile_binding, build_dir)
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
         objs = list(ex.map(compile_one, srcs))
     tmp = lib + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
@@ -122,8 +157,6 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, lib)
-    if binding is not None:
-        _link_binding(binding.result())
     return lib
 
 
