@@ -485,9 +485,9 @@ def _fp8b():
     global _fp8b_module
     if _fp8b_module is None:
         load_library()
-        path = _build.BINDING_PATH
+        path = _build.binding_path()
         if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing: build the CUDA library first "
+            raise RuntimeError(f"{path} is missing: build it for this PyTorch and Python first "
                                "(python -m expert_routed_ffn_selectedsoftmax_gb300.build)")
         spec = importlib.util.spec_from_file_location("_fp8b", path)
         module = importlib.util.module_from_spec(spec)

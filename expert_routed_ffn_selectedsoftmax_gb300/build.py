@@ -1,6 +1,6 @@
 """Compile the CUDA library (csrc/*.cu) into libmoe_gb300.so, in-tree, and the
 Python module of the block-scaled fp8 operators (csrc/fp8b_binding.cpp) into
-_fp8b.so beside it.
+_fp8b.<PyTorch's and Python's versions>.so beside it (binding_path()).
 
 nvcc, one -gencode for sm_103a, translation units compiled in parallel (the
 module by the host compiler against PyTorch's headers), no cmake.  Rebuilds only
@@ -33,7 +33,17 @@ DEBUG_LIB_PATH = os.path.join(PKG, "libmoe_gb300_debug.so")
 
 # the Python module of the block-scaled fp8 operators
 BINDING_SRC = os.path.join(CSRC, "fp8b_binding.cpp")
-BINDING_PATH = os.path.join(PKG, "_fp8b.so")
+
+
+def binding_path() -> str:
+    """Where the module of this interpreter and PyTorch lies.  It is bound to both
+    (C++ classes, CPython's own ABI), so their versions are part of its name: after
+    an upgrade, or from another environment on the same tree, an older build is not
+    found instead of being loaded."""
+    import torch
+    tag = f"torch{torch.__version__}.cxx11abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+    return os.path.join(PKG, f"_fp8b.{tag}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr",
@@ -57,15 +67,16 @@ def _deps():
         [os.path.abspath(__file__)]
 
 
-def _binding_deps():
-    return [BINDING_SRC, os.path.join(INCLUDE, "moe.h"), os.path.abspath(__file__)]
+def _newer(path: str, deps) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(p) <= os.path.getmtime(path) for p in deps)
 
 
 def up_to_date(lib: str = LIB_PATH) -> bool:
-    if not os.path.exists(lib):
-        return False
-    t = os.path.getmtime(lib)
-    return all(os.path.getmtime(p) <= t for p in (_binding_deps() if lib == BINDING_PATH else _deps()))
+    return _newer(lib, _deps())
+
+
+def binding_up_to_date() -> bool:
+    return _newer(binding_path(), [BINDING_SRC, os.path.join(INCLUDE, "moe.h"), os.path.abspath(__file__)])
 
 
 def _compile_binding(build_dir: str) -> str:
@@ -89,43 +100,50 @@ def _compile_binding(build_dir: str) -> str:
 def _link_binding(obj: str) -> None:
     import torch
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    path = binding_path()
+    tmp = path + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L", PKG, "-l:" + os.path.basename(LIB_PATH),
            "-L", lib, "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-lc10", "-lc10_cuda",
            "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"linking {os.path.basename(BINDING_PATH)} failed:\n{r.stderr}")
-    os.replace(tmp, BINDING_PATH)
+        raise RuntimeError(f"linking {os.path.basename(path)} failed:\n{r.stderr}")
+    os.replace(tmp, path)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: bool = False) -> str:
     """Compile libmoe_gb300.so (or, with debug=True, libmoe_gb300_debug.so with
-    MOE_DEBUG=1) from csrc/, and _fp8b.so beside the former; returns the
+    MOE_DEBUG=1) from csrc/, and the module beside the former; returns the
     library's path.  Raises where the library cannot be built; warns where the
     module cannot (build_binding() raises)."""
     if debug:
         return _build_library(force, verbose, extra_flags, debug)
     with cf.ThreadPoolExecutor(max_workers=1) as ex:
-        stale = force or not up_to_date(BINDING_PATH)
-        obj = ex.submit(_compile_binding, BUILD_DIR) if stale else None
+        obj = ex.submit(lambda: _compile_binding(BUILD_DIR) if force or not binding_up_to_date() else None)
         lib = _build_library(force, verbose, extra_flags, debug)
-        if obj is not None:
-            try:
+        try:
+            if obj.result():
                 _link_binding(obj.result())
-            except Exception as e:   # (no PyTorch, no headers, no host compiler)
-                if os.path.exists(BINDING_PATH):   # of older sources: not to be loaded beside this library
-                    os.remove(BINDING_PATH)
-                warnings.warn(f"{os.path.basename(BINDING_PATH)} was not built, the block-scaled fp8 calls of the "
-                              f"Python binding will raise: {e}", RuntimeWarning, stacklevel=2)
+        except Exception as e:   # (no PyTorch, no headers, no host compiler)
+            _remove_stale()
+            warnings.warn(f"the Python module of the block-scaled fp8 calls (_fp8b) was not built, they will raise: {e}",
+                          RuntimeWarning, stacklevel=2)
     return lib
 
 
+def _remove_stale() -> None:
+    """A module of older sources is not to be loaded beside a newer library."""
+    try:
+        os.remove(binding_path())
+    except (ImportError, OSError):
+        pass
+
+
 def build_binding(force: bool = False) -> str:
-    """Compile _fp8b.so if it is stale (the library has to be there); returns its path."""
-    if force or not up_to_date(BINDING_PATH):
+    """Compile the module if it is stale (the library has to be there); returns its path."""
+    if force or not binding_up_to_date():
         _link_binding(_compile_binding(BUILD_DIR))
-    return BINDING_PATH
+    return binding_path()
 
 
 def _build_library(force, verbose, extra_flags, debug) -> str:
