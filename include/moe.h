@@ -441,7 +441,9 @@ MOE_API moe_status moe_forward_noalloc(const void *x, moe_dtype act_dt, int T, i
  * K (d, F) is a multiple of 16; the last block of a row may be shorter.  Code
  * buffers are 16-byte aligned, scales 4-byte.
  * Quantisation of a block: s = max|x| / 448, code = E4M3 nearest to x * (1/s),
- * ties to even, each operation rounded to fp32.  All zeros, or so small that s
+ * ties to even, each operation rounded to fp32.  (x * (1/s) is within 3 x 2^-24
+ * of 448 x / max|x|: where that lies on the border of two codes, as it does for a
+ * few bf16 values in ten thousand, the code may be either.)  All zeros, or so small that s
  * would be below 2^-126: s = 0, codes 0.  A block that holds an infinity or
  * NaN: s = NaN, NaN codes.
  *

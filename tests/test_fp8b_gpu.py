@@ -129,6 +129,35 @@ def test_quant_special_values(moe, block_rows):
     assert bool((s[: 256 // block_rows] == 0).all()) and bool(s[512 // block_rows : 896 // block_rows].isnan().all())
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,cols,block_rows", [(4096, 1024, 1), (4096, 1024, 128), (999, 2000, 1), (300, 400, 128)])
+def test_quant_against_the_quotient(moe, dt, rows, cols, block_rows):
+    """Codes against the nearest-even ones of 448 x / max|x|, not by the kernel's own
+    operations.  s, 1/s and the product are each off by 2^-24 at most, so a code may
+    differ only where the quotient is within 3 x 2^-24 (and its square's share) of
+    the border, and then by one step.  A border is (n + 1/2) steps, n < 16: 448 |x|
+    and border * max|x| have at most 29 bits and are compared exactly in 64."""
+    x = (rand(rows, cols, seed=3) * torch.exp(rand(rows, 1, seed=4, sd=0.5))).to(DT[dt])
+    q, s = moe.moe_quant_fp8b(x, block_rows=block_rows)
+    nr, nc = -(-rows // block_rows), blocks(cols)
+    pad = torch.zeros(nr * block_rows, nc * B, dtype=torch.float64, device=DEV)
+    pad[:rows, :cols] = x.double().abs()
+    top = pad.view(nr, block_rows, nc, B).amax(dim=(1, 3))
+    assert bool(((s.double() * FMAX - top).abs() <= 2.0 ** -24 * top).all())
+    top = top.repeat_interleave(block_rows, 0)[:rows].repeat_interleave(B, 1)[:, :cols]
+    x448, got = FMAX * x.double().abs(), q.double().abs()
+    quo = x448 / top
+    step = torch.exp2(torch.floor(torch.log2(quo.clamp(min=2.0 ** -30))).clamp(min=-6) - 3)
+    low = torch.floor(quo / step)
+    side = x448 - (low + 0.5) * step * top                    # sign: above or below the border, 0 on it
+    even = low + (low % 2)
+    want = torch.where(side > 0, low + 1, torch.where(side < 0, low, even)) * step
+    near = side.abs() <= 3.01 * 2.0 ** -24 * x448
+    assert torch.equal(got[~near], want[~near])
+    assert bool(((got == low * step) | (got == (low + 1) * step)).all())
+    assert bool(((q.double() >= 0) | (x.double() < 0)).all()) and bool(((q.double() <= 0) | (x.double() > 0)).all())
+
+
 def test_quant_strided_and_given_outputs(moe):
     big = rand(2, 40, 512)
     x = big[..., :256]                      # rows 512 apart, batches 40 * 512 apart
