@@ -11,8 +11,8 @@
 // more than the weights' time.)
 //
 // What bounds it: memory.  64 x 2816 x 2048 over 16 experts (92 MB of weights)
-// takes 17.0 us, 5.4 TB/s; gate/up of 128 tokens over 64 experts (48 of them with
-// rows, 50 MB) 13.7 us, of which 8 us are the weights' and the rest the start
+// takes 17.1 us, 5.4 TB/s; gate/up of 128 tokens over 64 experts (48 of them with
+// rows, 50 MB) 13.9 us, of which 8 us are the weights' and the rest the start
 // (launch, group table, first tile) and the last tile's end.
 //
 // A tile is 128 output columns (PRODUCT: of W; GATEUP: of W_gate and W_up) of
@@ -478,6 +478,12 @@ static long long most_tiles(const Params &p)
 // 24: 21.2 / 21.3, 64: 27.5 / 22.8; one of 2048 x 5632 (44 column tiles), rows 16:
 // 6.1 / 10.3, 96: 7.8 / 10.3, 128: 9.6 / 10.4, 256: 15.9 / 10.5; 4096 x 4096 (32),
 // 16: 6.2 / 16.1, 128: 12.1 / 16.4, 192: 17.4 / 16.5.
+// The groups' sizes are known on the device only, so the rule goes by the mean.
+// Rows of 16 on average, evenly spread | half of them on one expert | all but one
+// for each of the others on one (here / there): 64 experts of 512 x 1024 9.9 / 12.0 |
+// 12.0 / 11.9 | 12.2 / 12.1, of 2048 x 1024 26.1 / 28.0 | 29.6 / 27.7 | 30.3 / 27.6,
+// 16 of 2816 x 2048 18.8 / 20.6 | 24.0 / 20.6 | 22.6 / 20.6 (gate/up 33.2 / 36.2 |
+// 42.0 / 35.7 | 39.7 / 35.7): up to 11 % gained at even loads, up to 18 % lost at these.
 bool decode_fits(const Params &p, int num_sms)
 {
     const long long experts = p.E < p.rows ? p.E : p.rows;

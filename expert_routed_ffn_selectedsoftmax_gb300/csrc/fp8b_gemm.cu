@@ -7,19 +7,21 @@
 // with E4M3 codes c, an activation scale per row and 128 columns and a weight
 // scale per 128 x 128 block.  The scales change every 128 columns of the
 // reduction, so the tensor cores sum one block (four MMAs of K = 32, fp32)
-// into one of two TMEM buffers, and the epilogue warps add that partial sum,
-// times the two scales, to the row's running fp32 sums in registers while the
-// tensor cores fill the other buffer.
+// into a TMEM buffer -- each half of a tile's columns has two, and a warp that
+// issues its MMAs -- and the epilogue warps add that partial sum, times the two
+// scales, to the row's running fp32 sums in registers while the tensor cores fill
+// the half's other buffer and those of the other half.
 //
-// What bounds it: 8192 x 2048 x 5632 takes 81 us, 2.3 PFLOP/s (a library product
+// What bounds it: 8192 x 2048 x 5632 takes 82 us, 2.3 PFLOP/s (a library product
 // with one scale for each matrix, which needs no such turns: 51 us).  A block of
-// a 128 x 256 tile takes 870 clocks of which the MMAs are 470: the rest is the
-// turn of a TMEM buffer -- commit, wake, read, sums, arrival, wake -- that the
-// other buffers' MMAs do not cover, and a tile's end, where its sums are written
-// while the MMAs run at most two blocks ahead (the ncu capture shows the tensor
-// pipe 54 % busy, shared memory and L2 a third, issue slots 45 %).  Tried and no
-// faster: CTA pairs (M = 256; 85 us, and ragged groups pad more), one issuing warp
-// with N = 256 (89), sixteen epilogue warps (98), scalar sums (89).
+// a 128 x 256 tile takes 870 clocks (traced in the kernel), in which its MMAs keep
+// the tensor pipe busy for 512 (ncu: 75.9k of 141k active cycles for 148 blocks an
+// SM, 54 %; L2 38 %, issue slots 44 %): the rest is the turn of a TMEM buffer --
+// commit, wake, read, sums, arrival, wake -- that the other buffers' MMAs do not
+// cover, and a tile's end, where its sums are written while the MMAs run at most
+// two blocks ahead.  Tried and no faster: CTA pairs (M = 256; 85 us, and ragged
+// groups pad more), one issuing warp with N = 256 (89), sixteen epilogue warps
+// (98), scalar sums (89), loads of 32 columns in two register buffers (spills; 127).
 //
 // A tile is 128 rows x 256 columns (PRODUCT), or 128 rows x 128 columns of
 // both W_gate and W_up (GATEUP: the epilogue has whole 128-column groups of h,

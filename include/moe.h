@@ -446,6 +446,9 @@ MOE_API moe_status moe_forward_noalloc(const void *x, moe_dtype act_dt, int T, i
  * few bf16 values in ten thousand, the code may be either.)  All zeros, or so small that s
  * would be below 2^-126: s = 0, codes 0.  A block that holds an infinity or
  * NaN: s = NaN, NaN codes.
+ * Products: a block's code products are summed, times the product of its two
+ * scales, into fp32 sums over the blocks.  The two scales' product is formed in
+ * fp32 first: below 2^-126 it loses bits, beyond 2^128 it is infinite.
  *
  * A layer as a chain of these calls, every one asynchronous on one stream:
  *   moe_norm_fp8b     residual + the previous layer's combine, RMS norm, codes
@@ -483,7 +486,9 @@ MOE_API moe_status moe_quant_fp8b(const void *x, moe_dtype x_dt, int batch, int 
  *              x[t] + delta[t]                               (k == 0)
  *              x[t] + sum_j topk_w[t,j] delta[inv[t*k + j]]  (k in 1..8)
  *     y[t,i] = r[t,i] * weight[i] / sqrt(mean_i r[t,i]^2 + eps)
- *   The sums are fp32 in slot order and y is taken from the unrounded r.
+ *   The sums are fp32 in slot order and y is taken from the unrounded r.  The
+ *   squares are summed in fp32 too: where their sum overflows (values of about
+ *   1e18 and more), y is 0.
  *   x [T, d] (fp32 or bf16, rows ldx apart); delta [delta_rows, d] (fp32 or
  *   bf16, rows ldd apart; delta_rows >= T when k == 0): with k > 0 the
  *   grouped outputs of a layer, inv and topk_w [T, k] as moe_permute and

@@ -296,6 +296,22 @@ def test_norm_of_small_and_large_rows(moe, size):
     assert bool((((got - want).abs() <= tol) | ~keep).all())
 
 
+def test_norm_of_rows_whose_squares_overflow(moe):
+    """Finite rows beyond the fp32 sum of squares give zeros, as the header says;
+    the residual and the other rows are as without them."""
+    x, w = rand(6, 384), torch.ones(384, device=DEV)
+    want = moe.moe_norm_fp8b(x, w, 1e-6, delta=x)
+    big = x.clone()
+    big[2], big[4] = 1e20, -3e37
+    resid, y, q, s = moe.moe_norm_fp8b(big, w, 1e-6, delta=big)
+    assert torch.equal(resid, big + big)
+    for r in (2, 4):
+        assert not y[r].any() and not q[r].float().any() and not s[r].any()
+    for a, b in zip((resid, y, q, s), want):
+        keep = [0, 1, 3, 5]
+        assert torch.equal(a[keep].float(), b[keep].float())
+
+
 def test_norm_in_place_and_strided(moe):
     T, d = 21, 512
     wide, dwide = rand(T, 1024), rand(T, 768).bfloat16()
