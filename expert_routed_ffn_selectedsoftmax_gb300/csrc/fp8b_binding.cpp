@@ -144,7 +144,9 @@ PyObject *norm(PyObject *, PyObject *const *a, Py_ssize_t n)
     const Tensor &x = tensor_of(a[0], "x"), &weight = tensor_of(a[1], "weight");
     const double eps = PyFloat_AsDouble(a[2]);
     if (eps == -1.0 && PyErr_Occurred()) return nullptr;
-    const bool adds = given(a[3]), combines = given(a[5]), want_normed = PyObject_IsTrue(a[6]) == 1;
+    const int wants = PyObject_IsTrue(a[6]);
+    if (wants < 0) return nullptr;
+    const bool adds = given(a[3]), combines = given(a[5]), want_normed = wants != 0;
     TORCH_CHECK_VALUE(x.dim() == 2, "x: ", x.dim(), " dimensions, expected 2");
     TORCH_CHECK_VALUE(given(a[4]) == combines, "topk_w and inv go together");
     TORCH_CHECK_VALUE(adds || !combines, "topk_w and inv need delta");

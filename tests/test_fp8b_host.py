@@ -149,3 +149,15 @@ def test_binding_refuses_wrong_pairs():
                      (dict(x=torch.zeros(2, 4, 512)[:, :3]), ValueError), (dict(x=[1.0]), TypeError), (dict(scales=torch.zeros(4, 3)), ValueError)):
         with pytest.raises(err):
             moe.moe_quant_fp8b(**dict(dict(x=x), **bad))
+
+
+def test_binding_passes_on_python_errors():
+    """An argument whose conversion raises gives that error, not a later one's."""
+    import expert_routed_ffn_selectedsoftmax_gb300 as moe
+    x, w = torch.zeros(4, 256), torch.ones(256)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        moe.moe_norm_fp8b(x, w, want_normed=torch.ones(2))
+    with pytest.raises(TypeError):
+        moe.moe_norm_fp8b(x, w, eps="small")
+    with pytest.raises(TypeError):
+        moe.moe_quant_fp8b(x, block_rows=None)
