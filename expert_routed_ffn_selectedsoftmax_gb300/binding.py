@@ -36,7 +36,9 @@ EXPORTS = ("moe_status_str", "moe_version", "moe_route", "moe_route_scored", "mo
            "moe_quant_fp8b", "moe_norm_fp8b", "moe_gemm_fp8b", "moe_grouped_gemm_fp8b",
            "moe_gate_up_fp8b", "moe_fp8b_workspace_size", "moe_grouped_gemm_fp8b_expire_wait",
            "moe_grouped_gemm_fp8b_expire_sums", "moe_gate_up_fp8b_expire_wait",
-           "moe_gate_up_fp8b_expire_sums")
+           "moe_gate_up_fp8b_expire_sums",
+           "moe_dispatch", "moe_dispatch_backward", "moe_combine", "moe_combine_backward",
+           "moe_quant_i8", "moe_gemm_i8", "moe_grouped_gemm_i8", "moe_gate_up_i8", "moe_i8_workspace_size")
 
 _lib = None
 _debug_lib = None
@@ -156,6 +158,19 @@ def _declare(L):
     L.moe_gate_up_fp8b.argtypes = [vp, vp, i, i, ll, vp, vp, vp, vp, i, i, vp, vp, i, vp, vp, vp,
                                    sz, vp, vp]
     L.moe_gate_up_fp8b.restype = i
+    L.moe_dispatch.argtypes = [vp, i, i, i, ll, vp, i, vp, i, ll, vp]
+    L.moe_dispatch_backward.argtypes = [vp, i, i, i, ll, vp, i, i, vp, ll, vp]
+    L.moe_combine.argtypes = [vp, i, i, i, ll, vp, vp, i, i, vp, i, ll, vp]
+    L.moe_combine_backward.argtypes = [vp, i, i, i, ll, vp, i, i, ll, vp, vp, i, vp, ll, vp, vp]
+    L.moe_quant_i8.argtypes = [vp, i, i, i, ll, vp, vp, vp]
+    L.moe_gemm_i8.argtypes = [vp, vp, i, i, ll, vp, vp, i, vp, i, ll, vp, sz, vp, vp]
+    L.moe_grouped_gemm_i8.argtypes = [vp, vp, i, i, ll, vp, vp, i, i, vp, vp, i, vp, i, ll, vp, sz, vp, vp]
+    L.moe_gate_up_i8.argtypes = [vp, vp, i, i, ll, vp, vp, vp, vp, i, i, vp, vp, i, vp, i, ll, vp, sz, vp, vp]
+    for call in (L.moe_dispatch, L.moe_dispatch_backward, L.moe_combine, L.moe_combine_backward, L.moe_quant_i8,
+                 L.moe_gemm_i8, L.moe_grouped_gemm_i8, L.moe_gate_up_i8):
+        call.restype = i
+    L.moe_i8_workspace_size.argtypes = [i, i]
+    L.moe_i8_workspace_size.restype = sz
     L.moe_check.argtypes = [vp, vp, vp]
     L.moe_check.restype = i
     L.moe_check_noalloc.argtypes = [vp, vp]
@@ -585,3 +600,107 @@ def moe_gate_up_fp8b(x_q: torch.Tensor, x_s: torch.Tensor, wg_q: torch.Tensor, w
     """
     return _checked((_fp8b_module or _fp8b()).gate_up(x_q, x_s, wg_q, wg_s, wu_q, wu_s, offsets, perm_tok, h_q, h_s,
                                                       workspace, status), "moe_gate_up_fp8b")
+
+
+# ---- rows to their experts and back, and the 8-bit integer operators (int8 codes, one
+# fp32 scale per row).  Their tensors are checked, and their outputs allocated, in the
+# compiled module too (csrc/i8_binding.cpp).
+
+def moe_dispatch(x: torch.Tensor, inv: torch.Tensor, k: int, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Tokens x [T, d] (fp32 / bf16) into grouped order -> out [rows, d]: out[inv[t*k + j]] = x[t].
+
+    inv [T*k] (moe_permute).  rows is T*k, or out's if it is given.  Rows that no slot
+    names are left as they were (uninitialised in an output allocated here); a slot whose
+    inv is outside [0, rows) writes nothing.
+    """
+    return _checked((_fp8b_module or _fp8b()).dispatch(x, inv, k, out), "moe_dispatch")
+
+
+def moe_dispatch_backward(grad: torch.Tensor, inv: torch.Tensor, k: int,
+                          out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """moe_dispatch's gradient -> [T, d] in grad's type: out[t] = sum_j grad[inv[t*k + j]]."""
+    return _checked((_fp8b_module or _fp8b()).dispatch_backward(grad, inv, k, out), "moe_dispatch_backward")
+
+
+def moe_combine(y: torch.Tensor, topk_w: torch.Tensor, inv: torch.Tensor, out: Optional[torch.Tensor] = None,
+                out_dtype: torch.dtype = torch.float32) -> torch.Tensor:
+    """The experts' outputs y [rows, d] (fp32 / bf16) back to tokens -> out [T, d] fp32 / bf16:
+    out[t] = sum_j topk_w[t, j] y[inv[t*k + j]].
+
+    topk_w [T, k] (moe_route), inv [T*k] (moe_permute); a slot whose inv is outside
+    [0, rows) adds nothing.
+    """
+    return _checked((_fp8b_module or _fp8b()).combine(y, topk_w, inv, out, out_dtype), "moe_combine")
+
+
+def moe_combine_backward(grad: torch.Tensor, y: torch.Tensor, topk_w: torch.Tensor, inv: torch.Tensor,
+                         want_dy: bool = True, want_dw: bool = True, dy: Optional[torch.Tensor] = None,
+                         dw: Optional[torch.Tensor] = None):
+    """moe_combine's gradients for grad [T, d] -> (dy [rows, d] in y's type, dw fp32 [T, k]):
+    dy[inv[t*k + j]] = topk_w[t, j] grad[t], dw[t, j] = <grad[t], y[inv[t*k + j]]>.
+
+    One that is not wanted is None.  Rows of dy that no slot names are left as they were
+    (uninitialised in an output allocated here).
+    """
+    return _checked((_fp8b_module or _fp8b()).combine_backward(grad, y, topk_w, inv, want_dy, want_dw, dy, dw),
+                    "moe_combine_backward")
+
+
+def moe_i8_workspace_size(rows: int, K: int) -> int:
+    return int(load_library().moe_i8_workspace_size(rows, K))
+
+
+def moe_quant_i8(x: torch.Tensor, codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None):
+    """int8 codes of x [rows, cols] or [batch, rows, cols] (fp32 / bf16) -> (codes int8 like x,
+    scales fp32 [..., rows]): one scale per row, max|x| / 127 (a token of activations, an
+    output channel of weights [E, N, K])."""
+    return _checked((_fp8b_module or _fp8b()).quant_i8(x, codes, scales), "moe_quant_i8")
+
+
+def moe_gemm_i8(x_q: torch.Tensor, x_s: torch.Tensor, w_q: torch.Tensor, w_s: torch.Tensor,
+                out: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+                workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """x [T, K] times W^T, W [N, K], int8 codes with a scale per row of each (x_s [T],
+    w_s [N]) -> out [T, N] bf16 / fp32.
+
+    x_q's and out's rows may be further apart than their length.  workspace: scratch of
+    moe_i8_workspace_size(T, K) bytes (allocated when not given).  status: optional int32
+    device word that collects device-side errors (zero it once; moe_check(status) reads it).
+    """
+    if w_q.dim() != 2:
+        raise ValueError(f"w_q: {w_q.dim()} dimensions, expected 2")
+    return _checked((_fp8b_module or _fp8b()).product_i8(x_q, x_s, w_q, w_s, None, None, out, out_dtype, workspace,
+                                                         status), "moe_gemm_i8")
+
+
+def moe_grouped_gemm_i8(x_q: torch.Tensor, x_s: torch.Tensor, w_q: torch.Tensor, w_s: torch.Tensor,
+                        offsets: torch.Tensor, perm_tok: Optional[torch.Tensor] = None,
+                        out: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+                        workspace: Optional[torch.Tensor] = None,
+                        status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Every expert's product with its rows, int8 codes with a scale per row -> out [rows, N].
+
+    w_q [E, N, K], w_s [E, N]; rows of expert e are [offsets[e], offsets[e+1])
+    (moe_permute), row r is x's row perm_tok[r], or r itself without perm_tok.  Rows from
+    offsets[E] on are left as they were.  workspace: scratch of
+    moe_i8_workspace_size(rows, K) bytes (allocated when not given).
+    """
+    if w_q.dim() != 3:
+        raise ValueError(f"w_q: {w_q.dim()} dimensions, expected 3")
+    return _checked((_fp8b_module or _fp8b()).product_i8(x_q, x_s, w_q, w_s, offsets, perm_tok, out, out_dtype,
+                                                         workspace, status), "moe_grouped_gemm_i8")
+
+
+def moe_gate_up_i8(x_q: torch.Tensor, x_s: torch.Tensor, wg_q: torch.Tensor, wg_s: torch.Tensor,
+                   wu_q: torch.Tensor, wu_s: torch.Tensor, offsets: Optional[torch.Tensor] = None,
+                   perm_tok: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None,
+                   h_dtype: torch.dtype = torch.bfloat16, workspace: Optional[torch.Tensor] = None,
+                   status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """h = SiLU(W_g x) * (W_u x) per grouped row -> h [rows, F] bf16 / fp32.
+
+    wg_q, wu_q [E, F, d] (or [F, d] without offsets: a dense layer) with scales [E, F];
+    offsets, perm_tok and workspace as moe_grouped_gemm_i8.  moe_quant_i8(h) gives the down
+    projection's codes.
+    """
+    return _checked((_fp8b_module or _fp8b()).gate_up_i8(x_q, x_s, wg_q, wg_s, wu_q, wu_s, offsets, perm_tok, h, h_dtype,
+                                                         workspace, status), "moe_gate_up_i8")

@@ -1,5 +1,5 @@
 """Compile the CUDA library (csrc/*.cu) into libmoe_gb300.so, in-tree, and the
-Python module of the block-scaled fp8 operators (csrc/fp8b_binding.cpp) into
+Python module of the operators beside the layer (csrc/*_binding.cpp) into
 _fp8b.<PyTorch's and Python's versions>.so beside it (binding_path()).
 
 nvcc, one -gencode for sm_103a, translation units compiled in parallel (the
@@ -31,8 +31,9 @@ LIB_PATH = os.path.join(PKG, "libmoe_gb300.so")
 DEBUG_BUILD_DIR = os.path.join(ROOT, "_build_debug")
 DEBUG_LIB_PATH = os.path.join(PKG, "libmoe_gb300_debug.so")
 
-# the Python module of the block-scaled fp8 operators
-BINDING_SRC = os.path.join(CSRC, "fp8b_binding.cpp")
+# the Python module of the operators beside the layer (block-scaled fp8, int8, dispatch and combine)
+BINDING_SRCS = [os.path.join(CSRC, name) for name in ("fp8b_binding.cpp", "i8_binding.cpp")]
+BINDING_HEADER = os.path.join(CSRC, "binding.h")
 
 
 def binding_path() -> str:
@@ -76,33 +77,38 @@ def up_to_date(lib: str = LIB_PATH) -> bool:
 
 
 def binding_up_to_date() -> bool:
-    return _newer(binding_path(), [BINDING_SRC, os.path.join(INCLUDE, "moe.h"), os.path.abspath(__file__)])
+    return _newer(binding_path(), [*BINDING_SRCS, BINDING_HEADER, os.path.join(INCLUDE, "moe.h"), os.path.abspath(__file__)])
 
 
-def _compile_binding(build_dir: str) -> str:
-    """fp8b_binding.cpp -> object file (host compiler, PyTorch's headers)."""
+def _compile_binding(build_dir: str) -> list:
+    """csrc/*_binding.cpp -> object files (host compiler, PyTorch's headers)."""
     import torch
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     cuda_inc = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
     os.makedirs(build_dir, exist_ok=True)
-    obj = os.path.join(build_dir, "fp8b_binding.o")
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
-           "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda_inc,
-           "-I", INCLUDE, "-c", BINDING_SRC, "-o", obj]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"{cmd[0]} failed on {os.path.basename(BINDING_SRC)}:\n{r.stderr}")
-    return obj
+
+    def compile_one(src):
+        obj = os.path.join(build_dir, os.path.basename(src)[:-4] + ".o")
+        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+               "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda_inc,
+               "-I", INCLUDE, "-c", src, "-o", obj]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{cmd[0]} failed on {os.path.basename(src)}:\n{r.stderr}")
+        return obj
+
+    with cf.ThreadPoolExecutor(max_workers=len(BINDING_SRCS)) as ex:
+        return list(ex.map(compile_one, BINDING_SRCS))
 
 
-def _link_binding(obj: str) -> None:
+def _link_binding(objs: list) -> None:
     import torch
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     path = binding_path()
     tmp = path + f".tmp{os.getpid()}"
-    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L", PKG, "-l:" + os.path.basename(LIB_PATH),
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, *objs, "-L", PKG, "-l:" + os.path.basename(LIB_PATH),
            "-L", lib, "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-lc10", "-lc10_cuda",
            "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -119,14 +125,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
     if debug:
         return _build_library(force, verbose, extra_flags, debug)
     with cf.ThreadPoolExecutor(max_workers=1) as ex:
-        obj = ex.submit(lambda: _compile_binding(BUILD_DIR) if force or not binding_up_to_date() else None)
+        objs = ex.submit(lambda: _compile_binding(BUILD_DIR) if force or not binding_up_to_date() else None)
         lib = _build_library(force, verbose, extra_flags, debug)
         try:
-            if obj.result():
-                _link_binding(obj.result())
+            if objs.result():
+                _link_binding(objs.result())
         except Exception as e:   # (no PyTorch, no headers, no host compiler)
             _remove_stale()
-            warnings.warn(f"the Python module of the block-scaled fp8 calls (_fp8b) was not built, they will raise: {e}",
+            warnings.warn(f"the Python module of the operators beside the layer (_fp8b) was not built, their calls will raise: {e}",
                           RuntimeWarning, stacklevel=2)
     return lib
 

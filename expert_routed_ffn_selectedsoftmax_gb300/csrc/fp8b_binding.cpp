@@ -6,102 +6,11 @@
 // bounds), and in Python the checks, the allocations and the marshalling took
 // 15-23 us a call on the host where the kernels of a decode step take 2-7 us;
 // here they take 3-6 us.  Nothing of the operators is computed here.
-#include <Python.h>
-
-#include <ATen/core/Tensor.h>
-#include <ATen/cuda/EmptyTensor.h>
-#include <c10/cuda/CUDAGuard.h>
-#include <c10/cuda/CUDAStream.h>
-#include <torch/csrc/Dtype.h>
-#include <torch/csrc/Exceptions.h>
-#include <torch/csrc/autograd/python_variable.h>
-
-#include "../../include/moe.h"
+#include "binding.h"
 
 namespace {
 
-using at::ScalarType;
-using at::Tensor;
-
-constexpr int64_t kBlock = 128;
-int64_t blocks(int64_t n) { return (n + kBlock - 1) / kBlock; }
-
-const Tensor &tensor_of(PyObject *o, const char *name)
-{
-    TORCH_CHECK_TYPE(THPVariable_Check(o), name, ": expected a tensor, got ", Py_TYPE(o)->tp_name);
-    return THPVariable_Unpack(o);
-}
-bool given(PyObject *o) { return o != Py_None; }
-
-int int_of(int64_t v, const char *name)
-{
-    TORCH_CHECK_VALUE(v >= 0 && v <= INT32_MAX, name, ": ", v, " is out of range");
-    return (int)v;
-}
-
-// Sets of element types an operand may have.
-enum Kind { CODES, REAL, FLOAT32, BFLOAT16, INT32 };
-bool is_kind(ScalarType t, Kind k)
-{
-    switch (k) {
-    case CODES: return t == ScalarType::Float8_e4m3fn || t == ScalarType::Byte;
-    case REAL: return t == ScalarType::Float || t == ScalarType::BFloat16;
-    case FLOAT32: return t == ScalarType::Float;
-    case BFLOAT16: return t == ScalarType::BFloat16;
-    default: return t == ScalarType::Int;
-    }
-}
-const char *kind_name(Kind k)
-{
-    static const char *const names[] = {"float8_e4m3fn or uint8", "float32 or bfloat16", "float32", "bfloat16", "int32"};
-    return names[k];
-}
-
-// The operand's pointer, after checks of device, type, shape and strides
-// (`strided`: its rows may be further apart than their length).
-void *need(const Tensor &t, const char *name, at::IntArrayRef shape, Kind kind, c10::Device dev, bool strided = false)
-{
-    TORCH_CHECK_VALUE(t.device() == dev, name, ": on ", t.device(), ", expected ", dev);
-    TORCH_CHECK_TYPE(is_kind(t.scalar_type(), kind), name, ": ", t.scalar_type(), ", expected ", kind_name(kind));
-    TORCH_CHECK_VALUE(t.sizes() == shape, name, ": shape ", t.sizes(), ", expected ", shape);
-    TORCH_CHECK_VALUE(t.is_contiguous() || (strided && t.stride(-1) == 1), name, ": strides ", t.strides(),
-                      " are not supported, make it contiguous");
-    return t.data_ptr();
-}
-int64_t row_stride(const Tensor &t) { return t.size(-2) > 1 ? t.stride(-2) : t.size(-1); }
-moe_dtype real_dtype(const Tensor &t) { return t.scalar_type() == ScalarType::Float ? MOE_F32 : MOE_BF16; }
-
-Tensor empty(at::IntArrayRef shape, ScalarType t, c10::Device dev)
-{
-    return at::detail::empty_cuda(shape, t, dev, c10::nullopt);
-}
-// `o` if it is a tensor, else a new one (`holder` keeps it)
-const Tensor &given_or_empty(PyObject *o, const char *name, Tensor &holder, at::IntArrayRef shape, ScalarType t,
-                             c10::Device dev)
-{
-    if (given(o)) return tensor_of(o, name);
-    holder = empty(shape, t, dev);
-    return holder;
-}
-void need_cuda(const Tensor &t, const char *name)
-{
-    TORCH_CHECK_VALUE(t.is_cuda(), name, ": on ", t.device(), ", expected a CUDA device");
-}
-moe_stream stream_of(c10::Device dev) { return c10::cuda::getCurrentCUDAStream(dev.index()).stream(); }
-
-// What a call returns: its outputs, or the status it failed with as an int
-// (the Python side raises MoeError).
-PyObject *wrap(PyObject *o, const Tensor &t)
-{
-    if (o && given(o) && THPVariable_Check(o)) {
-        Py_INCREF(o);
-        return o;
-    }
-    return THPVariable_Wrap(t);
-}
-PyObject *failed(moe_status st) { return PyLong_FromLong(st); }
-
-void need_args(Py_ssize_t n, Py_ssize_t want) { TORCH_CHECK_TYPE(n == want, "expected ", want, " arguments, got ", n); }
+using namespace moe_py;
 
 // quant(x, block_rows, codes, scales)
 PyObject *quant(PyObject *, PyObject *const *a, Py_ssize_t n)
@@ -206,62 +115,11 @@ PyObject *norm(PyObject *, PyObject *const *a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
-// What the products share: x, its groups, the scratch of gathered rows, status.
-struct Rows {
-    const void *x_q;
-    const float *x_s;
-    int x_rows, K, rows;
-    int64_t ldx;
-    const int32_t *offsets = nullptr, *perm_tok = nullptr;
-    uint32_t *status = nullptr;
-    c10::Device dev;
-};
-Rows rows_of(PyObject *x_q, PyObject *x_s, PyObject *offsets, PyObject *perm_tok, PyObject *status, int64_t E)
-{
-    const Tensor &x = tensor_of(x_q, "x_q");
-    TORCH_CHECK_VALUE(x.dim() == 2, "x_q: ", x.dim(), " dimensions, expected 2");
-    Rows r{nullptr, nullptr, int_of(x.size(0), "x_q"), int_of(x.size(1), "x_q"), 0, row_stride(x),
-           nullptr, nullptr, nullptr, x.device()};
-    r.x_q = need(x, "x_q", x.sizes(), CODES, r.dev, true);
-    const int64_t s_shape[2] = {r.x_rows, blocks(r.K)};
-    r.x_s = static_cast<const float *>(need(tensor_of(x_s, "x_s"), "x_s", s_shape, FLOAT32, r.dev));
-    r.rows = r.x_rows;
-    if (given(perm_tok)) {
-        const Tensor &p = tensor_of(perm_tok, "perm_tok");
-        const int64_t shape[1] = {p.numel()};
-        r.rows = int_of(p.numel(), "perm_tok");
-        r.perm_tok = static_cast<const int32_t *>(need(p, "perm_tok", shape, INT32, r.dev));
-    }
-    if (given(offsets)) {
-        const int64_t shape[1] = {E + 1};
-        r.offsets = static_cast<const int32_t *>(need(tensor_of(offsets, "offsets"), "offsets", shape, INT32, r.dev));
-    } else {
-        TORCH_CHECK_VALUE(E == 1, "offsets are required for ", E, " experts");
-    }
-    if (given(status)) {
-        const Tensor &t = tensor_of(status, "status");
-        TORCH_CHECK_VALUE(t.numel() > 0, "status: empty");
-        r.status = static_cast<uint32_t *>(need(t, "status", t.sizes(), INT32, r.dev));
-    }
-    return r;
-}
-// scratch of gathered rows: the caller's, or a new one (the allocator hands it
-// on in stream order)
+// scratch of gathered rows
 void *workspace_of(PyObject *o, const Rows &r, Tensor &holder, size_t *bytes)
 {
     *bytes = 0;
-    if (!r.perm_tok) return nullptr;
-    if (given(o)) {
-        const Tensor &t = tensor_of(o, "workspace");
-        TORCH_CHECK_VALUE(t.device() == r.dev, "workspace: on ", t.device(), ", expected ", r.dev);
-        TORCH_CHECK_VALUE(t.is_contiguous(), "workspace: make it contiguous");
-        *bytes = t.nbytes();
-        return t.data_ptr();
-    }
-    *bytes = moe_fp8b_workspace_size(r.rows, r.K);
-    const int64_t shape[1] = {(int64_t)*bytes};
-    holder = empty(shape, ScalarType::Byte, r.dev);
-    return holder.data_ptr();
+    return r.perm_tok ? scratch_of(o, r.dev, moe_fp8b_workspace_size(r.rows, r.K), holder, bytes) : nullptr;
 }
 
 // product(x_q, x_s, w_q, w_s, offsets, perm_tok, out, out_dtype, workspace, status): w_q [N, K] or [E, N, K]
@@ -333,14 +191,18 @@ PyObject *gate_up(PyObject *, PyObject *const *a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
-template <PyObject *(*F)(PyObject *, PyObject *const *, Py_ssize_t)> PyMethodDef method(const char *name)
-{
-    return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(F)), METH_FASTCALL, nullptr};
-}
 PyMethodDef methods[] = {method<quant>("quant"), method<norm>("norm"), method<product>("product"),
                          method<gate_up>("gate_up"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fp8b", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__fp8b(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__fp8b(void)
+{
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddFunctions(m, moe_py::i8_methods) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

@@ -1,0 +1,61 @@
+// i8.h -- shared pieces of the 8-bit integer operators (int8 codes, one fp32 scale
+// per row: a token of activations, an output channel of weights).
+#pragma once
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace moe {
+namespace i8 {
+
+enum Mode { PRODUCT = 0, GATEUP = 1 };
+enum Role { LOADS = 0, CONVERT = 1, SUMS = 2 };   // whose first wait a test hook lets expire
+
+// A product of the rows of every group with its expert's weights.
+struct Params {
+    const int8_t *x_q;        // [x_rows, K], rows ldx apart
+    const float *x_s;         // [x_rows]
+    const int8_t *w[2];       // [E, N, K] of W (PRODUCT) or W_gate, W_up
+    const float *w_s[2];      // [E, N]
+    const int32_t *offsets;   // [E+1], or NULL: one group of all rows
+    const int32_t *perm_tok;  // [rows], or NULL: row r is x's row r
+    long long ldx, ldo;
+    int E, rows, x_rows, K, N;
+    void *out;                // [rows, N] bf16 or fp32, rows ldo apart
+    int out_f32;
+    uint32_t *status;
+    uint32_t expire_ns;       // > 0: the first wait of `expire_role` gives up after this long (test hook)
+    int expire_role;
+};
+
+// Group e's rows, kept inside [0, rows] whatever the array holds.
+__device__ __forceinline__ int group_bound(const Params &p, int e)
+{
+    return p.offsets ? min(max(__ldg(p.offsets + e), 0), p.rows) : e * p.rows;
+}
+// x's row of grouped row r (an index out of range reads row 0: its row is undefined).
+__device__ __forceinline__ int source_row(const Params &p, int r)
+{
+    if (!p.perm_tok) return r;
+    const int t = __ldg(p.perm_tok + r);
+    return t >= 0 && t < p.x_rows ? t : 0;
+}
+
+// h = g / (1 + exp(-g)) u.  The fast form is off by (5 + 1.18 |g|) 2^-23 of itself
+// (__expf by 2 + 1.173 |g| units, sum, divide and product by the rest) and gives 0
+// from g = -87.4 down: against a bf16 output's half step of 2^-9 of the value that
+// is nothing.  fp32 outputs take the accurate exponential and divide.
+__device__ __forceinline__ float swiglu_fast(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+__device__ __forceinline__ float swiglu_accurate(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
+__device__ __forceinline__ void store_out(const Params &p, long long r, int n, float v)
+{
+    if (p.out_f32) static_cast<float *>(p.out)[r * p.ldo + n] = v;
+    else static_cast<__nv_bfloat16 *>(p.out)[r * p.ldo + n] = __float2bfloat16_rn(v);
+}
+
+// i8_vector.cu -- products of a few rows per group on the CUDA cores
+template <int MODE> cudaError_t launch_vector(const Params &p, cudaStream_t stream);
+
+}  // namespace i8
+}  // namespace moe

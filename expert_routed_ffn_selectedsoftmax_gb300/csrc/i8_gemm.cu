@@ -1,0 +1,106 @@
+// i8_gemm.cu -- products of int8 matrices with a scale for each token and each output
+// channel: the calls, and which kernel takes them.
+//
+//   y[r,n] = (sum_i cx[r,i] cw[n,i]) sx[r] sw[n]
+#include "i8.h"
+
+namespace moe {
+namespace i8 {
+
+template <int MODE> cudaError_t launch_product(const Params &p, void *workspace, cudaStream_t stream)
+{
+    (void)workspace;
+    return launch_vector<MODE>(p, stream);
+}
+
+bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// The checks the products share; MOE_OK with *go = false for an empty call.
+moe_status product_args(const Params &p, moe_dtype out_dt, const void *workspace, size_t ws_bytes, bool *go)
+{
+    *go = false;
+    if (p.x_rows < 0 || p.rows < 0 || p.K <= 0 || p.K % 16 || p.N <= 0 || p.E <= 0) return MOE_ERR_INVALID_ARG;
+    if (p.ldx < p.K || p.ldx % 16 || p.ldo < p.N) return MOE_ERR_INVALID_ARG;
+    if (out_dt != MOE_F32 && out_dt != MOE_BF16) return MOE_ERR_INVALID_ARG;
+    if (p.E > kMaxExperts) return MOE_ERR_UNSUPPORTED;
+    if (p.E > 1 && !p.offsets && p.rows > 0) return MOE_ERR_INVALID_ARG;
+    if (p.rows == 0) return MOE_OK;
+    if (!p.perm_tok && p.rows > p.x_rows) return MOE_ERR_INVALID_ARG;
+    if (p.x_rows == 0) return MOE_ERR_INVALID_ARG;
+    if (p.rows > INT32_MAX / 2 || p.x_rows > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
+    if (!p.x_q || !p.x_s || !p.w[0] || !p.w_s[0] || !p.w[1] || !p.w_s[1] || !p.out) return MOE_ERR_INVALID_ARG;
+    if (!aligned_to(p.x_q, 16) || !aligned_to(p.x_s, 4) || !aligned_to(p.offsets, 4) || !aligned_to(p.perm_tok, 4) ||
+        !aligned_to(p.status, 4) || !aligned_to(p.out, out_dt == MOE_F32 ? 4 : 2))
+        return MOE_ERR_INVALID_ARG;
+    for (int m = 0; m < 2; ++m)
+        if (!aligned_to(p.w[m], 16) || !aligned_to(p.w_s[m], 4)) return MOE_ERR_INVALID_ARG;
+    const size_t need = moe_i8_workspace_size(p.rows, p.K);
+    if (need && (!workspace || !aligned_to(workspace, 256))) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+    *go = true;
+    return MOE_OK;
+}
+
+template <int MODE>
+moe_status product(const void *x_q, const float *x_s, int x_rows, int K, long long ldx, const void *w0, const float *s0,
+                   const void *w1, const float *s1, int E, int N, const int32_t *offsets, const int32_t *perm_tok, int rows,
+                   void *out, moe_dtype out_dt, long long ldo, void *workspace, size_t ws_bytes, uint32_t *status,
+                   int expire_role, uint32_t expire_ns, moe_stream stream)
+{
+    Params p{};
+    p.x_q = static_cast<const int8_t *>(x_q); p.x_s = x_s;
+    p.w[0] = static_cast<const int8_t *>(w0); p.w[1] = static_cast<const int8_t *>(w1);
+    p.w_s[0] = s0; p.w_s[1] = s1;
+    p.offsets = offsets; p.perm_tok = perm_tok;
+    p.ldx = ldx; p.ldo = ldo;
+    p.E = E; p.rows = rows; p.x_rows = x_rows; p.K = K; p.N = N;
+    p.out = out; p.out_f32 = out_dt == MOE_F32;
+    p.status = status; p.expire_ns = expire_ns; p.expire_role = expire_role;
+    bool go;
+    const moe_status st = product_args(p, out_dt, workspace, ws_bytes, &go);
+    if (st != MOE_OK || !go) return st;
+    const cudaError_t e = launch_product<MODE>(p, workspace, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // namespace i8
+}  // namespace moe
+
+using namespace moe;
+using namespace moe::i8;
+
+extern "C" {
+
+size_t moe_i8_workspace_size(int rows, int K)
+{
+    if (rows < 0 || K <= 0 || K % 16) return 0;
+    return 0;
+}
+
+moe_status moe_grouped_gemm_i8(const void *x_q, const float *x_s, int x_rows, int K, long long ldx, const void *w_q,
+                               const float *w_s, int E, int N, const int32_t *offsets, const int32_t *perm_tok, int rows,
+                               void *out, moe_dtype out_dt, long long ldo, void *workspace, size_t ws_bytes,
+                               uint32_t *status, moe_stream stream)
+{
+    return product<PRODUCT>(x_q, x_s, x_rows, K, ldx, w_q, w_s, w_q, w_s, E, N, offsets, perm_tok, rows, out, out_dt, ldo,
+                            workspace, ws_bytes, status, 0, 0, stream);
+}
+
+moe_status moe_gemm_i8(const void *x_q, const float *x_s, int T, int K, long long ldx, const void *w_q, const float *w_s,
+                       int N, void *out, moe_dtype out_dt, long long ldo, void *workspace, size_t ws_bytes,
+                       uint32_t *status, moe_stream stream)
+{
+    return moe_grouped_gemm_i8(x_q, x_s, T, K, ldx, w_q, w_s, 1, N, nullptr, nullptr, T, out, out_dt, ldo, workspace,
+                               ws_bytes, status, stream);
+}
+
+moe_status moe_gate_up_i8(const void *x_q, const float *x_s, int x_rows, int d, long long ldx, const void *wg_q,
+                          const float *wg_s, const void *wu_q, const float *wu_s, int E, int F, const int32_t *offsets,
+                          const int32_t *perm_tok, int rows, void *h, moe_dtype h_dt, long long ldh, void *workspace,
+                          size_t ws_bytes, uint32_t *status, moe_stream stream)
+{
+    return product<GATEUP>(x_q, x_s, x_rows, d, ldx, wg_q, wg_s, wu_q, wu_s, E, F, offsets, perm_tok, rows, h, h_dt, ldh,
+                           workspace, ws_bytes, status, 0, 0, stream);
+}
+
+}  // extern "C"

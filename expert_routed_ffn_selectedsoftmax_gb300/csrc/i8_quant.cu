@@ -1,0 +1,213 @@
+// i8_quant.cu -- int8 codes of rows, one fp32 scale per row:
+//   s = max|x| / 127,   c = the whole number nearest to 127 x / max|x|, ties to even.
+//
+// The codes are those of the quotient itself, not of a rounded one: 127 / max|x| is
+// held in two fp32 numbers (a quotient and the quotient of its remainder, Dekker 1971),
+// so x times their sum is off by half a unit in the last place and little more.  A
+// bf16 quotient that is not a tie is at least 2^-17 of itself away from one (127 x and
+// max|x| have short significands), so its rounding cannot reach it, and a tie is exact;
+// an fp32 quotient that comes out within 2^-15 of a tie is compared with it in 64
+// bits, where both sides are exact (31 and 32 bits).
+//
+// What bounds it: memory.  Every value is read once into registers and stays there
+// between the maximum and the codes.
+#include <type_traits>
+
+#include "i8.h"
+
+namespace moe {
+namespace i8 {
+
+constexpr float kCodeMax = 127.0f;
+constexpr float kMinNormal = 1.17549435e-38f;   // 2^-126
+constexpr uint32_t kInfBits = 0x7f800000u;
+constexpr int kQuantThreads = 512;              // most of a CTA
+
+// |v| as bits: their order is that of the magnitudes, infinity above every finite
+// value and NaN above infinity, so a maximum does not lose a NaN.
+__device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// Eight values as loaded.
+template <typename XT> struct Raw8;
+template <> struct Raw8<float> {
+    uint4 a, b;
+    __device__ __forceinline__ void load(const float *p)
+    {
+        a = __ldg(reinterpret_cast<const uint4 *>(p));
+        b = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+    }
+    __device__ __forceinline__ void zero() { a = b = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ float get(int i) const
+    {
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        return __uint_as_float(w[i]);
+    }
+    __device__ __forceinline__ uint32_t max_bits() const
+    {
+        uint32_t m = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, mag_bits(get(i)));
+        return m;
+    }
+};
+template <> struct Raw8<__nv_bfloat16> {
+    uint4 a;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = __ldg(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ float get(int i) const
+    {
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+        return (i & 1) ? bf16hi(w[i >> 1]) : bf16lo(w[i >> 1]);
+    }
+    __device__ __forceinline__ uint32_t max_bits() const
+    {
+        const uint32_t k = 0x7fff7fffu;
+        const uint32_t m = __vmaxu2(__vmaxu2(a.x & k, a.y & k), __vmaxu2(a.z & k, a.w & k));
+        return max(m << 16, m & 0xffff0000u);
+    }
+};
+
+// What takes a row's values to codes.
+struct Factor {
+    float hi, lo, top;   // 127 / max|x| = hi + lo; zeros for a row of zero codes
+};
+__device__ __forceinline__ Factor factor_of(uint32_t top_bits, float &scale)
+{
+    const float top = __uint_as_float(top_bits);
+    Factor f{0.f, 0.f, top};
+    scale = top / kCodeMax;
+    if (top_bits >= kInfBits) {          // an infinity or a NaN: NaN scale, zero codes
+        scale = __uint_as_float(0x7fffffffu);
+    } else if (scale < kMinNormal) {     // (so that 127 / max|x| is finite)
+        scale = 0.f;
+    } else {
+        f.hi = kCodeMax / top;
+        f.lo = fmaf(-f.hi, top, kCodeMax) / top;
+    }
+    return f;
+}
+template <typename XT> __device__ __forceinline__ int code_of(float x, const Factor &f)
+{
+    // (a row of zero codes: an infinity times 0 would be NaN, whose code is 0 too)
+    const float q = fmaf(x, f.hi, x * f.lo);
+    int c = __float2int_rn(q);
+    if (std::is_same<XT, float>::value) {
+        const float m = fabsf(q), low = floorf(m);
+        if (fabsf(m - low - 0.5f) < 0x1p-15f) {
+            const double left = 127.0 * (double)fabsf(x), right = ((double)low + 0.5) * (double)f.top;
+            const int l = (int)low, n = left > right ? l + 1 : left < right ? l : l + (l & 1);
+            c = x < 0.f ? -n : n;
+        }
+    }
+    return c;
+}
+template <typename XT> __device__ __forceinline__ uint2 codes_of(const Raw8<XT> &r, const Factor &f)
+{
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i >> 2] |= ((uint32_t)code_of<XT>(r.get(i), f) & 0xffu) << (8 * (i & 3));
+    return make_uint2(w[0], w[1]);
+}
+
+// `lanes` threads (a multiple of 32) to a row, NV chunks of 8 values each, all in
+// registers; rows wider than that (LONG) are read a second time.
+template <typename XT, int NV, bool LONG>
+__global__ void __launch_bounds__(kQuantThreads)
+quant_rows_kernel(const XT *__restrict__ x, long long rows, int cols, long long ldx, int lanes,
+                  uint8_t *__restrict__ codes, float *__restrict__ scales)
+{
+    pdl_enter();
+    __shared__ uint32_t part[kQuantThreads / 32];
+    const int group = threadIdx.x / lanes, lane = threadIdx.x - group * lanes;
+    const long long row = (long long)blockIdx.x * (blockDim.x / lanes) + group;
+    const int chunks = cols / 8;
+    Raw8<XT> r[NV];
+    uint32_t m = 0u;
+    if (row < rows) {
+        const XT *p = x + row * ldx;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = lane + i * lanes;
+            if (c < chunks) r[i].load(p + c * 8);
+            else r[i].zero();
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) m = max(m, r[i].max_bits());
+        if (LONG) {
+            for (int c = lane + NV * lanes; c < chunks; c += lanes) {
+                Raw8<XT> v;
+                v.load(p + (long long)c * 8);
+                m = max(m, v.max_bits());
+            }
+        }
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (lanes > 32) {   // (uniform over the CTA)
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+        __syncthreads();
+        const int n = lanes >> 5, l = threadIdx.x & 31;
+        m = __reduce_max_sync(0xffffffffu, l < n ? part[group * n + l] : 0u);
+    }
+    if (row >= rows) return;
+    float scale;
+    const Factor f = factor_of(m, scale);
+    uint8_t *o = codes + row * cols;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = lane + i * lanes;
+        if (c < chunks) *reinterpret_cast<uint2 *>(o + c * 8) = codes_of<XT>(r[i], f);
+    }
+    if (LONG) {
+        const XT *p = x + row * ldx;
+        for (int c = lane + NV * lanes; c < chunks; c += lanes) {
+            Raw8<XT> v;
+            v.load(p + (long long)c * 8);
+            *reinterpret_cast<uint2 *>(o + (long long)c * 8) = codes_of<XT>(v, f);
+        }
+    }
+    if (lane == 0) scales[row] = scale;
+}
+
+template <typename XT>
+cudaError_t launch_quant(const void *x, int rows, int cols, long long ldx, uint8_t *codes, float *scales, cudaStream_t s)
+{
+    constexpr int kMost = sizeof(XT) == 4 ? 4 : 8;   // chunks a thread holds: 32 registers
+    const int chunks = cols / 8;
+    // A warp to a row while there are rows for a warp on every scheduler (no barrier,
+    // several chunks in flight a thread), else as many threads as chunks: few rows
+    // are latency.
+    int lanes = rows >= 16 * device_sm_count() ? ceil_div(chunks, kMost) : chunks;
+    lanes = (int)align_up((size_t)(lanes < kQuantThreads ? lanes : kQuantThreads), 32);
+    const int nv = ceil_div(chunks, lanes), threads = lanes < 128 ? 128 / lanes * lanes : lanes;
+    const int per = threads / lanes;
+    auto go = [&](auto kern) {
+        return launch_pdl(kern, dim3((unsigned)(((long long)rows + per - 1) / per)), dim3(threads), 0, s,
+                          static_cast<const XT *>(x), (long long)rows, cols, ldx, lanes, codes, scales);
+    };
+    if (nv <= 1) return go(quant_rows_kernel<XT, 1, false>);
+    if (nv <= 2) return go(quant_rows_kernel<XT, 2, false>);
+    if (nv <= 4) return go(quant_rows_kernel<XT, 4, false>);
+    if (nv <= kMost) return go(quant_rows_kernel<XT, kMost, false>);
+    return go(quant_rows_kernel<XT, kMost, true>);
+}
+
+}  // namespace i8
+}  // namespace moe
+
+using namespace moe;
+using namespace moe::i8;
+
+extern "C" moe_status moe_quant_i8(const void *x, moe_dtype x_dt, int rows, int cols, long long ldx, int8_t *codes,
+                                   float *scales, moe_stream stream)
+{
+    auto aligned = [](const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; };
+    if (rows < 0 || cols <= 0 || cols % 16 || (x_dt != MOE_F32 && x_dt != MOE_BF16)) return MOE_ERR_INVALID_ARG;
+    if (ldx < cols || ldx % 8) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (!x || !codes || !scales || !aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint8_t *q = reinterpret_cast<uint8_t *>(codes);
+    const cudaError_t e = x_dt == MOE_F32 ? launch_quant<float>(x, rows, cols, ldx, q, scales, s)
+                                          : launch_quant<__nv_bfloat16>(x, rows, cols, ldx, q, scales, s);
+    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}

@@ -564,6 +564,137 @@ MOE_API moe_status moe_gate_up_fp8b(const void *x_q, const float *x_s, int x_row
                                     uint32_t *status, moe_stream stream);
 
 /*
+ * Rows to their experts and back.  (No counterpart on the source pages, where they are
+ * parts of the layer: additions of this library for callers that compute the experts'
+ * products themselves, in another format or with a backward pass.)
+ *   inv [T*k] names the grouped row of each slot (t, j), as moe_permute writes it.  A
+ *   value outside [0, rows) is a slot without a row (an expert id that the grouping left
+ *   out, a token dropped by the caller): it adds nothing, nothing is written for it, and
+ *   its weight's gradient is 0.  Within a call that writes grouped rows (moe_dispatch,
+ *   moe_combine_backward) the rows that inv names are distinct; grouped rows that no slot
+ *   names are left as they were.
+ *   Matrices are fp32 or bf16, rows `ld` elements apart (ld >= d), of any width d >= 1 and
+ *   alignment of their type; widths and distances that are multiples of 8 with 16-byte
+ *   aligned pointers move 16 bytes at a time.  Sums run over the slots in order, in
+ *   fp32, and are rounded once; every call gives bitwise identical results from run to
+ *   run.  k in 1..8.  No output may overlap an input or another output.
+ */
+
+/*
+ * moe_dispatch -- out[inv[t*k + j]] = x[t]: tokens into grouped order.  x [T, d],
+ *   out [rows, d], both of type dt.
+ */
+MOE_API moe_status moe_dispatch(const void *x, moe_dtype dt, int T, int d, long long ldx,
+                                const int32_t *inv, int k, void *out, int rows, long long ldo,
+                                moe_stream stream);
+
+/*
+ * moe_dispatch_backward -- its gradient: dx[t] = sum_j grad[inv[t*k + j]].
+ *   grad [rows, d], dx [T, d], both of type dt.
+ */
+MOE_API moe_status moe_dispatch_backward(const void *grad, moe_dtype dt, int rows, int d,
+                                         long long ldg, const int32_t *inv, int T, int k, void *dx,
+                                         long long ldx, moe_stream stream);
+
+/*
+ * moe_combine -- out[t] = sum_j topk_w[t,j] y[inv[t*k + j]]: the experts' outputs back
+ *   to tokens.  y [rows, d] of type y_dt, topk_w [T, k] fp32 (moe_route), out [T, d] of
+ *   type out_dt.
+ */
+MOE_API moe_status moe_combine(const void *y, moe_dtype y_dt, int rows, int d, long long ldy,
+                               const float *topk_w, const int32_t *inv, int T, int k, void *out,
+                               moe_dtype out_dt, long long ldo, moe_stream stream);
+
+/*
+ * moe_combine_backward -- its gradients:
+ *     dy[inv[t*k + j]] = topk_w[t,j] grad[t],   dw[t,j] = sum_i grad[t,i] y[inv[t*k + j],i]
+ *   grad [T, d] of type grad_dt; y [rows, d] of type y_dt; dy [rows, d] of type y_dt, or
+ *   NULL; dw [T, k] fp32, or NULL (y may then be NULL).
+ */
+MOE_API moe_status moe_combine_backward(const void *grad, moe_dtype grad_dt, int T, int d,
+                                        long long ldg, const void *y, moe_dtype y_dt, int rows,
+                                        long long ldy, const float *topk_w, const int32_t *inv,
+                                        int k, void *dy, long long lddy, float *dw,
+                                        moe_stream stream);
+
+/*
+ * 8-bit integer operators ("i8"): the expert FFN with int8 codes on both sides of its
+ * products and one fp32 scale per row (a token of activations, an output channel of
+ * weights), as separate calls around moe_route, moe_permute and moe_combine.  (No
+ * counterpart on the source pages: an addition of this library, beside the weight-only
+ * MOE_Q8_0 experts of moe_forward.)
+ *
+ * A matrix is int8 codes, row-major, value = code * scale: activations [rows, K] with
+ * scales [rows], weights [E, N, K] with scales [E, N].  K (d) is a multiple of 16.  Code
+ * buffers are 16-byte aligned, scales 4-byte.
+ * Quantisation of a row: s = max|x| / 127, code = the whole number nearest to
+ * 127 x / max|x|, ties to even, of the exact quotient.  All zeros, or so small that s
+ * would be below 2^-126: s = 0, codes 0.  A row that holds an infinity or NaN: s = NaN,
+ * codes 0.
+ * Products: out[r,n] = (sum_i x_q[r,i] w_q[n,i]) x_s[r] w_s[n].  Any code from -128 to 127
+ * is taken.  The codes' products are summed exactly while the sums stay below 2^24 in
+ * magnitude (any row up to K = 1024), and otherwise to fp32's accuracy; the two scales
+ * are multiplied in one after the other, fp32, rounded each time.
+ *
+ * Failure handling, `status` and reproducibility as the block-scaled fp8 operators (a row
+ * whose wait gave up is NaN).  No output may overlap an input or another output.
+ */
+
+/*
+ * moe_quant_i8 -- codes [rows, cols] and scales [rows] of x [rows, cols] (fp32 or bf16; rows
+ *   ldx elements apart, ldx >= cols and a multiple of 8; cols a multiple of 16; 16-byte
+ *   aligned).  Weights [E, N, K] are E*N rows.
+ */
+MOE_API moe_status moe_quant_i8(const void *x, moe_dtype x_dt, int rows, int cols, long long ldx,
+                                int8_t *codes, float *scales, moe_stream stream);
+
+/*
+ * Bytes of device workspace that the products of `rows` rows of K columns need, 256-byte
+ * aligned, not shared by calls that can overlap (0: none, and NULL is taken; also 0 on
+ * invalid sizes).
+ */
+MOE_API size_t moe_i8_workspace_size(int rows, int K);
+
+/*
+ * moe_gemm_i8 -- out[T, N] = x W^T.  x_q [T, K] codes (rows ldx bytes apart, ldx a
+ *   multiple of 16), x_s [T]; w_q [N, K], w_s [N]; out fp32 or bf16 (out_dt), rows ldo
+ *   elements apart.  Any N >= 1.
+ */
+MOE_API moe_status moe_gemm_i8(const void *x_q, const float *x_s, int T, int K, long long ldx,
+                               const void *w_q, const float *w_s, int N, void *out,
+                               moe_dtype out_dt, long long ldo, void *workspace, size_t ws_bytes,
+                               uint32_t *status, moe_stream stream);
+
+/*
+ * moe_grouped_gemm_i8 -- the product of every expert with its rows:
+ *     out[r] = x[perm_tok[r]] W[e]^T   for r in [offsets[e], offsets[e+1])
+ *   w_q [E, N, K], w_s [E, N], E <= 256.  offsets, perm_tok, rows and what is left as it
+ *   was: as moe_grouped_gemm_fp8b; the other arguments as moe_gemm_i8.
+ */
+MOE_API moe_status moe_grouped_gemm_i8(const void *x_q, const float *x_s, int x_rows, int K,
+                                       long long ldx, const void *w_q, const float *w_s, int E,
+                                       int N, const int32_t *offsets, const int32_t *perm_tok,
+                                       int rows, void *out, moe_dtype out_dt, long long ldo,
+                                       void *workspace, size_t ws_bytes, uint32_t *status,
+                                       moe_stream stream);
+
+/*
+ * moe_gate_up_i8 -- both products of a SwiGLU expert and its h:
+ *     h[r] = SiLU(W_g[e] x[perm_tok[r]]) * (W_u[e] x[perm_tok[r]])
+ *   h [rows, F] fp32 or bf16 (h_dt), rows ldh elements apart, any F >= 1 (moe_quant_i8 takes it
+ *   to the down projection: a row's scale needs all of its F values).  wg_q, wu_q
+ *   [E, F, d] with scales [E, F].  In bf16 SiLU(g) is taken to (5 + 1.18 |g|) 2^-23 of
+ *   itself, and to 0 below about g = -87.  Groups, perm_tok and rows as
+ *   moe_grouped_gemm_i8 (E == 1 with offsets NULL is the dense layer's).
+ */
+MOE_API moe_status moe_gate_up_i8(const void *x_q, const float *x_s, int x_rows, int d,
+                                  long long ldx, const void *wg_q, const float *wg_s,
+                                  const void *wu_q, const float *wu_s, int E, int F,
+                                  const int32_t *offsets, const int32_t *perm_tok, int rows,
+                                  void *h, moe_dtype h_dt, long long ldh, void *workspace,
+                                  size_t ws_bytes, uint32_t *status, moe_stream stream);
+
+/*
  * Test hook of the failure handling.  Every wait of the library's
  * tensor-core kernels is bounded (2 s); a wait that gives up records
  * MOE_ERR_TIMEOUT in the status word, the kernel's other roles stop, its
