@@ -1,5 +1,6 @@
 // fp8b_tc.cuh -- what the kernels of the block-scaled fp8 products share:
-// parameters, tcgen05 kind::f8f6f4, tensor maps.
+// parameters, tcgen05 kind::f8f6f4, tensor maps; the groups of a call and their tiles
+// serve the int8 products too.
 #pragma once
 
 #include <cuda.h>
@@ -132,14 +133,15 @@ struct Groups {
 };
 // Group bounds, kept inside [0, rows] whatever the array holds (every thread of
 // the CTA; a barrier before scan_groups).
-__device__ __forceinline__ void load_groups(Groups &g, const Params &p)
+template <typename P> __device__ __forceinline__ void load_groups(Groups &g, const P &p)
 {
     for (int e = threadIdx.x; e <= p.E; e += blockDim.x)
         g.off[e] = p.offsets ? min(max(p.offsets[e], 0), p.rows) : e * p.rows;
 }
 // Exclusive scan of row tiles (of `rows_per_tile`) * column tiles over the
 // experts, 8 to a lane (one warp).
-__device__ __forceinline__ void scan_groups(Groups &g, const Params &p, int rows_per_tile, int lane)
+template <typename P>
+__device__ __forceinline__ void scan_groups(Groups &g, const P &p, int rows_per_tile, int lane)
 {
     int local[8], sum = 0;
 #pragma unroll

@@ -23,6 +23,8 @@ struct Params {
     int E, rows, x_rows, K, N;
     void *out;                // [rows, N] bf16 or fp32, rows ldo apart
     int out_f32;
+    int n_tiles;              // column tiles (the tensor-core kernels)
+    int split;                // CTAs of a cluster that share a reduction (i8_tc.cu)
     uint32_t *status;
     uint32_t expire_ns;       // > 0: the first wait of `expire_role` gives up after this long (test hook)
     int expire_role;
@@ -41,12 +43,14 @@ __device__ __forceinline__ int source_row(const Params &p, int r)
     return t >= 0 && t < p.x_rows ? t : 0;
 }
 
-// h = g / (1 + exp(-g)) u.  The fast form is off by (5 + 1.18 |g|) 2^-23 of itself
-// (__expf by 2 + 1.173 |g| units, sum, divide and product by the rest) and gives 0
-// from g = -87.4 down: against a bf16 output's half step of 2^-9 of the value that
-// is nothing.  fp32 outputs take the accurate exponential and divide.
+// h = g / (1 + exp(-g)) u.  With the fast exponential h is off by (5 + 1.18 |g|) 2^-23 of
+// itself (__expf by 2 + 1.173 |g| units in the last place, sum, divide and product by the
+// rest), nothing beside a bf16 output's half step of 2^-9; fp32 outputs take expf, 5
+// units in all.  From g = -87.4 down the divisor is above 2^126, where __fdividef gives
+// 0.  (A true divide is a call where its operands are extreme, and across a call the sums
+// do not stay in the registers that setmaxnreg gives.)
 __device__ __forceinline__ float swiglu_fast(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
-__device__ __forceinline__ float swiglu_accurate(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+__device__ __forceinline__ float swiglu_accurate(float g, float u) { return __fdividef(g, 1.0f + expf(-g)) * u; }
 
 __device__ __forceinline__ void store_out(const Params &p, long long r, int n, float v)
 {
@@ -56,6 +60,12 @@ __device__ __forceinline__ void store_out(const Params &p, long long r, int n, f
 
 // i8_vector.cu -- products of a few rows per group on the CUDA cores
 template <int MODE> cudaError_t launch_vector(const Params &p, cudaStream_t stream);
+
+// i8_tc.cu -- the products on the tensor cores: tiles of 128 rows (their codes as fp16
+// in `workspace`), or of few rows
+size_t tiled_workspace(int rows, int K);
+template <int MODE> cudaError_t launch_tiled(const Params &p, void *workspace, cudaStream_t stream);
+template <int MODE> cudaError_t launch_few(const Params &p, cudaStream_t stream);
 
 }  // namespace i8
 }  // namespace moe

@@ -2,15 +2,28 @@
 // channel: the calls, and which kernel takes them.
 //
 //   y[r,n] = (sum_i cx[r,i] cw[n,i]) sx[r] sw[n]
+#ifdef I8_FORCE
+#include <stdlib.h>
+#endif
 #include "i8.h"
 
 namespace moe {
 namespace i8 {
 
+constexpr int kFewRows = 32;   // up to here no call takes the tiled kernel, and none needs a workspace
+
 template <int MODE> cudaError_t launch_product(const Params &p, void *workspace, cudaStream_t stream)
 {
-    (void)workspace;
-    return launch_vector<MODE>(p, stream);
+#ifdef I8_FORCE
+    const char *f = getenv("I8_FORCE");
+    if (f && *f == 'v') return launch_vector<MODE>(p, stream);
+    if (f && *f == 'f') return launch_few<MODE>(p, stream);
+    if (f && *f == 't' && p.rows > kFewRows) return launch_tiled<MODE>(p, workspace, stream);
+#endif
+    const long long experts = p.E < p.rows ? p.E : p.rows;
+    if (p.rows <= 2 * experts && p.rows <= 64) return launch_vector<MODE>(p, stream);
+    if (p.rows <= kFewRows || p.rows <= 16 * experts) return launch_few<MODE>(p, stream);
+    return launch_tiled<MODE>(p, workspace, stream);
 }
 
 bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -73,8 +86,8 @@ extern "C" {
 
 size_t moe_i8_workspace_size(int rows, int K)
 {
-    if (rows < 0 || K <= 0 || K % 16) return 0;
-    return 0;
+    if (rows <= kFewRows || K <= 0 || K % 16) return 0;
+    return tiled_workspace(rows, K);
 }
 
 moe_status moe_grouped_gemm_i8(const void *x_q, const float *x_s, int x_rows, int K, long long ldx, const void *w_q,
