@@ -22,7 +22,7 @@ struct Params {
     long long ldx, ldo;
     int E, rows, x_rows, K, N;
     void *out;                // [rows, N] bf16 or fp32, rows ldo apart
-    int out_f32;
+    int out_f32, out_vec;     // out_vec: rows begin and end on 16-byte boundaries
     int n_tiles;              // column tiles (the tensor-core kernels)
     int split;                // CTAs of a cluster that share a reduction (i8_tc.cu)
     uint32_t *status;

@@ -68,6 +68,8 @@ moe_status product(const void *x_q, const float *x_s, int x_rows, int K, long lo
     p.ldx = ldx; p.ldo = ldo;
     p.E = E; p.rows = rows; p.x_rows = x_rows; p.K = K; p.N = N;
     p.out = out; p.out_f32 = out_dt == MOE_F32;
+    const int v = out_dt == MOE_F32 ? 4 : 8;
+    p.out_vec = N % v == 0 && ldo % v == 0 && aligned_to(out, 16);
     p.status = status; p.expire_ns = expire_ns; p.expire_role = expire_role;
     bool go;
     const moe_status st = product_args(p, out_dt, workspace, ws_bytes, &go);

@@ -17,12 +17,14 @@
 //             weight rows a tile (or of both); two CTAs an SM.  Few tiles split the
 //             reduction over a cluster, whose partial sums meet in distributed shared
 //             memory.
-// Every unit of conversion is 128 weight rows x 64 columns, and a stage of the ring holds
-// two: both weight tiles' (BK = 64), or both halves of one tile's (BK = 128).
+// A stage of the reduction is 128 x 128 codes of weights: 64 columns of two tiles, or 128
+// of one.  Weights and tokens have rings of their own, as the converters are done with
+// the former long before the MMAs are with the latter.
 //
-// Warp 0 loads, warp 1 multiplies, warps 4.. (4 or 8) write the output, the last 8
-// convert.  A thread of the output warps holds an output channel; a token's values are
-// contiguous over the warp, so they are stored from registers.
+// Warp 0 loads weights, warp 3 tokens (one warp for both issued its loads in 930 clocks a
+// stage, where the MMAs take 512), warps 1 and 2 multiply a weight tile each, the last 8
+// warps convert, four of them a stage, and warps 4.. (4 or 16) write the output.  A
+// thread of these holds an output channel; a token's values lie along the warp.
 //
 // Every wait is bounded (2 s).  Where one gives up, the rows of the CTA's remaining
 // tiles are written as NaN, and the status word says so if the caller passed one.
@@ -48,19 +50,20 @@ using fp8b::tma_load_3d;
 namespace {
 
 constexpr int M = 128;                       // weight rows of an MMA
-constexpr int kUnitCols = 32;                // TMEM columns of a converted unit (64 codes as fp16)
-constexpr int kConvWarps = 8;                // two groups of four, a unit of each stage to a group
+constexpr int kUnitCols = 32;                // TMEM columns of 64 codes as fp16
+constexpr int kStageCols = 2 * kUnitCols;    // ... of a stage's weights
+constexpr int kConvWarps = 8;                // two groups of four, which take the stages in turn
 
 template <int MODE, bool FEW> struct Cfg {
     static constexpr int NW = (MODE == GATEUP || !FEW) ? 2 : 1;    // weight tiles of a stage
     static constexpr int BK = NW == 2 ? 64 : 128;
     static constexpr int NT = FEW ? 32 : 128;                      // tokens of a tile
     static constexpr int ROWS = MODE == PRODUCT ? NW * M : M;      // output channels of a tile
-    static constexpr int W_BYTES = NW * M * BK;
+    static constexpr int W_BYTES = NW * M * BK;                    // 16 KB
     static constexpr int X_BYTES = NT * BK * (FEW ? 1 : 2);
-    static constexpr int STAGE = W_BYTES + X_BYTES;
-    static constexpr int STAGES = FEW ? (MODE == GATEUP ? 5 : 4) : 6;
-    static constexpr int NA = FEW ? 2 : 4;                         // converted stages in flight
+    static constexpr int WS = FEW ? (MODE == GATEUP ? 5 : 4) : 5;  // stages of the weights' ring
+    static constexpr int XS = FEW ? 4 : 8;                         // ... of the tokens'
+    static constexpr int NA = FEW ? (MODE == GATEUP ? 2 : 3) : 4;  // converted stages in flight
     static constexpr int XF_BYTES = FEW ? NT * BK * 2 : 0;         // widened tokens of one
     static constexpr int ND = FEW ? 2 : 1;                         // accumulators
     static constexpr int D_COLS = NW * NT;
@@ -68,22 +71,25 @@ template <int MODE, bool FEW> struct Cfg {
     static constexpr int TMEM_COLS = FEW ? 256 : 512;
     static constexpr int EPI = FEW ? 4 : 16;                       // output warps
     static constexpr int THREADS = 128 + 32 * (EPI + kConvWarps);
-    static constexpr size_t RING = (size_t)STAGES * STAGE;
-    static constexpr size_t CTL = RING + (size_t)NA * XF_BYTES;
-    static_assert(A_COL + NA * 2 * kUnitCols <= TMEM_COLS, "tensor memory");
+    static constexpr size_t XRING = (size_t)WS * W_BYTES;
+    static constexpr size_t XF = XRING + (size_t)XS * X_BYTES;
+    static constexpr size_t CTL = XF + (size_t)NA * XF_BYTES;
+    static_assert(A_COL + NA * kStageCols <= TMEM_COLS, "tensor memory");
+    static_assert(!FEW || (size_t)NT * NW * M * 4 <= XRING, "split partial sums reuse the weights' ring");
 };
-constexpr int kMaxStages = 6, kMaxA = 4, kTable = 32;
+constexpr int kMaxW = 5, kMaxX = 8, kMaxA = 4, kTable = 32;
 
-struct alignas(16) Ctl {
-    uint64_t full[kMaxStages], empty[kMaxStages], cfull[kMaxA], cempty[kMaxA], dfull[2], dempty[2], drain;
+template <int EPI, int NT> struct alignas(16) Ctl {
+    uint64_t wfull[kMaxW], wempty[kMaxW], xfull[kMaxX], xempty[kMaxX], cfull[kMaxA], cempty[kMaxA], dfull[2], dempty[2], drain[2];
     uint64_t never;                          // nothing arrives here (test hook)
     uint32_t tmem_base;
     int abort_flag;
-    alignas(16) float sx[16][M];             // each output warp's token scales
+    alignas(16) float sx[EPI][NT];           // each output warp's token scales
     Groups g;
     Tile tiles[kTable];                      // this CTA's first tiles (each role asks for them in turn)
 };
-template <int MODE, bool FEW> constexpr size_t smem_bytes() { return 1024 + Cfg<MODE, FEW>::CTL + sizeof(Ctl); }
+template <int MODE, bool FEW> using CtlOf = Ctl<Cfg<MODE, FEW>::EPI, Cfg<MODE, FEW>::NT>;
+template <int MODE, bool FEW> constexpr size_t smem_bytes() { return 1024 + Cfg<MODE, FEW>::CTL + sizeof(CtlOf<MODE, FEW>); }
 static_assert(smem_bytes<PRODUCT, false>() <= 232448 && smem_bytes<GATEUP, false>() <= 232448, "shared memory per CTA");
 static_assert(smem_bytes<PRODUCT, true>() <= 115712 && smem_bytes<GATEUP, true>() <= 115712, "two CTAs per SM");
 // registers a thread after the split at start (setmaxnreg) of the tiled kernel: 28 warps
@@ -137,6 +143,45 @@ template <int BK> __device__ __forceinline__ int piece_at(int r, int c)
     return r * BK + ((BK == 64 ? c ^ ((r >> 1) & 3) : c ^ (r & 7)) << 4);
 }
 
+// Lane l holds channel l's values of 8 tokens, two of bf16 to a word; afterwards it holds
+// token l % 8's values of channels 8 (l / 8) .. + 7: a transpose, lane bit by lane bit.
+__device__ __forceinline__ void turn8(uint32_t (&w)[4], int lane)
+{
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, lane & 4 ? w[q] : w[q + 2], 4);
+        if (lane & 4) w[q] = got;
+        else w[q + 2] = got;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; q += 2) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, lane & 2 ? w[q] : w[q + 1], 2);
+        if (lane & 2) w[q] = got;
+        else w[q + 1] = got;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, w[q], 1);
+        w[q] = lane & 1 ? __byte_perm(got, w[q], 0x7632) : __byte_perm(w[q], got, 0x5410);
+    }
+}
+// The same of 4 tokens in fp32: token l % 4's values of channels 4 (l / 4) .. + 3.
+__device__ __forceinline__ void turn4(uint32_t (&w)[4], int lane)
+{
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, lane & 2 ? w[q] : w[q + 2], 2);
+        if (lane & 2) w[q] = got;
+        else w[q + 2] = got;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; q += 2) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, lane & 1 ? w[q] : w[q + 1], 1);
+        if (lane & 1) w[q] = got;
+        else w[q + 1] = got;
+    }
+}
+
 template <int MODE>
 __device__ __forceinline__ float finish(const Params &p, float a, float b, float sx, float sw0, float sw1)
 {
@@ -145,24 +190,65 @@ __device__ __forceinline__ float finish(const Params &p, float a, float b, float
     return p.out_f32 ? swiglu_accurate(g, u) : swiglu_fast(g, u);
 }
 
+// The warp's sums of COUNT tokens (a, and for gate/up b) of output channels n0 + lane:
+// scaled and stored.  `row`: the first token's output row; `cnt` of the tokens exist.
+// Rows on 16-byte boundaries are turned in registers so that a store covers 8 tokens x 64
+// bytes (fp32: 4 x 128) in pieces of 16; else a token at a time, an element a lane.
+template <int MODE, int COUNT>
+__device__ __forceinline__ void store_tokens(const Params &p, const uint32_t *a, const uint32_t *b, long long row, int cnt, int n0,
+                                             int lane, const float *sx, float sw0, float sw1)
+{
+    const auto value = [&](int q) { return finish<MODE>(p, __uint_as_float(a[q]), __uint_as_float(b[q]), sx[q], sw0, sw1); };
+    if (!p.out_vec) {
+#pragma unroll
+        for (int q = 0; q < COUNT; ++q)
+            if (q < cnt && n0 + lane < p.N) store_out(p, row + q, n0 + lane, value(q));
+    } else if (p.out_f32) {
+        const int n = n0 + (lane >> 2) * 4;
+        float *o = static_cast<float *>(p.out) + (row + (lane & 3)) * p.ldo + n;
+#pragma unroll
+        for (int q = 0; q < COUNT; q += 4) {
+            if (q >= cnt) break;
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = __float_as_uint(value(q + j));
+            turn4(w, lane);
+            if (q + (lane & 3) < cnt && n < p.N) *reinterpret_cast<uint4 *>(o + q * p.ldo) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    } else {
+        const int n = n0 + (lane >> 3) * 8;
+        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + (row + (lane & 7)) * p.ldo + n;
+#pragma unroll
+        for (int q = 0; q < COUNT; q += 8) {
+            if (q >= cnt) break;
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = fp8b::bf16x2(value(q + 2 * j), value(q + 2 * j + 1));
+            turn8(w, lane);
+            if (q + (lane & 7) < cnt && n < p.N) *reinterpret_cast<uint4 *>(o + q * p.ldo) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
 template <int MODE, bool FEW, bool SPLIT>
 __global__ void __launch_bounds__((Cfg<MODE, FEW>::THREADS), FEW ? 2 : 1)
 product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w0,
                const __grid_constant__ CUtensorMap tm_w1, const Params p)
 {
     using C = Cfg<MODE, FEW>;
-    constexpr int NW = C::NW, BK = C::BK, NT = C::NT, STAGES = C::STAGES, NA = C::NA;
+    constexpr int NW = C::NW, BK = C::BK, NT = C::NT, WS = C::WS, XS = C::XS, NA = C::NA;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    Ctl &c = *reinterpret_cast<Ctl *>(smem + C::CTL);
+    auto &c = *reinterpret_cast<CtlOf<MODE, FEW> *>(smem + C::CTL);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int E = p.E;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) { mbar_init(&c.full[s], 1); mbar_init(&c.empty[s], FEW ? kConvWarps : 1); }
-        for (int a = 0; a < NA; ++a) { mbar_init(&c.cfull[a], kConvWarps); mbar_init(&c.cempty[a], 1); }
-        for (int d = 0; d < C::ND; ++d) { mbar_init(&c.dfull[d], 1); mbar_init(&c.dempty[d], C::EPI); }
-        mbar_init(&c.drain, 1);
+        for (int s = 0; s < WS; ++s) { mbar_init(&c.wfull[s], 1); mbar_init(&c.wempty[s], 4); }
+        for (int s = 0; s < XS; ++s) { mbar_init(&c.xfull[s], 1); mbar_init(&c.xempty[s], FEW ? 4 : NW); }
+        for (int a = 0; a < NA; ++a) { mbar_init(&c.cfull[a], 4); mbar_init(&c.cempty[a], NW); }
+        for (int d = 0; d < C::ND; ++d) { mbar_init(&c.dfull[d], NW); mbar_init(&c.dempty[d], C::EPI); }
+        for (int w = 0; w < 2; ++w) mbar_init(&c.drain[w], 1);
         mbar_init(&c.never, 1);
         c.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -170,7 +256,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_w0)) : "memory");
         if (MODE == GATEUP) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_w1)) : "memory");
     }
-    if (warp == 2) tmem_alloc(&c.tmem_base, C::TMEM_COLS);
+    if (warp == 3) tmem_alloc(&c.tmem_base, C::TMEM_COLS);
     tc_fence_before();
     // (without offsets nothing up to here reads what the kernel before writes)
     if (p.offsets) pdl_enter();
@@ -203,77 +289,75 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
 
     if (warp < 4) {
         if (!FEW) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsAux));
-        if (warp == 0) {
-            // -------------------------------------------- loads
-            uint32_t it = 0;
+        if (warp == 0 || warp == 3) {
+            // -------------------------------------------- loads: weights, tokens
+            const bool weights = warp == 0;
+            const int stages = weights ? WS : XS;
+            uint64_t *full = weights ? c.wfull : c.xfull, *empty = weights ? c.wempty : c.xempty;
+            uint8_t *ring = smem + (weights ? 0 : C::XRING);
+            uint32_t s = 0, phase = 0;
             ok = !expires(p, LOADS) || __all_sync(0xffffffffu, bar_wait(&c.never, 0, abort_flag, p.expire_ns));
             for (int t = first, i = 0; t < total && ok; t += stride, ++i) {
                 const Tile tile = nth_tile(i, t);
                 const int n0 = tile.nt * C::ROWS;
                 int4 tok = make_int4(0, 0, 0, 0);
-                const int gathers = FEW && p.perm_tok ? (tile.cnt + 3) / 4 : 0;
+                const int gathers = FEW && p.perm_tok && !weights ? (tile.cnt + 3) / 4 : 0;
                 if (FEW && lane < gathers) {
                     int v[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) v[q] = source_row(p, tile.row0 + min(4 * lane + q, tile.cnt - 1));
                     tok = make_int4(v[0], v[1], v[2], v[3]);
                 }
-                // token rows in boxes: only as many as the tile has (tiled)
-                constexpr int XBOX = FEW ? NT : 64;
-                const int boxes = FEW ? 1 : (tile.cnt + XBOX - 1) / XBOX;
-                const uint32_t bytes = C::W_BYTES + (FEW && p.perm_tok ? gathers * 4 * BK : boxes * XBOX * BK * (FEW ? 1 : 2));
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const int s = it % STAGES;
-                    ok = __all_sync(0xffffffffu, bar_wait(&c.empty[s], ((it / STAGES) & 1u) ^ 1u, abort_flag));
+                const uint32_t bytes = weights ? C::W_BYTES : gathers ? gathers * 4 * BK : C::X_BYTES;
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    ok = __all_sync(0xffffffffu, bar_wait(&empty[s], phase ^ 1u, abort_flag));
                     if (!ok) break;
-                    uint8_t *sw = smem + s * C::STAGE, *sx = sw + C::W_BYTES;
-                    if (lane == 0) {
-                        mbar_expect_tx(&c.full[s], bytes);
-                        tma_load_3d(sw, &tm_w0, &c.full[s], kb * BK, n0, tile.e);
-                        if (MODE == GATEUP) tma_load_3d(sw + M * BK, &tm_w1, &c.full[s], kb * BK, n0, tile.e);
-                        if (!gathers)
-                            for (int b = 0; b < boxes; ++b)
-                                tma_load_2d(sx + b * XBOX * 128, &tm_x, &c.full[s], kb * BK, tile.row0 + b * XBOX);
+                    uint8_t *at = ring + s * (weights ? C::W_BYTES : C::X_BYTES);
+                    if (elect_one()) {
+                        mbar_expect_tx(&full[s], bytes);
+                        if (weights) {
+                            tma_load_3d(at, &tm_w0, &full[s], kb * BK, n0, tile.e);
+                            if (MODE == GATEUP) tma_load_3d(at + M * BK, &tm_w1, &full[s], kb * BK, n0, tile.e);
+                        } else if (!gathers) {
+                            tma_load_2d(at, &tm_x, &full[s], kb * BK, tile.row0);
+                        }
                     }
                     __syncwarp();
-                    if (FEW && lane < gathers) tma_gather4(sx + lane * 4 * BK, &tm_x, &c.full[s], kb * BK, tok);
+                    if (FEW && lane < gathers) tma_gather4(at + lane * 4 * BK, &tm_x, &full[s], kb * BK, tok);
+                    ++issued;
+                    if (++s == (uint32_t)stages) { s = 0; phase ^= 1u; }
                 }
             }
             if (!ok) {
                 if (lane == 0) flag_status(p.status, kDevTimeout);
                 c.abort_flag = 1;
             }
-            issued = it;
-        } else if (warp == 1) {
-            // -------------------------------------------- multiply
+        } else if (warp <= NW) {
+            // -------------------------------------------- multiply: a weight tile to a warp
             const bool leader = elect_one();
-            const uint32_t ring = smem_u32(smem);
+            const int w = warp - 1;
+            const uint32_t tokens = smem_u32(smem + (FEW ? C::XF : C::XRING));
             uint32_t it = 0;
             for (int t = first, i = 0; t < total && ok; t += stride, ++i) {
                 const Tile tile = nth_tile(i, t);
                 // (N: as many columns as the tile has tokens, in sixteens)
                 const uint32_t idesc = idesc_f16_mn(1, M, (tile.cnt + 15) & ~15);
                 const int db = i % C::ND;
-                const uint32_t d = tmem + db * C::D_COLS;
+                const uint32_t d = tmem + db * C::D_COLS + w * NT;
                 ok = bar_wait(&c.dempty[db], ((i / C::ND) & 1u) ^ 1u, abort_flag);
                 for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
-                    const int s = it % STAGES, a = it % NA;
-                    ok = bar_wait(&c.cfull[a], (it / NA) & 1u, abort_flag);
-                    // (the converters have seen the stage land; its fp16 tokens are this warp's to see)
-                    if (!FEW) ok = ok && bar_wait(&c.full[s], (it / STAGES) & 1u, abort_flag);
+                    const uint32_t s = it % XS, a = it % NA;
+                    ok = (FEW || bar_wait(&c.xfull[s], (it / XS) & 1u, abort_flag)) &&
+                         bar_wait(&c.cfull[a], (it / NA) & 1u, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint64_t dx = sw128_desc(FEW ? ring + (uint32_t)C::RING + a * C::XF_BYTES : ring + s * C::STAGE + C::W_BYTES);
-                    const uint32_t at = tmem + C::A_COL + a * 2 * kUnitCols;
+                    const uint64_t dx = sw128_desc(tokens + (FEW ? a * C::XF_BYTES : s * C::X_BYTES));
+                    const uint32_t at = tmem + C::A_COL + a * kStageCols + (NW == 2 ? w * kUnitCols : 0);
                     if (leader) {
 #pragma unroll
-                        for (int kk = 0; kk < BK / 16; ++kk) {
-                            const uint64_t dk = desc_step(dx, (kk / 4) * NT * 128 + (kk % 4) * 32);
-#pragma unroll
-                            for (int w = 0; w < NW; ++w)
-                                umma_f16_ts(d + w * NT, at + (NW == 2 ? w * kUnitCols : 0) + kk * 8, dk, idesc, kb != kb0 || kk != 0);
-                        }
-                        if (!FEW) umma_commit(&c.empty[s]);
+                        for (int kk = 0; kk < BK / 16; ++kk)
+                            umma_f16_ts(d, at + kk * 8, desc_step(dx, (kk / 4) * NT * 128 + (kk % 4) * 32), idesc, kb != kb0 || kk != 0);
+                        if (!FEW) umma_commit(&c.xempty[s]);
                         umma_commit(&c.cempty[a]);
                         if (kb == kb1 - 1) umma_commit(&c.dfull[db]);
                     }
@@ -289,50 +373,61 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     } else if (warp >= 4 + C::EPI) {
         // ------------------------------------------------ convert
         if (!FEW) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
-        const int tid = threadIdx.x - 128 - 32 * C::EPI;
-        const int unit = tid >> 7, quad = warp & 3, row = quad * 32 + lane;
-        const uint32_t mine = tmem + ((uint32_t)(quad * 32) << 16) + C::A_COL + unit * kUnitCols;
-        // this thread's 64 codes: row `row` of weight tile `unit`, or half `unit` of its row
-        const int tile_off = NW == 2 ? unit * M * BK : 0, piece0 = NW == 2 ? 0 : unit * 4;
+        // Warps of a group of four take every second stage: a thread row `row` of both
+        // weight tiles, or all of its row, and a piece or two of the tokens.
+        const int tid = (threadIdx.x - 128 - 32 * C::EPI) & 127, group = (warp - 4 - C::EPI) >> 2;
+        const int quad = warp & 3, row = quad * 32 + lane;
+        const uint32_t mine = tmem + ((uint32_t)(quad * 32) << 16) + C::A_COL;
         uint32_t it = 0;
         ok = !expires(p, CONVERT) || __all_sync(0xffffffffu, bar_wait(&c.never, 0, abort_flag, p.expire_ns));
         for (int t = first; t < total && ok; t += stride) {
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                const int s = it % STAGES, a = it % NA;
-                ok = __all_sync(0xffffffffu, bar_wait(&c.full[s], (it / STAGES) & 1u, abort_flag) &&
+                if ((it & 1u) != (uint32_t)group) continue;
+                const uint32_t s = it % WS, a = it % NA, sx = it % XS;
+                ok = __all_sync(0xffffffffu, bar_wait(&c.wfull[s], (it / WS) & 1u, abort_flag) &&
                                                  bar_wait(&c.cempty[a], ((it / NA) & 1u) ^ 1u, abort_flag));
                 if (!ok) break;
                 tc_fence_after();
-                const uint8_t *sw = smem + s * C::STAGE + tile_off;
-                uint4 v[4];
+                const uint8_t *sw = smem + s * C::W_BYTES;
+                const uint32_t at = mine + a * kStageCols;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const uint4 *>(sw + piece_at<BK>(row, piece0 + q));
-                uint4 xv;
-                const int xr = NW == 2 ? tid >> 2 : tid >> 3, xp = NW == 2 ? tid & 3 : tid & 7;
-                const bool xmine = FEW && (NW == 1 || tid < 128);
-                if (xmine) xv = *reinterpret_cast<const uint4 *>(smem + s * C::STAGE + C::W_BYTES + piece_at<BK>(xr, xp));
-                if (FEW) {   // the stage has been read
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&c.empty[s]);
+                for (int u = 0; u < 2; ++u) {   // 64 codes: a row of tile u, or half u of a row
+                    uint4 v[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        v[q] = *reinterpret_cast<const uint4 *>(sw + (NW == 2 ? u * M * BK : 0) + piece_at<BK>(row, (NW == 2 ? 0 : 4 * u) + q));
+                    if (u == 1) {   // the stage has been read
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&c.wempty[s]);
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t o[16];
+                        widen16(v[2 * h], o);
+                        widen16(v[2 * h + 1], o + 8);
+                        tmem_st16(at + u * kUnitCols + h * 16, o);
+                    }
                 }
-                uint32_t o[16];
-                widen16(v[0], o);
-                widen16(v[1], o + 8);
-                tmem_st16(mine + a * 2 * kUnitCols, o);
-                uint32_t o2[16];
-                widen16(v[2], o2);
-                widen16(v[3], o2 + 8);
-                tmem_st16(mine + a * 2 * kUnitCols + 16, o2);
-                if (xmine) {
-                    uint32_t h[8];
-                    widen16(xv, h);
-                    uint8_t *xf = smem + C::RING + a * C::XF_BYTES + (xp >> 2) * NT * 128;
-                    const int q = (xp & 3) * 2;
-                    *reinterpret_cast<uint4 *>(xf + piece_at<128>(xr, q)) = make_uint4(h[0], h[1], h[2], h[3]);
-                    *reinterpret_cast<uint4 *>(xf + piece_at<128>(xr, q + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+                if (FEW) {
+                    ok = __all_sync(0xffffffffu, bar_wait(&c.xfull[sx], (it / XS) & 1u, abort_flag));
+                    if (!ok) break;
+                    const uint8_t *xs = smem + C::XRING + sx * C::X_BYTES;
+                    uint8_t *xf = smem + C::XF + a * C::XF_BYTES;
+                    constexpr int PIECES = BK / 16, EACH = NT * PIECES / 128;
+#pragma unroll
+                    for (int j = 0; j < EACH; ++j) {
+                        const int q = tid + j * 128, xr = q / PIECES, xp = q % PIECES;
+                        uint32_t h[8];
+                        widen16(*reinterpret_cast<const uint4 *>(xs + piece_at<BK>(xr, xp)), h);
+                        uint8_t *to = xf + (xp >> 2) * NT * 128;
+                        *reinterpret_cast<uint4 *>(to + piece_at<128>(xr, (xp & 3) * 2)) = make_uint4(h[0], h[1], h[2], h[3]);
+                        *reinterpret_cast<uint4 *>(to + piece_at<128>(xr, (xp & 3) * 2 + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&c.xempty[sx]);
                 }
                 tmem_st_wait();
-                if (FEW) fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&c.cfull[a]);
@@ -403,11 +498,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                         for (int q = 0; q < 16; ++q) v[0][q] = v[NW - 1][q] = 0x7fffffffu;
                     }
                     if (i0 + 16 >= tile.cnt) done_reading();
-#pragma unroll
-                    for (int q = 0; q < 16; ++q)
-                        if (i0 + q < tile.cnt && n < p.N)
-                            store_out(p, tile.row0 + i0 + q, n,
-                                      finish<MODE>(p, __uint_as_float(v[0][q]), __uint_as_float(v[NW - 1][q]), sx[i0 + q], sw0, sw1));
+                    store_tokens<MODE, 16>(p, v[0], v[NW - 1], tile.row0 + i0, tile.cnt - i0, n - lane, lane, sx + i0, sw0, sw1);
                 }
             } else {
                 // all of the warp's sums go into registers first: the accumulator is the
@@ -424,14 +515,8 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                     tmem_ld32_wait(from + (MODE == GATEUP ? NT : 32), v + 32);
                 }
                 done_reading();
-                if (n < p.N) {
-#pragma unroll
-                    for (int q = 0; q < TOK; ++q) {
-                        if (tok0 + q >= tile.cnt) break;
-                        store_out(p, tile.row0 + tok0 + q, n,
-                                  finish<MODE>(p, __uint_as_float(v[q]), __uint_as_float(v[(q + 32) & 63]), sx[tok0 + q], sw0, sw1));
-                    }
-                }
+                store_tokens<MODE, TOK>(p, v, MODE == GATEUP ? v + 32 : v, tile.row0 + tok0, tile.cnt - tok0, n - lane, lane, sx + tok0,
+                                        sw0, sw1);
             }
         }
     }
@@ -489,53 +574,54 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         // A role gave up, and nothing says that the others have waited for what was
         // issued: loads land before the CTA exits, MMAs end before TMEM is freed.
         volatile int no_abort = 0;
-        if (warp == 0) {
-            for (uint32_t j = issued >= STAGES ? issued - STAGES : 0; j < issued; ++j)
-                bar_wait(&c.full[j % STAGES], (j / STAGES) & 1u, &no_abort, 1000000ull);
-        } else if (warp == 1 && issued > 0) {
-            if (elect_one()) umma_commit(&c.drain);
-            bar_wait(&c.drain, 0, &no_abort);
+        if (warp == 0 || warp == 3) {
+            const uint32_t stages = warp == 0 ? WS : XS;
+            for (uint32_t j = issued >= stages ? issued - stages : 0; j < issued; ++j)
+                bar_wait(warp == 0 ? &c.wfull[j % stages] : &c.xfull[j % stages], (j / stages) & 1u, &no_abort, 1000000ull);
+        } else if (warp <= NW && issued > 0) {
+            if (elect_one()) umma_commit(&c.drain[warp - 1]);
+            bar_wait(&c.drain[warp - 1], 0, &no_abort);
         }
         __syncthreads();
     }
-    if (warp == 2) {
+    if (warp == 3) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, C::TMEM_COLS);
     }
 }
 
-// x's codes as fp16 rows in group order, 16 codes a thread; a token index out of range
-// gives a row of zeros.
-constexpr int kConvertThreads = 256;
+// x's codes as fp16 rows in group order, 16 codes a thread of `kConvertRows` rows (all
+// asked for before the first is widened); a token index out of range gives a row of zeros.
+constexpr int kConvertThreads = 256, kConvertRows = 4;
+struct ConvertLayout { int lanes_log2, col_blocks; };   // threads of a CTA along a row, CTAs along it
 __global__ void __launch_bounds__(kConvertThreads)
-convert_rows_kernel(const Params p, uint4 *__restrict__ xf)
+convert_rows_kernel(const Params p, const ConvertLayout l, uint4 *__restrict__ xf)
 {
     pdl_enter();
-    const int pieces = p.K / 16;
-    const long long total = (long long)p.rows * pieces;
-    const long long step = (long long)gridDim.x * kConvertThreads;
-    constexpr int U = 4;   // pieces in flight
-    for (long long i0 = (long long)blockIdx.x * kConvertThreads + threadIdx.x; i0 < total; i0 += U * step) {
-        uint4 v[U];
+    const int pieces = p.K / 16, lanes = 1 << l.lanes_log2, each = kConvertThreads >> l.lanes_log2;
+    const long long band = blockIdx.x / l.col_blocks;
+    const int c = (int)(blockIdx.x - band * l.col_blocks) * lanes + (threadIdx.x & (lanes - 1));
+    const long long r0 = band * (kConvertRows * each) + (threadIdx.x >> l.lanes_log2);
+    if (c >= pieces) return;
+    uint4 v[kConvertRows];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const long long i = i0 + u * step;
-            v[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (i >= total) continue;
-            const int r = (int)(i / pieces), c = (int)(i - (long long)r * pieces);
-            const int src = p.perm_tok ? __ldg(p.perm_tok + r) : r;
-            if (src >= 0 && src < p.x_rows) v[u] = __ldg(reinterpret_cast<const uint4 *>(p.x_q + src * p.ldx) + c);
-        }
+    for (int u = 0; u < kConvertRows; ++u) {
+        const long long r = r0 + u * each;
+        v[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (r >= p.rows) continue;
+        const long long src = p.perm_tok ? __ldg(p.perm_tok + r) : r;
+        if (src >= 0 && src < p.x_rows) v[u] = __ldg(reinterpret_cast<const uint4 *>(p.x_q + src * p.ldx) + c);
+    }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const long long i = i0 + u * step;
-            if (i >= total) continue;
-            uint32_t o[8];
-            widen16(v[u], o);
-            xf[2 * i] = make_uint4(o[0], o[1], o[2], o[3]);
-            xf[2 * i + 1] = make_uint4(o[4], o[5], o[6], o[7]);
-        }
+    for (int u = 0; u < kConvertRows; ++u) {
+        const long long r = r0 + u * each;
+        if (r >= p.rows) continue;
+        uint32_t o[8];
+        widen16(v[u], o);
+        uint4 *to = xf + (r * pieces + c) * 2;
+        to[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        to[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
 }
 
@@ -608,13 +694,17 @@ template <int MODE> cudaError_t launch_tiled(const Params &args, void *workspace
     p.split = 1;
     const long long tiles = most_tiles(p, C::NT);
     if (tiles > 0x3fffffffLL) return cudaErrorInvalidValue;
-    const long long pieces = (long long)p.rows * (p.K / 16), per = kConvertThreads * 4;
-    const long long want = (pieces + per - 1) / per, most = (long long)num_sms * 8;
-    cudaError_t e = launch_pdl(convert_rows_kernel, dim3((unsigned)(want < most ? want : most)), dim3(kConvertThreads), 0,
-                               stream, p, static_cast<uint4 *>(workspace));
+    ConvertLayout l{0, 1};
+    while (l.lanes_log2 < 8 && (1 << l.lanes_log2) < p.K / 16) ++l.lanes_log2;
+    l.col_blocks = ceil_div(p.K / 16, 1 << l.lanes_log2);
+    const int per = kConvertRows * (kConvertThreads >> l.lanes_log2);
+    const long long ctas = (long long)ceil_div(p.rows, per) * l.col_blocks;
+    if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const cudaError_t e = launch_pdl(convert_rows_kernel, dim3((unsigned)ctas), dim3(kConvertThreads), 0, stream, p, l,
+                                     static_cast<uint4 *>(workspace));
     if (e != cudaSuccess) return e;
     CUtensorMap mx, mw0, mw1;
-    if (!make_map(&mx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, workspace, 0, p.rows, p.K, (long long)p.K * 2, C::BK, 64,
+    if (!make_map(&mx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, workspace, 0, p.rows, p.K, (long long)p.K * 2, C::BK, C::NT,
                   CU_TENSOR_MAP_SWIZZLE_128B) ||
         !weight_maps<MODE, false>(p, &mw0, &mw1))
         return cudaErrorInvalidValue;
