@@ -52,6 +52,7 @@ namespace {
 constexpr int M = 128;                       // weight rows of an MMA
 constexpr int kUnitCols = 32;                // TMEM columns of 64 codes as fp16
 constexpr int kStageCols = 2 * kUnitCols;    // ... of a stage's weights
+constexpr int kStaging = 2048;
 constexpr int kConvWarps = 8;                // two groups of four, which take the stages in turn
 
 template <int MODE, bool FEW> struct Cfg {
@@ -62,7 +63,7 @@ template <int MODE, bool FEW> struct Cfg {
     static constexpr int W_BYTES = NW * M * BK;                    // 16 KB
     static constexpr int X_BYTES = NT * BK * (FEW ? 1 : 2);
     static constexpr int WS = FEW ? (MODE == GATEUP ? 5 : 4) : 5;  // stages of the weights' ring
-    static constexpr int XS = FEW ? 4 : 8;                         // ... of the tokens'
+    static constexpr int XS = FEW ? 4 : 6;                         // ... of the tokens'
     static constexpr int NA = FEW ? (MODE == GATEUP ? 2 : 3) : 4;  // converted stages in flight
     static constexpr int XF_BYTES = FEW ? NT * BK * 2 : 0;         // widened tokens of one
     static constexpr int ND = FEW ? 2 : 1;                         // accumulators
@@ -73,43 +74,34 @@ template <int MODE, bool FEW> struct Cfg {
     static constexpr int THREADS = 128 + 32 * (EPI + kConvWarps);
     static constexpr size_t XRING = (size_t)WS * W_BYTES;
     static constexpr size_t XF = XRING + (size_t)XS * X_BYTES;
-    static constexpr size_t CTL = XF + (size_t)NA * XF_BYTES;
+    static constexpr size_t STAGING = XF + (size_t)NA * XF_BYTES;  // (tiled: kStaging bytes an output warp)
+    static constexpr size_t CTL = STAGING + (FEW ? 0 : (size_t)EPI * kStaging);
     static_assert(A_COL + NA * kStageCols <= TMEM_COLS, "tensor memory");
     static_assert(!FEW || (size_t)NT * NW * M * 4 <= XRING, "split partial sums reuse the weights' ring");
 };
-constexpr int kMaxW = 5, kMaxX = 8, kMaxA = 4, kTable = 32;
+constexpr int kMaxW = 5, kMaxX = 6, kMaxA = 4, kTable = 32;
 
-template <int EPI, int NT> struct alignas(16) Ctl {
+template <int EPI, int TOK> struct alignas(16) Ctl {
     uint64_t wfull[kMaxW], wempty[kMaxW], xfull[kMaxX], xempty[kMaxX], cfull[kMaxA], cempty[kMaxA], dfull[2], dempty[2], drain[2];
     uint64_t never;                          // nothing arrives here (test hook)
     uint32_t tmem_base;
     int abort_flag;
-    alignas(16) float sx[EPI][NT];           // each output warp's token scales
+    alignas(16) float sx[EPI][TOK];          // each output warp's token scales
     Groups g;
     Tile tiles[kTable];                      // this CTA's first tiles (each role asks for them in turn)
 };
-template <int MODE, bool FEW> using CtlOf = Ctl<Cfg<MODE, FEW>::EPI, Cfg<MODE, FEW>::NT>;
+template <int MODE, bool FEW> using CtlOf = Ctl<Cfg<MODE, FEW>::EPI, FEW ? 32 : 64>;
 template <int MODE, bool FEW> constexpr size_t smem_bytes() { return 1024 + Cfg<MODE, FEW>::CTL + sizeof(CtlOf<MODE, FEW>); }
 static_assert(smem_bytes<PRODUCT, false>() <= 232448 && smem_bytes<GATEUP, false>() <= 232448, "shared memory per CTA");
 static_assert(smem_bytes<PRODUCT, true>() <= 115712 && smem_bytes<GATEUP, true>() <= 115712, "two CTAs per SM");
 // registers a thread after the split at start (setmaxnreg) of the tiled kernel: 28 warps
-// launch with 72 each, 2016; 4 x 32 + 8 x 56 + 16 x 88 = 1984
-constexpr int kRegsLaunch = 72, kRegsAux = 32, kRegsConv = 56, kRegsEpi = 88;
+// launch with 72 each, 2016; 4 x 40 + 8 x 56 + 16 x 88 = 2016
+constexpr int kRegsLaunch = 72, kRegsAux = 40, kRegsConv = 56, kRegsEpi = 88;
 static_assert(4 * kRegsAux + 8 * kRegsConv + 16 * kRegsEpi <= 28 * kRegsLaunch, "more registers than the block has");
 
 #define MOE_OUTS8(i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), "=r"(v[i + 6]), "=r"(v[i + 7])
-// 32 columns of the warp's TMEM lanes and the wait for them, in one statement (nothing that
+// 16 columns of the warp's TMEM lanes and the wait for them, in one statement (nothing that
 // reads the registers moves above it)
-__device__ __forceinline__ void tmem_ld32_wait(uint32_t taddr, uint32_t *v)
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : MOE_OUTS8(0), MOE_OUTS8(8), MOE_OUTS8(16), MOE_OUTS8(24)
-        : "r"(taddr)
-        : "memory");
-}
 __device__ __forceinline__ void tmem_ld16_wait(uint32_t taddr, uint32_t *v)
 {
     asm volatile(
@@ -119,6 +111,51 @@ __device__ __forceinline__ void tmem_ld16_wait(uint32_t taddr, uint32_t *v)
         : "r"(taddr)
         : "memory");
 }
+
+// The sums of the warp's 32 TMEM lanes (channels) as 8 x 8 fragments, and the wait for them
+// in the same statement.  64 columns (tokens): v[32 h + 4 j + 2 r + c] of lane l is channel
+// 16 h + 8 r + l / 4, token 8 j + 2 (l % 4) + c.
+__device__ __forceinline__ void tmem_ld_frags(uint32_t taddr, uint32_t *v)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+        "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : MOE_OUTS8(0), MOE_OUTS8(8), MOE_OUTS8(16), MOE_OUTS8(24), MOE_OUTS8(32), MOE_OUTS8(40), MOE_OUTS8(48), MOE_OUTS8(56)
+        : "r"(taddr), "r"(taddr + (16u << 16))
+        : "memory");
+}
+// 32 columns at each of two places: v[32 m + 16 h + 4 j + 2 r + c]
+__device__ __forceinline__ void tmem_ld_frags2(uint32_t a, uint32_t b, uint32_t *v)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%64];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%65];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47}, [%66];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%67];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : MOE_OUTS8(0), MOE_OUTS8(8), MOE_OUTS8(16), MOE_OUTS8(24), MOE_OUTS8(32), MOE_OUTS8(40), MOE_OUTS8(48), MOE_OUTS8(56)
+        : "r"(a), "r"(a + (16u << 16)), "r"(b), "r"(b + (16u << 16))
+        : "memory");
+}
+// Four 8 x 8 fragments of 16-bit values, transposed, to the rows that the lanes name:
+// lane 8 m + i row i of fragment m, 16 bytes.
+__device__ __forceinline__ void store_frags(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int x, int y)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(src))
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// this thread's stores: their shared memory has been read / they are complete
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // 16 codes -> 16 fp16 values, in order: q ^ 0x80 = q + 128 in the significand of 1024,
 // minus 1152, both exact.
@@ -230,10 +267,29 @@ __device__ __forceinline__ void store_tokens(const Params &p, const uint32_t *a,
     }
 }
 
+// Staged rows of CHANNELS values (16-byte piece c of row t at c ^ (t % 8)) to `rows` of TOKENS output
+// rows, CHANNELS threads: 16 bytes at a time where the rows allow, else an element a thread.
+template <typename T, int CHANNELS, int TOKENS>
+__device__ __forceinline__ void store_staged(T *o, long long ldo, const uint8_t *stg, int tid, int rows, int left, bool vec)
+{
+    constexpr int V = 16 / (int)sizeof(T);
+    if (vec) {
+#pragma unroll
+        for (int i = 0; i < TOKENS * 8 / CHANNELS; ++i) {
+            const int q = tid + i * CHANNELS, t = q >> 3, ch = (q & 7) * V;
+            if (t < rows && ch < left) *reinterpret_cast<uint4 *>(o + t * ldo + ch) = *reinterpret_cast<const uint4 *>(stg + piece_at<128>(t, q & 7));
+        }
+    } else if (tid < left) {
+#pragma unroll 4
+        for (int t = 0; t < rows; ++t) o[t * ldo + tid] = *reinterpret_cast<const T *>(stg + piece_at<128>(t, tid / V) + (tid % V) * sizeof(T));
+    }
+}
+__device__ __forceinline__ void pair_barrier(int pair) { asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory"); }
+
 template <int MODE, bool FEW, bool SPLIT>
 __global__ void __launch_bounds__((Cfg<MODE, FEW>::THREADS), FEW ? 2 : 1)
 product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w0,
-               const __grid_constant__ CUtensorMap tm_w1, const Params p)
+               const __grid_constant__ CUtensorMap tm_w1, const __grid_constant__ CUtensorMap tm_out, const Params p)
 {
     using C = Cfg<MODE, FEW>;
     constexpr int NW = C::NW, BK = C::BK, NT = C::NT, WS = C::WS, XS = C::XS, NA = C::NA;
@@ -451,12 +507,19 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             const uint32_t d = lane_base + db * C::D_COLS;
             // output channel (tiled PRODUCT: `part` is the weight tile and a half of the
             // tokens; GATEUP: a quarter of them)
+            constexpr int TOK = FEW ? NT : MODE == GATEUP ? 32 : 64;
+            const int tok0 = FEW ? 0 : (MODE == GATEUP ? part : part & 1) * TOK;
             const int n = tile.nt * C::ROWS + (MODE == PRODUCT ? (part >> 1) * M : 0) + chan;
-            const long long wn = (long long)tile.e * p.N + min(n, p.N - 1);
-            const float sw0 = __ldg(p.w_s[0] + wn), sw1 = MODE == GATEUP ? __ldg(p.w_s[1] + wn) : 0.f;
+            float sw0 = 0.f, sw1 = 0.f;
+            if (FEW) {
+                const long long wn = (long long)tile.e * p.N + min(n, p.N - 1);
+                sw0 = __ldg(p.w_s[0] + wn);
+                if (MODE == GATEUP) sw1 = __ldg(p.w_s[1] + wn);
+            }
             float *sx = c.sx[ew];
             __syncwarp();
-            for (int l = lane; l < tile.cnt; l += 32) sx[l] = __ldg(p.x_s + source_row(p, tile.row0 + l));
+            for (int l = lane; l < TOK; l += 32)
+                sx[l] = tok0 + l < tile.cnt ? __ldg(p.x_s + source_row(p, tile.row0 + tok0 + l)) : 0.f;
             __syncwarp();
             ok = ok && __all_sync(0xffffffffu, bar_wait(&c.dfull[db], (i / C::ND) & 1u, abort_flag));
             if (!ok) {
@@ -503,22 +566,96 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             } else {
                 // all of the warp's sums go into registers first: the accumulator is the
                 // next tile's from then on
+                constexpr int H = MODE == GATEUP ? 16 : 32;   // registers of 16 channels
+                const uint32_t from = d + (MODE == GATEUP ? 0 : (part >> 1) * NT) + tok0;
                 uint32_t v[64];
-                constexpr int TOK = MODE == GATEUP ? 32 : 64;
-                const int tok0 = (MODE == GATEUP ? part : part & 1) * TOK;
                 if (!ok) {
 #pragma unroll
                     for (int q = 0; q < 64; ++q) v[q] = 0x7fffffffu;
                 } else {
-                    const uint32_t from = d + (MODE == GATEUP ? 0 : (part >> 1) * NT) + tok0;
-                    tmem_ld32_wait(from, v);
-                    tmem_ld32_wait(from + (MODE == GATEUP ? NT : 32), v + 32);
+                    if (MODE == GATEUP) tmem_ld_frags2(from, from + NT, v);
+                    else tmem_ld_frags(from, v);
                 }
                 done_reading();
-                store_tokens<MODE, TOK>(p, v, MODE == GATEUP ? v + 32 : v, tile.row0 + tok0, tile.cnt - tok0, n - lane, lane, sx + tok0,
-                                        sw0, sw1);
+                // v[h H + 4 j + 2 r + q]: channel 16 h + 8 r + lane / 4, token 8 j + 2 (lane % 4) + q
+                float sw[NW][4];
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                    const long long at = (long long)tile.e * p.N + min(n - lane + f * 8 + (lane >> 2), p.N - 1);
+                    sw[0][f] = __ldg(p.w_s[0] + at);
+                    sw[NW - 1][f] = __ldg(p.w_s[NW - 1 < 1 || MODE == PRODUCT ? 0 : 1] + at);
+                }
+                auto value = [&](int j, int f, int q) {   // octet of tokens, octet of channels, token of a pair
+                    const int i = (f >> 1) * H + 4 * j + 2 * (f & 1) + q;
+                    const float s = sx[8 * j + 2 * (lane & 3) + q];
+                    return finish<MODE>(p, __uint_as_float(v[i]), __uint_as_float(v[(i + 32) & 63]), s, sw[0][f], sw[NW - 1][f]);
+                };
+                const long long row0 = tile.row0 + tok0;
+                const int rows = tile.cnt - tok0;
+                if (p.out_f32) {
+                    // the warp's 32 channels of 16 tokens at a time
+                    uint8_t *stg = smem + C::STAGING + ew * kStaging;
+#pragma unroll
+                    for (int rd = 0; rd < TOK / 16; ++rd) {
+                        if (rd * 16 >= rows) break;
+                        if (lane == 0) bulk_wait_read();
+                        __syncwarp();
+#pragma unroll
+                        for (int jj = 0; jj < 2; ++jj)
+#pragma unroll
+                            for (int f = 0; f < 4; ++f)
+#pragma unroll
+                                for (int q = 0; q < 2; ++q) {
+                                    const int tr = 8 * jj + 2 * (lane & 3) + q, ch = f * 8 + (lane >> 2);
+                                    *reinterpret_cast<float *>(stg + piece_at<128>(tr, ch >> 2) + (ch & 3) * 4) = value(2 * rd + jj, f, q);
+                                }
+                        if (p.out_vec && rows - rd * 16 >= 16) {
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                if (n < p.N) tma_store_2d(&tm_out, stg, n, (int)row0 + rd * 16);
+                                bulk_commit();
+                            }
+                        } else {
+                            __syncwarp();
+                            float *o = static_cast<float *>(p.out) + (row0 + rd * 16) * p.ldo + n - lane;
+                            store_staged<float, 32, 16>(o, p.ldo, stg, lane, min(rows - rd * 16, 16), p.N - (n - lane), p.out_vec);
+                        }
+                    }
+                } else {
+                    // the pair's 64 channels of 32 tokens at a time
+                    uint8_t *stg = smem + C::STAGING + (ew >> 1) * 2 * kStaging;
+                    const int half = ew & 1, n0 = n - lane - half * 32;
+#pragma unroll
+                    for (int rd = 0; rd < TOK / 32; ++rd) {
+                        if (rd * 32 >= rows) break;
+                        if (half == 0 && lane == 0) bulk_wait_read();
+                        pair_barrier(ew >> 1);
+#pragma unroll
+                        for (int jj = 0; jj < 4; ++jj) {
+                            const int tr = 8 * jj + (lane & 7), j = 4 * rd + jj;
+                            uint32_t w[4];
+#pragma unroll
+                            for (int f = 0; f < 4; ++f) w[f] = fp8b::bf16x2(value(j, f, 0), value(j, f, 1));
+                            store_frags(smem_u32(stg + piece_at<128>(tr, half * 4 + (lane >> 3))), w[0], w[1], w[2], w[3]);
+                        }
+                        if (p.out_vec && rows - rd * 32 >= 32) {
+                            fence_proxy_async_smem();
+                            pair_barrier(ew >> 1);
+                            if (half == 0 && lane == 0) {
+                                if (n0 < p.N) tma_store_2d(&tm_out, stg, n0, (int)row0 + rd * 32);
+                                bulk_commit();
+                            }
+                        } else {
+                            pair_barrier(ew >> 1);
+                            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + (row0 + rd * 32) * p.ldo + n0;
+                            store_staged<__nv_bfloat16, 64, 32>(o, p.ldo, stg, half * 32 + lane, min(rows - rd * 32, 32), p.N - n0, p.out_vec);
+                        }
+                    }
+                }
             }
         }
+        if (!FEW && lane == 0) bulk_wait_all();
     }
 
     if constexpr (SPLIT) {
@@ -641,7 +778,7 @@ bool make_map(CUtensorMap *m, CUtensorMapDataType type, const void *base, int n,
 }
 
 template <int MODE, bool FEW, bool SPLIT>
-cudaError_t launch_variant(const CUtensorMap &x, const CUtensorMap &w0, const CUtensorMap &w1, const Params &p,
+cudaError_t launch_variant(const CUtensorMap &x, const CUtensorMap &w0, const CUtensorMap &w1, const CUtensorMap &out, const Params &p,
                            long long tiles, int num_sms, cudaStream_t stream)
 {
     using C = Cfg<MODE, FEW>;
@@ -655,9 +792,9 @@ cudaError_t launch_variant(const CUtensorMap &x, const CUtensorMap &w0, const CU
         done.mark(dev);
     }
     if (SPLIT)
-        return launch_pdl_cluster(kern, dim3((unsigned)(tiles * p.split)), dim3(C::THREADS), smem, stream, p.split, x, w0, w1, p);
+        return launch_pdl_cluster(kern, dim3((unsigned)(tiles * p.split)), dim3(C::THREADS), smem, stream, p.split, x, w0, w1, out, p);
     const long long most = (long long)num_sms * (FEW ? 2 : 1);
-    return launch_pdl(kern, dim3((unsigned)(tiles < most ? tiles : most)), dim3(C::THREADS), smem, stream, x, w0, w1, p);
+    return launch_pdl(kern, dim3((unsigned)(tiles < most ? tiles : most)), dim3(C::THREADS), smem, stream, x, w0, w1, out, p);
 }
 
 // Most tiles there can be: an expert with r rows has (r - 1) / rows_per_tile + 1, so as
@@ -708,7 +845,11 @@ template <int MODE> cudaError_t launch_tiled(const Params &args, void *workspace
                   CU_TENSOR_MAP_SWIZZLE_128B) ||
         !weight_maps<MODE, false>(p, &mw0, &mw1))
         return cudaErrorInvalidValue;
-    return launch_variant<MODE, false, false>(mx, mw0, mw1, p, tiles, num_sms, stream);
+    CUtensorMap mout = mx;   // (not used where rows are not on 16-byte boundaries)
+    if (p.out_vec && !make_map(&mout, p.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.out, 0, p.rows,
+                               p.N, p.ldo * (p.out_f32 ? 4 : 2), p.out_f32 ? 32 : 64, p.out_f32 ? 16 : 32, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    return launch_variant<MODE, false, false>(mx, mw0, mw1, mout, p, tiles, num_sms, stream);
 }
 
 template <int MODE> cudaError_t launch_few(const Params &args, cudaStream_t stream)
@@ -732,8 +873,8 @@ template <int MODE> cudaError_t launch_few(const Params &args, cudaStream_t stre
                   C::BK == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B) ||
         !weight_maps<MODE, true>(p, &mw0, &mw1))
         return cudaErrorInvalidValue;
-    return p.split > 1 ? launch_variant<MODE, true, true>(mx, mw0, mw1, p, tiles, num_sms, stream)
-                       : launch_variant<MODE, true, false>(mx, mw0, mw1, p, tiles, num_sms, stream);
+    return p.split > 1 ? launch_variant<MODE, true, true>(mx, mw0, mw1, mx, p, tiles, num_sms, stream)
+                       : launch_variant<MODE, true, false>(mx, mw0, mw1, mx, p, tiles, num_sms, stream);
 }
 
 template cudaError_t launch_tiled<PRODUCT>(const Params &, void *, cudaStream_t);
