@@ -6,25 +6,21 @@
 // sm_103a has no 8-bit integer MMA.  An int8 code is exact in fp16 and a product of two
 // in fp32, so the sums run on kind::f16 and are whole numbers, exact up to 2^24.
 //
-// Weights are the MMA's rows.  They are read as int8 (TMA), and converter warps -- one
-// TMEM lane, that is one weight row, to a thread -- turn 64 codes at a time into fp16 and
-// store them into tensor memory, where the MMA takes its A operand: the widened weights
-// touch neither HBM nor shared memory.  Tokens are the columns:
+// Weights are the MMA's 128 rows (PRODUCT: of W; GATEUP: 64 of W_gate and the same 64 of
+// W_up).  They are read as int8 (TMA), and converter warps -- one TMEM lane, that is one
+// weight row, to a thread -- widen 128 codes of it at a time to fp16 and store them into
+// tensor memory, where the MMA takes its A operand: the widened weights touch neither HBM
+// nor shared memory.  Tokens are the columns:
 //   tiled     128 of them, as fp16 rows that convert_rows_kernel has written (in group
-//             order, so it gathers too), by TMA; 256 weight rows a tile (two MMAs of 128
-//             rows share the tokens), or 128 of W_gate and the same of W_up;
-//   few rows  32, read as int8 and widened into shared memory by the same warps; 128
-//             weight rows a tile (or of both); two CTAs an SM.  Few tiles split the
-//             reduction over a cluster, whose partial sums meet in distributed shared
-//             memory.
-// A stage of the reduction is 128 x 128 codes of weights: 64 columns of two tiles, or 128
-// of one.  Weights and tokens have rings of their own, as the converters are done with
-// the former long before the MMAs are with the latter.
+//             order, so it gathers too), by TMA;
+//   few rows  32, read as int8 and widened into shared memory by the same warps; two CTAs
+//             an SM.  Few tiles split the reduction over a cluster, whose partial sums
+//             meet in distributed shared memory.
+// Accumulators are two, so a tile's output overlaps the next tile's products.
 //
 // Warp 0 loads weights, warp 3 tokens (one warp for both issued its loads in 930 clocks a
-// stage, where the MMAs take 512), warps 1 and 2 multiply a weight tile each, the last 8
-// warps convert, four of them a stage, and warps 4.. (4 or 16) write the output.  A
-// thread of these holds an output channel; a token's values lie along the warp.
+// block of 128 columns' 256 x 64, where the MMAs take 512), warp 1 multiplies, the last 8
+// warps convert, four of them a block in turn, and warps 4.. (4 or 16) write the output.
 //
 // Every wait is bounded (2 s).  Where one gives up, the rows of the CTA's remaining
 // tiles are written as NaN, and the status word says so if the caller passed one.
@@ -37,7 +33,6 @@ namespace moe {
 namespace i8 {
 
 using namespace sm100;
-using fp8b::bar_wait;
 using fp8b::elect_one;
 using fp8b::Groups;
 using fp8b::load_groups;
@@ -50,53 +45,54 @@ using fp8b::tma_load_3d;
 namespace {
 
 constexpr int M = 128;                       // weight rows of an MMA
-constexpr int kUnitCols = 32;                // TMEM columns of 64 codes as fp16
-constexpr int kStageCols = 2 * kUnitCols;    // ... of a stage's weights
+constexpr int BK = 128;                      // columns of a block of the reduction
+constexpr int W_BYTES = M * BK;
+constexpr int kBlockCols = BK / 2;           // TMEM columns of a block's weights as fp16
 constexpr int kStaging = 2048;
-constexpr int kConvWarps = 8;                // two groups of four, which take the stages in turn
 
-template <int MODE, bool FEW> struct Cfg {
-    static constexpr int NW = (MODE == GATEUP || !FEW) ? 2 : 1;    // weight tiles of a stage
-    static constexpr int BK = NW == 2 ? 64 : 128;
+// output channels of a tile
+constexpr int rows_of_mode(int mode) { return mode == GATEUP ? M / 2 : M; }
+
+template <bool FEW> struct Cfg {
     static constexpr int NT = FEW ? 32 : 128;                      // tokens of a tile
-    static constexpr int ROWS = MODE == PRODUCT ? NW * M : M;      // output channels of a tile
-    static constexpr int W_BYTES = NW * M * BK;                    // 16 KB
     static constexpr int X_BYTES = NT * BK * (FEW ? 1 : 2);
-    static constexpr int WS = FEW ? (MODE == GATEUP ? 5 : 4) : 5;  // stages of the weights' ring
-    static constexpr int XS = FEW ? 4 : 6;                         // ... of the tokens'
-    static constexpr int NA = FEW ? (MODE == GATEUP ? 2 : 3) : 4;  // converted stages in flight
-    static constexpr int XF_BYTES = FEW ? NT * BK * 2 : 0;         // widened tokens of one
-    static constexpr int ND = FEW ? 2 : 1;                         // accumulators
-    static constexpr int D_COLS = NW * NT;
-    static constexpr int A_COL = ND * D_COLS;
+    static constexpr int WS = 4;                                   // blocks of the weights' ring
+    static constexpr int NA = FEW ? 3 : 4;                         // converted blocks in flight
+    static constexpr int XS = FEW ? 4 : NA;                        // blocks of the tokens' ring (tiled: block a's
+                                                                   // tokens are freed with its converted weights)
+    static constexpr int XF_BYTES = FEW ? NT * BK * 2 : 0;         // widened tokens of a block
+    static constexpr int A_COL = 2 * NT;                           // (two accumulators before)
     static constexpr int TMEM_COLS = FEW ? 256 : 512;
+    static constexpr int MMAS = FEW ? 1 : 2;                       // multiplying warps, each with its share of the tokens
     static constexpr int EPI = FEW ? 4 : 16;                       // output warps
-    static constexpr int THREADS = 128 + 32 * (EPI + kConvWarps);
+    static constexpr int GROUPS = 2;                               // of four converting warps, which take the blocks in turn
+    static constexpr int THREADS = 128 + 32 * (EPI + 4 * GROUPS);
     static constexpr size_t XRING = (size_t)WS * W_BYTES;
     static constexpr size_t XF = XRING + (size_t)XS * X_BYTES;
-    static constexpr size_t STAGING = XF + (size_t)NA * XF_BYTES;  // (tiled: kStaging bytes an output warp)
-    static constexpr size_t CTL = STAGING + (FEW ? 0 : (size_t)EPI * kStaging);
-    static_assert(A_COL + NA * kStageCols <= TMEM_COLS, "tensor memory");
-    static_assert(!FEW || (size_t)NT * NW * M * 4 <= XRING, "split partial sums reuse the weights' ring");
+    static constexpr size_t STAGING = XF + (size_t)NA * XF_BYTES;
+    static constexpr size_t CTL = STAGING + (FEW ? 2 * kStaging : (size_t)EPI * kStaging / 2);
+    static_assert(A_COL + NA * kBlockCols <= TMEM_COLS, "tensor memory");
+    static_assert(!FEW || (size_t)NT * M * 4 <= XRING, "split partial sums reuse the weights' ring");
 };
-constexpr int kMaxW = 5, kMaxX = 6, kMaxA = 4, kTable = 32;
+constexpr int kMaxRing = 4, kTable = 32;
 
-template <int EPI, int TOK> struct alignas(16) Ctl {
-    uint64_t wfull[kMaxW], wempty[kMaxW], xfull[kMaxX], xempty[kMaxX], cfull[kMaxA], cempty[kMaxA], dfull[2], dempty[2], drain[2];
+template <int EPI> struct alignas(16) Ctl {
+    uint64_t wfull[kMaxRing], wempty[kMaxRing], xfull[kMaxRing], xempty[kMaxRing], cfull[kMaxRing], cempty[kMaxRing];
+    uint64_t dfull[2], dempty[2], drain[2];
     uint64_t never;                          // nothing arrives here (test hook)
     uint32_t tmem_base;
     int abort_flag;
-    alignas(16) float sx[EPI][TOK];          // each output warp's token scales
+    alignas(16) float sx[EPI][32];           // each output warp's token scales
     Groups g;
     Tile tiles[kTable];                      // this CTA's first tiles (each role asks for them in turn)
 };
-template <int MODE, bool FEW> using CtlOf = Ctl<Cfg<MODE, FEW>::EPI, FEW ? 32 : 64>;
-template <int MODE, bool FEW> constexpr size_t smem_bytes() { return 1024 + Cfg<MODE, FEW>::CTL + sizeof(CtlOf<MODE, FEW>); }
-static_assert(smem_bytes<PRODUCT, false>() <= 232448 && smem_bytes<GATEUP, false>() <= 232448, "shared memory per CTA");
-static_assert(smem_bytes<PRODUCT, true>() <= 115712 && smem_bytes<GATEUP, true>() <= 115712, "two CTAs per SM");
+template <bool FEW> using CtlOf = Ctl<Cfg<FEW>::EPI>;
+template <bool FEW> constexpr size_t smem_bytes() { return 1024 + Cfg<FEW>::CTL + sizeof(CtlOf<FEW>); }
+static_assert(smem_bytes<false>() <= 232448, "shared memory per CTA");
+static_assert(smem_bytes<true>() <= 115712, "two CTAs per SM");
 // registers a thread after the split at start (setmaxnreg) of the tiled kernel: 28 warps
-// launch with 72 each, 2016; 4 x 40 + 8 x 56 + 16 x 88 = 2016
-constexpr int kRegsLaunch = 72, kRegsAux = 40, kRegsConv = 56, kRegsEpi = 88;
+// launch with 72 each, 2016; 4 x 56 + 8 x 64 + 16 x 80 = 2016
+constexpr int kRegsLaunch = 72, kRegsAux = 56, kRegsConv = 64, kRegsEpi = 80;
 static_assert(4 * kRegsAux + 8 * kRegsConv + 16 * kRegsEpi <= 28 * kRegsLaunch, "more registers than the block has");
 
 #define MOE_OUTS8(i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), "=r"(v[i + 6]), "=r"(v[i + 7])
@@ -112,32 +108,17 @@ __device__ __forceinline__ void tmem_ld16_wait(uint32_t taddr, uint32_t *v)
         : "memory");
 }
 
-// The sums of the warp's 32 TMEM lanes (channels) as 8 x 8 fragments, and the wait for them
-// in the same statement.  64 columns (tokens): v[32 h + 4 j + 2 r + c] of lane l is channel
+// 32 columns (tokens) of the warp's 32 TMEM lanes (channels) as 8 x 8 fragments, and the
+// wait for them in the same statement: v[16 h + 4 j + 2 r + c] of lane l is channel
 // 16 h + 8 r + l / 4, token 8 j + 2 (l % 4) + c.
 __device__ __forceinline__ void tmem_ld_frags(uint32_t taddr, uint32_t *v)
 {
     asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t"
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
-        "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
-        : MOE_OUTS8(0), MOE_OUTS8(8), MOE_OUTS8(16), MOE_OUTS8(24), MOE_OUTS8(32), MOE_OUTS8(40), MOE_OUTS8(48), MOE_OUTS8(56)
+        : MOE_OUTS8(0), MOE_OUTS8(8), MOE_OUTS8(16), MOE_OUTS8(24)
         : "r"(taddr), "r"(taddr + (16u << 16))
-        : "memory");
-}
-// 32 columns at each of two places: v[32 m + 16 h + 4 j + 2 r + c]
-__device__ __forceinline__ void tmem_ld_frags2(uint32_t a, uint32_t b, uint32_t *v)
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%64];\n\t"
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%65];\n\t"
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47}, [%66];\n\t"
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%67];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : MOE_OUTS8(0), MOE_OUTS8(8), MOE_OUTS8(16), MOE_OUTS8(24), MOE_OUTS8(32), MOE_OUTS8(40), MOE_OUTS8(48), MOE_OUTS8(56)
-        : "r"(a), "r"(a + (16u << 16)), "r"(b), "r"(b + (16u << 16))
         : "memory");
 }
 // Four 8 x 8 fragments of 16-bit values, transposed, to the rows that the lanes name:
@@ -157,6 +138,14 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
+// bar_wait with a non-blocking test first: a try_wait takes 130 clocks even of a phase
+// that is complete, and the multiplying warp's waits are what its MMAs wait for.
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+                                         unsigned long long timeout_ns = kTimeoutNs)
+{
+    return mbar_test_wait(bar, parity) || fp8b::bar_wait(bar, parity, abort_flag, timeout_ns);
+}
+
 // 16 codes -> 16 fp16 values, in order: q ^ 0x80 = q + 128 in the significand of 1024,
 // minus 1152, both exact.
 __device__ __forceinline__ void widen16(const uint4 v, uint32_t *o)
@@ -173,12 +162,8 @@ __device__ __forceinline__ void widen16(const uint4 v, uint32_t *o)
     }
 }
 __device__ __forceinline__ bool expires(const Params &p, Role role) { return p.expire_ns && p.expire_role == role; }
-// Byte offset of 16-byte piece c of row r in a TMA tile whose rows are BK bytes long
-// (64- or 128-byte swizzle).
-template <int BK> __device__ __forceinline__ int piece_at(int r, int c)
-{
-    return r * BK + ((BK == 64 ? c ^ ((r >> 1) & 3) : c ^ (r & 7)) << 4);
-}
+// Byte offset of 16-byte piece c of row r in a tile of 128-byte rows (TMA's 128-byte swizzle).
+__device__ __forceinline__ int piece_at(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 
 // Lane l holds channel l's values of 8 tokens, two of bf16 to a word; afterwards it holds
 // token l % 8's values of channels 8 (l / 8) .. + 7: a transpose, lane bit by lane bit.
@@ -277,33 +262,39 @@ __device__ __forceinline__ void store_staged(T *o, long long ldo, const uint8_t 
 #pragma unroll
         for (int i = 0; i < TOKENS * 8 / CHANNELS; ++i) {
             const int q = tid + i * CHANNELS, t = q >> 3, ch = (q & 7) * V;
-            if (t < rows && ch < left) *reinterpret_cast<uint4 *>(o + t * ldo + ch) = *reinterpret_cast<const uint4 *>(stg + piece_at<128>(t, q & 7));
+            if (t < rows && ch < left) *reinterpret_cast<uint4 *>(o + t * ldo + ch) = *reinterpret_cast<const uint4 *>(stg + piece_at(t, q & 7));
         }
     } else if (tid < left) {
 #pragma unroll 4
-        for (int t = 0; t < rows; ++t) o[t * ldo + tid] = *reinterpret_cast<const T *>(stg + piece_at<128>(t, tid / V) + (tid % V) * sizeof(T));
+        for (int t = 0; t < rows; ++t) o[t * ldo + tid] = *reinterpret_cast<const T *>(stg + piece_at(t, tid / V) + (tid % V) * sizeof(T));
     }
 }
-__device__ __forceinline__ void pair_barrier(int pair) { asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory"); }
+// Barrier of the four output warps that share their tokens.  (bar.sync is .aligned: the warp
+// reconverges first.)
+__device__ __forceinline__ void group_barrier(int group)
+{
+    __syncwarp();
+    asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
+}
 
 template <int MODE, bool FEW, bool SPLIT>
-__global__ void __launch_bounds__((Cfg<MODE, FEW>::THREADS), FEW ? 2 : 1)
+__global__ void __launch_bounds__(Cfg<FEW>::THREADS, FEW ? 2 : 1)
 product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w0,
                const __grid_constant__ CUtensorMap tm_w1, const __grid_constant__ CUtensorMap tm_out, const Params p)
 {
-    using C = Cfg<MODE, FEW>;
-    constexpr int NW = C::NW, BK = C::BK, NT = C::NT, WS = C::WS, XS = C::XS, NA = C::NA;
+    using C = Cfg<FEW>;
+    constexpr int NT = C::NT, WS = C::WS, XS = C::XS, NA = C::NA, ROWS = rows_of_mode(MODE);
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    auto &c = *reinterpret_cast<CtlOf<MODE, FEW> *>(smem + C::CTL);
+    auto &c = *reinterpret_cast<CtlOf<FEW> *>(smem + C::CTL);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int E = p.E;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < WS; ++s) { mbar_init(&c.wfull[s], 1); mbar_init(&c.wempty[s], 4); }
-        for (int s = 0; s < XS; ++s) { mbar_init(&c.xfull[s], 1); mbar_init(&c.xempty[s], FEW ? 4 : NW); }
-        for (int a = 0; a < NA; ++a) { mbar_init(&c.cfull[a], 4); mbar_init(&c.cempty[a], NW); }
-        for (int d = 0; d < C::ND; ++d) { mbar_init(&c.dfull[d], NW); mbar_init(&c.dempty[d], C::EPI); }
+        for (int s = 0; s < XS; ++s) { mbar_init(&c.xfull[s], 1); mbar_init(&c.xempty[s], 4); }
+        for (int a = 0; a < NA; ++a) { mbar_init(&c.cfull[a], 4); mbar_init(&c.cempty[a], C::MMAS); }
+        for (int d = 0; d < 2; ++d) { mbar_init(&c.dfull[d], C::MMAS); mbar_init(&c.dempty[d], C::EPI); }
         for (int w = 0; w < 2; ++w) mbar_init(&c.drain[w], 1);
         mbar_init(&c.never, 1);
         c.abort_flag = 0;
@@ -340,154 +331,164 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     __syncthreads();
     auto nth_tile = [&](int i, int t) { return i < kTable ? c.tiles[i] : tile_at(c.g, E, t, NT); };
     volatile int *abort_flag = &c.abort_flag;
-    uint32_t issued = 0;   // stages this warp has loaded or multiplied
+    uint32_t issued = 0;   // blocks this warp has loaded or multiplied
     bool ok = true;
 
     if (warp < 4) {
         if (!FEW) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsAux));
-        if (warp == 0 || warp == 3) {
-            // -------------------------------------------- loads: weights, tokens
-            const bool weights = warp == 0;
-            const int stages = weights ? WS : XS;
-            uint64_t *full = weights ? c.wfull : c.xfull, *empty = weights ? c.wempty : c.xempty;
-            uint8_t *ring = smem + (weights ? 0 : C::XRING);
-            uint32_t s = 0, phase = 0;
+        if (warp == 0) {
+            // -------------------------------------------- loads: weights
+            uint32_t it = 0;
             ok = !expires(p, LOADS) || __all_sync(0xffffffffu, bar_wait(&c.never, 0, abort_flag, p.expire_ns));
             for (int t = first, i = 0; t < total && ok; t += stride, ++i) {
                 const Tile tile = nth_tile(i, t);
-                const int n0 = tile.nt * C::ROWS;
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    const uint32_t s = it % WS;
+                    ok = __all_sync(0xffffffffu, bar_wait(&c.wempty[s], ((it / WS) & 1u) ^ 1u, abort_flag));
+                    if (!ok) break;
+                    if (elect_one()) {
+                        uint8_t *at = smem + s * W_BYTES;
+                        mbar_expect_tx(&c.wfull[s], W_BYTES);
+                        tma_load_3d(at, &tm_w0, &c.wfull[s], kb * BK, tile.nt * ROWS, tile.e);
+                        if (MODE == GATEUP) tma_load_3d(at + ROWS * BK, &tm_w1, &c.wfull[s], kb * BK, tile.nt * ROWS, tile.e);
+                    }
+                    __syncwarp();
+                }
+            }
+            issued = it;
+        } else if (warp == 3) {
+            // -------------------------------------------- loads: tokens
+            uint32_t it = 0;
+            uint64_t *empty = FEW ? c.xempty : c.cempty;
+            ok = !expires(p, LOADS) || __all_sync(0xffffffffu, bar_wait(&c.never, 0, abort_flag, p.expire_ns));
+            for (int t = first, i = 0; t < total && ok; t += stride, ++i) {
+                const Tile tile = nth_tile(i, t);
                 int4 tok = make_int4(0, 0, 0, 0);
-                const int gathers = FEW && p.perm_tok && !weights ? (tile.cnt + 3) / 4 : 0;
+                const int gathers = FEW && p.perm_tok ? (tile.cnt + 3) / 4 : 0;
                 if (FEW && lane < gathers) {
                     int v[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) v[q] = source_row(p, tile.row0 + min(4 * lane + q, tile.cnt - 1));
                     tok = make_int4(v[0], v[1], v[2], v[3]);
                 }
-                const uint32_t bytes = weights ? C::W_BYTES : gathers ? gathers * 4 * BK : C::X_BYTES;
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    ok = __all_sync(0xffffffffu, bar_wait(&empty[s], phase ^ 1u, abort_flag));
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    const uint32_t s = it % XS;
+                    ok = __all_sync(0xffffffffu, bar_wait(&empty[s], ((it / XS) & 1u) ^ 1u, abort_flag));
                     if (!ok) break;
-                    uint8_t *at = ring + s * (weights ? C::W_BYTES : C::X_BYTES);
+                    uint8_t *at = smem + C::XRING + s * C::X_BYTES;
                     if (elect_one()) {
-                        mbar_expect_tx(&full[s], bytes);
-                        if (weights) {
-                            tma_load_3d(at, &tm_w0, &full[s], kb * BK, n0, tile.e);
-                            if (MODE == GATEUP) tma_load_3d(at + M * BK, &tm_w1, &full[s], kb * BK, n0, tile.e);
-                        } else if (!gathers) {
-                            tma_load_2d(at, &tm_x, &full[s], kb * BK, tile.row0);
+                        mbar_expect_tx(&c.xfull[s], gathers ? gathers * 4 * BK : C::X_BYTES);
+                        if (!gathers) {
+                            tma_load_2d(at, &tm_x, &c.xfull[s], kb * BK, tile.row0);
+                            // (a 128-byte row holds 64 columns of fp16)
+                            if (!FEW) tma_load_2d(at + NT * 128, &tm_x, &c.xfull[s], kb * BK + 64, tile.row0);
                         }
                     }
                     __syncwarp();
-                    if (FEW && lane < gathers) tma_gather4(at + lane * 4 * BK, &tm_x, &full[s], kb * BK, tok);
-                    ++issued;
-                    if (++s == (uint32_t)stages) { s = 0; phase ^= 1u; }
+                    if (FEW && lane < gathers) tma_gather4(at + lane * 4 * BK, &tm_x, &c.xfull[s], kb * BK, tok);
                 }
             }
-            if (!ok) {
-                if (lane == 0) flag_status(p.status, kDevTimeout);
-                c.abort_flag = 1;
-            }
-        } else if (warp <= NW) {
-            // -------------------------------------------- multiply: a weight tile to a warp
+            issued = it;
+        } else if (warp <= C::MMAS) {
+            // -------------------------------------------- multiply
             const bool leader = elect_one();
-            const int w = warp - 1;
-            const uint32_t tokens = smem_u32(smem + (FEW ? C::XF : C::XRING));
+            constexpr int NM = NT / C::MMAS;
+            const int from = (warp - 1) * NM;   // this warp's first token
+            const uint32_t tokens = smem_u32(smem + (FEW ? C::XF : C::XRING)) + from * 128;
             uint32_t it = 0;
             for (int t = first, i = 0; t < total && ok; t += stride, ++i) {
                 const Tile tile = nth_tile(i, t);
                 // (N: as many columns as the tile has tokens, in sixteens)
-                const uint32_t idesc = idesc_f16_mn(1, M, (tile.cnt + 15) & ~15);
-                const int db = i % C::ND;
-                const uint32_t d = tmem + db * C::D_COLS + w * NT;
-                ok = bar_wait(&c.dempty[db], ((i / C::ND) & 1u) ^ 1u, abort_flag);
+                const int mine = min(tile.cnt - from, NM);
+                const uint32_t idesc = idesc_f16_mn(1, M, (mine + 15) & ~15);
+                const int db = i & 1;
+                const uint32_t d = tmem + db * NT + from;
+                ok = bar_wait(&c.dempty[db], ((i >> 1) & 1u) ^ 1u, abort_flag);
                 for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
-                    const uint32_t s = it % XS, a = it % NA;
-                    ok = (FEW || bar_wait(&c.xfull[s], (it / XS) & 1u, abort_flag)) &&
-                         bar_wait(&c.cfull[a], (it / NA) & 1u, abort_flag);
+                    const uint32_t a = it % NA;
+                    // (the converters have seen the tokens land too)
+                    ok = bar_wait(&c.cfull[a], (it / NA) & 1u, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint64_t dx = sw128_desc(tokens + (FEW ? a * C::XF_BYTES : s * C::X_BYTES));
-                    const uint32_t at = tmem + C::A_COL + a * kStageCols + (NW == 2 ? w * kUnitCols : 0);
+                    const uint64_t dx = sw128_desc(tokens + a * (FEW ? C::XF_BYTES : C::X_BYTES));
+                    const uint32_t at = tmem + C::A_COL + a * kBlockCols;
                     if (leader) {
+                        if (mine > 0)
 #pragma unroll
                         for (int kk = 0; kk < BK / 16; ++kk)
                             umma_f16_ts(d, at + kk * 8, desc_step(dx, (kk / 4) * NT * 128 + (kk % 4) * 32), idesc, kb != kb0 || kk != 0);
-                        if (!FEW) umma_commit(&c.xempty[s]);
                         umma_commit(&c.cempty[a]);
                         if (kb == kb1 - 1) umma_commit(&c.dfull[db]);
                     }
                     __syncwarp();
                 }
             }
-            if (!ok) {
-                if (leader) flag_status(p.status, kDevTimeout);
-                c.abort_flag = 1;
-            }
             issued = it;
+        }
+        if (!ok) {
+            if (lane == 0) flag_status(p.status, kDevTimeout);
+            c.abort_flag = 1;
         }
     } else if (warp >= 4 + C::EPI) {
         // ------------------------------------------------ convert
         if (!FEW) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
-        // Warps of a group of four take every second stage: a thread row `row` of both
-        // weight tiles, or all of its row, and a piece or two of the tokens.
-        const int tid = (threadIdx.x - 128 - 32 * C::EPI) & 127, group = (warp - 4 - C::EPI) >> 2;
+        // The groups take the blocks in turn: a thread its weight row, and (few rows) two pieces
+        // of the tokens.
+        const int tid = (threadIdx.x - 128 - 32 * C::EPI) & 127;
         const int quad = warp & 3, row = quad * 32 + lane;
         const uint32_t mine = tmem + ((uint32_t)(quad * 32) << 16) + C::A_COL;
-        uint32_t it = 0;
+        const uint32_t turns = total > first ? (uint32_t)((total - first - 1) / stride + 1) * (uint32_t)(kb1 - kb0) : 0u;
         ok = !expires(p, CONVERT) || __all_sync(0xffffffffu, bar_wait(&c.never, 0, abort_flag, p.expire_ns));
-        for (int t = first; t < total && ok; t += stride) {
-            for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                if ((it & 1u) != (uint32_t)group) continue;
-                const uint32_t s = it % WS, a = it % NA, sx = it % XS;
-                ok = __all_sync(0xffffffffu, bar_wait(&c.wfull[s], (it / WS) & 1u, abort_flag) &&
-                                                 bar_wait(&c.cempty[a], ((it / NA) & 1u) ^ 1u, abort_flag));
-                if (!ok) break;
-                tc_fence_after();
-                const uint8_t *sw = smem + s * C::W_BYTES;
-                const uint32_t at = mine + a * kStageCols;
+        for (uint32_t it = (warp - 4 - C::EPI) >> 2; it < turns && ok; it += C::GROUPS) {
+            const uint32_t s = it % WS, a = it % NA;
+            ok = __all_sync(0xffffffffu, bar_wait(&c.wfull[s], (it / WS) & 1u, abort_flag) &&
+                                             bar_wait(&c.cempty[a], ((it / NA) & 1u) ^ 1u, abort_flag));
+            if (!ok) break;
+            tc_fence_after();
+            const uint8_t *sw = smem + s * W_BYTES;
+            const uint32_t at = mine + a * kBlockCols;
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {   // 64 codes: a row of tile u, or half u of a row
-                    uint4 v[4];
+            for (int u = 0; u < 2; ++u) {
+                uint4 v[4];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        v[q] = *reinterpret_cast<const uint4 *>(sw + (NW == 2 ? u * M * BK : 0) + piece_at<BK>(row, (NW == 2 ? 0 : 4 * u) + q));
-                    if (u == 1) {   // the stage has been read
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&c.wempty[s]);
-                    }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t o[16];
-                        widen16(v[2 * h], o);
-                        widen16(v[2 * h + 1], o + 8);
-                        tmem_st16(at + u * kUnitCols + h * 16, o);
-                    }
-                }
-                if (FEW) {
-                    ok = __all_sync(0xffffffffu, bar_wait(&c.xfull[sx], (it / XS) & 1u, abort_flag));
-                    if (!ok) break;
-                    const uint8_t *xs = smem + C::XRING + sx * C::X_BYTES;
-                    uint8_t *xf = smem + C::XF + a * C::XF_BYTES;
-                    constexpr int PIECES = BK / 16, EACH = NT * PIECES / 128;
-#pragma unroll
-                    for (int j = 0; j < EACH; ++j) {
-                        const int q = tid + j * 128, xr = q / PIECES, xp = q % PIECES;
-                        uint32_t h[8];
-                        widen16(*reinterpret_cast<const uint4 *>(xs + piece_at<BK>(xr, xp)), h);
-                        uint8_t *to = xf + (xp >> 2) * NT * 128;
-                        *reinterpret_cast<uint4 *>(to + piece_at<128>(xr, (xp & 3) * 2)) = make_uint4(h[0], h[1], h[2], h[3]);
-                        *reinterpret_cast<uint4 *>(to + piece_at<128>(xr, (xp & 3) * 2 + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
-                    }
-                    fence_proxy_async_smem();
+                for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const uint4 *>(sw + piece_at(row, 4 * u + q));
+                if (u == 1) {   // the block has been read
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&c.xempty[sx]);
+                    if (lane == 0) mbar_arrive(&c.wempty[s]);
+                    __syncwarp();   // (here and below: the instructions that follow are .aligned)
                 }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&c.cfull[a]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t o[16];
+                    widen16(v[2 * h], o);
+                    widen16(v[2 * h + 1], o + 8);
+                    tmem_st16(at + u * 32 + h * 16, o);
+                }
             }
+            const uint32_t sx = it % XS;
+            ok = __all_sync(0xffffffffu, bar_wait(&c.xfull[sx], (it / XS) & 1u, abort_flag));
+            if (!ok) break;
+            if (FEW) {
+                const uint8_t *xs = smem + C::XRING + sx * C::X_BYTES;
+                uint8_t *xf = smem + C::XF + a * C::XF_BYTES;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int q = tid + j * 128, xr = q >> 3, xp = q & 7;
+                    uint32_t h[8];
+                    widen16(*reinterpret_cast<const uint4 *>(xs + piece_at(xr, xp)), h);
+                    uint8_t *to = xf + (xp >> 2) * NT * 128;
+                    *reinterpret_cast<uint4 *>(to + piece_at(xr, (xp & 3) * 2)) = make_uint4(h[0], h[1], h[2], h[3]);
+                    *reinterpret_cast<uint4 *>(to + piece_at(xr, (xp & 3) * 2 + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c.xempty[sx]);
+                __syncwarp();
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c.cfull[a]);
         }
         if (!ok) {
             if (lane == 0) flag_status(p.status, kDevTimeout);
@@ -496,161 +497,216 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     } else {
         // ------------------------------------------------ output
         if (!FEW) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
-        const int ew = warp - 4, quarter = warp & 3, part = ew >> 2;
-        const int chan = quarter * 32 + lane;
-        const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
+        // A warp has the 32 channels of its TMEM lanes and (tiled) 32 of the tokens.  GATEUP:
+        // lanes 0-63 are gate sums, 64-127 up sums of the same channels; the two warps of a
+        // channel exchange half of their tokens, and each finishes the other half.
+        const int ew = warp - 4, quarter = warp & 3, group = ew >> 2, tok0 = FEW ? 0 : group * 32;
+        const bool upper = MODE == GATEUP && quarter >= 2;
+        const int chan = (MODE == GATEUP ? quarter & 1 : quarter) * 32;
+        const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16) + tok0;
+        float *sx = c.sx[ew];
         // (once false, no more waits: the remaining rows become NaN)
         ok = !expires(p, SUMS) || __all_sync(0xffffffffu, bar_wait(&c.never, 0, abort_flag, p.expire_ns));
         for (int t = first, i = 0; t < total; t += stride, ++i) {
             const Tile tile = nth_tile(i, t);
-            const int db = i % C::ND;
-            const uint32_t d = lane_base + db * C::D_COLS;
-            // output channel (tiled PRODUCT: `part` is the weight tile and a half of the
-            // tokens; GATEUP: a quarter of them)
-            constexpr int TOK = FEW ? NT : MODE == GATEUP ? 32 : 64;
-            const int tok0 = FEW ? 0 : (MODE == GATEUP ? part : part & 1) * TOK;
-            const int n = tile.nt * C::ROWS + (MODE == PRODUCT ? (part >> 1) * M : 0) + chan;
-            float sw0 = 0.f, sw1 = 0.f;
-            if (FEW) {
-                const long long wn = (long long)tile.e * p.N + min(n, p.N - 1);
-                sw0 = __ldg(p.w_s[0] + wn);
-                if (MODE == GATEUP) sw1 = __ldg(p.w_s[1] + wn);
-            }
-            float *sx = c.sx[ew];
+            const int db = i & 1, n0 = tile.nt * ROWS + chan;   // the warp's first channel
+            const uint32_t d = lane_base + db * NT;
+            const int cnt = tile.cnt - tok0;                     // the warp's tokens (none or less: nothing to do)
+            const long long row0 = tile.row0 + tok0, wbase = (long long)tile.e * p.N;
             __syncwarp();
-            for (int l = lane; l < TOK; l += 32)
-                sx[l] = tok0 + l < tile.cnt ? __ldg(p.x_s + source_row(p, tile.row0 + tok0 + l)) : 0.f;
+            sx[lane] = lane < cnt ? __ldg(p.x_s + source_row(p, (int)row0 + lane)) : 0.f;
             __syncwarp();
-            ok = ok && __all_sync(0xffffffffu, bar_wait(&c.dfull[db], (i / C::ND) & 1u, abort_flag));
+            ok = ok && __all_sync(0xffffffffu, bar_wait(&c.dfull[db], (i >> 1) & 1u, abort_flag));
             if (!ok) {
                 // (the other roles may have left their loops: this warp reports too)
                 if (lane == 0) flag_status(p.status, kDevTimeout);
                 c.abort_flag = 1;
+                __syncwarp();
             }
             tc_fence_after();
             auto done_reading = [&] {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&c.dempty[db]);
+                __syncwarp();
             };
             if constexpr (SPLIT) {
-                // every MMA of this CTA has completed: the ring holds the partial sums
-                // from here on, [token][matrix][channel]
-                float *part_sum = reinterpret_cast<float *>(smem) + chan;
+                // every MMA of this CTA has completed: the weights' ring holds the partial
+                // sums from here on, [token][weight row]
+                float *part_sum = reinterpret_cast<float *>(smem) + quarter * 32 + lane;
 #pragma unroll 1
-                for (int i0 = 0; i0 < tile.cnt; i0 += 16) {
+                for (int i0 = 0; i0 < cnt; i0 += 16) {
+                    uint32_t v[16];
+                    __syncwarp();
+                    if (ok) tmem_ld16_wait(d + i0, v);
 #pragma unroll
-                    for (int w = 0; w < NW; ++w) {
-                        uint32_t v[16];
-                        if (ok) tmem_ld16_wait(d + w * NT + i0, v);
-#pragma unroll
-                        for (int q = 0; q < 16; ++q)
-                            if (i0 + q < tile.cnt) part_sum[((i0 + q) * NW + w) * M] = ok ? __uint_as_float(v[q]) : 0.f;
-                    }
+                    for (int q = 0; q < 16; ++q)
+                        if (i0 + q < cnt) part_sum[(i0 + q) * M] = ok ? __uint_as_float(v[q]) : 0.f;
                 }
                 break;   // one tile per cluster
             } else if constexpr (FEW) {
+                const long long wn = wbase + min(n0 + lane, p.N - 1);
+                const float sw0 = __ldg(p.w_s[0] + wn), sw1 = MODE == GATEUP ? __ldg(p.w_s[1] + wn) : 0.f;
 #pragma unroll 1
-                for (int i0 = 0; i0 < tile.cnt; i0 += 16) {
-                    uint32_t v[NW][16];
+                for (int i0 = 0; i0 < cnt; i0 += 16) {
+                    uint32_t v[16];
+                    __syncwarp();
                     if (ok) {
-#pragma unroll
-                        for (int w = 0; w < NW; ++w) tmem_ld16_wait(d + w * NT + i0, v[w]);
+                        tmem_ld16_wait(d + i0, v);
                     } else {
 #pragma unroll
-                        for (int q = 0; q < 16; ++q) v[0][q] = v[NW - 1][q] = 0x7fffffffu;
+                        for (int q = 0; q < 16; ++q) v[q] = 0x7fffffffu;
                     }
-                    if (i0 + 16 >= tile.cnt) done_reading();
-                    store_tokens<MODE, 16>(p, v[0], v[NW - 1], tile.row0 + i0, tile.cnt - i0, n - lane, lane, sx + i0, sw0, sw1);
+                    if (i0 + 16 >= cnt) done_reading();
+                    if constexpr (MODE == GATEUP) {
+                        // (the lower warp finishes tokens 0-7 of the sixteen, the upper 8-15)
+                        uint32_t *box = reinterpret_cast<uint32_t *>(smem + C::STAGING) + quarter * 32 + lane;
+                        uint32_t own[8], got[8];
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            box[q * M] = upper ? v[q] : v[8 + q];
+                            own[q] = upper ? v[8 + q] : v[q];
+                        }
+                        group_barrier(group);
+                        const uint32_t *from = reinterpret_cast<uint32_t *>(smem + C::STAGING) + (quarter ^ 2) * 32 + lane;
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) got[q] = from[q * M];
+                        group_barrier(group);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const uint32_t g = upper ? got[q] : own[q];
+                            got[q] = upper ? own[q] : got[q];
+                            own[q] = g;
+                        }
+                        const int l = i0 + (upper ? 8 : 0);
+                        store_tokens<MODE, 8>(p, own, got, row0 + l, cnt - l, n0, lane, sx + l, sw0, sw1);
+                    } else {
+                        store_tokens<MODE, 16>(p, v, v, row0 + i0, cnt - i0, n0, lane, sx + i0, sw0, sw1);
+                    }
                 }
             } else {
-                // all of the warp's sums go into registers first: the accumulator is the
-                // next tile's from then on
-                constexpr int H = MODE == GATEUP ? 16 : 32;   // registers of 16 channels
-                const uint32_t from = d + (MODE == GATEUP ? 0 : (part >> 1) * NT) + tok0;
-                uint32_t v[64];
-                if (!ok) {
+                uint32_t v[32];
+                if (cnt > 0) {   // (the whole group)
+                    if (ok) {
+                        tmem_ld_frags(d, v);
+                    } else {
 #pragma unroll
-                    for (int q = 0; q < 64; ++q) v[q] = 0x7fffffffu;
-                } else {
-                    if (MODE == GATEUP) tmem_ld_frags2(from, from + NT, v);
-                    else tmem_ld_frags(from, v);
+                        for (int q = 0; q < 32; ++q) v[q] = 0x7fffffffu;
+                    }
                 }
                 done_reading();
-                // v[h H + 4 j + 2 r + q]: channel 16 h + 8 r + lane / 4, token 8 j + 2 (lane % 4) + q
-                float sw[NW][4];
+                if (cnt <= 0) continue;
+                float sw[2][4];   // of channels n0 + 8 f + lane / 4
 #pragma unroll
                 for (int f = 0; f < 4; ++f) {
-                    const long long at = (long long)tile.e * p.N + min(n - lane + f * 8 + (lane >> 2), p.N - 1);
+                    const long long at = wbase + min(n0 + f * 8 + (lane >> 2), p.N - 1);
                     sw[0][f] = __ldg(p.w_s[0] + at);
-                    sw[NW - 1][f] = __ldg(p.w_s[NW - 1 < 1 || MODE == PRODUCT ? 0 : 1] + at);
+                    sw[1][f] = MODE == GATEUP ? __ldg(p.w_s[1] + at) : 0.f;
+                }
+                uint8_t *stg = smem + C::STAGING + group * 4 * (kStaging / 2);   // the group's
+                constexpr int J = MODE == GATEUP ? 2 : 4;                        // octets of tokens to finish
+                int l0 = 0;                                                      // the first of them
+                if constexpr (MODE == GATEUP) {
+                    // keep octets 0, 1 (upper: 2, 3), send the others: 16 values a thread, in two
+                    // turns through the group's 4 KB
+                    l0 = upper ? 16 : 0;
+                    uint4 *box = reinterpret_cast<uint4 *>(stg) + quarter * 32 + lane;
+                    const uint4 *from = reinterpret_cast<uint4 *>(stg) + (quarter ^ 2) * 32 + lane;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t *a = v + 16 * h;
+                        if (h) group_barrier(group);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            box[j * 128] = upper ? make_uint4(a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3])
+                                                 : make_uint4(a[8 + 4 * j], a[9 + 4 * j], a[10 + 4 * j], a[11 + 4 * j]);
+                        group_barrier(group);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const uint4 got = from[j * 128];
+                            const uint32_t w[4] = {got.x, got.y, got.z, got.w};
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                // a[4 j + q] becomes the gate's, a[8 + 4 j + q] the up's
+                                const uint32_t own = upper ? a[8 + 4 * j + q] : a[4 * j + q];
+                                a[4 * j + q] = upper ? w[q] : own;
+                                a[8 + 4 * j + q] = upper ? own : w[q];
+                            }
+                        }
+                    }
                 }
                 auto value = [&](int j, int f, int q) {   // octet of tokens, octet of channels, token of a pair
-                    const int i = (f >> 1) * H + 4 * j + 2 * (f & 1) + q;
-                    const float s = sx[8 * j + 2 * (lane & 3) + q];
-                    return finish<MODE>(p, __uint_as_float(v[i]), __uint_as_float(v[(i + 32) & 63]), s, sw[0][f], sw[NW - 1][f]);
+                    const int at = (f >> 1) * 16 + 4 * j + 2 * (f & 1) + q;
+                    return finish<MODE>(p, __uint_as_float(v[at]), __uint_as_float(v[MODE == GATEUP ? at + 8 : at]),
+                                        sx[l0 + 8 * j + 2 * (lane & 3) + q], sw[0][f], sw[1][f]);
                 };
-                const long long row0 = tile.row0 + tok0;
-                const int rows = tile.cnt - tok0;
+                const int rows = cnt - l0;   // (GATEUP's upper warps may have none)
                 if (p.out_f32) {
-                    // the warp's 32 channels of 16 tokens at a time
-                    uint8_t *stg = smem + C::STAGING + ew * kStaging;
+                    // the warp's 32 channels of 8 tokens at a time
+                    uint8_t *st = stg + quarter * (kStaging / 2);
+                    if (MODE == GATEUP) group_barrier(group);
 #pragma unroll
-                    for (int rd = 0; rd < TOK / 16; ++rd) {
-                        if (rd * 16 >= rows) break;
+                    for (int j = 0; j < J; ++j) {
+                        if (j * 8 >= rows) break;
                         if (lane == 0) bulk_wait_read();
                         __syncwarp();
 #pragma unroll
-                        for (int jj = 0; jj < 2; ++jj)
+                        for (int f = 0; f < 4; ++f)
 #pragma unroll
-                            for (int f = 0; f < 4; ++f)
-#pragma unroll
-                                for (int q = 0; q < 2; ++q) {
-                                    const int tr = 8 * jj + 2 * (lane & 3) + q, ch = f * 8 + (lane >> 2);
-                                    *reinterpret_cast<float *>(stg + piece_at<128>(tr, ch >> 2) + (ch & 3) * 4) = value(2 * rd + jj, f, q);
-                                }
-                        if (p.out_vec && rows - rd * 16 >= 16) {
+                            for (int q = 0; q < 2; ++q) {
+                                const int tr = 2 * (lane & 3) + q, ch = f * 8 + (lane >> 2);
+                                *reinterpret_cast<float *>(st + piece_at(tr, ch >> 2) + (ch & 3) * 4) = value(j, f, q);
+                            }
+                        if (p.out_vec && rows - j * 8 >= 8) {
                             fence_proxy_async_smem();
                             __syncwarp();
                             if (lane == 0) {
-                                if (n < p.N) tma_store_2d(&tm_out, stg, n, (int)row0 + rd * 16);
+                                if (n0 < p.N) tma_store_2d(&tm_out, st, n0, (int)row0 + l0 + j * 8);
                                 bulk_commit();
                             }
                         } else {
                             __syncwarp();
-                            float *o = static_cast<float *>(p.out) + (row0 + rd * 16) * p.ldo + n - lane;
-                            store_staged<float, 32, 16>(o, p.ldo, stg, lane, min(rows - rd * 16, 16), p.N - (n - lane), p.out_vec);
+                            float *o = static_cast<float *>(p.out) + (row0 + l0 + j * 8) * p.ldo + n0;
+                            store_staged<float, 32, 8>(o, p.ldo, st, lane, min(rows - j * 8, 8), p.N - n0, p.out_vec);
                         }
                     }
+                    if (MODE == GATEUP) {   // (the group's next exchange: all four warps' stores have left)
+                        if (lane == 0) bulk_wait_read();
+                        group_barrier(group);
+                    }
                 } else {
-                    // the pair's 64 channels of 32 tokens at a time
-                    uint8_t *stg = smem + C::STAGING + (ew >> 1) * 2 * kStaging;
-                    const int half = ew & 1, n0 = n - lane - half * 32;
+                    // two warps' 64 channels of 16 tokens at a time: 2 KB for each pair
+                    const int pair = quarter >> 1, half = quarter & 1, np = n0 - half * 32;
+                    uint8_t *st = stg + pair * kStaging;
 #pragma unroll
-                    for (int rd = 0; rd < TOK / 32; ++rd) {
-                        if (rd * 32 >= rows) break;
+                    for (int j0 = 0; j0 < J; j0 += 2) {
+                        if (j0 * 8 >= cnt) break;   // (the group)
                         if (half == 0 && lane == 0) bulk_wait_read();
-                        pair_barrier(ew >> 1);
+                        group_barrier(group);
 #pragma unroll
-                        for (int jj = 0; jj < 4; ++jj) {
-                            const int tr = 8 * jj + (lane & 7), j = 4 * rd + jj;
+                        for (int j = j0; j < j0 + 2; ++j) {
                             uint32_t w[4];
 #pragma unroll
                             for (int f = 0; f < 4; ++f) w[f] = fp8b::bf16x2(value(j, f, 0), value(j, f, 1));
-                            store_frags(smem_u32(stg + piece_at<128>(tr, half * 4 + (lane >> 3))), w[0], w[1], w[2], w[3]);
+                            store_frags(smem_u32(st + piece_at(8 * (j - j0) + (lane & 7), half * 4 + (lane >> 3))), w[0], w[1], w[2], w[3]);
                         }
-                        if (p.out_vec && rows - rd * 32 >= 32) {
-                            fence_proxy_async_smem();
-                            pair_barrier(ew >> 1);
+                        const int left = rows - j0 * 8;
+                        const bool tma = p.out_vec && left >= 16;
+                        if (tma) fence_proxy_async_smem();
+                        group_barrier(group);
+                        if (tma) {
                             if (half == 0 && lane == 0) {
-                                if (n0 < p.N) tma_store_2d(&tm_out, stg, n0, (int)row0 + rd * 32);
+                                if (np < p.N) tma_store_2d(&tm_out, st, np, (int)row0 + l0 + j0 * 8);
                                 bulk_commit();
                             }
-                        } else {
-                            pair_barrier(ew >> 1);
-                            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + (row0 + rd * 32) * p.ldo + n0;
-                            store_staged<__nv_bfloat16, 64, 32>(o, p.ldo, stg, half * 32 + lane, min(rows - rd * 32, 32), p.N - n0, p.out_vec);
+                        } else if (left > 0) {
+                            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + (row0 + l0 + j0 * 8) * p.ldo + np;
+                            store_staged<__nv_bfloat16, 64, 16>(o, p.ldo, st, half * 32 + lane, min(left, 16), p.N - np, p.out_vec);
                         }
+                    }
+                    if (MODE == GATEUP) {
+                        if (half == 0 && lane == 0) bulk_wait_read();
+                        group_barrier(group);
                     }
                 }
             }
@@ -661,19 +717,21 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     if constexpr (SPLIT) {
         cluster_sync_all();   // every CTA's partial sums are written
         if (first < total && warp >= 4 && warp < 4 + C::EPI) {
-            // tokens rank, rank + S, ...: a thread to a channel adds the CTAs' sums in
-            // the order of the blocks
+            // tokens rank, rank + S, ...: a thread to a channel (GATEUP: two tokens at a time)
+            // adds the CTAs' sums in the order of the blocks
             const Tile tile = nth_tile(0, first);
-            const int chan = (warp & 3) * 32 + lane, n = tile.nt * C::ROWS + chan;
+            const int tid = threadIdx.x - 128, chan = tid & (ROWS - 1), sub = tid / ROWS, n = tile.nt * ROWS + chan;
+            constexpr int NW = M / ROWS;   // sums of a channel, and tokens at a time
             const long long wn = (long long)tile.e * p.N + min(n, p.N - 1);
             const float sw0 = __ldg(p.w_s[0] + wn), sw1 = MODE == GATEUP ? __ldg(p.w_s[1] + wn) : 0.f;
             // (a CTA that gave up may still have had loads landing on its sums)
             bool failed = false;
             for (int q = 0; q < S; ++q) failed |= ld_cluster_u32(peer_addr(&c.abort_flag, q)) != 0u;
-            // (four tokens in flight where this CTA has more than one)
+            // (four tokens in flight where this thread has more than one)
             auto add_up = [&](auto tokens) {
                 constexpr int U = decltype(tokens)::value, kPeers = U == 1 ? 8 : 2;   // (eight reads in flight)
-                for (int i0 = rank; i0 < tile.cnt; i0 += U * S) {
+                const int step = S * NW;
+                for (int i0 = rank + sub * S; i0 < tile.cnt; i0 += U * step) {
                     float v[U][NW];
 #pragma unroll
                     for (int u = 0; u < U; ++u)
@@ -684,14 +742,14 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                         const uint32_t at = peer_addr(smem, q) + (uint32_t)chan * 4;
 #pragma unroll
                         for (int u = 0; u < U; ++u) {
-                            const int l = min(i0 + u * S, tile.cnt - 1);
+                            const int l = min(i0 + u * step, tile.cnt - 1);
 #pragma unroll
-                            for (int w = 0; w < NW; ++w) v[u][w] += ld_cluster_f32(at + (uint32_t)((l * NW + w) * M) * 4);
+                            for (int w = 0; w < NW; ++w) v[u][w] += ld_cluster_f32(at + (uint32_t)(l * M + w * ROWS) * 4);
                         }
                     }
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
-                        const int l = i0 + u * S;
+                        const int l = i0 + u * step;
                         if (l < tile.cnt && n < p.N) {
                             const float bad = __uint_as_float(0x7fffffffu);
                             store_out(p, tile.row0 + l, n,
@@ -700,7 +758,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                     }
                 }
             };
-            if (tile.cnt <= S) add_up(std::integral_constant<int, 1>());
+            if (tile.cnt <= S * NW) add_up(std::integral_constant<int, 1>());
             else add_up(std::integral_constant<int, 4>());
         }
         cluster_sync_all();   // no CTA leaves while a peer reads its shared memory
@@ -712,10 +770,10 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         // issued: loads land before the CTA exits, MMAs end before TMEM is freed.
         volatile int no_abort = 0;
         if (warp == 0 || warp == 3) {
-            const uint32_t stages = warp == 0 ? WS : XS;
-            for (uint32_t j = issued >= stages ? issued - stages : 0; j < issued; ++j)
-                bar_wait(warp == 0 ? &c.wfull[j % stages] : &c.xfull[j % stages], (j / stages) & 1u, &no_abort, 1000000ull);
-        } else if (warp <= NW && issued > 0) {
+            const uint32_t depth = warp == 0 ? WS : XS;
+            for (uint32_t j = issued >= depth ? issued - depth : 0; j < issued; ++j)
+                bar_wait(warp == 0 ? &c.wfull[j % depth] : &c.xfull[j % depth], (j / depth) & 1u, &no_abort, 1000000ull);
+        } else if (warp <= C::MMAS && issued > 0) {
             if (elect_one()) umma_commit(&c.drain[warp - 1]);
             bar_wait(&c.drain[warp - 1], 0, &no_abort);
         }
@@ -781,11 +839,11 @@ template <int MODE, bool FEW, bool SPLIT>
 cudaError_t launch_variant(const CUtensorMap &x, const CUtensorMap &w0, const CUtensorMap &w1, const CUtensorMap &out, const Params &p,
                            long long tiles, int num_sms, cudaStream_t stream)
 {
-    using C = Cfg<MODE, FEW>;
+    using C = Cfg<FEW>;
     static PerDeviceFlag done;
     const int dev = current_device();
     auto *kern = product_kernel<MODE, FEW, SPLIT>;
-    constexpr size_t smem = smem_bytes<MODE, FEW>();
+    constexpr size_t smem = smem_bytes<FEW>();
     if (!done.done(dev)) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
@@ -805,13 +863,10 @@ long long most_tiles(const Params &p, int rows_per_tile)
     return ((p.rows - experts) / rows_per_tile + experts) * p.n_tiles;
 }
 
-template <int MODE, bool FEW>
-bool weight_maps(const Params &p, CUtensorMap *w0, CUtensorMap *w1)
+template <int MODE> bool weight_maps(const Params &p, CUtensorMap *w0, CUtensorMap *w1)
 {
-    using C = Cfg<MODE, FEW>;
-    const auto swizzle = C::BK == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
     const auto map = [&](CUtensorMap *m, const void *w) {
-        return make_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, p.E, p.N, p.K, p.K, C::BK, C::ROWS, swizzle);
+        return make_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, p.E, p.N, p.K, p.K, BK, rows_of_mode(MODE), CU_TENSOR_MAP_SWIZZLE_128B);
     };
     if (!map(w0, p.w[0])) return false;
     if (MODE != GATEUP) { *w1 = *w0; return true; }
@@ -824,10 +879,10 @@ size_t tiled_workspace(int rows, int K) { return align_up((size_t)rows * K * 2, 
 
 template <int MODE> cudaError_t launch_tiled(const Params &args, void *workspace, cudaStream_t stream)
 {
-    using C = Cfg<MODE, false>;
+    using C = Cfg<false>;
     Params p = args;
     const int num_sms = device_sm_count();
-    p.n_tiles = ceil_div(p.N, C::ROWS);
+    p.n_tiles = ceil_div(p.N, rows_of_mode(MODE));
     p.split = 1;
     const long long tiles = most_tiles(p, C::NT);
     if (tiles > 0x3fffffffLL) return cudaErrorInvalidValue;
@@ -841,37 +896,37 @@ template <int MODE> cudaError_t launch_tiled(const Params &args, void *workspace
                                      static_cast<uint4 *>(workspace));
     if (e != cudaSuccess) return e;
     CUtensorMap mx, mw0, mw1;
-    if (!make_map(&mx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, workspace, 0, p.rows, p.K, (long long)p.K * 2, C::BK, C::NT,
+    if (!make_map(&mx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, workspace, 0, p.rows, p.K, (long long)p.K * 2, 64, C::NT,
                   CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !weight_maps<MODE, false>(p, &mw0, &mw1))
+        !weight_maps<MODE>(p, &mw0, &mw1))
         return cudaErrorInvalidValue;
     CUtensorMap mout = mx;   // (not used where rows are not on 16-byte boundaries)
     if (p.out_vec && !make_map(&mout, p.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.out, 0, p.rows,
-                               p.N, p.ldo * (p.out_f32 ? 4 : 2), p.out_f32 ? 32 : 64, p.out_f32 ? 16 : 32, CU_TENSOR_MAP_SWIZZLE_128B))
+                               p.N, p.ldo * (p.out_f32 ? 4 : 2), p.out_f32 ? 32 : 64, p.out_f32 ? 8 : 16, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
     return launch_variant<MODE, false, false>(mx, mw0, mw1, mout, p, tiles, num_sms, stream);
 }
 
 template <int MODE> cudaError_t launch_few(const Params &args, cudaStream_t stream)
 {
-    using C = Cfg<MODE, true>;
+    using C = Cfg<true>;
     Params p = args;
     const int num_sms = device_sm_count();
-    p.n_tiles = ceil_div(p.N, C::ROWS);
+    p.n_tiles = ceil_div(p.N, rows_of_mode(MODE));
     const long long tiles = most_tiles(p, C::NT);
     if (tiles > 0x3fffffffLL) return cudaErrorInvalidValue;
     // tiles for fewer than half the SMs: split the reduction over a CTA for each SM, at
     // most 8 a tile
     p.split = 1;
-    const int KB = ceil_div(p.K, C::BK);
+    const int KB = ceil_div(p.K, BK);
     if (2 * tiles <= num_sms && KB >= 8) {
         const long long each = num_sms / tiles;
         p.split = (int)(each < 8 ? each : 8);
     }
     CUtensorMap mx, mw0, mw1;
-    if (!make_map(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.x_q, 0, p.x_rows, p.K, p.ldx, C::BK, p.perm_tok ? 1 : C::NT,
-                  C::BK == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !weight_maps<MODE, true>(p, &mw0, &mw1))
+    if (!make_map(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.x_q, 0, p.x_rows, p.K, p.ldx, BK, p.perm_tok ? 1 : C::NT,
+                  CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !weight_maps<MODE>(p, &mw0, &mw1))
         return cudaErrorInvalidValue;
     return p.split > 1 ? launch_variant<MODE, true, true>(mx, mw0, mw1, mx, p, tiles, num_sms, stream)
                        : launch_variant<MODE, true, false>(mx, mw0, mw1, mx, p, tiles, num_sms, stream);
