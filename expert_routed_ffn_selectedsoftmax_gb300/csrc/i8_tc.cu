@@ -82,7 +82,7 @@ template <int EPI> struct alignas(16) Ctl {
     uint64_t never;                          // nothing arrives here (test hook)
     uint32_t tmem_base;
     int abort_flag;
-    alignas(16) float sx[EPI][32];           // each output warp's token scales
+    alignas(16) float sx[EPI][32], sw[EPI][2][EPI == 4 ? 1 : 32];   // each output warp's scales: tokens', channels' (tiled)
     Groups g;
     Tile tiles[kTable];                      // this CTA's first tiles (each role asks for them in turn)
 };
@@ -91,8 +91,8 @@ template <bool FEW> constexpr size_t smem_bytes() { return 1024 + Cfg<FEW>::CTL 
 static_assert(smem_bytes<false>() <= 232448, "shared memory per CTA");
 static_assert(smem_bytes<true>() <= 115712, "two CTAs per SM");
 // registers a thread after the split at start (setmaxnreg) of the tiled kernel: 28 warps
-// launch with 72 each, 2016; 4 x 56 + 8 x 64 + 16 x 80 = 2016
-constexpr int kRegsLaunch = 72, kRegsAux = 56, kRegsConv = 64, kRegsEpi = 80;
+// launch with 72 each, 2016; 4 x 40 + 8 x 56 + 16 x 88 = 2016
+constexpr int kRegsLaunch = 72, kRegsAux = 40, kRegsConv = 56, kRegsEpi = 88;
 static_assert(4 * kRegsAux + 8 * kRegsConv + 16 * kRegsEpi <= 28 * kRegsLaunch, "more registers than the block has");
 
 #define MOE_OUTS8(i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), "=r"(v[i + 6]), "=r"(v[i + 7])
@@ -505,17 +505,33 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         const int chan = (MODE == GATEUP ? quarter & 1 : quarter) * 32;
         const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16) + tok0;
         float *sx = c.sx[ew];
+        auto &sw = c.sw[ew];
         // (once false, no more waits: the remaining rows become NaN)
         ok = !expires(p, SUMS) || __all_sync(0xffffffffu, bar_wait(&c.never, 0, abort_flag, p.expire_ns));
+        // A tile's scales are asked for a tile ahead, lane l's token and channel l's (two loads,
+        // one after the other, where rows are gathered).
+        float nx = 0.f, nw[2] = {0.f, 0.f};
+        auto enter = [&](int i, int t) {
+            if (t >= total) return;
+            const Tile next = nth_tile(i, t);
+            nx = lane < next.cnt - tok0 ? __ldg(p.x_s + source_row(p, next.row0 + tok0 + lane)) : 0.f;
+            const long long at = (long long)next.e * p.N + min(next.nt * ROWS + chan + lane, p.N - 1);
+            nw[0] = __ldg(p.w_s[0] + at);
+            if (MODE == GATEUP) nw[1] = __ldg(p.w_s[1] + at);
+        };
+        enter(0, first);
         for (int t = first, i = 0; t < total; t += stride, ++i) {
             const Tile tile = nth_tile(i, t);
             const int db = i & 1, n0 = tile.nt * ROWS + chan;   // the warp's first channel
             const uint32_t d = lane_base + db * NT;
             const int cnt = tile.cnt - tok0;                     // the warp's tokens (none or less: nothing to do)
-            const long long row0 = tile.row0 + tok0, wbase = (long long)tile.e * p.N;
+            const long long row0 = tile.row0 + tok0;
             __syncwarp();
-            sx[lane] = lane < cnt ? __ldg(p.x_s + source_row(p, (int)row0 + lane)) : 0.f;
+            sx[lane] = nx;
+            const float sw0 = nw[0], sw1 = nw[1];
+            if constexpr (!FEW) { sw[0][lane] = sw0; sw[1][lane] = sw1; }
             __syncwarp();
+            enter(i + 1, t + stride);
             ok = ok && __all_sync(0xffffffffu, bar_wait(&c.dfull[db], (i >> 1) & 1u, abort_flag));
             if (!ok) {
                 // (the other roles may have left their loops: this warp reports too)
@@ -545,8 +561,6 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                 }
                 break;   // one tile per cluster
             } else if constexpr (FEW) {
-                const long long wn = wbase + min(n0 + lane, p.N - 1);
-                const float sw0 = __ldg(p.w_s[0] + wn), sw1 = MODE == GATEUP ? __ldg(p.w_s[1] + wn) : 0.f;
 #pragma unroll 1
                 for (int i0 = 0; i0 < cnt; i0 += 16) {
                     uint32_t v[16];
@@ -596,13 +610,6 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                 }
                 done_reading();
                 if (cnt <= 0) continue;
-                float sw[2][4];   // of channels n0 + 8 f + lane / 4
-#pragma unroll
-                for (int f = 0; f < 4; ++f) {
-                    const long long at = wbase + min(n0 + f * 8 + (lane >> 2), p.N - 1);
-                    sw[0][f] = __ldg(p.w_s[0] + at);
-                    sw[1][f] = MODE == GATEUP ? __ldg(p.w_s[1] + at) : 0.f;
-                }
                 uint8_t *stg = smem + C::STAGING + group * 4 * (kStaging / 2);   // the group's
                 constexpr int J = MODE == GATEUP ? 2 : 4;                        // octets of tokens to finish
                 int l0 = 0;                                                      // the first of them
@@ -638,7 +645,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                 auto value = [&](int j, int f, int q) {   // octet of tokens, octet of channels, token of a pair
                     const int at = (f >> 1) * 16 + 4 * j + 2 * (f & 1) + q;
                     return finish<MODE>(p, __uint_as_float(v[at]), __uint_as_float(v[MODE == GATEUP ? at + 8 : at]),
-                                        sx[l0 + 8 * j + 2 * (lane & 3) + q], sw[0][f], sw[1][f]);
+                                        sx[l0 + 8 * j + 2 * (lane & 3) + q], sw[0][8 * f + (lane >> 2)], sw[1][8 * f + (lane >> 2)]);
                 };
                 const int rows = cnt - l0;   // (GATEUP's upper warps may have none)
                 if (p.out_f32) {
