@@ -14,8 +14,8 @@
 //   tiled     128 of them, as fp16 rows that convert_rows_kernel has written (in group
 //             order, so it gathers too), by TMA;
 //   few rows  32, read as int8 and widened into shared memory by the same warps; two CTAs
-//             an SM.  Few tiles split the reduction over a cluster, whose partial sums
-//             meet in distributed shared memory.
+//             an SM.  Few tiles split the reduction over a cluster, whose CTAs send their
+//             partial sums to the one that finishes the token (distributed shared memory).
 // Accumulators are two, so a tile's output overlaps the next tile's products.
 //
 // Warp 0 loads weights, warp 3 tokens (one warp for both issued its loads in 930 clocks a
@@ -49,14 +49,16 @@ constexpr int BK = 128;                      // columns of a block of the reduct
 constexpr int W_BYTES = M * BK;
 constexpr int kBlockCols = BK / 2;           // TMEM columns of a block's weights as fp16
 constexpr int kStaging = 2048;
+constexpr int kMaxSplit = 8;                 // CTAs of a cluster
+constexpr size_t kPartial = (size_t)(32 + kMaxSplit) * M * 4;   // whole turns of 32 tokens over the CTAs
 
 // output channels of a tile
 constexpr int rows_of_mode(int mode) { return mode == GATEUP ? M / 2 : M; }
 
-template <bool FEW> struct Cfg {
+template <bool FEW, bool SPLIT = false> struct Cfg {
     static constexpr int NT = FEW ? 32 : 128;                      // tokens of a tile
     static constexpr int X_BYTES = NT * BK * (FEW ? 1 : 2);
-    static constexpr int WS = 4;                                   // blocks of the weights' ring
+    static constexpr int WS = SPLIT ? 3 : 4;                       // blocks of the weights' ring
     static constexpr int NA = FEW ? 3 : 4;                         // converted blocks in flight
     static constexpr int XS = FEW ? 4 : NA;                        // blocks of the tokens' ring (tiled: block a's
                                                                    // tokens are freed with its converted weights)
@@ -65,14 +67,18 @@ template <bool FEW> struct Cfg {
     static constexpr int TMEM_COLS = FEW ? 256 : 512;
     static constexpr int MMAS = FEW ? 1 : 2;                       // multiplying warps, each with its share of the tokens
     static constexpr int EPI = FEW ? 4 : 16;                       // output warps
-    static constexpr int GROUPS = 2;                               // of four converting warps, which take the blocks in turn
-    static constexpr int THREADS = 128 + 32 * (EPI + 4 * GROUPS);
+    // Converting warps are eight: four of them a block in turn, a thread a weight row; or
+    // (split) all of them a block, a thread half a row, as the first block is what a short
+    // reduction waits for (one token, 2048 x 5632: 8.5 -> 7.5 us; 64 tokens, whole: 10.4 -> 12.3).
+    static constexpr int GROUPS = SPLIT ? 1 : 2, PER_BLOCK = 8 / GROUPS;
+    static constexpr int THREADS = 128 + 32 * (EPI + 8);
     static constexpr size_t XRING = (size_t)WS * W_BYTES;
     static constexpr size_t XF = XRING + (size_t)XS * X_BYTES;
     static constexpr size_t STAGING = XF + (size_t)NA * XF_BYTES;
-    static constexpr size_t CTL = STAGING + (FEW ? 2 * kStaging : (size_t)EPI * kStaging / 2);
+    // (split: the CTAs' sums of this CTA's tokens; two CTAs an SM also let the next kernel of
+    // the stream start beside this one)
+    static constexpr size_t CTL = STAGING + (SPLIT ? kPartial : FEW ? 2 * kStaging : EPI * kStaging / 2);
     static_assert(A_COL + NA * kBlockCols <= TMEM_COLS, "tensor memory");
-    static_assert(!FEW || (size_t)NT * M * 4 <= XRING, "split partial sums reuse the weights' ring");
 };
 constexpr int kMaxRing = 4, kTable = 32;
 
@@ -87,9 +93,9 @@ template <int EPI> struct alignas(16) Ctl {
     Tile tiles[kTable];                      // this CTA's first tiles (each role asks for them in turn)
 };
 template <bool FEW> using CtlOf = Ctl<Cfg<FEW>::EPI>;
-template <bool FEW> constexpr size_t smem_bytes() { return 1024 + Cfg<FEW>::CTL + sizeof(CtlOf<FEW>); }
+template <bool FEW, bool SPLIT = false> constexpr size_t smem_bytes() { return 1024 + Cfg<FEW, SPLIT>::CTL + sizeof(CtlOf<FEW>); }
 static_assert(smem_bytes<false>() <= 232448, "shared memory per CTA");
-static_assert(smem_bytes<true>() <= 115712, "two CTAs per SM");
+static_assert(smem_bytes<true>() <= 115712 && smem_bytes<true, true>() <= 115712, "two CTAs per SM");
 // registers a thread after the split at start (setmaxnreg) of the tiled kernel: 28 warps
 // launch with 72 each, 2016; 4 x 40 + 8 x 56 + 16 x 88 = 2016
 constexpr int kRegsLaunch = 72, kRegsAux = 40, kRegsConv = 56, kRegsEpi = 88;
@@ -161,6 +167,13 @@ __device__ __forceinline__ void widen16(const uint4 v, uint32_t *o)
         o[2 * i + 1] = *reinterpret_cast<const uint32_t *>(&b);
     }
 }
+__device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+// The two halves of a barrier of all threads of the cluster (each warp converged).
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 __device__ __forceinline__ bool expires(const Params &p, Role role) { return p.expire_ns && p.expire_role == role; }
 // Byte offset of 16-byte piece c of row r in a tile of 128-byte rows (TMA's 128-byte swizzle).
 __device__ __forceinline__ int piece_at(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
@@ -282,7 +295,7 @@ __global__ void __launch_bounds__(Cfg<FEW>::THREADS, FEW ? 2 : 1)
 product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w0,
                const __grid_constant__ CUtensorMap tm_w1, const __grid_constant__ CUtensorMap tm_out, const Params p)
 {
-    using C = Cfg<FEW>;
+    using C = Cfg<FEW, SPLIT>;
     constexpr int NT = C::NT, WS = C::WS, XS = C::XS, NA = C::NA, ROWS = rows_of_mode(MODE);
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -291,9 +304,9 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     const int E = p.E;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < WS; ++s) { mbar_init(&c.wfull[s], 1); mbar_init(&c.wempty[s], 4); }
-        for (int s = 0; s < XS; ++s) { mbar_init(&c.xfull[s], 1); mbar_init(&c.xempty[s], 4); }
-        for (int a = 0; a < NA; ++a) { mbar_init(&c.cfull[a], 4); mbar_init(&c.cempty[a], C::MMAS); }
+        for (int s = 0; s < WS; ++s) { mbar_init(&c.wfull[s], 1); mbar_init(&c.wempty[s], C::PER_BLOCK); }
+        for (int s = 0; s < XS; ++s) { mbar_init(&c.xfull[s], 1); mbar_init(&c.xempty[s], C::PER_BLOCK); }
+        for (int a = 0; a < NA; ++a) { mbar_init(&c.cfull[a], C::PER_BLOCK); mbar_init(&c.cempty[a], C::MMAS); }
         for (int d = 0; d < 2; ++d) { mbar_init(&c.dfull[d], C::MMAS); mbar_init(&c.dempty[d], C::EPI); }
         for (int w = 0; w < 2; ++w) mbar_init(&c.drain[w], 1);
         mbar_init(&c.never, 1);
@@ -305,7 +318,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     }
     if (warp == 3) tmem_alloc(&c.tmem_base, C::TMEM_COLS);
     tc_fence_before();
-    // (without offsets nothing up to here reads what the kernel before writes)
+    // (without offsets nothing up to the roles reads what the kernel before writes)
     if (p.offsets) pdl_enter();
     load_groups(c.g, p);
     __syncthreads();
@@ -313,22 +326,26 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (!p.offsets) pdl_enter();
 
     const uint32_t tmem = c.tmem_base;
-    const int S = SPLIT ? p.split : 1;
-    const int rank = SPLIT ? (int)cluster_rank() : 0;
+    const uint32_t S = SPLIT ? p.split : 1;
+    const uint32_t rank = SPLIT ? cluster_rank() : 0;
     const int first = SPLIT ? blockIdx.x / S : blockIdx.x;
     const int stride = SPLIT ? gridDim.x / S : gridDim.x;
     // (a cluster takes one tile, whatever total the offsets add up to)
     const int total = SPLIT ? min(c.g.total, first + 1) : c.g.total;
-    // this CTA's blocks of the reduction
-    const int KB = (p.K + BK - 1) / BK;
-    const int kb0 = (int)((long long)KB * rank / S), kb1 = (int)((long long)KB * (rank + 1) / S);
+    // this CTA's blocks of the reduction (at most 2^24 of them, and 8 CTAs)
+    const uint32_t KB = (uint32_t)(p.K + BK - 1) / BK;
+    const int kb0 = (int)(KB * rank / S), kb1 = (int)(KB * (rank + 1) / S);
     // (a search and two divides a tile)
     if (threadIdx.x < kTable && first + (int)threadIdx.x * stride < total)
         c.tiles[threadIdx.x] = tile_at(c.g, E, first + threadIdx.x * stride, NT);
     __syncthreads();
+    if (!p.offsets) pdl_enter();
+    // (the CTAs of a cluster may write one another's memory once all have started)
+    if (SPLIT) cluster_arrive();
+    bool met = false;
+    uint8_t *partial = smem + C::STAGING;
     auto nth_tile = [&](int i, int t) { return i < kTable ? c.tiles[i] : tile_at(c.g, E, t, NT); };
     volatile int *abort_flag = &c.abort_flag;
     uint32_t issued = 0;   // blocks this warp has loaded or multiplied
@@ -432,27 +449,28 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     } else if (warp >= 4 + C::EPI) {
         // ------------------------------------------------ convert
         if (!FEW) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
-        // The groups take the blocks in turn: a thread its weight row, and (few rows) two pieces
-        // of the tokens.
-        const int tid = (threadIdx.x - 128 - 32 * C::EPI) & 127;
-        const int quad = warp & 3, row = quad * 32 + lane;
-        const uint32_t mine = tmem + ((uint32_t)(quad * 32) << 16) + C::A_COL;
+        // A thread widens a weight row of its block, or half of one, and (few rows) two pieces of
+        // the tokens, or one.
+        const int tid = threadIdx.x - 128 - 32 * C::EPI, upper = tid >> 7;   // the second four warps
+        const int quad = warp & 3, row = quad * 32 + lane, half = SPLIT ? upper : 0;
+        const uint32_t mine = tmem + ((uint32_t)(quad * 32) << 16) + C::A_COL + half * 32;
         const uint32_t turns = total > first ? (uint32_t)((total - first - 1) / stride + 1) * (uint32_t)(kb1 - kb0) : 0u;
         ok = !expires(p, CONVERT) || __all_sync(0xffffffffu, bar_wait(&c.never, 0, abort_flag, p.expire_ns));
-        for (uint32_t it = (warp - 4 - C::EPI) >> 2; it < turns && ok; it += C::GROUPS) {
-            const uint32_t s = it % WS, a = it % NA;
+        for (uint32_t it = SPLIT ? 0 : upper; it < turns && ok; it += C::GROUPS) {
+            const uint32_t s = it % WS, a = it % NA, sx = it % XS;
             ok = __all_sync(0xffffffffu, bar_wait(&c.wfull[s], (it / WS) & 1u, abort_flag) &&
                                              bar_wait(&c.cempty[a], ((it / NA) & 1u) ^ 1u, abort_flag));
             if (!ok) break;
             tc_fence_after();
             const uint8_t *sw = smem + s * W_BYTES;
             const uint32_t at = mine + a * kBlockCols;
+            constexpr int UNITS = SPLIT ? 1 : 2;   // of 64 codes
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < UNITS; ++u) {
                 uint4 v[4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const uint4 *>(sw + piece_at(row, 4 * u + q));
-                if (u == 1) {   // the block has been read
+                for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const uint4 *>(sw + piece_at(row, 4 * (u + half) + q));
+                if (u == UNITS - 1) {   // the block has been read
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&c.wempty[s]);
                     __syncwarp();   // (here and below: the instructions that follow are .aligned)
@@ -465,18 +483,15 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                     tmem_st16(at + u * 32 + h * 16, o);
                 }
             }
-            const uint32_t sx = it % XS;
             ok = __all_sync(0xffffffffu, bar_wait(&c.xfull[sx], (it / XS) & 1u, abort_flag));
             if (!ok) break;
             if (FEW) {
-                const uint8_t *xs = smem + C::XRING + sx * C::X_BYTES;
-                uint8_t *xf = smem + C::XF + a * C::XF_BYTES;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int q = tid + j * 128, xr = q >> 3, xp = q & 7;
+                for (int j = 0; j < UNITS; ++j) {
+                    const int q = SPLIT ? tid : (tid & 127) + j * 128, xr = q >> 3, xp = q & 7;
+                    uint8_t *to = smem + C::XF + a * C::XF_BYTES + (xp >> 2) * NT * 128;
                     uint32_t h[8];
-                    widen16(*reinterpret_cast<const uint4 *>(xs + piece_at(xr, xp)), h);
-                    uint8_t *to = xf + (xp >> 2) * NT * 128;
+                    widen16(*reinterpret_cast<const uint4 *>(smem + C::XRING + sx * C::X_BYTES + piece_at(xr, xp)), h);
                     *reinterpret_cast<uint4 *>(to + piece_at(xr, (xp & 3) * 2)) = make_uint4(h[0], h[1], h[2], h[3]);
                     *reinterpret_cast<uint4 *>(to + piece_at(xr, (xp & 3) * 2 + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
                 }
@@ -547,17 +562,20 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                 __syncwarp();
             };
             if constexpr (SPLIT) {
-                // every MMA of this CTA has completed: the weights' ring holds the partial
-                // sums from here on, [token][weight row]
-                float *part_sum = reinterpret_cast<float *>(smem) + quarter * 32 + lane;
+                cluster_wait();
+                met = true;
+                // token l's sums go to CTA l % S, which finishes it: [token l / S][CTA][weight row]
+                uint32_t to = 0, at = (uint32_t)(quarter * 32 + lane) * 4 + rank * (M * 4);
 #pragma unroll 1
                 for (int i0 = 0; i0 < cnt; i0 += 16) {
                     uint32_t v[16];
                     __syncwarp();
                     if (ok) tmem_ld16_wait(d + i0, v);
 #pragma unroll
-                    for (int q = 0; q < 16; ++q)
-                        if (i0 + q < cnt) part_sum[(i0 + q) * M] = ok ? __uint_as_float(v[q]) : 0.f;
+                    for (int q = 0; q < 16; ++q) {
+                        if (i0 + q < cnt) st_cluster_u32(peer_addr(partial, to) + at, ok ? v[q] : 0x7fffffffu);
+                        if (++to == S) { to = 0; at += S * M * 4; }
+                    }
                 }
                 break;   // one tile per cluster
             } else if constexpr (FEW) {
@@ -722,53 +740,30 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     }
 
     if constexpr (SPLIT) {
-        cluster_sync_all();   // every CTA's partial sums are written
+        __syncwarp();
+        if (!met) cluster_wait();
+        cluster_sync_all();   // every CTA's partial sums have arrived
         if (first < total && warp >= 4 && warp < 4 + C::EPI) {
             // tokens rank, rank + S, ...: a thread to a channel (GATEUP: two tokens at a time)
-            // adds the CTAs' sums in the order of the blocks
+            // adds the CTAs' sums in the order of the blocks (a CTA that gave up sent NaN)
             const Tile tile = nth_tile(0, first);
-            const int tid = threadIdx.x - 128, chan = tid & (ROWS - 1), sub = tid / ROWS, n = tile.nt * ROWS + chan;
+            const int tid = threadIdx.x - 128, chan = tid & (ROWS - 1), n = tile.nt * ROWS + chan;
             constexpr int NW = M / ROWS;   // sums of a channel, and tokens at a time
             const long long wn = (long long)tile.e * p.N + min(n, p.N - 1);
             const float sw0 = __ldg(p.w_s[0] + wn), sw1 = MODE == GATEUP ? __ldg(p.w_s[1] + wn) : 0.f;
-            // (a CTA that gave up may still have had loads landing on its sums)
-            bool failed = false;
-            for (int q = 0; q < S; ++q) failed |= ld_cluster_u32(peer_addr(&c.abort_flag, q)) != 0u;
-            // (four tokens in flight where this thread has more than one)
-            auto add_up = [&](auto tokens) {
-                constexpr int U = decltype(tokens)::value, kPeers = U == 1 ? 8 : 2;   // (eight reads in flight)
-                const int step = S * NW;
-                for (int i0 = rank + sub * S; i0 < tile.cnt; i0 += U * step) {
-                    float v[U][NW];
+            for (int own = tid / ROWS, l = rank + own * S; l < tile.cnt; own += NW, l += NW * S) {
+                const float *from = reinterpret_cast<const float *>(partial) + own * S * M + chan;
+                float v[NW];
 #pragma unroll
-                    for (int u = 0; u < U; ++u)
+                for (int w = 0; w < NW; ++w) v[w] = 0.f;
+#pragma unroll 8
+                for (uint32_t q = 0; q < S; ++q)
 #pragma unroll
-                        for (int w = 0; w < NW; ++w) v[u][w] = 0.f;
-#pragma unroll kPeers
-                    for (int q = 0; q < S; ++q) {
-                        const uint32_t at = peer_addr(smem, q) + (uint32_t)chan * 4;
-#pragma unroll
-                        for (int u = 0; u < U; ++u) {
-                            const int l = min(i0 + u * step, tile.cnt - 1);
-#pragma unroll
-                            for (int w = 0; w < NW; ++w) v[u][w] += ld_cluster_f32(at + (uint32_t)(l * M + w * ROWS) * 4);
-                        }
-                    }
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const int l = i0 + u * step;
-                        if (l < tile.cnt && n < p.N) {
-                            const float bad = __uint_as_float(0x7fffffffu);
-                            store_out(p, tile.row0 + l, n,
-                                      finish<MODE>(p, failed ? bad : v[u][0], failed ? bad : v[u][NW - 1], c.sx[warp - 4][l], sw0, sw1));
-                        }
-                    }
-                }
-            };
-            if (tile.cnt <= S * NW) add_up(std::integral_constant<int, 1>());
-            else add_up(std::integral_constant<int, 4>());
+                    for (int w = 0; w < NW; ++w) v[w] += from[q * M + w * ROWS];
+                if (n < p.N) store_out(p, tile.row0 + l, n, finish<MODE>(p, v[0], v[NW - 1], c.sx[warp - 4][l], sw0, sw1));
+            }
         }
-        cluster_sync_all();   // no CTA leaves while a peer reads its shared memory
+        __syncthreads();
     } else {
         __syncthreads();
     }
@@ -846,11 +841,11 @@ template <int MODE, bool FEW, bool SPLIT>
 cudaError_t launch_variant(const CUtensorMap &x, const CUtensorMap &w0, const CUtensorMap &w1, const CUtensorMap &out, const Params &p,
                            long long tiles, int num_sms, cudaStream_t stream)
 {
-    using C = Cfg<FEW>;
+    using C = Cfg<FEW, SPLIT>;
     static PerDeviceFlag done;
     const int dev = current_device();
     auto *kern = product_kernel<MODE, FEW, SPLIT>;
-    constexpr size_t smem = smem_bytes<FEW>();
+    constexpr size_t smem = smem_bytes<FEW, SPLIT>();
     if (!done.done(dev)) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
@@ -928,7 +923,7 @@ template <int MODE> cudaError_t launch_few(const Params &args, cudaStream_t stre
     const int KB = ceil_div(p.K, BK);
     if (2 * tiles <= num_sms && KB >= 8) {
         const long long each = num_sms / tiles;
-        p.split = (int)(each < 8 ? each : 8);
+        p.split = (int)(each < kMaxSplit ? each : kMaxSplit);
     }
     CUtensorMap mx, mw0, mw1;
     if (!make_map(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.x_q, 0, p.x_rows, p.K, p.ldx, BK, p.perm_tok ? 1 : C::NT,
