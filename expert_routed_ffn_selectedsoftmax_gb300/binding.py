@@ -38,7 +38,8 @@ EXPORTS = ("moe_status_str", "moe_version", "moe_route", "moe_route_scored", "mo
            "moe_grouped_gemm_fp8b_expire_sums", "moe_gate_up_fp8b_expire_wait",
            "moe_gate_up_fp8b_expire_sums",
            "moe_dispatch", "moe_dispatch_backward", "moe_combine", "moe_combine_backward",
-           "moe_quant_i8", "moe_gemm_i8", "moe_grouped_gemm_i8", "moe_gate_up_i8", "moe_i8_workspace_size")
+           "moe_quant_i8", "moe_gemm_i8", "moe_grouped_gemm_i8", "moe_gate_up_i8", "moe_i8_workspace_size",
+           "moe_grouped_gemm_i8_expire_wait", "moe_gate_up_i8_expire_wait")
 
 _lib = None
 _debug_lib = None
@@ -166,7 +167,11 @@ def _declare(L):
     L.moe_gemm_i8.argtypes = [vp, vp, i, i, ll, vp, vp, i, vp, i, ll, vp, sz, vp, vp]
     L.moe_grouped_gemm_i8.argtypes = [vp, vp, i, i, ll, vp, vp, i, i, vp, vp, i, vp, i, ll, vp, sz, vp, vp]
     L.moe_gate_up_i8.argtypes = [vp, vp, i, i, ll, vp, vp, vp, vp, i, i, vp, vp, i, vp, i, ll, vp, sz, vp, vp]
-    for call in (L.moe_dispatch, L.moe_dispatch_backward, L.moe_combine, L.moe_combine_backward, L.moe_quant_i8,
+    L.moe_grouped_gemm_i8_expire_wait.argtypes = [vp, vp, i, i, ll, vp, vp, i, i, vp, vp, i, vp, i, ll, vp, sz, vp, i,
+                                                  ctypes.c_uint32, vp]
+    L.moe_gate_up_i8_expire_wait.argtypes = [vp, vp, i, i, ll, vp, vp, vp, vp, i, i, vp, vp, i, vp, i, ll, vp, sz, vp, i,
+                                             ctypes.c_uint32, vp]
+    for call in (L.moe_grouped_gemm_i8_expire_wait, L.moe_gate_up_i8_expire_wait, L.moe_dispatch, L.moe_dispatch_backward, L.moe_combine, L.moe_combine_backward, L.moe_quant_i8,
                  L.moe_gemm_i8, L.moe_grouped_gemm_i8, L.moe_gate_up_i8):
         call.restype = i
     L.moe_i8_workspace_size.argtypes = [i, i]

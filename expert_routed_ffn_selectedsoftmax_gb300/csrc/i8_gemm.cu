@@ -12,6 +12,46 @@ namespace i8 {
 
 constexpr int kFewRows = 32;   // up to here no call takes the tiled kernel, and none needs a workspace
 
+// The CUDA-core kernel: one or two rows, or up to 32 with at most 8 a group and 6e7
+// products.  It starts without barriers, tensor maps and TMEM, but a row costs it a pass of
+// dot products where the tensor cores take 32 at once.  us a call (here / few rows):
+// 2048 x 5632 of 1 token 4.4 / 7.1, 4: 6.6 / 7.3, 8: 9.1 / 7.6; 1024 x 1024 of 8 2.5 / 3.7;
+// 8192 x 8192 of 1 14.6 / 17.8, 4: 19.1 / 18.1; 8 rows over 16 experts of 2816 x 2048
+// 12.6 / 13.1, 64 over 64 of 512 x 1024 10.0 / 8.3; gate/up of 16 tokens x 2 over 64
+// experts of 1024 x 512 8.5 / 10.2, of 64 rows 14.2 / 10.9.
+template <int MODE> bool vector_fits(const Params &p, long long experts)
+{
+    if (p.K >= 131072) return false;   // (its sums are 32-bit whole numbers)
+    if (p.rows <= 2) return true;
+    return p.rows <= kFewRows && p.rows <= 8 * experts &&
+           (double)p.rows * p.N * p.K * (MODE == GATEUP ? 2 : 1) <= 6e7;
+}
+
+// Few rows or tiled, by what each is expected to take (us).  Blocks of 128 columns cost
+// the few-rows kernel 0.40 us where every tile has an SM, 0.62 where two share one, and 0.33
+// an SM beyond; the tiled kernel 0.41, on an eighth of the tiles or fewer, but it starts
+// later (its rows are widened first, at 3 bytes a code) and each tile's end shows.  The
+// groups' sizes are known on the device only: their last tiles are taken as half full.
+// Measured (few rows / tiled): 4096 x 4096 of 128 rows 16.4 / 20.0, 192: 23.3 / 19.8;
+// 2048 x 5632 of 192 14.2 / 14.6, 256: 19.4 / 15.0; 1024 x 1024 of 1024 9.0 / 11.8;
+// 8192 x 1024 of 512 28.6 / 31.1, 1024: 41.8 / 35.7; 64 experts of 2048 x 1024, rows per
+// expert 32: 35.3 / 42.3, 64: 51.9 / 45.2; 16 of 2816 x 2048, 24: 25.6 / 30.4, 64:
+// 37.1 / 33.1; gate/up, 64 of 1024 x 512, 32: 23.7 / 30.1, 64: 34.5 / 31.7.
+template <int MODE> bool few_rows_fit(const Params &p, double experts)
+{
+    if (p.rows <= kFewRows) return true;
+    const double sms = device_sm_count(), blocks = ceil_div(p.K, 128), columns = ceil_div(p.N, MODE == GATEUP ? 64 : 128);
+    const auto tiles = [&](int tokens) {
+        if (experts == 1) return ceil_div(p.rows, tokens) * columns;
+        const double each = (double)p.rows / tokens + experts / 2;
+        return (each > experts ? each : experts) * columns;
+    };
+    const double f = tiles(32) / sms, t = tiles(128) / sms;
+    const double few = 3.5 + blocks * (f <= 1 ? 0.40 : f * 0.33 > 0.62 ? f * 0.33 : 0.62);
+    const double tiled = 7 + (double)p.rows * p.K * 6e-7 + (t > 1 ? t : 1) * (blocks * 0.41 + 0.8);
+    return few <= tiled;
+}
+
 template <int MODE> cudaError_t launch_product(const Params &p, void *workspace, cudaStream_t stream)
 {
 #ifdef I8_FORCE
@@ -20,9 +60,9 @@ template <int MODE> cudaError_t launch_product(const Params &p, void *workspace,
     if (f && *f == 'f') return launch_few<MODE>(p, stream);
     if (f && *f == 't' && p.rows > kFewRows) return launch_tiled<MODE>(p, workspace, stream);
 #endif
-    const long long experts = p.E < p.rows ? p.E : p.rows;
-    if (p.rows <= 2 * experts && p.rows <= 64) return launch_vector<MODE>(p, stream);
-    if (p.rows <= kFewRows || p.rows <= 16 * experts) return launch_few<MODE>(p, stream);
+    const int experts = p.E < p.rows ? p.E : p.rows;
+    if (p.expire_ns == 0 && vector_fits<MODE>(p, experts)) return launch_vector<MODE>(p, stream);   // (it has no waits)
+    if (few_rows_fit<MODE>(p, experts)) return launch_few<MODE>(p, stream);
     return launch_tiled<MODE>(p, workspace, stream);
 }
 
@@ -84,6 +124,12 @@ moe_status product(const void *x_q, const float *x_s, int x_rows, int K, long lo
 using namespace moe;
 using namespace moe::i8;
 
+namespace {
+
+bool hook_ok(int role, uint32_t wait_ns) { return role >= LOADS && role <= SUMS && wait_ns > 0 && wait_ns <= 100000000u; }
+
+}  // namespace
+
 extern "C" {
 
 size_t moe_i8_workspace_size(int rows, int K)
@@ -101,6 +147,17 @@ moe_status moe_grouped_gemm_i8(const void *x_q, const float *x_s, int x_rows, in
                             workspace, ws_bytes, status, 0, 0, stream);
 }
 
+moe_status moe_grouped_gemm_i8_expire_wait(const void *x_q, const float *x_s, int x_rows, int K, long long ldx,
+                                           const void *w_q, const float *w_s, int E, int N, const int32_t *offsets,
+                                           const int32_t *perm_tok, int rows, void *out, moe_dtype out_dt, long long ldo,
+                                           void *workspace, size_t ws_bytes, uint32_t *status, int role, uint32_t wait_ns,
+                                           moe_stream stream)
+{
+    if (!hook_ok(role, wait_ns)) return MOE_ERR_INVALID_ARG;
+    return product<PRODUCT>(x_q, x_s, x_rows, K, ldx, w_q, w_s, w_q, w_s, E, N, offsets, perm_tok, rows, out, out_dt, ldo,
+                            workspace, ws_bytes, status, role, wait_ns, stream);
+}
+
 moe_status moe_gemm_i8(const void *x_q, const float *x_s, int T, int K, long long ldx, const void *w_q, const float *w_s,
                        int N, void *out, moe_dtype out_dt, long long ldo, void *workspace, size_t ws_bytes,
                        uint32_t *status, moe_stream stream)
@@ -116,6 +173,17 @@ moe_status moe_gate_up_i8(const void *x_q, const float *x_s, int x_rows, int d, 
 {
     return product<GATEUP>(x_q, x_s, x_rows, d, ldx, wg_q, wg_s, wu_q, wu_s, E, F, offsets, perm_tok, rows, h, h_dt, ldh,
                            workspace, ws_bytes, status, 0, 0, stream);
+}
+
+moe_status moe_gate_up_i8_expire_wait(const void *x_q, const float *x_s, int x_rows, int d, long long ldx, const void *wg_q,
+                                      const float *wg_s, const void *wu_q, const float *wu_s, int E, int F,
+                                      const int32_t *offsets, const int32_t *perm_tok, int rows, void *h, moe_dtype h_dt,
+                                      long long ldh, void *workspace, size_t ws_bytes, uint32_t *status, int role,
+                                      uint32_t wait_ns, moe_stream stream)
+{
+    if (!hook_ok(role, wait_ns)) return MOE_ERR_INVALID_ARG;
+    return product<GATEUP>(x_q, x_s, x_rows, d, ldx, wg_q, wg_s, wu_q, wu_s, E, F, offsets, perm_tok, rows, h, h_dt, ldh,
+                           workspace, ws_bytes, status, role, wait_ns, stream);
 }
 
 }  // extern "C"

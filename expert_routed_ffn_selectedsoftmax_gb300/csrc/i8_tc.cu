@@ -49,6 +49,7 @@ constexpr int BK = 128;                      // columns of a block of the reduct
 constexpr int W_BYTES = M * BK;
 constexpr int kBlockCols = BK / 2;           // TMEM columns of a block's weights as fp16
 constexpr int kStaging = 2048;
+constexpr int kConvWarps = 8;                // two groups of four, which take the blocks in turn
 constexpr int kMaxSplit = 8;                 // CTAs of a cluster
 constexpr size_t kPartial = (size_t)(32 + kMaxSplit) * M * 4;   // whole turns of 32 tokens over the CTAs
 
@@ -67,11 +68,7 @@ template <bool FEW, bool SPLIT = false> struct Cfg {
     static constexpr int TMEM_COLS = FEW ? 256 : 512;
     static constexpr int MMAS = FEW ? 1 : 2;                       // multiplying warps, each with its share of the tokens
     static constexpr int EPI = FEW ? 4 : 16;                       // output warps
-    // Converting warps are eight: four of them a block in turn, a thread a weight row; or
-    // (split) all of them a block, a thread half a row, as the first block is what a short
-    // reduction waits for (one token, 2048 x 5632: 8.5 -> 7.5 us; 64 tokens, whole: 10.4 -> 12.3).
-    static constexpr int GROUPS = SPLIT ? 1 : 2, PER_BLOCK = 8 / GROUPS;
-    static constexpr int THREADS = 128 + 32 * (EPI + 8);
+    static constexpr int THREADS = 128 + 32 * (EPI + kConvWarps);
     static constexpr size_t XRING = (size_t)WS * W_BYTES;
     static constexpr size_t XF = XRING + (size_t)XS * X_BYTES;
     static constexpr size_t STAGING = XF + (size_t)NA * XF_BYTES;
@@ -304,9 +301,9 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     const int E = p.E;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < WS; ++s) { mbar_init(&c.wfull[s], 1); mbar_init(&c.wempty[s], C::PER_BLOCK); }
-        for (int s = 0; s < XS; ++s) { mbar_init(&c.xfull[s], 1); mbar_init(&c.xempty[s], C::PER_BLOCK); }
-        for (int a = 0; a < NA; ++a) { mbar_init(&c.cfull[a], C::PER_BLOCK); mbar_init(&c.cempty[a], C::MMAS); }
+        for (int s = 0; s < WS; ++s) { mbar_init(&c.wfull[s], 1); mbar_init(&c.wempty[s], 4); }
+        for (int s = 0; s < XS; ++s) { mbar_init(&c.xfull[s], 1); mbar_init(&c.xempty[s], 4); }
+        for (int a = 0; a < NA; ++a) { mbar_init(&c.cfull[a], 4); mbar_init(&c.cempty[a], C::MMAS); }
         for (int d = 0; d < 2; ++d) { mbar_init(&c.dfull[d], C::MMAS); mbar_init(&c.dempty[d], C::EPI); }
         for (int w = 0; w < 2; ++w) mbar_init(&c.drain[w], 1);
         mbar_init(&c.never, 1);
@@ -449,14 +446,13 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     } else if (warp >= 4 + C::EPI) {
         // ------------------------------------------------ convert
         if (!FEW) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
-        // A thread widens a weight row of its block, or half of one, and (few rows) two pieces of
-        // the tokens, or one.
-        const int tid = threadIdx.x - 128 - 32 * C::EPI, upper = tid >> 7;   // the second four warps
-        const int quad = warp & 3, row = quad * 32 + lane, half = SPLIT ? upper : 0;
-        const uint32_t mine = tmem + ((uint32_t)(quad * 32) << 16) + C::A_COL + half * 32;
+        // A group takes every second block: a thread a weight row, and (few rows) two pieces of
+        // the tokens.
+        const int tid = (threadIdx.x - 128 - 32 * C::EPI) & 127, quad = warp & 3, row = quad * 32 + lane;
+        const uint32_t mine = tmem + ((uint32_t)(quad * 32) << 16) + C::A_COL;
         const uint32_t turns = total > first ? (uint32_t)((total - first - 1) / stride + 1) * (uint32_t)(kb1 - kb0) : 0u;
         ok = !expires(p, CONVERT) || __all_sync(0xffffffffu, bar_wait(&c.never, 0, abort_flag, p.expire_ns));
-        for (uint32_t it = SPLIT ? 0 : upper; it < turns && ok; it += C::GROUPS) {
+        for (uint32_t it = (warp - 4 - C::EPI) >> 2; it < turns && ok; it += 2) {
             const uint32_t s = it % WS, a = it % NA, sx = it % XS;
             ok = __all_sync(0xffffffffu, bar_wait(&c.wfull[s], (it / WS) & 1u, abort_flag) &&
                                              bar_wait(&c.cempty[a], ((it / NA) & 1u) ^ 1u, abort_flag));
@@ -464,13 +460,12 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             tc_fence_after();
             const uint8_t *sw = smem + s * W_BYTES;
             const uint32_t at = mine + a * kBlockCols;
-            constexpr int UNITS = SPLIT ? 1 : 2;   // of 64 codes
 #pragma unroll
-            for (int u = 0; u < UNITS; ++u) {
+            for (int u = 0; u < 2; ++u) {   // 64 codes
                 uint4 v[4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const uint4 *>(sw + piece_at(row, 4 * (u + half) + q));
-                if (u == UNITS - 1) {   // the block has been read
+                for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const uint4 *>(sw + piece_at(row, 4 * u + q));
+                if (u == 1) {   // the block has been read
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&c.wempty[s]);
                     __syncwarp();   // (here and below: the instructions that follow are .aligned)
@@ -487,8 +482,8 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             if (!ok) break;
             if (FEW) {
 #pragma unroll
-                for (int j = 0; j < UNITS; ++j) {
-                    const int q = SPLIT ? tid : (tid & 127) + j * 128, xr = q >> 3, xp = q & 7;
+                for (int j = 0; j < 2; ++j) {
+                    const int q = tid + j * 128, xr = q >> 3, xp = q & 7;
                     uint8_t *to = smem + C::XF + a * C::XF_BYTES + (xp >> 2) * NT * 128;
                     uint32_t h[8];
                     widen16(*reinterpret_cast<const uint4 *>(smem + C::XRING + sx * C::X_BYTES + piece_at(xr, xp)), h);

@@ -650,8 +650,8 @@ MOE_API moe_status moe_quant_i8(const void *x, moe_dtype x_dt, int rows, int col
 
 /*
  * Bytes of device workspace that the products of `rows` rows of K columns need, 256-byte
- * aligned, not shared by calls that can overlap (0: none, and NULL is taken; also 0 on
- * invalid sizes).
+ * aligned, not shared by calls that can overlap.  0 for up to 32 rows (NULL is taken), and
+ * on invalid sizes.
  */
 MOE_API size_t moe_i8_workspace_size(int rows, int K);
 
@@ -766,6 +766,24 @@ MOE_API moe_status moe_gate_up_fp8b_expire_sums(
     const float *wg_s, const void *wu_q, const float *wu_s, int E, int F, const int32_t *offsets,
     const int32_t *perm_tok, int rows, void *h_q, float *h_s, void *workspace, size_t ws_bytes,
     uint32_t *status, uint32_t wait_ns, moe_stream stream);
+
+/*
+ * moe_grouped_gemm_i8_expire_wait, moe_gate_up_i8_expire_wait -- the same hook for the
+ * int8 products on the tensor cores (whichever of their kernels the sizes choose):
+ * the first wait of one of its roles, 0: loads, 1: conversion, 2: sums and output, is limited
+ * to `wait_ns` (1 ns .. 100 ms).  Every row of every group becomes NaN and `status`
+ * reports MOE_ERR_TIMEOUT.  Not for production use.
+ */
+MOE_API moe_status moe_grouped_gemm_i8_expire_wait(
+    const void *x_q, const float *x_s, int x_rows, int K, long long ldx, const void *w_q,
+    const float *w_s, int E, int N, const int32_t *offsets, const int32_t *perm_tok, int rows,
+    void *out, moe_dtype out_dt, long long ldo, void *workspace, size_t ws_bytes, uint32_t *status,
+    int role, uint32_t wait_ns, moe_stream stream);
+MOE_API moe_status moe_gate_up_i8_expire_wait(
+    const void *x_q, const float *x_s, int x_rows, int d, long long ldx, const void *wg_q,
+    const float *wg_s, const void *wu_q, const float *wu_s, int E, int F, const int32_t *offsets,
+    const int32_t *perm_tok, int rows, void *h, moe_dtype h_dt, long long ldh, void *workspace,
+    size_t ws_bytes, uint32_t *status, int role, uint32_t wait_ns, moe_stream stream);
 
 /*
  * moe_check_noalloc -- moe_check for moe_forward_noalloc: wait for `stream`,

@@ -437,6 +437,41 @@ def test_an_expert_layer(moe, T, d, E, k, F):
         assert torch.equal(held, layer(*args)[0])
 
 
+@pytest.mark.parametrize("role", [0, 1, 2])
+@pytest.mark.parametrize("gate_up", [False, True])
+@pytest.mark.parametrize("T,K,N,E", [(20, 2048, 300, 1), (300, 256, 200, 6), (3000, 2048, 520, 3)])   # split, few rows, tiled
+def test_a_wait_that_expires(moe, T, K, N, E, gate_up, role):
+    """The first wait of the loads, the converters or the sums gives up after 1 ms in every
+    CTA (nothing arrives on its barrier): NaN rows, the status word, rows outside the groups as
+    they were, and the next call right."""
+    import ctypes
+    L = moe.load_library()
+    (xq, xs), (wq, ws), (uq, us) = codes(T, K), codes(E, N, K, seed=1), codes(E, N, K, seed=2)
+    cut = [T * e // (E + 1) for e in range(E + 1)]         # (rows behind the last group)
+    off = torch.tensor(cut, dtype=torch.int32, device=DEV)
+    out = torch.full((T, N), 7.0, device=DEV)
+    scratch = torch.empty(max(moe.moe_i8_workspace_size(T, K), 256), dtype=torch.uint8, device=DEV)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    p = lambda t: ctypes.c_void_p(t.data_ptr())
+    tail = (E, N, p(off), None, T, p(out), 0, N, p(scratch), scratch.numel(), p(st), role, 1_000_000,
+            ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    if gate_up:
+        assert L.moe_gate_up_i8_expire_wait(p(xq), p(xs), T, K, K, p(wq), p(ws), p(uq), p(us), *tail) == 0
+    else:
+        assert L.moe_grouped_gemm_i8_expire_wait(p(xq), p(xs), T, K, K, p(wq), p(ws), *tail) == 0
+    torch.cuda.synchronize()
+    assert bool(out[:cut[-1]].isnan().all()) and bool((out[cut[-1]:] == 7).all()) and int(st) & 1
+    with pytest.raises(moe.MoeError):
+        moe.moe_check(st)
+    st.zero_()
+    if gate_up:
+        moe.moe_gate_up_i8(xq, xs, wq, ws, uq, us, offsets=off, h=out, workspace=scratch, status=st)
+    else:
+        moe.moe_grouped_gemm_i8(xq, xs, wq, ws, off, out=out, workspace=scratch, status=st)
+    check_grouped(out, xq, xs, [(wq, ws), (uq, us)] if gate_up else [(wq, ws)], off, None)
+    assert bool((out[cut[-1]:] == 7).all()) and moe.moe_check(st) == 0
+
+
 def test_two_calls_at_once(moe):
     """Two streams with calls of their own workspaces; one workspace shared by calls in order."""
     T, K, N = 700, 512, 640

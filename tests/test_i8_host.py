@@ -47,8 +47,17 @@ def test_product_arguments(lib):
     assert grouped(E=257) == U and gate_up(E=257) == U
     assert grouped(rows=2 ** 30 + 1, xr=2 ** 30 + 1) == U
     assert grouped(rows=0, xr=0, xq=None, out=None) == OK and gate_up(rows=0, xr=0, xq=None, out=None) == OK
-    for rows, K in ((-1, 256), (8, 250), (8, 0)):
+    # scratch of widened rows, 2 bytes a code, to 256 bytes; none up to 32 rows
+    for rows, K in ((-1, 256), (80, 250), (80, 0), (32, 256)):
         assert lib.moe_i8_workspace_size(rows, K) == 0
+    assert lib.moe_i8_workspace_size(33, 48) == 3328
+    for call in (grouped, gate_up):
+        for bad in (dict(rows=33, xr=33, ws_=None), dict(rows=33, xr=33, ws_=vp(0x10080))):
+            assert call(**bad) == I, bad
+        assert call(rows=33, xr=33, wsb=33 * 512 - 1) == W
+    for role, ns in ((-1, 1000), (3, 1000), (0, 0), (1, 100_000_001)):
+        assert lib.moe_grouped_gemm_i8_expire_wait(*base.values(), role, ns, None) == I
+        assert lib.moe_gate_up_i8_expire_wait(*gu.values(), role, ns, None) == I
     dense = dict(xq=FAKE, xs=FAKE, T=4, K=256, ldx=256, wq=FAKE, ws=FAKE, N=64, out=FAKE, odt=BF16, ldo=64, ws_=FAKE,
                  wsb=1 << 20, st=None)
     gemm = lambda **kw: lib.moe_gemm_i8(*dict(dense, **kw).values(), None)
