@@ -9,8 +9,7 @@
 //
 // All of them go by tokens: a token's row is read (or written) once and its k
 // grouped rows are found through inv, so each byte moves once and nothing needs an
-// atomic.  A thread holds 8 neighbouring columns (16 bytes of bf16) of its token and
-// asks for the k rows' at once.  What bounds them is memory.  Sums run over the
+// atomic.  A thread holds 8 columns of its token and asks for the k rows' at once.  What bounds them is memory.  Sums run over the
 // slots in order, in fp32, and are rounded once.
 #include <type_traits>
 
@@ -23,32 +22,54 @@ namespace rows {
 constexpr int kThreads = 256;
 constexpr int V = 8;            // columns of a thread's chunk
 
-// V columns, or one (rows that do not lie on 16-byte boundaries).
-template <typename T, int N> struct Chunk;
-template <> struct Chunk<float, 1> {
-    uint32_t a;
-    __device__ __forceinline__ void load(const float *p) { a = __ldg(reinterpret_cast<const uint32_t *>(p)); }
-    __device__ __forceinline__ void store(float *p) const { *reinterpret_cast<uint32_t *>(p) = a; }
-    __device__ __forceinline__ void zero() { a = 0u; }
-    __device__ __forceinline__ float get(int) const { return __uint_as_float(a); }
-    __device__ __forceinline__ void set(const float (&v)[1]) { a = __float_as_uint(v[0]); }
+// V columns of a thread.  VEC: neighbours, 16 bytes a load (or two).  Else, where rows do not
+// lie on 16-byte boundaries, `step` apart, an element a load: the threads of a row still
+// read neighbouring elements, and V loads are in flight.
+template <typename T, bool VEC> struct Chunk;
+template <typename T> struct Bits;
+template <> struct Bits<float> {
+    using Raw = uint32_t;
+    __device__ static __forceinline__ float get(uint32_t r) { return __uint_as_float(r); }
+    __device__ static __forceinline__ uint32_t put(float v) { return __float_as_uint(v); }
 };
-template <> struct Chunk<__nv_bfloat16, 1> {
-    uint16_t a;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = __ldg(reinterpret_cast<const uint16_t *>(p)); }
-    __device__ __forceinline__ void store(__nv_bfloat16 *p) const { *reinterpret_cast<uint16_t *>(p) = a; }
-    __device__ __forceinline__ void zero() { a = 0; }
-    __device__ __forceinline__ float get(int) const { return __uint_as_float((uint32_t)a << 16); }
-    __device__ __forceinline__ void set(const float (&v)[1]) { a = __bfloat16_as_ushort(__float2bfloat16_rn(v[0])); }
+template <> struct Bits<__nv_bfloat16> {
+    using Raw = uint16_t;
+    __device__ static __forceinline__ float get(uint16_t r) { return __uint_as_float((uint32_t)r << 16); }
+    __device__ static __forceinline__ uint16_t put(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 };
-template <> struct Chunk<float, V> {
+template <typename T> struct Chunk<T, false> {
+    typename Bits<T>::Raw a[V];
+    __device__ __forceinline__ void load(const T *p, int step, int left)
+    {
+#pragma unroll
+        for (int i = 0; i < V; ++i) a[i] = i * step < left ? __ldg(reinterpret_cast<const typename Bits<T>::Raw *>(p) + i * step) : 0;
+    }
+    __device__ __forceinline__ void store(T *p, int step, int left) const
+    {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i * step < left) reinterpret_cast<typename Bits<T>::Raw *>(p)[i * step] = a[i];
+    }
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < V; ++i) a[i] = 0;
+    }
+    __device__ __forceinline__ float get(int i) const { return Bits<T>::get(a[i]); }
+    __device__ __forceinline__ void set(const float (&v)[V])
+    {
+#pragma unroll
+        for (int i = 0; i < V; ++i) a[i] = Bits<T>::put(v[i]);
+    }
+};
+template <> struct Chunk<float, true> {
     uint4 a, b;
-    __device__ __forceinline__ void load(const float *p)
+    __device__ __forceinline__ void load(const float *p, int, int)
     {
         a = __ldg(reinterpret_cast<const uint4 *>(p));
         b = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
     }
-    __device__ __forceinline__ void store(float *p) const
+    __device__ __forceinline__ void store(float *p, int, int) const
     {
         reinterpret_cast<uint4 *>(p)[0] = a;
         reinterpret_cast<uint4 *>(p)[1] = b;
@@ -65,10 +86,10 @@ template <> struct Chunk<float, V> {
         b = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
     }
 };
-template <> struct Chunk<__nv_bfloat16, V> {
+template <> struct Chunk<__nv_bfloat16, true> {
     uint4 a;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = __ldg(reinterpret_cast<const uint4 *>(p)); }
-    __device__ __forceinline__ void store(__nv_bfloat16 *p) const { *reinterpret_cast<uint4 *>(p) = a; }
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p, int, int) { a = __ldg(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void store(__nv_bfloat16 *p, int, int) const { *reinterpret_cast<uint4 *>(p) = a; }
     __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
     __device__ __forceinline__ float get(int i) const
     {
@@ -96,59 +117,61 @@ struct Args {
     float *dw;
     long long ldx, ldg, ldo;  // elements from row to row
     int T, k, rows, d;
-    int chunks, col_blocks;   // chunks of a row; CTAs along it
+    int col_blocks;           // CTAs along a row
     int lanes_log2;           // threads of a CTA along a row
 };
 
-// This thread's token and chunk; a CTA holds kThreads >> lanes_log2 tokens, and
-// a row's chunks are spread over col_blocks CTAs (a thread takes one chunk, so
-// that a few tokens still fill the SMs).
-__device__ __forceinline__ bool place(const Args &a, long long &t, int &chunk)
+// This thread's token and first column; a CTA holds kThreads >> lanes_log2 tokens, and a
+// row's chunks are spread over col_blocks CTAs (a thread takes one chunk, so that a few
+// tokens still fill the SMs).  Without VEC its columns lie 1 << lanes_log2 apart.
+template <bool VEC> __device__ __forceinline__ bool place(const Args &a, long long &t, int &col)
 {
-    const int lanes = 1 << a.lanes_log2;
+    const int lanes = 1 << a.lanes_log2, lane = threadIdx.x & (lanes - 1);
     const long long tb = blockIdx.x / a.col_blocks;
     t = tb * (kThreads >> a.lanes_log2) + (threadIdx.x >> a.lanes_log2);
-    chunk = (int)(blockIdx.x - tb * a.col_blocks) * lanes + (threadIdx.x & (lanes - 1));
-    return t < a.T && chunk < a.chunks;
+    col = (int)(blockIdx.x - tb * a.col_blocks) * (lanes * V) + (VEC ? lane * V : lane);
+    return t < a.T && col < a.d;
 }
 
-template <typename XT, int N>
+template <typename XT, bool VEC>
 __global__ void __launch_bounds__(kThreads)
 scatter_rows_kernel(const Args a)
 {
     pdl_enter();
     long long t;
-    int chunk;
-    if (!place(a, t, chunk)) return;
-    Chunk<XT, N> c;
-    c.load(static_cast<const XT *>(a.x) + t * a.ldx + (long long)chunk * N);
-    XT *out = static_cast<XT *>(a.out) + (long long)chunk * N;
+    int col;
+    if (!place<VEC>(a, t, col)) return;
+    const int step = 1 << a.lanes_log2, left = a.d - col;
+    Chunk<XT, VEC> c;
+    c.load(static_cast<const XT *>(a.x) + t * a.ldx + col, step, left);
+    XT *out = static_cast<XT *>(a.out) + col;
     const int32_t *inv = a.inv + t * a.k;
 #pragma unroll 4
     for (int j = 0; j < a.k; ++j) {
         const int r = __ldg(inv + j);
-        if (r >= 0 && r < a.rows) c.store(out + r * a.ldo);
+        if (r >= 0 && r < a.rows) c.store(out + r * a.ldo, step, left);
     }
 }
 
 // WEIGHTED: combine; else dispatch's backward pass.
-template <typename XT, typename OT, int N, bool WEIGHTED>
+template <typename XT, typename OT, bool VEC, bool WEIGHTED>
 __global__ void __launch_bounds__(kThreads)
 gather_sum_kernel(const Args a)
 {
     pdl_enter();
     long long t;
-    int chunk;
-    if (!place(a, t, chunk)) return;
-    const XT *x = static_cast<const XT *>(a.x) + (long long)chunk * N;
+    int col;
+    if (!place<VEC>(a, t, col)) return;
+    const int step = 1 << a.lanes_log2, left = a.d - col;
+    const XT *x = static_cast<const XT *>(a.x) + col;
     const int32_t *inv = a.inv + t * a.k;
     const float *w = a.topk_w + t * a.k;
-    float sum[N];
+    float sum[V];
 #pragma unroll
-    for (int i = 0; i < N; ++i) sum[i] = 0.f;
-    constexpr int U = 4;   // rows asked for at once
+    for (int i = 0; i < V; ++i) sum[i] = 0.f;
+    constexpr int U = VEC ? 4 : 2;   // rows asked for at once
     for (int j0 = 0; j0 < a.k; j0 += U) {
-        Chunk<XT, N> c[U];
+        Chunk<XT, VEC> c[U];
         float f[U];
         bool in[U];
 #pragma unroll
@@ -157,7 +180,7 @@ gather_sum_kernel(const Args a)
             in[u] = r >= 0 && r < a.rows;
             f[u] = 1.f;
             if (in[u]) {
-                c[u].load(x + r * a.ldx);
+                c[u].load(x + r * a.ldx, step, left);
                 if (WEIGHTED) f[u] = __ldg(w + j0 + u);
             }
         }
@@ -165,18 +188,18 @@ gather_sum_kernel(const Args a)
         for (int u = 0; u < U; ++u) {
             if (!in[u]) continue;   // (a slot without a row adds nothing, whatever its weight)
 #pragma unroll
-            for (int i = 0; i < N; ++i) sum[i] = WEIGHTED ? fmaf(f[u], c[u].get(i), sum[i]) : sum[i] + c[u].get(i);
+            for (int i = 0; i < V; ++i) sum[i] = WEIGHTED ? fmaf(f[u], c[u].get(i), sum[i]) : sum[i] + c[u].get(i);
         }
     }
-    Chunk<OT, N> o;
+    Chunk<OT, VEC> o;
     o.set(sum);
-    o.store(static_cast<OT *>(a.out) + t * a.ldo + (long long)chunk * N);
+    o.store(static_cast<OT *>(a.out) + t * a.ldo + col, step, left);
 }
 
 // Combine's backward pass: a token to a group of `G` threads (a warp, or the CTA),
 // which walk its chunks; each thread sums its part of every slot's product, and the
 // parts meet in a fixed order (shuffles, then the warps in order).
-template <typename XT, typename GT, int N, int G>
+template <typename XT, typename GT, bool VEC, int G>
 __global__ void __launch_bounds__(kThreads)
 combine_backward_kernel(const Args a)
 {
@@ -199,36 +222,46 @@ combine_backward_kernel(const Args a)
             if (r[j] >= a.rows) r[j] = -1;
             w[j] = j < a.k ? __ldg(a.topk_w + t * a.k + j) : 0.f;
         }
-        for (int chunk = lane; chunk < a.chunks; chunk += G) {
-            const long long at = (long long)chunk * N;
-            Chunk<GT, N> c;
-            c.load(g + at);
+        constexpr int C = VEC ? 2 : 1;   // chunks in flight
+        for (int base = 0; base < a.d; base += C * G * V) {
+            Chunk<GT, VEC> c[C];
+            int col[C];
+#pragma unroll
+            for (int q = 0; q < C; ++q) {
+                col[q] = base + q * G * V + (VEC ? lane * V : lane);
+                c[q].zero();
+                if (col[q] < a.d) c[q].load(g + col[q], G, a.d - col[q]);
+            }
             // (two rows at a time: their loads stand ahead of the stores)
 #pragma unroll
             for (int j0 = 0; j0 < kMaxTopK; j0 += 2) {
                 if (j0 >= a.k) break;
-                Chunk<XT, N> v[2];
+                Chunk<XT, VEC> v[C][2];
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    v[u].zero();
-                    if (r[j0 + u] >= 0 && a.dw) v[u].load(y + r[j0 + u] * a.ldx + at);
-                }
+                for (int q = 0; q < C; ++q)
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int j = j0 + u;
-                    if (r[j] < 0) continue;
-                    float o[N];
-#pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        dot[j] = fmaf(c.get(i), v[u].get(i), dot[j]);
-                        o[i] = w[j] * c.get(i);
+                    for (int u = 0; u < 2; ++u) {
+                        v[q][u].zero();
+                        if (r[j0 + u] >= 0 && a.dw && col[q] < a.d) v[q][u].load(y + r[j0 + u] * a.ldx + col[q], G, a.d - col[q]);
                     }
-                    if (dy) {
-                        Chunk<XT, N> s;
-                        s.set(o);
-                        s.store(dy + r[j] * a.ldo + at);
+#pragma unroll
+                for (int q = 0; q < C; ++q)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int j = j0 + u;
+                        if (r[j] < 0 || col[q] >= a.d) continue;
+                        float o[V];
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            dot[j] = fmaf(c[q].get(i), v[q][u].get(i), dot[j]);
+                            o[i] = w[j] * c[q].get(i);
+                        }
+                        if (dy) {
+                            Chunk<XT, VEC> s;
+                            s.set(o);
+                            s.store(dy + r[j] * a.ldo + col[q], G, a.d - col[q]);
+                        }
                     }
-                }
             }
         }
     }
@@ -277,12 +310,12 @@ bool matrix_ok(const void *p, moe_dtype dt, long long ld, int d, bool may_be_emp
 }
 
 // grid of a kernel whose threads take a chunk each
-bool lay_out(Args &a, int n, dim3 *grid)
+bool lay_out(Args &a, dim3 *grid)
 {
-    a.chunks = a.d / n;
+    const int chunks = ceil_div(a.d, V);
     a.lanes_log2 = 5;
-    while (a.lanes_log2 < 8 && (1 << a.lanes_log2) < a.chunks) ++a.lanes_log2;
-    a.col_blocks = ceil_div(a.chunks, 1 << a.lanes_log2);
+    while (a.lanes_log2 < 8 && (1 << a.lanes_log2) < chunks) ++a.lanes_log2;
+    a.col_blocks = ceil_div(chunks, 1 << a.lanes_log2);
     const int per = kThreads >> a.lanes_log2;
     const long long ctas = ((long long)a.T + per - 1) / per * a.col_blocks;
     *grid = dim3((unsigned)ctas);
@@ -294,14 +327,14 @@ template <typename F> moe_status launched(F launch)
     return launch() == cudaSuccess && cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-// kern<type or types, columns a thread> by run-time values
+// kern<type or types, VEC> by run-time values
 template <typename F> moe_status with_type(int dt, F f)
 {
     return dt == MOE_F32 ? f(static_cast<float *>(nullptr)) : f(static_cast<__nv_bfloat16 *>(nullptr));
 }
 template <typename F> moe_status with_width(bool vec, F f)
 {
-    return vec ? f(std::integral_constant<int, V>()) : f(std::integral_constant<int, 1>());
+    return vec ? f(std::true_type()) : f(std::false_type());
 }
 
 template <bool WEIGHTED>
@@ -313,13 +346,13 @@ moe_status gather_sum(Args a, moe_dtype x_dt, moe_dtype out_dt, cudaStream_t s)
             return with_width(vec, [&](auto width) {
                 using XT = std::remove_pointer_t<decltype(xt)>;
                 using OT = std::remove_pointer_t<decltype(ot)>;
-                constexpr int N = decltype(width)::value;
+                [[maybe_unused]] constexpr bool VEC = decltype(width)::value;
                 if constexpr (!WEIGHTED && !std::is_same<XT, OT>::value) return MOE_ERR_INVALID_ARG;   // (never asked for)
                 else {
                     dim3 grid;
-                    if (!lay_out(a, N, &grid)) return MOE_ERR_UNSUPPORTED;
+                    if (!lay_out(a, &grid)) return MOE_ERR_UNSUPPORTED;
                     return launched([&] {
-                        return launch_pdl(gather_sum_kernel<XT, OT, N, WEIGHTED>, grid, dim3(kThreads), 0, s, a);
+                        return launch_pdl(gather_sum_kernel<XT, OT, VEC, WEIGHTED>, grid, dim3(kThreads), 0, s, a);
                     });
                 }
             });
@@ -348,11 +381,11 @@ moe_status moe_dispatch(const void *x, moe_dtype dt, int T, int d, long long ldx
     return with_type(dt, [&](auto *xt) {
         return with_width(vectors(x, ldx, d) && vectors(out, ldo, d), [&](auto width) {
             using XT = std::remove_pointer_t<decltype(xt)>;
-            constexpr int N = decltype(width)::value;
+            constexpr bool VEC = decltype(width)::value;
             dim3 grid;
-            if (!lay_out(a, N, &grid)) return MOE_ERR_UNSUPPORTED;
+            if (!lay_out(a, &grid)) return MOE_ERR_UNSUPPORTED;
             return launched([&] {
-                return launch_pdl(scatter_rows_kernel<XT, N>, grid, dim3(kThreads), 0, static_cast<cudaStream_t>(stream), a);
+                return launch_pdl(scatter_rows_kernel<XT, VEC>, grid, dim3(kThreads), 0, static_cast<cudaStream_t>(stream), a);
             });
         });
     });
@@ -406,14 +439,13 @@ moe_status moe_combine_backward(const void *grad, moe_dtype grad_dt, int T, int 
             return with_width(vec, [&](auto width) {
                 using XT = std::remove_pointer_t<decltype(xt)>;
                 using GT = std::remove_pointer_t<decltype(gt)>;
-                constexpr int N = decltype(width)::value;
-                a.chunks = d / N;
+                constexpr bool VEC = decltype(width)::value;
                 return launched([&] {
                     cudaStream_t s = static_cast<cudaStream_t>(stream);
                     if (T >= 16 * device_sm_count())
-                        return launch_pdl(combine_backward_kernel<XT, GT, N, 32>, dim3((unsigned)ceil_div(T, kThreads / 32)),
+                        return launch_pdl(combine_backward_kernel<XT, GT, VEC, 32>, dim3((unsigned)ceil_div(T, kThreads / 32)),
                                           dim3(kThreads), 0, s, a);
-                    return launch_pdl(combine_backward_kernel<XT, GT, N, kThreads>, dim3((unsigned)T), dim3(kThreads), 0, s, a);
+                    return launch_pdl(combine_backward_kernel<XT, GT, VEC, kThreads>, dim3((unsigned)T), dim3(kThreads), 0, s, a);
                 });
             });
         });

@@ -86,27 +86,35 @@ __device__ __forceinline__ Factor factor_of(uint32_t top_bits, float &scale)
     }
     return f;
 }
-template <typename XT> __device__ __forceinline__ int code_of(float x, const Factor &f)
+// The code in the low byte: adding 1.5 * 2^23 leaves the nearest whole number in the low
+// bits, ties to even (a conversion to int runs at a quarter of the rate).
+template <typename XT> __device__ __forceinline__ uint32_t code_of(float x, const Factor &f)
 {
-    // (a row of zero codes: an infinity times 0 would be NaN, whose code is 0 too)
-    const float q = fmaf(x, f.hi, x * f.lo);
-    int c = __float2int_rn(q);
+    constexpr float kWhole = 12582912.0f;
+    const float q = fmaf(x, f.hi, x * f.lo), t = q + kWhole;
+    uint32_t c = __float_as_uint(t);
     if (std::is_same<XT, float>::value) {
-        const float m = fabsf(q), low = floorf(m);
-        if (fabsf(m - low - 0.5f) < 0x1p-15f) {
+        if (fabsf(q - (t - kWhole)) > 0.5f - 0x1p-15f) {
+            const float low = floorf(fabsf(q));
             const double left = 127.0 * (double)fabsf(x), right = ((double)low + 0.5) * (double)f.top;
             const int l = (int)low, n = left > right ? l + 1 : left < right ? l : l + (l & 1);
-            c = x < 0.f ? -n : n;
+            c = (uint32_t)(x < 0.f ? -n : n);
         }
     }
     return c;
 }
 template <typename XT> __device__ __forceinline__ uint2 codes_of(const Raw8<XT> &r, const Factor &f)
 {
-    uint32_t w[2] = {0u, 0u};
+    uint32_t w[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i >> 2] |= ((uint32_t)code_of<XT>(r.get(i), f) & 0xffu) << (8 * (i & 3));
-    return make_uint2(w[0], w[1]);
+    for (int h = 0; h < 2; ++h) {
+        uint32_t c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = code_of<XT>(r.get(4 * h + i), f);
+        w[h] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+    }
+    // (zero codes, whatever the products of a row's infinities and NaN with 0 are)
+    return f.hi == 0.f ? make_uint2(0u, 0u) : make_uint2(w[0], w[1]);
 }
 
 // `lanes` threads (a multiple of 32) to a row, NV chunks of 8 values each, all in
@@ -173,10 +181,18 @@ cudaError_t launch_quant(const void *x, int rows, int cols, long long ldx, uint8
 {
     constexpr int kMost = sizeof(XT) == 4 ? 4 : 8;   // chunks a thread holds: 32 registers
     const int chunks = cols / 8;
-    // A warp to a row while there are rows for a warp on every scheduler (no barrier,
-    // several chunks in flight a thread), else as many threads as chunks: few rows
-    // are latency.
-    int lanes = rows >= 16 * device_sm_count() ? ceil_div(chunks, kMost) : chunks;
+    // Many rows: as few threads to a row as hold it with most of their chunks in use (a
+    // warp needs no barrier, and several chunks are in flight a thread); few rows: as many
+    // threads as chunks, as they are latency.  (8192 x 2816 in bf16: 64 threads of 8 chunks,
+    // of which 352 of 512 are used, 13.5 us; 96 of 4 10.9.)
+    int lanes = chunks;
+    if (rows >= 16 * device_sm_count()) {
+        int best = 0;   // slots that a choice leaves unused, of 1024 for each it has
+        for (int nv = kMost; nv >= 1; nv /= 2) {
+            const int l = (int)align_up((size_t)ceil_div(chunks, nv), 32), waste = (l * nv - chunks) * 1024 / (l * nv);
+            if (nv == kMost || waste < best - 100) { lanes = l; best = waste; }
+        }
+    }
     lanes = (int)align_up((size_t)(lanes < kQuantThreads ? lanes : kQuantThreads), 32);
     const int nv = ceil_div(chunks, lanes), threads = lanes < 128 ? 128 / lanes * lanes : lanes;
     const int per = threads / lanes;
