@@ -22,91 +22,143 @@ namespace rows {
 constexpr int kThreads = 256;
 constexpr int V = 8;            // columns of a thread's chunk
 
-// V columns of a thread.  VEC: neighbours, 16 bytes a load (or two).  Else, where rows do not
-// lie on 16-byte boundaries, `step` apart, an element a load: the threads of a row still
-// read neighbouring elements, and V loads are in flight.
-template <typename T, bool VEC> struct Chunk;
-template <typename T> struct Bits;
-template <> struct Bits<float> {
-    using Raw = uint32_t;
-    __device__ static __forceinline__ float get(uint32_t r) { return __uint_as_float(r); }
-    __device__ static __forceinline__ uint32_t put(float v) { return __float_as_uint(v); }
-};
-template <> struct Bits<__nv_bfloat16> {
-    using Raw = uint16_t;
-    __device__ static __forceinline__ float get(uint16_t r) { return __uint_as_float((uint32_t)r << 16); }
-    __device__ static __forceinline__ uint16_t put(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
-};
-template <typename T> struct Chunk<T, false> {
-    typename Bits<T>::Raw a[V];
-    __device__ __forceinline__ void load(const T *p, int step, int left)
+// V neighbouring columns of a thread, as loaded.
+template <typename T> struct Chunk;
+template <> struct Chunk<float> {
+    uint32_t a[8];
+    __device__ __forceinline__ void load(const float *p)
     {
-#pragma unroll
-        for (int i = 0; i < V; ++i) a[i] = i * step < left ? __ldg(reinterpret_cast<const typename Bits<T>::Raw *>(p) + i * step) : 0;
+        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p)), y = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+        a[0] = x.x; a[1] = x.y; a[2] = x.z; a[3] = x.w; a[4] = y.x; a[5] = y.y; a[6] = y.z; a[7] = y.w;
     }
-    __device__ __forceinline__ void store(T *p, int step, int left) const
+    __device__ __forceinline__ void store(float *p) const
+    {
+        reinterpret_cast<uint4 *>(p)[0] = make_uint4(a[0], a[1], a[2], a[3]);
+        reinterpret_cast<uint4 *>(p)[1] = make_uint4(a[4], a[5], a[6], a[7]);
+    }
+    // element i if `in`, else 0 (from i = 0 on, in order)
+    __device__ __forceinline__ void load_one(int i, bool in, const float *p)
+    {
+        a[i] = in ? __ldg(reinterpret_cast<const uint32_t *>(p)) : 0u;
+    }
+    __device__ __forceinline__ void store_one(int i, float *p) const { *reinterpret_cast<uint32_t *>(p) = a[i]; }
+    __device__ __forceinline__ float get(int i) const { return __uint_as_float(a[i]); }
+    __device__ __forceinline__ void set(const float (&v)[V])
     {
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (i * step < left) reinterpret_cast<typename Bits<T>::Raw *>(p)[i * step] = a[i];
+        for (int i = 0; i < V; ++i) a[i] = __float_as_uint(v[i]);
     }
     __device__ __forceinline__ void zero()
     {
 #pragma unroll
-        for (int i = 0; i < V; ++i) a[i] = 0;
-    }
-    __device__ __forceinline__ float get(int i) const { return Bits<T>::get(a[i]); }
-    __device__ __forceinline__ void set(const float (&v)[V])
-    {
-#pragma unroll
-        for (int i = 0; i < V; ++i) a[i] = Bits<T>::put(v[i]);
+        for (int i = 0; i < 8; ++i) a[i] = 0u;
     }
 };
-template <> struct Chunk<float, true> {
-    uint4 a, b;
-    __device__ __forceinline__ void load(const float *p, int, int)
+template <> struct Chunk<__nv_bfloat16> {
+    uint32_t a[4];
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p)
     {
-        a = __ldg(reinterpret_cast<const uint4 *>(p));
-        b = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p));
+        a[0] = x.x; a[1] = x.y; a[2] = x.z; a[3] = x.w;
     }
-    __device__ __forceinline__ void store(float *p, int, int) const
+    __device__ __forceinline__ void store(__nv_bfloat16 *p) const { *reinterpret_cast<uint4 *>(p) = make_uint4(a[0], a[1], a[2], a[3]); }
+    __device__ __forceinline__ void load_one(int i, bool in, const __nv_bfloat16 *p)
     {
-        reinterpret_cast<uint4 *>(p)[0] = a;
-        reinterpret_cast<uint4 *>(p)[1] = b;
+        const uint32_t v = in ? __ldg(reinterpret_cast<const uint16_t *>(p)) : 0;
+        a[i >> 1] = (i & 1) ? a[i >> 1] | (v << 16) : v;
     }
-    __device__ __forceinline__ void zero() { a = b = make_uint4(0u, 0u, 0u, 0u); }
-    __device__ __forceinline__ float get(int i) const
+    __device__ __forceinline__ void store_one(int i, __nv_bfloat16 *p) const
     {
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        return __uint_as_float(w[i]);
+        *reinterpret_cast<uint16_t *>(p) = (uint16_t)(a[i >> 1] >> (16 * (i & 1)));
     }
+    __device__ __forceinline__ float get(int i) const { return (i & 1) ? bf16hi(a[i >> 1]) : bf16lo(a[i >> 1]); }
     __device__ __forceinline__ void set(const float (&v)[V])
     {
-        a = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-        b = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
-    }
-};
-template <> struct Chunk<__nv_bfloat16, true> {
-    uint4 a;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p, int, int) { a = __ldg(reinterpret_cast<const uint4 *>(p)); }
-    __device__ __forceinline__ void store(__nv_bfloat16 *p, int, int) const { *reinterpret_cast<uint4 *>(p) = a; }
-    __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
-    __device__ __forceinline__ float get(int i) const
-    {
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-        return (i & 1) ? bf16hi(w[i >> 1]) : bf16lo(w[i >> 1]);
-    }
-    __device__ __forceinline__ void set(const float (&v)[V])
-    {
-        uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            a[i] = *reinterpret_cast<const uint32_t *>(&h);
         }
-        a = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = 0u;
     }
 };
+
+// How a thread's V columns lie.
+//   WHOLE    neighbours; rows lie on 16-byte boundaries
+//   APART    `step` apart, an element a load: the threads of a row read neighbouring elements.
+//            Rows on any boundary, where elements are 4 bytes or little is written.
+//   SHIFTED  neighbours that begin on a boundary of the written row, so that stores of
+//            2-byte elements are whole too; what is read there comes as the 16-byte pieces
+//            around it, shifted into place (only pieces inside the row: at its ends it goes
+//            by elements).
+// Measured (us, APART / SHIFTED): gradients of 8192 x 2 x 1001 in bf16 52 / 34, of 4096 x 4 x 2049 in
+// fp32 56 / 73; combine of 4096 x 4 x 2049 in bf16 38 / 31.
+enum Way { WHOLE = 0, APART = 1, SHIFTED = 2 };
+template <typename T> __device__ __forceinline__ void load_apart(Chunk<T> &c, const T *p, int step, int left)
+{
+#pragma unroll
+    for (int i = 0; i < V; ++i) c.load_one(i, i * step < left, p + i * step);
+}
+template <typename T> __device__ __forceinline__ void store_apart(const Chunk<T> &c, T *p, int step, int left)
+{
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (i * step < left) c.store_one(i, p + i * step);
+}
+// Columns before the first boundary of a row.
+template <typename T> __device__ __forceinline__ int lead_of(const T *row)
+{
+    return (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / (int)sizeof(T);
+}
+// Columns col .. col + 7 of a row of d (zeros outside it).
+template <typename T> __device__ __forceinline__ void load_any(Chunk<T> &c, const T *row, int col, int d)
+{
+    constexpr int W = V * (int)sizeof(T) / 4;               // words of a chunk
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row + col);
+    const int off = (int)(at & 15);
+    if (col >= 0 && col + V <= d && off == 0) {
+        c.load(row + col);
+        return;
+    }
+    const T *from = reinterpret_cast<const T *>(at - off);
+    const int before = off / (int)sizeof(T);
+    if (col - before >= 0 && col - before + V + 16 / (int)sizeof(T) <= d) {
+        uint32_t w[W + 4];
+#pragma unroll
+        for (int i = 0; i < W / 4 + 1; ++i) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(from) + i);
+            w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+        }
+        if (off & 8) {
+#pragma unroll
+            for (int i = 0; i < W + 2; ++i) w[i] = w[i + 2];
+        }
+        if (off & 4) {
+#pragma unroll
+            for (int i = 0; i < W + 1; ++i) w[i] = w[i + 1];
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i) c.a[i] = (off & 2) ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) c.load_one(i, col + i >= 0 && col + i < d, row + col + i);
+}
+// ... to a row on one of whose boundaries `col` lies.
+template <typename T> __device__ __forceinline__ void store_any(const Chunk<T> &c, T *row, int col, int d)
+{
+    if (col >= 0 && col + V <= d) {
+        c.store(row + col);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (col + i >= 0 && col + i < d) c.store_one(i, row + col + i);
+}
 
 struct Args {
     const void *x;            // dispatch: [T, d]; combine: y [rows, d]
@@ -117,61 +169,86 @@ struct Args {
     float *dw;
     long long ldx, ldg, ldo;  // elements from row to row
     int T, k, rows, d;
-    int col_blocks;           // CTAs along a row
+    int chunks, col_blocks;   // chunks of a row; CTAs along it
+    int each;                 // chunks a thread takes
     int lanes_log2;           // threads of a CTA along a row
 };
 
-// This thread's token and first column; a CTA holds kThreads >> lanes_log2 tokens, and a
-// row's chunks are spread over col_blocks CTAs (a thread takes one chunk, so that a few
-// tokens still fill the SMs).  Without VEC its columns lie 1 << lanes_log2 apart.
-template <bool VEC> __device__ __forceinline__ bool place(const Args &a, long long &t, int &col)
+// This thread's token and chunk; a CTA holds kThreads >> lanes_log2 tokens, and a row's
+// chunks are spread over col_blocks CTAs.
+__device__ __forceinline__ bool place(const Args &a, long long &t, int &chunk)
 {
-    const int lanes = 1 << a.lanes_log2, lane = threadIdx.x & (lanes - 1);
+    const int lanes = 1 << a.lanes_log2;
     const long long tb = blockIdx.x / a.col_blocks;
     t = tb * (kThreads >> a.lanes_log2) + (threadIdx.x >> a.lanes_log2);
-    col = (int)(blockIdx.x - tb * a.col_blocks) * (lanes * V) + (VEC ? lane * V : lane);
-    return t < a.T && col < a.d;
+    chunk = (int)(blockIdx.x - tb * a.col_blocks) * (lanes * a.each) + (threadIdx.x & (lanes - 1));
+    return t < a.T && chunk < a.chunks;
+}
+// The first column of chunk c (SHIFTED: chunk 0 is what stands before the first boundary).
+template <int WAY, typename T> __device__ __forceinline__ int column(int c, int lanes, const T *written)
+{
+    const int lane = c & (lanes - 1);   // (lanes is a power of two)
+    return WAY == WHOLE ? c * V : WAY == APART ? (c - lane) * V + lane : lead_of(written) + (c - 1) * V;
+}
+template <int WAY, typename T> __device__ __forceinline__ void load(Chunk<T> &c, const T *row, int col, int lanes, int d)
+{
+    if (WAY == WHOLE) c.load(row + col);
+    else if (WAY == APART) load_apart(c, row + col, lanes, d - col);
+    else load_any(c, row, col, d);
+}
+template <int WAY, typename T> __device__ __forceinline__ void store(const Chunk<T> &c, T *row, int col, int lanes, int d)
+{
+    if (WAY == WHOLE) c.store(row + col);
+    else if (WAY == APART) store_apart(c, row + col, lanes, d - col);
+    else store_any(c, row, col, d);
 }
 
-template <typename XT, bool VEC>
+template <typename XT, int WAY>
 __global__ void __launch_bounds__(kThreads)
 scatter_rows_kernel(const Args a)
 {
     pdl_enter();
     long long t;
-    int col;
-    if (!place<VEC>(a, t, col)) return;
-    const int step = 1 << a.lanes_log2, left = a.d - col;
-    Chunk<XT, VEC> c;
-    c.load(static_cast<const XT *>(a.x) + t * a.ldx + col, step, left);
-    XT *out = static_cast<XT *>(a.out) + col;
+    int chunk;
+    if (!place(a, t, chunk)) return;
+    const int lanes = 1 << a.lanes_log2;
+    const XT *x = static_cast<const XT *>(a.x) + t * a.ldx;
     const int32_t *inv = a.inv + t * a.k;
+    Chunk<XT> c;
+    if (WAY != SHIFTED) load<WAY>(c, x, column<WAY>(chunk, lanes, x), lanes, a.d);
 #pragma unroll 4
     for (int j = 0; j < a.k; ++j) {
         const int r = __ldg(inv + j);
-        if (r >= 0 && r < a.rows) c.store(out + r * a.ldo, step, left);
+        if (r < 0 || r >= a.rows) continue;
+        XT *out = static_cast<XT *>(a.out) + r * a.ldo;
+        const int col = column<WAY>(chunk, lanes, out);
+        if (WAY == SHIFTED) load<WAY>(c, x, col, lanes, a.d);
+        store<WAY>(c, out, col, lanes, a.d);
     }
 }
 
-// WEIGHTED: combine; else dispatch's backward pass.
-template <typename XT, typename OT, bool VEC, bool WEIGHTED>
+// WEIGHTED: combine; else dispatch's backward pass.  A thread takes EACH chunks, lanes
+// apart, and asks for U rows of them at once.
+template <typename XT, typename OT, int WAY, bool WEIGHTED, int EACH, int U>
 __global__ void __launch_bounds__(kThreads)
 gather_sum_kernel(const Args a)
 {
     pdl_enter();
     long long t;
-    int col;
-    if (!place<VEC>(a, t, col)) return;
-    const int step = 1 << a.lanes_log2, left = a.d - col;
-    const XT *x = static_cast<const XT *>(a.x) + col;
+    int chunk;
+    if (!place(a, t, chunk)) return;
+    const int lanes = 1 << a.lanes_log2;
+    OT *out = static_cast<OT *>(a.out) + t * a.ldo;
+    const XT *x = static_cast<const XT *>(a.x);
     const int32_t *inv = a.inv + t * a.k;
     const float *w = a.topk_w + t * a.k;
-    float sum[V];
+    float sum[EACH][V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) sum[i] = 0.f;
-    constexpr int U = VEC ? 4 : 2;   // rows asked for at once
+    for (int e = 0; e < EACH; ++e)
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum[e][i] = 0.f;
     for (int j0 = 0; j0 < a.k; j0 += U) {
-        Chunk<XT, VEC> c[U];
+        Chunk<XT> c[EACH][U];
         float f[U];
         bool in[U];
 #pragma unroll
@@ -180,7 +257,11 @@ gather_sum_kernel(const Args a)
             in[u] = r >= 0 && r < a.rows;
             f[u] = 1.f;
             if (in[u]) {
-                c[u].load(x + r * a.ldx, step, left);
+#pragma unroll
+                for (int e = 0; e < EACH; ++e) {
+                    const int at = chunk + e * lanes;
+                    if (at < a.chunks) load<WAY>(c[e][u], x + r * a.ldx, column<WAY>(at, lanes, out), lanes, a.d);
+                }
                 if (WEIGHTED) f[u] = __ldg(w + j0 + u);
             }
         }
@@ -188,18 +269,26 @@ gather_sum_kernel(const Args a)
         for (int u = 0; u < U; ++u) {
             if (!in[u]) continue;   // (a slot without a row adds nothing, whatever its weight)
 #pragma unroll
-            for (int i = 0; i < V; ++i) sum[i] = WEIGHTED ? fmaf(f[u], c[u].get(i), sum[i]) : sum[i] + c[u].get(i);
+            for (int e = 0; e < EACH; ++e)
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    sum[e][i] = WEIGHTED ? fmaf(f[u], c[e][u].get(i), sum[e][i]) : sum[e][i] + c[e][u].get(i);
         }
     }
-    Chunk<OT, VEC> o;
-    o.set(sum);
-    o.store(static_cast<OT *>(a.out) + t * a.ldo + col, step, left);
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) {
+        const int at = chunk + e * lanes;
+        if (at >= a.chunks) break;
+        Chunk<OT> o;
+        o.set(sum[e]);
+        store<WAY>(o, out, column<WAY>(at, lanes, out), lanes, a.d);
+    }
 }
 
 // Combine's backward pass: a token to a group of `G` threads (a warp, or the CTA),
 // which walk its chunks; each thread sums its part of every slot's product, and the
 // parts meet in a fixed order (shuffles, then the warps in order).
-template <typename XT, typename GT, bool VEC, int G>
+template <typename XT, typename GT, int WAY, int G>
 __global__ void __launch_bounds__(kThreads)
 combine_backward_kernel(const Args a)
 {
@@ -222,46 +311,69 @@ combine_backward_kernel(const Args a)
             if (r[j] >= a.rows) r[j] = -1;
             w[j] = j < a.k ? __ldg(a.topk_w + t * a.k + j) : 0.f;
         }
-        constexpr int C = VEC ? 2 : 1;   // chunks in flight
-        for (int base = 0; base < a.d; base += C * G * V) {
-            Chunk<GT, VEC> c[C];
-            int col[C];
+        // a row's share of a chunk: its part of the dot product, and its gradient
+        auto finish = [&](int j, const Chunk<GT> &c, const Chunk<XT> &v, int col) {
+            float o[V];
 #pragma unroll
-            for (int q = 0; q < C; ++q) {
-                col[q] = base + q * G * V + (VEC ? lane * V : lane);
-                c[q].zero();
-                if (col[q] < a.d) c[q].load(g + col[q], G, a.d - col[q]);
+            for (int i = 0; i < V; ++i) {
+                dot[j] = fmaf(c.get(i), v.get(i), dot[j]);
+                o[i] = w[j] * c.get(i);
             }
-            // (two rows at a time: their loads stand ahead of the stores)
+            if (dy) {
+                Chunk<XT> s;
+                s.set(o);
+                store<WAY>(s, dy + r[j] * a.ldo, col, G, a.d);
+            }
+        };
+        if constexpr (WAY == SHIFTED) {
+            for (int chunk = lane; chunk < a.chunks; chunk += G) {
+                // (two rows at a time: their loads stand ahead of the stores)
 #pragma unroll
-            for (int j0 = 0; j0 < kMaxTopK; j0 += 2) {
-                if (j0 >= a.k) break;
-                Chunk<XT, VEC> v[C][2];
-#pragma unroll
-                for (int q = 0; q < C; ++q)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        v[q][u].zero();
-                        if (r[j0 + u] >= 0 && a.dw && col[q] < a.d) v[q][u].load(y + r[j0 + u] * a.ldx + col[q], G, a.d - col[q]);
-                    }
-#pragma unroll
-                for (int q = 0; q < C; ++q)
+                for (int j0 = 0; j0 < kMaxTopK; j0 += 2) {
+                    if (j0 >= a.k) break;
+                    Chunk<XT> v[2];
+                    Chunk<GT> c[2];   // the gradient at each row's own columns
+                    int col[2];
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         const int j = j0 + u;
-                        if (r[j] < 0 || col[q] >= a.d) continue;
-                        float o[V];
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            dot[j] = fmaf(c[q].get(i), v[q][u].get(i), dot[j]);
-                            o[i] = w[j] * c[q].get(i);
-                        }
-                        if (dy) {
-                            Chunk<XT, VEC> s;
-                            s.set(o);
-                            s.store(dy + r[j] * a.ldo + col[q], G, a.d - col[q]);
-                        }
+                        if (r[j] < 0) continue;
+                        // (without dy nothing is written: y's rows decide)
+                        col[u] = column<WAY>(chunk, G, dy ? dy + r[j] * a.ldo : y + r[j] * a.ldx);
+                        v[u].zero();
+                        if (a.dw) load_any(v[u], y + r[j] * a.ldx, col[u], a.d);
+                        load_any(c[u], g, col[u], a.d);
                     }
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        if (r[j0 + u] >= 0) finish(j0 + u, c[u], v[u], col[u]);
+                }
+            }
+        } else {
+            constexpr int C = WAY == WHOLE ? 2 : 1;   // chunks in flight
+            for (int c0 = lane; c0 < a.chunks; c0 += C * G) {
+                Chunk<GT> c[C];
+#pragma unroll
+                for (int q = 0; q < C; ++q)
+                    if (c0 + q * G < a.chunks) load<WAY>(c[q], g, column<WAY>(c0 + q * G, G, g), G, a.d);
+#pragma unroll
+                for (int j0 = 0; j0 < kMaxTopK; j0 += 2) {
+                    if (j0 >= a.k) break;
+                    Chunk<XT> v[C][2];
+#pragma unroll
+                    for (int q = 0; q < C; ++q)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            v[q][u].zero();
+                            if (r[j0 + u] >= 0 && a.dw && c0 + q * G < a.chunks)
+                                load<WAY>(v[q][u], y + r[j0 + u] * a.ldx, column<WAY>(c0 + q * G, G, y), G, a.d);
+                        }
+#pragma unroll
+                    for (int q = 0; q < C; ++q)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+                            if (r[j0 + u] >= 0 && c0 + q * G < a.chunks) finish(j0 + u, c[q], v[q][u], column<WAY>(c0 + q * G, G, y));
+                }
             }
         }
     }
@@ -309,13 +421,23 @@ bool matrix_ok(const void *p, moe_dtype dt, long long ld, int d, bool may_be_emp
     return float_ok(dt) && ld >= d && (p || may_be_empty) && aligned(p, size_of(dt));
 }
 
-// grid of a kernel whose threads take a chunk each
-bool lay_out(Args &a, dim3 *grid)
+// Chunks of a row that have columns.  SHIFTED: one more, for what stands before its first
+// boundary; APART: `lanes` of them hold lanes * V columns together, and the last lanes' are
+// the shorter ones.
+int chunks_of(int d, int way, int lanes)
 {
-    const int chunks = ceil_div(a.d, V);
+    if (way == APART) return d / (lanes * V) * lanes + (d % (lanes * V) < lanes ? d % (lanes * V) : lanes);
+    return ceil_div(d, V) + (way == SHIFTED);
+}
+// grid of a kernel whose threads take `each` chunks
+bool lay_out(Args &a, int way, int each, dim3 *grid)
+{
+    const int threads = ceil_div(chunks_of(a.d, way == APART ? WHOLE : way, 1), each);
     a.lanes_log2 = 5;
-    while (a.lanes_log2 < 8 && (1 << a.lanes_log2) < chunks) ++a.lanes_log2;
-    a.col_blocks = ceil_div(chunks, 1 << a.lanes_log2);
+    while (a.lanes_log2 < 8 && (1 << a.lanes_log2) < threads) ++a.lanes_log2;
+    a.chunks = chunks_of(a.d, way, 1 << a.lanes_log2);
+    a.each = each;
+    a.col_blocks = ceil_div(a.chunks, each << a.lanes_log2);
     const int per = kThreads >> a.lanes_log2;
     const long long ctas = ((long long)a.T + per - 1) / per * a.col_blocks;
     *grid = dim3((unsigned)ctas);
@@ -327,35 +449,42 @@ template <typename F> moe_status launched(F launch)
     return launch() == cudaSuccess && cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-// kern<type or types, VEC> by run-time values
+// a kernel's types by run-time values
 template <typename F> moe_status with_type(int dt, F f)
 {
     return dt == MOE_F32 ? f(static_cast<float *>(nullptr)) : f(static_cast<__nv_bfloat16 *>(nullptr));
 }
-template <typename F> moe_status with_width(bool vec, F f)
+template <int WAY> using WayOf = std::integral_constant<int, WAY>;
+
+template <typename XT, typename OT, int WAY, bool WEIGHTED>
+moe_status launch_gather_sum(Args a, cudaStream_t s)
 {
-    return vec ? f(std::true_type()) : f(std::false_type());
+    // Many tokens: about 64 bytes in flight a thread (16384 x 2 x 2048 in bf16: one chunk a
+    // thread 44 us, two 35); few: a chunk a thread and its rows at once, as that is latency.
+    const bool many = (long long)a.T * (a.d / V) >= 2LL * kThreads * 8 * device_sm_count();
+    constexpr int kTwice = sizeof(XT) == 4 ? 1 : 2;   // (fp32 chunks are twice as long)
+    const auto go = [&](auto kern, int each) {
+        dim3 grid;
+        if (!lay_out(a, WAY, each, &grid)) return MOE_ERR_UNSUPPORTED;
+        return launched([&] { return launch_pdl(kern, grid, dim3(kThreads), 0, s, a); });
+    };
+    if constexpr (WAY == WHOLE) {
+        if (many && a.k == 1) return go(gather_sum_kernel<XT, OT, WAY, WEIGHTED, 2 * kTwice, 1>, 2 * kTwice);
+        if (many && a.k <= 3) return go(gather_sum_kernel<XT, OT, WAY, WEIGHTED, kTwice, 2>, kTwice);
+    }
+    return go(gather_sum_kernel<XT, OT, WAY, WEIGHTED, 1, WAY == WHOLE ? 4 : 2>, 1);
 }
 
 template <bool WEIGHTED>
-moe_status gather_sum(Args a, moe_dtype x_dt, moe_dtype out_dt, cudaStream_t s)
+moe_status gather_sum(const Args &a, moe_dtype x_dt, moe_dtype out_dt, cudaStream_t s)
 {
-    const bool vec = vectors(a.x, a.ldx, a.d) && vectors(a.out, a.ldo, a.d);
+    const bool whole = vectors(a.x, a.ldx, a.d) && vectors(a.out, a.ldo, a.d);
     return with_type(x_dt, [&](auto *xt) {
         return with_type(out_dt, [&](auto *ot) {
-            return with_width(vec, [&](auto width) {
-                using XT = std::remove_pointer_t<decltype(xt)>;
-                using OT = std::remove_pointer_t<decltype(ot)>;
-                [[maybe_unused]] constexpr bool VEC = decltype(width)::value;
-                if constexpr (!WEIGHTED && !std::is_same<XT, OT>::value) return MOE_ERR_INVALID_ARG;   // (never asked for)
-                else {
-                    dim3 grid;
-                    if (!lay_out(a, &grid)) return MOE_ERR_UNSUPPORTED;
-                    return launched([&] {
-                        return launch_pdl(gather_sum_kernel<XT, OT, VEC, WEIGHTED>, grid, dim3(kThreads), 0, s, a);
-                    });
-                }
-            });
+            using XT = std::remove_pointer_t<decltype(xt)>;
+            using OT = std::remove_pointer_t<decltype(ot)>;
+            if constexpr (!WEIGHTED && !std::is_same<XT, OT>::value) return MOE_ERR_INVALID_ARG;   // (never asked for)
+            else return whole ? launch_gather_sum<XT, OT, WHOLE, WEIGHTED>(a, s) : launch_gather_sum<XT, OT, sizeof(XT) == 4 ? APART : SHIFTED, WEIGHTED>(a, s);
         });
     });
 }
@@ -379,15 +508,15 @@ moe_status moe_dispatch(const void *x, moe_dtype dt, int T, int d, long long ldx
     Args a{};
     a.x = x; a.out = out; a.inv = inv; a.ldx = ldx; a.ldo = ldo; a.T = T; a.k = k; a.rows = rows; a.d = d;
     return with_type(dt, [&](auto *xt) {
-        return with_width(vectors(x, ldx, d) && vectors(out, ldo, d), [&](auto width) {
-            using XT = std::remove_pointer_t<decltype(xt)>;
-            constexpr bool VEC = decltype(width)::value;
+        using XT = std::remove_pointer_t<decltype(xt)>;
+        constexpr int kOff = sizeof(XT) == 4 ? APART : SHIFTED;
+        const auto go = [&](auto kern, int way) {
             dim3 grid;
-            if (!lay_out(a, &grid)) return MOE_ERR_UNSUPPORTED;
-            return launched([&] {
-                return launch_pdl(scatter_rows_kernel<XT, VEC>, grid, dim3(kThreads), 0, static_cast<cudaStream_t>(stream), a);
-            });
-        });
+            if (!lay_out(a, way, 1, &grid)) return MOE_ERR_UNSUPPORTED;
+            return launched([&] { return launch_pdl(kern, grid, dim3(kThreads), 0, static_cast<cudaStream_t>(stream), a); });
+        };
+        if (vectors(x, ldx, d) && vectors(out, ldo, d)) return go(scatter_rows_kernel<XT, WHOLE>, WHOLE);
+        return go(scatter_rows_kernel<XT, kOff>, kOff);
     });
 }
 
@@ -433,21 +562,25 @@ moe_status moe_combine_backward(const void *grad, moe_dtype grad_dt, int T, int 
     Args a{};
     a.x = y; a.g = grad; a.out = dy; a.dw = dw; a.topk_w = topk_w; a.inv = inv;
     a.ldx = ldy; a.ldg = ldg; a.ldo = lddy; a.T = T; a.k = k; a.rows = rows; a.d = d;
-    const bool vec = vectors(grad, ldg, d) && (!dw || vectors(y, ldy, d)) && (!dy || vectors(dy, lddy, d));
+    const bool whole = vectors(grad, ldg, d) && (!dw || vectors(y, ldy, d)) && (!dy || vectors(dy, lddy, d));
     return with_type(y_dt, [&](auto *xt) {
         return with_type(grad_dt, [&](auto *gt) {
-            return with_width(vec, [&](auto width) {
-                using XT = std::remove_pointer_t<decltype(xt)>;
-                using GT = std::remove_pointer_t<decltype(gt)>;
-                constexpr bool VEC = decltype(width)::value;
+            using XT = std::remove_pointer_t<decltype(xt)>;
+            using GT = std::remove_pointer_t<decltype(gt)>;
+            constexpr int kOff = sizeof(XT) == 4 ? APART : SHIFTED;
+            const auto go = [&](auto way) {
+                constexpr int WAY = decltype(way)::value;
+                const bool warps = T >= 16 * device_sm_count();   // (a warp to a token, or a CTA)
+                a.chunks = chunks_of(d, WAY, warps ? 32 : kThreads);
                 return launched([&] {
                     cudaStream_t s = static_cast<cudaStream_t>(stream);
-                    if (T >= 16 * device_sm_count())
-                        return launch_pdl(combine_backward_kernel<XT, GT, VEC, 32>, dim3((unsigned)ceil_div(T, kThreads / 32)),
+                    if (warps)
+                        return launch_pdl(combine_backward_kernel<XT, GT, WAY, 32>, dim3((unsigned)ceil_div(T, kThreads / 32)),
                                           dim3(kThreads), 0, s, a);
-                    return launch_pdl(combine_backward_kernel<XT, GT, VEC, kThreads>, dim3((unsigned)T), dim3(kThreads), 0, s, a);
+                    return launch_pdl(combine_backward_kernel<XT, GT, WAY, kThreads>, dim3((unsigned)T), dim3(kThreads), 0, s, a);
                 });
-            });
+            };
+            return whole ? go(WayOf<WHOLE>()) : go(WayOf<kOff>());
         });
     });
 }
