@@ -13,8 +13,8 @@
 // nor shared memory.  Tokens are the columns:
 //   tiled     128 of them, as fp16 rows that convert_rows_kernel has written (in group
 //             order, so it gathers too), by TMA;
-//   few rows  32, read as int8 and widened into shared memory by the same warps; two CTAs
-//             an SM.  Few tiles split the reduction over a cluster, whose CTAs send their
+//   few rows  32 or 64, read as int8 and widened into shared memory by the same warps; two
+//             CTAs an SM.  Few tiles split the reduction over a cluster, whose CTAs send their
 //             partial sums to the one that finishes the token (distributed shared memory).
 // Accumulators are two, so a tile's output overlaps the next tile's products.
 //
@@ -56,18 +56,20 @@ constexpr size_t kPartial = (size_t)(32 + kMaxSplit) * M * 4;   // whole turns o
 // output channels of a tile
 constexpr int rows_of_mode(int mode) { return mode == GATEUP ? M / 2 : M; }
 
-template <bool FEW, bool SPLIT = false> struct Cfg {
-    static constexpr int NT = FEW ? 32 : 128;                      // tokens of a tile
+// The kernels: NT tokens a tile; fewer than 128 are few rows; a split reduction with 32.
+template <int NT, bool SPLIT = false> struct Cfg {
+    static constexpr bool FEW = NT < 128;
     static constexpr int X_BYTES = NT * BK * (FEW ? 1 : 2);
-    static constexpr int WS = SPLIT ? 3 : 4;                       // blocks of the weights' ring
-    static constexpr int NA = FEW ? 3 : 4;                         // converted blocks in flight
-    static constexpr int XS = FEW ? 4 : NA;                        // blocks of the tokens' ring (tiled: block a's
+    static constexpr int WS = SPLIT || NT == 64 ? 3 : 4;           // blocks of the weights' ring
+    static constexpr int NA = NT == 64 ? 2 : FEW ? 3 : 4;          // converted blocks in flight
+    static constexpr int XS = NT == 64 ? 3 : 4;                    // blocks of the tokens' ring (tiled: block a's
                                                                    // tokens are freed with its converted weights)
     static constexpr int XF_BYTES = FEW ? NT * BK * 2 : 0;         // widened tokens of a block
     static constexpr int A_COL = 2 * NT;                           // (two accumulators before)
     static constexpr int TMEM_COLS = FEW ? 256 : 512;
     static constexpr int MMAS = FEW ? 1 : 2;                       // multiplying warps, each with its share of the tokens
     static constexpr int EPI = FEW ? 4 : 16;                       // output warps
+    static constexpr int EACH = FEW ? NT : 32;                     // ... and the tokens of one
     static constexpr int THREADS = 128 + 32 * (EPI + kConvWarps);
     static constexpr size_t XRING = (size_t)WS * W_BYTES;
     static constexpr size_t XF = XRING + (size_t)XS * X_BYTES;
@@ -76,23 +78,26 @@ template <bool FEW, bool SPLIT = false> struct Cfg {
     // the stream start beside this one)
     static constexpr size_t CTL = STAGING + (SPLIT ? kPartial : FEW ? 2 * kStaging : EPI * kStaging / 2);
     static_assert(A_COL + NA * kBlockCols <= TMEM_COLS, "tensor memory");
+    static_assert(WS >= NA && XS >= NA, "a converting group waits for a phase that the other has left");
+    static_assert(FEW || XS == NA, "a tiled block's tokens and converted weights share an index");
+    static_assert(!SPLIT || NT == 32, "partial sums");
 };
 constexpr int kMaxRing = 4, kTable = 32;
 
-template <int EPI> struct alignas(16) Ctl {
+template <int EPI, int EACH> struct alignas(16) Ctl {
     uint64_t wfull[kMaxRing], wempty[kMaxRing], xfull[kMaxRing], xempty[kMaxRing], cfull[kMaxRing], cempty[kMaxRing];
     uint64_t dfull[2], dempty[2], drain[2];
     uint64_t never;                          // nothing arrives here (test hook)
     uint32_t tmem_base;
     int abort_flag;
-    alignas(16) float sx[EPI][32], sw[EPI][2][EPI == 4 ? 1 : 32];   // each output warp's scales: tokens', channels' (tiled)
+    alignas(16) float sx[EPI][EACH], sw[EPI][2][EPI == 4 ? 1 : 32];   // each output warp's scales: tokens', channels' (tiled)
     Groups g;
     Tile tiles[kTable];                      // this CTA's first tiles (each role asks for them in turn)
 };
-template <bool FEW> using CtlOf = Ctl<Cfg<FEW>::EPI>;
-template <bool FEW, bool SPLIT = false> constexpr size_t smem_bytes() { return 1024 + Cfg<FEW, SPLIT>::CTL + sizeof(CtlOf<FEW>); }
-static_assert(smem_bytes<false>() <= 232448, "shared memory per CTA");
-static_assert(smem_bytes<true>() <= 115712 && smem_bytes<true, true>() <= 115712, "two CTAs per SM");
+template <int NT> using CtlOf = Ctl<Cfg<NT>::EPI, Cfg<NT>::EACH>;
+template <int NT, bool SPLIT = false> constexpr size_t smem_bytes() { return 1024 + Cfg<NT, SPLIT>::CTL + sizeof(CtlOf<NT>); }
+static_assert(smem_bytes<128>() <= 232448, "shared memory per CTA");
+static_assert(smem_bytes<32>() <= 115712 && smem_bytes<64>() <= 115712 && smem_bytes<32, true>() <= 115712, "two CTAs per SM");
 // registers a thread after the split at start (setmaxnreg) of the tiled kernel: 28 warps
 // launch with 72 each, 2016; 4 x 40 + 8 x 56 + 16 x 88 = 2016
 constexpr int kRegsLaunch = 72, kRegsAux = 40, kRegsConv = 56, kRegsEpi = 88;
@@ -287,16 +292,17 @@ __device__ __forceinline__ void group_barrier(int group)
     asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
 }
 
-template <int MODE, bool FEW, bool SPLIT>
-__global__ void __launch_bounds__(Cfg<FEW>::THREADS, FEW ? 2 : 1)
+template <int MODE, int NT, bool SPLIT>
+__global__ void __launch_bounds__(Cfg<NT>::THREADS, Cfg<NT>::FEW ? 2 : 1)
 product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w0,
                const __grid_constant__ CUtensorMap tm_w1, const __grid_constant__ CUtensorMap tm_out, const Params p)
 {
-    using C = Cfg<FEW, SPLIT>;
-    constexpr int NT = C::NT, WS = C::WS, XS = C::XS, NA = C::NA, ROWS = rows_of_mode(MODE);
+    using C = Cfg<NT, SPLIT>;
+    constexpr bool FEW = C::FEW;
+    constexpr int WS = C::WS, XS = C::XS, NA = C::NA, ROWS = rows_of_mode(MODE);
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    auto &c = *reinterpret_cast<CtlOf<FEW> *>(smem + C::CTL);
+    auto &c = *reinterpret_cast<CtlOf<NT> *>(smem + C::CTL);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int E = p.E;
 
@@ -446,17 +452,22 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     } else if (warp >= 4 + C::EPI) {
         // ------------------------------------------------ convert
         if (!FEW) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
-        // A group takes every second block: a thread a weight row, and (few rows) two pieces of
-        // the tokens.
+        // A group takes every second block: a thread a weight row, and (few rows) pieces of the
+        // tokens.
         const int tid = (threadIdx.x - 128 - 32 * C::EPI) & 127, quad = warp & 3, row = quad * 32 + lane;
         const uint32_t mine = tmem + ((uint32_t)(quad * 32) << 16) + C::A_COL;
         const uint32_t turns = total > first ? (uint32_t)((total - first - 1) / stride + 1) * (uint32_t)(kb1 - kb0) : 0u;
         ok = !expires(p, CONVERT) || __all_sync(0xffffffffu, bar_wait(&c.never, 0, abort_flag, p.expire_ns));
         for (uint32_t it = (warp - 4 - C::EPI) >> 2; it < turns && ok; it += 2) {
             const uint32_t s = it % WS, a = it % NA, sx = it % XS;
-            ok = __all_sync(0xffffffffu, bar_wait(&c.wfull[s], (it / WS) & 1u, abort_flag) &&
-                                             bar_wait(&c.cempty[a], ((it / NA) & 1u) ^ 1u, abort_flag));
+            // cempty first: the MMAs of block it - NA are done, so both groups are past block
+            // it - WS, and the ring's barriers are at this block's phase.  (Asked first, a
+            // barrier that the other group's block is still to complete has the parity of two
+            // phases ago, and the wait would pass.)
+            ok = __all_sync(0xffffffffu, bar_wait(&c.cempty[a], ((it / NA) & 1u) ^ 1u, abort_flag) &&
+                                             bar_wait(&c.wfull[s], (it / WS) & 1u, abort_flag));
             if (!ok) break;
+            __syncwarp();
             tc_fence_after();
             const uint8_t *sw = smem + s * W_BYTES;
             const uint32_t at = mine + a * kBlockCols;
@@ -465,11 +476,6 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                 uint4 v[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const uint4 *>(sw + piece_at(row, 4 * u + q));
-                if (u == 1) {   // the block has been read
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&c.wempty[s]);
-                    __syncwarp();   // (here and below: the instructions that follow are .aligned)
-                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t o[16];
@@ -478,11 +484,17 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                     tmem_st16(at + u * 32 + h * 16, o);
                 }
             }
+            // The block has been read: its codes are in registers that have been used.  (An
+            // arrival right behind the loads does not wait for them, and the next block's TMA
+            // writes are not ordered with them: rows of the next block's codes came in.)
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c.wempty[s]);
+            __syncwarp();   // (here and below: the instructions that follow are .aligned)
             ok = __all_sync(0xffffffffu, bar_wait(&c.xfull[sx], (it / XS) & 1u, abort_flag));
             if (!ok) break;
             if (FEW) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
+                for (int j = 0; j < NT / 16; ++j) {
                     const int q = tid + j * 128, xr = q >> 3, xp = q & 7;
                     uint8_t *to = smem + C::XF + a * C::XF_BYTES + (xp >> 2) * NT * 128;
                     uint32_t h[8];
@@ -520,11 +532,16 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         ok = !expires(p, SUMS) || __all_sync(0xffffffffu, bar_wait(&c.never, 0, abort_flag, p.expire_ns));
         // A tile's scales are asked for a tile ahead, lane l's token and channel l's (two loads,
         // one after the other, where rows are gathered).
-        float nx = 0.f, nw[2] = {0.f, 0.f};
+        constexpr int XL = C::EACH / 32;   // tokens of a lane
+        float nx[XL], nw[2] = {0.f, 0.f};
         auto enter = [&](int i, int t) {
             if (t >= total) return;
             const Tile next = nth_tile(i, t);
-            nx = lane < next.cnt - tok0 ? __ldg(p.x_s + source_row(p, next.row0 + tok0 + lane)) : 0.f;
+#pragma unroll
+            for (int q = 0; q < XL; ++q) {
+                const int l = tok0 + q * 32 + lane;
+                nx[q] = l < next.cnt ? __ldg(p.x_s + source_row(p, next.row0 + l)) : 0.f;
+            }
             const long long at = (long long)next.e * p.N + min(next.nt * ROWS + chan + lane, p.N - 1);
             nw[0] = __ldg(p.w_s[0] + at);
             if (MODE == GATEUP) nw[1] = __ldg(p.w_s[1] + at);
@@ -537,7 +554,8 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             const int cnt = tile.cnt - tok0;                     // the warp's tokens (none or less: nothing to do)
             const long long row0 = tile.row0 + tok0;
             __syncwarp();
-            sx[lane] = nx;
+#pragma unroll
+            for (int q = 0; q < XL; ++q) sx[q * 32 + lane] = nx[q];
             const float sw0 = nw[0], sw1 = nw[1];
             if constexpr (!FEW) { sw[0][lane] = sw0; sw[1][lane] = sw1; }
             __syncwarp();
@@ -832,15 +850,15 @@ bool make_map(CUtensorMap *m, CUtensorMapDataType type, const void *base, int n,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE, bool FEW, bool SPLIT>
+template <int MODE, int NT, bool SPLIT>
 cudaError_t launch_variant(const CUtensorMap &x, const CUtensorMap &w0, const CUtensorMap &w1, const CUtensorMap &out, const Params &p,
                            long long tiles, int num_sms, cudaStream_t stream)
 {
-    using C = Cfg<FEW, SPLIT>;
+    using C = Cfg<NT, SPLIT>;
     static PerDeviceFlag done;
     const int dev = current_device();
-    auto *kern = product_kernel<MODE, FEW, SPLIT>;
-    constexpr size_t smem = smem_bytes<FEW, SPLIT>();
+    auto *kern = product_kernel<MODE, NT, SPLIT>;
+    constexpr size_t smem = smem_bytes<NT, SPLIT>();
     if (!done.done(dev)) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
@@ -848,7 +866,7 @@ cudaError_t launch_variant(const CUtensorMap &x, const CUtensorMap &w0, const CU
     }
     if (SPLIT)
         return launch_pdl_cluster(kern, dim3((unsigned)(tiles * p.split)), dim3(C::THREADS), smem, stream, p.split, x, w0, w1, out, p);
-    const long long most = (long long)num_sms * (FEW ? 2 : 1);
+    const long long most = (long long)num_sms * (C::FEW ? 2 : 1);
     return launch_pdl(kern, dim3((unsigned)(tiles < most ? tiles : most)), dim3(C::THREADS), smem, stream, x, w0, w1, out, p);
 }
 
@@ -876,12 +894,12 @@ size_t tiled_workspace(int rows, int K) { return align_up((size_t)rows * K * 2, 
 
 template <int MODE> cudaError_t launch_tiled(const Params &args, void *workspace, cudaStream_t stream)
 {
-    using C = Cfg<false>;
+    constexpr int NT = 128;
     Params p = args;
     const int num_sms = device_sm_count();
     p.n_tiles = ceil_div(p.N, rows_of_mode(MODE));
     p.split = 1;
-    const long long tiles = most_tiles(p, C::NT);
+    const long long tiles = most_tiles(p, NT);
     if (tiles > 0x3fffffffLL) return cudaErrorInvalidValue;
     ConvertLayout l{0, 1};
     while (l.lanes_log2 < 8 && (1 << l.lanes_log2) < p.K / 16) ++l.lanes_log2;
@@ -893,7 +911,7 @@ template <int MODE> cudaError_t launch_tiled(const Params &args, void *workspace
                                      static_cast<uint4 *>(workspace));
     if (e != cudaSuccess) return e;
     CUtensorMap mx, mw0, mw1;
-    if (!make_map(&mx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, workspace, 0, p.rows, p.K, (long long)p.K * 2, 64, C::NT,
+    if (!make_map(&mx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, workspace, 0, p.rows, p.K, (long long)p.K * 2, 64, NT,
                   CU_TENSOR_MAP_SWIZZLE_128B) ||
         !weight_maps<MODE>(p, &mw0, &mw1))
         return cudaErrorInvalidValue;
@@ -901,38 +919,38 @@ template <int MODE> cudaError_t launch_tiled(const Params &args, void *workspace
     if (p.out_vec && !make_map(&mout, p.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.out, 0, p.rows,
                                p.N, p.ldo * (p.out_f32 ? 4 : 2), p.out_f32 ? 32 : 64, p.out_f32 ? 8 : 16, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
-    return launch_variant<MODE, false, false>(mx, mw0, mw1, mout, p, tiles, num_sms, stream);
+    return launch_variant<MODE, NT, false>(mx, mw0, mw1, mout, p, tiles, num_sms, stream);
 }
 
-template <int MODE> cudaError_t launch_few(const Params &args, cudaStream_t stream)
+template <int MODE> cudaError_t launch_few(const Params &args, int tokens, cudaStream_t stream)
 {
-    using C = Cfg<true>;
     Params p = args;
     const int num_sms = device_sm_count();
     p.n_tiles = ceil_div(p.N, rows_of_mode(MODE));
-    const long long tiles = most_tiles(p, C::NT);
+    const long long tiles = most_tiles(p, tokens);
     if (tiles > 0x3fffffffLL) return cudaErrorInvalidValue;
     // tiles for fewer than half the SMs: split the reduction over a CTA for each SM, at
     // most 8 a tile
     p.split = 1;
     const int KB = ceil_div(p.K, BK);
-    if (2 * tiles <= num_sms && KB >= 8) {
+    if (tokens == 32 && 2 * tiles <= num_sms && KB >= 8) {
         const long long each = num_sms / tiles;
         p.split = (int)(each < kMaxSplit ? each : kMaxSplit);
     }
     CUtensorMap mx, mw0, mw1;
-    if (!make_map(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.x_q, 0, p.x_rows, p.K, p.ldx, BK, p.perm_tok ? 1 : C::NT,
+    if (!make_map(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.x_q, 0, p.x_rows, p.K, p.ldx, BK, p.perm_tok ? 1 : tokens,
                   CU_TENSOR_MAP_SWIZZLE_128B) ||
         !weight_maps<MODE>(p, &mw0, &mw1))
         return cudaErrorInvalidValue;
-    return p.split > 1 ? launch_variant<MODE, true, true>(mx, mw0, mw1, mx, p, tiles, num_sms, stream)
-                       : launch_variant<MODE, true, false>(mx, mw0, mw1, mx, p, tiles, num_sms, stream);
+    if (tokens == 64) return launch_variant<MODE, 64, false>(mx, mw0, mw1, mx, p, tiles, num_sms, stream);
+    return p.split > 1 ? launch_variant<MODE, 32, true>(mx, mw0, mw1, mx, p, tiles, num_sms, stream)
+                       : launch_variant<MODE, 32, false>(mx, mw0, mw1, mx, p, tiles, num_sms, stream);
 }
 
 template cudaError_t launch_tiled<PRODUCT>(const Params &, void *, cudaStream_t);
 template cudaError_t launch_tiled<GATEUP>(const Params &, void *, cudaStream_t);
-template cudaError_t launch_few<PRODUCT>(const Params &, cudaStream_t);
-template cudaError_t launch_few<GATEUP>(const Params &, cudaStream_t);
+template cudaError_t launch_few<PRODUCT>(const Params &, int, cudaStream_t);
+template cudaError_t launch_few<GATEUP>(const Params &, int, cudaStream_t);
 
 }  // namespace i8
 }  // namespace moe

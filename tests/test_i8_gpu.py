@@ -472,6 +472,40 @@ def test_a_wait_that_expires(moe, T, K, N, E, gate_up, role):
     assert bool((out[cut[-1]:] == 7).all()) and moe.moe_check(st) == 0
 
 
+@pytest.mark.parametrize("T,E,d,F", [(512, 16, 2048, 2816), (128, 16, 2048, 2816), (20, 1, 8192, 2048), (6, 2, 8192, 4096), (1500, 16, 2048, 2816)])
+def test_weights_that_come_late(moe, T, E, d, F):
+    """Weights from HBM, larger than the L2 together, whose blocks may land out of order: the
+    converters of a block wait for that block.  Every call's outputs are the same, and those of
+    one call right."""
+    off, tok = groups(T, E, 1)
+    xq, xs = codes(T, d)
+    sets = [(codes(E, F, d, seed=i), codes(E, F, d, seed=i + 7)) for i in range(3)]
+    first = [None] * 3
+    for turn in range(30):
+        (gq, gs), (uq, us) = sets[turn % 3]
+        h = moe.moe_gate_up_i8(xq, xs, gq, gs, uq, us, offsets=off, perm_tok=tok)
+        y = moe.moe_grouped_gemm_i8(xq, xs, uq, us, off, perm_tok=tok)
+        if first[turn % 3] is None:
+            first[turn % 3] = (h, y)
+        assert torch.equal(h, first[turn % 3][0]) and torch.equal(y, first[turn % 3][1])
+    g, u = sets[0]
+    check_grouped(first[0][0], xq, xs, [g, u], off, tok)
+    check_grouped(first[0][1], xq, xs, [u], off, tok)
+
+
+@pytest.mark.parametrize("T,K,N", [(64, 2048, 5632), (700, 4096, 1024), (1000, 1536, 777), (2050, 2048, 640), (24, 4096, 2048),
+                                   (3000, 2048, 2048), (8, 8192, 1024)])
+def test_repeated_calls(moe, T, K, N):
+    """Calls back to back on fresh codes, each against 64 bits: a block that is read while the
+    next one lands, or before it has, shows in some of many."""
+    for turn in range(40):
+        (xq, xs), (wq, ws) = codes(T, K, seed=turn), codes(N, K, seed=turn + 1)
+        outs = [moe.moe_gemm_i8(xq, xs, wq, ws, out_dtype=torch.float32) for _ in range(4)]
+        ref, bound = product_ref(xq, wq, xs, ws)
+        for out in outs:
+            close(out, ref, bound)
+
+
 def test_two_calls_at_once(moe):
     """Two streams with calls of their own workspaces; one workspace shared by calls in order."""
     T, K, N = 700, 512, 640
