@@ -65,7 +65,7 @@ template <int MODE> cudaError_t launch_vector(const Params &p, cudaStream_t stre
 // in `workspace`), or of few rows
 size_t tiled_workspace(int rows, int K);
 template <int MODE> cudaError_t launch_tiled(const Params &p, void *workspace, cudaStream_t stream);
-template <int MODE> cudaError_t launch_few(const Params &p, int tokens, cudaStream_t stream);
+template <int MODE> cudaError_t launch_few(const Params &p, cudaStream_t stream);
 
 }  // namespace i8
 }  // namespace moe

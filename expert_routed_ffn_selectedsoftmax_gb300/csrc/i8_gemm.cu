@@ -57,13 +57,12 @@ template <int MODE> cudaError_t launch_product(const Params &p, void *workspace,
 #ifdef I8_FORCE
     const char *f = getenv("I8_FORCE");
     if (f && *f == 'v') return launch_vector<MODE>(p, stream);
-    if (f && *f == 'f') return launch_few<MODE>(p, 32, stream);
-    if (f && *f == 'g') return launch_few<MODE>(p, 64, stream);
+    if (f && *f == 'f') return launch_few<MODE>(p, stream);
     if (f && *f == 't' && p.rows > kFewRows) return launch_tiled<MODE>(p, workspace, stream);
 #endif
     const int experts = p.E < p.rows ? p.E : p.rows;
     if (p.expire_ns == 0 && vector_fits<MODE>(p, experts)) return launch_vector<MODE>(p, stream);   // (it has no waits)
-    if (few_rows_fit<MODE>(p, experts)) return launch_few<MODE>(p, 32, stream);
+    if (few_rows_fit<MODE>(p, experts)) return launch_few<MODE>(p, stream);
     return launch_tiled<MODE>(p, workspace, stream);
 }
 

@@ -13,8 +13,8 @@
 // nor shared memory.  Tokens are the columns:
 //   tiled     128 of them, as fp16 rows that convert_rows_kernel has written (in group
 //             order, so it gathers too), by TMA;
-//   few rows  32 or 64, read as int8 and widened into shared memory by the same warps; two
-//             CTAs an SM.  Few tiles split the reduction over a cluster, whose CTAs send their
+//   few rows  32, read as int8 and widened into shared memory by the same warps; two CTAs
+//             an SM.  Few tiles split the reduction over a cluster, whose CTAs send their
 //             partial sums to the one that finishes the token (distributed shared memory).
 // Accumulators are two, so a tile's output overlaps the next tile's products.
 //
@@ -56,20 +56,21 @@ constexpr size_t kPartial = (size_t)(32 + kMaxSplit) * M * 4;   // whole turns o
 // output channels of a tile
 constexpr int rows_of_mode(int mode) { return mode == GATEUP ? M / 2 : M; }
 
-// The kernels: NT tokens a tile; fewer than 128 are few rows; a split reduction with 32.
+// The kernels: NT tokens a tile, 128 or (few rows, whole or with a split reduction) 32.  (Tiles
+// of 64 tokens, which leave room for 3 blocks of weights and 2 converted, took 0.69 us a block
+// where 32 take 0.40.)
 template <int NT, bool SPLIT = false> struct Cfg {
     static constexpr bool FEW = NT < 128;
     static constexpr int X_BYTES = NT * BK * (FEW ? 1 : 2);
-    static constexpr int WS = SPLIT || NT == 64 ? 3 : 4;           // blocks of the weights' ring
-    static constexpr int NA = NT == 64 ? 2 : FEW ? 3 : 4;          // converted blocks in flight
-    static constexpr int XS = NT == 64 ? 3 : 4;                    // blocks of the tokens' ring (tiled: block a's
+    static constexpr int WS = SPLIT ? 3 : 4;                       // blocks of the weights' ring
+    static constexpr int NA = FEW ? 3 : 4;                         // converted blocks in flight
+    static constexpr int XS = 4;                                   // blocks of the tokens' ring (tiled: block a's
                                                                    // tokens are freed with its converted weights)
     static constexpr int XF_BYTES = FEW ? NT * BK * 2 : 0;         // widened tokens of a block
     static constexpr int A_COL = 2 * NT;                           // (two accumulators before)
     static constexpr int TMEM_COLS = FEW ? 256 : 512;
     static constexpr int MMAS = FEW ? 1 : 2;                       // multiplying warps, each with its share of the tokens
     static constexpr int EPI = FEW ? 4 : 16;                       // output warps
-    static constexpr int EACH = FEW ? NT : 32;                     // ... and the tokens of one
     static constexpr int THREADS = 128 + 32 * (EPI + kConvWarps);
     static constexpr size_t XRING = (size_t)WS * W_BYTES;
     static constexpr size_t XF = XRING + (size_t)XS * X_BYTES;
@@ -80,24 +81,24 @@ template <int NT, bool SPLIT = false> struct Cfg {
     static_assert(A_COL + NA * kBlockCols <= TMEM_COLS, "tensor memory");
     static_assert(WS >= NA && XS >= NA, "a converting group waits for a phase that the other has left");
     static_assert(FEW || XS == NA, "a tiled block's tokens and converted weights share an index");
-    static_assert(!SPLIT || NT == 32, "partial sums");
+    static_assert(NT == 128 || NT == 32, "an output warp has 32 tokens");
 };
 constexpr int kMaxRing = 4, kTable = 32;
 
-template <int EPI, int EACH> struct alignas(16) Ctl {
+template <int EPI> struct alignas(16) Ctl {
     uint64_t wfull[kMaxRing], wempty[kMaxRing], xfull[kMaxRing], xempty[kMaxRing], cfull[kMaxRing], cempty[kMaxRing];
     uint64_t dfull[2], dempty[2], drain[2];
     uint64_t never;                          // nothing arrives here (test hook)
     uint32_t tmem_base;
     int abort_flag;
-    alignas(16) float sx[EPI][EACH], sw[EPI][2][EPI == 4 ? 1 : 32];   // each output warp's scales: tokens', channels' (tiled)
+    alignas(16) float sx[EPI][32], sw[EPI][2][EPI == 4 ? 1 : 32];   // each output warp's scales: tokens', channels' (tiled)
     Groups g;
     Tile tiles[kTable];                      // this CTA's first tiles (each role asks for them in turn)
 };
-template <int NT> using CtlOf = Ctl<Cfg<NT>::EPI, Cfg<NT>::EACH>;
+template <int NT> using CtlOf = Ctl<Cfg<NT>::EPI>;
 template <int NT, bool SPLIT = false> constexpr size_t smem_bytes() { return 1024 + Cfg<NT, SPLIT>::CTL + sizeof(CtlOf<NT>); }
 static_assert(smem_bytes<128>() <= 232448, "shared memory per CTA");
-static_assert(smem_bytes<32>() <= 115712 && smem_bytes<64>() <= 115712 && smem_bytes<32, true>() <= 115712, "two CTAs per SM");
+static_assert(smem_bytes<32>() <= 115712 && smem_bytes<32, true>() <= 115712, "two CTAs per SM");
 // registers a thread after the split at start (setmaxnreg) of the tiled kernel: 28 warps
 // launch with 72 each, 2016; 4 x 40 + 8 x 56 + 16 x 88 = 2016
 constexpr int kRegsLaunch = 72, kRegsAux = 40, kRegsConv = 56, kRegsEpi = 88;
@@ -452,8 +453,8 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     } else if (warp >= 4 + C::EPI) {
         // ------------------------------------------------ convert
         if (!FEW) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
-        // A group takes every second block: a thread a weight row, and (few rows) pieces of the
-        // tokens.
+        // A group takes every second block: a thread a weight row, and (few rows) two pieces of
+        // the tokens.
         const int tid = (threadIdx.x - 128 - 32 * C::EPI) & 127, quad = warp & 3, row = quad * 32 + lane;
         const uint32_t mine = tmem + ((uint32_t)(quad * 32) << 16) + C::A_COL;
         const uint32_t turns = total > first ? (uint32_t)((total - first - 1) / stride + 1) * (uint32_t)(kb1 - kb0) : 0u;
@@ -494,7 +495,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             if (!ok) break;
             if (FEW) {
 #pragma unroll
-                for (int j = 0; j < NT / 16; ++j) {
+                for (int j = 0; j < 2; ++j) {
                     const int q = tid + j * 128, xr = q >> 3, xp = q & 7;
                     uint8_t *to = smem + C::XF + a * C::XF_BYTES + (xp >> 2) * NT * 128;
                     uint32_t h[8];
@@ -532,16 +533,11 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         ok = !expires(p, SUMS) || __all_sync(0xffffffffu, bar_wait(&c.never, 0, abort_flag, p.expire_ns));
         // A tile's scales are asked for a tile ahead, lane l's token and channel l's (two loads,
         // one after the other, where rows are gathered).
-        constexpr int XL = C::EACH / 32;   // tokens of a lane
-        float nx[XL], nw[2] = {0.f, 0.f};
+        float nx = 0.f, nw[2] = {0.f, 0.f};
         auto enter = [&](int i, int t) {
             if (t >= total) return;
             const Tile next = nth_tile(i, t);
-#pragma unroll
-            for (int q = 0; q < XL; ++q) {
-                const int l = tok0 + q * 32 + lane;
-                nx[q] = l < next.cnt ? __ldg(p.x_s + source_row(p, next.row0 + l)) : 0.f;
-            }
+            nx = tok0 + lane < next.cnt ? __ldg(p.x_s + source_row(p, next.row0 + tok0 + lane)) : 0.f;
             const long long at = (long long)next.e * p.N + min(next.nt * ROWS + chan + lane, p.N - 1);
             nw[0] = __ldg(p.w_s[0] + at);
             if (MODE == GATEUP) nw[1] = __ldg(p.w_s[1] + at);
@@ -554,8 +550,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             const int cnt = tile.cnt - tok0;                     // the warp's tokens (none or less: nothing to do)
             const long long row0 = tile.row0 + tok0;
             __syncwarp();
-#pragma unroll
-            for (int q = 0; q < XL; ++q) sx[q * 32 + lane] = nx[q];
+            sx[lane] = nx;
             const float sw0 = nw[0], sw1 = nw[1];
             if constexpr (!FEW) { sw[0][lane] = sw0; sw[1][lane] = sw1; }
             __syncwarp();
@@ -922,35 +917,35 @@ template <int MODE> cudaError_t launch_tiled(const Params &args, void *workspace
     return launch_variant<MODE, NT, false>(mx, mw0, mw1, mout, p, tiles, num_sms, stream);
 }
 
-template <int MODE> cudaError_t launch_few(const Params &args, int tokens, cudaStream_t stream)
+template <int MODE> cudaError_t launch_few(const Params &args, cudaStream_t stream)
 {
+    constexpr int NT = 32;
     Params p = args;
     const int num_sms = device_sm_count();
     p.n_tiles = ceil_div(p.N, rows_of_mode(MODE));
-    const long long tiles = most_tiles(p, tokens);
+    const long long tiles = most_tiles(p, NT);
     if (tiles > 0x3fffffffLL) return cudaErrorInvalidValue;
     // tiles for fewer than half the SMs: split the reduction over a CTA for each SM, at
     // most 8 a tile
     p.split = 1;
     const int KB = ceil_div(p.K, BK);
-    if (tokens == 32 && 2 * tiles <= num_sms && KB >= 8) {
+    if (2 * tiles <= num_sms && KB >= 8) {
         const long long each = num_sms / tiles;
         p.split = (int)(each < kMaxSplit ? each : kMaxSplit);
     }
     CUtensorMap mx, mw0, mw1;
-    if (!make_map(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.x_q, 0, p.x_rows, p.K, p.ldx, BK, p.perm_tok ? 1 : tokens,
+    if (!make_map(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.x_q, 0, p.x_rows, p.K, p.ldx, BK, p.perm_tok ? 1 : NT,
                   CU_TENSOR_MAP_SWIZZLE_128B) ||
         !weight_maps<MODE>(p, &mw0, &mw1))
         return cudaErrorInvalidValue;
-    if (tokens == 64) return launch_variant<MODE, 64, false>(mx, mw0, mw1, mx, p, tiles, num_sms, stream);
-    return p.split > 1 ? launch_variant<MODE, 32, true>(mx, mw0, mw1, mx, p, tiles, num_sms, stream)
-                       : launch_variant<MODE, 32, false>(mx, mw0, mw1, mx, p, tiles, num_sms, stream);
+    return p.split > 1 ? launch_variant<MODE, NT, true>(mx, mw0, mw1, mx, p, tiles, num_sms, stream)
+                       : launch_variant<MODE, NT, false>(mx, mw0, mw1, mx, p, tiles, num_sms, stream);
 }
 
 template cudaError_t launch_tiled<PRODUCT>(const Params &, void *, cudaStream_t);
 template cudaError_t launch_tiled<GATEUP>(const Params &, void *, cudaStream_t);
-template cudaError_t launch_few<PRODUCT>(const Params &, int, cudaStream_t);
-template cudaError_t launch_few<GATEUP>(const Params &, int, cudaStream_t);
+template cudaError_t launch_few<PRODUCT>(const Params &, cudaStream_t);
+template cudaError_t launch_few<GATEUP>(const Params &, cudaStream_t);
 
 }  // namespace i8
 }  // namespace moe
