@@ -2,9 +2,6 @@
 // channel: the calls, and which kernel takes them.
 //
 //   y[r,n] = (sum_i cx[r,i] cw[n,i]) sx[r] sw[n]
-#ifdef I8_FORCE
-#include <stdlib.h>
-#endif
 #include "i8.h"
 
 namespace moe {
@@ -54,12 +51,6 @@ template <int MODE> bool few_rows_fit(const Params &p, double experts)
 
 template <int MODE> cudaError_t launch_product(const Params &p, void *workspace, cudaStream_t stream)
 {
-#ifdef I8_FORCE
-    const char *f = getenv("I8_FORCE");
-    if (f && *f == 'v') return launch_vector<MODE>(p, stream);
-    if (f && *f == 'f') return launch_few<MODE>(p, stream);
-    if (f && *f == 't' && p.rows > kFewRows) return launch_tiled<MODE>(p, workspace, stream);
-#endif
     const int experts = p.E < p.rows ? p.E : p.rows;
     if (p.expire_ns == 0 && vector_fits<MODE>(p, experts)) return launch_vector<MODE>(p, stream);   // (it has no waits)
     if (few_rows_fit<MODE>(p, experts)) return launch_few<MODE>(p, stream);

@@ -19,7 +19,7 @@ namespace moe {
 namespace i8 {
 
 constexpr float kCodeMax = 127.0f;
-constexpr float kMinNormal = 1.17549435e-38f;   // 2^-126
+constexpr float kLeastTop = 0x1.fcp-120f;        // 127 * 2^-126: below, top / 127 rounds to less than 2^-126
 constexpr uint32_t kInfBits = 0x7f800000u;
 constexpr int kQuantThreads = 512;              // most of a CTA
 
@@ -71,35 +71,54 @@ template <> struct Raw8<__nv_bfloat16> {
 struct Factor {
     float hi, lo, top;   // 127 / max|x| = hi + lo; zeros for a row of zero codes
 };
-__device__ __forceinline__ Factor factor_of(uint32_t top_bits, float &scale)
+__device__ __forceinline__ Factor factor_of(uint32_t top_bits)
 {
     const float top = __uint_as_float(top_bits);
     Factor f{0.f, 0.f, top};
-    scale = top / kCodeMax;
-    if (top_bits >= kInfBits) {          // an infinity or a NaN: NaN scale, zero codes
-        scale = __uint_as_float(0x7fffffffu);
-    } else if (scale < kMinNormal) {     // (so that 127 / max|x| is finite)
-        scale = 0.f;
-    } else {
+    if (top_bits < kInfBits && top >= kLeastTop) {   // (so that 127 / max|x| is finite)
         f.hi = kCodeMax / top;
-        f.lo = fmaf(-f.hi, top, kCodeMax) / top;
+        // the remainder's quotient, to 2^-22 of itself: 1 / top is hi / 127
+        f.lo = fmaf(-f.hi, top, kCodeMax) * (f.hi * (1.0f / kCodeMax));
     }
     return f;
 }
-// The code in the low byte: adding 1.5 * 2^23 leaves the nearest whole number in the low
-// bits, ties to even (a conversion to int runs at a quarter of the rate).
-template <typename XT> __device__ __forceinline__ uint32_t code_of(float x, const Factor &f)
+__device__ __forceinline__ float scale_of(uint32_t top_bits)
 {
-    constexpr float kWhole = 12582912.0f;
+    const float top = __uint_as_float(top_bits);
+    if (top_bits >= kInfBits) return __uint_as_float(0x7fffffffu);   // an infinity or a NaN: NaN scale, zero codes
+    return top < kLeastTop ? 0.f : top / kCodeMax;
+}
+// Adding 1.5 * 2^23 leaves the nearest whole number in the low bits, ties to even (a
+// conversion to int runs at a quarter of the rate).
+constexpr float kWhole = 12582912.0f;
+__device__ __forceinline__ uint64_t pack2(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+// Two values' codes in the low bytes (two fp32 operations an instruction, each rounded as
+// alone).
+__device__ __forceinline__ void codes2(float x0, float x1, const Factor &f, uint32_t &c0, uint32_t &c1)
+{
+    const uint64_t x = pack2(x0, x1);
+    uint64_t t;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(x), "l"(pack2(f.lo, f.lo)));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(t) : "l"(x), "l"(pack2(f.hi, f.hi)));
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(t) : "l"(pack2(kWhole, kWhole)));
+    c0 = (uint32_t)t;
+    c1 = (uint32_t)(t >> 32);
+}
+// One fp32 value's code: near a tie, by both sides in 64 bits.
+__device__ __forceinline__ uint32_t code_of(float x, const Factor &f)
+{
     const float q = fmaf(x, f.hi, x * f.lo), t = q + kWhole;
     uint32_t c = __float_as_uint(t);
-    if (std::is_same<XT, float>::value) {
-        if (fabsf(q - (t - kWhole)) > 0.5f - 0x1p-15f) {
-            const float low = floorf(fabsf(q));
-            const double left = 127.0 * (double)fabsf(x), right = ((double)low + 0.5) * (double)f.top;
-            const int l = (int)low, n = left > right ? l + 1 : left < right ? l : l + (l & 1);
-            c = (uint32_t)(x < 0.f ? -n : n);
-        }
+    if (fabsf(q - (t - kWhole)) > 0.5f - 0x1p-15f) {
+        const float low = floorf(fabsf(q));
+        const double left = 127.0 * (double)fabsf(x), right = ((double)low + 0.5) * (double)f.top;
+        const int l = (int)low, n = left > right ? l + 1 : left < right ? l : l + (l & 1);
+        c = (uint32_t)(x < 0.f ? -n : n);
     }
     return c;
 }
@@ -109,25 +128,30 @@ template <typename XT> __device__ __forceinline__ uint2 codes_of(const Raw8<XT> 
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         uint32_t c[4];
+        if constexpr (std::is_same<XT, float>::value) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = code_of<XT>(r.get(4 * h + i), f);
+            for (int i = 0; i < 4; ++i) c[i] = code_of(r.get(4 * h + i), f);
+        } else {
+            codes2(r.get(4 * h), r.get(4 * h + 1), f, c[0], c[1]);
+            codes2(r.get(4 * h + 2), r.get(4 * h + 3), f, c[2], c[3]);
+        }
         w[h] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
     }
     // (zero codes, whatever the products of a row's infinities and NaN with 0 are)
     return f.hi == 0.f ? make_uint2(0u, 0u) : make_uint2(w[0], w[1]);
 }
 
-// `lanes` threads (a multiple of 32) to a row, NV chunks of 8 values each, all in
+// blockDim.x threads (a multiple of 32) to a row, NV chunks of 8 values each, all in
 // registers; rows wider than that (LONG) are read a second time.
 template <typename XT, int NV, bool LONG>
 __global__ void __launch_bounds__(kQuantThreads)
-quant_rows_kernel(const XT *__restrict__ x, long long rows, int cols, long long ldx, int lanes,
+quant_rows_kernel(const XT *__restrict__ x, long long rows, int cols, long long ldx,
                   uint8_t *__restrict__ codes, float *__restrict__ scales)
 {
     pdl_enter();
     __shared__ uint32_t part[kQuantThreads / 32];
-    const int group = threadIdx.x / lanes, lane = threadIdx.x - group * lanes;
-    const long long row = (long long)blockIdx.x * (blockDim.x / lanes) + group;
+    const int lanes = blockDim.x, lane = threadIdx.x;
+    const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
     const int chunks = cols / 8;
     Raw8<XT> r[NV];
     uint32_t m = 0u;
@@ -151,14 +175,14 @@ quant_rows_kernel(const XT *__restrict__ x, long long rows, int cols, long long 
     }
     m = __reduce_max_sync(0xffffffffu, m);
     if (lanes > 32) {   // (uniform over the CTA)
-        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+        const int n = lanes >> 5, l = lane & 31;
+        uint32_t *mine = part + threadIdx.y * n;
+        if (l == 0) mine[lane >> 5] = m;
         __syncthreads();
-        const int n = lanes >> 5, l = threadIdx.x & 31;
-        m = __reduce_max_sync(0xffffffffu, l < n ? part[group * n + l] : 0u);
+        m = __reduce_max_sync(0xffffffffu, l < n ? mine[l] : 0u);
     }
     if (row >= rows) return;
-    float scale;
-    const Factor f = factor_of(m, scale);
+    const Factor f = factor_of(m);
     uint8_t *o = codes + row * cols;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -173,7 +197,7 @@ quant_rows_kernel(const XT *__restrict__ x, long long rows, int cols, long long 
             *reinterpret_cast<uint2 *>(o + (long long)c * 8) = codes_of<XT>(v, f);
         }
     }
-    if (lane == 0) scales[row] = scale;
+    if (lane == 0) scales[row] = scale_of(m);
 }
 
 template <typename XT>
@@ -194,11 +218,10 @@ cudaError_t launch_quant(const void *x, int rows, int cols, long long ldx, uint8
         }
     }
     lanes = (int)align_up((size_t)(lanes < kQuantThreads ? lanes : kQuantThreads), 32);
-    const int nv = ceil_div(chunks, lanes), threads = lanes < 128 ? 128 / lanes * lanes : lanes;
-    const int per = threads / lanes;
+    const int nv = ceil_div(chunks, lanes), per = lanes < 128 ? 128 / lanes : 1;
     auto go = [&](auto kern) {
-        return launch_pdl(kern, dim3((unsigned)(((long long)rows + per - 1) / per)), dim3(threads), 0, s,
-                          static_cast<const XT *>(x), (long long)rows, cols, ldx, lanes, codes, scales);
+        return launch_pdl(kern, dim3((unsigned)(((long long)rows + per - 1) / per)), dim3(lanes, per), 0, s,
+                          static_cast<const XT *>(x), (long long)rows, cols, ldx, codes, scales);
     };
     if (nv <= 1) return go(quant_rows_kernel<XT, 1, false>);
     if (nv <= 2) return go(quant_rows_kernel<XT, 2, false>);

@@ -155,20 +155,24 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatil
     return mbar_test_wait(bar, parity) || fp8b::bar_wait(bar, parity, abort_flag, timeout_ns);
 }
 
-// 16 codes -> 16 fp16 values, in order: q ^ 0x80 = q + 128 in the significand of 1024,
-// minus 1152, both exact.
+// 4 codes -> 4 fp16 values, in order: q ^ 0x80 = q + 128 in the significand of 1024, minus
+// 1152, both exact.
+__device__ __forceinline__ void widen4(uint32_t v, uint32_t *o)
+{
+    const uint32_t w = v ^ 0x80808080u;
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));   // 1152
+    const uint32_t lo = __byte_perm(w, 0x64646464u, 0x4140), hi = __byte_perm(w, 0x64646464u, 0x4342);
+    const __half2 a = __hsub2(*reinterpret_cast<const __half2 *>(&lo), off);
+    const __half2 b = __hsub2(*reinterpret_cast<const __half2 *>(&hi), off);
+    o[0] = *reinterpret_cast<const uint32_t *>(&a);
+    o[1] = *reinterpret_cast<const uint32_t *>(&b);
+}
 __device__ __forceinline__ void widen16(const uint4 v, uint32_t *o)
 {
-    const uint32_t w[4] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u};
-    const __half2 off = __half2half2(__ushort_as_half(0x6480));   // 1152
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = __byte_perm(w[i], 0x64646464u, 0x4140), hi = __byte_perm(w[i], 0x64646464u, 0x4342);
-        const __half2 a = __hsub2(*reinterpret_cast<const __half2 *>(&lo), off);
-        const __half2 b = __hsub2(*reinterpret_cast<const __half2 *>(&hi), off);
-        o[2 * i] = *reinterpret_cast<const uint32_t *>(&a);
-        o[2 * i + 1] = *reinterpret_cast<const uint32_t *>(&b);
-    }
+    widen4(v.x, o);
+    widen4(v.y, o + 2);
+    widen4(v.z, o + 4);
+    widen4(v.w, o + 6);
 }
 __device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v)
 {
@@ -796,38 +800,29 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     }
 }
 
-// x's codes as fp16 rows in group order, 16 codes a thread of `kConvertRows` rows (all
-// asked for before the first is widened); a token index out of range gives a row of zeros.
-constexpr int kConvertThreads = 256, kConvertRows = 4;
+// x's codes as fp16 rows in group order, 8 codes a thread (16 bytes written: a warp's stores
+// are whole sectors); a token index out of range gives a row of zeros.  One piece a thread, and
+// as many threads as that takes: 192 rows of 2048 columns and their product 12.9 us (several
+// rows a thread, all asked for at once: 2 13.2, 4 14.1, 8 16.3), 8192 rows 126.4 (127.0, 127.1,
+// 131.2); 128 threads a CTA 132.0, as CTAs start too slowly.
+constexpr int kConvertThreads = 256;
 struct ConvertLayout { int lanes_log2, col_blocks; };   // threads of a CTA along a row, CTAs along it
 __global__ void __launch_bounds__(kConvertThreads)
 convert_rows_kernel(const Params p, const ConvertLayout l, uint4 *__restrict__ xf)
 {
     pdl_enter();
-    const int pieces = p.K / 16, lanes = 1 << l.lanes_log2, each = kConvertThreads >> l.lanes_log2;
+    const int pieces = p.K / 8, lanes = 1 << l.lanes_log2;
     const long long band = blockIdx.x / l.col_blocks;
     const int c = (int)(blockIdx.x - band * l.col_blocks) * lanes + (threadIdx.x & (lanes - 1));
-    const long long r0 = band * (kConvertRows * each) + (threadIdx.x >> l.lanes_log2);
-    if (c >= pieces) return;
-    uint4 v[kConvertRows];
-#pragma unroll
-    for (int u = 0; u < kConvertRows; ++u) {
-        const long long r = r0 + u * each;
-        v[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (r >= p.rows) continue;
-        const long long src = p.perm_tok ? __ldg(p.perm_tok + r) : r;
-        if (src >= 0 && src < p.x_rows) v[u] = __ldg(reinterpret_cast<const uint4 *>(p.x_q + src * p.ldx) + c);
-    }
-#pragma unroll
-    for (int u = 0; u < kConvertRows; ++u) {
-        const long long r = r0 + u * each;
-        if (r >= p.rows) continue;
-        uint32_t o[8];
-        widen16(v[u], o);
-        uint4 *to = xf + (r * pieces + c) * 2;
-        to[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        to[1] = make_uint4(o[4], o[5], o[6], o[7]);
-    }
+    const long long r = band * (kConvertThreads >> l.lanes_log2) + (threadIdx.x >> l.lanes_log2);
+    if (c >= pieces || r >= p.rows) return;
+    const long long src = p.perm_tok ? __ldg(p.perm_tok + r) : r;
+    uint2 v = make_uint2(0u, 0u);
+    if (src >= 0 && src < p.x_rows) v = __ldg(reinterpret_cast<const uint2 *>(p.x_q + src * p.ldx) + c);
+    uint32_t o[4];
+    widen4(v.x, o);
+    widen4(v.y, o + 2);
+    xf[r * pieces + c] = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // ------------------------------------------------------------------- host
@@ -897,10 +892,9 @@ template <int MODE> cudaError_t launch_tiled(const Params &args, void *workspace
     const long long tiles = most_tiles(p, NT);
     if (tiles > 0x3fffffffLL) return cudaErrorInvalidValue;
     ConvertLayout l{0, 1};
-    while (l.lanes_log2 < 8 && (1 << l.lanes_log2) < p.K / 16) ++l.lanes_log2;
-    l.col_blocks = ceil_div(p.K / 16, 1 << l.lanes_log2);
-    const int per = kConvertRows * (kConvertThreads >> l.lanes_log2);
-    const long long ctas = (long long)ceil_div(p.rows, per) * l.col_blocks;
+    while ((1 << l.lanes_log2) < kConvertThreads && (1 << l.lanes_log2) < p.K / 8) ++l.lanes_log2;
+    l.col_blocks = ceil_div(p.K / 8, 1 << l.lanes_log2);
+    const long long ctas = (long long)ceil_div(p.rows, kConvertThreads >> l.lanes_log2) * l.col_blocks;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
     const cudaError_t e = launch_pdl(convert_rows_kernel, dim3((unsigned)ctas), dim3(kConvertThreads), 0, stream, p, l,
                                      static_cast<uint4 *>(workspace));
