@@ -61,6 +61,29 @@ __device__ __forceinline__ void store_out(const Params &p, long long r, int n, f
 // i8_vector.cu -- products of a few rows per group on the CUDA cores
 template <int MODE> cudaError_t launch_vector(const Params &p, cudaStream_t stream);
 
+constexpr int kBlock = 128;    // columns of a block of a tensor-core kernel's reduction
+constexpr int kMaxSplit = 8;   // CTAs of a cluster that share a reduction
+
+// output channels of a tensor-core tile (its 128 weight rows are of W, or 64 of each of two)
+constexpr int channels_of_tile(int mode) { return mode == GATEUP ? 64 : 128; }
+
+// Most tiles of `tokens` rows there can be: an expert with r rows has (r - 1) / tokens + 1, so
+// as many experts as possible with rows, and the rest of the rows in whole tiles.
+inline long long most_tiles(int rows, int experts, int tokens)
+{
+    if (experts > rows) experts = rows;
+    return (long long)(rows - experts) / tokens + experts;
+}
+
+// Few rows: CTAs that share a tile's reduction.  Tiles for fewer than half the SMs get a CTA
+// for each SM, at most 8 a tile, where there are 8 blocks or more to share.
+inline int split_of(long long tiles, int blocks, int sms)
+{
+    if (2 * tiles > sms || blocks < 8) return 1;
+    const long long each = sms / tiles;
+    return (int)(each < kMaxSplit ? each : kMaxSplit);
+}
+
 // i8_tc.cu -- the products on the tensor cores: tiles of 128 rows (their codes as fp16
 // in `workspace`), or of few rows
 size_t tiled_workspace(int rows, int K);

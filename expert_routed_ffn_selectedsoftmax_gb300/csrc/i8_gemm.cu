@@ -24,28 +24,33 @@ template <int MODE> bool vector_fits(const Params &p, long long experts)
            (double)p.rows * p.N * p.K * (MODE == GATEUP ? 2 : 1) <= 6e7;
 }
 
-// Few rows or tiled, by what each is expected to take (us).  Blocks of 128 columns cost
-// the few-rows kernel 0.40 us where every tile has an SM, 0.62 where two share one, and 0.33
-// an SM beyond; the tiled kernel 0.41, on an eighth of the tiles or fewer, but it starts
-// later (its rows are widened first, at 3 bytes a code) and each tile's end shows.  The
-// groups' sizes are known on the device only: their last tiles are taken as half full.
-// Measured (few rows / tiled): 4096 x 4096 of 128 rows 16.4 / 20.0, 192: 23.3 / 19.8;
-// 2048 x 5632 of 192 14.2 / 14.6, 256: 19.4 / 15.0; 1024 x 1024 of 1024 9.0 / 11.8;
-// 8192 x 1024 of 512 28.6 / 31.1, 1024: 41.8 / 35.7; 64 experts of 2048 x 1024, rows per
-// expert 32: 35.3 / 42.3, 64: 51.9 / 45.2; 16 of 2816 x 2048, 24: 25.6 / 30.4, 64:
-// 37.1 / 33.1; gate/up, 64 of 1024 x 512, 32: 23.7 / 30.1, 64: 34.5 / 31.7.
-template <int MODE> bool few_rows_fit(const Params &p, double experts)
+// Few rows or tiled, by what each is expected to take (us).  The few-rows kernel takes
+// blocks of 128 columns in 0.39 us where every tile has an SM and 0.62 where two share one;
+// a split reduction has its share of the blocks and the exchange.  The tiled kernel takes
+// 0.335 and a tile's end 0.8, on an eighth of the tiles or fewer, but it starts later (its
+// rows are widened first).  A tile more than the SMs have places for is a round more; the
+// groups' sizes are known on the device only, so there their last tiles are taken as half
+// full and rounds as fractions.  Measured (few rows / tiled): 4096 x 4096 of 64 rows 13.6 /
+// 17.2, 128: 16.0 / 18.0, 192: 23.3 / 18.3; 2048 x 5632 of 128 13.6 / 12.7; 1024 x 1024 of
+// 1024 8.7 / 10.0, 2048: 14.4 / 10.9; 8192 x 1024 of 512 27.5 / 29.3, 1024: 42.1 / 30.7; 64
+// experts of 2048 x 1024, rows per expert 16: 28.0 / 33.3, 32: 35.4 / 37.3, 47: 44.6 / 38.9;
+// 16 of 2816 x 2048, 24: 25.6 / 26.6, 40: 32.3 / 27.8; gate/up, 64 of 1024 x 512, 16: 18.0 /
+// 22.0, 64: 33.6 / 28.0; one of 2048 x 5632, 100 rows: 26.7 / 14.5.
+template <int MODE> bool few_rows_fit(const Params &p, int experts)
 {
     if (p.rows <= kFewRows) return true;
-    const double sms = device_sm_count(), blocks = ceil_div(p.K, 128), columns = ceil_div(p.N, MODE == GATEUP ? 64 : 128);
-    const auto tiles = [&](int tokens) {
-        if (experts == 1) return ceil_div(p.rows, tokens) * columns;
-        const double each = (double)p.rows / tokens + experts / 2;
-        return (each > experts ? each : experts) * columns;
+    const int sms = device_sm_count(), blocks = ceil_div(p.K, kBlock), columns = ceil_div(p.N, channels_of_tile(MODE));
+    const auto rounds = [&](int tokens, int places) {
+        if (experts == 1) return ceil((double)ceil_div(p.rows, tokens) * columns / places);
+        const double each = (double)p.rows / tokens + experts * 0.5;
+        const double r = (each > experts ? each : experts) * columns / places;
+        return r > 1 ? r : 1;
     };
-    const double f = tiles(32) / sms, t = tiles(128) / sms;
-    const double few = 3.5 + blocks * (f <= 1 ? 0.40 : f * 0.33 > 0.62 ? f * 0.33 : 0.62);
-    const double tiled = 7 + (double)p.rows * p.K * 6e-7 + (t > 1 ? t : 1) * (blocks * 0.41 + 0.8);
+    const int split = split_of(most_tiles(p.rows, experts, 32) * columns, blocks, sms);
+    const double few = split > 1 ? 6.5 + 0.39 * ceil_div(blocks, split)
+                     : rounds(32, sms) <= 1 ? 3.5 + 0.39 * blocks
+                                            : 3.5 + 0.62 * blocks * rounds(32, 2 * sms);
+    const double tiled = 6.3 + (double)p.rows * p.K * 3.4e-7 + rounds(128, sms) * (0.335 * blocks + 0.8);
     return few <= tiled;
 }
 

@@ -45,16 +45,12 @@ using fp8b::tma_load_3d;
 namespace {
 
 constexpr int M = 128;                       // weight rows of an MMA
-constexpr int BK = 128;                      // columns of a block of the reduction
+constexpr int BK = kBlock;
 constexpr int W_BYTES = M * BK;
 constexpr int kBlockCols = BK / 2;           // TMEM columns of a block's weights as fp16
 constexpr int kStaging = 2048;
 constexpr int kConvWarps = 8;                // two groups of four, which take the blocks in turn
-constexpr int kMaxSplit = 8;                 // CTAs of a cluster
 constexpr size_t kPartial = (size_t)(32 + kMaxSplit) * M * 4;   // whole turns of 32 tokens over the CTAs
-
-// output channels of a tile
-constexpr int rows_of_mode(int mode) { return mode == GATEUP ? M / 2 : M; }
 
 // The kernels: NT tokens a tile, 128 or (few rows, whole or with a split reduction) 32.  (Tiles
 // of 64 tokens, which leave room for 3 blocks of weights and 2 converted, took 0.69 us a block
@@ -304,7 +300,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
 {
     using C = Cfg<NT, SPLIT>;
     constexpr bool FEW = C::FEW;
-    constexpr int WS = C::WS, XS = C::XS, NA = C::NA, ROWS = rows_of_mode(MODE);
+    constexpr int WS = C::WS, XS = C::XS, NA = C::NA, ROWS = channels_of_tile(MODE);
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     auto &c = *reinterpret_cast<CtlOf<NT> *>(smem + C::CTL);
@@ -860,18 +856,10 @@ cudaError_t launch_variant(const CUtensorMap &x, const CUtensorMap &w0, const CU
     return launch_pdl(kern, dim3((unsigned)(tiles < most ? tiles : most)), dim3(C::THREADS), smem, stream, x, w0, w1, out, p);
 }
 
-// Most tiles there can be: an expert with r rows has (r - 1) / rows_per_tile + 1, so as
-// many experts as possible with rows, and the rest of the rows in whole tiles.
-long long most_tiles(const Params &p, int rows_per_tile)
-{
-    const long long experts = p.E < p.rows ? p.E : p.rows;
-    return ((p.rows - experts) / rows_per_tile + experts) * p.n_tiles;
-}
-
 template <int MODE> bool weight_maps(const Params &p, CUtensorMap *w0, CUtensorMap *w1)
 {
     const auto map = [&](CUtensorMap *m, const void *w) {
-        return make_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, p.E, p.N, p.K, p.K, BK, rows_of_mode(MODE), CU_TENSOR_MAP_SWIZZLE_128B);
+        return make_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, p.E, p.N, p.K, p.K, BK, channels_of_tile(MODE), CU_TENSOR_MAP_SWIZZLE_128B);
     };
     if (!map(w0, p.w[0])) return false;
     if (MODE != GATEUP) { *w1 = *w0; return true; }
@@ -887,9 +875,9 @@ template <int MODE> cudaError_t launch_tiled(const Params &args, void *workspace
     constexpr int NT = 128;
     Params p = args;
     const int num_sms = device_sm_count();
-    p.n_tiles = ceil_div(p.N, rows_of_mode(MODE));
+    p.n_tiles = ceil_div(p.N, channels_of_tile(MODE));
     p.split = 1;
-    const long long tiles = most_tiles(p, NT);
+    const long long tiles = most_tiles(p.rows, p.E, NT) * p.n_tiles;
     if (tiles > 0x3fffffffLL) return cudaErrorInvalidValue;
     ConvertLayout l{0, 1};
     while ((1 << l.lanes_log2) < kConvertThreads && (1 << l.lanes_log2) < p.K / 8) ++l.lanes_log2;
@@ -916,17 +904,10 @@ template <int MODE> cudaError_t launch_few(const Params &args, cudaStream_t stre
     constexpr int NT = 32;
     Params p = args;
     const int num_sms = device_sm_count();
-    p.n_tiles = ceil_div(p.N, rows_of_mode(MODE));
-    const long long tiles = most_tiles(p, NT);
+    p.n_tiles = ceil_div(p.N, channels_of_tile(MODE));
+    const long long tiles = most_tiles(p.rows, p.E, NT) * p.n_tiles;
     if (tiles > 0x3fffffffLL) return cudaErrorInvalidValue;
-    // tiles for fewer than half the SMs: split the reduction over a CTA for each SM, at
-    // most 8 a tile
-    p.split = 1;
-    const int KB = ceil_div(p.K, BK);
-    if (2 * tiles <= num_sms && KB >= 8) {
-        const long long each = num_sms / tiles;
-        p.split = (int)(each < kMaxSplit ? each : kMaxSplit);
-    }
+    p.split = split_of(tiles, ceil_div(p.K, BK), num_sms);
     CUtensorMap mx, mw0, mw1;
     if (!make_map(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.x_q, 0, p.x_rows, p.K, p.ldx, BK, p.perm_tok ? 1 : NT,
                   CU_TENSOR_MAP_SWIZZLE_128B) ||
