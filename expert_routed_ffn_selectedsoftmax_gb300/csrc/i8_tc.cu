@@ -73,7 +73,7 @@ template <int NT, bool SPLIT = false> struct Cfg {
     static constexpr size_t STAGING = XF + (size_t)NA * XF_BYTES;
     // (split: the CTAs' sums of this CTA's tokens; two CTAs an SM also let the next kernel of
     // the stream start beside this one)
-    static constexpr size_t CTL = STAGING + (SPLIT ? kPartial : FEW ? 2 * kStaging : EPI * kStaging / 2);
+    static constexpr size_t CTL = STAGING + (SPLIT ? kPartial : FEW ? 0 : EPI / 2 * kStaging);
     static_assert(A_COL + NA * kBlockCols <= TMEM_COLS, "tensor memory");
     static_assert(WS >= NA && XS >= NA, "a converting group waits for a phase that the other has left");
     static_assert(FEW || XS == NA, "a tiled block's tokens and converted weights share an index");
@@ -177,6 +177,12 @@ __device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v
 // The two halves of a barrier of all threads of the cluster (each warp converged).
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+// The block's weight row of TMEM lane 32 `quad` + `lane`.  Gate/up: lanes 0-15 of each warp are
+// gate rows, 16-31 the up rows of the same 16 channels.
+template <int MODE> __device__ __forceinline__ int weight_row(int quad, int lane)
+{
+    return MODE == GATEUP ? (lane >> 4) * 64 + quad * 16 + (lane & 15) : quad * 32 + lane;
+}
 __device__ __forceinline__ bool expires(const Params &p, Role role) { return p.expire_ns && p.expire_role == role; }
 // Byte offset of 16-byte piece c of row r in a tile of 128-byte rows (TMA's 128-byte swizzle).
 __device__ __forceinline__ int piece_at(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
@@ -230,8 +236,11 @@ __device__ __forceinline__ float finish(const Params &p, float a, float b, float
 
 // The warp's sums of COUNT tokens (a, and for gate/up b) of output channels n0 + lane:
 // scaled and stored.  `row`: the first token's output row; `cnt` of the tokens exist.
-// Rows on 16-byte boundaries are turned in registers so that a store covers 8 tokens x 64
-// bytes (fp32: 4 x 128) in pieces of 16; else a token at a time, an element a lane.
+// Gate/up: 16 channels, the upper lanes' (as 0-15) of other tokens, so row, cnt and sx are a
+// lane's own.
+// Rows on 16-byte boundaries are turned in registers so that a store covers whole sectors
+// (PRODUCT: 8 tokens x 64 bytes, fp32 4 x 128) in pieces of 16; else a token at a time, an
+// element a lane.
 template <int MODE, int COUNT>
 __device__ __forceinline__ void store_tokens(const Params &p, const uint32_t *a, const uint32_t *b, long long row, int cnt, int n0,
                                              int lane, const float *sx, float sw0, float sw1)
@@ -246,7 +255,7 @@ __device__ __forceinline__ void store_tokens(const Params &p, const uint32_t *a,
         float *o = static_cast<float *>(p.out) + (row + (lane & 3)) * p.ldo + n;
 #pragma unroll
         for (int q = 0; q < COUNT; q += 4) {
-            if (q >= cnt) break;
+            if (MODE == PRODUCT && q >= cnt) break;
             uint32_t w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) w[j] = __float_as_uint(value(q + j));
@@ -258,7 +267,7 @@ __device__ __forceinline__ void store_tokens(const Params &p, const uint32_t *a,
         __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + (row + (lane & 7)) * p.ldo + n;
 #pragma unroll
         for (int q = 0; q < COUNT; q += 8) {
-            if (q >= cnt) break;
+            if (MODE == PRODUCT && q >= cnt) break;
             uint32_t w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) w[j] = fp8b::bf16x2(value(q + 2 * j), value(q + 2 * j + 1));
@@ -455,7 +464,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         if (!FEW) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
         // A group takes every second block: a thread a weight row, and (few rows) two pieces of
         // the tokens.
-        const int tid = (threadIdx.x - 128 - 32 * C::EPI) & 127, quad = warp & 3, row = quad * 32 + lane;
+        const int tid = (threadIdx.x - 128 - 32 * C::EPI) & 127, quad = warp & 3, row = weight_row<MODE>(quad, lane);
         const uint32_t mine = tmem + ((uint32_t)(quad * 32) << 16) + C::A_COL;
         const uint32_t turns = total > first ? (uint32_t)((total - first - 1) / stride + 1) * (uint32_t)(kb1 - kb0) : 0u;
         ok = !expires(p, CONVERT) || __all_sync(0xffffffffu, bar_wait(&c.never, 0, abort_flag, p.expire_ns));
@@ -520,12 +529,11 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     } else {
         // ------------------------------------------------ output
         if (!FEW) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
-        // A warp has the 32 channels of its TMEM lanes and (tiled) 32 of the tokens.  GATEUP:
-        // lanes 0-63 are gate sums, 64-127 up sums of the same channels; the two warps of a
-        // channel exchange half of their tokens, and each finishes the other half.
+        // A warp has the channels of its 32 TMEM lanes (GATEUP: gate and up of 16) and (tiled)
+        // 32 of the tokens.
         const int ew = warp - 4, quarter = warp & 3, group = ew >> 2, tok0 = FEW ? 0 : group * 32;
-        const bool upper = MODE == GATEUP && quarter >= 2;
-        const int chan = (MODE == GATEUP ? quarter & 1 : quarter) * 32;
+        constexpr int CH = ROWS / 4;   // channels of a warp
+        const int chan = quarter * CH, cl = lane % CH;
         const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16) + tok0;
         float *sx = c.sx[ew];
         auto &sw = c.sw[ew];
@@ -538,11 +546,24 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             if (t >= total) return;
             const Tile next = nth_tile(i, t);
             nx = tok0 + lane < next.cnt ? __ldg(p.x_s + source_row(p, next.row0 + tok0 + lane)) : 0.f;
-            const long long at = (long long)next.e * p.N + min(next.nt * ROWS + chan + lane, p.N - 1);
+            const long long at = (long long)next.e * p.N + min(next.nt * ROWS + chan + cl, p.N - 1);
             nw[0] = __ldg(p.w_s[0] + at);
             if (MODE == GATEUP) nw[1] = __ldg(p.w_s[1] + at);
         };
         enter(0, first);
+        // 64 channels (from n) of the next 16 tokens (from `row`, `left` exist) out of the staging, by two warps
+        auto store_pair = [&](long long row, int n, int left, const uint8_t *st) {
+            if (p.out_vec && left >= 16) {
+                if ((quarter & 1) == 0 && lane == 0) {
+                    if (n < p.N) tma_store_2d(&tm_out, st, n, (int)row);
+                    bulk_commit();
+                }
+            } else if (left > 0) {
+                __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + row * p.ldo + n;
+                store_staged<__nv_bfloat16, 64, 16>(o, p.ldo, st, (quarter & 1) * 32 + lane, min(left, 16), p.N - n, p.out_vec);
+            }
+            __syncwarp();
+        };
         for (int t = first, i = 0; t < total; t += stride, ++i) {
             const Tile tile = nth_tile(i, t);
             const int db = i & 1, n0 = tile.nt * ROWS + chan;   // the warp's first channel
@@ -573,7 +594,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                 cluster_wait();
                 met = true;
                 // token l's sums go to CTA l % S, which finishes it: [token l / S][CTA][weight row]
-                uint32_t to = 0, at = (uint32_t)(quarter * 32 + lane) * 4 + rank * (M * 4);
+                uint32_t to = 0, at = (uint32_t)weight_row<MODE>(quarter, lane) * 4 + rank * (M * 4);
 #pragma unroll 1
                 for (int i0 = 0; i0 < cnt; i0 += 16) {
                     uint32_t v[16];
@@ -599,27 +620,17 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                     }
                     if (i0 + 16 >= cnt) done_reading();
                     if constexpr (MODE == GATEUP) {
-                        // (the lower warp finishes tokens 0-7 of the sixteen, the upper 8-15)
-                        uint32_t *box = reinterpret_cast<uint32_t *>(smem + C::STAGING) + quarter * 32 + lane;
-                        uint32_t own[8], got[8];
+                        // (the lower lanes finish tokens 0-7 of the sixteen, the upper 8-15)
+                        const bool upper = lane >= 16;
+                        uint32_t g[8], u[8];
 #pragma unroll
                         for (int q = 0; q < 8; ++q) {
-                            box[q * M] = upper ? v[q] : v[8 + q];
-                            own[q] = upper ? v[8 + q] : v[q];
-                        }
-                        group_barrier(group);
-                        const uint32_t *from = reinterpret_cast<uint32_t *>(smem + C::STAGING) + (quarter ^ 2) * 32 + lane;
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) got[q] = from[q * M];
-                        group_barrier(group);
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            const uint32_t g = upper ? got[q] : own[q];
-                            got[q] = upper ? own[q] : got[q];
-                            own[q] = g;
+                            const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? v[q] : v[8 + q], 16);
+                            g[q] = upper ? got : v[q];
+                            u[q] = upper ? v[8 + q] : got;
                         }
                         const int l = i0 + (upper ? 8 : 0);
-                        store_tokens<MODE, 8>(p, own, got, row0 + l, cnt - l, n0, lane, sx + l, sw0, sw1);
+                        store_tokens<MODE, 8>(p, g, u, row0 + l, cnt - l, n0, cl, sx + l, sw0, sw1);
                     } else {
                         store_tokens<MODE, 16>(p, v, v, row0 + i0, cnt - i0, n0, lane, sx + i0, sw0, sw1);
                     }
@@ -636,86 +647,75 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                 }
                 done_reading();
                 if (cnt <= 0) continue;
-                uint8_t *stg = smem + C::STAGING + group * 4 * (kStaging / 2);   // the group's
-                constexpr int J = MODE == GATEUP ? 2 : 4;                        // octets of tokens to finish
-                int l0 = 0;                                                      // the first of them
-                if constexpr (MODE == GATEUP) {
-                    // keep octets 0, 1 (upper: 2, 3), send the others: 16 values a thread, in two
-                    // turns through the group's 4 KB
-                    l0 = upper ? 16 : 0;
-                    uint4 *box = reinterpret_cast<uint4 *>(stg) + quarter * 32 + lane;
-                    const uint4 *from = reinterpret_cast<uint4 *>(stg) + (quarter ^ 2) * 32 + lane;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t *a = v + 16 * h;
-                        if (h) group_barrier(group);
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            box[j * 128] = upper ? make_uint4(a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3])
-                                                 : make_uint4(a[8 + 4 * j], a[9 + 4 * j], a[10 + 4 * j], a[11 + 4 * j]);
-                        group_barrier(group);
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const uint4 got = from[j * 128];
-                            const uint32_t w[4] = {got.x, got.y, got.z, got.w};
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                // a[4 j + q] becomes the gate's, a[8 + 4 j + q] the up's
-                                const uint32_t own = upper ? a[8 + 4 * j + q] : a[4 * j + q];
-                                a[4 * j + q] = upper ? w[q] : own;
-                                a[8 + 4 * j + q] = upper ? own : w[q];
-                            }
-                        }
-                    }
-                }
+                // Two warps' channels, staged in the pair's 2 KB as rows of 128 bytes; a warp's
+                // share of the values goes out by TMA where its tokens are all there.
+                const int pair = quarter >> 1, half = quarter & 1;
+                uint8_t *stg = smem + C::STAGING + group * 2 * kStaging, *st = stg + pair * kStaging;
+                constexpr int OCTETS = CH / 8;   // of the warp's channels
                 auto value = [&](int j, int f, int q) {   // octet of tokens, octet of channels, token of a pair
                     const int at = (f >> 1) * 16 + 4 * j + 2 * (f & 1) + q;
-                    return finish<MODE>(p, __uint_as_float(v[at]), __uint_as_float(v[MODE == GATEUP ? at + 8 : at]),
-                                        sx[l0 + 8 * j + 2 * (lane & 3) + q], sw[0][8 * f + (lane >> 2)], sw[1][8 * f + (lane >> 2)]);
+                    return finish<MODE>(p, __uint_as_float(v[at]), __uint_as_float(v[MODE == GATEUP ? at + 16 : at]),
+                                        sx[8 * j + 2 * (lane & 3) + q], sw[0][8 * f + (lane >> 2)], sw[1][8 * f + (lane >> 2)]);
                 };
-                const int rows = cnt - l0;   // (GATEUP's upper warps may have none)
+                // The staging's rows have left (read by the TMA stores of lanes 0, or by these
+                // warps): it may be written.  / It has been written.
+                auto staging_free = [&] {
+                    if (lane == 0) bulk_wait_read();
+                    group_barrier(group);
+                };
+                auto staged = [&] {
+                    fence_proxy_async_smem();
+                    group_barrier(group);
+                };
                 if (p.out_f32) {
-                    // the warp's 32 channels of 8 tokens at a time
-                    uint8_t *st = stg + quarter * (kStaging / 2);
-                    if (MODE == GATEUP) group_barrier(group);
+                    // 32 channels: of one warp and 8 tokens (PRODUCT), of two and 16 (each sends 8)
+                    constexpr int T = MODE == GATEUP ? 2 : 1;   // octets of tokens at a time
+                    uint8_t *own = st + half * (kStaging / 2);
+                    const int np = MODE == GATEUP ? n0 - half * 16 : n0;
 #pragma unroll
-                    for (int j = 0; j < J; ++j) {
-                        if (j * 8 >= rows) break;
-                        if (lane == 0) bulk_wait_read();
-                        __syncwarp();
+                    for (int j0 = 0; j0 < 4; j0 += T) {
+                        if (j0 * 8 >= cnt) break;   // (the group)
+                        if (MODE == GATEUP) {
+                            staging_free();
+                        } else {
+                            if (lane == 0) bulk_wait_read();
+                            __syncwarp();
+                        }
 #pragma unroll
-                        for (int f = 0; f < 4; ++f)
+                        for (int j = 0; j < T; ++j)
 #pragma unroll
-                            for (int q = 0; q < 2; ++q) {
-                                const int tr = 2 * (lane & 3) + q, ch = f * 8 + (lane >> 2);
-                                *reinterpret_cast<float *>(st + piece_at(tr, ch >> 2) + (ch & 3) * 4) = value(j, f, q);
-                            }
-                        if (p.out_vec && rows - j * 8 >= 8) {
+                            for (int f = 0; f < OCTETS; ++f)
+#pragma unroll
+                                for (int q = 0; q < 2; ++q) {
+                                    const int tr = 2 * (lane & 3) + q, ch = (MODE == GATEUP ? half * 16 : 0) + f * 8 + (lane >> 2);
+                                    uint8_t *to = MODE == GATEUP ? st + j * (kStaging / 2) : own;
+                                    *reinterpret_cast<float *>(to + piece_at(tr, ch >> 2) + (ch & 3) * 4) = value(j0 + j, f, q);
+                                }
+                        if (MODE == GATEUP) {
+                            staged();
+                        } else {
                             fence_proxy_async_smem();
                             __syncwarp();
+                        }
+                        const int t0 = j0 * 8 + (MODE == GATEUP ? half * 8 : 0), left = cnt - t0;
+                        if (p.out_vec && left >= 8) {
                             if (lane == 0) {
-                                if (n0 < p.N) tma_store_2d(&tm_out, st, n0, (int)row0 + l0 + j * 8);
+                                if (np < p.N) tma_store_2d(&tm_out, own, np, (int)row0 + t0);
                                 bulk_commit();
                             }
-                        } else {
-                            __syncwarp();
-                            float *o = static_cast<float *>(p.out) + (row0 + l0 + j * 8) * p.ldo + n0;
-                            store_staged<float, 32, 8>(o, p.ldo, st, lane, min(rows - j * 8, 8), p.N - n0, p.out_vec);
+                        } else if (left > 0) {
+                            float *o = static_cast<float *>(p.out) + (row0 + t0) * p.ldo + np;
+                            store_staged<float, 32, 8>(o, p.ldo, own, lane, min(left, 8), p.N - np, p.out_vec);
                         }
+                        __syncwarp();
                     }
-                    if (MODE == GATEUP) {   // (the group's next exchange: all four warps' stores have left)
-                        if (lane == 0) bulk_wait_read();
-                        group_barrier(group);
-                    }
-                } else {
-                    // two warps' 64 channels of 16 tokens at a time: 2 KB for each pair
-                    const int pair = quarter >> 1, half = quarter & 1, np = n0 - half * 32;
-                    uint8_t *st = stg + pair * kStaging;
+                } else if constexpr (MODE == PRODUCT) {
+                    // two warps' 64 channels of 16 tokens at a time
+                    const int np = n0 - half * 32;
 #pragma unroll
-                    for (int j0 = 0; j0 < J; j0 += 2) {
+                    for (int j0 = 0; j0 < 4; j0 += 2) {
                         if (j0 * 8 >= cnt) break;   // (the group)
-                        if (half == 0 && lane == 0) bulk_wait_read();
-                        group_barrier(group);
+                        staging_free();
 #pragma unroll
                         for (int j = j0; j < j0 + 2; ++j) {
                             uint32_t w[4];
@@ -723,24 +723,22 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                             for (int f = 0; f < 4; ++f) w[f] = fp8b::bf16x2(value(j, f, 0), value(j, f, 1));
                             store_frags(smem_u32(st + piece_at(8 * (j - j0) + (lane & 7), half * 4 + (lane >> 3))), w[0], w[1], w[2], w[3]);
                         }
-                        const int left = rows - j0 * 8;
-                        const bool tma = p.out_vec && left >= 16;
-                        if (tma) fence_proxy_async_smem();
-                        group_barrier(group);
-                        if (tma) {
-                            if (half == 0 && lane == 0) {
-                                if (np < p.N) tma_store_2d(&tm_out, st, np, (int)row0 + l0 + j0 * 8);
-                                bulk_commit();
-                            }
-                        } else if (left > 0) {
-                            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + (row0 + l0 + j0 * 8) * p.ldo + np;
-                            store_staged<__nv_bfloat16, 64, 16>(o, p.ldo, st, half * 32 + lane, min(left, 16), p.N - np, p.out_vec);
-                        }
+                        staged();
+                        store_pair(row0 + j0 * 8, np, cnt - j0 * 8, st);
                     }
-                    if (MODE == GATEUP) {
-                        if (half == 0 && lane == 0) bulk_wait_read();
-                        group_barrier(group);
+                } else {
+                    // four warps' 64 channels of all 32 tokens, 16 for each pair to send
+                    staging_free();
+#pragma unroll
+                    for (int j0 = 0; j0 < 4; j0 += 2) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) w[m] = fp8b::bf16x2(value(j0 + (m >> 1), m & 1, 0), value(j0 + (m >> 1), m & 1, 1));
+                        store_frags(smem_u32(stg + (j0 >> 1) * kStaging + piece_at(8 * (lane >> 4) + (lane & 7), quarter * 2 + ((lane >> 3) & 1))),
+                                    w[0], w[1], w[2], w[3]);
                     }
+                    staged();
+                    store_pair(row0 + pair * 16, n0 - chan, cnt - pair * 16, st);
                 }
             }
         }
