@@ -234,6 +234,25 @@ __device__ __forceinline__ float finish(const Params &p, float a, float b, float
     return p.out_f32 ? swiglu_accurate(g, u) : swiglu_fast(g, u);
 }
 
+// Two tokens' at once (two fp32 operations an instruction, each rounded as alone).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 r;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+template <int MODE>
+__device__ __forceinline__ float2 finish2(const Params &p, const uint32_t *a, const uint32_t *b, float2 sx, float sw0, float sw1)
+{
+    const float2 g = mul2(mul2(make_float2(__uint_as_float(a[0]), __uint_as_float(a[1])), sx), make_float2(sw0, sw0));
+    if (MODE == PRODUCT) return g;
+    const float2 u = mul2(mul2(make_float2(__uint_as_float(b[0]), __uint_as_float(b[1])), sx), make_float2(sw1, sw1));
+    return p.out_f32 ? make_float2(swiglu_accurate(g.x, u.x), swiglu_accurate(g.y, u.y))
+                     : make_float2(swiglu_fast(g.x, u.x), swiglu_fast(g.y, u.y));
+}
+
 // The warp's sums of COUNT tokens (a, and for gate/up b) of output channels n0 + lane:
 // scaled and stored.  `row`: the first token's output row; `cnt` of the tokens exist.
 // Gate/up: 16 channels, the upper lanes' (as 0-15) of other tokens, so row, cnt and sx are a
@@ -652,10 +671,14 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                 const int pair = quarter >> 1, half = quarter & 1;
                 uint8_t *stg = smem + C::STAGING + group * 2 * kStaging, *st = stg + pair * kStaging;
                 constexpr int OCTETS = CH / 8;   // of the warp's channels
-                auto value = [&](int j, int f, int q) {   // octet of tokens, octet of channels, token of a pair
-                    const int at = (f >> 1) * 16 + 4 * j + 2 * (f & 1) + q;
-                    return finish<MODE>(p, __uint_as_float(v[at]), __uint_as_float(v[MODE == GATEUP ? at + 16 : at]),
-                                        sx[8 * j + 2 * (lane & 3) + q], sw[0][8 * f + (lane >> 2)], sw[1][8 * f + (lane >> 2)]);
+                auto values = [&](int j, int f) {   // two tokens' of an octet of tokens, an octet of channels
+                    const uint32_t *a = v + (f >> 1) * 16 + 4 * j + 2 * (f & 1);
+                    return finish2<MODE>(p, a, MODE == GATEUP ? a + 16 : a, *reinterpret_cast<const float2 *>(sx + 8 * j + 2 * (lane & 3)),
+                                         sw[0][8 * f + (lane >> 2)], sw[1][8 * f + (lane >> 2)]);
+                };
+                auto packed = [&](int j, int f) {
+                    const float2 x = values(j, f);
+                    return fp8b::bf16x2(x.x, x.y);
                 };
                 // The staging's rows have left (read by the TMA stores of lanes 0, or by these
                 // warps): it may be written.  / It has been written.
@@ -684,13 +707,13 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
 #pragma unroll
                         for (int j = 0; j < T; ++j)
 #pragma unroll
-                            for (int f = 0; f < OCTETS; ++f)
-#pragma unroll
-                                for (int q = 0; q < 2; ++q) {
-                                    const int tr = 2 * (lane & 3) + q, ch = (MODE == GATEUP ? half * 16 : 0) + f * 8 + (lane >> 2);
-                                    uint8_t *to = MODE == GATEUP ? st + j * (kStaging / 2) : own;
-                                    *reinterpret_cast<float *>(to + piece_at(tr, ch >> 2) + (ch & 3) * 4) = value(j0 + j, f, q);
-                                }
+                            for (int f = 0; f < OCTETS; ++f) {
+                                const float2 x = values(j0 + j, f);
+                                const int tr = 2 * (lane & 3), ch = (MODE == GATEUP ? half * 16 : 0) + f * 8 + (lane >> 2);
+                                uint8_t *to = (MODE == GATEUP ? st + j * (kStaging / 2) : own) + (ch & 3) * 4;
+                                *reinterpret_cast<float *>(to + piece_at(tr, ch >> 2)) = x.x;
+                                *reinterpret_cast<float *>(to + piece_at(tr + 1, ch >> 2)) = x.y;
+                            }
                         if (MODE == GATEUP) {
                             staged();
                         } else {
@@ -720,7 +743,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                         for (int j = j0; j < j0 + 2; ++j) {
                             uint32_t w[4];
 #pragma unroll
-                            for (int f = 0; f < 4; ++f) w[f] = fp8b::bf16x2(value(j, f, 0), value(j, f, 1));
+                            for (int f = 0; f < 4; ++f) w[f] = packed(j, f);
                             store_frags(smem_u32(st + piece_at(8 * (j - j0) + (lane & 7), half * 4 + (lane >> 3))), w[0], w[1], w[2], w[3]);
                         }
                         staged();
@@ -733,7 +756,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                     for (int j0 = 0; j0 < 4; j0 += 2) {
                         uint32_t w[4];
 #pragma unroll
-                        for (int m = 0; m < 4; ++m) w[m] = fp8b::bf16x2(value(j0 + (m >> 1), m & 1, 0), value(j0 + (m >> 1), m & 1, 1));
+                        for (int m = 0; m < 4; ++m) w[m] = packed(j0 + (m >> 1), m & 1);
                         store_frags(smem_u32(stg + (j0 >> 1) * kStaging + piece_at(8 * (lane >> 4) + (lane & 7), quarter * 2 + ((lane >> 3) & 1))),
                                     w[0], w[1], w[2], w[3]);
                     }
