@@ -527,3 +527,87 @@ def test_two_calls_at_once(moe):
     a = moe.moe_gemm_i8(xq, xs, wq, ws, workspace=shared)
     b = moe.moe_gemm_i8(other, os_, wq, ws, workspace=shared)
     assert torch.equal(a, want) and torch.equal(b, moe.moe_gemm_i8(other, os_, wq, ws))
+
+
+def tiled_scratch(moe, rows, K):
+    """A workspace whose bytes tell whether a call wrote it: the 128-token tiles' kernel does."""
+    return torch.full((moe.moe_i8_workspace_size(rows, K),), 0xA5, dtype=torch.uint8, device=DEV)
+
+
+@pytest.mark.parametrize("odt", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [1057, 1100, 1169])          # last tiles of 33, 76 and 17 tokens
+@pytest.mark.parametrize("off,N,wide", [(0, 640, 640), (0, 600, 648), (8, 584, 616), (1, 577, 700), (3, 517, 540)])
+def test_tiled_outputs(moe, odt, T, off, N, wide):
+    """128-token tiles: output rows that go out whole, that end inside a tile, and that lie on
+    any boundary of their type; x rows apart; what lies beside the output stays."""
+    K = 3088
+    big, xs = codes(T, 3200)
+    xq = big[:, 48:48 + K]
+    (wq, ws), (uq, us) = codes(N, K, seed=1), codes(N, K, seed=2)
+    base = torch.full((T, wide), 7.0, device=DEV, dtype=DT[odt])
+    out = base[:, off:off + N]
+    y, u = product_ref(xq, wq, xs, ws), product_ref(xq, uq, xs, us)
+    for gate_up in (False, True):
+        base.fill_(7.0)
+        scratch = tiled_scratch(moe, T, K)
+        if gate_up:
+            moe.moe_gate_up_i8(xq, xs, wq, ws, uq, us, h=out, workspace=scratch)
+            close(out, *swiglu_ref(*y, *u, odt == "f32"))
+        else:
+            moe.moe_gemm_i8(xq, xs, wq, ws, out=out, workspace=scratch)
+            close(out, *y)
+        assert bool((base[:, :off] == 7).all()) and bool((base[:, off + N:] == 7).all())
+        assert not bool((scratch == 0xA5).all())
+
+
+@pytest.mark.parametrize("odt", ["f32", "bf16"])
+@pytest.mark.parametrize("gate_up", [False, True])
+@pytest.mark.parametrize("sizes,N", [([700, 0, 1, 129, 128, 17, 400], 777), ([0, 0, 1500], 777), ([33, 1000, 5, 6], 1000)])
+def test_tiled_groups(moe, odt, gate_up, sizes, N):
+    """128-token tiles of ragged groups, gathered from tokens named more than once; grouped rows
+    behind the last group stay."""
+    K, x_rows, E = 2064, 500, len(sizes)
+    (xq, xs), (wq, ws), (uq, us) = codes(x_rows, K), codes(E, N, K, seed=1), codes(E, N, K, seed=2)
+    off = torch.tensor([0] + sizes, device=DEV).cumsum(0).int()
+    used = sum(sizes)
+    rows = used + 50
+    tok = torch.randint(0, x_rows, (rows,), device=DEV, dtype=torch.int32)
+    out = torch.full((rows, N), 7.0, device=DEV, dtype=DT[odt])
+    scratch = tiled_scratch(moe, rows, K)
+    if gate_up:
+        moe.moe_gate_up_i8(xq, xs, wq, ws, uq, us, offsets=off, perm_tok=tok, h=out, workspace=scratch)
+    else:
+        moe.moe_grouped_gemm_i8(xq, xs, wq, ws, off, perm_tok=tok, out=out, workspace=scratch)
+    check_grouped(out, xq, xs, [(wq, ws), (uq, us)] if gate_up else [(wq, ws)], off, tok)
+    assert bool((out[used:] == 7).all()) and not bool((scratch == 0xA5).all())
+
+
+def test_two_tiled_calls_at_once(moe):
+    """128-token tiles on two streams and as two captured graphs replayed side by side, each
+    call with a workspace of its own."""
+    T, K, N = 700, 4096, 1024
+    sets = [(codes(T, K, seed=i), codes(N, K, seed=i + 1)) for i in range(2)]
+    scratch = [tiled_scratch(moe, T, K) for _ in sets]
+    want = [moe.moe_gemm_i8(*x, *w) for x, w in sets]
+    outs = [torch.empty_like(v) for v in want]
+    calls = [lambda i=i: moe.moe_gemm_i8(*sets[i][0], *sets[i][1], out=outs[i], workspace=scratch[i]) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in sets]
+    graphs = []
+    for call in calls:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            for _ in range(4):
+                call()
+    for run in (calls, [g.replay for g in graphs]):
+        for o in outs:
+            o.zero_()
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+        for _ in range(6):
+            for i, s in enumerate(streams):
+                with torch.cuda.stream(s):
+                    run[i]()
+        for s in streams:
+            torch.cuda.current_stream().wait_stream(s)
+        assert all(torch.equal(o, v) for o, v in zip(outs, want))
+    assert all(not bool((s == 0xA5).all()) for s in scratch)
