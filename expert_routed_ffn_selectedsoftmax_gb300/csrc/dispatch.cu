@@ -9,8 +9,12 @@
 //
 // All of them go by tokens: a token's row is read (or written) once and its k
 // grouped rows are found through inv, so each byte moves once and nothing needs an
-// atomic.  A thread holds 8 columns of its token and asks for the k rows' at once.  What bounds them is memory.  Sums run over the
-// slots in order, in fp32, and are rounded once.
+// atomic.  A thread holds 8 columns of its token and asks for the k rows' at once.  Sums run
+// over the slots in order, in fp32, and are rounded once.
+//
+// What bounds them is memory.  16384 tokens x 2 of 2048 bf16 columns (us, of the measured copy
+// rate): dispatch 30.6, 99 %; its gradient 36.0, 84 %; combine 39.5, 77 %; its gradients 53.7,
+// 94 %.  Few tokens are latency: combine of 128 x 2 of 1024 takes 1.7.
 #include <type_traits>
 
 #include "common.cuh"
@@ -459,8 +463,8 @@ template <int WAY> using WayOf = std::integral_constant<int, WAY>;
 template <typename XT, typename OT, int WAY, bool WEIGHTED>
 moe_status launch_gather_sum(Args a, cudaStream_t s)
 {
-    // Many tokens: about 64 bytes in flight a thread (16384 x 2 x 2048 in bf16: one chunk a
-    // thread 44 us, two 35); few: a chunk a thread and its rows at once, as that is latency.
+    // Many tokens: about 64 bytes in flight a thread (combine of 16384 x 2 x 2048 in bf16: one
+    // chunk a thread 44 us, two 39.5); few: a chunk a thread and its rows at once, as that is latency.
     const bool many = (long long)a.T * (a.d / V) >= 2LL * kThreads * 8 * device_sm_count();
     constexpr int kTwice = sizeof(XT) == 4 ? 1 : 2;   // (fp32 chunks are twice as long)
     const auto go = [&](auto kern, int each) {

@@ -12,10 +12,10 @@ constexpr int kFewRows = 32;   // up to here no call takes the tiled kernel, and
 // The CUDA-core kernel: one or two rows, or up to 32 with at most 8 a group and 6e7
 // products.  It starts without barriers, tensor maps and TMEM, but a row costs it a pass of
 // dot products where the tensor cores take 32 at once.  us a call (here / few rows):
-// 2048 x 5632 of 1 token 4.4 / 7.1, 4: 6.6 / 7.3, 8: 9.1 / 7.6; 1024 x 1024 of 8 2.5 / 3.7;
-// 8192 x 8192 of 1 14.6 / 17.8, 4: 19.1 / 18.1; 8 rows over 16 experts of 2816 x 2048
-// 12.6 / 13.1, 64 over 64 of 512 x 1024 10.0 / 8.3; gate/up of 16 tokens x 2 over 64
-// experts of 1024 x 512 8.5 / 10.2, of 64 rows 14.2 / 10.9.
+// 2048 x 5632 of 1 token 4.4 / 6.9, 4: 6.6 / 7.2, 8: 9.1 / 7.5; 1024 x 1024 of 8 2.5 / 3.7;
+// 8192 x 8192 of 1 14.5 / 18.3, 4: 19.0 / 18.7; 8 rows over 16 experts of 2816 x 2048
+// 11.3 / 13.4, 64 over 64 of 512 x 1024 11.5 / 8.3; gate/up of 16 tokens x 2 over 64
+// experts of 1024 x 512 8.3 / 9.7, of 64 rows 16.4 / 10.8.
 template <int MODE> bool vector_fits(const Params &p, long long experts)
 {
     if (p.K >= 131072) return false;   // (its sums are 32-bit whole numbers)
@@ -26,13 +26,14 @@ template <int MODE> bool vector_fits(const Params &p, long long experts)
 
 // Few rows or tiled, by what each is expected to take (us).  The few-rows kernel takes
 // blocks of 128 columns in 0.39 us where every tile has an SM and 0.62 where two share one;
-// a split reduction has its share of the blocks and the exchange.  The tiled kernel takes
-// 0.335 and a tile's end 0.8, on an eighth of the tiles or fewer, but it starts later (its
-// rows are widened first).  A tile more than the SMs have places for is a round more; the
-// groups' sizes are known on the device only, so there their last tiles are taken as half
-// full and rounds as fractions.  Measured (few rows / tiled): 4096 x 4096 of 64 rows 13.6 /
-// 17.2, 128: 16.0 / 18.0, 192: 23.3 / 18.3; 2048 x 5632 of 128 13.6 / 12.7; 1024 x 1024 of
-// 1024 8.7 / 10.0, 2048: 14.4 / 10.9; 8192 x 1024 of 512 27.5 / 29.3, 1024: 42.1 / 30.7; 64
+// the tiled kernel takes 0.335 and a tile's end 0.8, on an eighth of the tiles or fewer, but
+// it starts later (its rows are widened first).  Where a reduction is split, a CTA has its
+// share of the blocks, and its cluster's meeting.  A tile more than the SMs have places for is
+// a round more; the groups' sizes are known on the device only, so there their last tiles are
+// taken as half full and rounds as fractions.
+// Measured (few rows / tiled): 4096 x 4096 of 64 rows 13.6 / 12.6, 128: 16.0 / 14.1, 300:
+// 33.0 / 19.1; 2048 x 5632 of 128 13.6 / 12.7; 1024 x 1024 of 1024 8.8 / 9.9, 2048: 14.4 / 10.9;
+// 2048 x 2048 of 128 10.0 / 12.1; 8192 x 1024 of 256 18.6 / 15.7, 1024: 42.0 / 25.3; 64
 // experts of 2048 x 1024, rows per expert 16: 28.0 / 33.3, 32: 35.4 / 37.3, 47: 44.6 / 38.9;
 // 16 of 2816 x 2048, 24: 25.6 / 26.6, 40: 32.3 / 27.8; gate/up, 64 of 1024 x 512, 16: 18.0 /
 // 22.0, 64: 33.6 / 28.0; one of 2048 x 5632, 100 rows: 26.7 / 14.5.
@@ -50,7 +51,9 @@ template <int MODE> bool few_rows_fit(const Params &p, int experts)
     const double few = split > 1 ? 6.5 + 0.39 * ceil_div(blocks, split)
                      : rounds(32, sms) <= 1 ? 3.5 + 0.39 * blocks
                                             : 3.5 + 0.62 * blocks * rounds(32, 2 * sms);
-    const double tiled = 6.3 + (double)p.rows * p.K * 3.4e-7 + rounds(128, sms) * (0.335 * blocks + 0.8);
+    const int tiled_split = split_of_tiled<MODE>(most_tiles(p.rows, experts, 128) * columns, blocks);
+    const double tiled = 6.3 + (double)p.rows * p.K * 3.4e-7 +
+                         (tiled_split > 1 ? 5 + 0.335 * ceil_div(blocks, tiled_split) : rounds(128, sms) * (0.335 * blocks + 0.8));
     return few <= tiled;
 }
 

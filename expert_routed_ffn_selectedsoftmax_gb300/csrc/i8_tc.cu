@@ -7,23 +7,35 @@
 // in fp32, so the sums run on kind::f16 and are whole numbers, exact up to 2^24.
 //
 // Weights are the MMA's 128 rows (PRODUCT: of W; GATEUP: 64 of W_gate and the same 64 of
-// W_up).  They are read as int8 (TMA), and converter warps -- one TMEM lane, that is one
+// W_up, 16 of each to the lanes of a warp, so that the warp that writes a channel has both of
+// its sums).  They are read as int8 (TMA), and converter warps -- one TMEM lane, that is one
 // weight row, to a thread -- widen 128 codes of it at a time to fp16 and store them into
 // tensor memory, where the MMA takes its A operand: the widened weights touch neither HBM
 // nor shared memory.  Tokens are the columns:
 //   tiled     128 of them, as fp16 rows that convert_rows_kernel has written (in group
-//             order, so it gathers too), by TMA;
+//             order, so it gathers too), by TMA; one CTA an SM;
 //   few rows  32, read as int8 and widened into shared memory by the same warps; two CTAs
-//             an SM.  Few tiles split the reduction over a cluster, whose CTAs send their
-//             partial sums to the one that finishes the token (distributed shared memory).
-// Accumulators are two, so a tile's output overlaps the next tile's products.
+//             an SM.
+// Accumulators are two, so a tile's output overlaps the next tile's products.  Few tiles
+// split the reduction over a cluster, whose CTAs send their partial sums to the one that
+// finishes the token (distributed shared memory).
 //
 // Warp 0 loads weights, warp 3 tokens (one warp for both issued its loads in 930 clocks a
-// block of 128 columns' 256 x 64, where the MMAs take 512), warp 1 multiplies, the last 8
-// warps convert, four of them a block in turn, and warps 4.. (4 or 16) write the output.
+// block of 128 columns' 256 x 64, where the MMAs take 512), warp 1 (tiled: 1 and 2, 64 tokens
+// each, 128 us for 8192 x 2048 x 5632 and 141 with one) multiplies, the last 8 warps convert,
+// four of them a block in turn, and warps 4.. (4 or 16) write the output.
+//
+// What bounds it (us, one GB300).  Few rows: the weights' bytes once it runs, and its start and
+// end.  Gate/up of 64 experts of 1024 x 512 and 128 x 2 rows takes 16.4; each further block of
+// 128 columns adds 1.31, which is 6.4 TB/s, and 6 do not depend on K.  Tiled: the MMAs, and
+// what they share the SM with.  8192 x 2048 x 5632 takes 128 (1.47 PFLOP/s, 78 % of the
+// measured fp16 rate): without the converters' work it takes 120, without the output 120,
+// without the tokens' loads 119, and with the MMAs alone 102.  The tensor pipe is busy for
+// 72 % of the cycles, and the L2 is at 68 % of its rate.
 //
 // Every wait is bounded (2 s).  Where one gives up, the rows of the CTA's remaining
 // tiles are written as NaN, and the status word says so if the caller passed one.
+#include <atomic>
 #include <type_traits>
 
 #include "fp8b_tc.cuh"
@@ -50,7 +62,9 @@ constexpr int W_BYTES = M * BK;
 constexpr int kBlockCols = BK / 2;           // TMEM columns of a block's weights as fp16
 constexpr int kStaging = 2048;
 constexpr int kConvWarps = 8;                // two groups of four, which take the blocks in turn
-constexpr size_t kPartial = (size_t)(32 + kMaxSplit) * M * 4;   // whole turns of 32 tokens over the CTAs
+// a CTA's share of a tile's tokens, with the sums of every CTA that splits the reduction (few
+// rows: whole turns of the tokens over the CTAs)
+constexpr size_t partial_bytes(int tokens) { return (size_t)(tokens + kMaxSplit) * M * 4; }
 
 // The kernels: NT tokens a tile, 128 or (few rows, whole or with a split reduction) 32.  (Tiles
 // of 64 tokens, which leave room for 3 blocks of weights and 2 converted, took 0.69 us a block
@@ -58,7 +72,7 @@ constexpr size_t kPartial = (size_t)(32 + kMaxSplit) * M * 4;   // whole turns o
 template <int NT, bool SPLIT = false> struct Cfg {
     static constexpr bool FEW = NT < 128;
     static constexpr int X_BYTES = NT * BK * (FEW ? 1 : 2);
-    static constexpr int WS = SPLIT ? 3 : 4;                       // blocks of the weights' ring
+    static constexpr int WS = FEW && SPLIT ? 3 : 4;                       // blocks of the weights' ring
     static constexpr int NA = FEW ? 3 : 4;                         // converted blocks in flight
     static constexpr int XS = 4;                                   // blocks of the tokens' ring (tiled: block a's
                                                                    // tokens are freed with its converted weights)
@@ -71,9 +85,12 @@ template <int NT, bool SPLIT = false> struct Cfg {
     static constexpr size_t XRING = (size_t)WS * W_BYTES;
     static constexpr size_t XF = XRING + (size_t)XS * X_BYTES;
     static constexpr size_t STAGING = XF + (size_t)NA * XF_BYTES;
-    // (split: the CTAs' sums of this CTA's tokens; two CTAs an SM also let the next kernel of
-    // the stream start beside this one)
-    static constexpr size_t CTL = STAGING + (SPLIT ? kPartial : FEW ? 0 : EPI / 2 * kStaging);
+    // split: the CTAs' sums of this CTA's tokens, sent as soon as each has them (few rows) or
+    // into the rings when all have (tiled).  (Two CTAs an SM also let the next kernel of the
+    // stream start beside this one.)
+    static constexpr size_t PARTIAL = FEW ? STAGING : 0;
+    static constexpr size_t CTL = STAGING + (!FEW ? EPI / 2 * kStaging : SPLIT ? partial_bytes(NT) : 0);
+    static_assert(PARTIAL + partial_bytes(NT) <= (FEW ? PARTIAL + partial_bytes(NT) : STAGING), "the rings hold the sums");
     static_assert(A_COL + NA * kBlockCols <= TMEM_COLS, "tensor memory");
     static_assert(WS >= NA && XS >= NA, "a converting group waits for a phase that the other has left");
     static_assert(FEW || XS == NA, "a tiled block's tokens and converted weights share an index");
@@ -87,13 +104,14 @@ template <int EPI> struct alignas(16) Ctl {
     uint64_t never;                          // nothing arrives here (test hook)
     uint32_t tmem_base;
     int abort_flag;
+    uint32_t lost;                           // split: a CTA of the cluster has no sums to send
     alignas(16) float sx[EPI][32], sw[EPI][2][EPI == 4 ? 1 : 32];   // each output warp's scales: tokens', channels' (tiled)
     Groups g;
     Tile tiles[kTable];                      // this CTA's first tiles (each role asks for them in turn)
 };
 template <int NT> using CtlOf = Ctl<Cfg<NT>::EPI>;
 template <int NT, bool SPLIT = false> constexpr size_t smem_bytes() { return 1024 + Cfg<NT, SPLIT>::CTL + sizeof(CtlOf<NT>); }
-static_assert(smem_bytes<128>() <= 232448, "shared memory per CTA");
+static_assert(smem_bytes<128>() <= 232448 && smem_bytes<128, true>() <= 232448, "shared memory per CTA");
 static_assert(smem_bytes<32>() <= 115712 && smem_bytes<32, true>() <= 115712, "two CTAs per SM");
 // registers a thread after the split at start (setmaxnreg) of the tiled kernel: 28 warps
 // launch with 72 each, 2016; 4 x 40 + 8 x 56 + 16 x 88 = 2016
@@ -173,6 +191,11 @@ __device__ __forceinline__ void widen16(const uint4 v, uint32_t *o)
 __device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v)
 {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_v4(uint32_t cluster_addr, const uint32_t *v)
+{
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                 : "memory");
 }
 // The two halves of a barrier of all threads of the cluster (each warp converged).
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
@@ -343,6 +366,7 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         for (int w = 0; w < 2; ++w) mbar_init(&c.drain[w], 1);
         mbar_init(&c.never, 1);
         c.abort_flag = 0;
+        c.lost = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_x)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_w0)) : "memory");
@@ -374,10 +398,11 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         c.tiles[threadIdx.x] = tile_at(c.g, E, first + threadIdx.x * stride, NT);
     __syncthreads();
     if (!p.offsets) pdl_enter();
-    // (the CTAs of a cluster may write one another's memory once all have started)
-    if (SPLIT) cluster_arrive();
+    // (the CTAs of a cluster may write one another's memory once all have started; tiled: once
+    // all have their sums)
+    if (SPLIT && FEW) cluster_arrive();
     bool met = false;
-    uint8_t *partial = smem + C::STAGING;
+    uint8_t *partial = smem + C::PARTIAL;
     auto nth_tile = [&](int i, int t) { return i < kTable ? c.tiles[i] : tile_at(c.g, E, t, NT); };
     volatile int *abort_flag = &c.abort_flag;
     uint32_t issued = 0;   // blocks this warp has loaded or multiplied
@@ -610,20 +635,41 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                 __syncwarp();
             };
             if constexpr (SPLIT) {
-                cluster_wait();
-                met = true;
-                // token l's sums go to CTA l % S, which finishes it: [token l / S][CTA][weight row]
-                uint32_t to = 0, at = (uint32_t)weight_row<MODE>(quarter, lane) * 4 + rank * (M * 4);
+                if constexpr (FEW) {
+                    cluster_wait();
+                    met = true;
+                    // token l's sums go to CTA l % S, which finishes it: [token l / S][CTA][weight row]
+                    uint32_t to = 0, at = (uint32_t)weight_row<MODE>(quarter, lane) * 4 + rank * (M * 4);
 #pragma unroll 1
-                for (int i0 = 0; i0 < cnt; i0 += 16) {
-                    uint32_t v[16];
-                    __syncwarp();
-                    if (ok) tmem_ld16_wait(d + i0, v);
+                    for (int i0 = 0; i0 < cnt; i0 += 16) {
+                        uint32_t v[16];
+                        __syncwarp();
+                        if (ok) tmem_ld16_wait(d + i0, v);
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) {
-                        if (i0 + q < cnt) st_cluster_u32(peer_addr(partial, to) + at, ok ? v[q] : 0x7fffffffu);
-                        if (++to == S) { to = 0; at += S * M * 4; }
+                        for (int q = 0; q < 16; ++q) {
+                            if (i0 + q < cnt) st_cluster_u32(peer_addr(partial, to) + at, ok ? v[q] : 0x7fffffffu);
+                            if (++to == S) { to = 0; at += S * M * 4; }
+                        }
                     }
+                } else {
+                    cluster_sync_all();
+                    met = true;
+                    if (!ok && lane < S) st_cluster_u32(peer_addr(&c.lost, lane), 1u);
+                    // NT / S neighbouring tokens to each CTA: [CTA][four tokens][weight row][token]
+                    const uint32_t share = NT / S;
+#pragma unroll 1
+                    for (int i0 = 0; i0 < min(cnt, 32) && ok; i0 += 16) {
+                        uint32_t v[16];
+                        __syncwarp();
+                        tmem_ld16_wait(d + i0, v);
+                        const uint32_t l = tok0 + i0;
+                        const uint32_t at = peer_addr(partial, l / share) +
+                                            ((rank * share + l % share) / 4 * M + weight_row<MODE>(quarter, lane)) * 16;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (i0 + 4 * q < cnt) st_cluster_v4(at + q * M * 16, v + 4 * q);
+                    }
+                    __syncwarp();
                 }
                 break;   // one tile per cluster
             } else if constexpr (FEW) {
@@ -770,26 +816,57 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
 
     if constexpr (SPLIT) {
         __syncwarp();
-        if (!met) cluster_wait();
+        if (FEW) {
+            if (!met) cluster_wait();
+        } else if (!met) {
+            cluster_sync_all();
+        }
         cluster_sync_all();   // every CTA's partial sums have arrived
         if (first < total && warp >= 4 && warp < 4 + C::EPI) {
-            // tokens rank, rank + S, ...: a thread to a channel (GATEUP: two tokens at a time)
-            // adds the CTAs' sums in the order of the blocks (a CTA that gave up sent NaN)
+            // A thread to a channel adds the CTAs' sums of this CTA's tokens in the order of the
+            // blocks.
             const Tile tile = nth_tile(0, first);
             const int tid = threadIdx.x - 128, chan = tid & (ROWS - 1), n = tile.nt * ROWS + chan;
-            constexpr int NW = M / ROWS;   // sums of a channel, and tokens at a time
+            constexpr int NW = M / ROWS, AT = C::EPI * 32 / ROWS;   // sums of a channel; tokens (tiled: fours) at a time
             const long long wn = (long long)tile.e * p.N + min(n, p.N - 1);
             const float sw0 = __ldg(p.w_s[0] + wn), sw1 = MODE == GATEUP ? __ldg(p.w_s[1] + wn) : 0.f;
-            for (int own = tid / ROWS, l = rank + own * S; l < tile.cnt; own += NW, l += NW * S) {
-                const float *from = reinterpret_cast<const float *>(partial) + own * S * M + chan;
-                float v[NW];
+            if constexpr (FEW) {
+                // tokens rank, rank + S, ... (a CTA that gave up sent NaN)
+                for (int own = tid / ROWS, l = rank + own * S; l < tile.cnt; own += AT, l += AT * S) {
+                    const float *from = reinterpret_cast<const float *>(partial) + own * S * M + chan;
+                    float v[NW];
 #pragma unroll
-                for (int w = 0; w < NW; ++w) v[w] = 0.f;
+                    for (int w = 0; w < NW; ++w) v[w] = 0.f;
 #pragma unroll 8
-                for (uint32_t q = 0; q < S; ++q)
+                    for (uint32_t q = 0; q < S; ++q)
 #pragma unroll
-                    for (int w = 0; w < NW; ++w) v[w] += from[q * M + w * ROWS];
-                if (n < p.N) store_out(p, tile.row0 + l, n, finish<MODE>(p, v[0], v[NW - 1], c.sx[warp - 4][l], sw0, sw1));
+                        for (int w = 0; w < NW; ++w) v[w] += from[q * M + w * ROWS];
+                    if (n < p.N) store_out(p, tile.row0 + l, n, finish<MODE>(p, v[0], v[NW - 1], c.sx[warp - 4][l], sw0, sw1));
+                }
+            } else {
+                // (a CTA that gave up said so: loads may still have come into the rings)
+                const int share = NT / S, from = rank * share;
+                const bool lost = c.lost;
+                for (int four = tid / ROWS; four < share / 4 && from + 4 * four < tile.cnt; four += AT) {
+                    const float4 *at = reinterpret_cast<const float4 *>(partial) + four * M + chan;
+                    float4 v[NW];
+#pragma unroll
+                    for (int w = 0; w < NW; ++w) v[w] = at[w * ROWS];
+                    for (uint32_t q = 1; q < S; ++q)
+#pragma unroll
+                        for (int w = 0; w < NW; ++w) {
+                            const float4 x = at[q * (share / 4) * M + w * ROWS];
+                            v[w] = make_float4(v[w].x + x.x, v[w].y + x.y, v[w].z + x.z, v[w].w + x.w);
+                        }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        // (32 tokens' scales with each group of four warps)
+                        const int l = from + 4 * four + i;
+                        const auto of = [&](const float4 &x) { return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w; };
+                        const float y = finish<MODE>(p, lost ? __uint_as_float(0x7fffffffu) : of(v[0]), of(v[NW - 1]), c.sx[l / 32 * 4][l % 32], sw0, sw1);
+                        if (l < tile.cnt && n < p.N) store_out(p, tile.row0 + l, n, y);
+                    }
+                }
             }
         }
         __syncthreads();
@@ -857,20 +934,53 @@ bool make_map(CUtensorMap *m, CUtensorMapDataType type, const void *base, int n,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <int MODE, int NT, bool SPLIT> cudaError_t prepare(int dev)
+{
+    static PerDeviceFlag done;
+    if (done.done(dev)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(product_kernel<MODE, NT, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)smem_bytes<NT, SPLIT>());
+    if (e == cudaSuccess) done.mark(dev);
+    return e;
+}
+
+// Clusters of `S` CTAs of the tiled kernel that run at the same time (0 where that cannot be told).
+template <int MODE> int most_clusters(int S)
+{
+    using C = Cfg<128, true>;
+    static std::atomic<int> known[kCachedDevices][kMaxSplit + 1];   // 1 more than the number
+    const int dev = current_device();
+    if (dev < kCachedDevices)
+        if (const int n = known[dev][S].load()) return n - 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(S);
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = smem_bytes<128, true>();
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = S;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (prepare<MODE, 128, true>(dev) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, product_kernel<MODE, 128, true>, &cfg) != cudaSuccess || n < 0) {
+        (void)cudaGetLastError();
+        return 0;
+    }
+    if (dev < kCachedDevices) known[dev][S].store(n + 1);
+    return n;
+}
+
 template <int MODE, int NT, bool SPLIT>
 cudaError_t launch_variant(const CUtensorMap &x, const CUtensorMap &w0, const CUtensorMap &w1, const CUtensorMap &out, const Params &p,
                            long long tiles, int num_sms, cudaStream_t stream)
 {
     using C = Cfg<NT, SPLIT>;
-    static PerDeviceFlag done;
-    const int dev = current_device();
     auto *kern = product_kernel<MODE, NT, SPLIT>;
     constexpr size_t smem = smem_bytes<NT, SPLIT>();
-    if (!done.done(dev)) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-        done.mark(dev);
-    }
+    const cudaError_t e = prepare<MODE, NT, SPLIT>(current_device());
+    if (e != cudaSuccess) return e;
     if (SPLIT)
         return launch_pdl_cluster(kern, dim3((unsigned)(tiles * p.split)), dim3(C::THREADS), smem, stream, p.split, x, w0, w1, out, p);
     const long long most = (long long)num_sms * (C::FEW ? 2 : 1);
@@ -891,13 +1001,19 @@ template <int MODE> bool weight_maps(const Params &p, CUtensorMap *w0, CUtensorM
 
 size_t tiled_workspace(int rows, int K) { return align_up((size_t)rows * K * 2, 256); }
 
+template <int MODE> int split_of_tiled(long long tiles, int blocks)
+{
+    for (int s = kMaxSplit; s > 1; s /= 2)
+        if (s * tiles <= device_sm_count() && blocks - blocks / s >= 14 && tiles <= most_clusters<MODE>(s)) return s;
+    return 1;
+}
+
 template <int MODE> cudaError_t launch_tiled(const Params &args, void *workspace, cudaStream_t stream)
 {
     constexpr int NT = 128;
     Params p = args;
     const int num_sms = device_sm_count();
     p.n_tiles = ceil_div(p.N, channels_of_tile(MODE));
-    p.split = 1;
     const long long tiles = most_tiles(p.rows, p.E, NT) * p.n_tiles;
     if (tiles > 0x3fffffffLL) return cudaErrorInvalidValue;
     ConvertLayout l{0, 1};
@@ -917,7 +1033,9 @@ template <int MODE> cudaError_t launch_tiled(const Params &args, void *workspace
     if (p.out_vec && !make_map(&mout, p.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.out, 0, p.rows,
                                p.N, p.ldo * (p.out_f32 ? 4 : 2), p.out_f32 ? 32 : 64, p.out_f32 ? 8 : 16, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
-    return launch_variant<MODE, NT, false>(mx, mw0, mw1, mout, p, tiles, num_sms, stream);
+    p.split = split_of_tiled<MODE>(tiles, ceil_div(p.K, BK));
+    return p.split > 1 ? launch_variant<MODE, NT, true>(mx, mw0, mw1, mout, p, tiles, num_sms, stream)
+                       : launch_variant<MODE, NT, false>(mx, mw0, mw1, mout, p, tiles, num_sms, stream);
 }
 
 template <int MODE> cudaError_t launch_few(const Params &args, cudaStream_t stream)
@@ -938,6 +1056,8 @@ template <int MODE> cudaError_t launch_few(const Params &args, cudaStream_t stre
                        : launch_variant<MODE, NT, false>(mx, mw0, mw1, mx, p, tiles, num_sms, stream);
 }
 
+template int split_of_tiled<PRODUCT>(long long, int);
+template int split_of_tiled<GATEUP>(long long, int);
 template cudaError_t launch_tiled<PRODUCT>(const Params &, void *, cudaStream_t);
 template cudaError_t launch_tiled<GATEUP>(const Params &, void *, cudaStream_t);
 template cudaError_t launch_few<PRODUCT>(const Params &, cudaStream_t);

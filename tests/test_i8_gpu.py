@@ -611,3 +611,75 @@ def test_two_tiled_calls_at_once(moe):
             torch.cuda.current_stream().wait_stream(s)
         assert all(torch.equal(o, v) for o, v in zip(outs, want))
     assert all(not bool((s == 0xA5).all()) for s in scratch)
+
+
+# (tokens, columns, channels): the reduction of a 128-token tile is split over clusters of 2, 4 and 8
+SPLIT_TILES = [(1000, 4096, 1001), (300, 8192, 1000), (107, 16384, 899), (401, 8208, 640)]
+
+
+@pytest.mark.parametrize("odt", ["f32", "bf16"])
+@pytest.mark.parametrize("T,K,N", SPLIT_TILES)
+def test_tiles_split_over_clusters(moe, odt, T, K, N):
+    (xq, xs), (wq, ws), (uq, us) = codes(T, K), codes(N, K, seed=1), codes(N, K, seed=2)
+    y, u = product_ref(xq, wq, xs, ws), product_ref(xq, uq, xs, us)
+    base = torch.full((T, N + 5), 7.0, device=DEV, dtype=DT[odt])
+    for gate_up in (False, True):
+        scratch, out = tiled_scratch(moe, T, K), base[:, 3:3 + N]
+        for _ in range(3):
+            base.fill_(7.0)
+            if gate_up:
+                moe.moe_gate_up_i8(xq, xs, wq, ws, uq, us, h=out, workspace=scratch)
+                close(out, *swiglu_ref(*y, *u, odt == "f32"))
+            else:
+                moe.moe_gemm_i8(xq, xs, wq, ws, out=out, workspace=scratch)
+                close(out, *y)
+            assert bool((base[:, :3] == 7).all()) and bool((base[:, 3 + N:] == 7).all())
+        assert not bool((scratch == 0xA5).all())
+
+
+@pytest.mark.parametrize("gate_up", [False, True])
+@pytest.mark.parametrize("sizes,N", [([333], 640), ([0, 200, 133], 640), ([129, 0, 1, 70], 512)])
+def test_groups_of_split_tiles(moe, gate_up, sizes, N):
+    """Fewer tiles than the grid has clusters for, rows behind the last group."""
+    K, E = 8192, len(sizes)
+    off = torch.tensor([0] + sizes, device=DEV).cumsum(0).int()
+    used = sum(sizes)
+    (xq, xs), (wq, ws), (uq, us) = codes(used + 40, K), codes(E, N, K, seed=1), codes(E, N, K, seed=2)
+    for odt in (torch.float32, torch.bfloat16):
+        out = torch.full((used + 40, N), 7.0, device=DEV, dtype=odt)
+        if gate_up:
+            moe.moe_gate_up_i8(xq, xs, wq, ws, uq, us, offsets=off, h=out)
+        else:
+            moe.moe_grouped_gemm_i8(xq, xs, wq, ws, off, out=out)
+        check_grouped(out, xq, xs, [(wq, ws), (uq, us)] if gate_up else [(wq, ws)], off, None)
+        assert bool((out[used:] == 7).all())
+
+
+@pytest.mark.parametrize("role", [0, 1, 2])
+@pytest.mark.parametrize("gate_up", [False, True])
+def test_a_wait_that_expires_in_a_split_tile(moe, gate_up, role):
+    test_a_wait_that_expires(moe, 400, 8192, 640, 1, gate_up, role)
+
+
+def test_split_tiles_side_by_side(moe):
+    """Clusters of two calls on two streams, more than run at the same time, and captured."""
+    T, K, N = 512, 8192, 1024
+    sets = [(codes(T, K, seed=i), codes(N, K, seed=i + 1)) for i in range(2)]
+    want = [moe.moe_gemm_i8(*x, *w) for x, w in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    outs = [[], []]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(8):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i].append(moe.moe_gemm_i8(*sets[i][0], *sets[i][1]))
+    for s in streams:
+        torch.cuda.current_stream().wait_stream(s)
+    assert all(torch.equal(o, v) for each, v in zip(outs, want) for o in each)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = [moe.moe_gemm_i8(*x, *w) for x, w in sets]
+    for _ in range(5):
+        graph.replay()
+    assert all(torch.equal(o, v) for o, v in zip(held, want))
