@@ -683,3 +683,31 @@ def test_split_tiles_side_by_side(moe):
     for _ in range(5):
         graph.replay()
     assert all(torch.equal(o, v) for o, v in zip(held, want))
+
+
+def test_the_first_call_of_a_process_is_captured():
+    """Kernel attributes and the number of clusters that run at once are asked for inside a
+    capture: of the split tiles, the whole ones, the few-rows and the CUDA-core kernel."""
+    import subprocess
+    import sys
+    code = """
+import torch
+import expert_routed_ffn_selectedsoftmax_gb300 as moe
+moe.load_library()
+c = lambda *s: (torch.randint(-127, 128, s, dtype=torch.int8, device="cuda"), torch.rand(*s[:-1], device="cuda"))
+sizes = [(512, 8192, 1024), (3000, 512, 2048), (64, 512, 512), (1, 512, 512)]
+sets = [(c(T, K), c(N, K)) for T, K, N in sizes]
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    held = [moe.moe_gemm_i8(*x, *w) for x, w in sets]
+for _ in range(2):
+    graph.replay()
+assert all(torch.equal(o, moe.moe_gemm_i8(*x, *w)) for o, (x, w) in zip(held, sets))
+for o, ((x, xs), (w, ws)) in zip(held, sets):
+    ref = (x.double() @ w.double().T) * xs.double()[:, None] * ws.double()
+    a = (x.double().abs() @ w.double().abs().T) * xs.double()[:, None] * ws.double()
+    assert bool(((o.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + x.shape[1] * 2.0 ** -23 * a).all())
+print("right")
+"""
+    done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0 and "right" in done.stdout, done.stderr[-2000:]
