@@ -27,7 +27,11 @@
 //
 // What bounds it (us, one GB300).  Few rows: the weights' bytes once it runs, and its start and
 // end.  Gate/up of 64 experts of 1024 x 512 and 128 x 2 rows takes 16.4; each further block of
-// 128 columns adds 1.31, which is 6.4 TB/s, and 6 do not depend on K.  Tiled: the MMAs, and
+// 128 columns adds 1.31, which is 6.4 TB/s, and 6 do not depend on K.  With an SM for each
+// tile a block takes 0.39: 1040 clocks to convert, 830 from the MMAs' issue until the buffer
+// is free again, three buffers (4096 x 4096 of 128 rows 16.0; rings of 6 and 8 blocks 15.6 and
+// 15.9, the output warps as a third converting group 15.9, half blocks in six buffers 18.8, a
+// warp of its own for the tokens 22.6).  Tiled: the MMAs, and
 // what they share the SM with.  8192 x 2048 x 5632 takes 128 (1.47 PFLOP/s, 78 % of the
 // measured fp16 rate): without the converters' work it takes 120, without the output 120,
 // without the tokens' loads 119, and with the MMAs alone 102.  The tensor pipe is busy for
