@@ -13,8 +13,8 @@
 // over the slots in order, in fp32, and are rounded once.
 //
 // What bounds them is memory.  16384 tokens x 2 of 2048 bf16 columns (us, of the measured copy
-// rate): dispatch 30.6, 99 %; its gradient 36.0, 84 %; combine 39.5, 77 %; its gradients 53.7,
-// 94 %.  Few tokens are latency: combine of 128 x 2 of 1024 takes 1.7.
+// rate): dispatch 30.6, 99 %; its gradient 36.6, 83 %; combine 37.0, 82 %; its gradients 52.9,
+// 95 %.  Few tokens are latency: combine of 128 x 2 of 1024 takes 1.7.
 #include <type_traits>
 
 #include "common.cuh"
@@ -23,7 +23,11 @@
 namespace moe {
 namespace rows {
 
-constexpr int kThreads = 256;
+// Threads of a CTA: dispatch, which only copies, starts too many CTAs of fewer (16384 x 1 x 4096
+// 42 us with 256, 66 with 128); sums and combine's gradients, whose CTAs end together, are
+// better off with more of them (combine of 16384 x 2 x 2048 39.9 and 37.0, of 16384 x 1 x 4096
+// 47.8 and 44.0; gradients of 999 x 3 x 1000 7.8 and 5.2; 64 threads as 128 or slower).
+constexpr int kCopyThreads = 256, kSumThreads = 128;
 constexpr int V = 8;            // columns of a thread's chunk
 
 // V neighbouring columns of a thread, as loaded.
@@ -178,13 +182,13 @@ struct Args {
     int lanes_log2;           // threads of a CTA along a row
 };
 
-// This thread's token and chunk; a CTA holds kThreads >> lanes_log2 tokens, and a row's
+// This thread's token and chunk; a CTA holds blockDim.x >> lanes_log2 tokens, and a row's
 // chunks are spread over col_blocks CTAs.
 __device__ __forceinline__ bool place(const Args &a, long long &t, int &chunk)
 {
     const int lanes = 1 << a.lanes_log2;
     const long long tb = blockIdx.x / a.col_blocks;
-    t = tb * (kThreads >> a.lanes_log2) + (threadIdx.x >> a.lanes_log2);
+    t = tb * (blockDim.x >> a.lanes_log2) + (threadIdx.x >> a.lanes_log2);
     chunk = (int)(blockIdx.x - tb * a.col_blocks) * (lanes * a.each) + (threadIdx.x & (lanes - 1));
     return t < a.T && chunk < a.chunks;
 }
@@ -208,7 +212,7 @@ template <int WAY, typename T> __device__ __forceinline__ void store(const Chunk
 }
 
 template <typename XT, int WAY>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kCopyThreads)
 scatter_rows_kernel(const Args a)
 {
     pdl_enter();
@@ -234,7 +238,7 @@ scatter_rows_kernel(const Args a)
 // WEIGHTED: combine; else dispatch's backward pass.  A thread takes EACH chunks, lanes
 // apart, and asks for U rows of them at once.
 template <typename XT, typename OT, int WAY, bool WEIGHTED, int EACH, int U>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kSumThreads)
 gather_sum_kernel(const Args a)
 {
     pdl_enter();
@@ -293,13 +297,13 @@ gather_sum_kernel(const Args a)
 // which walk its chunks; each thread sums its part of every slot's product, and the
 // parts meet in a fixed order (shuffles, then the warps in order).
 template <typename XT, typename GT, int WAY, int G>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kSumThreads)
 combine_backward_kernel(const Args a)
 {
     pdl_enter();
-    __shared__ float part[kThreads / 32][kMaxTopK];
+    __shared__ float part[kSumThreads / 32][kMaxTopK];
     const int lane = threadIdx.x & (G - 1);
-    const long long t = (long long)blockIdx.x * (kThreads / G) + threadIdx.x / G;
+    const long long t = (long long)blockIdx.x * (kSumThreads / G) + threadIdx.x / G;
     float dot[kMaxTopK];
 #pragma unroll
     for (int j = 0; j < kMaxTopK; ++j) dot[j] = 0.f;
@@ -433,16 +437,16 @@ int chunks_of(int d, int way, int lanes)
     if (way == APART) return d / (lanes * V) * lanes + (d % (lanes * V) < lanes ? d % (lanes * V) : lanes);
     return ceil_div(d, V) + (way == SHIFTED);
 }
-// grid of a kernel whose threads take `each` chunks
-bool lay_out(Args &a, int way, int each, dim3 *grid)
+// grid of a kernel whose threads, `cta` to a CTA, take `each` chunks
+bool lay_out(Args &a, int way, int each, int cta, dim3 *grid)
 {
     const int threads = ceil_div(chunks_of(a.d, way == APART ? WHOLE : way, 1), each);
     a.lanes_log2 = 5;
-    while (a.lanes_log2 < 8 && (1 << a.lanes_log2) < threads) ++a.lanes_log2;
+    while ((1 << a.lanes_log2) < cta && (1 << a.lanes_log2) < threads) ++a.lanes_log2;
     a.chunks = chunks_of(a.d, way, 1 << a.lanes_log2);
     a.each = each;
     a.col_blocks = ceil_div(a.chunks, each << a.lanes_log2);
-    const int per = kThreads >> a.lanes_log2;
+    const int per = cta >> a.lanes_log2;
     const long long ctas = ((long long)a.T + per - 1) / per * a.col_blocks;
     *grid = dim3((unsigned)ctas);
     return ctas <= 0x7fffffffLL;
@@ -464,19 +468,22 @@ template <typename XT, typename OT, int WAY, bool WEIGHTED>
 moe_status launch_gather_sum(Args a, cudaStream_t s)
 {
     // Many tokens: about 64 bytes in flight a thread (combine of 16384 x 2 x 2048 in bf16: one
-    // chunk a thread 44 us, two 39.5); few: a chunk a thread and its rows at once, as that is latency.
-    const bool many = (long long)a.T * (a.d / V) >= 2LL * kThreads * 8 * device_sm_count();
+    // chunk a thread 38.2 us, two 37.0); few: a chunk a thread and its rows at once, as that is
+    // latency, with registers for no more of them than there are (4096 x 2 x 1024: two at once
+    // 6.6, four 7.2; 16384 x 4 x 1024 30.1 and 28.5).
+    const bool many = (long long)a.T * (a.d / V) >= 4096LL * device_sm_count();
     constexpr int kTwice = sizeof(XT) == 4 ? 1 : 2;   // (fp32 chunks are twice as long)
     const auto go = [&](auto kern, int each) {
         dim3 grid;
-        if (!lay_out(a, WAY, each, &grid)) return MOE_ERR_UNSUPPORTED;
-        return launched([&] { return launch_pdl(kern, grid, dim3(kThreads), 0, s, a); });
+        if (!lay_out(a, WAY, each, kSumThreads, &grid)) return MOE_ERR_UNSUPPORTED;
+        return launched([&] { return launch_pdl(kern, grid, dim3(kSumThreads), 0, s, a); });
     };
     if constexpr (WAY == WHOLE) {
         if (many && a.k == 1) return go(gather_sum_kernel<XT, OT, WAY, WEIGHTED, 2 * kTwice, 1>, 2 * kTwice);
         if (many && a.k <= 3) return go(gather_sum_kernel<XT, OT, WAY, WEIGHTED, kTwice, 2>, kTwice);
+        if (a.k > 2) return go(gather_sum_kernel<XT, OT, WAY, WEIGHTED, 1, 4>, 1);
     }
-    return go(gather_sum_kernel<XT, OT, WAY, WEIGHTED, 1, WAY == WHOLE ? 4 : 2>, 1);
+    return go(gather_sum_kernel<XT, OT, WAY, WEIGHTED, 1, 2>, 1);
 }
 
 template <bool WEIGHTED>
@@ -516,8 +523,8 @@ moe_status moe_dispatch(const void *x, moe_dtype dt, int T, int d, long long ldx
         constexpr int kOff = sizeof(XT) == 4 ? APART : SHIFTED;
         const auto go = [&](auto kern, int way) {
             dim3 grid;
-            if (!lay_out(a, way, 1, &grid)) return MOE_ERR_UNSUPPORTED;
-            return launched([&] { return launch_pdl(kern, grid, dim3(kThreads), 0, static_cast<cudaStream_t>(stream), a); });
+            if (!lay_out(a, way, 1, kCopyThreads, &grid)) return MOE_ERR_UNSUPPORTED;
+            return launched([&] { return launch_pdl(kern, grid, dim3(kCopyThreads), 0, static_cast<cudaStream_t>(stream), a); });
         };
         if (vectors(x, ldx, d) && vectors(out, ldo, d)) return go(scatter_rows_kernel<XT, WHOLE>, WHOLE);
         return go(scatter_rows_kernel<XT, kOff>, kOff);
@@ -575,13 +582,13 @@ moe_status moe_combine_backward(const void *grad, moe_dtype grad_dt, int T, int 
             const auto go = [&](auto way) {
                 constexpr int WAY = decltype(way)::value;
                 const bool warps = T >= 16 * device_sm_count();   // (a warp to a token, or a CTA)
-                a.chunks = chunks_of(d, WAY, warps ? 32 : kThreads);
+                a.chunks = chunks_of(d, WAY, warps ? 32 : kSumThreads);
                 return launched([&] {
                     cudaStream_t s = static_cast<cudaStream_t>(stream);
                     if (warps)
-                        return launch_pdl(combine_backward_kernel<XT, GT, WAY, 32>, dim3((unsigned)ceil_div(T, kThreads / 32)),
-                                          dim3(kThreads), 0, s, a);
-                    return launch_pdl(combine_backward_kernel<XT, GT, WAY, kThreads>, dim3((unsigned)T), dim3(kThreads), 0, s, a);
+                        return launch_pdl(combine_backward_kernel<XT, GT, WAY, 32>, dim3((unsigned)ceil_div(T, kSumThreads / 32)),
+                                          dim3(kSumThreads), 0, s, a);
+                    return launch_pdl(combine_backward_kernel<XT, GT, WAY, kSumThreads>, dim3((unsigned)T), dim3(kSumThreads), 0, s, a);
                 });
             };
             return whole ? go(WayOf<WHOLE>()) : go(WayOf<kOff>());
