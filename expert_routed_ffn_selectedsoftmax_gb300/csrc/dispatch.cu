@@ -13,8 +13,8 @@
 // over the slots in order, in fp32, and are rounded once.
 //
 // What bounds them is memory.  16384 tokens x 2 of 2048 bf16 columns (us, of the measured copy
-// rate): dispatch 30.6, 99 %; its gradient 36.6, 83 %; combine 37.0, 82 %; its gradients 52.9,
-// 95 %.  Few tokens are latency: combine of 128 x 2 of 1024 takes 1.7.
+// rate): dispatch 30.6, 99 %; its gradient 36.6, 83 %; combine 37.0, 82 %; its gradients 50.5,
+// 100 %.  Few tokens are latency: combine of 128 x 2 of 1024 takes 1.7.
 #include <type_traits>
 
 #include "common.cuh"
@@ -24,9 +24,9 @@ namespace moe {
 namespace rows {
 
 // Threads of a CTA: dispatch, which only copies, starts too many CTAs of fewer (16384 x 1 x 4096
-// 42 us with 256, 66 with 128); sums and combine's gradients, whose CTAs end together, are
-// better off with more of them (combine of 16384 x 2 x 2048 39.9 and 37.0, of 16384 x 1 x 4096
-// 47.8 and 44.0; gradients of 999 x 3 x 1000 7.8 and 5.2; 64 threads as 128 or slower).
+// 42 us with 256, 66 with 128); sums, whose CTAs end together, are better off with more of
+// them (combine of 16384 x 2 x 2048 39.9 and 37.0, of 16384 x 1 x 4096 47.8 and 44.0; 64
+// threads as 128 or slower).
 constexpr int kCopyThreads = 256, kSumThreads = 128;
 constexpr int V = 8;            // columns of a thread's chunk
 
@@ -293,17 +293,19 @@ gather_sum_kernel(const Args a)
     }
 }
 
-// Combine's backward pass: a token to a group of `G` threads (a warp, or the CTA),
+// Combine's backward pass: a token to a group of `G` threads (a warp, or a CTA),
 // which walk its chunks; each thread sums its part of every slot's product, and the
 // parts meet in a fixed order (shuffles, then the warps in order).
+constexpr int backward_threads(int G) { return G == 32 ? 128 : G; }
 template <typename XT, typename GT, int WAY, int G>
-__global__ void __launch_bounds__(kSumThreads)
+__global__ void __launch_bounds__(backward_threads(G))
 combine_backward_kernel(const Args a)
 {
     pdl_enter();
-    __shared__ float part[kSumThreads / 32][kMaxTopK];
+    constexpr int N = backward_threads(G);
+    __shared__ float part[N / 32][kMaxTopK];
     const int lane = threadIdx.x & (G - 1);
-    const long long t = (long long)blockIdx.x * (kSumThreads / G) + threadIdx.x / G;
+    const long long t = (long long)blockIdx.x * (N / G) + threadIdx.x / G;
     float dot[kMaxTopK];
 #pragma unroll
     for (int j = 0; j < kMaxTopK; ++j) dot[j] = 0.f;
@@ -581,15 +583,25 @@ moe_status moe_combine_backward(const void *grad, moe_dtype grad_dt, int T, int 
             constexpr int kOff = sizeof(XT) == 4 ? APART : SHIFTED;
             const auto go = [&](auto way) {
                 constexpr int WAY = decltype(way)::value;
-                const bool warps = T >= 16 * device_sm_count();   // (a warp to a token, or a CTA)
-                a.chunks = chunks_of(d, WAY, warps ? 32 : kSumThreads);
-                return launched([&] {
-                    cudaStream_t s = static_cast<cudaStream_t>(stream);
-                    if (warps)
-                        return launch_pdl(combine_backward_kernel<XT, GT, WAY, 32>, dim3((unsigned)ceil_div(T, kSumThreads / 32)),
-                                          dim3(kSumThreads), 0, s, a);
-                    return launch_pdl(combine_backward_kernel<XT, GT, WAY, kSumThreads>, dim3((unsigned)T), dim3(kSumThreads), 0, s, a);
-                });
+                // Threads of a token.  Many tokens: a warp, or two where it has more than two
+                // chunks a lane; few: as many as their chunks keep in use.  us, 32 / 64 / 128 / 512:
+                // 16384 x 2 x 128 12.7 / 18.5 / 28.1, x 2048 52.7 / 50.6 / 52.3; 1945 x 7 x 278
+                // 18.2 / 19.5 / 27.5; 999 x 3 x 1000 7.0 / 5.2 / 5.3 / 13.1; 3000 x 8 x 8192
+                // 133 / 137 / 131; 300 x 4 x 4096 18.6 / 10.8 / 7.4 / 6.3; 64 x 2 x 2048 3.6 / 2.5 /
+                // 1.9 / 2.1; 16 x 2 x 8192 10.3 / 5.8 / 3.6 / 2.5.
+                const int sms = device_sm_count(), chunks = ceil_div(d, V);
+                const auto launch = [&](auto group) {
+                    constexpr int G = decltype(group)::value, N = backward_threads(G);
+                    a.chunks = chunks_of(d, WAY, G);
+                    return launched([&] {
+                        return launch_pdl(combine_backward_kernel<XT, GT, WAY, G>, dim3((unsigned)ceil_div(T, N / G)), dim3(N), 0,
+                                          static_cast<cudaStream_t>(stream), a);
+                    });
+                };
+                if (T >= 10 * sms && chunks <= 64) return launch(std::integral_constant<int, 32>());
+                if (chunks <= 64 || (T >= 10 * sms && chunks < 1024)) return launch(std::integral_constant<int, 64>());
+                if (T <= 2 * sms && chunks > 256) return launch(std::integral_constant<int, 512>());
+                return launch(std::integral_constant<int, 128>());
             };
             return whole ? go(WayOf<WHOLE>()) : go(WayOf<kOff>());
         });

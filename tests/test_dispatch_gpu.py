@@ -376,3 +376,11 @@ def test_device_refusals(moe):
         moe.moe_combine(rand(8, 16), torch.ones(4, 2), inv)
     with pytest.raises(moe.MoeError):
         moe.moe_dispatch(rand(1, 16), perm(9), 9)
+
+
+@pytest.mark.parametrize("dt,odt", [("f32", "bf16"), ("bf16", "bf16")])
+@pytest.mark.parametrize("T,k,d", [(1601, 2, 1000), (1600, 3, 1003), (1555, 1, 8200), (1530, 1, 8197), (304, 2, 2312), (305, 2, 2309),
+                                   (300, 8, 520), (16, 2, 513)])
+def test_combine_by_threads_of_a_token(moe, dt, odt, T, k, d):
+    """Many and few tokens, narrow and wide: one warp, two, four or sixteen to a token."""
+    test_combine_and_its_gradients(moe, dt, odt, T, k, d)
