@@ -25,18 +25,19 @@ template <int MODE> bool vector_fits(const Params &p, long long experts)
 }
 
 // Few rows or tiled, by what each is expected to take (us).  The few-rows kernel takes
-// blocks of 128 columns in 0.39 us where every tile has an SM and 0.62 where two share one;
-// the tiled kernel takes 0.335 and a tile's end 0.8, on an eighth of the tiles or fewer, but
-// it starts later (its rows are widened first).  Where a reduction is split, a CTA has its
+// blocks of 128 columns in 0.39 us where every tile has an SM and 0.62 where two share one,
+// and a tile's end in 0.6 (SwiGLU's 1.0); the tiled kernel takes 0.335 and a tile's end 0.8, on
+// a quarter of the tiles, but it starts later (its rows are widened first).  Where a reduction is split, a CTA has its
 // share of the blocks, and its cluster's meeting.  A tile more than the SMs have places for is
 // a round more; the groups' sizes are known on the device only, so there their last tiles are
-// taken as half full and rounds as fractions.
+// taken as half full, and a tenth of a round more as none.
 // Measured (few rows / tiled): 4096 x 4096 of 64 rows 13.6 / 12.6, 128: 16.0 / 14.1, 300:
 // 33.0 / 19.1; 2048 x 5632 of 128 13.6 / 12.7; 1024 x 1024 of 1024 8.8 / 9.9, 2048: 14.4 / 10.9;
 // 2048 x 2048 of 128 10.0 / 12.1; 8192 x 1024 of 256 18.6 / 15.7, 1024: 42.0 / 25.3; 64
 // experts of 2048 x 1024, rows per expert 16: 28.0 / 33.3, 32: 35.4 / 37.3, 47: 44.6 / 38.9;
 // 16 of 2816 x 2048, 24: 25.6 / 26.6, 40: 32.3 / 27.8; gate/up, 64 of 1024 x 512, 16: 18.0 /
-// 22.0, 64: 33.6 / 28.0; one of 2048 x 5632, 100 rows: 26.7 / 14.5.
+// 22.0, 64: 33.6 / 28.0; one of 2048 x 5632, 100 rows: 26.7 / 14.5; two of 160 x 2805, 742 rows
+// each: 27.4 / 17.0.
 template <int MODE> bool few_rows_fit(const Params &p, int experts)
 {
     if (p.rows <= kFewRows) return true;
@@ -44,13 +45,13 @@ template <int MODE> bool few_rows_fit(const Params &p, int experts)
     const auto rounds = [&](int tokens, int places) {
         if (experts == 1) return ceil((double)ceil_div(p.rows, tokens) * columns / places);
         const double each = (double)p.rows / tokens + experts * 0.5;
-        const double r = (each > experts ? each : experts) * columns / places;
+        const double r = ceil((each > experts ? each : experts) * columns / places - 0.1);
         return r > 1 ? r : 1;
     };
     const int split = split_of(most_tiles(p.rows, experts, 32) * columns, blocks, sms);
     const double few = split > 1 ? 6.5 + 0.39 * ceil_div(blocks, split)
                      : rounds(32, sms) <= 1 ? 3.5 + 0.39 * blocks
-                                            : 3.5 + 0.62 * blocks * rounds(32, 2 * sms);
+                                            : 3.5 + (0.62 * blocks + (MODE == GATEUP ? 1.0 : 0.6)) * rounds(32, 2 * sms);
     const int tiled_split = split_of_tiled<MODE>(most_tiles(p.rows, experts, 128) * columns, blocks);
     const double tiled = 6.3 + (double)p.rows * p.K * 3.4e-7 +
                          (tiled_split > 1 ? 5 + 0.335 * ceil_div(blocks, tiled_split) : rounds(128, sms) * (0.335 * blocks + 0.8));
