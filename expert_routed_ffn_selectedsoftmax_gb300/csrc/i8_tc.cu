@@ -481,11 +481,12 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                 const uint32_t idesc = idesc_f16_mn(1, M, (mine + 15) & ~15);
                 const int db = i & 1;
                 const uint32_t d = tmem + db * NT + from;
-                ok = bar_wait(&c.dempty[db], ((i >> 1) & 1u) ^ 1u, abort_flag);
+                // (voted, as the other roles' waits: lanes that give up leave the loop together)
+                ok = __all_sync(0xffffffffu, bar_wait(&c.dempty[db], ((i >> 1) & 1u) ^ 1u, abort_flag));
                 for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
                     const uint32_t a = it % NA;
                     // (the converters have seen the tokens land too)
-                    ok = bar_wait(&c.cfull[a], (it / NA) & 1u, abort_flag);
+                    ok = __all_sync(0xffffffffu, bar_wait(&c.cfull[a], (it / NA) & 1u, abort_flag));
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t dx = sw128_desc(tokens + a * (FEW ? C::XF_BYTES : C::X_BYTES));

@@ -1,6 +1,8 @@
 """Host-side checks of the 8-bit integer operators and of dispatch and combine: every
 refused argument comes back before any CUDA call, from the library and from the binding."""
 import ctypes
+import os
+import re
 
 import pytest
 
@@ -162,3 +164,24 @@ def test_binding_refuses_wrong_slots():
             moe.moe_combine_backward(**dict(dict(grad=x, y=y, topk_w=w, inv=inv), **kw))
     with pytest.raises(RuntimeError, match="ambiguous"):
         moe.moe_combine_backward(x, y, w, inv, want_dy=torch.ones(2))
+
+
+def warp_waits(name):
+    """The statements of a kernel's source that wait on a barrier as part of a role (not the ones
+    that let copies and MMAs in flight end, which nothing follows)."""
+    text = open(os.path.join(os.path.dirname(os.path.abspath(__file__)), "..", "expert_routed_ffn_selectedsoftmax_gb300", "csrc",
+                             name)).read()
+    text = re.sub(r"//[^\n]*", "", text)
+    found = [s for s in re.split(r"[;{}]", text) if re.search(r"\b(bar_wait|mbar_wait_slow)\(&", s)]
+    return [" ".join(s.split()) for s in found if "no_abort" not in s]
+
+
+@pytest.mark.parametrize("name", ["i8_tc.cu"])
+def test_a_warp_gives_up_as_a_whole(name):
+    """A bounded wait's answer is each lane's own (its lanes poll one after the other): a role
+    that a whole warp runs takes the warp's vote, or lanes that give up would leave the
+    others at a barrier of the full warp."""
+    waits = warp_waits(name)
+    assert len(waits) >= 4
+    for statement in waits:
+        assert "__all_sync(0xffffffffu" in statement, statement
