@@ -219,7 +219,8 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
             if (leader) flag_status(p.status, kDevTimeout);
             c.abort_flag = 1;
         }
-        issued = it;
+        // (the waits' answers are each lane's own, and what follows is the whole warp's)
+        issued = __reduce_max_sync(0xffffffffu, it);
     } else {
         // ------------------------------------------------ sums and output
         const int ew = warp - 2, quarter = warp & 3, chan = quarter * 32 + lane;

@@ -166,13 +166,17 @@ def test_binding_refuses_wrong_slots():
         moe.moe_combine_backward(x, y, w, inv, want_dy=torch.ones(2))
 
 
+def source(name):
+    """A kernel's source without its comments."""
+    text = open(os.path.join(os.path.dirname(os.path.abspath(__file__)), "..", "expert_routed_ffn_selectedsoftmax_gb300", "csrc",
+                             name)).read()
+    return re.sub(r"//[^\n]*", "", text)
+
+
 def warp_waits(name):
     """The statements of a kernel's source that wait on a barrier as part of a role (not the ones
     that let copies and MMAs in flight end, which nothing follows)."""
-    text = open(os.path.join(os.path.dirname(os.path.abspath(__file__)), "..", "expert_routed_ffn_selectedsoftmax_gb300", "csrc",
-                             name)).read()
-    text = re.sub(r"//[^\n]*", "", text)
-    found = [s for s in re.split(r"[;{}]", text) if re.search(r"\b(bar_wait|mbar_wait_slow)\(&", s)]
+    found = [s for s in re.split(r"[;{}]", source(name)) if re.search(r"\b(bar_wait|mbar_wait_slow)\(&", s)]
     return [" ".join(s.split()) for s in found if "no_abort" not in s]
 
 
@@ -185,3 +189,15 @@ def test_a_warp_gives_up_as_a_whole(name):
     assert len(waits) >= 4
     for statement in waits:
         assert "__all_sync(0xffffffffu" in statement, statement
+
+
+@pytest.mark.parametrize("name", ["fp8b_decode.cu", "fp8b_gemm.cu"])
+def test_an_unvoted_role_ends_as_a_whole(name):
+    """The multiplying warps of the block-scaled fp8 products wait lane by lane and hold no
+    barrier of the warp in their loop; how much they have issued, which decides whether the
+    whole warp waits for it after a wait that gave up, is taken over all lanes."""
+    text = source(name)
+    role = text[text.index("const bool leader = elect_one()"):]
+    role = role[:role.index("} else {")]
+    assert role.count("bar_wait(&") == 2 and "__syncwarp" not in role and "__all_sync" not in role
+    assert "issued = __reduce_max_sync(0xffffffffu, it)" in role and "issued = it" not in role
