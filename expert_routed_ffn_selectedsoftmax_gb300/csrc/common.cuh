@@ -23,6 +23,9 @@ constexpr uint32_t kDevCheckFailed = 2u;   // device consistency check failed
 
 __host__ __device__ inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+// Most columns of a matrix whose kernels count them in 32 bits: the last tile, or the last
+// thread's chunks, may end up to 256 columns behind them.
+constexpr int kMostColumns = 0x7fffffff - 256;
 
 // ---------------------------------------------------------------- conversions
 __device__ __forceinline__ float bf16lo(uint32_t v) { return __uint_as_float(v << 16); }

@@ -418,7 +418,7 @@ moe_status check(int T, int k, int rows, int d, const int32_t *inv, bool *go)
 {
     *go = false;
     if (T < 0 || k < 1 || rows < 0 || d <= 0) return MOE_ERR_INVALID_ARG;
-    if (k > kMaxTopK) return MOE_ERR_UNSUPPORTED;
+    if (k > kMaxTopK || d > kMostColumns) return MOE_ERR_UNSUPPORTED;
     if (T == 0) return MOE_OK;
     if (T > INT32_MAX / kMaxTopK) return MOE_ERR_UNSUPPORTED;
     if (!inv || !aligned(inv, 4)) return MOE_ERR_INVALID_ARG;

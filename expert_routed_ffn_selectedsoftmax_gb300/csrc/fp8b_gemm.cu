@@ -602,7 +602,7 @@ moe_status product_args(const void *x_q, const float *x_s, int x_rows, int K, lo
     *go = false;
     if (x_rows < 0 || rows < 0 || K <= 0 || K % 16 || N <= 0 || E <= 0) return MOE_ERR_INVALID_ARG;
     if (ldx < K || ldx % 16) return MOE_ERR_INVALID_ARG;
-    if (E > kMaxExperts) return MOE_ERR_UNSUPPORTED;
+    if (E > kMaxExperts || K > kMostColumns || N > kMostColumns) return MOE_ERR_UNSUPPORTED;
     if (E > 1 && !offsets && rows > 0) return MOE_ERR_INVALID_ARG;
     if (rows == 0) return MOE_OK;
     if (!perm_tok && rows > x_rows) return MOE_ERR_INVALID_ARG;

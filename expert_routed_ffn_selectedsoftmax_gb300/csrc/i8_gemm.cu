@@ -75,7 +75,7 @@ moe_status product_args(const Params &p, moe_dtype out_dt, const void *workspace
     if (p.x_rows < 0 || p.rows < 0 || p.K <= 0 || p.K % 16 || p.N <= 0 || p.E <= 0) return MOE_ERR_INVALID_ARG;
     if (p.ldx < p.K || p.ldx % 16 || p.ldo < p.N) return MOE_ERR_INVALID_ARG;
     if (out_dt != MOE_F32 && out_dt != MOE_BF16) return MOE_ERR_INVALID_ARG;
-    if (p.E > kMaxExperts) return MOE_ERR_UNSUPPORTED;
+    if (p.E > kMaxExperts || p.K > kMostColumns || p.N > kMostColumns) return MOE_ERR_UNSUPPORTED;
     if (p.E > 1 && !p.offsets && p.rows > 0) return MOE_ERR_INVALID_ARG;
     if (p.rows == 0) return MOE_OK;
     if (!p.perm_tok && p.rows > p.x_rows) return MOE_ERR_INVALID_ARG;

@@ -438,7 +438,8 @@ MOE_API moe_status moe_forward_noalloc(const void *x, moe_dtype act_dt, int T, i
  *     [rows, ceil(K/128)];
  *   weights [E, N, K]: one scale per block of 128 rows x 128 columns, scales
  *     [E, ceil(N/128), ceil(K/128)] (blocks do not cross experts).
- * K (d, F) is a multiple of 16; the last block of a row may be shorter.  Code
+ * K (d, F) is a multiple of 16; the last block of a row may be shorter; K and N of a
+ * product reach 2^31 - 257.  Code
  * buffers are 16-byte aligned, scales 4-byte.
  * Quantisation of a block: s = max|x| / 448, code = E4M3 nearest to x * (1/s),
  * ties to even, each operation rounded to fp32.  (x * (1/s) is within 3 x 2^-24
@@ -577,7 +578,7 @@ MOE_API moe_status moe_gate_up_fp8b(const void *x_q, const float *x_s, int x_row
  *   alignment of their type; widths and distances that are multiples of 8 with 16-byte
  *   aligned pointers move 16 bytes at a time.  Sums run over the slots in order, in
  *   fp32, and are rounded once; every call gives bitwise identical results from run to
- *   run.  k in 1..8.  No output may overlap an input or another output.
+ *   run.  k in 1..8, d up to 2^31 - 257.  No output may overlap an input or another output.
  */
 
 /*
@@ -625,7 +626,8 @@ MOE_API moe_status moe_combine_backward(const void *grad, moe_dtype grad_dt, int
  * MOE_Q8_0 experts of moe_forward.)
  *
  * A matrix is int8 codes, row-major, value = code * scale: activations [rows, K] with
- * scales [rows], weights [E, N, K] with scales [E, N].  K (d) is a multiple of 16.  Code
+ * scales [rows], weights [E, N, K] with scales [E, N].  K (d) is a multiple of 16; it and
+ * N (F) reach 2^31 - 257.  Code
  * buffers are 16-byte aligned, scales 4-byte.
  * Quantisation of a row: s = max|x| / 127, code = the whole number nearest to
  * 127 x / max|x|, ties to even, of the exact quotient.  All zeros, or so small that s

@@ -201,3 +201,25 @@ def test_an_unvoted_role_ends_as_a_whole(name):
     role = role[:role.index("} else {")]
     assert role.count("bar_wait(&") == 2 and "__syncwarp" not in role and "__all_sync" not in role
     assert "issued = __reduce_max_sync(0xffffffffu, it)" in role and "issued = it" not in role
+
+
+def test_widths_near_the_end_of_32_bits_are_refused(lib):
+    """A tile's, or a thread's, columns may end behind the matrix's last one and are counted in
+    32 bits: widths within 256 of 2^31 are not taken."""
+    most = 2 ** 31 - 1
+    for d in (most, most - 255):
+        for dt in (F32, BF16):
+            assert lib.moe_dispatch(FAKE, dt, 1, d, d, FAKE, 1, FAKE, 1, d, None) == U
+            assert lib.moe_dispatch_backward(FAKE, dt, 1, d, d, FAKE, 1, 1, FAKE, d, None) == U
+            assert lib.moe_combine(FAKE, dt, 1, d, d, FAKE, FAKE, 1, 1, FAKE, dt, d, None) == U
+            assert lib.moe_combine_backward(FAKE, dt, 1, d, d, FAKE, dt, 1, d, FAKE, FAKE, 1, FAKE, d, FAKE, None) == U
+    for K, N in ((16, most), (16, most - 255), (most - 15, 16), (most - 255, 16)):
+        K -= K % 16
+        wide = 1 << 40
+        assert lib.moe_gemm_i8(FAKE, FAKE, 1, K, K, FAKE, FAKE, N, FAKE, BF16, N, FAKE, wide, None, None) == U
+        assert lib.moe_grouped_gemm_i8(FAKE, FAKE, 1, K, K, FAKE, FAKE, 1, N, None, None, 1, FAKE, F32, N, FAKE, wide, None, None) == U
+        assert lib.moe_gate_up_i8(FAKE, FAKE, 1, K, K, FAKE, FAKE, FAKE, FAKE, 1, N, None, None, 1, FAKE, F32, N, FAKE, wide, None,
+                                  None) == U
+        assert lib.moe_gemm_fp8b(FAKE, FAKE, 1, K, K, FAKE, FAKE, N, FAKE, F32, N, None, None) == U
+        assert lib.moe_gate_up_fp8b(FAKE, FAKE, 1, K, K, FAKE, FAKE, FAKE, FAKE, 1, N - N % 16, None, None, 1, FAKE, FAKE, FAKE, wide,
+                                    None, None) == U
