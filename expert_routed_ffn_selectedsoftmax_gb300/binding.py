@@ -37,8 +37,8 @@ EXPORTS = ("moe_status_str", "moe_version", "moe_route", "moe_route_scored", "mo
            "moe_gate_up_fp8b", "moe_fp8b_workspace_size", "moe_grouped_gemm_fp8b_expire_wait",
            "moe_grouped_gemm_fp8b_expire_sums", "moe_gate_up_fp8b_expire_wait",
            "moe_gate_up_fp8b_expire_sums",
-           "moe_dispatch", "moe_dispatch_backward", "moe_combine", "moe_combine_backward",
-           "moe_quant_i8", "moe_gemm_i8", "moe_grouped_gemm_i8", "moe_gate_up_i8", "moe_i8_workspace_size",
+           "moe_dispatch", "moe_dispatch_filled", "moe_dispatch_backward", "moe_combine", "moe_combine_backward",
+           "moe_combine_backward_filled", "moe_quant_i8", "moe_gemm_i8", "moe_grouped_gemm_i8", "moe_gate_up_i8", "moe_i8_workspace_size",
            "moe_grouped_gemm_i8_expire_wait", "moe_gate_up_i8_expire_wait")
 
 _lib = None
@@ -160,9 +160,11 @@ def _declare(L):
                                    sz, vp, vp]
     L.moe_gate_up_fp8b.restype = i
     L.moe_dispatch.argtypes = [vp, i, i, i, ll, vp, i, vp, i, ll, vp]
+    L.moe_dispatch_filled.argtypes = L.moe_dispatch.argtypes
     L.moe_dispatch_backward.argtypes = [vp, i, i, i, ll, vp, i, i, vp, ll, vp]
     L.moe_combine.argtypes = [vp, i, i, i, ll, vp, vp, i, i, vp, i, ll, vp]
     L.moe_combine_backward.argtypes = [vp, i, i, i, ll, vp, i, i, ll, vp, vp, i, vp, ll, vp, vp]
+    L.moe_combine_backward_filled.argtypes = L.moe_combine_backward.argtypes
     L.moe_quant_i8.argtypes = [vp, i, i, i, ll, vp, vp, vp]
     L.moe_gemm_i8.argtypes = [vp, vp, i, i, ll, vp, vp, i, vp, i, ll, vp, sz, vp, vp]
     L.moe_grouped_gemm_i8.argtypes = [vp, vp, i, i, ll, vp, vp, i, i, vp, vp, i, vp, i, ll, vp, sz, vp, vp]
@@ -171,7 +173,8 @@ def _declare(L):
                                                   ctypes.c_uint32, vp]
     L.moe_gate_up_i8_expire_wait.argtypes = [vp, vp, i, i, ll, vp, vp, vp, vp, i, i, vp, vp, i, vp, i, ll, vp, sz, vp, i,
                                              ctypes.c_uint32, vp]
-    for call in (L.moe_grouped_gemm_i8_expire_wait, L.moe_gate_up_i8_expire_wait, L.moe_dispatch, L.moe_dispatch_backward, L.moe_combine, L.moe_combine_backward, L.moe_quant_i8,
+    for call in (L.moe_grouped_gemm_i8_expire_wait, L.moe_gate_up_i8_expire_wait, L.moe_dispatch, L.moe_dispatch_filled,
+                 L.moe_dispatch_backward, L.moe_combine, L.moe_combine_backward, L.moe_combine_backward_filled, L.moe_quant_i8,
                  L.moe_gemm_i8, L.moe_grouped_gemm_i8, L.moe_gate_up_i8):
         call.restype = i
     L.moe_i8_workspace_size.argtypes = [i, i]
@@ -615,8 +618,8 @@ def moe_dispatch(x: torch.Tensor, inv: torch.Tensor, k: int, out: Optional[torch
     """Tokens x [T, d] (fp32 / bf16) into grouped order -> out [rows, d]: out[inv[t*k + j]] = x[t].
 
     inv [T*k] (moe_permute).  rows is T*k, or out's if it is given.  Rows that no slot
-    names are left as they were (uninitialised in an output allocated here); a slot whose
-    inv is outside [0, rows) writes nothing.
+    names are left as they were in an output that is given, and zeros in one allocated
+    here; a slot whose inv is outside [0, rows) writes nothing.
     """
     return _checked((_fp8b_module or _fp8b()).dispatch(x, inv, k, out), "moe_dispatch")
 
@@ -644,8 +647,8 @@ def moe_combine_backward(grad: torch.Tensor, y: torch.Tensor, topk_w: torch.Tens
     """moe_combine's gradients for grad [T, d] -> (dy [rows, d] in y's type, dw fp32 [T, k]):
     dy[inv[t*k + j]] = topk_w[t, j] grad[t], dw[t, j] = <grad[t], y[inv[t*k + j]]>.
 
-    One that is not wanted is None.  Rows of dy that no slot names are left as they were
-    (uninitialised in an output allocated here).
+    One that is not wanted is None.  Rows of dy that no slot names are left as they were in
+    a dy that is given, and zeros (their gradient) in one allocated here.
     """
     return _checked((_fp8b_module or _fp8b()).combine_backward(grad, y, topk_w, inv, want_dy, want_dw, dy, dw),
                     "moe_combine_backward")

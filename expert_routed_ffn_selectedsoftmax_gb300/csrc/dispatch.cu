@@ -180,16 +180,111 @@ struct Args {
     int chunks, col_blocks;   // chunks of a row; CTAs along it
     int each;                 // chunks a thread takes
     int lanes_log2;           // threads of a CTA along a row
+    int fill;                 // CTAs ahead of the others that look for rows no slot names
 };
+
+// Zeros into the rows that no slot names, for an output whose memory holds nothing yet, by the
+// first `fill` CTAs of a grid, beside the others' work.  As many rows as slots all have a slot
+// if no slot is without a row: each of these CTAs looks at its share of inv, and goes home
+// if all is well there (dispatch of 16384 x 8 x 64: 5.6 us, 5.5 without them, 36 where each
+// reads all of inv).  Else those that found a slot without a row share the rows
+// among themselves: each marks its own by all of inv (one bit a row in shared memory, as many
+// rows at a time as there are bits) and zeroes what stays unmarked.  With a tenth of the slots
+// dropped: dispatch of 8192 x 2 x 1024 16 us (8.5), of 16384 x 8 x 64 51 (5.5), combine's
+// gradients of 16384 x 2 x 2048 65 (47).
+constexpr int kMarkWords = 2048;
+template <typename T> __device__ __forceinline__ void zero_row(T *row, int d, int lane)
+{
+    constexpr int N = 16 / (int)sizeof(T);
+    const int lead = min(lead_of(row), d), whole = (d - lead) / N, tail = lead + whole * N;
+    Chunk<T> c;
+    c.zero();
+    if (lane < lead) c.store_one(0, row + lane);
+    for (int i = lane; i < whole; i += 32) reinterpret_cast<uint4 *>(row + lead)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (tail + lane < d) c.store_one(0, row + tail + lane);
+}
+// f(number, values) of the fours of slots at(0), at(1), ... up to `hi` of them (U loads of a
+// thread in flight).  Ends early once `done` says so.
+template <int U, typename AT, typename DONE, typename F>
+__device__ __forceinline__ void each_four(const int4 *inv, int fours, int hi, AT at, DONE done, F f)
+{
+    for (int t = threadIdx.x; t < hi && !done(); t += U * blockDim.x) {
+        int4 v[U];
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+            const int i = at(t + q * blockDim.x);
+            if (i < fours) v[q] = __ldg(inv + i);
+        }
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+            const int i = at(t + q * blockDim.x);
+            if (i < fours) f(i, v[q]);
+        }
+    }
+}
+template <typename T, int U> __device__ __forceinline__ void zero_unnamed(const Args &a)
+{
+    __shared__ uint32_t named[kMarkWords], found;
+    const int lane = threadIdx.x & 31;
+    const int n = a.T * a.k;   // (at most kMostMarked)
+    const int head = min((int)((16 - (reinterpret_cast<uintptr_t>(a.inv) & 15)) & 15) / 4, n), fours = (n - head) / 4;
+    const int4 *inv = reinterpret_cast<const int4 *>(a.inv + head);
+    const auto lone = [&](int i) { return __ldg(a.inv + (i < head ? i : i + 4 * fours)); };   // the slots beside the fours
+    const int lones = n - 4 * fours;   // (at most 6)
+    const auto same = [](int i) { return i; };
+    const auto never = [] { return false; };
+    uint32_t parts = a.fill, part = blockIdx.x;
+    if (n == a.rows) {
+        // then there are 1, 2, 4, .. 32 of these CTAs, and a share is every parts-th 64 fours
+        const auto without = [&](int r) { return (uint32_t)r >= (uint32_t)a.rows; };
+        const auto any = [&](int4 v) { return without(v.x) || without(v.y) || without(v.z) || without(v.w); };
+        bool mine = part == 0 && (int)threadIdx.x < lones && without(lone(threadIdx.x));
+        each_four<U>(inv, fours, fours / (int)parts + 64, [&](int t) { return ((t >> 6) * (int)parts + (int)part) * 64 + (t & 63); }, never,
+                     [&](int, int4 v) { mine |= any(v); });
+        if (threadIdx.x == 0) found = 0u;
+        if (!__syncthreads_or(mine)) return;
+        const uint32_t all = parts == 32 ? 0xffffffffu : (1u << parts) - 1u;
+        if ((int)threadIdx.x < lones && without(lone(threadIdx.x))) atomicOr(&found, 1u);
+        each_four<U>(inv, fours, fours, same, [&] { return *static_cast<volatile uint32_t *>(&found) == all; },
+                     [&](int i, int4 v) { if (any(v)) atomicOr(&found, 1u << ((i >> 6) & (parts - 1))); });
+        __syncthreads();
+        part = __popc(found & ((1u << part) - 1u));
+        parts = __popc(found);
+    }
+    uint32_t first = (uint32_t)((uint64_t)a.rows * part / parts);
+    uint32_t rows = (uint32_t)((uint64_t)a.rows * (part + 1) / parts) - first;
+    while (rows > 0) {
+        const uint32_t count = min(rows, kMarkWords * 32u);
+        for (int i = threadIdx.x; i < kMarkWords; i += blockDim.x) named[i] = 0u;
+        __syncthreads();
+        const auto mark = [&](int r) {
+            const uint32_t at = (uint32_t)r - first;   // (negative indexes are beyond any count)
+            if (at < count) atomicOr(&named[at >> 5], 1u << (at & 31));
+        };
+        each_four<U>(inv, fours, fours, same, never, [&](int, int4 v) { mark(v.x); mark(v.y); mark(v.z); mark(v.w); });
+        if ((int)threadIdx.x < lones) mark(lone(threadIdx.x));
+        __syncthreads();
+        for (uint32_t w = threadIdx.x >> 5; w * 32 < count; w += blockDim.x >> 5) {
+            uint32_t left = ~named[w];
+            if (count - w * 32 < 32) left &= (1u << (count - w * 32)) - 1u;
+            for (; left; left &= left - 1u)
+                zero_row(static_cast<T *>(a.out) + (long long)(first + w * 32 + (__ffs(left) - 1)) * a.ldo, a.d, lane);
+        }
+        __syncthreads();
+        first += count;
+        rows -= count;
+    }
+}
 
 // This thread's token and chunk; a CTA holds blockDim.x >> lanes_log2 tokens, and a row's
 // chunks are spread over col_blocks CTAs.
 __device__ __forceinline__ bool place(const Args &a, long long &t, int &chunk)
 {
     const int lanes = 1 << a.lanes_log2;
-    const long long tb = blockIdx.x / a.col_blocks;
+    const uint32_t block = blockIdx.x - a.fill;
+    const long long tb = block / a.col_blocks;
     t = tb * (blockDim.x >> a.lanes_log2) + (threadIdx.x >> a.lanes_log2);
-    chunk = (int)(blockIdx.x - tb * a.col_blocks) * (lanes * a.each) + (threadIdx.x & (lanes - 1));
+    chunk = (int)(block - tb * a.col_blocks) * (lanes * a.each) + (threadIdx.x & (lanes - 1));
     return t < a.T && chunk < a.chunks;
 }
 // The first column of chunk c (SHIFTED: chunk 0 is what stands before the first boundary).
@@ -212,10 +307,14 @@ template <int WAY, typename T> __device__ __forceinline__ void store(const Chunk
 }
 
 template <typename XT, int WAY>
-__global__ void __launch_bounds__(kCopyThreads)
+__global__ void __launch_bounds__(kCopyThreads, 8)   // (34 registers a thread: 16384 x 1 x 4096 47.3 us, 32: 42.3)
 scatter_rows_kernel(const Args a)
 {
     pdl_enter();
+    if (blockIdx.x < (uint32_t)a.fill) {
+        zero_unnamed<XT, 2>(a);
+        return;
+    }
     long long t;
     int chunk;
     if (!place(a, t, chunk)) return;
@@ -303,9 +402,13 @@ combine_backward_kernel(const Args a)
 {
     pdl_enter();
     constexpr int N = backward_threads(G);
+    if (blockIdx.x < (uint32_t)a.fill) {
+        zero_unnamed<XT, 8>(a);
+        return;
+    }
     __shared__ float part[N / 32][kMaxTopK];
     const int lane = threadIdx.x & (G - 1);
-    const long long t = (long long)blockIdx.x * (N / G) + threadIdx.x / G;
+    const long long t = (long long)(blockIdx.x - a.fill) * (N / G) + threadIdx.x / G;
     float dot[kMaxTopK];
 #pragma unroll
     for (int j = 0; j < kMaxTopK; ++j) dot[j] = 0.f;
@@ -449,14 +552,40 @@ bool lay_out(Args &a, int way, int each, int cta, dim3 *grid)
     a.each = each;
     a.col_blocks = ceil_div(a.chunks, each << a.lanes_log2);
     const int per = cta >> a.lanes_log2;
-    const long long ctas = ((long long)a.T + per - 1) / per * a.col_blocks;
+    const long long ctas = ((long long)a.T + per - 1) / per * a.col_blocks + a.fill;
     *grid = dim3((unsigned)ctas);
     return ctas <= 0x7fffffffLL;
+}
+
+// The CTAs that look for rows no slot names: 1, 2, 4, .. 32, one for 1024 rows, more for
+// rows that no slot can name.  They read inv once for every kMarkWords * 32 rows, so beyond
+// kMostMarked slots the rows are zeroed as a whole ahead (`all`: the grid is these CTAs alone,
+// and no slot names a row).
+constexpr long long kMostMarked = 1 << 21;
+void plan_fill(Args &a, bool all)
+{
+    if (all) a.T = 0;
+    const long long rows = a.rows, n = (long long)a.T * a.k, more = rows > n ? (rows - n) / 64 : 0, most = 4LL * device_sm_count();
+    a.fill = 1;
+    while (a.fill < 32 && a.fill * 1024LL < rows) a.fill *= 2;
+    a.fill += (int)(more < most ? more : most);
 }
 
 template <typename F> moe_status launched(F launch)
 {
     return launch() == cudaSuccess && cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+// A launch that writes grouped rows, `filled` or not: with its fill plan, or behind one that
+// zeroes every row.
+template <typename F> moe_status with_fill(const Args &a, bool filled, F launch)
+{
+    Args b = a;
+    if (!filled) return launch(b);
+    const bool all = a.T == 0 || (long long)a.T * a.k > kMostMarked;
+    plan_fill(b, all);
+    const moe_status st = launch(b);
+    return all && a.T > 0 && st == MOE_OK ? launch(a) : st;
 }
 
 // a kernel's types by run-time values
@@ -502,6 +631,83 @@ moe_status gather_sum(const Args &a, moe_dtype x_dt, moe_dtype out_dt, cudaStrea
     });
 }
 
+// `filled`: rows of the output that no slot names become zeros.
+moe_status dispatch(const void *x, moe_dtype dt, int T, int d, long long ldx, const int32_t *inv, int k, void *out, int rows,
+                    long long ldo, bool filled, cudaStream_t stream)
+{
+    bool go;
+    const moe_status st = check(T, k, rows, d, inv, &go);
+    if (st != MOE_OK) return st;
+    if (!matrix_ok(x, dt, ldx, d, T == 0) || !matrix_ok(out, dt, ldo, d, rows == 0 || (T == 0 && !filled))) return MOE_ERR_INVALID_ARG;
+    if (rows == 0 || (!go && !filled)) return MOE_OK;
+    Args a{};
+    a.x = x; a.out = out; a.inv = inv; a.ldx = ldx; a.ldo = ldo; a.T = T; a.k = k; a.rows = rows; a.d = d;
+    return with_type(dt, [&](auto *xt) {
+        using XT = std::remove_pointer_t<decltype(xt)>;
+        constexpr int kOff = sizeof(XT) == 4 ? APART : SHIFTED;
+        const auto go = [&](auto kern, int way) {
+            return with_fill(a, filled, [&](Args b) {
+                dim3 grid;
+                if (!lay_out(b, way, 1, kCopyThreads, &grid)) return MOE_ERR_UNSUPPORTED;
+                return launched([&] { return launch_pdl(kern, grid, dim3(kCopyThreads), 0, stream, b); });
+            });
+        };
+        if (vectors(x, ldx, d) && vectors(out, ldo, d)) return go(scatter_rows_kernel<XT, WHOLE>, WHOLE);
+        return go(scatter_rows_kernel<XT, kOff>, kOff);
+    });
+}
+
+moe_status combine_backward(const void *grad, moe_dtype grad_dt, int T, int d, long long ldg, const void *y, moe_dtype y_dt,
+                            int rows, long long ldy, const float *topk_w, const int32_t *inv, int k, void *dy, long long lddy,
+                            float *dw, bool filled, cudaStream_t stream)
+{
+    bool go;
+    const moe_status st = check(T, k, rows, d, inv, &go);
+    if (st != MOE_OK) return st;
+    if (!matrix_ok(grad, grad_dt, ldg, d, T == 0) || !matrix_ok(y, y_dt, ldy, d, rows == 0 || T == 0 || !dw))
+        return MOE_ERR_INVALID_ARG;
+    if ((dy && !matrix_ok(dy, y_dt, lddy, d, true)) || !aligned(dw, 4)) return MOE_ERR_INVALID_ARG;
+    filled = filled && dy && rows > 0;
+    if ((!go && !filled) || (!dy && !dw)) return MOE_OK;
+    if (go && (!topk_w || !aligned(topk_w, 4))) return MOE_ERR_INVALID_ARG;
+    Args a{};
+    a.x = y; a.g = grad; a.out = dy; a.dw = dw; a.topk_w = topk_w; a.inv = inv;
+    a.ldx = ldy; a.ldg = ldg; a.ldo = lddy; a.T = T; a.k = k; a.rows = rows; a.d = d;
+    const bool whole = vectors(grad, ldg, d) && (!dw || vectors(y, ldy, d)) && (!dy || vectors(dy, lddy, d));
+    return with_type(y_dt, [&](auto *xt) {
+        return with_type(grad_dt, [&](auto *gt) {
+            using XT = std::remove_pointer_t<decltype(xt)>;
+            using GT = std::remove_pointer_t<decltype(gt)>;
+            constexpr int kOff = sizeof(XT) == 4 ? APART : SHIFTED;
+            const auto go = [&](auto way) {
+                constexpr int WAY = decltype(way)::value;
+                // Threads of a token.  Many tokens: a warp, or two where it has more than two
+                // chunks a lane; few: as many as their chunks keep in use.  us, 32 / 64 / 128 / 512:
+                // 16384 x 2 x 128 12.7 / 18.5 / 28.1, x 2048 52.7 / 50.6 / 52.3; 1945 x 7 x 278
+                // 18.2 / 19.5 / 27.5; 999 x 3 x 1000 7.0 / 5.2 / 5.3 / 13.1; 3000 x 8 x 8192
+                // 133 / 137 / 131; 300 x 4 x 4096 18.6 / 10.8 / 7.4 / 6.3; 64 x 2 x 2048 3.6 / 2.5 /
+                // 1.9 / 2.1; 16 x 2 x 8192 10.3 / 5.8 / 3.6 / 2.5.
+                const int sms = device_sm_count(), chunks = ceil_div(d, V);
+                const auto launch = [&](auto group) {
+                    constexpr int G = decltype(group)::value, N = backward_threads(G);
+                    return with_fill(a, filled, [&](Args b) {
+                        b.chunks = chunks_of(d, WAY, G);
+                        const long long ctas = (long long)ceil_div(b.T, N / G) + b.fill;
+                        return launched([&] {
+                            return launch_pdl(combine_backward_kernel<XT, GT, WAY, G>, dim3((unsigned)ctas), dim3(N), 0, stream, b);
+                        });
+                    });
+                };
+                if (T >= 10 * sms && chunks <= 64) return launch(std::integral_constant<int, 32>());
+                if (chunks <= 64 || (T >= 10 * sms && chunks < 1024)) return launch(std::integral_constant<int, 64>());
+                if (T <= 2 * sms && chunks > 256) return launch(std::integral_constant<int, 512>());
+                return launch(std::integral_constant<int, 128>());
+            };
+            return whole ? go(WayOf<WHOLE>()) : go(WayOf<kOff>());
+        });
+    });
+}
+
 }  // namespace rows
 }  // namespace moe
 
@@ -513,24 +719,13 @@ extern "C" {
 moe_status moe_dispatch(const void *x, moe_dtype dt, int T, int d, long long ldx, const int32_t *inv, int k, void *out,
                         int rows, long long ldo, moe_stream stream)
 {
-    bool go;
-    const moe_status st = check(T, k, rows, d, inv, &go);
-    if (st != MOE_OK) return st;
-    if (!matrix_ok(x, dt, ldx, d, T == 0) || !matrix_ok(out, dt, ldo, d, rows == 0 || T == 0)) return MOE_ERR_INVALID_ARG;
-    if (!go || rows == 0) return MOE_OK;
-    Args a{};
-    a.x = x; a.out = out; a.inv = inv; a.ldx = ldx; a.ldo = ldo; a.T = T; a.k = k; a.rows = rows; a.d = d;
-    return with_type(dt, [&](auto *xt) {
-        using XT = std::remove_pointer_t<decltype(xt)>;
-        constexpr int kOff = sizeof(XT) == 4 ? APART : SHIFTED;
-        const auto go = [&](auto kern, int way) {
-            dim3 grid;
-            if (!lay_out(a, way, 1, kCopyThreads, &grid)) return MOE_ERR_UNSUPPORTED;
-            return launched([&] { return launch_pdl(kern, grid, dim3(kCopyThreads), 0, static_cast<cudaStream_t>(stream), a); });
-        };
-        if (vectors(x, ldx, d) && vectors(out, ldo, d)) return go(scatter_rows_kernel<XT, WHOLE>, WHOLE);
-        return go(scatter_rows_kernel<XT, kOff>, kOff);
-    });
+    return dispatch(x, dt, T, d, ldx, inv, k, out, rows, ldo, false, static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_dispatch_filled(const void *x, moe_dtype dt, int T, int d, long long ldx, const int32_t *inv, int k, void *out,
+                               int rows, long long ldo, moe_stream stream)
+{
+    return dispatch(x, dt, T, d, ldx, inv, k, out, rows, ldo, true, static_cast<cudaStream_t>(stream));
 }
 
 moe_status moe_dispatch_backward(const void *grad, moe_dtype dt, int rows, int d, long long ldg, const int32_t *inv, int T,
@@ -564,48 +759,16 @@ moe_status moe_combine_backward(const void *grad, moe_dtype grad_dt, int T, int 
                                 moe_dtype y_dt, int rows, long long ldy, const float *topk_w, const int32_t *inv, int k,
                                 void *dy, long long lddy, float *dw, moe_stream stream)
 {
-    bool go;
-    const moe_status st = check(T, k, rows, d, inv, &go);
-    if (st != MOE_OK) return st;
-    if (!matrix_ok(grad, grad_dt, ldg, d, T == 0) || !matrix_ok(y, y_dt, ldy, d, rows == 0 || T == 0 || !dw))
-        return MOE_ERR_INVALID_ARG;
-    if ((dy && !matrix_ok(dy, y_dt, lddy, d, true)) || !aligned(dw, 4)) return MOE_ERR_INVALID_ARG;
-    if (!go || (!dy && !dw)) return MOE_OK;
-    if (!topk_w || !aligned(topk_w, 4)) return MOE_ERR_INVALID_ARG;
-    Args a{};
-    a.x = y; a.g = grad; a.out = dy; a.dw = dw; a.topk_w = topk_w; a.inv = inv;
-    a.ldx = ldy; a.ldg = ldg; a.ldo = lddy; a.T = T; a.k = k; a.rows = rows; a.d = d;
-    const bool whole = vectors(grad, ldg, d) && (!dw || vectors(y, ldy, d)) && (!dy || vectors(dy, lddy, d));
-    return with_type(y_dt, [&](auto *xt) {
-        return with_type(grad_dt, [&](auto *gt) {
-            using XT = std::remove_pointer_t<decltype(xt)>;
-            using GT = std::remove_pointer_t<decltype(gt)>;
-            constexpr int kOff = sizeof(XT) == 4 ? APART : SHIFTED;
-            const auto go = [&](auto way) {
-                constexpr int WAY = decltype(way)::value;
-                // Threads of a token.  Many tokens: a warp, or two where it has more than two
-                // chunks a lane; few: as many as their chunks keep in use.  us, 32 / 64 / 128 / 512:
-                // 16384 x 2 x 128 12.7 / 18.5 / 28.1, x 2048 52.7 / 50.6 / 52.3; 1945 x 7 x 278
-                // 18.2 / 19.5 / 27.5; 999 x 3 x 1000 7.0 / 5.2 / 5.3 / 13.1; 3000 x 8 x 8192
-                // 133 / 137 / 131; 300 x 4 x 4096 18.6 / 10.8 / 7.4 / 6.3; 64 x 2 x 2048 3.6 / 2.5 /
-                // 1.9 / 2.1; 16 x 2 x 8192 10.3 / 5.8 / 3.6 / 2.5.
-                const int sms = device_sm_count(), chunks = ceil_div(d, V);
-                const auto launch = [&](auto group) {
-                    constexpr int G = decltype(group)::value, N = backward_threads(G);
-                    a.chunks = chunks_of(d, WAY, G);
-                    return launched([&] {
-                        return launch_pdl(combine_backward_kernel<XT, GT, WAY, G>, dim3((unsigned)ceil_div(T, N / G)), dim3(N), 0,
-                                          static_cast<cudaStream_t>(stream), a);
-                    });
-                };
-                if (T >= 10 * sms && chunks <= 64) return launch(std::integral_constant<int, 32>());
-                if (chunks <= 64 || (T >= 10 * sms && chunks < 1024)) return launch(std::integral_constant<int, 64>());
-                if (T <= 2 * sms && chunks > 256) return launch(std::integral_constant<int, 512>());
-                return launch(std::integral_constant<int, 128>());
-            };
-            return whole ? go(WayOf<WHOLE>()) : go(WayOf<kOff>());
-        });
-    });
+    return combine_backward(grad, grad_dt, T, d, ldg, y, y_dt, rows, ldy, topk_w, inv, k, dy, lddy, dw, false,
+                            static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_combine_backward_filled(const void *grad, moe_dtype grad_dt, int T, int d, long long ldg, const void *y,
+                                       moe_dtype y_dt, int rows, long long ldy, const float *topk_w, const int32_t *inv,
+                                       int k, void *dy, long long lddy, float *dw, moe_stream stream)
+{
+    return combine_backward(grad, grad_dt, T, d, ldg, y, y_dt, rows, ldy, topk_w, inv, k, dy, lddy, dw, true,
+                            static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -151,8 +151,10 @@ PyObject *dispatch(PyObject *, PyObject *const *a, Py_ssize_t n)
     const c10::cuda::CUDAGuard guard(dev);
     Tensor h0;
     const Tensor &out = given_or_empty(a[3], "out", h0, shape, x.scalar_type(), dev);
-    const moe_status st = moe_dispatch(px, real_dtype(x), int_of(s.T, "x"), int_of(x.size(1), "x"), row_stride(x), s.inv, s.k,
-                                       out.data_ptr(), int_of(shape[0], "out"), row_stride(out), stream_of(dev));
+    // (a new output is written as a whole)
+    const moe_status st = (given(a[3]) ? moe_dispatch : moe_dispatch_filled)(
+        px, real_dtype(x), int_of(s.T, "x"), int_of(x.size(1), "x"), row_stride(x), s.inv, s.k, out.data_ptr(),
+        int_of(shape[0], "out"), row_stride(out), stream_of(dev));
     if (st != MOE_OK) return failed(st);
     return wrap(a[3], out);
     END_HANDLE_TH_ERRORS
@@ -255,9 +257,9 @@ PyObject *combine_backward(PyObject *, PyObject *const *a, Py_ssize_t n)
         lddy = row_stride(dy);
     }
     if (want_dw) pdw = given_or_empty(a[7], "dw", h1, w_shape, ScalarType::Float, dev).data_ptr<float>();
-    const moe_status st = moe_combine_backward(pg, real_dtype(g), int_of(s.T, "topk_w"), int_of(y.size(1), "y"), row_stride(g),
-                                               py, real_dtype(y), int_of(y.size(0), "y"), row_stride(y), pw, s.inv, s.k, pdy,
-                                               lddy, pdw, stream_of(dev));
+    const moe_status st = (given(a[6]) ? moe_combine_backward : moe_combine_backward_filled)(
+        pg, real_dtype(g), int_of(s.T, "topk_w"), int_of(y.size(1), "y"), row_stride(g), py, real_dtype(y), int_of(y.size(0), "y"),
+        row_stride(y), pw, s.inv, s.k, pdy, lddy, pdw, stream_of(dev));
     if (st != MOE_OK) return failed(st);
     auto result = [](bool wanted, PyObject *o, const Tensor &t) {
         if (wanted) return wrap(o, t);

@@ -573,7 +573,8 @@ MOE_API moe_status moe_gate_up_fp8b(const void *x_q, const float *x_s, int x_row
  *   out, a token dropped by the caller): it adds nothing, nothing is written for it, and
  *   its weight's gradient is 0.  Within a call that writes grouped rows (moe_dispatch,
  *   moe_combine_backward) the rows that inv names are distinct; grouped rows that no slot
- *   names are left as they were.
+ *   names are left as they were, or become zeros in the calls' `_filled` forms (for an output
+ *   whose memory holds nothing yet: the gradient of such a row is 0).
  *   Matrices are fp32 or bf16, rows `ld` elements apart (ld >= d), of any width d >= 1 and
  *   alignment of their type; widths and distances that are multiples of 8 with 16-byte
  *   aligned pointers move 16 bytes at a time.  Sums run over the slots in order, in
@@ -588,6 +589,14 @@ MOE_API moe_status moe_gate_up_fp8b(const void *x_q, const float *x_s, int x_row
 MOE_API moe_status moe_dispatch(const void *x, moe_dtype dt, int T, int d, long long ldx,
                                 const int32_t *inv, int k, void *out, int rows, long long ldo,
                                 moe_stream stream);
+
+/*
+ * moe_dispatch_filled -- as moe_dispatch, and every row of out that no slot names becomes zeros
+ *   (all of them where T is 0).
+ */
+MOE_API moe_status moe_dispatch_filled(const void *x, moe_dtype dt, int T, int d, long long ldx,
+                                       const int32_t *inv, int k, void *out, int rows,
+                                       long long ldo, moe_stream stream);
 
 /*
  * moe_dispatch_backward -- its gradient: dx[t] = sum_j grad[inv[t*k + j]].
@@ -617,6 +626,16 @@ MOE_API moe_status moe_combine_backward(const void *grad, moe_dtype grad_dt, int
                                         long long ldy, const float *topk_w, const int32_t *inv,
                                         int k, void *dy, long long lddy, float *dw,
                                         moe_stream stream);
+
+/*
+ * moe_combine_backward_filled -- as moe_combine_backward, and every row of dy that no slot names
+ *   becomes zeros (all of them where T is 0).
+ */
+MOE_API moe_status moe_combine_backward_filled(const void *grad, moe_dtype grad_dt, int T, int d,
+                                               long long ldg, const void *y, moe_dtype y_dt,
+                                               int rows, long long ldy, const float *topk_w,
+                                               const int32_t *inv, int k, void *dy, long long lddy,
+                                               float *dw, moe_stream stream);
 
 /*
  * 8-bit integer operators ("i8"): the expert FFN with int8 codes on both sides of its

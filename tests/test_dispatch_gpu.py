@@ -384,3 +384,110 @@ def test_device_refusals(moe):
 def test_combine_by_threads_of_a_token(moe, dt, odt, T, k, d):
     """Many and few tokens, narrow and wide: one warp, two, four or sixteen to a token."""
     test_combine_and_its_gradients(moe, dt, odt, T, k, d)
+
+
+def poisoned(moe, call):
+    """`call`'s new outputs out of memory that held NaN: blocks of every size it allocates are
+    filled and given back first."""
+    shapes = [t.shape for t in call() if t is not None]
+    dtypes = [t.dtype for t in call() if t is not None]
+    for _ in range(2):
+        held = [torch.full(s, float("nan"), dtype=t, device=DEV) for s, t in zip(shapes, dtypes) for _ in range(3)]
+        del held
+    return call()
+
+
+def padded_slots(T, k, rows, drop, seed=0):
+    """inv of T*k slots over `rows` rows, some of them dropped, and which rows are named."""
+    inv = perm(max(rows, T * k), seed=seed)[:T * k].clone()      # (beyond rows: dropped, where rows < T*k)
+    if drop:
+        values = torch.tensor([-1, rows, 2 ** 31 - 1, -2 ** 31, -5, rows + 1], dtype=torch.int32, device=DEV)
+        at = torch.arange(0, T * k, drop, device=DEV)
+        inv[at] = values[torch.arange(len(at), device=DEV) % 6]
+    named = torch.zeros(rows, dtype=torch.bool, device=DEV)
+    named[inv[(inv >= 0) & (inv < rows)].long()] = True
+    return inv, named
+
+
+FILL = [(1, 1, 5, 1, 0), (0, 2, 40, 16, 0), (7, 3, 21, 33, 2), (50, 4, 230, 5, 7), (600, 2, 1200, 264, 5), (600, 2, 70000, 24, 5),
+        (1700, 2, 3400, 520, 9), (1700, 8, 13600, 48, 1), (1700, 3, 5000, 1001, 11), (40, 2, 80, 4100, 3), (5000, 8, 41000, 3, 4),
+        (300, 2, 500, 64, 0)]
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("T,k,rows,d,drop", FILL)
+def test_rows_without_slots_are_zeros_in_new_outputs(moe, dt, T, k, rows, d, drop):
+    """Padded batches and dropped slots: a new output's other rows hold zeros, whatever the
+    memory held; the named ones are the same bits as in an output that is given."""
+    inv, named = padded_slots(T, k, rows, drop)
+    y, w, g = rand(rows, d).to(DT[dt]), rand(T, k), rand(T, d, seed=1).to(DT[dt])
+    dy, dw = poisoned(moe, lambda: moe.moe_combine_backward(g, y, w, inv))
+    given = torch.full_like(y, 7.0)
+    dw2 = moe.moe_combine_backward(g, y, w, inv, dy=given)[1]
+    assert torch.equal(dy[named], given[named]) and torch.equal(dw, dw2)
+    assert not dy[~named].any() and bool((given[~named] == 7).all())
+    check_combine_backward(dy, dw, g, y, w, inv)
+    if rows <= T * k:                                      # a dispatch's own rows: T*k
+        inv, named = padded_slots(T, k, T * k, drop)
+        sent, = poisoned(moe, lambda: (moe.moe_dispatch(g, inv, k),))
+        given = torch.full_like(sent, 7.0)
+        moe.moe_dispatch(g, inv, k, out=given)
+        assert torch.equal(sent[named], given[named]) and not sent[~named].any() and bool((given[~named] == 7).all())
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("off,d,wide", [(0, 64, 80), (1, 61, 97), (3, 5, 70), (4, 64, 76)])
+def test_filled_rows_apart(moe, dt, off, d, wide):
+    """The C calls' filled forms into column slices: zeros inside them only; inv off 16-byte
+    boundaries; replayed from a graph on other slots."""
+    import ctypes
+    L, t = moe.load_library(), DT[dt]
+    T, k, rows = 200, 3, 700
+    both = torch.zeros(T * k + 3, dtype=torch.int32, device=DEV)
+    inv = both[off % 4:off % 4 + T * k]
+    base = torch.full((rows, wide), 7.0, device=DEV, dtype=t)
+    out, x = base[:, off:off + d], rand(T, d).to(t)
+    w, y, dw = rand(T, k), rand(rows, d, seed=2).to(t), torch.empty(T, k, device=DEV)
+    p = lambda v: ctypes.c_void_p(v.data_ptr())
+    stream = lambda: ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    e = 0 if dt == "f32" else 1
+
+    def sent():
+        assert L.moe_dispatch_filled(p(x), e, T, d, d, p(inv), k, p(out), rows, wide, stream()) == 0
+
+    def back():
+        assert L.moe_combine_backward_filled(p(x), e, T, d, d, p(y), e, rows, d, p(w), p(inv), k, p(out), wide, p(dw), stream()) == 0
+    inv.copy_(padded_slots(T, k, rows, 5)[0])
+    sent(), back()
+    graphs = []
+    for call in (sent, back):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call()
+    for seed, drop in ((1, 0), (2, 4), (3, 1)):
+        new, named = padded_slots(T, k, rows, drop, seed=seed)
+        inv.copy_(new)
+        slot = ((new >= 0) & (new < rows)).nonzero()[:, 0]
+        for i, graph in enumerate(graphs):
+            base.fill_(7.0)
+            graph.replay()
+            assert not out[~named].any() and bool((base[:, :off] == 7).all()) and bool((base[:, off + d:] == 7).all())
+            if i == 0:
+                assert torch.equal(out[new[slot].long()], x[slot // k])
+            else:
+                check_combine_backward(out, dw, x, y, w, new)
+
+
+def test_filled_beyond_the_marked_slots(moe):
+    """More slots than are marked bit by bit (2^21): every row is zeroed ahead."""
+    T, k, d = 300_000, 8, 3
+    rows = T * k
+    inv, named = padded_slots(T, k, rows, 3)
+    x = rand(T, d).bfloat16()
+    sent, = poisoned(moe, lambda: (moe.moe_dispatch(x, inv, k),))
+    slot = ((inv >= 0) & (inv < rows)).nonzero()[:, 0]
+    assert torch.equal(sent[inv[slot].long()], x[slot // k]) and not sent[~named].any()
+    y, w = rand(rows, d).bfloat16(), rand(T, k)
+    dy, dw = poisoned(moe, lambda: moe.moe_combine_backward(x, y, w, inv))
+    assert not dy[~named].any()
+    check_combine_backward(dy, dw, x, y, w, inv)

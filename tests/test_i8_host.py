@@ -223,3 +223,22 @@ def test_widths_near_the_end_of_32_bits_are_refused(lib):
         assert lib.moe_gemm_fp8b(FAKE, FAKE, 1, K, K, FAKE, FAKE, N, FAKE, F32, N, None, None) == U
         assert lib.moe_gate_up_fp8b(FAKE, FAKE, 1, K, K, FAKE, FAKE, FAKE, FAKE, 1, N - N % 16, None, None, 1, FAKE, FAKE, FAKE, wide,
                                     None, None) == U
+
+
+def test_filled_forms_check_what_the_plain_ones_do(lib):
+    send = lambda **kw: lib.moe_dispatch_filled(*dict(dict(x=FAKE, dt=F32, T=4, d=5, ldx=5, inv=FAKE, k=2, out=FAKE, rows=8, ldo=5),
+                                                      **kw).values(), None)
+    back = lambda **kw: lib.moe_combine_backward_filled(*dict(
+        dict(g=FAKE, gdt=F32, T=4, d=5, ldg=5, y=FAKE, dt=F32, rows=8, ldy=5, w=FAKE, inv=FAKE, k=2, dy=FAKE, lddy=5, dw=FAKE),
+        **kw).values(), None)
+    for call in (send, back):
+        for bad in (dict(T=-1), dict(k=0), dict(rows=-1), dict(d=0), dict(inv=None), dict(inv=ODD2), dict(dt=Q8_0)):
+            assert call(**bad) == I, bad
+        assert call(k=9) == U and call(T=2 ** 31 - 1) == U
+    for bad in (dict(x=None), dict(out=None), dict(ldo=4), dict(out=ODD1), dict(T=0, out=None)):
+        assert send(**bad) == I, bad
+    for bad in (dict(g=None), dict(y=None), dict(w=None), dict(lddy=4), dict(dw=ODD2), dict(dy=ODD1)):
+        assert back(**bad) == I, bad
+    assert send(rows=0, out=None) == OK and send(T=0, rows=0, x=None, out=None, inv=None) == OK
+    assert back(T=0, rows=0, g=None, y=None, w=None, inv=None) == OK and back(T=0, dy=None, g=None, y=None, w=None, inv=None) == OK
+    assert back(dy=None, dw=None, y=None) == OK
