@@ -614,20 +614,99 @@ def moe_gate_up_fp8b(x_q: torch.Tensor, x_s: torch.Tensor, wg_q: torch.Tensor, w
 # fp32 scale per row).  Their tensors are checked, and their outputs allocated, in the
 # compiled module too (csrc/i8_binding.cpp).
 
+# Autograd: where an input requires grad and gradients are recorded, the compiled module
+# answers NotImplemented, and the call is made by a Function, whose backward pass is made of the
+# same four calls (dispatch and its backward are each other's; combine's backward is linear in
+# each of grad, y and topk_w).
+
+def _rows(g: torch.Tensor) -> torch.Tensor:
+    """A gradient as the calls take it (one of a sum is a single value seen everywhere)."""
+    return g if g.stride(1) == 1 and g.stride(0) >= g.shape[1] else g.contiguous()
+
+
+class _Dispatch(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, inv, k, rows):
+        ctx.save_for_backward(inv)
+        ctx.k = k
+        if rows is None:
+            return moe_dispatch(x, inv, k)
+        return moe_dispatch(x, inv, k, out=x.new_zeros(rows, x.shape[1]))
+
+    @staticmethod
+    def backward(ctx, g):
+        return moe_dispatch_backward(_rows(g), ctx.saved_tensors[0], ctx.k), None, None, None
+
+
+class _DispatchBackward(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, grad, inv, k):
+        ctx.save_for_backward(inv)
+        ctx.k, ctx.rows = k, grad.shape[0]
+        return moe_dispatch_backward(grad, inv, k)
+
+    @staticmethod
+    def backward(ctx, g):
+        return _Dispatch.apply(_rows(g), ctx.saved_tensors[0], ctx.k, ctx.rows), None, None
+
+
+class _Combine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, y, topk_w, inv, out_dtype):
+        ctx.save_for_backward(y, topk_w, inv)
+        return moe_combine(y, topk_w, inv, out_dtype=out_dtype)
+
+    @staticmethod
+    def backward(ctx, g):
+        y, w, inv = ctx.saved_tensors
+        return (*moe_combine_backward(_rows(g), y, w, inv, *ctx.needs_input_grad[:2]), None, None)
+
+
+class _CombineBackward(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, grad, y, topk_w, inv, want_dy, want_dw):
+        ctx.save_for_backward(grad, y, topk_w, inv)
+        ctx.set_materialize_grads(False)
+        return moe_combine_backward(grad, y, topk_w, inv, want_dy, want_dw)
+
+    @staticmethod
+    def backward(ctx, of_dy, of_dw):
+        grad, y, w, inv = ctx.saved_tensors
+        g_grad = g_y = g_w = None
+        if of_dy is not None:                     # dy = topk_w grad, by slots
+            of_dy = _rows(of_dy)
+            if ctx.needs_input_grad[0]:
+                g_grad = moe_combine(of_dy, w, inv)
+            if ctx.needs_input_grad[2]:
+                g_w = moe_combine_backward(grad, of_dy, w, inv, want_dy=False)[1]
+        if of_dw is not None:                     # dw = <grad, y>, by slots
+            of_dw = of_dw.contiguous()
+            if ctx.needs_input_grad[0]:
+                more = moe_combine(y, of_dw, inv)
+                g_grad = more if g_grad is None else g_grad + more
+            if ctx.needs_input_grad[1]:
+                g_y = moe_combine_backward(grad, y, of_dw, inv, want_dw=False)[0]
+        return None if g_grad is None else g_grad.to(grad.dtype), g_y, g_w, None, None, None
+
+
 def moe_dispatch(x: torch.Tensor, inv: torch.Tensor, k: int, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Tokens x [T, d] (fp32 / bf16) into grouped order -> out [rows, d]: out[inv[t*k + j]] = x[t].
 
     inv [T*k] (moe_permute).  rows is T*k, or out's if it is given.  Rows that no slot
     names are left as they were in an output that is given, and zeros in one allocated
-    here; a slot whose inv is outside [0, rows) writes nothing.
+    here; a slot whose inv is outside [0, rows) writes nothing.  Recorded for autograd where x
+    requires grad (out is then not to be given).
     """
-    return _checked((_fp8b_module or _fp8b()).dispatch(x, inv, k, out), "moe_dispatch")
+    got = (_fp8b_module or _fp8b()).dispatch(x, inv, k, out)
+    return _Dispatch.apply(x, inv, k, None) if got is NotImplemented else _checked(got, "moe_dispatch")
 
 
 def moe_dispatch_backward(grad: torch.Tensor, inv: torch.Tensor, k: int,
                           out: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """moe_dispatch's gradient -> [T, d] in grad's type: out[t] = sum_j grad[inv[t*k + j]]."""
-    return _checked((_fp8b_module or _fp8b()).dispatch_backward(grad, inv, k, out), "moe_dispatch_backward")
+    """moe_dispatch's gradient -> [T, d] in grad's type: out[t] = sum_j grad[inv[t*k + j]].
+    Recorded for autograd where grad requires it (out is then not to be given)."""
+    got = (_fp8b_module or _fp8b()).dispatch_backward(grad, inv, k, out)
+    return _DispatchBackward.apply(grad, inv, k) if got is NotImplemented else _checked(got, "moe_dispatch_backward")
 
 
 def moe_combine(y: torch.Tensor, topk_w: torch.Tensor, inv: torch.Tensor, out: Optional[torch.Tensor] = None,
@@ -636,9 +715,11 @@ def moe_combine(y: torch.Tensor, topk_w: torch.Tensor, inv: torch.Tensor, out: O
     out[t] = sum_j topk_w[t, j] y[inv[t*k + j]].
 
     topk_w [T, k] (moe_route), inv [T*k] (moe_permute); a slot whose inv is outside
-    [0, rows) adds nothing.
+    [0, rows) adds nothing.  Recorded for autograd where y or topk_w requires grad (out is then
+    not to be given).
     """
-    return _checked((_fp8b_module or _fp8b()).combine(y, topk_w, inv, out, out_dtype), "moe_combine")
+    got = (_fp8b_module or _fp8b()).combine(y, topk_w, inv, out, out_dtype)
+    return _Combine.apply(y, topk_w, inv, out_dtype) if got is NotImplemented else _checked(got, "moe_combine")
 
 
 def moe_combine_backward(grad: torch.Tensor, y: torch.Tensor, topk_w: torch.Tensor, inv: torch.Tensor,
@@ -648,10 +729,13 @@ def moe_combine_backward(grad: torch.Tensor, y: torch.Tensor, topk_w: torch.Tens
     dy[inv[t*k + j]] = topk_w[t, j] grad[t], dw[t, j] = <grad[t], y[inv[t*k + j]]>.
 
     One that is not wanted is None.  Rows of dy that no slot names are left as they were in
-    a dy that is given, and zeros (their gradient) in one allocated here.
+    a dy that is given, and zeros (their gradient) in one allocated here.  Recorded for
+    autograd where grad, y or topk_w requires it (dy and dw are then not to be given).
     """
-    return _checked((_fp8b_module or _fp8b()).combine_backward(grad, y, topk_w, inv, want_dy, want_dw, dy, dw),
-                    "moe_combine_backward")
+    got = (_fp8b_module or _fp8b()).combine_backward(grad, y, topk_w, inv, want_dy, want_dw, dy, dw)
+    if got is NotImplemented:
+        return _CombineBackward.apply(grad, y, topk_w, inv, want_dy, want_dw)
+    return _checked(got, "moe_combine_backward")
 
 
 def moe_i8_workspace_size(rows: int, K: int) -> int:

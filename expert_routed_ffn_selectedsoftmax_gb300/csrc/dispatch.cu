@@ -565,9 +565,11 @@ constexpr long long kMostMarked = 1 << 21;
 void plan_fill(Args &a, bool all)
 {
     if (all) a.T = 0;
-    const long long rows = a.rows, n = (long long)a.T * a.k, more = rows > n ? (rows - n) / 64 : 0, most = 4LL * device_sm_count();
+    const long long rows = a.rows, n = (long long)a.T * a.k;
     a.fill = 1;
     while (a.fill < 32 && a.fill * 1024LL < rows) a.fill *= 2;
+    if (rows <= n) return;
+    const long long more = (rows - n) / 64, most = 4LL * device_sm_count();
     a.fill += (int)(more < most ? more : most);
 }
 

@@ -1,6 +1,8 @@
 // i8_binding.cpp -- the Python side of the 8-bit integer operators and of dispatch and
 // combine (checks, outputs, the call into the C ABI), part of the module of
 // fp8b_binding.cpp.  Nothing of the operators is computed here.
+#include <c10/core/GradMode.h>
+
 #include "binding.h"
 
 namespace {
@@ -122,6 +124,19 @@ Slots slots_of(PyObject *o, int64_t k, c10::Device dev)
     TORCH_CHECK_VALUE(inv.numel() % k == 0, "inv: ", inv.numel(), " values, expected ", k, " a token");
     return {static_cast<const int32_t *>(p), inv.numel() / k, int_of(k, "k")};
 }
+// Whether an input requires grad where gradients are recorded: the call is then left to the
+// Python side (the answer is NotImplemented), which comes again without recording.
+bool recorded(const char *call, bool has_output, std::initializer_list<const Tensor *> inputs)
+{
+    if (!c10::GradMode::is_enabled()) return false;
+    for (const Tensor *t : inputs)
+        if (t->requires_grad()) {
+            TORCH_CHECK(!has_output, call, ": an output that is given keeps no graph, and an input requires grad: detach it, or "
+                        "let the call allocate its outputs");
+            return true;
+        }
+    return false;
+}
 void need_matrix(const Tensor &t, const char *name)
 {
     TORCH_CHECK_VALUE(t.dim() == 2, name, ": ", t.dim(), " dimensions, expected 2");
@@ -148,6 +163,7 @@ PyObject *dispatch(PyObject *, PyObject *const *a, Py_ssize_t n)
         need(out, "out", shape, kind_of(x), dev, true);
     }
     need_cuda(x, "x");
+    if (recorded("moe_dispatch", given(a[3]), {&x})) Py_RETURN_NOTIMPLEMENTED;
     const c10::cuda::CUDAGuard guard(dev);
     Tensor h0;
     const Tensor &out = given_or_empty(a[3], "out", h0, shape, x.scalar_type(), dev);
@@ -175,6 +191,7 @@ PyObject *dispatch_backward(PyObject *, PyObject *const *a, Py_ssize_t n)
     const int64_t shape[2] = {s.T, g.size(1)};
     if (given(a[3])) need(tensor_of(a[3], "out"), "out", shape, kind_of(g), dev, true);
     need_cuda(g, "grad");
+    if (recorded("moe_dispatch_backward", given(a[3]), {&g})) Py_RETURN_NOTIMPLEMENTED;
     const c10::cuda::CUDAGuard guard(dev);
     Tensor h0;
     const Tensor &out = given_or_empty(a[3], "out", h0, shape, g.scalar_type(), dev);
@@ -212,6 +229,7 @@ PyObject *combine(PyObject *, PyObject *const *a, Py_ssize_t n)
     const int64_t shape[2] = {s.T, y.size(1)};
     if (given(a[3])) need(tensor_of(a[3], "out"), "out", shape, REAL, dev, true);
     need_cuda(y, "y");
+    if (recorded("moe_combine", given(a[3]), {&y, &tensor_of(a[1], "topk_w")})) Py_RETURN_NOTIMPLEMENTED;
     const c10::cuda::CUDAGuard guard(dev);
     Tensor h0;
     const Tensor &out = given_or_empty(a[3], "out", h0, shape, out_dtype, dev);
@@ -246,6 +264,8 @@ PyObject *combine_backward(PyObject *, PyObject *const *a, Py_ssize_t n)
     if (given(a[6])) need(tensor_of(a[6], "dy"), "dy", y.sizes(), kind_of(y), dev, true);
     if (given(a[7])) need(tensor_of(a[7], "dw"), "dw", w_shape, FLOAT32, dev);
     need_cuda(g, "grad");
+    if (recorded("moe_combine_backward", given(a[6]) || given(a[7]), {&g, &y, &tensor_of(a[2], "topk_w")}))
+        Py_RETURN_NOTIMPLEMENTED;
     const c10::cuda::CUDAGuard guard(dev);
     Tensor h0, h1;
     void *pdy = nullptr;

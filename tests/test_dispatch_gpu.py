@@ -491,3 +491,114 @@ def test_filled_beyond_the_marked_slots(moe):
     dy, dw = poisoned(moe, lambda: moe.moe_combine_backward(x, y, w, inv))
     assert not dy[~named].any()
     check_combine_backward(dy, dw, x, y, w, inv)
+
+
+def test_calls_are_recorded(moe):
+    """Inputs that require grad: the outputs carry their graph, and the gradients are the backward
+    calls' own bits (bf16 and fp32, a padded batch, dropped slots, one input alone, a gradient
+    that is one value seen everywhere, one whose rows lie apart)."""
+    T, k, d, rows = 60, 3, 40, 200
+    for dt, odt in ((torch.float32, torch.float32), (torch.bfloat16, torch.float32), (torch.bfloat16, torch.bfloat16)):
+        inv, named = padded_slots(T, k, rows, 7)
+        y, w = rand(rows, d).to(dt).requires_grad_(), rand(T, k).requires_grad_()
+        g = rand(T, d, seed=3).to(odt)
+        out = moe.moe_combine(y, w, inv, out_dtype=odt)
+        assert out.requires_grad and torch.equal(out, moe.moe_combine(y.detach(), w.detach(), inv, out_dtype=odt))
+        out.backward(g)
+        dy, dw = moe.moe_combine_backward(g, y.detach(), w.detach(), inv)
+        assert torch.equal(y.grad, dy) and torch.equal(w.grad, dw) and not y.grad[~named].any()
+        for a, b, want in ((y, w.detach(), dy), (y.detach(), w, dw)):
+            got, = torch.autograd.grad(moe.moe_combine(a, b, inv, out_dtype=odt), a if a.requires_grad else b, g)
+            assert torch.equal(got, want)
+        one = moe.moe_combine(y, w, inv, out_dtype=odt)
+        got = torch.autograd.grad(one.sum(), (y, w))
+        want = moe.moe_combine_backward(torch.ones_like(one).detach(), y.detach(), w.detach(), inv)
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+        x = rand(T, d, seed=4).to(dt).requires_grad_()
+        inv, named = padded_slots(T, k, T * k, 5)
+        wide = rand(T * k, 2 * d, seed=5).to(dt)
+        sent = moe.moe_dispatch(x, inv, k)
+        assert sent.requires_grad and torch.equal(sent, moe.moe_dispatch(x.detach(), inv, k))
+        got, = torch.autograd.grad(sent, x, wide[:, :d])
+        assert torch.equal(got, moe.moe_dispatch_backward(wide[:, :d], inv, k))
+        with torch.no_grad():
+            assert not moe.moe_dispatch(x, inv, k).requires_grad
+            moe.moe_dispatch(x, inv, k, out=torch.zeros_like(sent))
+        assert not moe.moe_dispatch(x.detach(), inv, k).requires_grad
+
+
+def test_recorded_twice(moe):
+    """Gradients of the gradients against autograd's of the plain form in 64 bits.  Every value
+    is a sum of at most d = 40 products of two factors, in fp32 and in some order: (d + 8) 2^-24
+    of the sum of their magnitudes, which the plain form gives for inputs without signs."""
+    T, k, d, rows = 30, 3, 40, 100
+    inv, _ = padded_slots(T, k, rows, 7)
+    at = inv.view(T, k).long()
+    ok = ((at >= 0) & (at < rows))[..., None]
+    at = torch.where(ok[..., 0], at, 0)
+    y, w, g, x = rand(rows, d), rand(T, k), rand(T, d, seed=1), rand(T, d, seed=2)
+    u, v = rand(rows, d, seed=3), rand(T, k, seed=4)
+
+    def plain(sign):
+        p = [sign(t.double()).clone().requires_grad_() for t in (y, w, g)]
+        out = (p[1][..., None] * torch.where(ok, p[0][at], 0.0)).sum(1)
+        dy, dw = torch.autograd.grad(out, p[:2], p[2], create_graph=True)
+        return torch.autograd.grad((dy * sign(u.double())).sum() + (dw * sign(v.double())).sum(), p)
+
+    def ours():
+        p = [t.clone().requires_grad_() for t in (y, w, g)]
+        dy, dw = torch.autograd.grad(moe.moe_combine(*p[:2], inv), p[:2], p[2], create_graph=True)
+        return torch.autograd.grad((dy * u).sum() + (dw * v).sum(), p)
+    for a, b, m in zip(ours(), plain(lambda t: t), plain(torch.abs)):
+        assert bool(((a.double() - b).abs() <= (d + 8) * 2.0 ** -24 * m).all())
+    # by hand, one output alone
+    p = [t.clone().requires_grad_() for t in (g, y, w)]
+    dy, none = moe.moe_combine_backward(*p, inv, want_dw=False)
+    assert none is None
+    got = torch.autograd.grad(dy, p, u, allow_unused=True)
+    assert torch.equal(got[0], moe.moe_combine(u, w, inv)) and got[1] is None
+    assert torch.equal(got[2], moe.moe_combine_backward(g, u, w, inv, want_dy=False)[1])
+    # dispatch is linear: the gradient of its gradient is itself (rows beyond the slots: zeros)
+    q = u.clone().requires_grad_()
+    got, = torch.autograd.grad(moe.moe_dispatch_backward(q, inv, k), q, x)
+    want = torch.zeros_like(u)
+    moe.moe_dispatch(x, inv, k, out=want)
+    assert torch.equal(got, want)
+
+
+def test_recorded_calls_refuse_given_outputs(moe):
+    x, inv = rand(4, 16).requires_grad_(), perm(8)
+    y, w = rand(8, 16), torch.rand(4, 2, device=DEV, requires_grad=True)
+    for call in (lambda: moe.moe_dispatch(x, inv, 2, out=torch.empty_like(y)), lambda: moe.moe_combine(y, w, inv, out=torch.empty(4, 16, device=DEV)),
+                 lambda: moe.moe_dispatch_backward(y.clone().requires_grad_(), inv, 2, out=torch.empty(4, 16, device=DEV)),
+                 lambda: moe.moe_combine_backward(x, y, w, inv, dy=torch.empty_like(y))):
+        with pytest.raises(RuntimeError, match="given"):
+            call()
+
+
+def test_a_recorded_step_is_captured(moe):
+    """Forward and backward of a layer in one graph (warmed up on a side stream), replayed on
+    other inputs."""
+    T, k, d = 64, 2, 48
+    x, w, inv, g = rand(T, d).requires_grad_(), torch.softmax(rand(T, k), 1).requires_grad_(), perm(T * k), rand(T, d, seed=9)
+    up, down = rand(d).requires_grad_(), rand(d, seed=1).requires_grad_()
+    leaves = (x, w, up, down)
+
+    def step():
+        y = torch.relu(moe.moe_dispatch(x, inv, k) * up) * down
+        return torch.autograd.grad(moe.moe_combine(y, w, inv), leaves, g)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for seed in (11, 12):
+        with torch.no_grad():
+            x.copy_(rand(T, d, seed=seed))
+            inv.copy_(perm(T * k, seed=seed))
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(held, step()))
