@@ -43,14 +43,36 @@ __device__ __forceinline__ int source_row(const Params &p, int r)
     return t >= 0 && t < p.x_rows ? t : 0;
 }
 
-// h = g / (1 + exp(-g)) u.  With the fast exponential h is off by (5 + 1.18 |g|) 2^-23 of
-// itself (__expf by 2 + 1.173 |g| units in the last place, sum, divide and product by the
-// rest), nothing beside a bf16 output's half step of 2^-9; fp32 outputs take expf, 5
-// units in all.  From g = -87.4 down the divisor is above 2^126, where __fdividef gives
-// 0.  (A true divide is a call where its operands are extreme, and across a call the sums
-// do not stay in the registers that setmaxnreg gives.)
-__device__ __forceinline__ float swiglu_fast(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
-__device__ __forceinline__ float swiglu_accurate(float g, float u) { return __fdividef(g, 1.0f + expf(-g)) * u; }
+// h = g / (1 + exp(-g)) u, from e = exp(-|g|): g / (1 + e), or g e / (1 + e) below zero, which is the
+// larger of g and g e for either sign.  The divisor is between 1 and 2 and nothing overflows
+// (with 1 + exp(-g) for a divisor, which __fdividef takes to 0 above 2^126, h was 0 from
+// g = -87.4 down, whatever u).
+//   fast      off by (5 + 1.18 |g|) 2^-23 of itself (__expf by 2 + 1.173 |g| units in the last
+//             place, sum, divide and products by the rest), nothing beside a bf16 output's
+//             half step of 2^-9
+//   accurate  for fp32 outputs, 5 2^-23: expf and the reciprocal one unit each, the rest halves.
+//             (A true divide is a call where its operands are extreme, and across a call the sums
+//             do not stay in the registers that setmaxnreg gives.  A Newton step on the
+//             reciprocal took up to 4 % of the tiled kernel's time, and the relative 2-norm
+//             from 7.45e-8 to 7.35e-8 where g's own roundings leave 7.15e-8.)
+// Below g = -87.3 e is less than the smallest normal number: off by (|g| + 2) 2^-149 |u| more.
+// g = -inf gives NaN, as -inf * 0 in the definition does.
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+// 1 / d to one unit (of __fdividef's range nothing is needed).
+__device__ __forceinline__ float reciprocal(float d)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+    return r;
+}
+__device__ __forceinline__ float swiglu_of(float e, float g, float u) { return max_nan(g, g * e) * reciprocal(1.0f + e) * u; }
+__device__ __forceinline__ float swiglu_fast(float g, float u) { return swiglu_of(__expf(-fabsf(g)), g, u); }
+__device__ __forceinline__ float swiglu_accurate(float g, float u) { return swiglu_of(expf(-fabsf(g)), g, u); }
 
 __device__ __forceinline__ void store_out(const Params &p, long long r, int n, float v)
 {

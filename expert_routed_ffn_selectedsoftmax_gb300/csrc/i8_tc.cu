@@ -276,8 +276,9 @@ __device__ __forceinline__ float2 finish2(const Params &p, const uint32_t *a, co
     const float2 g = mul2(mul2(make_float2(__uint_as_float(a[0]), __uint_as_float(a[1])), sx), make_float2(sw0, sw0));
     if (MODE == PRODUCT) return g;
     const float2 u = mul2(mul2(make_float2(__uint_as_float(b[0]), __uint_as_float(b[1])), sx), make_float2(sw1, sw1));
-    return p.out_f32 ? make_float2(swiglu_accurate(g.x, u.x), swiglu_accurate(g.y, u.y))
-                     : make_float2(swiglu_fast(g.x, u.x), swiglu_fast(g.y, u.y));
+    const float2 e = p.out_f32 ? make_float2(expf(-fabsf(g.x)), expf(-fabsf(g.y))) : make_float2(__expf(-fabsf(g.x)), __expf(-fabsf(g.y)));
+    const float2 ge = mul2(g, e);
+    return mul2(mul2(make_float2(max_nan(g.x, ge.x), max_nan(g.y, ge.y)), make_float2(reciprocal(1.0f + e.x), reciprocal(1.0f + e.y))), u);
 }
 
 // The warp's sums of COUNT tokens (a, and for gate/up b) of output channels n0 + lane:

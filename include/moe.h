@@ -705,7 +705,8 @@ MOE_API moe_status moe_grouped_gemm_i8(const void *x_q, const float *x_s, int x_
  *   h [rows, F] fp32 or bf16 (h_dt), rows ldh elements apart, any F >= 1 (moe_quant_i8 takes it
  *   to the down projection: a row's scale needs all of its F values).  wg_q, wu_q
  *   [E, F, d] with scales [E, F].  SiLU(g) is taken to (5 + 1.18 |g|) 2^-23 of itself in
- *   bf16, 5 2^-23 in fp32, and to 0 below about g = -87 in both.  Groups, perm_tok and rows
+ *   bf16 and 5 2^-23 in fp32; below g = -87.3, where exp(g) is less than the smallest normal
+ *   number, to (|g| + 2) 2^-149 more.  Groups, perm_tok and rows
  *   as moe_grouped_gemm_i8 (E == 1 with offsets NULL is the dense layer's).
  */
 MOE_API moe_status moe_gate_up_i8(const void *x_q, const float *x_s, int x_rows, int d,

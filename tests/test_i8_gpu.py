@@ -711,3 +711,30 @@ print("right")
 """
     done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert done.returncode == 0 and "right" in done.stdout, done.stderr[-2000:]
+
+
+@pytest.mark.parametrize("odt", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,K,N", [(2, 128, 700), (40, 128, 400), (600, 128, 160), (1100, 3088, 600), (300, 8192, 1000)])
+def test_far_negative_gates(moe, odt, rows, K, N):
+    """Gate sums down to -110 beside factors of 1e30: silu(g) there is small, not 0.  In the
+    CUDA-core, the few-rows and the tiled kernel, whole and split.
+    Bounds: silu as in the header, (5 + 1.18 |g|) 2^-23 or 5 2^-23 of itself and, below the normal
+    numbers, (|g| + 2) 2^-149; g is two products of fp32 (2^-23 |g| at most), which silu's slope
+    |1 + g| exp(g) carries on (1.01 for its change on the way); u three roundings, 2^-22."""
+    (xq, _), (gq, _), (uq, _) = codes(rows, K), codes(N, K, seed=1), codes(N, K, seed=2)
+    sums = xq.double() @ gq.double().T
+    xs = (110.0 / -sums.amin(1)).float()
+    gs, us = torch.ones(N, device=DEV), torch.full((N,), 1e30, device=DEV)
+    scratch = tiled_scratch(moe, rows, K) if K > 128 else None
+    h = moe.moe_gate_up_i8(xq, xs, gq, gs, uq, us, h_dtype=DT[odt], workspace=scratch)
+    assert scratch is None or not bool((scratch == 0xA5).all())
+    g = sums * xs.double()[:, None]
+    u = (xq.double() @ uq.double().T) * xs.double()[:, None] * us.double()
+    ref = g * torch.sigmoid(g) * u
+    rel = 5 * 2.0 ** -23 if odt == "f32" else (5 + 1.18 * g.abs()) * 2.0 ** -23
+    bound = rel * ref.abs() + 1.01 * (1 + g).abs() * torch.exp(torch.minimum(g, -g)) * 2.0 ** -23 * g.abs() * u.abs()
+    bound = torch.where(g > -2, 1.1 * 2.0 ** -23 * g.abs() * u.abs() + rel * ref.abs(), bound) + 2.0 ** -22 * ref.abs()
+    bound = bound + torch.where(g < -87.3, (g.abs() + 2) * 2.0 ** -149 * u.abs(), 0.0)
+    close(h, ref, bound)
+    far = (g < -88) & (g > -102) & (u != 0)
+    assert int(far.sum()) > 0 and bool((h[far] != 0).all())
