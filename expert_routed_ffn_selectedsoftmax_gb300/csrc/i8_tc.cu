@@ -482,25 +482,28 @@ product_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                 const uint32_t idesc = idesc_f16_mn(1, M, (mine + 15) & ~15);
                 const int db = i & 1;
                 const uint32_t d = tmem + db * NT + from;
-                // (voted, as the other roles' waits: lanes that give up leave the loop together)
-                ok = __all_sync(0xffffffffu, bar_wait(&c.dempty[db], ((i >> 1) & 1u) ^ 1u, abort_flag));
+                // A lane's waits are its own until the warp votes, behind the issue (ahead of it the
+                // vote took up to 1 % of the time): a lane that gave up skips the block, and all
+                // of them leave the loop together.
+                bool mine_ok = bar_wait(&c.dempty[db], ((i >> 1) & 1u) ^ 1u, abort_flag);
                 for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
                     const uint32_t a = it % NA;
                     // (the converters have seen the tokens land too)
-                    ok = __all_sync(0xffffffffu, bar_wait(&c.cfull[a], (it / NA) & 1u, abort_flag));
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t dx = sw128_desc(tokens + a * (FEW ? C::XF_BYTES : C::X_BYTES));
-                    const uint32_t at = tmem + C::A_COL + a * kBlockCols;
-                    if (leader) {
-                        if (mine > 0)
+                    mine_ok = mine_ok && bar_wait(&c.cfull[a], (it / NA) & 1u, abort_flag);
+                    if (mine_ok) {
+                        tc_fence_after();
+                        const uint64_t dx = sw128_desc(tokens + a * (FEW ? C::XF_BYTES : C::X_BYTES));
+                        const uint32_t at = tmem + C::A_COL + a * kBlockCols;
+                        if (leader) {
+                            if (mine > 0)
 #pragma unroll
-                        for (int kk = 0; kk < BK / 16; ++kk)
-                            umma_f16_ts(d, at + kk * 8, desc_step(dx, (kk / 4) * NT * 128 + (kk % 4) * 32), idesc, kb != kb0 || kk != 0);
-                        umma_commit(&c.cempty[a]);
-                        if (kb == kb1 - 1) umma_commit(&c.dfull[db]);
+                            for (int kk = 0; kk < BK / 16; ++kk)
+                                umma_f16_ts(d, at + kk * 8, desc_step(dx, (kk / 4) * NT * 128 + (kk % 4) * 32), idesc, kb != kb0 || kk != 0);
+                            umma_commit(&c.cempty[a]);
+                            if (kb == kb1 - 1) umma_commit(&c.dfull[db]);
+                        }
                     }
-                    __syncwarp();
+                    ok = __all_sync(0xffffffffu, mine_ok);
                 }
             }
             issued = it;

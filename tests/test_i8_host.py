@@ -188,7 +188,11 @@ def test_a_warp_gives_up_as_a_whole(name):
     waits = warp_waits(name)
     assert len(waits) >= 4
     for statement in waits:
-        assert "__all_sync(0xffffffffu" in statement, statement
+        # (the multiplying warps vote once behind both of theirs)
+        assert "__all_sync(0xffffffffu" in statement or re.match(r"(bool )?mine_ok = ", statement), statement
+    role = source(name)
+    role = role[role.index("bool mine_ok"):]
+    assert "__all_sync(0xffffffffu, mine_ok)" in role[:role.index("issued = it")]
 
 
 @pytest.mark.parametrize("name", ["fp8b_decode.cu", "fp8b_gemm.cu"])
