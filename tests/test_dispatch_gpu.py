@@ -602,3 +602,27 @@ def test_a_recorded_step_is_captured(moe):
             inv.copy_(perm(T * k, seed=seed))
         graph.replay()
         assert all(torch.equal(a, b) for a, b in zip(held, step()))
+
+
+def test_gradients_beyond_32_bits(moe):
+    """dy's rows and a gradient's grouped rows whose elements lie past 2^31, given and new."""
+    d, rows = 1032, 2 ** 21 + 9                    # 2.16e9 elements of bf16
+    T, k = 3, 2
+    inv = torch.tensor([rows - 1, 5, rows - 2, rows - 9, 0, 2 ** 21 - 1], dtype=torch.int32, device=DEV)
+    x, w = rand(T, d).bfloat16(), torch.softmax(rand(T, k), 1)
+    y = torch.zeros(rows, d, device=DEV, dtype=torch.bfloat16)
+    y[inv.long()] = rand(T * k, d, seed=1).bfloat16()
+    ref, m = gather_ref(y, inv, T, k)
+    close(moe.moe_dispatch_backward(y, inv, k), ref, k * 2.0 ** -24 * m * (1 + 1e-6))
+    at = inv.long()
+    want = (w.view(-1, 1) * x.float().repeat_interleave(k, 0))
+    named = torch.zeros(rows, dtype=torch.bool, device=DEV)
+    named[at] = True
+    dy = torch.full_like(y, 7.0)
+    moe.moe_combine_backward(x, y, w, inv, want_dw=False, dy=dy)
+    close(dy[at], want.double(), 2.0 ** -24 * want.abs().double())
+    assert int((dy != 7).any(1).sum()) == T * k
+    del dy
+    new = moe.moe_combine_backward(x, y, w, inv, want_dw=False)[0]
+    close(new[at], want.double(), 2.0 ** -24 * want.abs().double())
+    assert int((new != 0).any(1).sum()) == T * k

@@ -738,3 +738,201 @@ def test_far_negative_gates(moe, odt, rows, K, N):
     close(h, ref, bound)
     far = (g < -88) & (g > -102) & (u != 0)
     assert int(far.sum()) > 0 and bool((h[far] != 0).all())
+
+
+# Sizes that the 128-token tiles take, whole and with a reduction split over clusters (a test that
+# uses them holds the scratch to it, so that another rule does not move it elsewhere).
+TILED = [(1100, 3088, 600), (300, 8192, 1000)]
+
+
+def tiled_gemm(moe, xq, xs, wq, ws, **kw):
+    scratch = tiled_scratch(moe, *xq.shape)
+    out = moe.moe_gemm_i8(xq, xs, wq, ws, workspace=scratch, **kw)
+    assert not bool((scratch == 0xA5).all())
+    return out
+
+
+def tiled_gate_up(moe, xq, xs, gq, gs, uq, us, **kw):
+    scratch = tiled_scratch(moe, *xq.shape)
+    out = moe.moe_gate_up_i8(xq, xs, gq, gs, uq, us, workspace=scratch, **kw)
+    assert not bool((scratch == 0xA5).all())
+    return out
+
+
+@pytest.mark.parametrize("T,K,N", [(2200, 1024, 1030), (300, 8192, 1000), (107, 16384, 899)])
+def test_tiled_largest_codes_add_up_exactly(moe, T, K, N):
+    """Rows of -128 and 127 in 1024 columns spread over K, zeros in the others: the largest
+    sums that are exact, 2^24 itself among them."""
+    xq, wq = torch.zeros(T, K, dtype=torch.int8, device=DEV), torch.zeros(N, K, dtype=torch.int8, device=DEV)
+    at = torch.arange(0, K, K // 1024, device=DEV)
+    a, b = xq[:, at], wq[:, at]
+    a[:], b[:] = -128, -128
+    a[1::3], b[1::3] = 127, 127
+    a[2::3, ::2], b[2::3, 1::3] = 127, 1
+    xq[:, at], wq[:, at] = a, b
+    one = lambda n: torch.ones(n, device=DEV)
+    out = tiled_gemm(moe, xq, one(T), wq, one(N), out_dtype=torch.float32)
+    assert torch.equal(out.double(), xq.double() @ wq.double().T)
+
+
+@pytest.mark.parametrize("T,K,N", [(2, 16384, 140), (40, 16384, 140), (3, 32768, 1000), (300, 4096, 64), (107, 16384, 899), (2100, 16384, 640)])
+def test_long_reductions_that_cancel_add_up_exactly(moe, T, K, N):
+    """Magnitudes whose sum passes 2^24 many times, products that cancel in pairs of columns but
+    for a few: every partial sum, of any 16 columns and of any share of the reduction, is a whole
+    number below 2^24, so the result is exact, and a column that is lost or read twice
+    shows.  In the CUDA-core, the few-rows and the tiled kernel, whole and split."""
+    xq = torch.randint(-127, 128, (T, K), generator=gen(1), device=DEV).to(torch.int8)
+    wq = torch.randint(100, 128, (N, K), generator=gen(2), device=DEV).to(torch.int8)
+    xq[:, 1::2], wq[:, 1::2] = -xq[:, ::2], wq[:, ::2]
+    odd = torch.randint(0, K // 2, (K // 64,), generator=gen(3), device=DEV).unique() * 2 + 1
+    wq[:, odd] -= torch.randint(1, 90, (N, len(odd)), generator=gen(4), device=DEV).to(torch.int8)
+    exact = xq.double() @ wq.double().T
+    assert float((xq.double().abs() @ wq.double().abs().T).max()) > 2 ** 24 and float(exact.abs().max()) < 2 ** 23
+    one = lambda n: torch.ones(n, device=DEV)
+    out = moe.moe_gemm_i8(xq, one(T), wq, one(N), out_dtype=torch.float32)
+    assert bool((exact != 0).any()) and torch.equal(out.double(), exact)
+
+
+@pytest.mark.parametrize("T,K,N", TILED)
+def test_tiled_scales_of_every_kind(moe, T, K, N):
+    (xq, xs), (wq, ws) = codes(T, K), codes(N, K, seed=1)
+    xs, ws = xs.clone(), ws.clone()
+    inf, nan = float("inf"), float("nan")
+    for at in (0, T - 4):
+        xs[at:at + 4] = torch.tensor([0.0, nan, 1e30, inf], device=DEV)
+    for at in (0, N - 6):
+        ws[at:at + 6] = torch.tensor([0.0, nan, 1e-30, 2.0 ** -126, inf, -1.0], device=DEV)
+    for odt in (torch.float32, torch.bfloat16):
+        out = tiled_gemm(moe, xq, xs, wq, ws, out_dtype=odt)
+        # in the call's order: the sum times the token's scale, times the channel's
+        y = (xq.double() @ wq.double().T).float() * xs[:, None] * ws[None, :]
+        plain = y.isfinite()
+        assert torch.equal(out.isnan(), y.isnan()) and torch.equal(out[~plain & ~y.isnan()].float(), y[~plain & ~y.isnan()])
+        ref, bound = product_ref(xq, wq, xs, ws)
+        close(torch.where(plain, out, 0.0), torch.where(plain, ref, 0.0), torch.where(plain, bound, 0.0))
+        h = tiled_gate_up(moe, xq, xs, wq, ws, wq, ws, h_dtype=odt)
+        assert bool(h[1].isnan().all()) and bool(h[:, 1].isnan().all()) and bool(h[T - 3].isnan().all())
+        assert not h[0, 2:4].any() and not h[T - 4, 2:4].any()
+
+
+@pytest.mark.parametrize("odt", ["f32", "bf16"])
+@pytest.mark.parametrize("T,K,N", TILED)
+def test_tiled_gate_sums_from_minus_200_to_200(moe, odt, T, K, N):
+    (xq, _), (gq, _), (uq, us) = codes(T, K), codes(N, K, seed=1), codes(N, K, seed=2)
+    sums = xq.double() @ gq.double().T
+    xs = (torch.rand(T, generator=gen(4), device=DEV) * 200 / sums.abs().amax(1)).float()
+    gs = torch.ones(N, device=DEV)
+    h = tiled_gate_up(moe, xq, xs, gq, gs, uq, us, h_dtype=DT[odt])
+    g, u = product_ref(xq, gq, xs, gs), product_ref(xq, uq, xs, us)
+    assert float(g[0].max()) > 100 and float(g[0].min()) < -100
+    close(h, *swiglu_ref(*g, *u, odt == "f32"))
+
+
+def ragged_call(moe, gate_up, xq, xs, mats, off, tok=None, out=None, tiled=False):
+    rows = len(tok) if tok is not None else xq.shape[0]
+    scratch = tiled_scratch(moe, rows, xq.shape[1]) if tiled else None
+    if gate_up:
+        (wq, ws), (uq, us) = mats
+        out = moe.moe_gate_up_i8(xq, xs, wq, ws, uq, us, offsets=off, perm_tok=tok, h=out, workspace=scratch)
+    else:
+        out = moe.moe_grouped_gemm_i8(xq, xs, *mats[0], off, perm_tok=tok, out=out, workspace=scratch)
+    assert not tiled or not bool((scratch == 0xA5).all())
+    return out
+
+
+RAGGED = [(2, 144, 72, False), (6, 144, 72, False), (70, 144, 72, False), (400, 144, 72, False), (1500, 2064, 777, True), (410, 8192, 320, True)]
+
+
+@pytest.mark.parametrize("gate_up", [False, True])
+@pytest.mark.parametrize("rows,K,N,tiled", RAGGED)
+def test_offsets_of_every_kind(moe, rows, K, N, tiled, gate_up):
+    """Groups in every kernel (CUDA cores, few rows, tiles whole and split): empty ones, one with
+    everything, a padded batch's rows behind them as they were; offsets out of range count as
+    the nearest row; a group that ends before it begins is empty, and rows that one group
+    alone holds are right where others overlap; bad token indices spoil their own row only."""
+    E, half = 5, rows // 2
+    (xq, xs), (wq, ws), (uq, us) = codes(rows, K), codes(E, N, K, seed=1), codes(E, N, K, seed=2)
+    mats = [(wq, ws), (uq, us)] if gate_up else [(wq, ws)]
+    third = rows // 3
+    cuts = [[0, 0, rows, rows, rows, rows], [0, 1, 1, 1, half, half], [0, half, half, half, half, rows],
+            [-5, 1, 1, half, half, 10 ** 9], [-2 ** 31, 0, third, third, 2 ** 31 - 1, 2 ** 31 - 1]]
+    for cut in cuts:
+        off = torch.tensor(cut, dtype=torch.int32, device=DEV)
+        out = torch.full((rows, N), 7.0, device=DEV, dtype=torch.bfloat16)
+        ragged_call(moe, gate_up, xq, xs, mats, off, out=out, tiled=tiled)
+        kept = off.clamp(0, rows)
+        check_grouped(out, xq, xs, mats, kept, None)
+        assert bool((out[int(kept[-1]):] == 7).all())
+    # 0 .. 2/3, none, 1/3 .. all, none, none: the first and the last third are one group's alone
+    off = torch.tensor([0, 2 * third, third, rows, rows, rows], dtype=torch.int32, device=DEV)
+    out = ragged_call(moe, gate_up, xq, xs, mats, off, tiled=tiled)
+    alone = torch.tensor([0, third, third, third, third, third], dtype=torch.int32)
+    if third:
+        check_grouped(out, xq, xs, mats, alone, None)
+        check_grouped(out[2 * third:], xq[2 * third:], xs[2 * third:], mats,
+                      torch.tensor([0, 0, 0, rows - 2 * third, rows - 2 * third, rows - 2 * third]), None)
+    tok = torch.arange(rows, device=DEV).int().flip(0).contiguous()
+    bad = tok.clone()
+    at = sorted({1, rows // 2, rows - 1})
+    bad[at] = torch.tensor([-7, rows, 2 ** 31 - 1], dtype=torch.int32, device=DEV)[:len(at)]
+    off = torch.tensor([0, 1, half, half, rows, rows], dtype=torch.int32, device=DEV)
+    a, b = (ragged_call(moe, gate_up, xq, xs, mats, off, tok=t, tiled=tiled) for t in (tok, bad))
+    keep = torch.ones(rows, dtype=torch.bool, device=DEV)
+    keep[at] = False
+    check_grouped(a, xq, xs, mats, off, tok)
+    assert torch.equal(a[keep], b[keep])
+
+
+@pytest.mark.parametrize("gate_up", [False, True])
+@pytest.mark.parametrize("T,K,N", TILED)
+def test_one_workspace_by_calls_in_order(moe, T, K, N, gate_up):
+    """Calls on other tokens that hold the same workspace, back to back on a stream and in one
+    graph: the next call's fp16 rows are written when the product before has read its own."""
+    sets = [codes(T, K, seed=20 + i) for i in range(4)]
+    (wq, ws), (uq, us) = codes(N, K, seed=1), codes(N, K, seed=2)
+    scratch = tiled_scratch(moe, T, K)
+    outs = [torch.empty(T, N, device=DEV) for _ in range(12)]
+    want = []
+    for xq, xs in sets:
+        y = product_ref(xq, wq, xs, ws)
+        want.append(swiglu_ref(*y, *product_ref(xq, uq, xs, us), True) if gate_up else y)
+
+    def chain():
+        for i, out in enumerate(outs):
+            xq, xs = sets[i % 4]
+            if gate_up:
+                moe.moe_gate_up_i8(xq, xs, wq, ws, uq, us, h=out, workspace=scratch)
+            else:
+                moe.moe_gemm_i8(xq, xs, wq, ws, out=out, workspace=scratch)
+    chain()
+    assert not bool((scratch == 0xA5).all())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain()
+    for run in (chain, graph.replay, graph.replay):
+        for out in outs:
+            out.zero_()
+        run()
+        for i, out in enumerate(outs):
+            close(out, *want[i % 4])
+
+
+@pytest.mark.parametrize("gate_up", [False, True])
+@pytest.mark.parametrize("T,K,N", [(2, 512, 200), (40, 512, 200), (40, 512, 201), (1100, 3088, 600), (1100, 3088, 601)])
+def test_rows_past_32_bits(moe, T, K, N, gate_up):
+    """Token rows whose codes, and output rows whose elements, lie past 2^31, in the CUDA-core, the
+    few-rows and the tiled kernel, stored in 16-byte pieces and element by element."""
+    apart = (2 ** 31 // (T - 1) + 64) // 16 * 16
+    xq, xs = codes(T, K)
+    far = torch.zeros((T - 1) * apart + K, dtype=torch.int8, device=DEV).as_strided((T, K), (apart, 1))
+    far.copy_(xq)
+    (wq, ws), (uq, us) = codes(N, K, seed=1), codes(N, K, seed=2)
+    out = torch.zeros((T - 1) * apart + N, dtype=torch.bfloat16, device=DEV).as_strided((T, N), (apart, 1))
+    assert (T - 1) * apart > 2 ** 31
+    y = product_ref(xq, wq, xs, ws)
+    if gate_up:
+        moe.moe_gate_up_i8(far, xs, wq, ws, uq, us, h=out)
+        y = swiglu_ref(*y, *product_ref(xq, uq, xs, us), False)
+    else:
+        moe.moe_gemm_i8(far, xs, wq, ws, out=out)
+    close(out.contiguous(), *y)
