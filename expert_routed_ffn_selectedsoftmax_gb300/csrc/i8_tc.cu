@@ -4,7 +4,9 @@
 //   y[r,n] = (sum_i cx[r,i] cw[n,i]) sx[r] sw[n]
 //
 // sm_103a has no 8-bit integer MMA.  An int8 code is exact in fp16 and a product of two
-// in fp32, so the sums run on kind::f16 and are whole numbers, exact up to 2^24.
+// in fp32, so the sums run on kind::f16 and are whole numbers, exact up to 2^24; beyond, each
+// step of 16 columns may cut off a unit in their last place (8192 x 2048 x 5632's sums of normal
+// values stay below; 16384 columns of codes from 100 to 127 came out 5.4e-5 too small).
 //
 // Weights are the MMA's 128 rows (PRODUCT: of W; GATEUP: 64 of W_gate and the same 64 of
 // W_up, 16 of each to the lanes of a warp, so that the warp that writes a channel has both of

@@ -3,9 +3,10 @@
 // A warp holds four weight rows (PRODUCT: four output channels; GATEUP: two of W_gate
 // and the same two of W_up), walks its share of the reduction 512 columns at a time, 16
 // bytes a lane, and multiplies each with up to TB tokens' by four-way integer dot products
-// (dp4a): sums in 32-bit whole numbers, exact up to K = 131072.  What bounds it is memory,
-// so what counts is bytes in flight: a long reduction is split over the warps of a CTA,
-// until a warp has a step or two (4096 x 4096 of 4 tokens, one warp for all of K: 9.1 us).
+// (dp4a): sums in 32-bit whole numbers, exact below K = 131072 (where (-128)^2 K is 2^31).
+// What bounds it is memory, so what counts is bytes in flight: a long reduction is split over
+// the warps of a CTA, until a warp has a step or two (4096 x 4096 of 4 tokens, one warp for
+// all of K: 9.1 us).
 // Weights are read once for every TB rows of a group.  2048 x 5632 of one token takes 4.4 us:
 // all of its 11.5 MB are asked for at once, 1.7 us at the measured copy rate, behind the start.
 #include "i8.h"

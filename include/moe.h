@@ -654,7 +654,11 @@ MOE_API moe_status moe_combine_backward_filled(const void *grad, moe_dtype grad_
  * codes 0.
  * Products: out[r,n] = (sum_i x_q[r,i] w_q[n,i]) x_s[r] w_s[n].  Any code from -128 to 127
  * is taken.  The codes' products are summed exactly while the sums stay below 2^24 in
- * magnitude (any row up to K = 1024), and otherwise to fp32's accuracy; the two scales
+ * magnitude (any row up to K = 1024).  Beyond that, calls of one or two rows (K < 131072) and
+ * some of few sum whole numbers and round once; the others sum in fp32 on the tensor cores,
+ * where each step of 16 columns may cut off a unit in the last place of the sum so far: up to
+ * K / 16 2^-23 of the sum of magnitudes (454 2^-23 measured at K = 16384, all of one sign).
+ * So there the bits of a row may depend on how many rows the call has.  The two scales
  * are multiplied in one after the other, fp32, rounded each time.
  *
  * Failure handling, `status` and reproducibility as the block-scaled fp8 operators (a row
@@ -670,8 +674,9 @@ MOE_API moe_status moe_quant_i8(const void *x, moe_dtype x_dt, int rows, int col
                                 int8_t *codes, float *scales, moe_stream stream);
 
 /*
- * Bytes of device workspace that the products of `rows` rows of K columns need, 256-byte
- * aligned, not shared by calls that can overlap.  0 for up to 32 rows (NULL is taken), and
+ * Bytes of device workspace that the products of `rows` rows of K columns may need, whatever
+ * N and E, 256-byte aligned, not shared by calls that can overlap.  (Those that the sizes send to
+ * tiles of few rows leave it as it was.)  0 for up to 32 rows (NULL is taken), and
  * on invalid sizes.
  */
 MOE_API size_t moe_i8_workspace_size(int rows, int K);

@@ -936,3 +936,21 @@ def test_rows_past_32_bits(moe, T, K, N, gate_up):
     else:
         moe.moe_gemm_i8(far, xs, wq, ws, out=out)
     close(out.contiguous(), *y)
+
+
+@pytest.mark.parametrize("T,K,N", [(2, 16384, 140), (40, 16384, 140), (64, 4096, 4096), (300, 16384, 140), (107, 16384, 899),
+                                   (2100, 16384, 640), (2100, 4096, 640)])
+def test_sums_beyond_2_to_24(moe, T, K, N):
+    """Large codes of one sign, the worst for sums that are cut off.  On the CUDA cores the sum is
+    a whole number, rounded once.  On the tensor cores each of the K / 16 steps may cut a unit
+    in the last place off the sum so far, at most 2^-23 of A, and a split reduction's up
+    to 7 additions round once each."""
+    xq = torch.randint(100, 128, (T, K), generator=gen(1), device=DEV).to(torch.int8)
+    wq = torch.randint(100, 128, (N, K), generator=gen(2), device=DEV).to(torch.int8)
+    one = lambda n: torch.ones(n, device=DEV)
+    out = moe.moe_gemm_i8(xq, one(T), wq, one(N), out_dtype=torch.float32)
+    exact = xq.double() @ wq.double().T
+    assert float(exact.min()) > 2 ** 24
+    if T <= 2:
+        assert torch.equal(out, exact.float())
+    assert bool(((out.double() - exact).abs() <= (K / 16 + 7) * 2.0 ** -23 * exact).all())
