@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kCopyThreads, 8)   // (34 registers a thread: 
 scatter_rows_kernel(const Args a)
 {
     pdl_enter();
-    if (blockIdx.x < (uint32_t)a.fill) {
+    if (__builtin_expect(blockIdx.x < (uint32_t)a.fill, 0)) {
         zero_unnamed<XT, 2>(a);
         return;
     }
@@ -402,7 +402,7 @@ combine_backward_kernel(const Args a)
 {
     pdl_enter();
     constexpr int N = backward_threads(G);
-    if (blockIdx.x < (uint32_t)a.fill) {
+    if (__builtin_expect(blockIdx.x < (uint32_t)a.fill, 0)) {
         zero_unnamed<XT, 8>(a);
         return;
     }

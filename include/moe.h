@@ -533,8 +533,9 @@ MOE_API size_t moe_fp8b_workspace_size(int rows, int K);
  *   rows <= x_rows) are device arrays as moe_permute writes them; offsets may
  *   be NULL when E == 1 (all rows).  Experts may be without rows.  Output rows
  *   that no group holds (offsets[E] < rows: a padded batch) are left as they
- *   were.  Offsets are clamped to [0, rows]; a row whose perm_tok is outside
- *   [0, x_rows) is undefined, and no other memory is touched.
+ *   were.  Offsets ascend, and are clamped to [0, rows]; where they do not ascend, output
+ *   rows are undefined, as is a row whose perm_tok is outside [0, x_rows), and no other
+ *   memory is touched.
  *   workspace: with perm_tok, scratch of at least moe_fp8b_workspace_size(rows,
  *   K) bytes, 256-byte aligned, not shared by calls that can overlap; without
  *   perm_tok it is not used and may be NULL.
