@@ -13,8 +13,8 @@
 // over the slots in order, in fp32, and are rounded once.
 //
 // What bounds them is memory.  16384 tokens x 2 of 2048 bf16 columns (us, of the measured copy
-// rate): dispatch 30.6, 99 %; its gradient 36.6, 83 %; combine 37.0, 82 %; its gradients 50.5,
-// 100 %.  Few tokens are latency: combine of 128 x 2 of 1024 takes 1.7.
+// rate): dispatch 30.9, 98 %; its gradient 37.1, 82 %; combine 37.0, 82 %; its gradients 50.6,
+// 100 %.  Few tokens are latency: combine of 128 x 2 of 1024 takes 1.5.
 #include <type_traits>
 
 #include "common.cuh"
@@ -103,8 +103,10 @@ template <> struct Chunk<__nv_bfloat16> {
 //            2-byte elements are whole too; what is read there comes as the 16-byte pieces
 //            around it, shifted into place (only pieces inside the row: at its ends it goes
 //            by elements).
-// Measured (us, APART / SHIFTED): gradients of 8192 x 2 x 1001 in bf16 52 / 34, of 4096 x 4 x 2049 in
-// fp32 56 / 73; combine of 4096 x 4 x 2049 in bf16 38 / 31.
+// Measured (us, APART / SHIFTED): combine of 4096 x 4 x 2049 in bf16 35.6 / 27.7, in fp32 33.4 /
+// 34.5; its gradients in fp32 50.6 / 66.1, of 8192 x 2 x 1001 in bf16 26.2 / 31.3; dispatch's
+// gradient of 999 x 3 x 1001 in fp32 5.2 / 5.7, of 4096 x 4 x 2049 33.1 / 33.8, of 8192 x 2 x 1001 in
+// bf16 15.4 / 16.2; dispatch there 11.7 / 13.4.  (bf16 goes SHIFTED in all of them, by combine.)
 enum Way { WHOLE = 0, APART = 1, SHIFTED = 2 };
 template <typename T> __device__ __forceinline__ void load_apart(Chunk<T> &c, const T *p, int step, int left)
 {
@@ -685,10 +687,10 @@ moe_status combine_backward(const void *grad, moe_dtype grad_dt, int T, int d, l
                 constexpr int WAY = decltype(way)::value;
                 // Threads of a token.  Many tokens: a warp, or two where it has more than two
                 // chunks a lane; few: as many as their chunks keep in use.  us, 32 / 64 / 128 / 512:
-                // 16384 x 2 x 128 12.7 / 18.5 / 28.1, x 2048 52.7 / 50.6 / 52.3; 1945 x 7 x 278
-                // 18.2 / 19.5 / 27.5; 999 x 3 x 1000 7.0 / 5.2 / 5.3 / 13.1; 3000 x 8 x 8192
-                // 133 / 137 / 131; 300 x 4 x 4096 18.6 / 10.8 / 7.4 / 6.3; 64 x 2 x 2048 3.6 / 2.5 /
-                // 1.9 / 2.1; 16 x 2 x 8192 10.3 / 5.8 / 3.6 / 2.5.
+                // 16384 x 2 x 128 10.8 / 18.8 / 29.5, x 2048 51.3 / 50.7 / 53.1; 1945 x 7 x 278
+                // 18.3 / 19.2 / 21.1; 999 x 3 x 1000 6.8 / 5.3 / 5.3 / 13.4; 3000 x 8 x 8192
+                // 135 / 137 / 130 / 131; 300 x 4 x 4096 18.4 / 11.0 / 7.6 / 6.4; 64 x 2 x 2048 3.6 / 2.6 /
+                // 2.0 / 2.1; 16 x 2 x 8192 10.5 / 5.8 / 3.7 / 2.5.
                 const int sms = device_sm_count(), chunks = ceil_div(d, V);
                 const auto launch = [&](auto group) {
                     constexpr int G = decltype(group)::value, N = backward_threads(G);

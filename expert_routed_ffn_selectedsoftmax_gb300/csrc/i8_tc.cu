@@ -34,8 +34,8 @@
 // is free again, three buffers (4096 x 4096 of 128 rows 16.0; rings of 6 and 8 blocks 15.6 and
 // 15.9, the output warps as a third converting group 15.9, half blocks in six buffers 18.8, a
 // warp of its own for the tokens 22.6).  Tiled: the MMAs, and
-// what they share the SM with.  8192 x 2048 x 5632 takes 128 (1.47 PFLOP/s, 78 % of the
-// measured fp16 rate): without the converters' work it takes 120, without the output 120,
+// what they share the SM with.  8192 x 2048 x 5632 takes 127 in a graph (1.49 PFLOP/s, 79 % of the
+// measured bf16 rate; 136, 74 %, called with new outputs): without the converters' work it takes 120, without the output 120,
 // without the tokens' loads 119, and with the MMAs alone 102.  The tensor pipe is busy for
 // 72 % of the cycles, and the L2 is at 68 % of its rate.
 //
