@@ -695,7 +695,7 @@ def moe_dispatch(x: torch.Tensor, inv: torch.Tensor, k: int, out: Optional[torch
     inv [T*k] (moe_permute).  rows is T*k, or out's if it is given.  Rows that no slot
     names are left as they were in an output that is given, and zeros in one allocated
     here; a slot whose inv is outside [0, rows) writes nothing.  Recorded for autograd where x
-    requires grad (out is then not to be given).
+    requires grad (not into an out that is given: a warning says so).
     """
     got = (_fp8b_module or _fp8b()).dispatch(x, inv, k, out)
     return _Dispatch.apply(x, inv, k, None) if got is NotImplemented else _checked(got, "moe_dispatch")
@@ -704,7 +704,7 @@ def moe_dispatch(x: torch.Tensor, inv: torch.Tensor, k: int, out: Optional[torch
 def moe_dispatch_backward(grad: torch.Tensor, inv: torch.Tensor, k: int,
                           out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """moe_dispatch's gradient -> [T, d] in grad's type: out[t] = sum_j grad[inv[t*k + j]].
-    Recorded for autograd where grad requires it (out is then not to be given)."""
+    Recorded for autograd where grad requires it (not into an out that is given: a warning says so)."""
     got = (_fp8b_module or _fp8b()).dispatch_backward(grad, inv, k, out)
     return _DispatchBackward.apply(grad, inv, k) if got is NotImplemented else _checked(got, "moe_dispatch_backward")
 
@@ -715,8 +715,8 @@ def moe_combine(y: torch.Tensor, topk_w: torch.Tensor, inv: torch.Tensor, out: O
     out[t] = sum_j topk_w[t, j] y[inv[t*k + j]].
 
     topk_w [T, k] (moe_route), inv [T*k] (moe_permute); a slot whose inv is outside
-    [0, rows) adds nothing.  Recorded for autograd where y or topk_w requires grad (out is then
-    not to be given).
+    [0, rows) adds nothing.  Recorded for autograd where y or topk_w requires grad (not into
+    an out that is given: a warning says so).
     """
     got = (_fp8b_module or _fp8b()).combine(y, topk_w, inv, out, out_dtype)
     return _Combine.apply(y, topk_w, inv, out_dtype) if got is NotImplemented else _checked(got, "moe_combine")
@@ -730,7 +730,8 @@ def moe_combine_backward(grad: torch.Tensor, y: torch.Tensor, topk_w: torch.Tens
 
     One that is not wanted is None.  Rows of dy that no slot names are left as they were in
     a dy that is given, and zeros (their gradient) in one allocated here.  Recorded for
-    autograd where grad, y or topk_w requires it (dy and dw are then not to be given).
+    autograd where grad, y or topk_w requires it (not into a dy or dw that is given: a warning
+    says so).
     """
     got = (_fp8b_module or _fp8b()).combine_backward(grad, y, topk_w, inv, want_dy, want_dw, dy, dw)
     if got is NotImplemented:

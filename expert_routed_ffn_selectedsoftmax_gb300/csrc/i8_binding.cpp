@@ -125,15 +125,17 @@ Slots slots_of(PyObject *o, int64_t k, c10::Device dev)
     return {static_cast<const int32_t *>(p), inv.numel() / k, int_of(k, "k")};
 }
 // Whether an input requires grad where gradients are recorded: the call is then left to the
-// Python side (the answer is NotImplemented), which comes again without recording.
+// Python side (the answer is NotImplemented), which comes again without recording.  An output that is
+// given keeps no graph: such a call runs as it is, with a warning.
 bool recorded(const char *call, bool has_output, std::initializer_list<const Tensor *> inputs)
 {
     if (!c10::GradMode::is_enabled()) return false;
     for (const Tensor *t : inputs)
         if (t->requires_grad()) {
-            TORCH_CHECK(!has_output, call, ": an output that is given keeps no graph, and an input requires grad: detach it, or "
-                        "let the call allocate its outputs");
-            return true;
+            if (has_output)
+                TORCH_WARN(call, ": an output that is given keeps no graph, and an input requires grad: detach it, or let the "
+                           "call allocate its outputs");
+            return !has_output;
         }
     return false;
 }

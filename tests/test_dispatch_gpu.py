@@ -566,14 +566,21 @@ def test_recorded_twice(moe):
     assert torch.equal(got, want)
 
 
-def test_recorded_calls_refuse_given_outputs(moe):
+def test_given_outputs_keep_no_graph(moe):
+    """An input requires grad and an output is given: the call runs, without a graph, and warns."""
     x, inv = rand(4, 16).requires_grad_(), perm(8)
-    y, w = rand(8, 16), torch.rand(4, 2, device=DEV, requires_grad=True)
-    for call in (lambda: moe.moe_dispatch(x, inv, 2, out=torch.empty_like(y)), lambda: moe.moe_combine(y, w, inv, out=torch.empty(4, 16, device=DEV)),
-                 lambda: moe.moe_dispatch_backward(y.clone().requires_grad_(), inv, 2, out=torch.empty(4, 16, device=DEV)),
-                 lambda: moe.moe_combine_backward(x, y, w, inv, dy=torch.empty_like(y))):
-        with pytest.raises(RuntimeError, match="given"):
-            call()
+    y, w = rand(8, 16).requires_grad_(), torch.rand(4, 2, device=DEV, requires_grad=True)
+    calls = ((lambda o: moe.moe_dispatch(x, inv, 2, out=o), (8, 16)), (lambda o: moe.moe_combine(y, w, inv, out=o), (4, 16)),
+             (lambda o: moe.moe_dispatch_backward(y, inv, 2, out=o), (4, 16)),
+             (lambda o: moe.moe_combine_backward(x, y, w, inv, dy=o)[0], (8, 16)))
+    for call, shape in calls:
+        out = torch.empty(*shape, device=DEV)
+        with pytest.warns(UserWarning, match="given"):
+            assert call(out) is out
+        assert not out.requires_grad
+        with torch.no_grad():
+            again = call(None)
+        assert torch.equal(out, again)
 
 
 def test_a_recorded_step_is_captured(moe):
