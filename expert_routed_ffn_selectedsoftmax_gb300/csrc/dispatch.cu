@@ -309,7 +309,9 @@ template <int WAY, typename T> __device__ __forceinline__ void store(const Chunk
 }
 
 template <typename XT, int WAY>
-__global__ void __launch_bounds__(kCopyThreads, 8)   // (34 registers a thread: 16384 x 1 x 4096 47.3 us, 32: 42.3)
+// (CTAs an SM: with 34 registers a thread, seven, 16384 x 1 x 4096 takes 47.3 us, with 32 42.3; element
+// loads want registers: 6545 x 1 x 124 in fp32 3.4 us with 32, 3.0 with 36)
+__global__ void __launch_bounds__(kCopyThreads, WAY == APART ? 6 : 8)
 scatter_rows_kernel(const Args a)
 {
     pdl_enter();
